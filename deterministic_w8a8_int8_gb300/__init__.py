@@ -26,6 +26,8 @@ Entry points (same names as the C ABI):
   prism_quant_act_f16(x, inv_s)                  -> (codes as float16, a_scale)
   prism_codes_to_f16(w)                          -> int8 codes as float16 (load time)
   prism_w8a8_linear_f16(qh, a_scale, wh, w_scale, ...) -> out   codes given as float16
+  prism_kv_append, prism_kv_attention, prism_w4g_linear, prism_token_logprobs
+                                                 the decode step (decode.py)
 """
 from __future__ import annotations
 
@@ -52,6 +54,9 @@ PRISM_DEV_ERR_COUNT = 2
 PRISM_DEV_ERR_ID_RANGE = 4
 PRISM_DEV_ERR_DUPLICATE = 8
 PRISM_DEV_ERR_ROW_RANGE = 16
+PRISM_DEV_ERR_PAGE_RANGE = 32
+PRISM_DEV_ERR_SEQ_RANGE = 64
+PRISM_MAX_TOP_K = 32
 PRISM_DEVSTATUS_WAIT_TIMEOUT = 1
 
 # (restype, argtypes) of every symbol the header declares
@@ -87,6 +92,15 @@ SIGNATURES = {
     "prism_w4a8_linear": (_I32, [_P, _I64, _P, _P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I32,
                                  _P, _SZ, _P]),
     "prism_unpack_w4": (_I32, [_P, _I64, _I64, _I64, _P, _I64, _P]),
+    "prism_kv_append": (_I32, [_P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _P,
+                               _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P]),
+    "prism_kv_attention_workspace_bytes": (_SZ, [_I64] * 8),
+    "prism_kv_attention": (_I32, [_P, _I64, _I64, _P, _P, _P, _P, _P, _I64, _P, _P, _P, _I64, _I64, _P,
+                                  ctypes.c_float, _I32, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64,
+                                  _P, _SZ, _P, _P]),
+    "prism_w4g_linear": (_I32, [_P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64,
+                                _I64, _P]),
+    "prism_token_logprobs": (_I32, [_P, _I32, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P]),
     "prism_status_string": (ctypes.c_char_p, [_I32]),
     "prism_version": (_I32, []),
     "prism_w8a8_kernel_kind": (_I32, [_I64, _I64, _I64]),
@@ -746,3 +760,18 @@ def prism_w8a8_linear_f16(qh, a_scale, wh, w_scale, residual=None, out=None, acc
         _ptr(acc_out), M, N, K, int(split_k), _ptr(workspace), ws_bytes, _stream(stream))
     _check("prism_w8a8_linear_f16", st)
     return out
+
+
+_DECODE = ("KvCache", "new_kv_cache", "prism_kv_append", "prism_kv_attention", "prism_kv_attention_workspace_bytes",
+           "prism_w4g_linear", "prism_token_logprobs")
+
+
+def __getattr__(name):
+    """The decode-step entry points live in decode.py, which imports torch; like
+    the functions above, that happens at their first use."""
+    if name in _DECODE:
+        from . import decode
+        for n in _DECODE:
+            globals()[n] = getattr(decode, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -83,6 +83,11 @@ typedef enum {
 #define PRISM_DEV_ERR_ID_RANGE  4u /* candidate id outside [0, V)             */
 #define PRISM_DEV_ERR_DUPLICATE 8u /* the same id twice in one position       */
 #define PRISM_DEV_ERR_ROW_RANGE 16u /* a row index outside the indexed matrix */
+#define PRISM_DEV_ERR_PAGE_RANGE 32u /* a page index outside [0, num_pages)   */
+#define PRISM_DEV_ERR_SEQ_RANGE 64u /* a sequence's length or offsets bad     */
+
+/* Largest top_k accepted by prism_token_logprobs. */
+#define PRISM_MAX_TOP_K 32
 
 /*
  * prism_quant_act -- per-token activation quantisation with SmoothQuant
@@ -482,6 +487,149 @@ int prism_candidate_softmax(const float *logits, const int32_t *cand_offsets,
 /* Bytes of workspace prism_candidate_readout needs for P positions, T
  * candidates and hidden size K: 0 for every shape in this implementation. */
 size_t prism_readout_workspace_bytes(int64_t P, int64_t T, int64_t K);
+
+/*
+ * ---- The decode step: one generated ("thought") token next to the linear
+ * layers above (StartLux-Prism: thought generation below a confidence gate;
+ * K/V rows shared by the branches of one evidence text).
+ *
+ * The K/V cache is paged.  A page holds the keys (or values) of `block`
+ * consecutive tokens of one sequence for every KV head:
+ *   k_codes, v_codes  [num_pages, H_kv, block, D] int8, dense, 16-byte aligned
+ *   k_scale, v_scale  [num_pages, H_kv] float32: a row's value is
+ *                     code * scale of its page and head
+ *   page_table        [S, max_pages] int32, row stride ld_table: page of a
+ *                     sequence's tokens [i * block, (i + 1) * block).  Full
+ *                     pages may be shared by several sequences (the branches
+ *                     of one evidence text); entries past a sequence's last
+ *                     token are not read.
+ *   seq_lens          [S] int32 token counts
+ *   block in {16, 32, 64, 128}, D in {64, 128, 256}, H_kv >= 1.
+ * The last page of a sequence is open while it holds fewer than `block`
+ * tokens; its rows are also kept in bf16,
+ *   k_open, v_open    [S, H_kv, block, D] bf16, dense, 16-byte aligned,
+ * so that a page's codes and scale depend on its tokens alone, not on the
+ * calls that brought them.  An open page belongs to one sequence.
+ *
+ * prism_kv_append -- append each sequence's new K/V rows.  For every page
+ * that gets rows: amax = max |x| over the page's rows so far (all D
+ * channels of one head), scale = RN(amax * RN(1 / 127)), code = clamp(rint_even(
+ * RN(x * f)), -127, 127) with f = RN(127 * RN(1 / amax)); amax < 2^-120 gives
+ * scale 0 and codes 0.
+ * Rows past the sequence's end are left as they are.
+ *   k_bf16, v_bf16    [T, H_kv, D] bf16, token stride ld?_t, head stride
+ *                     ld?_h (multiples of 8, 16-byte aligned bases)
+ *   seq_lens          tokens in the cache BEFORE the call (not changed)
+ *   cu_new            [S + 1] int32: sequence s gets rows cu_new[s] ..
+ *                     cu_new[s + 1] - 1 of k, v; NULL: row s (T == S)
+ *   max_new           a hint for the launch: the most rows of one sequence
+ *                     (results do not depend on it); >= 1
+ * Inputs must be finite.  A sequence whose length or offsets are malformed
+ * (negative, decreasing, beyond T or max_pages * block) sets
+ * PRISM_DEV_ERR_SEQ_RANGE and is not appended; a page index outside
+ * [0, num_pages) sets PRISM_DEV_ERR_PAGE_RANGE and that page is not written.
+ */
+int prism_kv_append(const void *k_bf16, int64_t ldk_t, int64_t ldk_h,
+                    const void *v_bf16, int64_t ldv_t, int64_t ldv_h,
+                    int8_t *k_codes, int8_t *v_codes, float *k_scale,
+                    float *v_scale, void *k_open, void *v_open,
+                    const int32_t *page_table, int64_t ld_table,
+                    const int32_t *seq_lens, const int32_t *cu_new, int64_t S,
+                    int64_t T, int64_t max_new, int64_t num_pages,
+                    int64_t max_pages, int64_t H_kv, int64_t D, int64_t block,
+                    int32_t *dev_error_word, void *cuda_stream);
+
+/*
+ * prism_kv_attention -- softmax attention of new queries over the cache.
+ * Query i of a sequence with n queries and length L (seq_lens: tokens in the
+ * cache INCLUDING the queries' own) stands at position p = L - n + i and sees
+ * the keys j < L with j <= p when causal, and j > p - window when window > 0
+ * (causal only).  Query head h reads KV head h / (H_q / H_kv):
+ *   out[t, h] = bf16( sum_j softmax_j(sm_scale * q[t, h] . k_j) * v_j )
+ *   lse[t, h] = ln sum_j exp(sm_scale * q[t, h] . k_j)
+ * A query that sees no key gives 0 and -inf.  Scores, the softmax's maximum
+ * and sum, and the weighted sums are binary32; the probabilities enter the
+ * tensor cores as binary16 (scaled by 2^12 below the running maximum), the
+ * codes exactly.  A sequence's outputs depend on its own queries, keys and
+ * lengths only, not on the other sequences of the call.
+ *   q_bf16, out_bf16  [T, H_q, D] bf16, strides as in prism_kv_append
+ *   lse               [T, H_q] float32 dense, or NULL
+ *   cu_q              [S + 1] int32 query offsets; NULL: one query each
+ *                     (T == S).  Rows of no sequence are not written.
+ *   max_q             the most queries of one sequence (1 <= max_q); a
+ *                     sequence with more sets PRISM_DEV_ERR_SEQ_RANGE
+ *   workspace         prism_kv_attention_workspace_bytes(...) bytes, 256-byte
+ *                     aligned, any contents
+ * A sequence with a malformed length or offsets, or a page index outside
+ * [0, num_pages) among the pages it reads, sets the error bit and gets NaN
+ * rows (none where its offsets are malformed).
+ */
+size_t prism_kv_attention_workspace_bytes(int64_t S, int64_t T, int64_t max_q,
+                                          int64_t max_pages, int64_t H_q,
+                                          int64_t H_kv, int64_t D,
+                                          int64_t block);
+int prism_kv_attention(const void *q_bf16, int64_t ldq_t, int64_t ldq_h,
+                       const int8_t *k_codes, const int8_t *v_codes,
+                       const float *k_scale, const float *v_scale,
+                       const int32_t *page_table, int64_t ld_table,
+                       const int32_t *seq_lens, const int32_t *cu_q,
+                       void *out_bf16, int64_t ldo_t, int64_t ldo_h, float *lse,
+                       float sm_scale, int causal, int64_t window, int64_t S,
+                       int64_t T, int64_t max_q, int64_t num_pages,
+                       int64_t max_pages, int64_t H_q, int64_t H_kv, int64_t D,
+                       int64_t block, void *workspace, size_t workspace_bytes,
+                       int32_t *dev_error_word, void *cuda_stream);
+
+/*
+ * prism_w4g_linear -- the W4A8 linear with a scale (and optionally an offset)
+ * for each group of `group` consecutive input channels of an output channel:
+ *   w[n, k]   = group_scale[n, k / group] * code[n, k] + group_offset[n, k / group]
+ *   out[m, n] = bf16( a_scale[m] * sum_k q[m, k] w[n, k] + residual[m, n] )
+ * The sums over a group, sum_k q * code and sum_k q, are exact integers; they
+ * are scaled and added over the groups in binary32, in an order that depends
+ * on K and group alone.  Meant for the few token rows of decode steps; more
+ * rows are taken 64 at a time.
+ *   q, ldq         [M, K] int8 codes in [-127, 127], a_scale [M] float32
+ *                  (prism_quant_act); ldq % 16 == 0, 16-byte aligned
+ *   w4, ldw4       [N, K / 2] packed bytes as in prism_w4a8_linear
+ *                  (ldw4 % 16 == 0, 16-byte aligned)
+ *   group_scale    [N, K / group] binary16, row stride lds elements
+ *   group_offset   the same, row stride ldb, or NULL for none
+ *   residual, out  bf16 [M, N], row strides ldr, ldo; residual may be NULL or
+ *                  out itself
+ *   group in {32, 64, 128}; K % group == 0, K <= PRISM_MAX_K.
+ */
+int prism_w4g_linear(const int8_t *q, int64_t ldq, const float *a_scale,
+                     const uint8_t *w4, int64_t ldw4,
+                     const uint16_t *group_scale, int64_t lds,
+                     const uint16_t *group_offset, int64_t ldb,
+                     const void *residual_bf16, int64_t ldr, void *out_bf16,
+                     int64_t ldo, int64_t M, int64_t N, int64_t K,
+                     int64_t group, void *cuda_stream);
+
+/*
+ * prism_token_logprobs -- log probabilities of given tokens under
+ * full-vocabulary logits, with the entropy and the top alternatives:
+ *   lse        = ln sum_v exp(x_v)
+ *   logprobs   [R, n_ids] float32: x[r, token_ids[r, i]] - lse
+ *   entropy    [R] float32: -sum_v p_v ln p_v (0 ln 0 = 0), or NULL
+ *   top_ids    [R, top_k] int32, top_logprobs [R, top_k] float32: the largest
+ *              logits in falling order, equal ones by rising id
+ *   logits     [R, V], float32 (logits_f32 != 0) or bf16, row stride ldl
+ *              elements, any alignment of its element type; -inf is a masked
+ *              token
+ *   token_ids  [R, n_ids] int32, row stride ld_ids; an id outside [0, V) sets
+ *              PRISM_DEV_ERR_ID_RANGE and gives NaN
+ * A row without a finite maximum (all -inf, a NaN or +inf among its logits)
+ * gives NaN and top_ids -1.  A row's outputs do not depend on the other rows.
+ *   0 <= top_k <= min(V, PRISM_MAX_TOP_K); V < 2^31; R < 2^31 / 8.
+ */
+int prism_token_logprobs(const void *logits, int logits_f32, int64_t ldl,
+                         const int32_t *token_ids, int64_t ld_ids,
+                         int64_t n_ids, int64_t R, int64_t V, int64_t top_k,
+                         float *logprobs, float *entropy, int32_t *top_ids,
+                         float *top_logprobs, int32_t *dev_error_word,
+                         void *cuda_stream);
 
 /* Human-readable text for a prism_status value (static storage). */
 const char *prism_status_string(int status);
