@@ -20,7 +20,7 @@ int check_cache(const int8_t* k_codes, const int8_t* v_codes, const float* k_sca
   while ((1LL << shift) < block && shift < 8) ++shift;
   if ((1LL << shift) != block || block < 16 || block > 128) return PRISM_ERR_UNSUPPORTED;
   if (D != 64 && D != 128 && D != 256) return PRISM_ERR_UNSUPPORTED;
-  if (S > (1 << 24) || H > (1 << 16) || num_pages > kInt31 || max_pages > (kInt31 >> shift)) return PRISM_ERR_UNSUPPORTED;
+  if (S > (1 << 24) || H > 65535 || num_pages > kInt31 || max_pages > (kInt31 >> shift)) return PRISM_ERR_UNSUPPORTED;
   if (!aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
       !aligned(page_table, 4) || !aligned(seq_lens, 4))
     return PRISM_ERR_ALIGNMENT;

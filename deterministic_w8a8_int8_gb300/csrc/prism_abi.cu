@@ -21,7 +21,8 @@ struct AttrEntry {
   const void* kernel;
   int bytes;
 };
-AttrEntry g_attr[kMaxDevices][8];
+constexpr int kMaxKernels = 32;
+AttrEntry g_attr[kMaxDevices][kMaxKernels];
 int g_attr_n[kMaxDevices];
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -37,7 +38,7 @@ cudaError_t ensure_smem_attr(const void* kernel, int bytes) {
     if (g_attr[dev][i].kernel == kernel && g_attr[dev][i].bytes >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  if (g_attr_n[dev] < 8) g_attr[dev][g_attr_n[dev]++] = AttrEntry{kernel, bytes};
+  if (g_attr_n[dev] < kMaxKernels) g_attr[dev][g_attr_n[dev]++] = AttrEntry{kernel, bytes};
   return cudaSuccess;
 }
 
