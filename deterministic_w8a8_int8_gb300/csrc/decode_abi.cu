@@ -20,7 +20,7 @@ int check_cache(const int8_t* k_codes, const int8_t* v_codes, const float* k_sca
   while ((1LL << shift) < block && shift < 8) ++shift;
   if ((1LL << shift) != block || block < 16 || block > 128) return PRISM_ERR_UNSUPPORTED;
   if (D != 64 && D != 128 && D != 256) return PRISM_ERR_UNSUPPORTED;
-  if (S > (1 << 24) || H > 65535 || num_pages > kInt31 || max_pages > (kInt31 >> shift)) return PRISM_ERR_UNSUPPORTED;
+  if (S > (1 << 24) || H > 32767 || num_pages > kInt31 || max_pages > (kInt31 >> shift)) return PRISM_ERR_UNSUPPORTED;
   if (!aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
       !aligned(page_table, 4) || !aligned(seq_lens, 4))
     return PRISM_ERR_ALIGNMENT;
@@ -151,7 +151,7 @@ int prism_w4g_linear(const int8_t* q, int64_t ldq, const float* a_scale, const u
     return PRISM_ERR_INVALID_ARG;
   if (group != 32 && group != 64 && group != 128) return PRISM_ERR_UNSUPPORTED;
   if (K % group != 0) return PRISM_ERR_INVALID_ARG;
-  if (K > PRISM_MAX_K || N > kInt31 || M > kInt31) return PRISM_ERR_UNSUPPORTED;
+  if (K > PRISM_MAX_K || N > kInt31 / 8 || M > 65535 * 64) return PRISM_ERR_UNSUPPORTED;
   if (ldq < K || ldw4 < K / 2 || lds < K / group || ldo < N || (group_offset != nullptr && ldb < K / group) ||
       (residual_bf16 != nullptr && ldr < N))
     return PRISM_ERR_INVALID_ARG;

@@ -1,73 +1,152 @@
 // kv_append.cu -- append K/V rows to the paged int8 cache, one scale per
 // (page, head).
+//
+// A page's codes and scale are a function of its rows: amax over the rows, one
+// scale, codes by one factor.  The rows of a sequence's open page are kept in
+// bf16 as well, so that a row that raises amax can be followed by a fresh
+// quantisation of the whole page.  A row that does not raise it (all but
+// ln(block) of a page's rows, for values in random order) leaves the other
+// codes as they are: then only the new rows are written, and the page's amax
+// is read back from its scale (a bf16 number; amax * RN(1/127) keeps 23 bits
+// of it).
+//
+// Bytes: 2 in and 1 out per value, 2 more out for the rows of a page that
+// stays open -- HBM-bound for prompts; one generated token is a chain of four
+// dependent reads (offsets, page, scale, rows of a raised page).  One CTA per
+// (sequence, page, head, K or V): a page's rows stay in registers between the
+// maximum and the codes.
 #include "decode.cuh"
 
 namespace prism {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 
 // scale = amax * RN(1/127) and code = rint(x * (127 * RN(1/amax))): one
 // reciprocal for a page instead of two divisions; every step binary32 RN, so
 // a page's codes are a fixed function of its rows.
-__device__ __forceinline__ float page_scale(float amax) { return __fmul_rn(amax, 1.0f / 127.0f); }
-__device__ __forceinline__ float code_factor(float amax) { return __fmul_rn(__frcp_rn(amax), 127.0f); }
+__device__ __forceinline__ float page_scale(float amax) {
+  return amax >= 0x1p-120f ? __fmul_rn(amax, 1.0f / 127.0f) : 0.0f;
+}
+__device__ __forceinline__ float code_factor(float amax) {
+  return amax >= 0x1p-120f ? __fmul_rn(__frcp_rn(amax), 127.0f) : 0.0f;
+}
+__device__ __forceinline__ float max8(const uint4& v, float m) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+  return m;
+}
+__device__ __forceinline__ uint2 codes8(const uint4& v, float f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int lo = max(-127, min(127, __float2int_rn(__fmul_rn(bf16_lo(w[i]), f))));
+    const int hi = max(-127, min(127, __float2int_rn(__fmul_rn(bf16_hi(w[i]), f))));
+    c[i >> 1] |= ((static_cast<uint32_t>(lo) & 0xffu) | ((static_cast<uint32_t>(hi) & 0xffu) << 8)) << (16 * (i & 1));
+  }
+  return make_uint2(c[0], c[1]);
+}
 
-// One CTA per (sequence, head, K or V) walks the pages that get rows.
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ KvAppendArgs a) {
+// NV: 16-byte pieces of a page's bf16 rows per thread.
+template <int NV>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ KvAppendArgs a, int row_shift) {
   __shared__ float s_red[kThreads / 32];
   pdl_trigger();
   pdl_wait();
   const KvPages& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int s = blockIdx.x, h = blockIdx.y;
-  const bool is_v = blockIdx.z != 0;
+  const int s = blockIdx.x, h = blockIdx.y >> 1;
+  const bool is_v = blockIdx.y & 1;
   SeqSpan sp;
   if (!seq_span(c, a.cu_new, a.T, s, false, sp)) {
-    if (tid == 0 && a.err != nullptr) atomicOr(a.err, PRISM_DEV_ERR_SEQ_RANGE);
+    if (tid == 0 && blockIdx.y == 0 && blockIdx.z == 0 && a.err != nullptr) atomicOr(a.err, PRISM_DEV_ERR_SEQ_RANGE);
     return;
   }
   if (sp.n == 0) return;
-  const uint16_t* rows = is_v ? a.v : a.k;
-  const int64_t ld_t = is_v ? a.ldv_t : a.ldk_t, ld_h = is_v ? a.ldv_h : a.ldk_h;
-  int8_t* codes = is_v ? c.v_codes : c.k_codes;
+  const int64_t ld_t = is_v ? a.ldv_t : a.ldk_t;
+  // row of position p: rows + (p - before) * ld_t
+  const uint16_t* rows = (is_v ? a.v : a.k) + sp.b * ld_t + h * (is_v ? a.ldv_h : a.ldk_h);
   float* scales = is_v ? c.v_scale : c.k_scale;
-  uint16_t* open = (is_v ? a.v_open : a.k_open) + (static_cast<int64_t>(s) * c.H + h) * c.block * c.D;
+  uint16_t* open = (is_v ? a.v_open : a.k_open) + ((static_cast<int64_t>(s) * c.H + h) << c.block_shift) * c.D;
   const int64_t before = sp.len, after = sp.len + sp.n;
-  for (int64_t pb = before >> c.block_shift; (pb << c.block_shift) < after; ++pb) {
-    const int64_t p0 = pb << c.block_shift;
+  const int64_t first = before >> c.block_shift, open_page = after >> c.block_shift;
+  const int64_t pages = ((after - 1) >> c.block_shift) - first + 1;
+  // piece i of a page: row i >> row_shift, channels 8 (i mod 2^row_shift) on
+  const int col = (tid & ((1 << row_shift) - 1)) * 8;   // 2^row_shift divides kThreads: the same for a thread's pieces
+  for (int64_t j = blockIdx.z; j < pages; j += gridDim.z) {
+    const int64_t p0 = (first + j) << c.block_shift;
+    const int n_old = static_cast<int>(max(static_cast<int64_t>(0), before - p0));
     const int n_rows = static_cast<int>(min(static_cast<int64_t>(c.block), after - p0));
-    auto value = [&](int r, int d) {
-      const int64_t pos = p0 + r;
-      const uint16_t* src = pos < before ? open + static_cast<int64_t>(r) * c.D
-                                         : rows + (sp.b + pos - before) * ld_t + h * ld_h;
-      return src[d];
-    };
+    const int32_t page = c.table[s * c.ld_table + first + j];
+    uint4 x[NV];
     float amax = 0.0f;
-    for (int i = tid; i < n_rows * c.D; i += kThreads)
-      amax = fmaxf(amax, fabsf(bf16_bits_to_float(value(i / c.D, i % c.D))));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (lane == 0) s_red[warp] = amax;
-    __syncthreads();
-    amax = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
-    const bool zero = !(amax >= 0x1p-120f);
-    const float inv = zero ? 0.0f : code_factor(amax);
-    const int32_t page = c.table[s * c.ld_table + pb];
-    if (page < 0 || page >= c.num_pages) {
-      if (tid == 0 && a.err != nullptr) atomicOr(a.err, PRISM_DEV_ERR_PAGE_RANGE);
-    } else {
-      const int64_t ph = static_cast<int64_t>(page) * c.H + h;
-      if (tid == 0) scales[ph] = zero ? 0.0f : page_scale(amax);
-      int8_t* dst = codes + ph * c.block * c.D;
-      for (int i = tid; i < n_rows * c.D; i += kThreads) {
-        const float x = bf16_bits_to_float(value(i / c.D, i % c.D));
-        dst[i] = static_cast<int8_t>(max(-127, min(127, __float2int_rn(__fmul_rn(x, inv)))));
+    for (int i = 0; i < NV; ++i) {
+      const int r = (i * kThreads + tid) >> row_shift;
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r >= n_old && r < n_rows) x[i] = *reinterpret_cast<const uint4*>(rows + (p0 + r - before) * ld_t + col);
+    }
+    const bool page_ok = page >= 0 && page < c.num_pages;
+    const int64_t ph = static_cast<int64_t>(page) * c.H + h;
+    const float old_scale = page_ok && n_old > 0 ? scales[ph] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) amax = max8(x[i], amax);
+    auto block_max = [&](float m) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      __syncthreads();
+      if (lane == 0) s_red[warp] = m;
+      __syncthreads();
+      m = s_red[0];
+#pragma unroll
+      for (int w = 1; w < kThreads / 32; ++w) m = fmaxf(m, s_red[w]);
+      return m;
+    };
+    amax = block_max(amax);
+    int from = n_old;                     // first row whose codes are written
+    if (n_old > 0 && page_ok) {
+      if (page_scale(amax) <= old_scale) {
+        amax = bf16_bits_to_float(static_cast<uint16_t>(float_to_bf16_rne(__fmul_rn(old_scale, 127.0f))));
+      } else {                            // a new maximum: the page's earlier rows again
+        from = 0;
+        float old = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int r = (i * kThreads + tid) >> row_shift;
+          if (r < n_old) {
+            x[i] = *reinterpret_cast<const uint4*>(open + r * c.D + col);
+            old = max8(x[i], old);
+          }
+        }
+        amax = fmaxf(amax, block_max(old));
       }
     }
-    __syncthreads();   // the open rows and s_red have been read
-    if (after - p0 < c.block) {
-      for (int i = tid; i < n_rows * c.D; i += kThreads) open[i] = value(i / c.D, i % c.D);
+    if (page_ok) {
+      const float f = code_factor(amax);
+      if (tid == 0 && from == 0) scales[ph] = page_scale(amax);
+      int8_t* dst = (is_v ? c.v_codes : c.k_codes) + (ph << c.block_shift) * c.D + col;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int r = (i * kThreads + tid) >> row_shift;
+        if (r >= from && r < n_rows) *reinterpret_cast<uint2*>(dst + r * c.D) = codes8(x[i], f);
+      }
+    } else if (tid == 0 && a.err != nullptr) {
+      atomicOr(a.err, PRISM_DEV_ERR_PAGE_RANGE);
+    }
+    // ---- the open page's rows, by the CTA of the first page: only it reads
+    // the open buffer, and it has (block_max's barriers come after its reads)
+    if (j == 0) {
+      const int64_t o0 = open_page << c.block_shift;
+      const int begin = open_page == first ? n_old : 0, end = static_cast<int>(after - o0);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int r = (i * kThreads + tid) >> row_shift;
+        if (r >= begin && r < end)
+          *reinterpret_cast<uint4*>(open + r * c.D + col) =
+              open_page == first ? x[i] : *reinterpret_cast<const uint4*>(rows + (o0 + r - before) * ld_t + col);
+      }
     }
   }
 }
@@ -75,7 +154,17 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream) {
-  return launch_kernel(kv_append_kernel, dim3(a.c.S, a.c.H, 2), dim3(kThreads), 0, stream, true, a);
+  const int shift = a.c.D == 64 ? 3 : a.c.D == 128 ? 4 : 5;
+  const int pieces = a.c.block * a.c.D / 8 / kThreads;
+  auto kernel = pieces <= 1   ? kv_append_kernel<1>
+                : pieces <= 2 ? kv_append_kernel<2>
+                : pieces <= 4 ? kv_append_kernel<4>
+                : pieces <= 8 ? kv_append_kernel<8>
+                              : kv_append_kernel<16>;
+  // pages that max_new rows can touch; a sequence with more is walked in turns
+  const int64_t pages = std::min<int64_t>((a.max_new + 2 * a.c.block - 2) >> a.c.block_shift, 65535);
+  return launch_kernel(kernel, dim3(a.c.S, a.c.H * 2, static_cast<unsigned>(pages)), dim3(kThreads), 0, stream, true, a,
+                       shift);
 }
 
 }  // namespace prism
