@@ -3,9 +3,9 @@
 //
 // A page's codes and scale are a function of its rows: amax over the rows, one
 // scale, codes by one factor.  The rows of a sequence's open page are kept in
-// bf16 as well, so that a row that raises amax can be followed by a fresh
-// quantisation of the whole page.  A row that does not raise it (all but
-// ln(block) of a page's rows, for values in random order) leaves the other
+// bf16 as well: a row that raises amax is followed by a fresh quantisation of
+// the whole page, and so is the row that completes it.  Any other row (all but
+// ln(block) of a page's rows, for values in random order) leaves the earlier
 // codes as they are: then only the new rows are written, and the page's amax
 // is read back from its scale (a bf16 number; amax * RN(1/127) keeps 23 bits
 // of it).
@@ -107,9 +107,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     amax = block_max(amax);
     int from = n_old;                     // first row whose codes are written
     if (n_old > 0 && page_ok) {
-      if (page_scale(amax) <= old_scale) {
+      if (open_page == first && page_scale(amax) <= old_scale) {
         amax = bf16_bits_to_float(static_cast<uint16_t>(float_to_bf16_rne(__fmul_rn(old_scale, 127.0f))));
-      } else {                            // a new maximum: the page's earlier rows again
+      } else {                            // the page's earlier rows again
         from = 0;
         float old = 0.0f;
 #pragma unroll
