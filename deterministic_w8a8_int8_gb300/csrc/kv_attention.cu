@@ -3,28 +3,34 @@
 // with codes ck, cv and one scale ks, vs per (page, head).
 //
 // Work: a sequence's n queries times its G query heads per KV head are rows;
-// 16 rows make a tile, and the tile's keys are cut into pieces of at least
-// kMinChunk keys (split_count below: a function of the sequence's own length
-// and rows, so its result does not depend on the rest of the batch).  A
-// persistent grid walks the items (sequence, KV head, piece, tile); pieces of
-// one tile are joined by kv_combine_kernel in piece order.
+// 8 NQ rows make a tile, and the keys are cut into pieces of at least
+// kMinChunk (split_count below: a function of the sequence's own length and
+// rows, so its result does not depend on the rest of the batch).  A persistent
+// grid walks the items (sequence, KV head, piece, tile); the pieces of a row
+// are joined by kv_combine_kernel in piece order.
 //
 // One item is one CTA of four warps; warp w takes every fourth step of 8 KB of
 // K and V.  Each warp is on its own: its steps arrive through a private ring
 // of cp.async copies, it keeps its own running maximum, sum and output, and
 // the four are joined in shared memory at the end -- no barrier in the loop.
-//   S = Q K^T and O += P V run on mma.sync m16n8k16 with binary16 operands and
-// binary32 sums.  The codes widen exactly (byte ^ 0x80 under the exponent of
-// 1024, minus 1152).  The order of channels inside S's contraction and of the
-// output's columns is free, so lane (r, c) of a warp reads its operands as
-// 16-byte pieces: channels 16c.. of key r for K; channels 16r.. of keys 2c,
-// 2c+1, 2c+8, 2c+9 for V, whose two-key pairs a byte permute forms.  Queries
-// become binary16 after an exact power-of-two scale that puts the row's
-// largest channel at 2^13 (channels 2^27 below it lose bits: under 2^-38 of
-// the row's maximum).  Probabilities are rounded to binary16 (half a step is
-// 2^-11) with 2^12 as the value of the running maximum, so that keys down to
-// 2^-26 of it stay normal numbers; a page's vs enters as its ratio to the
-// largest vs seen so far.  Maxima, sums and outputs are binary32.
+//   S^T = K Q^T and O^T += V^T P^T run on mma.sync m16n8k16 with binary16
+// operands and binary32 sums: 16 keys (channels) by 8 rows, so that the one to
+// eight rows of a decode step fill the instruction, and P^T's operand is S^T's
+// result transposed by movmatrix.  The order of channels inside S's
+// contraction and of the output's rows is free, so lane (r, c) of a warp reads
+// its operands as 16-byte pieces: channels 16c.. of keys r, r + 8 for K;
+// channels 16r.. of keys 2c, 2c+1, 2c+8, 2c+9 for V, whose two-key pairs a
+// byte permute forms.
+//   Codes widen exactly.  K: byte ^ 0x80 as a binary16 subnormal, (code + 128)
+// 2^-24, and the sums start at -128 * 2^-24 * sum q.  V: the same byte under
+// the exponent of 1024, minus 1152 (a start value would cancel badly there:
+// the weights are all positive).  Queries become binary16 after an exact
+// power-of-two scale that puts the row's largest channel at 2^13 (channels
+// 2^27 below it lose bits: under 2^-38 of the row's maximum).  Probabilities
+// are rounded to binary16 (half a step is 2^-11) with 2^12 as the value of the
+// running maximum, so that keys down to 2^-26 of it stay normal numbers; a
+// page's vs enters as its ratio to the largest vs seen so far.  Maxima, sums
+// and outputs are binary32.
 #include <cuda_fp16.h>
 
 #include "decode.cuh"
@@ -34,11 +40,11 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 16;
+constexpr int kPlanRows = 32;          // rows that count as one in the plan of pieces
 constexpr int kStages = 2;
 constexpr int kStageBytes = 8192;      // K and V of one step of a warp
 constexpr int kMinChunk = 512;         // keys of a piece at least
-constexpr int kMaxSplit = 64;          // pieces x row tiles of a (sequence, KV head) at most
+constexpr int kMaxSplit = 64;          // pieces x plan tiles of a (sequence, KV head) at most
 constexpr float kPShift = 12.0f;       // log2 of the probability of the running maximum
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -57,8 +63,8 @@ int64_t max_split_rows(int64_t max_q, int64_t G, int64_t max_keys) {
   int64_t most = 0;
   for (int64_t tiles = 1; tiles <= kMaxSplit / 2; ++tiles) {
     const int64_t splits = split_count(max_keys, tiles);
-    if (splits > 1) most = std::max(most, splits * std::min(tiles * kRows, max_q * G));
-    if (tiles * kRows >= max_q * G) break;
+    if (splits > 1) most = std::max(most, splits * std::min(tiles * kPlanRows, max_q * G));
+    if (tiles * kPlanRows >= max_q * G) break;
   }
   return most;
 }
@@ -70,19 +76,20 @@ struct SeqPlan {
   int32_t lo, chunk;     // first key seen by any of its queries (rounded down to 64), keys of a piece
   bool bad;              // malformed length: its rows get NaN
 };
+template <int NQ>
 __device__ __forceinline__ int seq_items(const KvAttentionArgs& a, int s, SeqPlan& p) {
   const bool ok = seq_span(a.c, a.cu_q, a.T, s, true, p.sp);
   if (p.sp.b < 0 || p.sp.n < 0 || static_cast<int64_t>(p.sp.b) + p.sp.n > a.T) return -1;   // no rows to answer for
   p.bad = !ok || p.sp.n > a.max_q;
   p.rows = p.sp.n * a.G;
-  p.tiles = (p.rows + kRows - 1) / kRows;
+  p.tiles = (p.rows + 8 * NQ - 1) / (8 * NQ);
   p.splits = 1;
   p.lo = p.chunk = 0;
   if (!p.bad && p.rows > 0) {
     const int64_t first = a.window > 0 ? p.sp.len - p.sp.n + 1 - a.window : 0;
     p.lo = first > 0 ? static_cast<int32_t>(first) & ~63 : 0;
     const int64_t keys = p.sp.len - p.lo;
-    p.splits = split_count(keys, p.tiles);
+    p.splits = split_count(keys, (p.rows + kPlanRows - 1) / kPlanRows);
     p.chunk = static_cast<int32_t>((((keys + p.splits - 1) / p.splits) + 63) & ~63ll);
   }
   return p.tiles * p.splits * a.c.H;
@@ -108,6 +115,12 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// The 8x8 matrix of binary16 whose row r lies in lanes 4r .. 4r + 3, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
 // Bytes 0, 1 (sel 0x4140) or 2, 3 (sel 0x4342) of codes ^ 0x80 as a binary16 pair, exact.
 __device__ __forceinline__ uint32_t widen(uint32_t biased, uint32_t sel) {
   const uint32_t h = __byte_perm(biased, 0x64646464u, sel);
@@ -118,7 +131,8 @@ __device__ __forceinline__ uint32_t widen(uint32_t biased, uint32_t sel) {
 
 // Shared-memory place of 16-byte piece `ch` of key `key` in a step's K (V):
 // pieces of neighbouring keys are turned so that the eight lanes of a phase
-// (keys r, r + 1 for K; keys 0, 2, 4, 6 for V) touch all banks once.
+// (keys r, r + 1 for K; keys 0, 2, 4, 6 for V) touch all banks once (D = 64:
+// at most twice).
 template <int D>
 __device__ __forceinline__ int k_place(int key, int ch) {
   return key * D + ((D == 64 ? ch : ch ^ ((key & 1) << 2)) << 4);
@@ -128,27 +142,31 @@ __device__ __forceinline__ int v_place(int key, int ch) {
   return key * D + ((D == 64 ? ch ^ (key & 2) : ch ^ (key & 6)) << 4);
 }
 
-template <int D>
+template <int D, int NQ>
 struct Smem {
+  static constexpr bool kQ = NQ > 1;          // the queries' fragments lie in shared memory
+  static constexpr int kRows = 8 * NQ;
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kJoin = kWarps * kRows * D * 4;   // reuses the ring
   static constexpr int kBody = kRing > kJoin ? kRing : kJoin;
-  static constexpr int kQ = D == 256 ? kRows * D * 2 : 0;
-  static constexpr int kBytes = kBody + kQ;
+  static constexpr int kBytes = kBody + (kQ ? kRows * D * 2 : 0);
+  // CTAs an SM holds, by registers and shared memory
+  static constexpr int kCtas = D * NQ <= 256 && NQ < 4 ? 3 : 2;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3)
+template <int D, int NQ>
+__global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
     kv_attention_kernel(const __grid_constant__ KvAttentionArgs a, int64_t part_stride) {
   constexpr int U = kUnits<D>;
-  constexpr int kSteps16 = D / 16;       // k16 steps of S
-  constexpr int kTiles = D / 8;          // n8 tiles of O
-  constexpr bool kQSmem = D == 256;
+  constexpr int kSteps16 = D / 16;       // k16 steps of S^T, m16 tiles of O^T
+  constexpr bool kQSmem = Smem<D, NQ>::kQ;
+  constexpr int kRows = 8 * NQ;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_scan[kThreads];
   __shared__ int s_warp[kWarps];
   __shared__ float s_scale[kWarps][kStages][U][2];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  __shared__ float2 s_q[kRows];          // unit and start value of a row's scores
   pdl_trigger();
   pdl_wait();
   const KvPages& c = a.c;
@@ -167,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3)
       s0 += kThreads;
       if (s0 >= c.S) return;
       SeqPlan p;
-      int n = s0 + tid < c.S ? seq_items(a, s0 + tid, p) : 0;
+      int n = s0 + tid < c.S ? seq_items<NQ>(a, s0 + tid, p) : 0;
       if (blockIdx.x == 0 && s0 + tid < c.S && (n < 0 || (p.bad && n > 0)) && a.err != nullptr)
         atomicOr(a.err, PRISM_DEV_ERR_SEQ_RANGE);
       n = max(n, 0);
@@ -191,39 +209,21 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3)
       if (s_scan[at + o - 1] <= local) at += o;
     const int s = s0 + at;
     SeqPlan p;
-    seq_items(a, s, p);
+    seq_items<NQ>(a, s, p);
     int rest = local - (at > 0 ? s_scan[at - 1] : 0);
     const int tile = rest % p.tiles;
     rest /= p.tiles;
     const int split = rest % p.splits, hk = rest / p.splits;
 
-    // ---- rows of this lane, and the keys they see
+    // ---- the keys that the tile's rows see: row r stands at first_pos + r / G
     const int row0 = tile * kRows;
-    int32_t r_lo[2], r_hi[2];
-    const uint16_t* qp[2];
-    int32_t t_lo = INT32_MAX, t_hi = 0;   // what any row of the tile sees
-    const int32_t first_pos = static_cast<int32_t>(p.sp.len) - p.sp.n;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = row0 + lr + 8 * i;
-      const int tok = r / a.G, g = r - tok * a.G;
-      r_lo[i] = r_hi[i] = 0;
-      qp[i] = nullptr;
-      if (r < p.rows && !p.bad) {
-        const int32_t pos = first_pos + tok;
-        r_hi[i] = a.causal ? max(0, pos + 1) : static_cast<int32_t>(p.sp.len);
-        r_lo[i] = a.window > 0 && pos + 1 > a.window ? static_cast<int32_t>(pos + 1 - a.window) : 0;
-        qp[i] = a.q + static_cast<int64_t>(p.sp.b + tok) * a.ldq_t + static_cast<int64_t>(hk * a.G + g) * a.ldq_h;
-        t_hi = max(t_hi, r_hi[i]);
-        if (r_hi[i] > r_lo[i]) t_lo = min(t_lo, r_lo[i]);
-      }
-    }
-    t_hi = __reduce_max_sync(0xffffffffu, t_hi);
-    t_lo = __reduce_min_sync(0xffffffffu, t_lo);
-    // every row sees [a_lo, a_hi): steps inside need no mask
-    const int32_t a_hi = __reduce_min_sync(0xffffffffu, min(qp[0] ? r_hi[0] : INT32_MAX, qp[1] ? r_hi[1] : INT32_MAX));
-    const int32_t a_lo = __reduce_max_sync(0xffffffffu, max(r_lo[0], r_lo[1]));
-    const int32_t k_begin = max(p.lo + split * p.chunk, min(t_lo, t_hi) & ~63);
+    const int n_rows = min(kRows, p.rows - row0);
+    const int32_t len = static_cast<int32_t>(p.sp.len), first_pos = len - p.sp.n;
+    auto row_hi = [&](int r) { return r >= n_rows || p.bad ? 0 : a.causal ? max(0, first_pos + (row0 + r) / a.G + 1) : len; };
+    auto row_lo = [&](int hi) { return a.window > 0 && hi > a.window ? hi - static_cast<int32_t>(a.window) : 0; };
+    const int32_t a_hi = row_hi(0), t_hi = row_hi(n_rows - 1);   // rows rise: every row sees [a_lo, a_hi), some row [t_lo, t_hi)
+    const int32_t t_lo = row_lo(a_hi), a_lo = row_lo(t_hi);
+    const int32_t k_begin = max(p.lo + split * p.chunk, t_lo & ~63);
     const int64_t piece_end = static_cast<int64_t>(p.lo) + static_cast<int64_t>(split + 1) * p.chunk;
     const int32_t k_end = static_cast<int32_t>(min(static_cast<int64_t>(t_hi), piece_end));
     const int steps = k_end > k_begin ? (k_end - k_begin + kStepKeys<D> - 1) / kStepKeys<D> : 0;
@@ -276,57 +276,87 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3)
 #pragma unroll
     for (int st = 0; st < kStages - 1; ++st) issue(st);
 
-    // ---- queries as binary16 fragments: lane (r, c) holds channels 64 i + 16 c .. + 15 of rows r, r + 8
-    uint32_t qf[kQSmem ? 1 : kSteps16][4];
-    float q_unit[2];
-    uint4* sq = reinterpret_cast<uint4*>(smem + Smem<D>::kBody);
-    {
-      uint4 raw[2][D / 32];
-      float amax[2] = {0.0f, 0.0f};
+    // ---- queries as binary16 fragments: lane (r, c) holds channels 64 i + 16 c .. + 15 of row r
+    uint2 qf[kQSmem ? 1 : kSteps16];
+    float q_unit[NQ][2], q_start[NQ][2];
+    uint2* sq = reinterpret_cast<uint2*>(smem + Smem<D, NQ>::kBody);   // [step][NQ][lane]
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          raw[i][j] = qp[i] != nullptr ? *reinterpret_cast<const uint4*>(qp[i] + (j >> 1) * 64 + lc * 16 + (j & 1) * 8)
-                                       : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {raw[i][j].x, raw[i][j].y, raw[i][j].z, raw[i][j].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) amax[i] = fmaxf(amax[i], fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
-        }
-        amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], 1));
-        amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], 2));
+    for (int t = 0; t < NQ; ++t) {
+      if (kQSmem && (t & (kWarps - 1)) != warp) continue;   // fragments in shared memory: a tile of rows each
+      const int r = 8 * t + lr;
+      const uint16_t* qp = nullptr;
+      if (r < n_rows) {
+        const int tok = (row0 + r) / a.G, g = (row0 + r) - tok * a.G;
+        qp = a.q + static_cast<int64_t>(p.sp.b + tok) * a.ldq_t + static_cast<int64_t>(hk * a.G + g) * a.ldq_h;
       }
-      float f[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int e = static_cast<int>(__float_as_uint(amax[i]) >> 23);   // biased exponent of the row's maximum
-        const int fe = e == 255 || e == 0 ? 127 : min(253, 127 + 13 + 127 - e);
-        f[i] = __uint_as_float(static_cast<uint32_t>(fe) << 23);
-        q_unit[i] = __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) * a.scale_log2;
-      }
+      uint4 raw[D / 32];
+      float amax = 0.0f;
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
-        const uint32_t w0[4] = {raw[0][j].x, raw[0][j].y, raw[0][j].z, raw[0][j].w};
-        const uint32_t w1[4] = {raw[1][j].x, raw[1][j].y, raw[1][j].z, raw[1][j].w};
+        raw[j] = qp != nullptr ? *reinterpret_cast<const uint4*>(qp + (j >> 1) * 64 + lc * 16 + (j & 1) * 8)
+                               : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int be = static_cast<int>(__float_as_uint(amax) >> 23);   // biased exponent of the row's maximum
+      const int fe = be == 255 || be == 0 ? 127 : min(253, 127 + 13 + 127 - be);
+      const float f = __uint_as_float(static_cast<uint32_t>(fe) << 23);
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {   // k16 step 2 j + e: four channels of the lane
-          const uint32_t f0 = half2_bits(bf16_lo(w0[2 * e]) * f[0], bf16_hi(w0[2 * e]) * f[0]);
-          const uint32_t f1 = half2_bits(bf16_lo(w1[2 * e]) * f[1], bf16_hi(w1[2 * e]) * f[1]);
-          const uint32_t f2 = half2_bits(bf16_lo(w0[2 * e + 1]) * f[0], bf16_hi(w0[2 * e + 1]) * f[0]);
-          const uint32_t f3 = half2_bits(bf16_lo(w1[2 * e + 1]) * f[1], bf16_hi(w1[2 * e + 1]) * f[1]);
+          const uint2 b = make_uint2(half2_bits(bf16_lo(w[2 * e]) * f, bf16_hi(w[2 * e]) * f),
+                                     half2_bits(bf16_lo(w[2 * e + 1]) * f, bf16_hi(w[2 * e + 1]) * f));
+          const float2 v0 = __half22float2(*reinterpret_cast<const __half2*>(&b.x));
+          const float2 v1 = __half22float2(*reinterpret_cast<const __half2*>(&b.y));
+          sum += (v0.x + v0.y) + (v1.x + v1.y);
           if constexpr (kQSmem) {
-            if (warp == 0) sq[(2 * j + e) * 32 + lane] = make_uint4(f0, f1, f2, f3);
+            sq[((2 * j + e) * NQ + t) * 32 + lane] = b;
           } else {
-            qf[2 * j + e][0] = f0, qf[2 * j + e][1] = f1, qf[2 * j + e][2] = f2, qf[2 * j + e][3] = f3;
+            qf[2 * j + e] = b;
           }
         }
       }
-      if constexpr (kQSmem) __syncthreads();
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const float unit = __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) * a.scale_log2 * 0x1p24f;
+      const float start = sum * -0x1p-17f;   // -128 * 2^-24
+      if constexpr (kQSmem) {
+        if (lc == 0) s_q[r] = make_float2(unit, start);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          q_unit[t][i] = __shfl_sync(0xffffffffu, unit, (2 * lc + i) * 4);
+          q_start[t][i] = __shfl_sync(0xffffffffu, start, (2 * lc + i) * 4);
+        }
+      }
+    }
+    if constexpr (kQSmem) {
+      __syncthreads();
+#pragma unroll
+      for (int t = 0; t < NQ; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 v = s_q[8 * t + 2 * lc + i];
+          q_unit[t][i] = v.x;
+          q_start[t][i] = v.y;
+        }
     }
 
-    float o[kTiles][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, v_ref = 0.0f;
+    // lane (r, c) holds rows (queries) 2c, 2c + 1 of each tile of eight
+    float o[kSteps16][NQ][4], m[NQ][2], l[NQ][2], v_ref = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    for (int t = 0; t < NQ; ++t) {
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kSteps16; ++i) o[i][t][0] = o[i][t][1] = o[i][t][2] = o[i][t][3] = 0.0f;
+    }
 
     for (int st = 0; st < my_steps; ++st) {
       issue(st + kStages - 1);
@@ -336,13 +366,16 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3)
       const uint8_t* kb = ring + stage * kStageBytes;
       const uint8_t* vb = kb + kStageBytes / 2;
       const int32_t key0 = k_begin + (warp + kWarps * st) * kStepKeys<D>;
-      // ---- S: scores of 16 rows x step keys, in log2 units
-      float x[2 * U][4];
+      // ---- S^T: scores of the step's keys (rows r, r + 8 of a unit) and 8 NQ rows, in log2 units
+      float x[U][NQ][4];
       float vs[U], v_top = v_ref;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) x[2 * u + j][0] = x[2 * u + j][1] = x[2 * u + j][2] = x[2 * u + j][3] = 0.0f;
+        for (int t = 0; t < NQ; ++t) {
+          x[u][t][0] = x[u][t][2] = q_start[t][0];
+          x[u][t][1] = x[u][t][3] = q_start[t][1];
+        }
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
           uint4 kw[2];
@@ -351,85 +384,96 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3)
             kw[j] = *reinterpret_cast<const uint4*>(kb + u * 16 * D + k_place<D>(j * 8 + lr, 4 * i + lc));
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            uint4 qv;
-            if constexpr (kQSmem) {
-              qv = sq[(4 * i + w) * 32 + lane];
-            } else {
-              qv = make_uint4(qf[4 * i + w][0], qf[4 * i + w][1], qf[4 * i + w][2], qf[4 * i + w][3]);
-            }
+            const uint32_t k0 = (w == 0 ? kw[0].x : w == 1 ? kw[0].y : w == 2 ? kw[0].z : kw[0].w) ^ 0x80808080u;
+            const uint32_t k1 = (w == 0 ? kw[1].x : w == 1 ? kw[1].y : w == 2 ? kw[1].z : kw[1].w) ^ 0x80808080u;
+            const uint32_t a0 = __byte_perm(k0, 0u, 0x4140u), a2 = __byte_perm(k0, 0u, 0x4342u);
+            const uint32_t a1 = __byte_perm(k1, 0u, 0x4140u), a3 = __byte_perm(k1, 0u, 0x4342u);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t b = (w == 0 ? kw[j].x : w == 1 ? kw[j].y : w == 2 ? kw[j].z : kw[j].w) ^ 0x80808080u;
-              mma_f16_16816(x[2 * u + j], qv.x, qv.y, qv.z, qv.w, widen(b, 0x4140u), widen(b, 0x4342u));
+            for (int t = 0; t < NQ; ++t) {
+              uint2 b;
+              if constexpr (kQSmem) {
+                b = sq[((4 * i + w) * NQ + t) * 32 + lane];
+              } else {
+                b = qf[4 * i + w];
+              }
+              mma_f16_16816(x[u][t], a0, a1, a2, a3, b.x, b.y);
             }
           }
         }
         const float ks = s_scale[warp][stage][u][0];
         vs[u] = s_scale[warp][stage][u][1];
         v_top = fmaxf(v_top, vs[u]);
-        const float f0 = ks * q_unit[0], f1 = ks * q_unit[1];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          x[2 * u + j][0] *= f0;
-          x[2 * u + j][1] *= f0;
-          x[2 * u + j][2] *= f1;
-          x[2 * u + j][3] *= f1;
+        for (int t = 0; t < NQ; ++t) {
+          const float f0 = ks * q_unit[t][0], f1 = ks * q_unit[t][1];
+          x[u][t][0] *= f0;
+          x[u][t][1] *= f1;
+          x[u][t][2] *= f0;
+          x[u][t][3] *= f1;
         }
       }
-      if (key0 < a_lo || key0 + kStepKeys<D> > a_hi) {   // the step's edge: keys a row does not see
+      if (key0 < a_lo || key0 + kStepKeys<D> > a_hi) {   // keys that a row does not see
 #pragma unroll
-        for (int j = 0; j < 2 * U; ++j)
+        for (int t = 0; t < NQ; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int32_t key = key0 + j * 8 + lc * 2 + (e & 1);
-            if (key < r_lo[e >> 1] || key >= r_hi[e >> 1]) x[j][e] = -INFINITY;
+          for (int i = 0; i < 2; ++i) {
+            const int32_t hi = row_hi(8 * t + 2 * lc + i), lo = row_lo(hi);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int32_t key = key0 + u * 16 + j * 8 + lr;
+                if (key < lo || key >= hi) x[u][t][2 * j + i] = -INFINITY;
+              }
           }
       }
       // ---- running maximum; the output is rescaled when it (or the value scale) grows
-      float al[2], base[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float t = x[0][2 * i];
-#pragma unroll
-        for (int j = 0; j < 2 * U; ++j) t = fmaxf(t, fmaxf(x[j][2 * i], x[j][2 * i + 1]));
-        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-        const float mn = fmaxf(m[i], t);
-        base[i] = mn == -INFINITY ? 0.0f : mn - kPShift;
-        al[i] = m[i] == -INFINITY ? 0.0f : ex2(m[i] - mn);
-        m[i] = mn;
-        l[i] *= al[i];
-      }
       const float v_inv = v_top >= 0x1p-126f ? __frcp_rn(v_top) : 0.0f;
-      if (v_top != v_ref) {
-        al[0] *= v_ref * v_inv;
-        al[1] *= v_ref * v_inv;
-        v_ref = v_top;
-      }
-      if (__any_sync(0xffffffffu, al[0] != 1.0f || al[1] != 1.0f)) {
+      const float v_al = v_top != v_ref ? v_ref * v_inv : 1.0f;
+      v_ref = v_top;
+      float base[NQ][2];
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-          o[i][0] *= al[0];
-          o[i][1] *= al[0];
-          o[i][2] *= al[1];
-          o[i][3] *= al[1];
+      for (int t = 0; t < NQ; ++t) {
+        float al[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float top = x[0][t][i];
+#pragma unroll
+          for (int u = 0; u < U; ++u) top = fmaxf(top, fmaxf(x[u][t][i], x[u][t][2 + i]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          const float mn = fmaxf(m[t][i], top);
+          base[t][i] = mn == -INFINITY ? 0.0f : mn - kPShift;
+          al[i] = m[t][i] == mn ? 1.0f : ex2(m[t][i] - mn);   // m = -inf: nothing to keep
+          m[t][i] = mn;
+          l[t][i] *= al[i];
+          al[i] *= v_al;
+        }
+        if (__any_sync(0xffffffffu, al[0] != 1.0f || al[1] != 1.0f)) {
+#pragma unroll
+          for (int i = 0; i < kSteps16; ++i) {
+            o[i][t][0] *= al[0];
+            o[i][t][1] *= al[1];
+            o[i][t][2] *= al[0];
+            o[i][t][3] *= al[1];
+          }
         }
       }
-      // ---- P and O += P V, a unit at a time
+      // ---- P^T and O^T += V^T P^T, a unit at a time
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        uint32_t pf[4];
+        uint32_t pf[NQ][2];
         const float vr = vs[u] * v_inv;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float* xj = x[2 * u + j];
-          const float p0 = ex2(xj[0] - base[0]), p1 = ex2(xj[1] - base[0]);
-          const float p2 = ex2(xj[2] - base[1]), p3 = ex2(xj[3] - base[1]);
-          l[0] += p0 + p1;
-          l[1] += p2 + p3;
-          pf[2 * j] = half2_bits(p0 * vr, p1 * vr);
-          pf[2 * j + 1] = half2_bits(p2 * vr, p3 * vr);
-        }
+        for (int t = 0; t < NQ; ++t)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float p0 = ex2(x[u][t][2 * j] - base[t][0]), p1 = ex2(x[u][t][2 * j + 1] - base[t][1]);
+            l[t][0] += p0;
+            l[t][1] += p1;
+            pf[t][j] = transpose8(half2_bits(p0 * vr, p1 * vr));
+          }
 #pragma unroll
         for (int h = 0; h < (D + 127) / 128; ++h) {
           constexpr int W = D == 64 ? 2 : 4;   // words of a lane's piece
@@ -438,25 +482,25 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3)
           for (int e = 0; e < 4; ++e) {
             const int key = 2 * lc + (e & 1) + 8 * (e >> 1);
             if constexpr (D == 64) {
-              const uint2 t = *reinterpret_cast<const uint2*>(vb + u * 16 * D + v_place<D>(key, lr >> 1) + (lr & 1) * 8);
-              vw[e][0] = t.x, vw[e][1] = t.y;
+              const uint2 v = *reinterpret_cast<const uint2*>(vb + u * 16 * D + v_place<D>(key, lr >> 1) + (lr & 1) * 8);
+              vw[e][0] = v.x, vw[e][1] = v.y;
             } else {
-              const uint4 t = *reinterpret_cast<const uint4*>(vb + u * 16 * D + v_place<D>(key, lr + 8 * h));
-              vw[e][0] = t.x, vw[e][1] = t.y, vw[e][2] = t.z, vw[e][3] = t.w;
+              const uint4 v = *reinterpret_cast<const uint4*>(vb + u * 16 * D + v_place<D>(key, lr + 8 * h));
+              vw[e][0] = v.x, vw[e][1] = v.y, vw[e][2] = v.z, vw[e][3] = v.w;
             }
           }
 #pragma unroll
-          for (int w = 0; w < W; ++w) {
-            const uint32_t a0 = __byte_perm(vw[0][w], vw[1][w], 0x5140u) ^ 0x80808080u;
-            const uint32_t a1 = __byte_perm(vw[0][w], vw[1][w], 0x7362u) ^ 0x80808080u;
-            const uint32_t b0 = __byte_perm(vw[2][w], vw[3][w], 0x5140u) ^ 0x80808080u;
-            const uint32_t b1 = __byte_perm(vw[2][w], vw[3][w], 0x7362u) ^ 0x80808080u;
-            float(*ot)[4] = o + h * 16 + 4 * w;
-            mma_f16_16816(ot[0], pf[0], pf[1], pf[2], pf[3], widen(a0, 0x4140u), widen(b0, 0x4140u));
-            mma_f16_16816(ot[1], pf[0], pf[1], pf[2], pf[3], widen(a0, 0x4342u), widen(b0, 0x4342u));
-            mma_f16_16816(ot[2], pf[0], pf[1], pf[2], pf[3], widen(a1, 0x4140u), widen(b1, 0x4140u));
-            mma_f16_16816(ot[3], pf[0], pf[1], pf[2], pf[3], widen(a1, 0x4342u), widen(b1, 0x4342u));
-          }
+          for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {      // channels 4 w + 2 j, + 1 of the lane's piece
+              const uint32_t sel = j == 0 ? 0x5140u : 0x7362u;
+              const uint32_t lo = __byte_perm(vw[0][w], vw[1][w], sel) ^ 0x80808080u;
+              const uint32_t hi = __byte_perm(vw[2][w], vw[3][w], sel) ^ 0x80808080u;
+              const uint32_t a0 = widen(lo, 0x4140u), a1 = widen(lo, 0x4342u);
+              const uint32_t a2 = widen(hi, 0x4140u), a3 = widen(hi, 0x4342u);
+#pragma unroll
+              for (int t = 0; t < NQ; ++t) mma_f16_16816(o[h * 8 + 2 * w + j][t], a0, a1, a2, a3, pf[t][0], pf[t][1]);
+            }
         }
       }
       __syncwarp();   // the stage is free for the copy that the next turn issues
@@ -465,36 +509,39 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3)
     // ---- join the four warps
     cp_async_wait<0>();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-    }
+    for (int t = 0; t < NQ; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 4);
+        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 8);
+        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 16);
+      }
     const bool bad = __syncthreads_or(bad_page) || p.bad;   // and every warp is done with the ring
     float* so = reinterpret_cast<float*>(smem) + warp * kRows * D;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = lr + 8 * i;
-      if (lc == 0) s_m[warp][r] = m[i], s_l[warp][r] = l[i];
-      constexpr int kPiece = D == 64 ? 8 : 16;   // consecutive channels of an output column
+    for (int t = 0; t < NQ; ++t)
 #pragma unroll
-      for (int h = 0; h < (D + 127) / 128; ++h)
+      for (int i = 0; i < 2; ++i) {
+        const int r = 8 * t + 2 * lc + i;
+        if (lr == 0) s_m[warp][r] = m[t][i], s_l[warp][r] = l[t][i];
+        constexpr int kPiece = D == 64 ? 8 : 16;   // consecutive channels of a lane
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int h = 0; h < (D + 127) / 128; ++h)
 #pragma unroll
-          for (int t = 0; t < kPiece; t += 4) {
-            float(*ot)[4] = o + h * 16 + t;
-            *reinterpret_cast<float4*>(so + r * D + h * 128 + (2 * lc + n) * kPiece + t) =
-                make_float4(ot[0][2 * i + n] * v_ref, ot[1][2 * i + n] * v_ref, ot[2][2 * i + n] * v_ref,
-                            ot[3][2 * i + n] * v_ref);
+          for (int e = 0; e < kPiece; e += 4) {
+            const float* o0 = o[h * 8 + e / 2][t];
+            const float* o1 = o[h * 8 + e / 2 + 1][t];
+            if (r < n_rows)
+              *reinterpret_cast<float4*>(so + r * D + h * 128 + lr * kPiece + e) =
+                  make_float4(o0[i] * v_ref, o0[2 + i] * v_ref, o1[i] * v_ref, o1[2 + i] * v_ref);
           }
-    }
+      }
     __syncthreads();
     if (bad && tid == 0 && !p.bad && a.err != nullptr) atomicOr(a.err, PRISM_DEV_ERR_PAGE_RANGE);
     const float nanf = __uint_as_float(0x7fc00000u);
     float* part = static_cast<float*>(a.ws);
-    for (int i = tid; i < kRows * (D / 4); i += kThreads) {
+    for (int i = tid; i < n_rows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-      if (row0 + r >= p.rows) break;
       float mx = s_m[0][r];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][r]);
@@ -510,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3)
         y.z = fmaf(f, v.z, y.z);
         y.w = fmaf(f, v.w, y.w);
       }
-      const int tok = (row0 + r) / a.G, h = hk * a.G + (row0 + r) % a.G;
+      const int tok = (row0 + r) / a.G, h = hk * a.G + (row0 + r) - tok * a.G;
       if (p.splits == 1) {
         const float inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
         uint2 w = make_uint2(float_to_bf16_rne(y.x * inv) | float_to_bf16_rne(y.y * inv) << 16,
@@ -527,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3)
         if (d == 0) ps[0] = bad ? nanf : mx, ps[1] = sum;
       }
     }
-    __syncthreads();   // s_m, s_l, the ring and s_scan are free again
+    __syncthreads();   // s_m, s_l, s_q, the ring and s_scan are free again
   }
 }
 
@@ -544,7 +591,7 @@ __global__ void __launch_bounds__(kThreads)
   const int hk = blockIdx.y, r = blockIdx.z;
   const int s = blockIdx.x;
   SeqPlan p;
-  if (seq_items(a, s, p) <= 0 || p.splits == 1 || r >= p.rows) return;
+  if (seq_items<1>(a, s, p) <= 0 || p.splits == 1 || r >= p.rows) return;
   const float* part = static_cast<const float*>(a.ws) +
                       ((static_cast<int64_t>(s) * a.c.H + hk) * part_stride + r) * (D + 4);
   const int64_t step = static_cast<int64_t>(p.rows) * (D + 4);
@@ -593,21 +640,32 @@ __global__ void __launch_bounds__(kThreads)
     a.lse[t * a.Hq + h] = nan ? nanf : mx == -INFINITY ? mx : (mx - kPShift + log2f(sum)) * kLn2;
 }
 
-template <int D>
-cudaError_t launch_d(const KvAttentionArgs& a, cudaStream_t stream) {
+template <int D, int NQ>
+cudaError_t launch_nq(const KvAttentionArgs& a, cudaStream_t stream) {
+  using M = Smem<D, NQ>;
   const int64_t max_keys = a.c.max_pages << a.c.block_shift;
   const int64_t part_stride = max_split_rows(a.max_q, a.G, max_keys);
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kv_attention_kernel<D>), Smem<D>::kBytes);
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kv_attention_kernel<D, NQ>), M::kBytes);
   if (e != cudaSuccess) return e;
   // persistent: as many CTAs as the SMs hold, or as the call can have items
-  const int64_t tiles = a.T * a.G / kRows + a.c.S;
-  const int64_t items = std::max(tiles, static_cast<int64_t>(a.c.S) * split_count(max_keys, 1)) * a.c.H;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sm_count() * (D == 256 ? 2 : 3)));
-  e = launch_kernel(kv_attention_kernel<D>, dim3(grid), dim3(kThreads), Smem<D>::kBytes, stream, true, a, part_stride);
+  const int64_t tiles = a.T * a.G / M::kRows + a.c.S;
+  const int64_t items = (tiles + static_cast<int64_t>(a.c.S) * (kMaxSplit * kPlanRows / M::kRows)) * a.c.H;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sm_count() * M::kCtas));
+  e = launch_kernel(kv_attention_kernel<D, NQ>, dim3(grid), dim3(kThreads), M::kBytes, stream, true, a, part_stride);
   if (e != cudaSuccess || part_stride == 0) return e;
-  const int64_t rows = std::min<int64_t>(a.max_q * a.G, kMaxSplit / 2 * kRows);
+  const int64_t rows = std::min<int64_t>(a.max_q * a.G, kMaxSplit / 2 * kPlanRows);
   return launch_kernel(kv_combine_kernel<D>, dim3(a.c.S, a.c.H, static_cast<unsigned>(rows)), dim3(kThreads), 0, stream,
                        true, a, part_stride);
+}
+
+// Rows of a tile: as many as one sequence can have, up to 32 (16 for D = 256,
+// by the registers of the output).  A row's bits do not depend on the choice.
+template <int D>
+cudaError_t launch_d(const KvAttentionArgs& a, cudaStream_t stream) {
+  const int64_t rows = a.max_q * a.G;
+  if (rows <= 8) return launch_nq<D, 1>(a, stream);
+  if (rows <= 16 || D == 256) return launch_nq<D, 2>(a, stream);
+  return launch_nq<D, D == 256 ? 2 : 4>(a, stream);
 }
 
 }  // namespace
