@@ -40,11 +40,13 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kJoinThreads = 256;
 constexpr int kPlanRows = 32;          // rows that count as one in the plan of pieces
 constexpr int kStages = 2;
 constexpr int kStageBytes = 8192;      // K and V of one step of a warp
-constexpr int kMinChunk = 512;         // keys of a piece at least
-constexpr int kMaxSplit = 64;          // pieces x plan tiles of a (sequence, KV head) at most
+constexpr int kMinChunk = 1024;        // keys of a piece at least
+constexpr int kMaxSplit = 128;         // pieces of a row at most
+constexpr int kFill = 456;             // items that one sequence is cut into where it has the keys: three on each of 152 SMs
 constexpr float kPShift = 12.0f;       // log2 of the probability of the running maximum
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -53,17 +55,20 @@ constexpr int kUnits = kStageBytes / (2 * 16 * D);   // 16-key units of a step: 
 template <int D>
 constexpr int kStepKeys = 16 * kUnits<D>;
 
-__host__ __device__ __forceinline__ int split_count(int64_t keys, int64_t tiles) {
-  const int64_t cap = tiles >= kMaxSplit ? 1 : kMaxSplit / tiles;
-  const int64_t n = (keys + kMinChunk - 1) / kMinChunk;
-  return static_cast<int>(n < 1 ? 1 : n > cap ? cap : n);
+// Pieces of the keys of a sequence with so many plan tiles of rows, H KV heads.
+__host__ __device__ __forceinline__ int split_count(int64_t keys, int64_t tiles, int64_t H) {
+  const int64_t cap = kFill / (tiles * H), n = (keys + kMinChunk - 1) / kMinChunk;
+  const int64_t m = cap > kMaxSplit ? kMaxSplit : cap;
+  return static_cast<int>(n > m ? (m < 1 ? 1 : m) : n < 1 ? 1 : n);
 }
-// Most (row, piece) pairs of one (sequence, KV head) that a call can split.
-int64_t max_split_rows(int64_t max_q, int64_t G, int64_t max_keys) {
+// Rows of one (sequence, KV head) that can be cut into pieces, and the most
+// (row, piece) pairs of it.
+int64_t max_split_rows(int64_t max_q, int64_t G, int64_t max_keys, int64_t H, int64_t* rows) {
   int64_t most = 0;
-  for (int64_t tiles = 1; tiles <= kMaxSplit / 2; ++tiles) {
-    const int64_t splits = split_count(max_keys, tiles);
-    if (splits > 1) most = std::max(most, splits * std::min(tiles * kPlanRows, max_q * G));
+  *rows = 0;
+  for (int64_t tiles = 1; split_count(max_keys, tiles, H) > 1; ++tiles) {
+    *rows = std::min(tiles * kPlanRows, max_q * G);
+    most = std::max(most, split_count(max_keys, tiles, H) * *rows);
     if (tiles * kPlanRows >= max_q * G) break;
   }
   return most;
@@ -89,7 +94,7 @@ __device__ __forceinline__ int seq_items(const KvAttentionArgs& a, int s, SeqPla
     const int64_t first = a.window > 0 ? p.sp.len - p.sp.n + 1 - a.window : 0;
     p.lo = first > 0 ? static_cast<int32_t>(first) & ~63 : 0;
     const int64_t keys = p.sp.len - p.lo;
-    p.splits = split_count(keys, (p.rows + kPlanRows - 1) / kPlanRows);
+    p.splits = split_count(keys, (p.rows + kPlanRows - 1) / kPlanRows, a.c.H);
     p.chunk = static_cast<int32_t>((((keys + p.splits - 1) / p.splits) + 63) & ~63ll);
   }
   return p.tiles * p.splits * a.c.H;
@@ -578,64 +583,72 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
   }
 }
 
-// Joins a row's pieces in piece order: one CTA per (sequence, KV head, row),
-// warp w takes every fourth piece.
+// Joins a row's pieces: one CTA per (sequence, KV head, row).  Thread i weighs
+// piece i; then D / 4 columns of threads by 1024 / D groups add every group-th
+// piece in order, and the groups are added in order.
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kJoinThreads)
     kv_combine_kernel(const __grid_constant__ KvAttentionArgs a, int64_t part_stride) {
-  constexpr int E = D / 32;
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
+  constexpr int kCols = D / 4, kGroups = kJoinThreads / kCols;
+  __shared__ float s_f[kJoinThreads], s_red[kJoinThreads / 32], s_sum[kJoinThreads / 32];
+  __shared__ float4 s_o[kJoinThreads];
+  static_assert(kMaxSplit <= kJoinThreads, "a thread for each piece");
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int hk = blockIdx.y, r = blockIdx.z;
-  const int s = blockIdx.x;
+  const int s = blockIdx.x, hk = blockIdx.y, r = blockIdx.z;
   SeqPlan p;
   if (seq_items<1>(a, s, p) <= 0 || p.splits == 1 || r >= p.rows) return;
   const float* part = static_cast<const float*>(a.ws) +
                       ((static_cast<int64_t>(s) * a.c.H + hk) * part_stride + r) * (D + 4);
   const int64_t step = static_cast<int64_t>(p.rows) * (D + 4);
-  float m = -INFINITY, l = 0.0f, o[E];
-  bool nan = false;
+  float pm = -INFINITY, pl = 0.0f;
+  if (tid < p.splits) pm = part[tid * step], pl = part[tid * step + 1];
+  const bool nan = __syncthreads_or(pm != pm);
+  float mx = pm;
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.0f;
-#pragma unroll 4
-  for (int i = warp; i < p.splits; i += kWarps) {
-    const float* ps = part + i * step;
-    const float pm = ps[0], pl = ps[1];
-    float v[E];
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (lane == 0) s_red[warp] = mx;
+  __syncthreads();
+  mx = s_red[0];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = ps[4 + e * 32 + lane];
-    nan |= pm != pm;
-    if (pm > -INFINITY) {
-      const float mn = fmaxf(m, pm), f0 = m == -INFINITY ? 0.0f : ex2(m - mn), f1 = ex2(pm - mn);
-      l = fmaf(l, f0, pl * f1);
+  for (int w = 1; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, s_red[w]);
+  const float f = pm == -INFINITY ? 0.0f : ex2(pm - mx);
+  s_f[tid] = f;
+  float l = f * pl;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], f0, v[e] * f1);
-      m = mn;
-    }
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) s_sum[warp] = l;
+  __syncthreads();
+  const int col = tid % kCols, group = tid / kCols;
+  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int i = group; i < p.splits; i += kGroups) {
+    const float4 v = *reinterpret_cast<const float4*>(part + i * step + 4 + col * 4);
+    const float w = s_f[i];
+    y.x = fmaf(w, v.x, y.x);
+    y.y = fmaf(w, v.y, y.y);
+    y.z = fmaf(w, v.z, y.z);
+    y.w = fmaf(w, v.w, y.w);
   }
-  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+  s_o[tid] = y;
+  __syncthreads();
+  if (group != 0) return;
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_o[warp][e * 32 + lane] = o[e];
-  nan = __syncthreads_or(nan);
-  float mx = s_m[0], sum = 0.0f, f[kWarps];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w]);
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    f[w] = s_m[w] == -INFINITY ? 0.0f : ex2(s_m[w] - mx);
-    sum = fmaf(f[w], s_l[w], sum);
+  for (int g = 1; g < kGroups; ++g) {
+    const float4 v = s_o[g * kCols + col];
+    y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
   }
+  float sum = s_sum[0];
+#pragma unroll
+  for (int w = 1; w < kJoinThreads / 32; ++w) sum += s_sum[w];
   const float nanf = __uint_as_float(0x7fc00000u), inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
   const int64_t t = p.sp.b + r / a.G;
   const int h = hk * a.G + r % a.G;
-  for (int d = tid; d < D; d += kThreads) {
-    float y = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) y = fmaf(f[w], s_o[w][d], y);
-    a.out[t * a.ldo_t + h * a.ldo_h + d] = static_cast<uint16_t>(nan ? kBf16NaN : float_to_bf16_rne(y * inv));
-  }
+  uint2 w = make_uint2(float_to_bf16_rne(y.x * inv) | float_to_bf16_rne(y.y * inv) << 16,
+                       float_to_bf16_rne(y.z * inv) | float_to_bf16_rne(y.w * inv) << 16);
+  if (nan) w = make_uint2(kBf16NaN * 0x10001u, kBf16NaN * 0x10001u);
+  *reinterpret_cast<uint2*>(a.out + t * a.ldo_t + h * a.ldo_h + col * 4) = w;
   if (tid == 0 && a.lse != nullptr)
     a.lse[t * a.Hq + h] = nan ? nanf : mx == -INFINITY ? mx : (mx - kPShift + log2f(sum)) * kLn2;
 }
@@ -644,18 +657,20 @@ template <int D, int NQ>
 cudaError_t launch_nq(const KvAttentionArgs& a, cudaStream_t stream) {
   using M = Smem<D, NQ>;
   const int64_t max_keys = a.c.max_pages << a.c.block_shift;
-  const int64_t part_stride = max_split_rows(a.max_q, a.G, max_keys);
+  int64_t split_rows;
+  const int64_t part_stride = max_split_rows(a.max_q, a.G, max_keys, a.c.H, &split_rows);
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kv_attention_kernel<D, NQ>), M::kBytes);
   if (e != cudaSuccess) return e;
+  // Not launched ahead of the previous kernel's end: a join that waits for
+  // these CTAs takes their places (64 ragged sequences: 85 us so, 65 us not).
   // persistent: as many CTAs as the SMs hold, or as the call can have items
   const int64_t tiles = a.T * a.G / M::kRows + a.c.S;
-  const int64_t items = (tiles + static_cast<int64_t>(a.c.S) * (kMaxSplit * kPlanRows / M::kRows)) * a.c.H;
+  const int64_t items = (tiles + (part_stride / M::kRows + kMaxSplit) * a.c.S) * a.c.H;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sm_count() * M::kCtas));
-  e = launch_kernel(kv_attention_kernel<D, NQ>, dim3(grid), dim3(kThreads), M::kBytes, stream, true, a, part_stride);
+  e = launch_kernel(kv_attention_kernel<D, NQ>, dim3(grid), dim3(kThreads), M::kBytes, stream, false, a, part_stride);
   if (e != cudaSuccess || part_stride == 0) return e;
-  const int64_t rows = std::min<int64_t>(a.max_q * a.G, kMaxSplit / 2 * kPlanRows);
-  return launch_kernel(kv_combine_kernel<D>, dim3(a.c.S, a.c.H, static_cast<unsigned>(rows)), dim3(kThreads), 0, stream,
-                       true, a, part_stride);
+  return launch_kernel(kv_combine_kernel<D>, dim3(a.c.S, a.c.H, static_cast<unsigned>(split_rows)), dim3(kJoinThreads), 0,
+                       stream, false, a, part_stride);
 }
 
 // Rows of a tile: as many as one sequence can have, up to 32 (16 for D = 256,
@@ -672,7 +687,8 @@ cudaError_t launch_d(const KvAttentionArgs& a, cudaStream_t stream) {
 
 size_t kv_attention_workspace_bytes(int64_t S, int64_t, int64_t max_q, int64_t max_pages, int64_t Hq, int64_t Hkv,
                                     int64_t D, int64_t block) {
-  return static_cast<size_t>(S * Hkv * max_split_rows(max_q, Hq / Hkv, max_pages * block)) * (D + 4) * 4;
+  int64_t rows;
+  return static_cast<size_t>(S * Hkv * max_split_rows(max_q, Hq / Hkv, max_pages * block, Hkv, &rows)) * (D + 4) * 4;
 }
 
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream) {
