@@ -5,19 +5,23 @@
 //   top k by (larger value, then lower id).
 //
 // Every logit is read once: V * 2 (4) bytes a row, HBM-bound for many rows and
-// a chain of latencies for one.  A row is one thread-block cluster (1 to 8
-// CTAs by V alone, so a row's bits do not depend on the call); thread t of
-// rank c copies the 8-logit pieces (i * ranks + c) * 512 + t into shared memory
-// (V up to 262144; longer rows are read again) and alone reads them there.
-//   Sums: a warp takes its own maximum m and adds 2^(x L - r), L = log2 e,
-// r = RN(m L) -- one fused multiply-add and one ex2 a logit, x L itself being
-// exact inside the former -- so nothing waits for the row's maximum; the
-// warps' (r, sum, weighted sum) are joined by the first CTA.  Sums are binary32
-// per thread, then fixed trees over lanes and warps.
+// a chain of latencies for one.  A row is cut into 1 to 8 parts by V alone, and
+// thread t of part c takes the 8-logit pieces (i * parts + c) * 512 + t as they
+// arrive.  With few rows each part is a CTA of the row's cluster; with many, a
+// CTA takes several parts or all of them in turn (a part's sums are the same
+// either way, so a row's bits do not depend on the call): 768 rows of 248000
+// take 185 us with eight CTAs a row, one row 7 us against 30 with one.
+//   Sums: a thread adds 2^y and y 2^y, y = x L - r, L = log2 e, against a
+// reference r = RN(L m), m the maximum of its first piece that has one -- one
+// fused multiply-add and one ex2 a logit, x L itself being exact inside the
+// former -- and takes a new reference only for a logit more than kSlack above
+// it.  The references are joined over lanes, warps and CTAs by fixed trees.
+// Everything is binary32.
 //   Alternatives: one exchange of 128 group maxima through distributed shared
 // memory gives every CTA, as the k-th largest of them, a bound that at least k
-// logits reach: for logits in no order about 1.2 k do, and these alone go to
-// the first CTA, which ranks them.  Where more than its list holds reach it
+// logits reach: for logits in no order about 1.2 k do.  The pieces of threads whose
+// maximum reaches it are read again (from L2) and these logits sent to the
+// first CTA, which ranks them.  Where more than its list holds reach the bound
 // (long ties, a row in rising order) every CTA extracts its own top k instead.
 #include <cuda_bf16.h>
 
@@ -29,15 +33,15 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kVec = 8;                       // logits of a piece
-constexpr int kPieces = 8;                    // pieces of a thread that stay in shared memory
 constexpr int kLogTile = 12;
 constexpr int kTile = 1 << kLogTile;          // logits of one piece of every thread
 static_assert(kTile == kThreads * kVec, "tile");
-constexpr int kMaxCluster = 8;
+constexpr int kMaxParts = 8;
 constexpr int kGroups = 128;                  // group maxima of a row
 constexpr int kList = 1024;                   // candidates the first CTA can take
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr float kFar = 1e37f;                 // beyond it x * log2(e) could leave binary32's range
+constexpr float kSlack = 27.0f;               // e^27 over the reference: far from binary32's limits
 
 typedef unsigned long long u64;
 
@@ -151,16 +155,16 @@ __device__ __forceinline__ Piece<F32> load_piece(const void* row, int64_t at, in
   return p;
 }
 
-// kHeld: the row fits the shared memory of its cluster.
-template <bool F32, bool kHeld>
-__global__ void __launch_bounds__(kThreads, F32 ? 1 : 3)
-    logprobs_kernel(const __grid_constant__ LogprobArgs a, int log_ctas) {
-  extern __shared__ __align__(16) uint4 s_row[];
+template <bool F32>
+__global__ void __launch_bounds__(kThreads, F32 ? 2 : 3)
+    logprobs_kernel(const __grid_constant__ LogprobArgs a, int log_parts, int log_ctas) {
   __shared__ __align__(16) float s_max[kGroups];
   __shared__ __align__(16) u64 s_list[kList];
-  __shared__ float s_part[kMaxCluster * kWarps][3];   // each warp's reference, sum and weighted sum
-  __shared__ float s_row_sum[3];
+  __shared__ float s_part[kMaxParts * kWarps][3];   // each warp's reference, sum and weighted sum
+  __shared__ float s_row_sum[4];
+  __shared__ float s_top[kMaxParts][kThreads];        // each thread's maximum of the CTA's parts
   __shared__ u64 s_best[kWarps];
+  __shared__ float s_far[kWarps][2];
   __shared__ uint32_t s_bound;
   __shared__ uint32_t s_count;
   pdl_trigger();
@@ -173,71 +177,58 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : 3)
                         : static_cast<const void*>(static_cast<const uint16_t*>(a.logits) + r * a.ldl);
   cluster_arrive();   // waited for before the first store into another CTA
   const bool aligned = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
-  const int tiles = static_cast<int>((a.V + kTile - 1) / kTile);
-  const int mine = (tiles - rank + ctas - 1) >> log_ctas;   // pieces of each thread
-  const int64_t first = static_cast<int64_t>(rank) * kTile + tid * kVec, stride = static_cast<int64_t>(ctas) * kTile;
-  // pieces that lie whole in an aligned row; at most one more is cut by V
-  const int whole = aligned && first + kVec <= a.V ? min(mine, static_cast<int>((a.V - kVec - first) >> (kLogTile + log_ctas)) + 1) : 0;
-  constexpr int kWords = F32 ? 2 : 1;        // 16-byte words of a piece
-  constexpr int kBytes = F32 ? 4 : 2;
-  uint4* held = s_row + tid;                 // word j of piece i: held[(i * kWords + j) * kThreads]
-  if constexpr (kHeld) {
-    const uint8_t* src = static_cast<const uint8_t*>(row) + first * kBytes;
-    uint32_t dst = smem_u32(held);
-    for (int i = 0; i < whole; ++i) {
-#pragma unroll
-      for (int j = 0; j < kWords; ++j) cp_async_16(dst + j * (kThreads * 16), src + j * 16, 16);
-      src += stride * kBytes;
-      dst += kWords * kThreads * 16;
-    }
-    cp_async_commit();
-    for (int i = whole; i < mine; ++i) {
-      const Piece<F32> p = load_piece<F32>(row, first + i * stride, a.V);
-#pragma unroll
-      for (int j = 0; j < kWords; ++j) held[(i * kWords + j) * kThreads] = p.w[j];
-    }
-    cp_async_wait<0>();
-  }
-  // f(piece, number) over the thread's pieces
-  auto each = [&](auto f) {
-    if constexpr (kHeld) {
-      const uint4* src = held;
-#pragma unroll 2
-      for (int i = 0; i < mine; ++i) {
-        Piece<F32> p;
-#pragma unroll
-        for (int j = 0; j < kWords; ++j) p.w[j] = src[j * kThreads];
-        src += kWords * kThreads;
-        f(p, i);
-      }
-    } else {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + first * kBytes);
-#pragma unroll 2
-      for (int i = 0; i < whole; ++i) {
-        Piece<F32> p;
-#pragma unroll
-        for (int j = 0; j < kWords; ++j) p.w[j] = __ldg(src + j);
-        src += stride * kBytes / 16;
-        f(p, i);
-      }
-      for (int i = whole; i < mine; ++i) f(load_piece<F32>(row, first + i * stride, a.V), i);
-    }
+  const int tiles = static_cast<int>((a.V + kTile - 1) / kTile), parts = 1 << log_parts;
+  const int64_t stride = static_cast<int64_t>(parts) * kTile;
+  struct Range {
+    int64_t first;     // the thread's first piece
+    int mine, whole;   // its pieces; those that lie whole in an aligned row (at most one more is cut by V)
   };
-  // ---- 1. maxima of the thread and its group (128 a row); the warp's sums of
-  // 2^y and y 2^y, y = x L - r for the warp's reference r
-  float t_max = -INFINITY;
-  each([&](const Piece<F32>& p, int) { t_max = fmaxf(t_max, p.top()); });
-  const int g_lanes = 4 * ctas;              // lanes of a group
-  float g_max = t_max;
-  for (int o = 1; o < g_lanes; o <<= 1) g_max = fmaxf(g_max, __shfl_xor_sync(0xffffffffu, g_max, o));
-  float m = g_max;
-  for (int o = g_lanes; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float ref = m == -INFINITY ? 0.0f : __fmul_rn(m, kLog2e);
-  float s = 0.0f, e = 0.0f;
-  if (m == -INFINITY || fabsf(m) < kFar) {
-    float s2 = 0.0f, e2 = 0.0f;
-    each([&](Piece<F32> p, int) {
+  auto range = [&](int part) {
+    Range g;
+    g.first = static_cast<int64_t>(part) * kTile + tid * kVec;
+    g.mine = (tiles - part + parts - 1) >> log_parts;
+    g.whole = aligned && g.first + kVec <= a.V
+                  ? min(g.mine, static_cast<int>((a.V - kVec - g.first) >> (kLogTile + log_parts)) + 1) : 0;
+    return g;
+  };
+  // f(piece, number) over the thread's pieces, kAhead of them in flight
+  auto each = [&](const Range& g, auto f) {
+    constexpr int kWords = F32 ? 2 : 1, kAhead = 4;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + g.first * (F32 ? 4 : 2));
+    const int64_t step = stride * (F32 ? 4 : 2) / 16;
+    for (int i0 = 0; i0 < g.whole; i0 += kAhead) {
+      Piece<F32> p[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (i0 + i < g.whole) {
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) p[i].w[j] = __ldg(src + i * step + j);
+        }
+      }
+      src += kAhead * step;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (i0 + i < g.whole) f(p[i], i0 + i);
+    }
+    for (int i = g.whole; i < g.mine; ++i) f(load_piece<F32>(row, g.first + i * stride, a.V), i);
+  };
+  if (tid == 0) s_count = 0, s_bound = 0xffffffffu;
+
+  // ---- 1. a part at a time: the thread's maximum and sums
+  for (int part = rank; part < parts; part += ctas) {
+    float limit = -INFINITY, ref = 0.0f, s = 0.0f, e = 0.0f, p_max = -INFINITY;
+    each(range(part), [&](Piece<F32> p, int) {
+      const float m = p.top();
+      p_max = fmaxf(p_max, m);
+      if (m > limit && fabsf(m) < kFar) {      // the first finite piece, or one far above the reference
+        const float to = __fmul_rn(m, kLog2e), d = limit == -INFINITY ? 0.0f : ref - to, f = ex2(d);
+        e = f * __fmaf_rn(s, d, e);
+        s *= f;
+        ref = to;
+        limit = m + kSlack;
+      }
       p.lift();
+      float s2 = 0.0f, e2 = 0.0f;
 #pragma unroll
       for (int i = 0; i < kVec; i += 2) {
         const float y0 = __fmaf_rn(p.get(i), kLog2e, -ref), y1 = __fmaf_rn(p.get(i + 1), kLog2e, -ref);
@@ -247,30 +238,30 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : 3)
         e = __fmaf_rn(q0, y0, e);
         e2 = __fmaf_rn(q1, y1, e2);
       }
+      s = __fadd_rn(s, s2);
+      e = __fadd_rn(e, e2);
     });
-    s = __fadd_rn(s, s2);
-    e = __fadd_rn(e, e2);
-  } else {   // a far maximum: differences first; the reference may be infinite, the row's join goes by m then
-    each([&](const Piece<F32>& p, int) {
+    s_top[part >> log_ctas][tid] = p_max;
+    // the group's maximum (128 groups a row), and the warp's reference and sums
+    const int g_lanes = 4 * parts;             // lanes of a group
+    for (int o = 1; o < g_lanes; o <<= 1) p_max = fmaxf(p_max, __shfl_xor_sync(0xffffffffu, p_max, o));
+    float w_ref = limit == -INFINITY ? -INFINITY : ref;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const float y = max_nan(__fmul_rn(__fsub_rn(p.get(i), m), kLog2e), -1000.0f), q = ex2(y);
-        s = __fadd_rn(s, q);
-        e = __fmaf_rn(q, y, e);
-      }
-    });
-  }
+    for (int o = 16; o > 0; o >>= 1) w_ref = fmaxf(w_ref, __shfl_xor_sync(0xffffffffu, w_ref, o));
+    {
+      const float d = limit == -INFINITY ? 0.0f : ref - w_ref, f = ex2(d);   // without a reference the sums are 0 or NaN
+      e = f * __fmaf_rn(s, d, e);
+      s *= f;
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, o);
-    e += __shfl_xor_sync(0xffffffffu, e, o);
-  }
-  if (tid == 0) s_count = 0, s_bound = 0xffffffffu;
-  cluster_wait();   // every CTA of the cluster runs
-  {
-    const int to = lane & (g_lanes - 1);     // lane j of a group writes rank j's copy
-    if (to < ctas) st_cluster(at_rank(&s_max[(rank * kThreads + tid) >> (2 + log_ctas)], to), g_max);
-    if (lane < 3) st_cluster(at_rank(&s_part[rank * kWarps + warp][lane], 0), lane == 0 ? m : lane == 1 ? s : e);
+    for (int o = 16; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      e += __shfl_xor_sync(0xffffffffu, e, o);
+    }
+    if (part == rank) cluster_wait();          // every CTA of the cluster runs
+    const int to = lane & (g_lanes - 1);       // lane j of a group writes rank j's copy
+    if (to < ctas) st_cluster(at_rank(&s_max[(part * kThreads + tid) >> (2 + log_parts)], to), p_max);
+    if (lane < 3) st_cluster(at_rank(&s_part[part * kWarps + warp][lane], 0), lane == 0 ? w_ref : lane == 1 ? s : e);
   }
   cluster_arrive();
   cluster_wait();
@@ -291,23 +282,28 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : 3)
     __syncthreads();
   }
 
-  // ---- 3. the logits that reach the bound go to the first CTA
+  // ---- 3. the logits that reach the bound go to the first CTA: the pieces of a
+  // thread whose maximum does are read again, two logits a lane of its warp
   const uint32_t count_at = at_rank(&s_count, 0);
   if (a.top_k > 0) {
     const float bound = key_value(static_cast<u64>(s_bound) << 32);
-    if (t_max >= bound) {
-      each([&](const Piece<F32>& p, int number) {
-        if (!(p.top() >= bound)) return;
-        const int64_t id = first + number * stride;
+    for (int part = rank; part < parts; part += ctas) {
+      uint32_t reach = __ballot_sync(0xffffffffu, s_top[part >> log_ctas][tid] >= bound);
+      for (; reach != 0; reach &= reach - 1) {
+        const int64_t at0 = static_cast<int64_t>(part) * kTile + (warp * 32 + __ffs(reach) - 1) * kVec + (lane & 3) * 2;
+        for (int64_t at = at0 + (lane >> 2) * stride; at < a.V; at += 8 * stride) {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          const float x = p.get(i);
-          if (x >= bound && id + i < a.V) {
-            const uint32_t at = add_cluster(count_at, 1);
-            if (at < kList) st_cluster(at_rank(&s_list[at], 0), order_key(x, static_cast<uint32_t>(id + i)));
+          for (int i = 0; i < 2; ++i) {
+            if (at + i >= a.V) break;
+            const float x = F32 ? __ldg(static_cast<const float*>(row) + at + i)
+                                : bf16_bits_to_float(__ldg(static_cast<const uint16_t*>(row) + at + i));
+            if (x >= bound) {
+              const uint32_t n = add_cluster(count_at, 1);
+              if (n < kList) st_cluster(at_rank(&s_list[n], 0), order_key(x, static_cast<uint32_t>(at + i)));
+            }
           }
         }
-      });
+      }
     }
   }
   cluster_arrive();
@@ -317,14 +313,17 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : 3)
     // every CTA's own top k: a thread offers its best, the winner looks for its next
     auto next = [&](u64 below) {
       u64 best = 0;
-      each([&](const Piece<F32>& p, int number) {
-        const int64_t id = first + number * stride;
+      for (int part = rank; part < parts; part += ctas) {
+      const Range g = range(part);
+      each(g, [&](const Piece<F32>& p, int number) {
+        const int64_t id = g.first + number * stride;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
           const u64 key = order_key(p.get(i), static_cast<uint32_t>(id + i));
           if (id + i < a.V && key < below && key > best) best = key;
         }
       });
+      }
       return best;
     };
     u64 offer = next(~0ull);
@@ -347,30 +346,28 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : 3)
   }
   cluster_arrive();   // the first CTA's count has been read
   if (rank == 0) {
-    // ---- 4. the row's reference and sums, and the outputs
+    // ---- 4. the row's maximum, reference and sums, and the outputs
     if (warp == 0) {
-      const int n = ctas * kWarps;
-      float wm[4], top = -INFINITY, sum = 0.0f, ent = 0.0f;
+      const int n = parts * kWarps;
+      float wr[4], top = -INFINITY, rr = -INFINITY, sum = 0.0f, ent = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        wm[i] = lane + 32 * i < n ? s_part[lane + 32 * i][0] : -INFINITY;
-        top = fmaxf(top, wm[i]);
+        top = fmaxf(top, s_max[lane + 32 * i]);
+        wr[i] = lane + 32 * i < n ? s_part[lane + 32 * i][0] : -INFINITY;
+        rr = fmaxf(rr, wr[i]);
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const bool far = !(fabsf(top) < kFar);
-      const float r = __fmul_rn(top, kLog2e);
+      for (int o = 16; o > 0; o >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        rr = fmaxf(rr, __shfl_xor_sync(0xffffffffu, rr, o));
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (lane + 32 * i < n) {
           const float ws = s_part[lane + 32 * i][1], we = s_part[lane + 32 * i][2];
-          // the warp's reference against the row's, in log2 units; a warp with a
-          // far maximum has it as it is (under a near one its terms are zero)
-          float d = far ? (wm[i] - top) * kLog2e : fabsf(wm[i]) < kFar ? __fsub_rn(__fmul_rn(wm[i], kLog2e), r) : -1000.0f;
-          d = max_nan(d, -1000.0f);
-          const float f = ex2(d);
+          const float d = wr[i] == -INFINITY ? 0.0f : wr[i] - rr, f = ex2(d);
           sum += f * ws;
-          ent += f * (we + d * ws);
+          ent += f * __fmaf_rn(ws, d, we);
         }
       }
 #pragma unroll
@@ -378,16 +375,36 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : 3)
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
         ent += __shfl_xor_sync(0xffffffffu, ent, o);
       }
-      if (lane == 0) s_row_sum[0] = top, s_row_sum[1] = sum, s_row_sum[2] = ent;
+      if (lane == 0) s_row_sum[0] = top, s_row_sum[1] = rr, s_row_sum[2] = sum, s_row_sum[3] = ent;
     }
     __syncthreads();
-    const float top = s_row_sum[0], sum = s_row_sum[1];
-    const bool ok = top > -INFINITY && top < INFINITY && sum == sum, far = !(fabsf(top) < kFar);
-    const float nanf = __uint_as_float(0x7fc00000u), log_sum = log2f(sum), ref_row = __fmul_rn(top, kLog2e);
-    // ln of the sum against the maximum itself: the reference's rounding taken off
-    const float logz = (far ? log_sum : log_sum - __fmaf_rn(top, kLog2e, -ref_row)) * kLn2;
+    const float top = s_row_sum[0];
+    float rr = s_row_sum[1], sum = s_row_sum[2], ent = s_row_sum[3];
+    const bool far = top > -INFINITY && top < INFINITY && !(fabsf(top) < kFar);
+    if (far) {   // a maximum near binary32's limits: the row once more, differences first
+      float fs = 0.0f, fe = 0.0f;
+      for (int64_t v = tid; v < a.V; v += kThreads) {
+        const float x = F32 ? static_cast<const float*>(row)[v] : bf16_bits_to_float(static_cast<const uint16_t*>(row)[v]);
+        const float y = max_nan(__fmul_rn(__fsub_rn(x, top), kLog2e), -1000.0f), q = ex2(y);
+        fs += q;
+        fe = __fmaf_rn(q, y, fe);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        fs += __shfl_xor_sync(0xffffffffu, fs, o);
+        fe += __shfl_xor_sync(0xffffffffu, fe, o);
+      }
+      if (lane == 0) s_far[warp][0] = fs, s_far[warp][1] = fe;
+      __syncthreads();
+      sum = ent = 0.0f;
+      for (int w = 0; w < kWarps; ++w) sum += s_far[w][0], ent += s_far[w][1];
+    }
+    const bool ok = top > -INFINITY && top < INFINITY && sum == sum;
+    const float nanf = __uint_as_float(0x7fc00000u), log_sum = log2f(sum);
+    // ln of the sum of e^(x - top): the sum's reference against the maximum
+    const float logz = (far ? log_sum : log_sum - __fmaf_rn(top, kLog2e, -rr)) * kLn2;
     auto log_prob = [&](float x) { return (x - top) - logz; };
-    if (tid == 0 && a.entropy != nullptr) a.entropy[r] = ok ? (log_sum - s_row_sum[2] / sum) * kLn2 : nanf;
+    if (tid == 0 && a.entropy != nullptr) a.entropy[r] = ok ? (log_sum - ent / sum) * kLn2 : nanf;
     for (int i = tid; i < a.n_ids; i += kThreads) {
       const int32_t id = a.ids[r * a.ld_ids + i];
       const bool in = id >= 0 && id < a.V;
@@ -416,41 +433,31 @@ __global__ void __launch_bounds__(kThreads, F32 ? 1 : 3)
   cluster_wait();
 }
 
-template <bool F32, bool kHeld>
-cudaError_t launch_kind(const LogprobArgs& a, int64_t tiles, int log_ctas, cudaStream_t stream) {
-  const int ctas = 1 << log_ctas;
-  constexpr int most = kPieces * kThreads * (F32 ? 32 : 16);
-  if (kHeld) {
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(logprobs_kernel<F32, kHeld>), most);
-    if (e != cudaSuccess) return e;
-  }
+}  // namespace
+
+cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream) {
+  // parts of a row: up to four pieces a thread, then up to eight parts; CTAs of
+  // a row: one a part while they all run at once (two on an SM)
+  const int64_t tiles = (a.V + kTile - 1) / kTile;
+  int log_parts = 0;
+  while ((1 << log_parts) < kMaxParts && tiles > (4 << log_parts)) ++log_parts;
+  int log_ctas = log_parts;
+  while (log_ctas > 0 && (a.R << log_ctas) > 2 * sm_count()) --log_ctas;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.R * ctas));
+  cfg.gridDim = dim3(static_cast<unsigned>(a.R << log_ctas));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kHeld ? static_cast<size_t>((tiles + ctas - 1) / ctas) * (most / kPieces) : 0;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr[1].val.clusterDim.x = 1u << log_ctas;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<F32, kHeld>, a, log_ctas);
-}
-
-}  // namespace
-
-cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream) {
-  // CTAs of a row: up to four pieces a thread, then up to eight CTAs
-  const int64_t tiles = (a.V + kTile - 1) / kTile;
-  int log_ctas = 0;
-  while ((1 << log_ctas) < kMaxCluster && tiles > (4 << log_ctas)) ++log_ctas;
-  const bool held = tiles <= kPieces << log_ctas;
-  if (a.f32) return held ? launch_kind<true, true>(a, tiles, log_ctas, stream) : launch_kind<true, false>(a, tiles, log_ctas, stream);
-  return held ? launch_kind<false, true>(a, tiles, log_ctas, stream) : launch_kind<false, false>(a, tiles, log_ctas, stream);
+  return a.f32 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<true>, a, log_parts, log_ctas)
+               : cudaLaunchKernelEx(&cfg, logprobs_kernel<false>, a, log_parts, log_ctas);
 }
 
 }  // namespace prism
