@@ -15,9 +15,11 @@ from typing import NamedTuple
 
 import torch
 
-from . import _check, _stream, lib
+from . import _check, lib
 
 _BF16, _F16, _F32, _I8, _U8, _I32 = (torch.bfloat16, torch.float16, torch.float32, torch.int8, torch.uint8, torch.int32)
+_Tensor = torch.Tensor
+_raw_stream = torch._C._cuda_getCurrentRawStream   # the current stream's handle without a Stream object around it
 
 
 class KvCache(NamedTuple):
@@ -39,65 +41,72 @@ def new_kv_cache(num_pages: int, heads: int, head_dim: int, block: int, num_seqs
     return KvCache(codes[0], codes[1], scales[0], scales[1], opens[0], opens[1])
 
 
-def _tensor(t, name, dtype, ndim, device):
-    """A CUDA tensor on ``device`` of this dtype and rank, whose last dimension is contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dims")
-    if t.stride(-1) != 1 and t.size(-1) > 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-
+# A decode step is a chain of short kernels: the checks below are plain
+# comparisons in the order of their cost, so that a call's host time stays
+# near its launch's.
 
 def _device(t, name):
-    if not isinstance(t, torch.Tensor):
+    """The CUDA device index of the first operand."""
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    return t.device
+    return t.get_device()
+
+
+def _tensor(t, name, dtype, shape, device):
+    """A tensor of this dtype and shape on CUDA device ``device``, its last
+    dimension contiguous; returns its address."""
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be of shape {list(shape)}, got {list(t.shape)}")
+    if t.stride(-1) != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.data_ptr()
+
+
+def _dense(t, name, dtype, shape, device):
+    if isinstance(t, _Tensor) and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _tensor(t, name, dtype, shape, device)
+
+
+def _rank(t, name, n):
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dims")
+    return t.shape
 
 
 def _cache(cache, page_table, seq_lens, device):
-    """Checks the cache's own tensors; (num_pages, heads, block, D, sequences, pages a sequence)."""
-    kc, vc, ks, vs = cache[0], cache[1], cache[2], cache[3]
-    for t, name, dtype, ndim in ((kc, "k_codes", _I8, 4), (vc, "v_codes", _I8, 4), (ks, "k_scale", _F32, 2),
-                                 (vs, "v_scale", _F32, 2)):
-        _tensor(t, name, dtype, ndim, device)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    _tensor(page_table, "page_table", _I32, 2, device)
-    _tensor(seq_lens, "seq_lens", _I32, 1, device)
-    num_pages, heads, block, d = kc.shape
-    if vc.shape != kc.shape or ks.shape != (num_pages, heads) or vs.shape != ks.shape:
-        raise ValueError("the cache's shapes do not agree")
-    seqs, max_pages = page_table.shape
-    if seq_lens.numel() != seqs:
-        raise ValueError("seq_lens must hold one length for each row of page_table")
-    return num_pages, heads, block, d, seqs, max_pages
+    """Checks the cache's own tensors: its geometry and the addresses of codes,
+    scales, page table and lengths."""
+    num_pages, heads, block, d = shape = _rank(cache[0], "k_codes", 4)
+    seqs, max_pages = _rank(page_table, "page_table", 2)
+    return (num_pages, heads, block, d, seqs, max_pages,
+            _dense(cache[0], "k_codes", _I8, shape, device), _dense(cache[1], "v_codes", _I8, shape, device),
+            _dense(cache[2], "k_scale", _F32, (num_pages, heads), device),
+            _dense(cache[3], "v_scale", _F32, (num_pages, heads), device),
+            _tensor(page_table, "page_table", _I32, (seqs, max_pages), device),
+            _tensor(seq_lens, "seq_lens", _I32, (seqs,), device))
 
 
 def _offsets(cu, name, seqs, rows, device):
     if cu is not None:
-        _tensor(cu, name, _I32, 1, device)
-        if cu.numel() != seqs + 1:
-            raise ValueError(f"{name} must hold one offset more than sequences")
-        return cu.data_ptr()
+        return _tensor(cu, name, _I32, (seqs + 1,), device)
     if rows != seqs:
         raise ValueError(f"without {name} there is one row for each sequence")
     return None
 
 
-def _err(err, device):
-    if err is None:
-        return None
-    _tensor(err, "err", _I32, 1, device)
-    if err.numel() < 1:
-        raise ValueError("err must hold one word")
-    return err.data_ptr()
+def _stream(stream, device):
+    return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
 def prism_kv_append(k, v, cache, page_table, seq_lens, cu_new=None, max_new=None, err=None, stream=None):
@@ -107,25 +116,21 @@ def prism_kv_append(k, v, cache, page_table, seq_lens, cu_new=None, max_new=None
     row each; ``max_new``: a launch hint, the most rows of one sequence;
     ``err``: optional int32 [1] device error word."""
     device = _device(k, "k")
-    num_pages, heads, block, d, seqs, max_pages = _cache(cache, page_table, seq_lens, device)
-    _tensor(k, "k", _BF16, 3, device)
-    _tensor(v, "v", _BF16, 3, device)
-    rows = k.size(0)
-    if k.shape != (rows, heads, d) or v.shape != k.shape:
-        raise ValueError("k and v must be [T, H_kv, D]")
-    ko, vo = cache[4], cache[5]
-    for t, name in ((ko, "k_open"), (vo, "v_open")):
-        _tensor(t, name, _BF16, 4, device)
-        if t.shape != (seqs, heads, block, d) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous [S, H_kv, block, D] tensor")
+    num_pages, heads, block, d, seqs, max_pages, kc, vc, ks, vs, table, lens = _cache(cache, page_table, seq_lens, device)
+    rows = _rank(k, "k", 3)[0]
+    shape, open_shape = (rows, heads, d), (seqs, heads, block, d)
+    k_ptr, v_ptr = _tensor(k, "k", _BF16, shape, device), _tensor(v, "v", _BF16, shape, device)
+    ko = _dense(cache[4], "k_open", _BF16, open_shape, device)
+    vo = _dense(cache[5], "v_open", _BF16, open_shape, device)
     cu = _offsets(cu_new, "cu_new", seqs, rows, device)
     if max_new is None:
         max_new = 1 if cu is None else max(1, rows)
+    k_t, k_h, _ = k.stride()
+    v_t, v_h, _ = v.stride()
     _check("prism_kv_append", lib().prism_kv_append(
-        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), cache[0].data_ptr(),
-        cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), ko.data_ptr(), vo.data_ptr(),
-        page_table.data_ptr(), page_table.stride(0), seq_lens.data_ptr(), cu, seqs, rows, max_new, num_pages,
-        max_pages, heads, d, block, _err(err, device), _stream(stream)))
+        k_ptr, k_t, k_h, v_ptr, v_t, v_h, kc, vc, ks, vs, ko, vo, table, page_table.stride(0), lens, cu, seqs, rows,
+        max_new, num_pages, max_pages, heads, d, block,
+        None if err is None else _tensor(err, "err", _I32, (1,), device), _stream(stream, device)))
 
 
 def prism_kv_attention_workspace_bytes(seqs: int, rows: int, max_q: int, max_pages: int, q_heads: int, heads: int,
@@ -146,36 +151,35 @@ def prism_kv_attention(q, cache, page_table, seq_lens, cu_q=None, max_q=None, sc
     tensor of prism_kv_attention_workspace_bytes bytes (allocated when None);
     ``err``: optional int32 [1] device error word."""
     device = _device(q, "q")
-    num_pages, heads, block, d, seqs, max_pages = _cache(cache, page_table, seq_lens, device)
-    _tensor(q, "q", _BF16, 3, device)
-    rows, q_heads = q.size(0), q.size(1)
-    if q.size(2) != d or q_heads == 0 or q_heads % heads:
+    num_pages, heads, block, d, seqs, max_pages, kc, vc, ks, vs, table, lens = _cache(cache, page_table, seq_lens, device)
+    shape = rows, q_heads, q_d = _rank(q, "q", 3)
+    if q_d != d or q_heads == 0 or heads == 0 or q_heads % heads:
         raise ValueError("q must be [T, H_q, D] with H_q a multiple of H_kv")
+    q_ptr = _tensor(q, "q", _BF16, shape, device)
     cu = _offsets(cu_q, "cu_q", seqs, rows, device)
     if max_q is None:
         max_q = 1 if cu is None else max(1, rows)
     if out is None:
-        out = torch.empty((rows, q_heads, d), dtype=_BF16, device=device)
-    else:
-        _tensor(out, "out", _BF16, 3, device)
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-    if lse is not None:
-        _tensor(lse, "lse", _F32, 2, device)
-        if lse.shape != (rows, q_heads) or not lse.is_contiguous():
-            raise ValueError("lse must be a contiguous [T, H_q] tensor")
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
+    out_ptr = _tensor(out, "out", _BF16, shape, device)
+    lse_ptr = None if lse is None else _dense(lse, "lse", _F32, (rows, q_heads), device)
     handle = lib()
     if workspace is None:
-        need = handle.prism_kv_attention_workspace_bytes(seqs, rows, max_q, max_pages, q_heads, heads, d, block)
-        if need:
-            workspace = torch.empty(need, dtype=_U8, device=device)
-    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        ws, ws_bytes = None, handle.prism_kv_attention_workspace_bytes(seqs, rows, max_q, max_pages, q_heads, heads, d, block)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=_U8, device=q.device)
+            ws = workspace.data_ptr()
+    else:
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{device}")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    q_t, q_h, _ = q.stride()
+    o_t, o_h, _ = out.stride()
     _check("prism_kv_attention", handle.prism_kv_attention(
-        q.data_ptr(), q.stride(0), q.stride(1), cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(),
-        cache[3].data_ptr(), page_table.data_ptr(), page_table.stride(0), seq_lens.data_ptr(), cu, out.data_ptr(),
-        out.stride(0), out.stride(1), None if lse is None else lse.data_ptr(), d ** -0.5 if scale is None else scale,
-        1 if causal else 0, window, seqs, rows, max_q, num_pages, max_pages, q_heads, heads, d, block, ws, ws_bytes,
-        _err(err, device), _stream(stream)))
+        q_ptr, q_t, q_h, kc, vc, ks, vs, table, page_table.stride(0), lens, cu, out_ptr, o_t, o_h, lse_ptr,
+        d ** -0.5 if scale is None else scale, 1 if causal else 0, window, seqs, rows, max_q, num_pages, max_pages,
+        q_heads, heads, d, block, ws, ws_bytes, None if err is None else _tensor(err, "err", _I32, (1,), device),
+        _stream(stream, device)))
     return out
 
 
@@ -188,34 +192,26 @@ def prism_w4g_linear(q, a_scale, w4, group_scale, group_offset=None, residual=No
     optional ``group_offset`` float16 [N, K/g], g = 32, 64 or 128; ``residual``
     bf16 [M, N] or None, may be ``out`` itself."""
     device = _device(q, "q")
-    _tensor(q, "q", _I8, 2, device)
-    _tensor(a_scale, "a_scale", _F32, 1, device)
-    _tensor(w4, "w4", _U8, 2, device)
-    _tensor(group_scale, "group_scale", _F16, 2, device)
-    m, k = q.shape
-    n, groups = group_scale.shape
-    if a_scale.numel() != m or w4.shape != (n, k // 2) or k % 2 or groups == 0 or k % groups:
-        raise ValueError("q [M, K], a_scale [M], w4 [N, K/2] and group_scale [N, K/g] do not agree")
-    if group_offset is not None:
-        _tensor(group_offset, "group_offset", _F16, 2, device)
-        if group_offset.shape != group_scale.shape:
-            raise ValueError("group_offset must have group_scale's shape")
-    if out is None:
-        out = torch.empty((m, n), dtype=_BF16, device=device)
+    m, k = _rank(q, "q", 2)
+    n, groups = _rank(group_scale, "group_scale", 2)
+    if groups == 0 or k % groups or k % 2:
+        raise ValueError("q [M, K] and group_scale [N, K/g] do not agree")
+    q_ptr, a_ptr = _tensor(q, "q", _I8, (m, k), device), _tensor(a_scale, "a_scale", _F32, (m,), device)
+    w_ptr = _tensor(w4, "w4", _U8, (n, k // 2), device)
+    s_ptr = _tensor(group_scale, "group_scale", _F16, (n, groups), device)
+    if group_offset is None:
+        b_ptr = ldb = 0
     else:
-        _tensor(out, "out", _BF16, 2, device)
-        if out.shape != (m, n):
-            raise ValueError("out must be [M, N]")
-    if residual is not None:
-        _tensor(residual, "residual", _BF16, 2, device)
-        if residual.shape != (m, n):
-            raise ValueError("residual must be [M, N]")
+        b_ptr, ldb = _tensor(group_offset, "group_offset", _F16, (n, groups), device), group_offset.stride(0)
+    if residual is None:
+        r_ptr = ldr = 0
+    else:
+        r_ptr, ldr = _tensor(residual, "residual", _BF16, (m, n), device), residual.stride(0)
+    if out is None:
+        out = torch.empty((m, n), dtype=_BF16, device=q.device)
     _check("prism_w4g_linear", lib().prism_w4g_linear(
-        q.data_ptr(), q.stride(0), a_scale.data_ptr(), w4.data_ptr(), w4.stride(0), group_scale.data_ptr(),
-        group_scale.stride(0), None if group_offset is None else group_offset.data_ptr(),
-        0 if group_offset is None else group_offset.stride(0), None if residual is None else residual.data_ptr(),
-        0 if residual is None else residual.stride(0), out.data_ptr(), out.stride(0), m, n, k, k // groups,
-        _stream(stream)))
+        q_ptr, q.stride(0), a_ptr, w_ptr, w4.stride(0), s_ptr, group_scale.stride(0), b_ptr, ldb, r_ptr, ldr,
+        _tensor(out, "out", _BF16, (m, n), device), out.stride(0), m, n, k, k // groups, _stream(stream, device)))
     return out
 
 
@@ -225,21 +221,25 @@ def prism_token_logprobs(logits, token_ids, top_k: int = 0, entropy=True, err=No
     top_ids int32 [R, top_k], top_logprobs float32 [R, top_k]; the last two
     None for top_k = 0).  ``err``: optional int32 [1] device error word."""
     device = _device(logits, "logits")
-    if logits.dtype is not _BF16 and logits.dtype is not _F32:
-        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
-    _tensor(logits, "logits", logits.dtype, 2, device)
-    _tensor(token_ids, "token_ids", _I32, 2, device)
-    rows, vocab = logits.shape
-    n = token_ids.size(1)
-    if token_ids.size(0) != rows:
-        raise ValueError("token_ids must have a row for each row of logits")
-    logprobs = torch.empty((rows, n), dtype=_F32, device=device)
-    ent = torch.empty((rows,), dtype=_F32, device=device) if entropy else None
-    top_ids = torch.empty((rows, top_k), dtype=_I32, device=device) if top_k else None
-    top_lp = torch.empty((rows, top_k), dtype=_F32, device=device) if top_k else None
+    rows, vocab = _rank(logits, "logits", 2)
+    n = _rank(token_ids, "token_ids", 2)[1]
+    dtype = logits.dtype
+    if dtype is not _BF16 and dtype is not _F32:
+        raise TypeError(f"logits must be bfloat16 or float32, got {dtype}")
+    x_ptr = _tensor(logits, "logits", dtype, (rows, vocab), device)
+    id_ptr = _tensor(token_ids, "token_ids", _I32, (rows, n), device)
+    on = logits.device
+    logprobs = torch.empty((rows, n), dtype=_F32, device=on)
+    ent = ent_ptr = top_ids = top_lp = ids_out = lp_out = None
+    if entropy:
+        ent = torch.empty((rows,), dtype=_F32, device=on)
+        ent_ptr = ent.data_ptr()
+    if top_k:
+        top_ids = torch.empty((rows, top_k), dtype=_I32, device=on)
+        top_lp = torch.empty((rows, top_k), dtype=_F32, device=on)
+        ids_out, lp_out = top_ids.data_ptr(), top_lp.data_ptr()
     _check("prism_token_logprobs", lib().prism_token_logprobs(
-        logits.data_ptr(), 1 if logits.dtype is _F32 else 0, logits.stride(0), token_ids.data_ptr(),
-        token_ids.stride(0), n, rows, vocab, top_k, logprobs.data_ptr(), None if ent is None else ent.data_ptr(),
-        None if top_ids is None else top_ids.data_ptr(), None if top_lp is None else top_lp.data_ptr(),
-        _err(err, device), _stream(stream)))
+        x_ptr, 1 if dtype is _F32 else 0, logits.stride(0), id_ptr, token_ids.stride(0), n, rows, vocab, top_k,
+        logprobs.data_ptr(), ent_ptr, ids_out, lp_out,
+        None if err is None else _tensor(err, "err", _I32, (1,), device), _stream(stream, device)))
     return logprobs, ent, top_ids, top_lp
