@@ -53,6 +53,8 @@ struct KvAttentionArgs {
 size_t kv_attention_workspace_bytes(int64_t S, int64_t T, int64_t max_q, int64_t max_pages, int64_t Hq, int64_t Hkv,
                                     int64_t D, int64_t block);
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream);
+// Device status bits of its bounded waits.
+cudaError_t read_and_clear_kv_status(uint32_t* out);
 
 struct W4gArgs {
   const int8_t* q;

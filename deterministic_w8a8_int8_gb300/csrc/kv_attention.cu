@@ -2,12 +2,9 @@
 //   o = sum_j softmax_j(sm_scale * ks * (q . ck_j)) * vs * cv_j
 // with codes ck, cv and one scale ks, vs per (page, head).
 //
-// Work: a sequence's n queries times its G query heads per KV head are rows;
-// 8 NQ rows make a tile, and the keys are cut into pieces of at least
-// kMinChunk (split_count below: a function of the sequence's own length and
-// rows, so its result does not depend on the rest of the batch).  A persistent
-// grid walks the items (sequence, KV head, piece, tile); the pieces of a row
-// are joined by kv_combine_kernel in piece order.
+// This file: the kernel for up to kv::kFewRows rows of a sequence and KV head
+// (kv_plan.cuh), 8 NQ rows a tile, and the join of pieces.  A persistent grid
+// walks the items (sequence, KV head, piece, tile).
 //
 // One item is one CTA of four warps; warp w takes every fourth step of 8 KB of
 // K and V.  Each warp is on its own: its steps arrive through a private ring
@@ -33,72 +30,22 @@
 // and outputs are binary32.
 #include <cuda_fp16.h>
 
-#include "decode.cuh"
+#include "kv_plan.cuh"
 
 namespace prism {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+using namespace kv;
+
+constexpr int kWarps = kThreads / 32;
 constexpr int kJoinThreads = 256;
-constexpr int kPlanRows = 32;          // rows that count as one in the plan of pieces
 constexpr int kStages = 2;
 constexpr int kStageBytes = 8192;      // K and V of one step of a warp
-constexpr int kMinChunk = 1024;        // keys of a piece at least
-constexpr int kMaxSplit = 128;         // pieces of a row at most
-constexpr int kFill = 456;             // items that one sequence is cut into where it has the keys: three on each of 152 SMs
-constexpr float kPShift = 12.0f;       // log2 of the probability of the running maximum
-constexpr float kLn2 = 0.69314718055994531f;
 
 template <int D>
 constexpr int kUnits = kStageBytes / (2 * 16 * D);   // 16-key units of a step: 4, 2, 1 for D = 64, 128, 256
 template <int D>
 constexpr int kStepKeys = 16 * kUnits<D>;
-
-// Pieces of the keys of a sequence with so many plan tiles of rows, H KV heads.
-__host__ __device__ __forceinline__ int split_count(int64_t keys, int64_t tiles, int64_t H) {
-  const int64_t cap = kFill / (tiles * H), n = (keys + kMinChunk - 1) / kMinChunk;
-  const int64_t m = cap > kMaxSplit ? kMaxSplit : cap;
-  return static_cast<int>(n > m ? (m < 1 ? 1 : m) : n < 1 ? 1 : n);
-}
-// Rows of one (sequence, KV head) that can be cut into pieces, and the most
-// (row, piece) pairs of it.
-int64_t max_split_rows(int64_t max_q, int64_t G, int64_t max_keys, int64_t H, int64_t* rows) {
-  int64_t most = 0;
-  *rows = 0;
-  for (int64_t tiles = 1; split_count(max_keys, tiles, H) > 1; ++tiles) {
-    *rows = std::min(tiles * kPlanRows, max_q * G);
-    most = std::max(most, split_count(max_keys, tiles, H) * *rows);
-    if (tiles * kPlanRows >= max_q * G) break;
-  }
-  return most;
-}
-
-// A sequence's plan: its rows, key range and pieces.
-struct SeqPlan {
-  SeqSpan sp;
-  int32_t rows, tiles, splits;
-  int32_t lo, chunk;     // first key seen by any of its queries (rounded down to 64), keys of a piece
-  bool bad;              // malformed length: its rows get NaN
-};
-template <int NQ>
-__device__ __forceinline__ int seq_items(const KvAttentionArgs& a, int s, SeqPlan& p) {
-  const bool ok = seq_span(a.c, a.cu_q, a.T, s, true, p.sp);
-  if (p.sp.b < 0 || p.sp.n < 0 || static_cast<int64_t>(p.sp.b) + p.sp.n > a.T) return -1;   // no rows to answer for
-  p.bad = !ok || p.sp.n > a.max_q;
-  p.rows = p.sp.n * a.G;
-  p.tiles = (p.rows + 8 * NQ - 1) / (8 * NQ);
-  p.splits = 1;
-  p.lo = p.chunk = 0;
-  if (!p.bad && p.rows > 0) {
-    const int64_t first = a.window > 0 ? p.sp.len - p.sp.n + 1 - a.window : 0;
-    p.lo = first > 0 ? static_cast<int32_t>(first) & ~63 : 0;
-    const int64_t keys = p.sp.len - p.lo;
-    p.splits = split_count(keys, (p.rows + kPlanRows - 1) / kPlanRows, a.c.H);
-    p.chunk = static_cast<int32_t>((((keys + p.splits - 1) / p.splits) + 63) & ~63ll);
-  }
-  return p.tiles * p.splits * a.c.H;
-}
 
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, int src_bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
@@ -110,30 +57,12 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // The 8x8 matrix of binary16 whose row r lies in lanes 4r .. 4r + 3, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-// Bytes 0, 1 (sel 0x4140) or 2, 3 (sel 0x4342) of codes ^ 0x80 as a binary16 pair, exact.
-__device__ __forceinline__ uint32_t widen(uint32_t biased, uint32_t sel) {
-  const uint32_t h = __byte_perm(biased, 0x64646464u, sel);
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));   // 1024 + 128
-  return r;
-}
-
 // Shared-memory place of 16-byte piece `ch` of key `key` in a step's K (V):
 // pieces of neighbouring keys are turned so that the eight lanes of a phase
 // (keys r, r + 1 for K; keys 0, 2, 4, 6 for V) touch all banks once (D = 64:
@@ -180,57 +109,13 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
   uint8_t* ring = smem + warp * kStages * kStageBytes;
   const uint32_t ring_u = smem_u32(ring);
 
-  int s0 = -kThreads;                      // first sequence of the window in s_scan
-  int64_t win_base = 0;                    // items before the window
-  int win_items = 0;
-  for (int64_t item = blockIdx.x;; item += gridDim.x) {
-    // ---- the item's sequence: inclusive scan of the item counts, 128 sequences at a time
-    while (item >= win_base + win_items) {
-      win_base += win_items;
-      s0 += kThreads;
-      if (s0 >= c.S) return;
-      SeqPlan p;
-      int n = s0 + tid < c.S ? seq_items<NQ>(a, s0 + tid, p) : 0;
-      if (blockIdx.x == 0 && s0 + tid < c.S && (n < 0 || (p.bad && n > 0)) && a.err != nullptr)
-        atomicOr(a.err, PRISM_DEV_ERR_SEQ_RANGE);
-      n = max(n, 0);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, n, o);
-        if (lane >= o) n += v;
-      }
-      __syncthreads();
-      if (lane == 31) s_warp[warp] = n;
-      __syncthreads();
-      for (int w = 0; w < warp; ++w) n += s_warp[w];
-      s_scan[tid] = n;
-      __syncthreads();
-      win_items = s_scan[kThreads - 1];
-    }
-    const int local = static_cast<int>(item - win_base);
-    int at = 0;
-#pragma unroll
-    for (int o = kThreads / 2; o > 0; o >>= 1)
-      if (s_scan[at + o - 1] <= local) at += o;
-    const int s = s0 + at;
-    SeqPlan p;
-    seq_items<NQ>(a, s, p);
-    int rest = local - (at > 0 ? s_scan[at - 1] : 0);
-    const int tile = rest % p.tiles;
-    rest /= p.tiles;
-    const int split = rest % p.splits, hk = rest / p.splits;
-
-    // ---- the keys that the tile's rows see: row r stands at first_pos + r / G
-    const int row0 = tile * kRows;
-    const int n_rows = min(kRows, p.rows - row0);
-    const int32_t len = static_cast<int32_t>(p.sp.len), first_pos = len - p.sp.n;
-    auto row_hi = [&](int r) { return r >= n_rows || p.bad ? 0 : a.causal ? max(0, first_pos + (row0 + r) / a.G + 1) : len; };
-    auto row_lo = [&](int hi) { return a.window > 0 && hi > a.window ? hi - static_cast<int32_t>(a.window) : 0; };
-    const int32_t a_hi = row_hi(0), t_hi = row_hi(n_rows - 1);   // rows rise: every row sees [a_lo, a_hi), some row [t_lo, t_hi)
-    const int32_t t_lo = row_lo(a_hi), a_lo = row_lo(t_hi);
-    const int32_t k_begin = max(p.lo + split * p.chunk, t_lo & ~63);
-    const int64_t piece_end = static_cast<int64_t>(p.lo) + static_cast<int64_t>(split + 1) * p.chunk;
-    const int32_t k_end = static_cast<int32_t>(min(static_cast<int64_t>(t_hi), piece_end));
+  Walk walk;
+  SeqPlan p;
+  for (int64_t item = blockIdx.x; find_item<false, kRows>(a, item, walk, s_scan, s_warp, p); item += gridDim.x) {
+    const int s = walk.s, hk = walk.hk, split = walk.split;
+    const TileKeys keys(a, p, walk, kRows);
+    const int row0 = keys.row0, n_rows = keys.n_rows;
+    const int32_t k_begin = keys.k_begin, k_end = keys.k_end;
     const int steps = k_end > k_begin ? (k_end - k_begin + kStepKeys<D> - 1) / kStepKeys<D> : 0;
     const int my_steps = (steps - warp + kWarps - 1) / kWarps;   // steps warp, warp + 4, ...
 
@@ -306,8 +191,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
       }
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const int be = static_cast<int>(__float_as_uint(amax) >> 23);   // biased exponent of the row's maximum
-      const int fe = be == 255 || be == 0 ? 127 : min(253, 127 + 13 + 127 - be);
+      const int fe = query_exponent(amax);
       const float f = __uint_as_float(static_cast<uint32_t>(fe) << 23);
       float sum = 0.0f;
 #pragma unroll
@@ -417,12 +301,12 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
           x[u][t][3] *= f1;
         }
       }
-      if (key0 < a_lo || key0 + kStepKeys<D> > a_hi) {   // keys that a row does not see
+      if (key0 < keys.a_lo || key0 + kStepKeys<D> > keys.a_hi) {   // keys that a row does not see
 #pragma unroll
         for (int t = 0; t < NQ; ++t)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int32_t hi = row_hi(8 * t + 2 * lc + i), lo = row_lo(hi);
+            const int32_t hi = keys.hi(8 * t + 2 * lc + i), lo = keys.lo(hi);
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -598,7 +482,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int s = blockIdx.x, hk = blockIdx.y, r = blockIdx.z;
   SeqPlan p;
-  if (seq_items<1>(a, s, p) <= 0 || p.splits == 1 || r >= p.rows) return;
+  if (seq_items<false, 1>(a, s, p) < 0 || p.bad || p.splits == 1 || r >= p.rows) return;
   const float* part = static_cast<const float*>(a.ws) +
                       ((static_cast<int64_t>(s) * a.c.H + hk) * part_stride + r) * (D + 4);
   const int64_t step = static_cast<int64_t>(p.rows) * (D + 4);
@@ -654,33 +538,34 @@ __global__ void __launch_bounds__(kJoinThreads)
 }
 
 template <int D, int NQ>
-cudaError_t launch_nq(const KvAttentionArgs& a, cudaStream_t stream) {
+cudaError_t launch_few(const KvAttentionArgs& a, int64_t part_stride, cudaStream_t stream) {
   using M = Smem<D, NQ>;
-  const int64_t max_keys = a.c.max_pages << a.c.block_shift;
-  int64_t split_rows;
-  const int64_t part_stride = max_split_rows(a.max_q, a.G, max_keys, a.c.H, &split_rows);
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kv_attention_kernel<D, NQ>), M::kBytes);
   if (e != cudaSuccess) return e;
+  // Persistent: as many CTAs as the SMs hold, or as the call can have items.
   // Not launched ahead of the previous kernel's end: a join that waits for
   // these CTAs takes their places (64 ragged sequences: 85 us so, 65 us not).
-  // persistent: as many CTAs as the SMs hold, or as the call can have items
-  const int64_t tiles = a.T * a.G / M::kRows + a.c.S;
+  const int64_t tiles = std::min<int64_t>(a.T * a.G, static_cast<int64_t>(a.c.S) * kFewRows) / M::kRows + a.c.S;
   const int64_t items = (tiles + (part_stride / M::kRows + kMaxSplit) * a.c.S) * a.c.H;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sm_count() * M::kCtas));
-  e = launch_kernel(kv_attention_kernel<D, NQ>, dim3(grid), dim3(kThreads), M::kBytes, stream, false, a, part_stride);
-  if (e != cudaSuccess || part_stride == 0) return e;
-  return launch_kernel(kv_combine_kernel<D>, dim3(a.c.S, a.c.H, static_cast<unsigned>(split_rows)), dim3(kJoinThreads), 0,
-                       stream, false, a, part_stride);
+  return launch_kernel(kv_attention_kernel<D, NQ>, dim3(grid), dim3(kThreads), M::kBytes, stream, false, a, part_stride);
 }
 
-// Rows of a tile: as many as one sequence can have, up to 32 (16 for D = 256,
-// by the registers of the output).  A row's bits do not depend on the choice.
+// Rows of a tile: as many as a sequence of this kernel can have in this call
+// (16 at most for D = 256, by the registers of the output).  A row's bits do
+// not depend on the choice.
 template <int D>
 cudaError_t launch_d(const KvAttentionArgs& a, cudaStream_t stream) {
   const int64_t rows = a.max_q * a.G;
-  if (rows <= 8) return launch_nq<D, 1>(a, stream);
-  if (rows <= 16 || D == 256) return launch_nq<D, 2>(a, stream);
-  return launch_nq<D, D == 256 ? 2 : 4>(a, stream);
+  int64_t split_rows;
+  const int64_t part_stride = max_split_rows(a.max_q, a.G, a.c.max_pages << a.c.block_shift, a.c.H, &split_rows);
+  cudaError_t e = rows <= 8                 ? launch_few<D, 1>(a, part_stride, stream)
+                  : rows <= 16 || D == 256  ? launch_few<D, 2>(a, part_stride, stream)
+                                            : launch_few<D, D == 256 ? 2 : 4>(a, part_stride, stream);
+  if (e == cudaSuccess && rows > kFewRows) e = launch_kv_attention_wide(a, part_stride, stream);
+  if (e != cudaSuccess || part_stride == 0) return e;
+  return launch_kernel(kv_combine_kernel<D>, dim3(a.c.S, a.c.H, static_cast<unsigned>(split_rows)), dim3(kJoinThreads), 0,
+                       stream, false, a, part_stride);
 }
 
 }  // namespace

@@ -3,7 +3,7 @@
 // to the kernel launchers.  See include/prism.h for the contract.
 #include <mutex>
 
-#include "common.cuh"
+#include "decode.cuh"
 
 namespace prism {
 
@@ -280,10 +280,11 @@ int prism_w8a8_kernel_kind(int64_t M, int64_t N, int64_t K) { return prism::line
 
 int prism_device_status(uint32_t* flags) {
   if (flags == nullptr) return PRISM_ERR_INVALID_ARG;
-  uint32_t a = 0, b = 0;
+  uint32_t a = 0, b = 0, c = 0;
   int st = prism::record_cuda(prism::read_and_clear_kernel_error(&a));
   if (st == PRISM_OK) st = prism::record_cuda(prism::read_and_clear_f16_status(&b));
-  *flags = a | b;
+  if (st == PRISM_OK) st = prism::record_cuda(prism::read_and_clear_kv_status(&c));
+  *flags = a | b | c;
   return st;
 }
 
