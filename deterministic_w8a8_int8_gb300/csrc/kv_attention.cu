@@ -37,7 +37,8 @@ namespace {
 
 using namespace kv;
 
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
 constexpr int kJoinThreads = 256;
 constexpr int kStages = 2;
 constexpr int kStageBytes = 8192;      // K and V of one step of a warp
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
 
   Walk walk;
   SeqPlan p;
-  for (int64_t item = blockIdx.x; find_item<false, kRows>(a, item, walk, s_scan, s_warp, p); item += gridDim.x) {
+  for (int64_t item = blockIdx.x; find_item<false, kRows, kThreads>(a, item, walk, s_scan, s_warp, p); item += gridDim.x) {
     const int s = walk.s, hk = walk.hk, split = walk.split;
     const TileKeys keys(a, p, walk, kRows);
     const int row0 = keys.row0, n_rows = keys.n_rows;
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
   }
 }
 
-// Joins a row's pieces: one CTA per (sequence, KV head, row).  Thread i weighs
+// Joins a row's pieces: a CTA takes rows of one (sequence, KV head) in turn.  Thread i weighs
 // piece i; then D / 4 columns of threads by 1024 / D groups add every group-th
 // piece in order, and the groups are added in order.
 template <int D>
@@ -480,61 +481,65 @@ __global__ void __launch_bounds__(kJoinThreads)
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int s = blockIdx.x, hk = blockIdx.y, r = blockIdx.z;
+  const int s = blockIdx.x, hk = blockIdx.y;
   SeqPlan p;
-  if (seq_items<false, 1>(a, s, p) < 0 || p.bad || p.splits == 1 || r >= p.rows) return;
-  const float* part = static_cast<const float*>(a.ws) +
-                      ((static_cast<int64_t>(s) * a.c.H + hk) * part_stride + r) * (D + 4);
-  const int64_t step = static_cast<int64_t>(p.rows) * (D + 4);
-  float pm = -INFINITY, pl = 0.0f;
-  if (tid < p.splits) pm = part[tid * step], pl = part[tid * step + 1];
-  const bool nan = __syncthreads_or(pm != pm);
-  float mx = pm;
+  if (seq_items<false, 1>(a, s, p) < 0 || p.bad || p.splits == 1) return;
+  for (int r = blockIdx.z; r < p.rows; r += gridDim.z) {
+    const float* part = static_cast<const float*>(a.ws) +
+                        ((static_cast<int64_t>(s) * a.c.H + hk) * part_stride + r) * (D + 4);
+    const int64_t step = static_cast<int64_t>(p.rows) * (D + 4);
+    float pm = -INFINITY, pl = 0.0f;
+    if (tid < p.splits) pm = part[tid * step], pl = part[tid * step + 1];
+    const bool nan = __syncthreads_or(pm != pm);
+    float mx = pm;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) s_red[warp] = mx;
-  __syncthreads();
-  mx = s_red[0];
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane == 0) s_red[warp] = mx;
+    __syncthreads();
+    mx = s_red[0];
 #pragma unroll
-  for (int w = 1; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, s_red[w]);
-  const float f = pm == -INFINITY ? 0.0f : ex2(pm - mx);
-  s_f[tid] = f;
-  float l = f * pl;
+    for (int w = 1; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, s_red[w]);
+    const float f = pm == -INFINITY ? 0.0f : ex2(pm - mx);
+    s_f[tid] = f;
+    float l = f * pl;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (lane == 0) s_sum[warp] = l;
-  __syncthreads();
-  const int col = tid % kCols, group = tid / kCols;
-  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) s_sum[warp] = l;
+    __syncthreads();
+    const int col = tid % kCols, group = tid / kCols;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
-  for (int i = group; i < p.splits; i += kGroups) {
-    const float4 v = *reinterpret_cast<const float4*>(part + i * step + 4 + col * 4);
-    const float w = s_f[i];
-    y.x = fmaf(w, v.x, y.x);
-    y.y = fmaf(w, v.y, y.y);
-    y.z = fmaf(w, v.z, y.z);
-    y.w = fmaf(w, v.w, y.w);
-  }
-  s_o[tid] = y;
-  __syncthreads();
-  if (group != 0) return;
+    for (int i = group; i < p.splits; i += kGroups) {
+      const float4 v = *reinterpret_cast<const float4*>(part + i * step + 4 + col * 4);
+      const float w = s_f[i];
+      y.x = fmaf(w, v.x, y.x);
+      y.y = fmaf(w, v.y, y.y);
+      y.z = fmaf(w, v.z, y.z);
+      y.w = fmaf(w, v.w, y.w);
+    }
+    s_o[tid] = y;
+    __syncthreads();
+    if (group == 0) {
 #pragma unroll
-  for (int g = 1; g < kGroups; ++g) {
-    const float4 v = s_o[g * kCols + col];
-    y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
-  }
-  float sum = s_sum[0];
+      for (int g = 1; g < kGroups; ++g) {
+        const float4 v = s_o[g * kCols + col];
+        y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+      }
+      float sum = s_sum[0];
 #pragma unroll
-  for (int w = 1; w < kJoinThreads / 32; ++w) sum += s_sum[w];
-  const float nanf = __uint_as_float(0x7fc00000u), inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
-  const int64_t t = p.sp.b + r / a.G;
-  const int h = hk * a.G + r % a.G;
-  uint2 w = make_uint2(float_to_bf16_rne(y.x * inv) | float_to_bf16_rne(y.y * inv) << 16,
-                       float_to_bf16_rne(y.z * inv) | float_to_bf16_rne(y.w * inv) << 16);
-  if (nan) w = make_uint2(kBf16NaN * 0x10001u, kBf16NaN * 0x10001u);
-  *reinterpret_cast<uint2*>(a.out + t * a.ldo_t + h * a.ldo_h + col * 4) = w;
-  if (tid == 0 && a.lse != nullptr)
-    a.lse[t * a.Hq + h] = nan ? nanf : mx == -INFINITY ? mx : (mx - kPShift + log2f(sum)) * kLn2;
+      for (int w = 1; w < kJoinThreads / 32; ++w) sum += s_sum[w];
+      const float nanf = __uint_as_float(0x7fc00000u), inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
+      const int64_t t = p.sp.b + r / a.G;
+      const int h = hk * a.G + r % a.G;
+      uint2 w = make_uint2(float_to_bf16_rne(y.x * inv) | float_to_bf16_rne(y.y * inv) << 16,
+                           float_to_bf16_rne(y.z * inv) | float_to_bf16_rne(y.w * inv) << 16);
+      if (nan) w = make_uint2(kBf16NaN * 0x10001u, kBf16NaN * 0x10001u);
+      *reinterpret_cast<uint2*>(a.out + t * a.ldo_t + h * a.ldo_h + col * 4) = w;
+      if (tid == 0 && a.lse != nullptr)
+        a.lse[t * a.Hq + h] = nan ? nanf : mx == -INFINITY ? mx : (mx - kPShift + log2f(sum)) * kLn2;
+    }
+    __syncthreads();   // the weights and sums are free again
+  }
 }
 
 template <int D, int NQ>
@@ -564,8 +569,8 @@ cudaError_t launch_d(const KvAttentionArgs& a, cudaStream_t stream) {
                                             : launch_few<D, D == 256 ? 2 : 4>(a, part_stride, stream);
   if (e == cudaSuccess && rows > kFewRows) e = launch_kv_attention_wide(a, part_stride, stream);
   if (e != cudaSuccess || part_stride == 0) return e;
-  return launch_kernel(kv_combine_kernel<D>, dim3(a.c.S, a.c.H, static_cast<unsigned>(split_rows)), dim3(kJoinThreads), 0,
-                       stream, false, a, part_stride);
+  const dim3 grid(a.c.S, a.c.H, static_cast<unsigned>(std::min<int64_t>(split_rows, 64)));
+  return launch_kernel(kv_combine_kernel<D>, grid, dim3(kJoinThreads), 0, stream, false, a, part_stride);
 }
 
 }  // namespace

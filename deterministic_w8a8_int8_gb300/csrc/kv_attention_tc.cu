@@ -1,12 +1,13 @@
 // kv_attention_tc.cu -- attention over the paged int8 cache for many rows (a
 // prompt's piece, questions of many tokens) on the tcgen05 tensor cores.
 //
-// A tile is 128 rows (queries x heads of a KV head), one a thread: a thread's
-// row is its lane of tensor memory, so the softmax needs no exchange.  Keys go
-// by in blocks of KB:
+// A tile is 128 rows (queries x heads of a KV head), each a lane of tensor
+// memory.  Two threads have a row, one for each half of a block's keys (and of
+// the output's channels); they exchange their maxima.  Keys go by in blocks of
+// KB:
 //   S = Q K^T      D / 16 steps of kind::f16, M 128, N KB; into KB columns
 //   O += P V       KB / 16 steps, M 128, N D; P as the A operand from tensor
-//                  memory, over S's own columns
+//                  memory, each half over its own half of S
 // Bound by issue slots: the codes of a block become binary16 once for the 128
 // rows (exactly: byte ^ 0x80 under the exponent of 1024, minus 1152), K as its
 // rows, V transposed (8 keys of a channel are one 16-byte piece), both into the
@@ -17,8 +18,8 @@
 //
 // Scores are scaled as in the few-row kernel (queries by a power of two, ks of
 // the unit of 16 keys).  The reference of the exponents follows the row's
-// maximum only when that grows by more than 2^kSlack: then the thread rescales
-// its output in tensor memory.  Probabilities are binary16 with 2^kShift as the
+// maximum only when that grows by more than 2^kSlack: then the threads rescale
+// the row's output in tensor memory.  Probabilities are binary16 with 2^kShift as the
 // value of the reference (2^15 at most), times vs relative to the piece's
 // largest; sums and outputs are binary32.
 //
@@ -37,6 +38,7 @@ using namespace kv;
 
 constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr float kShift = 9.0f, kSlack = 6.0f;
+constexpr int kThreads = 256;
 
 template <int D>
 struct Tc {
@@ -65,6 +67,7 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
   __shared__ int s_scan[kThreads];
   __shared__ int s_warp[kThreads / 32];
   __shared__ float s_max[kThreads / 32];
+  __shared__ float s_top[2][kWideRows], s_l[kWideRows];   // the halves' maxima; one half's sum
   __shared__ int32_t s_page[3][U];       // of block j in buffer j mod 3
   __shared__ float s_ks[3][U], s_vr[3][U];
   __shared__ __align__(8) uint64_t s_bar[3];
@@ -92,7 +95,11 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const uint32_t t_s = tmem + (static_cast<uint32_t>(warp) << 21), t_o = t_s + KB;   // this warp's 32 lanes
+  // this warp's 32 lanes, and its half of the scores' and the output's columns
+  const int half = warp >> 2, r = tid & (kWideRows - 1);
+  const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+  const uint32_t t_s = t_lane + half * (KB / 2), t_o = t_lane + KB + half * (D / 2);
+  constexpr int UH = U / 2;         // units of a half
   pdl_trigger();
   pdl_wait();
   const KvPages& c = a.c;
@@ -101,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
 
   Walk walk;
   SeqPlan p;
-  for (int64_t item = blockIdx.x; ok && find_item<true, kWideRows>(a, item, walk, s_scan, s_warp, p); item += gridDim.x) {
+  for (int64_t item = blockIdx.x; ok && find_item<true, kWideRows, kThreads>(a, item, walk, s_scan, s_warp, p); item += gridDim.x) {
     const int hk = walk.hk;
     const TileKeys keys(a, p, walk, kWideRows);
     const int32_t k_begin = keys.k_begin, k_end = keys.k_end;
@@ -125,7 +132,9 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
     for (int o = 16; o > 0; o >>= 1) v_top = fmaxf(v_top, __shfl_xor_sync(0xffffffffu, v_top, o));
     if (lane == 0) s_max[warp] = v_top;
     const bool bad = __syncthreads_or(bad_page);
-    v_top = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+    v_top = s_max[0];
+#pragma unroll
+    for (int i = 1; i < kThreads / 32; ++i) v_top = fmaxf(v_top, s_max[i]);
     const float v_inv = v_top >= 0x1p-126f ? __frcp_rn(v_top) : 0.0f;
 
     // page ids and scales of block j's units (threads below U)
@@ -157,8 +166,8 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
       }
     };
     // item i: keys 8 kg .. + 7, channels 4 dq .. + 3; a warp has 4 kg x 8 dq
-    auto v_kg = [&](int i) { return (i * 4 + warp) / (D / 32) * 4 + (lane & 3); };
-    auto v_dq = [&](int i) { return (i * 4 + warp) % (D / 32) * 8 + (lane >> 2); };
+    auto v_kg = [&](int i) { return (i * 8 + warp) / (D / 32) * 4 + (lane & 3); };
+    auto v_dq = [&](int i) { return (i * 8 + warp) % (D / 32) * 8 + (lane >> 2); };
     auto load_v = [&](int j) {
 #pragma unroll
       for (int i = 0; i < C::kLoadsV; ++i) {
@@ -175,8 +184,7 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
     }
     __syncwarp();
 
-    // ---- the tile's queries as binary16, K-major: row tid of this thread
-    const int r = tid;
+    // ---- the tile's queries as binary16, K-major: row r, a half of its channels
     float unit;
     {
       const int tok = (keys.row0 + r) / a.G, g = keys.row0 + r - tok * a.G;
@@ -196,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
       const float f = __uint_as_float(static_cast<uint32_t>(fe) << 23);
       unit = __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) * a.scale_log2;
 #pragma unroll 8
-      for (int i = 0; i < D / 8; ++i) {
+      for (int i = half * (D / 16); i < (half + 1) * (D / 16); ++i) {
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (live) v = *reinterpret_cast<const uint4*>(qp + i * 8);
         const uint4 h = make_uint4(half2_bits(bf16_lo(v.x) * f, bf16_hi(v.x) * f), half2_bits(bf16_lo(v.y) * f, bf16_hi(v.y) * f),
@@ -271,17 +279,17 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
       if (stage) next_scales = unit_scales(j + 2, next_page);
       tc::fence_proxy_async();
 
-      // ---- softmax of the thread's row: the block's maximum, then P over S
+      // ---- softmax of the row's half: the block's maximum, then P over S
       if (!wait(bar_s, ph_s, &s_abort)) ok = false;
       ph_s ^= 1;
       tc::tc_fence_after();
-      const int32_t key0 = k_begin + j * KB;
+      const int32_t key0 = k_begin + j * KB, my_key = key0 + half * (KB / 2);
       const bool edge = key0 < keys.a_lo || key0 + KB > min(keys.a_hi, k_end);   // some row does not see all of it, or the next piece has it
-      const float* ks = s_ks[j % 3];
-      const float* vs = s_vr[j % 3];
+      const float* ks = s_ks[j % 3] + half * UH;
+      const float* vs = s_vr[j % 3] + half * UH;
       float top = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
+      for (int u = 0; u < UH; ++u) {
         uint32_t x[16];
         tc::tmem_ld16(t_s + u * 16, x);
         tc::tmem_wait_ld();
@@ -289,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
         if (edge) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const int32_t key = key0 + u * 16 + e;
+            const int32_t key = my_key + u * 16 + e;
             if (key >= my_lo && key < my_hi) t = fmaxf(t, __uint_as_float(x[e]));
           }
         } else {
@@ -298,12 +306,15 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
         }
         if (t > -INFINITY) top = fmaxf(top, t * (ks[u] * unit));
       }
+      s_top[half][r] = top;
+      __syncthreads();
+      top = fmaxf(top, s_top[half ^ 1][r]);
       const float old = m;
       if (top > m + kSlack || m == -INFINITY) m = top;
       const float al = old == m ? 1.0f : ex2(old - m);   // old = -inf: nothing to keep
       if (__any_sync(0xffffffffu, al != 1.0f) && j > 0) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
+        for (int i = 0; i < D / 32; ++i) {
           uint32_t o[16];
           tc::tmem_ld16(t_o + i * 16, o);
           tc::tmem_wait_ld();
@@ -315,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
       l *= al;
       const float base = m == -INFINITY ? 0.0f : m - kShift;
 #pragma unroll
-      for (int u = 0; u < U; u += 2) {
+      for (int u = 0; u < UH; u += 2) {
         uint32_t pk[16];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -329,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
           if (edge) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const int32_t key = key0 + (u + h) * 16 + e;
+              const int32_t key = my_key + (u + h) * 16 + e;
               if (key < my_lo || key >= my_hi) q[e] = 0.0f;
             }
           }
@@ -356,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
         const uint32_t idesc = tc::idesc_f16_f32(D);
 #pragma unroll
         for (int k = 0; k < KB / 16; ++k)
-          tc::tc_mma_ta(tmem + KB, tmem + k * 8, tc::smem_desc_sw128(smem_u32(s_v) + (k >> 2) * (D * 128)) + 2 * (k & 3), idesc,
+          tc::tc_mma_ta(tmem + KB, tmem + k / UH * (KB / 2) + k % UH * 8, tc::smem_desc_sw128(smem_u32(s_v) + (k >> 2) * (D * 128)) + 2 * (k & 3), idesc,
                         (j | k) != 0 ? 1u : 0u);
         tc::tc_commit(bar_o);
       }
@@ -373,6 +384,11 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
     }
 
     // ---- the row's output, or its piece
+    if (half == 1) s_l[r] = l;
+    __syncthreads();
+    if (half == 0) s_l[r] = l + s_l[r];
+    __syncthreads();
+    l = s_l[r];
     if (bad && tid == 0 && a.err != nullptr) atomicOr(a.err, PRISM_DEV_ERR_PAGE_RANGE);
     const float nanf = __uint_as_float(0x7fc00000u);
     const int tok = (keys.row0 + r) / a.G, h = hk * a.G + keys.row0 + r - tok * a.G;
@@ -383,12 +399,13 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
                 ((static_cast<int64_t>(walk.s) * c.H + hk) * part_stride + walk.split * p.rows + keys.row0 + r) * (D + 4);
     const float scale = !some ? 0.0f : p.splits == 1 ? v_top / l : v_top;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
+    for (int i = 0; i < D / 32; ++i) {
       uint32_t o[16] = {};
       if (blocks > 0) {
         tc::tmem_ld16(t_o + i * 16, o);
         tc::tmem_wait_ld();
       }
+      const int d = half * (D / 2) + i * 16;
       float y[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) y[e] = some ? __uint_as_float(o[e]) * scale : 0.0f;
@@ -397,17 +414,17 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           w[e] = bad ? kBf16NaN * 0x10001u : float_to_bf16_rne(y[2 * e]) | float_to_bf16_rne(y[2 * e + 1]) << 16;
-        uint4* dst = reinterpret_cast<uint4*>(a.out + t * a.ldo_t + h * a.ldo_h + i * 16);
+        uint4* dst = reinterpret_cast<uint4*>(a.out + t * a.ldo_t + h * a.ldo_h + d);
         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
       } else if (live) {
 #pragma unroll
         for (int e = 0; e < 16; e += 4)
-          *reinterpret_cast<float4*>(ps + 4 + i * 16 + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+          *reinterpret_cast<float4*>(ps + 4 + d + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
       }
       __syncwarp();
     }
-    if (live) {
+    if (live && half == 0) {
       const float mx = some ? m - kShift + kPShift : -INFINITY;   // the weights' common form
       if (p.splits > 1) {
         ps[0] = bad ? nanf : mx;

@@ -16,7 +16,6 @@
 namespace prism {
 namespace kv {
 
-constexpr int kThreads = 128;          // of both kernels
 constexpr int kFewRows = 32;
 constexpr int kWideRows = 128;         // rows of a tile of the tcgen05 kernel: the lanes of tensor memory
 constexpr int kMinChunk = 1024;        // keys of a piece at least
@@ -81,23 +80,26 @@ __device__ __forceinline__ int seq_items(const KvAttentionArgs& a, int s, SeqPla
   return p.tiles * p.splits * a.c.H;
 }
 
-// Walks a CTA's items: sequences are counted kThreads at a time by a scan.
+// Walks a CTA's items: sequences are counted a window of one a thread at a
+// time, by a scan.
 struct Walk {
-  int s0 = -kThreads;          // first sequence of the window
+  int s0 = 0, next = 0;        // first sequence of the window, and of the one after
   int64_t base = 0;            // items before it
   int items = 0;               // items in it
   int tile, split, hk, s;      // the item found
 };
-// Finds `item`; false past the last one.  All threads; s_scan [kThreads] and
-// s_warp [kThreads / 32] are free again after the caller's next barrier.
-template <bool kWide, int kTileRows>
+// Finds `item`; false past the last one.  All kThreads threads; s_scan
+// [kThreads] and s_warp [kThreads / 32] are free again after the caller's next
+// barrier.
+template <bool kWide, int kTileRows, int kThreads>
 __device__ __forceinline__ bool find_item(const KvAttentionArgs& a, int64_t item, Walk& w, int* s_scan, int* s_warp,
                                           SeqPlan& p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   while (item >= w.base + w.items) {
     w.base += w.items;
-    w.s0 += kThreads;
-    if (w.s0 >= a.c.S) return false;
+    if (w.next >= a.c.S) return false;
+    w.s0 = w.next;
+    w.next += kThreads;
     SeqPlan q;
     int n = w.s0 + tid < a.c.S ? seq_items<kWide, kTileRows>(a, w.s0 + tid, q) : 0;
     if (!kWide && blockIdx.x == 0 && w.s0 + tid < a.c.S && (n < 0 || (q.bad && n > 0)) && a.err != nullptr)
