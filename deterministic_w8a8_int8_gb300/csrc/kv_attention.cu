@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
   uint8_t* ring = smem + warp * kStages * kStageBytes;
   const uint32_t ring_u = smem_u32(ring);
 
-  Walk walk;
+  Walk walk = new_walk();
   SeqPlan p;
   for (int64_t item = blockIdx.x; find_item<false, kRows, kThreads>(a, item, walk, s_scan, s_warp, p); item += gridDim.x) {
     const int s = walk.s, hk = walk.hk, split = walk.split;
@@ -468,14 +468,35 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
   }
 }
 
-// Joins a row's pieces: a CTA takes rows of one (sequence, KV head) in turn.  Thread i weighs
-// piece i; then D / 4 columns of threads by 1024 / D groups add every group-th
-// piece in order, and the groups are added in order.
+// A joined row's output and lse: y and sum against the reference mx.
+template <int E>
+__device__ __forceinline__ void store_row(const KvAttentionArgs& a, const SeqPlan& p, int hk, int r, int d, const float* y,
+                                          float sum, float mx, bool nan) {
+  const float inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
+  const int64_t t = p.sp.b + r / a.G;
+  const int h = hk * a.G + r % a.G;
+  uint32_t w[E / 2];
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e)
+    w[e] = nan ? kBf16NaN * 0x10001u : float_to_bf16_rne(y[2 * e] * inv) | float_to_bf16_rne(y[2 * e + 1] * inv) << 16;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + t * a.ldo_t + h * a.ldo_h + d);
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) dst[e] = w[e];
+  if (d == 0 && a.lse != nullptr)
+    a.lse[t * a.Hq + h] = nan ? __uint_as_float(0x7fc00000u) : mx == -INFINITY ? mx : (mx - kPShift + log2f(sum)) * kLn2;
+}
+
+// Joins the pieces of rows of one (sequence, KV head).  Up to kWarpPieces
+// pieces: a row a warp, each lane D / 32 channels.  More: a row a CTA; thread i
+// weighs piece i, then D / 4 columns of threads by 1024 / D groups add every
+// group-th piece in order, and the groups are added in order.
+constexpr int kWarpPieces = 16;
+
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
     kv_combine_kernel(const __grid_constant__ KvAttentionArgs a, int64_t part_stride) {
-  constexpr int kCols = D / 4, kGroups = kJoinThreads / kCols;
-  __shared__ float s_f[kJoinThreads], s_red[kJoinThreads / 32], s_sum[kJoinThreads / 32];
+  constexpr int kCols = D / 4, kGroups = kJoinThreads / kCols, kJoinWarps = kJoinThreads / 32, E = D / 32;
+  __shared__ float s_f[kJoinThreads], s_red[kJoinWarps], s_sum[kJoinWarps];
   __shared__ float4 s_o[kJoinThreads];
   static_assert(kMaxSplit <= kJoinThreads, "a thread for each piece");
   pdl_trigger();
@@ -484,10 +505,48 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int s = blockIdx.x, hk = blockIdx.y;
   SeqPlan p;
   if (seq_items<false, 1>(a, s, p) < 0 || p.bad || p.splits == 1) return;
+  const float* base = static_cast<const float*>(a.ws) + (static_cast<int64_t>(s) * a.c.H + hk) * part_stride * (D + 4);
+  const int64_t step = static_cast<int64_t>(p.rows) * (D + 4);
+  if (p.splits <= kWarpPieces) {
+    for (int r = blockIdx.z * kJoinWarps + warp; r < p.rows; r += gridDim.z * kJoinWarps) {
+      const float* part = base + static_cast<int64_t>(r) * (D + 4);
+      float pm = -INFINITY, pl = 0.0f;
+      if (lane < p.splits) pm = part[lane * step], pl = part[lane * step + 1];
+      const bool nan = __any_sync(0xffffffffu, pm != pm);
+      float mx = pm;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      mx = __shfl_sync(0xffffffffu, mx, 0);
+      const float f = pm == -INFINITY ? 0.0f : ex2(pm - mx);
+      float sum = 0.0f, y[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = 0.0f;
+#pragma unroll 4
+      for (int i = 0; i < p.splits; ++i) {
+        const float w = __shfl_sync(0xffffffffu, f, i);
+        sum = fmaf(w, __shfl_sync(0xffffffffu, pl, i), sum);
+        const float* v = part + i * step + 4 + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += E < 4 ? 2 : 4) {
+          if constexpr (E < 4) {
+            const float2 x = *reinterpret_cast<const float2*>(v + e);
+            y[e] = fmaf(w, x.x, y[e]);
+            y[e + 1] = fmaf(w, x.y, y[e + 1]);
+          } else {
+            const float4 x = *reinterpret_cast<const float4*>(v + e);
+            y[e] = fmaf(w, x.x, y[e]);
+            y[e + 1] = fmaf(w, x.y, y[e + 1]);
+            y[e + 2] = fmaf(w, x.z, y[e + 2]);
+            y[e + 3] = fmaf(w, x.w, y[e + 3]);
+          }
+        }
+      }
+      store_row<E>(a, p, hk, r, lane * E, y, sum, mx, nan);
+    }
+    return;
+  }
   for (int r = blockIdx.z; r < p.rows; r += gridDim.z) {
-    const float* part = static_cast<const float*>(a.ws) +
-                        ((static_cast<int64_t>(s) * a.c.H + hk) * part_stride + r) * (D + 4);
-    const int64_t step = static_cast<int64_t>(p.rows) * (D + 4);
+    const float* part = base + static_cast<int64_t>(r) * (D + 4);
     float pm = -INFINITY, pl = 0.0f;
     if (tid < p.splits) pm = part[tid * step], pl = part[tid * step + 1];
     const bool nan = __syncthreads_or(pm != pm);
@@ -498,7 +557,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     __syncthreads();
     mx = s_red[0];
 #pragma unroll
-    for (int w = 1; w < kJoinThreads / 32; ++w) mx = fmaxf(mx, s_red[w]);
+    for (int w = 1; w < kJoinWarps; ++w) mx = fmaxf(mx, s_red[w]);
     const float f = pm == -INFINITY ? 0.0f : ex2(pm - mx);
     s_f[tid] = f;
     float l = f * pl;
@@ -507,36 +566,28 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (lane == 0) s_sum[warp] = l;
     __syncthreads();
     const int col = tid % kCols, group = tid / kCols;
-    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
     for (int i = group; i < p.splits; i += kGroups) {
       const float4 v = *reinterpret_cast<const float4*>(part + i * step + 4 + col * 4);
       const float w = s_f[i];
-      y.x = fmaf(w, v.x, y.x);
-      y.y = fmaf(w, v.y, y.y);
-      y.z = fmaf(w, v.z, y.z);
-      y.w = fmaf(w, v.w, y.w);
+      y[0] = fmaf(w, v.x, y[0]);
+      y[1] = fmaf(w, v.y, y[1]);
+      y[2] = fmaf(w, v.z, y[2]);
+      y[3] = fmaf(w, v.w, y[3]);
     }
-    s_o[tid] = y;
+    s_o[tid] = make_float4(y[0], y[1], y[2], y[3]);
     __syncthreads();
     if (group == 0) {
 #pragma unroll
       for (int g = 1; g < kGroups; ++g) {
         const float4 v = s_o[g * kCols + col];
-        y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+        y[0] += v.x, y[1] += v.y, y[2] += v.z, y[3] += v.w;
       }
       float sum = s_sum[0];
 #pragma unroll
-      for (int w = 1; w < kJoinThreads / 32; ++w) sum += s_sum[w];
-      const float nanf = __uint_as_float(0x7fc00000u), inv = mx == -INFINITY ? 0.0f : 1.0f / sum;
-      const int64_t t = p.sp.b + r / a.G;
-      const int h = hk * a.G + r % a.G;
-      uint2 w = make_uint2(float_to_bf16_rne(y.x * inv) | float_to_bf16_rne(y.y * inv) << 16,
-                           float_to_bf16_rne(y.z * inv) | float_to_bf16_rne(y.w * inv) << 16);
-      if (nan) w = make_uint2(kBf16NaN * 0x10001u, kBf16NaN * 0x10001u);
-      *reinterpret_cast<uint2*>(a.out + t * a.ldo_t + h * a.ldo_h + col * 4) = w;
-      if (tid == 0 && a.lse != nullptr)
-        a.lse[t * a.Hq + h] = nan ? nanf : mx == -INFINITY ? mx : (mx - kPShift + log2f(sum)) * kLn2;
+      for (int w = 1; w < kJoinWarps; ++w) sum += s_sum[w];
+      store_row<4>(a, p, hk, r, col * 4, y, sum, mx, nan);
     }
     __syncthreads();   // the weights and sums are free again
   }
@@ -569,7 +620,7 @@ cudaError_t launch_d(const KvAttentionArgs& a, cudaStream_t stream) {
                                             : launch_few<D, D == 256 ? 2 : 4>(a, part_stride, stream);
   if (e == cudaSuccess && rows > kFewRows) e = launch_kv_attention_wide(a, part_stride, stream);
   if (e != cudaSuccess || part_stride == 0) return e;
-  const dim3 grid(a.c.S, a.c.H, static_cast<unsigned>(std::min<int64_t>(split_rows, 64)));
+  const dim3 grid(a.c.S, a.c.H, static_cast<unsigned>(std::min<int64_t>(split_rows, 128)));
   return launch_kernel(kv_combine_kernel<D>, grid, dim3(kJoinThreads), 0, stream, false, a, part_stride);
 }
 

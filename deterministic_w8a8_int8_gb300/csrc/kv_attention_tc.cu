@@ -2,29 +2,33 @@
 // prompt's piece, questions of many tokens) on the tcgen05 tensor cores.
 //
 // A tile is 128 rows (queries x heads of a KV head), each a lane of tensor
-// memory.  Two threads have a row, one for each half of a block's keys (and of
-// the output's channels); they exchange their maxima.  Keys go by in blocks of
-// KB:
+// memory.  Keys go by in blocks of KB:
 //   S = Q K^T      D / 16 steps of kind::f16, M 128, N KB; into KB columns
 //   O += P V       KB / 16 steps, M 128, N D; P as the A operand from tensor
 //                  memory, each half over its own half of S
-// Bound by issue slots: the codes of a block become binary16 once for the 128
-// rows (exactly: byte ^ 0x80 under the exponent of 1024, minus 1152), K as its
-// rows, V transposed (8 keys of a channel are one 16-byte piece), both into the
-// 128-byte-swizzled K-major operand layout; and each score costs about six
-// instructions.  Raw codes of the next block are read ahead into registers.
-// Two CTAs on an SM (one for D = 256) overlap one's conversion and softmax with
-// the other's instructions.
+// One CTA an SM, with three kinds of warps that pass blocks on by mbarriers:
+//   converters (4 warps)  read a block's codes ahead into registers, 8 keys by
+//     16 channels of K and of V a thread, and widen them once for the 128 rows,
+//     exactly (byte ^ 0x80 under the exponent of 1024, minus 1152), into two
+//     stages of the 128-byte-swizzled K-major operand layout: K as its rows, V
+//     transposed (8 keys of a channel are one 16-byte piece);
+//   the issuer (1 warp)   Q K^T of block j + 1, S being double-buffered, ahead
+//     of P V of block j;
+//   softmax (8 warps)     two threads a row, one for each half of the block's
+//     keys (and of the output's channels); they exchange their maxima.
+// The softmax's instructions bound it: about six a score.
 //
 // Scores are scaled as in the few-row kernel (queries by a power of two, ks of
 // the unit of 16 keys).  The reference of the exponents follows the row's
 // maximum only when that grows by more than 2^kSlack: then the threads rescale
-// the row's output in tensor memory.  Probabilities are binary16 with 2^kShift as the
-// value of the reference (2^15 at most), times vs relative to the piece's
-// largest; sums and outputs are binary32.
+// the row's output in tensor memory.  Probabilities are binary16 with 2^kShift
+// as the value of the reference (2^15 at most), times vs relative to the
+// piece's largest; sums and outputs are binary32.
 //
-// Every wait is bounded: after 2 s the kernel sets the device status bit, lets
-// its instructions in flight complete and returns.
+// Every wait on an mbarrier is bounded: after 2 s the kernel sets the device
+// status bit; every warp then runs its loops out without waiting (so that the
+// named barriers still meet), the instructions in flight complete, and the
+// kernel returns.
 #include "kv_plan.cuh"
 #include "tc_common.cuh"
 
@@ -38,18 +42,21 @@ using namespace kv;
 
 constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr float kShift = 9.0f, kSlack = 6.0f;
-constexpr int kThreads = 256;
+constexpr int kSoftWarps = 8, kConvWarps = 4;
+constexpr int kThreads = (kSoftWarps + kConvWarps + 1) * 32;
+constexpr int kSoft = kSoftWarps * 32, kConv = kConvWarps * 32;
+constexpr int kUnitSlots = 4;     // blocks whose units' scales are held
 
 template <int D>
 struct Tc {
   static constexpr int kKeys = D == 256 ? 64 : 128;            // keys of a block
   static constexpr int kUnits = kKeys / 16;
-  static constexpr int kCtas = D == 256 ? 1 : 2;               // on an SM: tensor memory has 512 columns
-  static constexpr int kCols = kKeys + D <= 256 ? 256 : 512;
+  static constexpr int kCols = 512;                            // S twice and O
   static constexpr int kQ = kWideRows * D * 2, kK = kKeys * D * 2, kV = kKeys * D * 2;
-  static constexpr int kBytes = kQ + kK + kV + 1024;           // operands start on 1024-byte boundaries
-  static constexpr int kLoadsK = kKeys * D / 16 / kThreads;    // 16-byte pieces of K a thread converts
-  static constexpr int kLoadsV = kKeys / 8 * (D / 4) / kThreads;   // 8 keys x 4 channels of V
+  static constexpr int kBytes = kQ + 2 * (kK + kV) + 1024;     // operands start on 1024-byte boundaries
+  static constexpr int kItems = kKeys / 8 * (D / 16);          // 8 keys x 16 channels, one a thread
+  static_assert(kItems <= kConv, "an item a thread");
+  static_assert(2 * kKeys + D <= kCols, "tensor memory");
 };
 
 // One answer for the warp, whose lanes are together again afterwards.
@@ -57,31 +64,74 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
   return __all_sync(0xffffffffu, tc::mbar_wait_bounded(bar, parity, abort_flag, kWaitNs, &g_kv_status,
                                                        PRISM_DEVSTATUS_WAIT_TIMEOUT));
 }
+// tc::tc_mma and tc::tc_mma_ta of the lane with `lead`, in code that the whole
+// warp runs.
+__device__ __forceinline__ void mma_if(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, l;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 l, %5, 0;\n"
+      " @l tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ta_if(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, l;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 l, %5, 0;\n"
+      " @l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
+__global__ void __launch_bounds__(kThreads, 1)
     kv_attention_tc_kernel(const __grid_constant__ KvAttentionArgs a, int64_t part_stride) {
   using C = Tc<D>;
-  constexpr int KB = C::kKeys, U = C::kUnits;
+  constexpr int KB = C::kKeys, U = C::kUnits, UH = U / 2;
   extern __shared__ uint8_t smem_raw[];
+  // the item in work lies in shared memory: no warp holds another's part of it
+  __shared__ struct {
+    Walk walk;
+    SeqPlan plan;
+    TileKeys keys;
+  } s_item;
   __shared__ int s_scan[kThreads];
   __shared__ int s_warp[kThreads / 32];
   __shared__ float s_max[kThreads / 32];
-  __shared__ float s_top[2][kWideRows], s_l[kWideRows];   // the halves' maxima; one half's sum
-  __shared__ int32_t s_page[3][U];       // of block j in buffer j mod 3
-  __shared__ float s_ks[3][U], s_vr[3][U];
-  __shared__ __align__(8) uint64_t s_bar[3];
+  __shared__ float s_top[2][2][kWideRows], s_l[kWideRows];   // the halves' maxima (by the block's parity); one half's sum
+  __shared__ float s_ks[kUnitSlots][U], s_vr[kUnitSlots][U];
+  // completions: K, V converted; scales in place; S formed (K free); P formed; O added to (V, P free); queries; the end
+  __shared__ __align__(8) uint64_t s_bar[6 * 2 + kUnitSlots + 2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* s_q = smem;
-  uint8_t* s_k = s_q + C::kQ;
-  uint8_t* s_v = s_k + C::kK;
-  const uint32_t bar_s = smem_u32(&s_bar[0]), bar_o = smem_u32(&s_bar[1]), bar_end = smem_u32(&s_bar[2]);
+  uint8_t* s_k = s_q + C::kQ;            // two stages
+  uint8_t* s_v = s_k + 2 * C::kK;
+  const uint32_t bars = smem_u32(s_bar);
+  auto bar_k = [&](uint32_t g) { return bars + 8 * (g & 1); };
+  auto bar_v = [&](uint32_t g) { return bars + 16 + 8 * (g & 1); };
+  auto bar_s = [&](uint32_t g) { return bars + 32 + 8 * (g & 1); };
+  auto bar_kfree = [&](uint32_t g) { return bars + 48 + 8 * (g & 1); };
+  auto bar_p = [&](uint32_t g) { return bars + 64 + 8 * (g & 1); };
+  auto bar_o = [&](uint32_t g) { return bars + 80 + 8 * (g & 1); };
+  auto bar_u = [&](uint32_t g) { return bars + 96 + 8 * (g & (kUnitSlots - 1)); };
+  const uint32_t bar_q = bars + 96 + 8 * kUnitSlots, bar_end = bar_q + 8;
   if (tid == 0) {
-    tc::mbar_init(bar_s, 1);
-    tc::mbar_init(bar_o, 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar_k(i), kConv);
+      tc::mbar_init(bar_v(i), kConv);
+      tc::mbar_init(bar_s(i), 1);
+      tc::mbar_init(bar_kfree(i), 1);
+      tc::mbar_init(bar_p(i), kSoft);
+      tc::mbar_init(bar_o(i), 1);
+    }
+    for (int i = 0; i < kUnitSlots; ++i) tc::mbar_init(bar_u(i), kConv);
+    tc::mbar_init(bar_q, kSoft);
     tc::mbar_init(bar_end, 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -95,25 +145,30 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = s_tmem;
-  // this warp's 32 lanes, and its half of the scores' and the output's columns
-  const int half = warp >> 2, r = tid & (kWideRows - 1);
-  const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp & 3) << 21);
-  const uint32_t t_s = t_lane + half * (KB / 2), t_o = t_lane + KB + half * (D / 2);
-  constexpr int UH = U / 2;         // units of a half
   pdl_trigger();
   pdl_wait();
   const KvPages& c = a.c;
-  uint32_t ph_s = 0, ph_o = 0;      // parity of the next completion
-  bool ok = true;
+  uint32_t g0 = 0, items = 0;      // blocks and items before this item: the phases of the mbarriers
+  if (tid == 0) s_item.walk = new_walk();
+  __syncthreads();
 
-  Walk walk;
-  SeqPlan p;
-  for (int64_t item = blockIdx.x; ok && find_item<true, kWideRows, kThreads>(a, item, walk, s_scan, s_warp, p); item += gridDim.x) {
-    const int hk = walk.hk;
-    const TileKeys keys(a, p, walk, kWideRows);
-    const int32_t k_begin = keys.k_begin, k_end = keys.k_end;
+  for (int64_t item = blockIdx.x;; item += gridDim.x, ++items) {
+    {
+      Walk walk = s_item.walk;
+      SeqPlan plan;
+      if (!find_item<true, kWideRows, kThreads>(a, item, walk, s_scan, s_warp, plan)) break;
+      __syncthreads();               // everyone has read s_item
+      if (tid == 0) {
+        s_item.walk = walk;
+        s_item.plan = plan;
+        s_item.keys = TileKeys(a, plan, walk, kWideRows);
+      }
+      __syncthreads();
+    }
+    const int hk = s_item.walk.hk;
+    const int32_t k_begin = s_item.keys.k_begin, k_end = s_item.keys.k_end;
     const int blocks = k_end > k_begin ? (k_end - k_begin + KB - 1) / KB : 0;
-    const int32_t* table = c.table + walk.s * c.ld_table;
+    const int32_t* table = c.table + s_item.walk.s * c.ld_table;
 
     // ---- the piece's largest value scale, and its pages' validity
     bool bad_page = false;
@@ -137,309 +192,359 @@ __global__ void __launch_bounds__(kThreads, Tc<D>::kCtas)
     for (int i = 1; i < kThreads / 32; ++i) v_top = fmaxf(v_top, s_max[i]);
     const float v_inv = v_top >= 0x1p-126f ? __frcp_rn(v_top) : 0.0f;
 
-    // page ids and scales of block j's units (threads below U)
-    auto unit_page = [&](int j) {
-      const int32_t key = k_begin + j * KB + tid * 16;
-      const int32_t page = key < k_end ? table[key >> c.block_shift] : 0;
-      return page < 0 || page >= c.num_pages ? 0 : page;
-    };
-    auto unit_scales = [&](int j, int32_t page) {
-      const int64_t at = static_cast<int64_t>(page) * c.H + hk;
-      return k_begin + j * KB + tid * 16 < k_end ? make_float2(c.k_scale[at], c.v_scale[at] * v_inv) : make_float2(0.0f, 0.0f);
-    };
-    auto stage_units = [&](int j, int32_t page, float2 scales) {
-      s_page[j % 3][tid] = page;
-      s_ks[j % 3][tid] = scales.x;
-      s_vr[j % 3][tid] = scales.y;
-    };
-    uint4 kr[C::kLoadsK];
-    uint32_t vr[C::kLoadsV][8];
-    auto row_ptr = [&](const int8_t* codes, int j, int key) {   // key of block j
-      const int32_t pos = k_begin + j * KB + key;
-      return codes + ((static_cast<int64_t>(s_page[j % 3][key >> 4]) * c.H + hk) * c.block + (pos & (c.block - 1))) * D;
-    };
-    auto load_k = [&](int j) {
+    if (warp >= kSoftWarps && warp < kSoftWarps + kConvWarps) {
+      // ============================ converters ==============================
+      const int ct = tid - kSoft;
+      const bool mine = ct < C::kItems;
+      // a thread's item, keys 8 kg .. + 7 and channels 16 ch .. + 15, of K: the
+      // pieces of a row side by side; of V: eight key groups of a channel, whose
+      // pieces fill all banks
+      const int k_kg = ct / (D / 16), k_ch = ct % (D / 16);
+      const int v_kg = ct / (8 * (D / 16)) * 8 + (ct & 7), v_ch = ct / 8 % (D / 16);
+      // a page id is read two blocks ahead and looked at when it is used
+      auto page_at = [&](int32_t key, bool live) { return live && key < k_end ? table[key >> c.block_shift] : 0; };
+      auto k_page = [&](int j) { return page_at(k_begin + j * KB + k_kg * 8, mine); };
+      auto v_page = [&](int j) { return page_at(k_begin + j * KB + v_kg * 8, mine); };
+      auto u_page = [&](int j) { return page_at(k_begin + j * KB + ct * 16, ct < U); };
+      auto row = [&](int32_t page) {          // an invalid page (the rows get NaN) or none: page 0, in its stead
+        return static_cast<int64_t>(page < 0 || page >= c.num_pages ? 0 : page) * c.H + hk;
+      };
+      auto u_scales = [&](int j, int32_t page) {        // of the block's unit ct; vs not yet divided
+        const int64_t at = row(page);
+        return ct < U && k_begin + j * KB + ct * 16 < k_end ? make_float2(c.k_scale[at], c.v_scale[at])
+                                                            : make_float2(0.0f, 0.0f);
+      };
+      uint4 rk[8], rv[8];
+      auto load = [&](uint4(&raw)[8], const int8_t* codes, int32_t key, int ch, int32_t page) {
+        const int8_t* src = codes + (row(page) * c.block + (key & (c.block - 1))) * D + ch * 16;
 #pragma unroll
-      for (int i = 0; i < C::kLoadsK; ++i) {
-        const int at = i * kThreads + tid;
-        kr[i] = ld_stream_16(row_ptr(c.k_codes, j, at / (D / 16)) + at % (D / 16) * 16);
-      }
-    };
-    // item i: keys 8 kg .. + 7, channels 4 dq .. + 3; a warp has 4 kg x 8 dq
-    auto v_kg = [&](int i) { return (i * 8 + warp) / (D / 32) * 4 + (lane & 3); };
-    auto v_dq = [&](int i) { return (i * 8 + warp) % (D / 32) * 8 + (lane >> 2); };
-    auto load_v = [&](int j) {
-#pragma unroll
-      for (int i = 0; i < C::kLoadsV; ++i) {
-        const int8_t* src = row_ptr(c.v_codes, j, v_kg(i) * 8) + v_dq(i) * 4;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) vr[i][k] = __ldg(reinterpret_cast<const uint32_t*>(src + k * D));
-      }
-    };
-    if (tid < U) {
-      for (int j = 0; j < min(blocks, 2); ++j) {
-        const int32_t page = unit_page(j);
-        stage_units(j, page, unit_scales(j, page));
-      }
-    }
-    __syncwarp();
-
-    // ---- the tile's queries as binary16, K-major: row r, a half of its channels
-    float unit;
-    {
-      const int tok = (keys.row0 + r) / a.G, g = keys.row0 + r - tok * a.G;
-      const uint16_t* qp = a.q + static_cast<int64_t>(p.sp.b + tok) * a.ldq_t + static_cast<int64_t>(hk * a.G + g) * a.ldq_h;
-      const bool live = r < keys.n_rows;
-      float amax = 0.0f;
-#pragma unroll 8
-      for (int i = 0; i < D / 8; ++i) {
-        if (live) {
-          const uint4 v = *reinterpret_cast<const uint4*>(qp + i * 8);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+        for (int k = 0; k < 8; ++k) raw[k] = ld_stream_16(src + k * D);
+      };
+      auto load_k = [&](int j, int32_t page) { load(rk, c.k_codes, k_begin + j * KB + k_kg * 8, k_ch, page); };
+      auto load_v = [&](int j, int32_t page) { load(rv, c.v_codes, k_begin + j * KB + v_kg * 8, v_ch, page); };
+      // ahead: codes by one block, their pages by two; scales by two, their pages by three
+      int32_t next_k = 0, next_v = 0, next_u = 0;
+      float2 scales = make_float2(0.0f, 0.0f), next_scales = scales;
+      if (blocks > 0) {
+        const int32_t pk = k_page(0), pv = v_page(0), pu = u_page(0), pu1 = u_page(1);
+        next_k = k_page(1);
+        next_v = v_page(1);
+        next_u = u_page(2);
+        if (mine) {
+          load_k(0, pk);
+          load_v(0, pv);
         }
+        scales = u_scales(0, pu);
+        next_scales = u_scales(1, pu1);
       }
-      const int fe = query_exponent(amax);
-      const float f = __uint_as_float(static_cast<uint32_t>(fe) << 23);
-      unit = __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) * a.scale_log2;
-#pragma unroll 8
-      for (int i = half * (D / 16); i < (half + 1) * (D / 16); ++i) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (live) v = *reinterpret_cast<const uint4*>(qp + i * 8);
-        const uint4 h = make_uint4(half2_bits(bf16_lo(v.x) * f, bf16_hi(v.x) * f), half2_bits(bf16_lo(v.y) * f, bf16_hi(v.y) * f),
-                                   half2_bits(bf16_lo(v.z) * f, bf16_hi(v.z) * f), half2_bits(bf16_lo(v.w) * f, bf16_hi(v.w) * f));
-        *reinterpret_cast<uint4*>(s_q + (i >> 3) * (kWideRows * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4)) = h;
-      }
-    }
-    const int32_t row_hi = keys.hi(r), my_lo = keys.lo(row_hi), my_hi = min(row_hi, k_end);
-    __syncthreads();   // pages and scales of blocks 0 and 1
-    if (blocks > 0) {
-      load_k(0);
-      load_v(0);
-    }
-    float m = -INFINITY, l = 0.0f;
-
-    for (int j = 0; j < blocks; ++j) {
-      // ---- K: 16 codes of a key are two pieces of the operand
-#pragma unroll
-      for (int i = 0; i < C::kLoadsK; ++i) {
-        const int at = i * kThreads + tid, key = at / (D / 16), ch = at % (D / 16);
-        const uint32_t x = kr[i].x ^ 0x80808080u, y = kr[i].y ^ 0x80808080u, z = kr[i].z ^ 0x80808080u, w = kr[i].w ^ 0x80808080u;
-        uint8_t* dst = s_k + (ch >> 2) * (KB * 128) + key * 128;
-        const int piece = (ch & 3) * 2;
-        *reinterpret_cast<uint4*>(dst + ((piece ^ (key & 7)) << 4)) =
-            make_uint4(widen(x, 0x4140u), widen(x, 0x4342u), widen(y, 0x4140u), widen(y, 0x4342u));
-        *reinterpret_cast<uint4*>(dst + (((piece + 1) ^ (key & 7)) << 4)) =
-            make_uint4(widen(z, 0x4140u), widen(z, 0x4342u), widen(w, 0x4140u), widen(w, 0x4342u));
-      }
-      if (j + 1 < blocks) load_k(j + 1);
-      const bool stage = tid < U && j + 2 < blocks;   // this thread reads a unit of block j + 2 ahead
-      int32_t next_page = 0;
-      float2 next_scales = make_float2(0.0f, 0.0f);
-      if (stage) next_page = unit_page(j + 2);
-      tc::fence_proxy_async();
-      if (j > 0) {          // P V of the block before: it read P where S goes now, and V
-        if (!wait(bar_o, ph_o, &s_abort)) ok = false;
-        ph_o ^= 1;
-        tc::tc_fence_after();
-      }
-      tc::tc_fence_before();
-      __syncthreads();      // K (and the queries) in place, S's columns free
-      if (tid == 0) {
-        tc::tc_fence_after();
-        const uint32_t idesc = tc::idesc_f16_f32(KB);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc::tc_mma(tmem, tc::smem_desc_sw128(smem_u32(s_q) + (k >> 2) * (kWideRows * 128)) + 2 * (k & 3),
-                     tc::smem_desc_sw128(smem_u32(s_k) + (k >> 2) * (KB * 128)) + 2 * (k & 3), idesc, k != 0 ? 1u : 0u);
-        tc::tc_commit(bar_s);
-      }
-      __syncwarp();
-      // ---- V, transposed: 8 keys of a channel are one piece of the operand
-#pragma unroll
-      for (int i = 0; i < C::kLoadsV; ++i) {
-        uint32_t h[4][4];   // [channel][key pair]
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t x = __byte_perm(vr[i][2 * k], vr[i][2 * k + 1], 0x5140u) ^ 0x80808080u;
-          const uint32_t y = __byte_perm(vr[i][2 * k], vr[i][2 * k + 1], 0x7362u) ^ 0x80808080u;
-          h[0][k] = widen(x, 0x4140u);
-          h[1][k] = widen(x, 0x4342u);
-          h[2][k] = widen(y, 0x4140u);
-          h[3][k] = widen(y, 0x4342u);
+      for (int j = 0; j < blocks; ++j) {
+        const uint32_t g = g0 + j, ph = (g >> 1) & 1;
+        if (ct < U) {
+          s_ks[g & (kUnitSlots - 1)][ct] = scales.x;
+          s_vr[g & (kUnitSlots - 1)][ct] = scales.y * v_inv;
         }
-        const int kg = v_kg(i), d0 = v_dq(i) * 4;
+        tc::mbar_arrive(bar_u(g));
+        scales = next_scales;
+        next_scales = u_scales(j + 2, next_u);
+        next_u = u_page(j + 3);
+        // ---- K: 16 codes of a key are two pieces of the operand
+        wait(bar_kfree(g), ph ^ 1u, &s_abort);
+        if (mine) {
+          uint8_t* dst = s_k + (g & 1) * C::kK + (k_ch >> 2) * (KB * 128) + k_kg * 1024;
+          const int piece = (k_ch & 3) * 2;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<uint4*>(s_v + (kg >> 3) * (D * 128) + (d0 + e) * 128 + (((kg & 7) ^ ((d0 + e) & 7)) << 4)) =
-              make_uint4(h[e][0], h[e][1], h[e][2], h[e][3]);
-      }
-      if (j + 1 < blocks) load_v(j + 1);
-      if (stage) next_scales = unit_scales(j + 2, next_page);
-      tc::fence_proxy_async();
-
-      // ---- softmax of the row's half: the block's maximum, then P over S
-      if (!wait(bar_s, ph_s, &s_abort)) ok = false;
-      ph_s ^= 1;
-      tc::tc_fence_after();
-      const int32_t key0 = k_begin + j * KB, my_key = key0 + half * (KB / 2);
-      const bool edge = key0 < keys.a_lo || key0 + KB > min(keys.a_hi, k_end);   // some row does not see all of it, or the next piece has it
-      const float* ks = s_ks[j % 3] + half * UH;
-      const float* vs = s_vr[j % 3] + half * UH;
-      float top = -INFINITY;
-#pragma unroll
-      for (int u = 0; u < UH; ++u) {
-        uint32_t x[16];
-        tc::tmem_ld16(t_s + u * 16, x);
-        tc::tmem_wait_ld();
-        float t = -INFINITY;
-        if (edge) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int32_t key = my_key + u * 16 + e;
-            if (key >= my_lo && key < my_hi) t = fmaxf(t, __uint_as_float(x[e]));
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t x = rk[k].x ^ 0x80808080u, y = rk[k].y ^ 0x80808080u;
+            const uint32_t z = rk[k].z ^ 0x80808080u, w = rk[k].w ^ 0x80808080u;
+            *reinterpret_cast<uint4*>(dst + k * 128 + ((piece ^ k) << 4)) =
+                make_uint4(widen(x, 0x4140u), widen(x, 0x4342u), widen(y, 0x4140u), widen(y, 0x4342u));
+            *reinterpret_cast<uint4*>(dst + k * 128 + (((piece + 1) ^ k) << 4)) =
+                make_uint4(widen(z, 0x4140u), widen(z, 0x4342u), widen(w, 0x4140u), widen(w, 0x4342u));
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) t = fmaxf(t, __uint_as_float(x[e]));
+          if (j + 1 < blocks) load_k(j + 1, next_k);
         }
-        if (t > -INFINITY) top = fmaxf(top, t * (ks[u] * unit));
-      }
-      s_top[half][r] = top;
-      __syncthreads();
-      top = fmaxf(top, s_top[half ^ 1][r]);
-      const float old = m;
-      if (top > m + kSlack || m == -INFINITY) m = top;
-      const float al = old == m ? 1.0f : ex2(old - m);   // old = -inf: nothing to keep
-      if (__any_sync(0xffffffffu, al != 1.0f) && j > 0) {
+        tc::fence_proxy_async();
+        tc::mbar_arrive(bar_k(g));
+        next_k = k_page(j + 2);
+        // ---- V, transposed: 8 keys of a channel are one piece of the operand
+        wait(bar_o(g), ph ^ 1u, &s_abort);
+        if (mine) {
+          uint8_t* dst = s_v + (g & 1) * C::kV + (v_kg >> 3) * (D * 128) + v_ch * 16 * 128;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          uint32_t o[16];
-          tc::tmem_ld16(t_o + i * 16, o);
-          tc::tmem_wait_ld();
+          for (int w = 0; w < 4; ++w) {
+            uint32_t h[4][4];   // [channel][key pair]
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-          tc::tmem_st16(t_o + i * 16, o);
+            for (int k = 0; k < 4; ++k) {
+              const uint4 r0 = rv[2 * k], r1 = rv[2 * k + 1];
+              const uint32_t w0 = w == 0 ? r0.x : w == 1 ? r0.y : w == 2 ? r0.z : r0.w;
+              const uint32_t w1 = w == 0 ? r1.x : w == 1 ? r1.y : w == 2 ? r1.z : r1.w;
+              const uint32_t x = __byte_perm(w0, w1, 0x5140u) ^ 0x80808080u;
+              const uint32_t y = __byte_perm(w0, w1, 0x7362u) ^ 0x80808080u;
+              h[0][k] = widen(x, 0x4140u);
+              h[1][k] = widen(x, 0x4342u);
+              h[2][k] = widen(y, 0x4140u);
+              h[3][k] = widen(y, 0x4342u);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(dst + (w * 4 + e) * 128 + (((v_kg & 7) ^ ((w * 4 + e) & 7)) << 4)) =
+                  make_uint4(h[e][0], h[e][1], h[e][2], h[e][3]);
+          }
+          if (j + 1 < blocks) load_v(j + 1, next_v);
         }
+        tc::fence_proxy_async();
+        tc::mbar_arrive(bar_v(g));
+        next_v = v_page(j + 2);
       }
-      l *= al;
-      const float base = m == -INFINITY ? 0.0f : m - kShift;
+    } else if (warp == kSoftWarps + kConvWarps) {
+      // ============================ issuer ==================================
+      // the whole warp forms the descriptors (uniform registers), one lane issues
+      const uint32_t lead = lane == 0 ? 1u : 0u;
+      const uint32_t id_s = tc::idesc_f16_f32(KB), id_o = tc::idesc_f16_f32(D);
+      const uint64_t qd = tc::smem_desc_sw128(smem_u32(s_q));
+      bool ok = blocks == 0 || wait(bar_q, items & 1u, &s_abort);
+      auto issue_scores = [&](uint32_t g) {       // S of block g, into its buffer
+        ok = ok && wait(bar_k(g), (g >> 1) & 1, &s_abort);
+        ok = ok && wait(bar_o(g), ((g >> 1) & 1) ^ 1u, &s_abort);   // P of block g - 2 was read there
+        if (ok) {
+          tc::tc_fence_after();
+          const uint64_t kd = tc::smem_desc_sw128(smem_u32(s_k + (g & 1) * C::kK));
+          const uint32_t dt = tmem + (g & 1) * KB;
 #pragma unroll
-      for (int u = 0; u < UH; u += 2) {
-        uint32_t pk[16];
+          for (int k = 0; k < D / 16; ++k)
+            mma_if(lead, dt, qd + (k >> 2) * (kWideRows * 8) + 2 * (k & 3), kd + (k >> 2) * (KB * 8) + 2 * (k & 3), id_s,
+                   k != 0 ? 1u : 0u);
+          if (lead) {
+            tc::tc_commit(bar_s(g));
+            tc::tc_commit(bar_kfree(g));
+          }
+        }
+        __syncwarp();
+      };
+      if (blocks > 0) issue_scores(g0);
+      for (int j = 0; j < blocks; ++j) {
+        const uint32_t g = g0 + j;
+        if (j + 1 < blocks) issue_scores(g + 1);
+        ok = ok && wait(bar_v(g), (g >> 1) & 1, &s_abort);
+        ok = ok && wait(bar_p(g), (g >> 1) & 1, &s_abort);
+        if (ok) {
+          tc::tc_fence_after();
+          const uint64_t vd = tc::smem_desc_sw128(smem_u32(s_v + (g & 1) * C::kV));
+          const uint32_t pt = tmem + (g & 1) * KB;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[16];
-          tc::tmem_ld16(t_s + (u + h) * 16, x);
+          for (int k = 0; k < KB / 16; ++k)
+            mma_ta_if(lead, tmem + 2 * KB, pt + k / UH * (KB / 2) + k % UH * 8, vd + (k >> 2) * (D * 8) + 2 * (k & 3), id_o,
+                      (j | k) != 0 ? 1u : 0u);
+          if (lead) tc::tc_commit(bar_o(g));
+        }
+        __syncwarp();
+      }
+    } else {
+      // ============================ softmax =================================
+      // this warp's 32 lanes, and its half of the scores' and the output's columns
+      const int half = warp >> 2, r = tid & (kWideRows - 1);
+      const SeqPlan& p = s_item.plan;
+      const TileKeys& keys = s_item.keys;
+      const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+      const uint32_t t_o = t_lane + 2 * KB + half * (D / 2);
+      const bool live = r < keys.n_rows;
+      auto place = [&](int64_t& t, int& h) {   // the row's token and head
+        const int row = keys.row0 + r, tok = row / a.G;
+        t = p.sp.b + tok;
+        h = hk * a.G + row - tok * a.G;
+      };
+      // ---- the tile's queries as binary16, K-major: row r, a half of its channels
+      float unit;
+      {
+        int64_t t;
+        int h;
+        place(t, h);
+        const uint16_t* qp = a.q + t * a.ldq_t + static_cast<int64_t>(h) * a.ldq_h;
+        float amax = 0.0f;
+#pragma unroll 8
+        for (int i = 0; i < D / 8; ++i) {
+          if (live) {
+            const uint4 v = *reinterpret_cast<const uint4*>(qp + i * 8);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+          }
+        }
+        const int fe = query_exponent(amax);
+        const float f = __uint_as_float(static_cast<uint32_t>(fe) << 23);
+        unit = __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) * a.scale_log2;
+#pragma unroll 8
+        for (int i = half * (D / 16); i < (half + 1) * (D / 16); ++i) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (live) v = *reinterpret_cast<const uint4*>(qp + i * 8);
+          const uint4 q = make_uint4(half2_bits(bf16_lo(v.x) * f, bf16_hi(v.x) * f), half2_bits(bf16_lo(v.y) * f, bf16_hi(v.y) * f),
+                                     half2_bits(bf16_lo(v.z) * f, bf16_hi(v.z) * f), half2_bits(bf16_lo(v.w) * f, bf16_hi(v.w) * f));
+          *reinterpret_cast<uint4*>(s_q + (i >> 3) * (kWideRows * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4)) = q;
+        }
+        tc::fence_proxy_async();
+        if (blocks > 0) tc::mbar_arrive(bar_q);
+      }
+      const int32_t row_hi = keys.hi(r), my_lo = keys.lo(row_hi), my_hi = min(row_hi, k_end);
+      const int32_t all_lo = keys.a_lo, all_hi = min(keys.a_hi, k_end);   // the keys that every row sees here
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < blocks; ++j) {
+        const uint32_t g = g0 + j;
+        wait(bar_u(g), (g / kUnitSlots) & 1, &s_abort);
+        wait(bar_s(g), (g >> 1) & 1, &s_abort);
+        tc::tc_fence_after();
+        const uint32_t t_s = t_lane + (g & 1) * KB + half * (KB / 2);
+        const int32_t key0 = k_begin + j * KB, my_key = key0 + half * (KB / 2);
+        // some row does not see all of the block, or the next piece has its end
+        const bool edge = key0 < all_lo || key0 + KB > all_hi;
+        const float* ks = s_ks[g & (kUnitSlots - 1)] + half * UH;
+        const float* vs = s_vr[g & (kUnitSlots - 1)] + half * UH;
+        float top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < UH; u += 2) {
+          uint32_t x[2][16];
+          tc::tmem_ld16(t_s + u * 16, x[0]);
+          tc::tmem_ld16(t_s + u * 16 + 16, x[1]);
           tc::tmem_wait_ld();
-          const float f = ks[u + h] * unit, vf = vs[u + h];
-          float q[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) q[e] = ex2(__fmaf_rn(__uint_as_float(x[e]), f, -base));
           if (edge) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int32_t key = my_key + (u + h) * 16 + e;
-              if (key < my_lo || key >= my_hi) q[e] = 0.0f;
+            for (int e = 0; e < 32; ++e) {
+              const int32_t key = my_key + u * 16 + e;
+              if (key < my_lo || key >= my_hi) x[e >> 4][e & 15] = 0xff800000u;   // -inf
             }
           }
-          float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            l0 += q[e];
-            l1 += q[e + 1];
-            pk[h * 8 + e / 2] = half2_bits(q[e] * vf, q[e + 1] * vf);
+          for (int v = 0; v < 2; ++v) {
+            float t0 = __uint_as_float(x[v][0]), t1 = __uint_as_float(x[v][1]);
+#pragma unroll
+            for (int e = 2; e < 16; e += 2) {
+              t0 = fmaxf(t0, __uint_as_float(x[v][e]));
+              t1 = fmaxf(t1, __uint_as_float(x[v][e + 1]));
+            }
+            t0 = fmaxf(t0, t1);
+            if (t0 > -INFINITY) top = fmaxf(top, t0 * (ks[u + v] * unit));
           }
-          l += l0 + l1;
         }
-        tc::tmem_st16(t_s + u * 8, pk);   // over scores that this thread has read
-      }
-      tc::tmem_wait_st();
-      if (stage) stage_units(j + 2, next_page, next_scales);
-      tc::tc_fence_before();
-      if (__syncthreads_or(!ok)) {        // P, V and the next block's units in place
-        ok = false;
-        break;
-      }
-      if (tid == 0) {
-        tc::tc_fence_after();
-        const uint32_t idesc = tc::idesc_f16_f32(D);
+        s_top[g & 1][half][r] = top;
+        named_barrier(1 + (warp & 3), 64);
+        top = fmaxf(top, s_top[g & 1][half ^ 1][r]);
+        const float old = m;
+        if (top > m + kSlack || m == -INFINITY) m = top;
+        const float al = old == m ? 1.0f : ex2(old - m);   // old = -inf: nothing to keep
+        if (__any_sync(0xffffffffu, al != 1.0f) && j > 0) {
+          wait(bar_o(g - 1), ((g - 1) >> 1) & 1, &s_abort);
+          tc::tc_fence_after();
+#pragma unroll 1
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t o[16];
+            tc::tmem_ld16(t_o + i * 16, o);
+            tc::tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < KB / 16; ++k)
-          tc::tc_mma_ta(tmem + KB, tmem + k / UH * (KB / 2) + k % UH * 8, tc::smem_desc_sw128(smem_u32(s_v) + (k >> 2) * (D * 128)) + 2 * (k & 3), idesc,
-                        (j | k) != 0 ? 1u : 0u);
-        tc::tc_commit(bar_o);
-      }
-      __syncwarp();
-    }
-    if (ok && blocks > 0) {
-      if (!wait(bar_o, ph_o, &s_abort)) ok = false;
-      ph_o ^= 1;
-      tc::tc_fence_after();
-    }
-    if (__syncthreads_or(!ok)) {
-      ok = false;
-      break;
-    }
-
-    // ---- the row's output, or its piece
-    if (half == 1) s_l[r] = l;
-    __syncthreads();
-    if (half == 0) s_l[r] = l + s_l[r];
-    __syncthreads();
-    l = s_l[r];
-    if (bad && tid == 0 && a.err != nullptr) atomicOr(a.err, PRISM_DEV_ERR_PAGE_RANGE);
-    const float nanf = __uint_as_float(0x7fc00000u);
-    const int tok = (keys.row0 + r) / a.G, h = hk * a.G + keys.row0 + r - tok * a.G;
-    const int64_t t = p.sp.b + tok;
-    const bool live = r < keys.n_rows;
-    const bool some = m > -INFINITY || l != l;   // saw a key (or a NaN score)
-    float* ps = static_cast<float*>(a.ws) +
-                ((static_cast<int64_t>(walk.s) * c.H + hk) * part_stride + walk.split * p.rows + keys.row0 + r) * (D + 4);
-    const float scale = !some ? 0.0f : p.splits == 1 ? v_top / l : v_top;
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+            tc::tmem_st16(t_o + i * 16, o);
+          }
+        }
+        l *= al;
+        const float base = m == -INFINITY ? 0.0f : m - kShift;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      uint32_t o[16] = {};
+        for (int u = 0; u < UH; u += 2) {
+          uint32_t x[2][16], pk[16];
+          tc::tmem_ld16(t_s + u * 16, x[0]);
+          tc::tmem_ld16(t_s + u * 16 + 16, x[1]);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const float f = ks[u + v] * unit, vf = vs[u + v];
+            float q[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) q[e] = ex2(__fmaf_rn(__uint_as_float(x[v][e]), f, -base));
+            if (edge) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int32_t key = my_key + (u + v) * 16 + e;
+                if (key < my_lo || key >= my_hi) q[e] = 0.0f;
+              }
+            }
+            float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              l0 += q[e];
+              l1 += q[e + 1];
+              pk[v * 8 + e / 2] = half2_bits(q[e] * vf, q[e + 1] * vf);
+            }
+            l += l0 + l1;
+          }
+          tc::tmem_st16(t_s + u * 8, pk);   // over scores that this thread has read
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        tc::mbar_arrive(bar_p(g));
+      }
       if (blocks > 0) {
-        tc::tmem_ld16(t_o + i * 16, o);
-        tc::tmem_wait_ld();
+        const uint32_t g = g0 + blocks - 1;
+        wait(bar_o(g), (g >> 1) & 1, &s_abort);
+        tc::tc_fence_after();
       }
-      const int d = half * (D / 2) + i * 16;
-      float y[16];
+
+      // ---- the row's output, or its piece
+      if (half == 1) s_l[r] = l;
+      named_barrier(1 + (warp & 3), 64);
+      if (half == 0) s_l[r] = l + s_l[r];
+      named_barrier(1 + (warp & 3), 64);
+      l = s_l[r];
+      if (bad && tid == 0 && a.err != nullptr) atomicOr(a.err, PRISM_DEV_ERR_PAGE_RANGE);
+      const float nanf = __uint_as_float(0x7fc00000u);
+      int64_t t;
+      int h;
+      place(t, h);
+      const bool some = m > -INFINITY || l != l;   // saw a key (or a NaN score)
+      float* ps = static_cast<float*>(a.ws) +
+                  ((static_cast<int64_t>(s_item.walk.s) * c.H + hk) * part_stride + s_item.walk.split * p.rows + keys.row0 + r) * (D + 4);
+      const float scale = !some ? 0.0f : p.splits == 1 ? v_top / l : v_top;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) y[e] = some ? __uint_as_float(o[e]) * scale : 0.0f;
-      if (live && p.splits == 1) {
-        uint32_t w[8];
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t o[16] = {};
+        if (blocks > 0) {
+          tc::tmem_ld16(t_o + i * 16, o);
+          tc::tmem_wait_ld();
+        }
+        const int d = half * (D / 2) + i * 16;
+        float y[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          w[e] = bad ? kBf16NaN * 0x10001u : float_to_bf16_rne(y[2 * e]) | float_to_bf16_rne(y[2 * e + 1]) << 16;
-        uint4* dst = reinterpret_cast<uint4*>(a.out + t * a.ldo_t + h * a.ldo_h + d);
-        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      } else if (live) {
+        for (int e = 0; e < 16; ++e) y[e] = some ? __uint_as_float(o[e]) * scale : 0.0f;
+        if (live && p.splits == 1) {
+          uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 16; e += 4)
-          *reinterpret_cast<float4*>(ps + 4 + d + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+          for (int e = 0; e < 8; ++e)
+            w[e] = bad ? kBf16NaN * 0x10001u : float_to_bf16_rne(y[2 * e]) | float_to_bf16_rne(y[2 * e + 1]) << 16;
+          uint4* dst = reinterpret_cast<uint4*>(a.out + t * a.ldo_t + h * a.ldo_h + d);
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else if (live) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(ps + 4 + d + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      if (live && half == 0) {
+        const float mx = some ? m - kShift + kPShift : -INFINITY;   // the weights' common form
+        if (p.splits > 1) {
+          ps[0] = bad ? nanf : mx;
+          ps[1] = l;
+        } else if (a.lse != nullptr) {
+          a.lse[t * a.Hq + h] = bad ? nanf : !some ? mx : (mx - kPShift + log2f(l)) * kLn2;
+        }
+      }
     }
-    if (live && half == 0) {
-      const float mx = some ? m - kShift + kPShift : -INFINITY;   // the weights' common form
-      if (p.splits > 1) {
-        ps[0] = bad ? nanf : mx;
-        ps[1] = l;
-      } else if (a.lse != nullptr) {
-        a.lse[t * a.Hq + h] = bad ? nanf : !some ? mx : (mx - kPShift + log2f(l)) * kLn2;
-      }
-    }
+    if (blocks == 0) --items;          // the queries' mbarrier did not turn
+    g0 += blocks;
     tc::tc_fence_before();
-    __syncthreads();   // the queries, s_scan and the output's columns are free again
+    __syncthreads();   // the queries, s_item, s_scan, s_max and the output's columns are free again
     tc::tc_fence_after();
   }
 
   // ---- every instruction in flight completes before the columns are given back
-  if (tid == 0) {
+  if (tid == kSoft + kConv) {   // the issuing thread
     tc::tc_commit(bar_end);
     tc::mbar_wait_drain_bounded(bar_end, 0, kWaitNs, &g_kv_status, PRISM_DEVSTATUS_WAIT_TIMEOUT);
   }
@@ -458,7 +563,7 @@ cudaError_t launch_d(const KvAttentionArgs& a, int64_t part_stride, cudaStream_t
   if (e != cudaSuccess) return e;
   const int64_t tiles = a.T * a.G / kWideRows + a.c.S;
   const int64_t items = (tiles + part_stride / kFewRows * a.c.S) * a.c.H;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sm_count() * C::kCtas));
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sm_count()));
   return launch_kernel(kv_attention_tc_kernel<D>, dim3(grid), dim3(kThreads), C::kBytes, stream, false, a, part_stride);
 }
 

@@ -21,18 +21,31 @@ constexpr int kWideRows = 128;         // rows of a tile of the tcgen05 kernel: 
 constexpr int kMinChunk = 1024;        // keys of a piece at least
 constexpr int kMaxSplit = 128;         // pieces of a row at most
 constexpr int kFillFew = 456;          // items that one sequence is cut into where it has the keys: three on each of 152 SMs
-constexpr int kFillWide = 304;         // and two
+constexpr int kSms = 152;              // one wide item on each at a time
 constexpr float kPShift = 12.0f;       // pieces keep their maximum m with 2^(x - m + 12) as the weight of score x
 constexpr float kLn2 = 0.69314718055994531f;
 
-// Pieces of the keys of a sequence with so many rows, H KV heads.
+// Pieces of the keys of a sequence with so many rows, H KV heads: for few rows
+// as many as fill the SMs, for more the fewest that leave at most a fifth of
+// the SMs' turns empty (or the best of eight).
 __host__ __device__ __forceinline__ int split_count(int64_t keys, int64_t rows, int64_t H) {
-  const int64_t cap = rows <= kFewRows ? kFillFew / H : kFillWide / ((rows + kWideRows - 1) / kWideRows * H);
-  const int64_t n = (keys + kMinChunk - 1) / kMinChunk, m = cap > kMaxSplit ? kMaxSplit : cap;
-  return static_cast<int>(n > m ? (m < 1 ? 1 : m) : n < 1 ? 1 : n);
+  const int64_t n = (keys + kMinChunk - 1) / kMinChunk, most = n < 1 ? 1 : n > kMaxSplit ? kMaxSplit : n;
+  if (rows <= kFewRows) {
+    const int64_t cap = kFillFew / H;
+    return static_cast<int>(most > cap ? (cap < 1 ? 1 : cap) : most);
+  }
+  const int64_t one = (rows + kWideRows - 1) / kWideRows * H;      // items with one piece
+  int64_t best = 1, best_n = 0, best_d = 1;                        // share of the turns in use, as a fraction
+  for (int64_t k = one >= kSms ? 1 : (kSms * 4 / 5 + one - 1) / one, i = 0; i < 8; ++k, ++i) {
+    if (k > most) k = most, i = 8;
+    const int64_t items = k * one, d = (items + kSms - 1) / kSms * kSms;
+    if (items * best_d > best_n * d) best = k, best_n = items, best_d = d;
+    if (items * 5 >= d * 4) break;
+  }
+  return static_cast<int>(best);
 }
 // The most rows of one (sequence, KV head) that can be cut into pieces, and
-// its most (row, piece) pairs.
+// its most (row, piece) pairs.  Fewer keys never make more pieces.
 inline int64_t max_split_rows(int64_t max_q, int64_t G, int64_t max_keys, int64_t H, int64_t* rows) {
   int64_t most = 0;
   *rows = 0;
@@ -43,9 +56,9 @@ inline int64_t max_split_rows(int64_t max_q, int64_t G, int64_t max_keys, int64_
     most = std::max(most, splits * r);
   };
   take(std::min<int64_t>(kFewRows, max_q * G));
-  for (int64_t r = kWideRows; max_q * G > kFewRows; r += kWideRows) {
-    take(std::min(r, max_q * G));
-    if (r >= max_q * G || split_count(max_keys, r, H) <= 1) break;
+  for (int64_t tiles = 1; max_q * G > kFewRows; ++tiles) {
+    take(std::min(tiles * kWideRows, max_q * G));
+    if (tiles * kWideRows >= max_q * G || tiles * H >= 4 * kSms) break;   // beyond: one piece uses four fifths
   }
   return most;
 }
@@ -83,14 +96,15 @@ __device__ __forceinline__ int seq_items(const KvAttentionArgs& a, int s, SeqPla
 // Walks a CTA's items: sequences are counted a window of one a thread at a
 // time, by a scan.
 struct Walk {
-  int s0 = 0, next = 0;        // first sequence of the window, and of the one after
-  int64_t base = 0;            // items before it
-  int items = 0;               // items in it
+  int s0, next;                // first sequence of the window, and of the one after
+  int64_t base;                // items before it
+  int items;                   // items in it
   int tile, split, hk, s;      // the item found
 };
+__device__ __forceinline__ Walk new_walk() { return Walk{0, 0, 0, 0, 0, 0, 0, 0}; }
 // Finds `item`; false past the last one.  All kThreads threads; s_scan
 // [kThreads] and s_warp [kThreads / 32] are free again after the caller's next
-// barrier.
+// barrier.  kThreads <= 1023.
 template <bool kWide, int kTileRows, int kThreads>
 __device__ __forceinline__ bool find_item(const KvAttentionArgs& a, int64_t item, Walk& w, int* s_scan, int* s_warp,
                                           SeqPlan& p) {
@@ -121,8 +135,8 @@ __device__ __forceinline__ bool find_item(const KvAttentionArgs& a, int64_t item
   const int local = static_cast<int>(item - w.base);
   int at = 0;
 #pragma unroll
-  for (int o = kThreads / 2; o > 0; o >>= 1)
-    if (s_scan[at + o - 1] <= local) at += o;
+  for (int o = 512; o > 0; o >>= 1)
+    if (at + o <= kThreads && s_scan[at + o - 1] <= local) at += o;
   w.s = w.s0 + at;
   seq_items<kWide, kTileRows>(a, w.s, p);
   int rest = local - (at > 0 ? s_scan[at - 1] : 0);
@@ -140,6 +154,7 @@ struct TileKeys {
   int32_t row0, n_rows, first_pos, len, G, window;
   bool causal, none;
   int32_t a_hi, t_hi, t_lo, a_lo, k_begin, k_end;
+  TileKeys() = default;
   __device__ __forceinline__ TileKeys(const KvAttentionArgs& a, const SeqPlan& p, const Walk& w, int tile_rows) {
     row0 = w.tile * tile_rows;
     n_rows = min(tile_rows, p.rows - row0);
