@@ -7,11 +7,11 @@
 //   O += P V       KB / 16 steps, M 128, N D; P as the A operand from tensor
 //                  memory, each half over its own half of S
 // One CTA an SM, with three kinds of warps that pass blocks on by mbarriers:
-//   converters (4 warps)  read a block's codes ahead into registers, 8 keys by
-//     16 channels of K and of V a thread, and widen them once for the 128 rows,
-//     exactly (byte ^ 0x80 under the exponent of 1024, minus 1152), into two
-//     stages of the 128-byte-swizzled K-major operand layout: K as its rows, V
-//     transposed (8 keys of a channel are one 16-byte piece);
+//   converters (4 warps for K, 4 for V)  read a block's codes ahead into
+//     registers, 8 keys by 16 channels a thread, and widen them once for the 128
+//     rows, exactly (byte ^ 0x80 under the exponent of 1024, minus 1152), into
+//     two stages of the 128-byte-swizzled K-major operand layout: K as its rows,
+//     V transposed (8 keys of a channel are one 16-byte piece);
 //   the issuer (1 warp)   Q K^T of block j + 1, S being double-buffered, ahead
 //     of P V of block j;
 //   softmax (8 warps)     two threads a row, one for each half of the block's
@@ -42,9 +42,9 @@ using namespace kv;
 
 constexpr unsigned long long kWaitNs = 2000000000ull;
 constexpr float kShift = 9.0f, kSlack = 6.0f;
-constexpr int kSoftWarps = 8, kConvWarps = 4;
+constexpr int kSoftWarps = 8, kConvWarps = 8;
 constexpr int kThreads = (kSoftWarps + kConvWarps + 1) * 32;
-constexpr int kSoft = kSoftWarps * 32, kConv = kConvWarps * 32;
+constexpr int kSoft = kSoftWarps * 32, kConv = kConvWarps * 32, kSide = kConv / 2;   // half for K, half for V
 constexpr int kUnitSlots = 4;     // blocks whose units' scales are held
 
 template <int D>
@@ -55,7 +55,7 @@ struct Tc {
   static constexpr int kQ = kWideRows * D * 2, kK = kKeys * D * 2, kV = kKeys * D * 2;
   static constexpr int kBytes = kQ + 2 * (kK + kV) + 1024;     // operands start on 1024-byte boundaries
   static constexpr int kItems = kKeys / 8 * (D / 16);          // 8 keys x 16 channels, one a thread
-  static_assert(kItems <= kConv, "an item a thread");
+  static_assert(kItems <= kSide, "an item a thread");
   static_assert(2 * kKeys + D <= kCols, "tensor memory");
 };
 
@@ -123,14 +123,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar_q = bars + 96 + 8 * kUnitSlots, bar_end = bar_q + 8;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(bar_k(i), kConv);
-      tc::mbar_init(bar_v(i), kConv);
+      tc::mbar_init(bar_k(i), kSide);
+      tc::mbar_init(bar_v(i), kSide);
       tc::mbar_init(bar_s(i), 1);
       tc::mbar_init(bar_kfree(i), 1);
       tc::mbar_init(bar_p(i), kSoft);
       tc::mbar_init(bar_o(i), 1);
     }
-    for (int i = 0; i < kUnitSlots; ++i) tc::mbar_init(bar_u(i), kConv);
+    for (int i = 0; i < kUnitSlots; ++i) tc::mbar_init(bar_u(i), kSide);
     tc::mbar_init(bar_q, kSoft);
     tc::mbar_init(bar_end, 1);
     s_abort = 0;
@@ -194,107 +194,104 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= kSoftWarps && warp < kSoftWarps + kConvWarps) {
       // ============================ converters ==============================
-      const int ct = tid - kSoft;
+      const bool is_v = warp >= kSoftWarps + kConvWarps / 2;
+      const int ct = (tid - kSoft) & (kSide - 1);
       const bool mine = ct < C::kItems;
-      // a thread's item, keys 8 kg .. + 7 and channels 16 ch .. + 15, of K: the
-      // pieces of a row side by side; of V: eight key groups of a channel, whose
+      // the thread's item, keys 8 kg .. + 7 and channels 16 ch .. + 15.  K: the
+      // pieces of a row side by side; V: eight key groups of a channel, whose
       // pieces fill all banks
-      const int k_kg = ct / (D / 16), k_ch = ct % (D / 16);
-      const int v_kg = ct / (8 * (D / 16)) * 8 + (ct & 7), v_ch = ct / 8 % (D / 16);
-      // a page id is read two blocks ahead and looked at when it is used
+      const int kg = is_v ? ct / (8 * (D / 16)) * 8 + (ct & 7) : ct / (D / 16);
+      const int ch = is_v ? ct / 8 % (D / 16) : ct % (D / 16);
+      const bool has_unit = !is_v && ct < U;            // passes on the scales of unit ct
+      // a page id is read ahead and looked at when it is used
       auto page_at = [&](int32_t key, bool live) { return live && key < k_end ? table[key >> c.block_shift] : 0; };
-      auto k_page = [&](int j) { return page_at(k_begin + j * KB + k_kg * 8, mine); };
-      auto v_page = [&](int j) { return page_at(k_begin + j * KB + v_kg * 8, mine); };
-      auto u_page = [&](int j) { return page_at(k_begin + j * KB + ct * 16, ct < U); };
+      auto code_page = [&](int j) { return page_at(k_begin + j * KB + kg * 8, mine); };
+      auto unit_page = [&](int j) { return page_at(k_begin + j * KB + ct * 16, has_unit); };
       auto row = [&](int32_t page) {          // an invalid page (the rows get NaN) or none: page 0, in its stead
         return static_cast<int64_t>(page < 0 || page >= c.num_pages ? 0 : page) * c.H + hk;
       };
-      auto u_scales = [&](int j, int32_t page) {        // of the block's unit ct; vs not yet divided
+      auto unit_scales = [&](int j, int32_t page) {     // vs not yet divided
         const int64_t at = row(page);
-        return ct < U && k_begin + j * KB + ct * 16 < k_end ? make_float2(c.k_scale[at], c.v_scale[at])
-                                                            : make_float2(0.0f, 0.0f);
+        return has_unit && k_begin + j * KB + ct * 16 < k_end ? make_float2(c.k_scale[at], c.v_scale[at])
+                                                              : make_float2(0.0f, 0.0f);
       };
-      uint4 rk[8], rv[8];
-      auto load = [&](uint4(&raw)[8], const int8_t* codes, int32_t key, int ch, int32_t page) {
-        const int8_t* src = codes + (row(page) * c.block + (key & (c.block - 1))) * D + ch * 16;
+      uint4 raw[8];
+      auto load = [&](int j, int32_t page) {
+        const int32_t key = k_begin + j * KB + kg * 8;
+        const int8_t* src = (is_v ? c.v_codes : c.k_codes) + (row(page) * c.block + (key & (c.block - 1))) * D + ch * 16;
 #pragma unroll
         for (int k = 0; k < 8; ++k) raw[k] = ld_stream_16(src + k * D);
       };
-      auto load_k = [&](int j, int32_t page) { load(rk, c.k_codes, k_begin + j * KB + k_kg * 8, k_ch, page); };
-      auto load_v = [&](int j, int32_t page) { load(rv, c.v_codes, k_begin + j * KB + v_kg * 8, v_ch, page); };
-      // ahead: codes by one block, their pages by two; scales by two, their pages by three
-      int32_t next_k = 0, next_v = 0, next_u = 0;
+      // ahead: codes by one block, their page by two; scales by two, their page by three
+      int32_t next_page = 0, next_unit = 0;
       float2 scales = make_float2(0.0f, 0.0f), next_scales = scales;
       if (blocks > 0) {
-        const int32_t pk = k_page(0), pv = v_page(0), pu = u_page(0), pu1 = u_page(1);
-        next_k = k_page(1);
-        next_v = v_page(1);
-        next_u = u_page(2);
-        if (mine) {
-          load_k(0, pk);
-          load_v(0, pv);
-        }
-        scales = u_scales(0, pu);
-        next_scales = u_scales(1, pu1);
+        const int32_t page = code_page(0), u0 = unit_page(0), u1 = unit_page(1);
+        next_page = code_page(1);
+        next_unit = unit_page(2);
+        if (mine) load(0, page);
+        scales = unit_scales(0, u0);
+        next_scales = unit_scales(1, u1);
       }
       for (int j = 0; j < blocks; ++j) {
         const uint32_t g = g0 + j, ph = (g >> 1) & 1;
-        if (ct < U) {
-          s_ks[g & (kUnitSlots - 1)][ct] = scales.x;
-          s_vr[g & (kUnitSlots - 1)][ct] = scales.y * v_inv;
-        }
-        tc::mbar_arrive(bar_u(g));
-        scales = next_scales;
-        next_scales = u_scales(j + 2, next_u);
-        next_u = u_page(j + 3);
-        // ---- K: 16 codes of a key are two pieces of the operand
-        wait(bar_kfree(g), ph ^ 1u, &s_abort);
-        if (mine) {
-          uint8_t* dst = s_k + (g & 1) * C::kK + (k_ch >> 2) * (KB * 128) + k_kg * 1024;
-          const int piece = (k_ch & 3) * 2;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t x = rk[k].x ^ 0x80808080u, y = rk[k].y ^ 0x80808080u;
-            const uint32_t z = rk[k].z ^ 0x80808080u, w = rk[k].w ^ 0x80808080u;
-            *reinterpret_cast<uint4*>(dst + k * 128 + ((piece ^ k) << 4)) =
-                make_uint4(widen(x, 0x4140u), widen(x, 0x4342u), widen(y, 0x4140u), widen(y, 0x4342u));
-            *reinterpret_cast<uint4*>(dst + k * 128 + (((piece + 1) ^ k) << 4)) =
-                make_uint4(widen(z, 0x4140u), widen(z, 0x4342u), widen(w, 0x4140u), widen(w, 0x4342u));
+        if (!is_v) {
+          // Q K^T of block g - 2 is complete: so the output of block g - 4 is
+          // (its P lay where that S went), and the units' slot is free
+          wait(bar_kfree(g), ph ^ 1u, &s_abort);
+          if (has_unit) {
+            s_ks[g & (kUnitSlots - 1)][ct] = scales.x;
+            s_vr[g & (kUnitSlots - 1)][ct] = scales.y * v_inv;
           }
-          if (j + 1 < blocks) load_k(j + 1, next_k);
-        }
-        tc::fence_proxy_async();
-        tc::mbar_arrive(bar_k(g));
-        next_k = k_page(j + 2);
-        // ---- V, transposed: 8 keys of a channel are one piece of the operand
-        wait(bar_o(g), ph ^ 1u, &s_abort);
-        if (mine) {
-          uint8_t* dst = s_v + (g & 1) * C::kV + (v_kg >> 3) * (D * 128) + v_ch * 16 * 128;
+          tc::mbar_arrive(bar_u(g));
+          scales = next_scales;
+          next_scales = unit_scales(j + 2, next_unit);
+          next_unit = unit_page(j + 3);
+          // ---- K: 16 codes of a key are two pieces of the operand
+          if (mine) {
+            uint8_t* dst = s_k + (g & 1) * C::kK + (ch >> 2) * (KB * 128) + kg * 1024;
+            const int piece = (ch & 3) * 2;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t h[4][4];   // [channel][key pair]
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint4 r0 = rv[2 * k], r1 = rv[2 * k + 1];
-              const uint32_t w0 = w == 0 ? r0.x : w == 1 ? r0.y : w == 2 ? r0.z : r0.w;
-              const uint32_t w1 = w == 0 ? r1.x : w == 1 ? r1.y : w == 2 ? r1.z : r1.w;
-              const uint32_t x = __byte_perm(w0, w1, 0x5140u) ^ 0x80808080u;
-              const uint32_t y = __byte_perm(w0, w1, 0x7362u) ^ 0x80808080u;
-              h[0][k] = widen(x, 0x4140u);
-              h[1][k] = widen(x, 0x4342u);
-              h[2][k] = widen(y, 0x4140u);
-              h[3][k] = widen(y, 0x4342u);
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t x = raw[k].x ^ 0x80808080u, y = raw[k].y ^ 0x80808080u;
+              const uint32_t z = raw[k].z ^ 0x80808080u, w = raw[k].w ^ 0x80808080u;
+              *reinterpret_cast<uint4*>(dst + k * 128 + ((piece ^ k) << 4)) =
+                  make_uint4(widen(x, 0x4140u), widen(x, 0x4342u), widen(y, 0x4140u), widen(y, 0x4342u));
+              *reinterpret_cast<uint4*>(dst + k * 128 + (((piece + 1) ^ k) << 4)) =
+                  make_uint4(widen(z, 0x4140u), widen(z, 0x4342u), widen(w, 0x4140u), widen(w, 0x4342u));
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(dst + (w * 4 + e) * 128 + (((v_kg & 7) ^ ((w * 4 + e) & 7)) << 4)) =
-                  make_uint4(h[e][0], h[e][1], h[e][2], h[e][3]);
           }
-          if (j + 1 < blocks) load_v(j + 1, next_v);
+        } else {
+          // ---- V, transposed: 8 keys of a channel are one piece of the operand
+          wait(bar_o(g), ph ^ 1u, &s_abort);
+          if (mine) {
+            uint8_t* dst = s_v + (g & 1) * C::kV + (kg >> 3) * (D * 128) + ch * 16 * 128;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              uint32_t h[4][4];   // [channel][key pair]
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint4 r0 = raw[2 * k], r1 = raw[2 * k + 1];
+                const uint32_t w0 = w == 0 ? r0.x : w == 1 ? r0.y : w == 2 ? r0.z : r0.w;
+                const uint32_t w1 = w == 0 ? r1.x : w == 1 ? r1.y : w == 2 ? r1.z : r1.w;
+                const uint32_t x = __byte_perm(w0, w1, 0x5140u) ^ 0x80808080u;
+                const uint32_t y = __byte_perm(w0, w1, 0x7362u) ^ 0x80808080u;
+                h[0][k] = widen(x, 0x4140u);
+                h[1][k] = widen(x, 0x4342u);
+                h[2][k] = widen(y, 0x4140u);
+                h[3][k] = widen(y, 0x4342u);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<uint4*>(dst + (w * 4 + e) * 128 + (((kg & 7) ^ ((w * 4 + e) & 7)) << 4)) =
+                    make_uint4(h[e][0], h[e][1], h[e][2], h[e][3]);
+            }
+          }
         }
+        if (mine && j + 1 < blocks) load(j + 1, next_page);
         tc::fence_proxy_async();
-        tc::mbar_arrive(bar_v(g));
-        next_v = v_page(j + 2);
+        tc::mbar_arrive(is_v ? bar_v(g) : bar_k(g));
+        next_page = code_page(j + 2);
       }
     } else if (warp == kSoftWarps + kConvWarps) {
       // ============================ issuer ==================================
