@@ -12,13 +12,21 @@
 // an integer below 2^18, so its binary32 accumulator is exact; only the sum
 // over the groups rounds, in group order.
 //
-// A CTA owns 64 or 128 channels (4 or 8 warps x 16) and one slice of K; the CTAs of a
+// A CTA owns 64 channels (up to 8 rows) or 128 and one slice of K; the CTAs of a
 // cluster hold the slices of one channel tile and add their sums through
-// distributed shared memory in slice order.  The activations and scales of up
-// to pass_units * 32 input channels at a time are laid into shared memory, the
-// activations widened once per CTA in the order that the weight words want;
-// each warp streams its weight rows through a private ring of cp.async copies
-// (128 bytes of a row a step).
+// distributed shared memory in slice order.  Each warp streams its weight rows
+// through a private ring of cp.async copies (128 bytes of a row a step); the
+// activations are widened once per CTA into shared memory, in the order that the
+// weight words want.
+//
+// Up to 8 rows the issue slots bound it: a weight word costs nine instructions
+// for eight codes, and half of the slots are taken (deeper rings change nothing:
+// 5120 x 34816, one row, 3, 4, 5 stages: 25.4, 26.7, 27.6 us, 3.5 TB/s of weights).
+// With more rows the instructions themselves (608 TFLOP/s at best) take 40 % of
+// the time and the slots 45 %: 37 rows of 5120 x 34816 take 69 us.  The same on
+// tcgen05 (weights widened into swizzled shared memory, group sums read back from
+// tensor memory) took 75 us, and 50 us against 36 with 12 rows: every weight then
+// passes through shared memory twice.
 #include <type_traits>
 
 #include "decode.cuh"
@@ -26,52 +34,47 @@
 namespace prism {
 namespace {
 
-// Warps of a CTA: with more token rows each CTA has more activations to lay
-// out, so more channels share them (37 rows of 5120 x 34816: four warps 202 us,
-// eight 94 us; 8 rows of 17408 x 5120: 30 and 41 us).
-template <int T>
-constexpr int kWarps = T <= 8 ? 4 : 8;
+constexpr int kWarps = 4, kThreads = kWarps * 32, kCh = kWarps * 16;   // of a CTA with up to 8 rows; its channels
 constexpr int kStageUnits = 8;            // a unit is 32 input channels: 16 bytes of a weight row
 constexpr int kPitch = kStageUnits * 16 + 16;   // bytes between the rows of a stage: words r * 36 + c hit all banks once
 constexpr int kStageBytes = 16 * kPitch;
 constexpr int kStages = 3;
 constexpr int kSlabRows = 64;             // token rows of one pass over the weights
-constexpr int kMaxPass = 40;              // units of a pass at most: four CTAs of up to 8 rows fit an SM, or two of up to 40
-constexpr int kMaxSmem = 128 * 1024;      // of a CTA; layout() stays below
+constexpr int kMaxBytes = 56 * 1024;      // of a CTA of up to 8 rows: four fit an SM
 
-// Shared memory of a CTA.  T: token rows held (1, 2, 4 or a multiple of 8: one
-// token's activations take 64 bytes a unit).
+constexpr int kActBytes = 12288;          // activations of a pass: 64 bytes a token and unit
+
+// Shared memory of a CTA of up to 8 rows.  T: token rows held (1, 2, 4 or 8).
 struct Layout {
   int pass_units, b, sum, scale, pitch, offset, bytes;
 };
 template <int T, int GU>
 Layout layout(int units, bool has_offset) {
-  constexpr int NT = (T + 7) / 8;
-  constexpr int kBudget = NT == 1 ? 12288 : NT <= 5 ? NT * 8192 : NT * 4096;   // bytes of activations
   Layout l;
-  l.pass_units = std::max(kStageUnits, std::min({kBudget / (T * 64), kMaxPass, units + kStageUnits - 1}) & ~(kStageUnits - 1));
-  const int groups = l.pass_units / GU;
-  constexpr int kCh = kWarps<T> * 16;
-  l.b = kWarps<T> * kStages * kStageBytes;
-  l.sum = l.b + l.pass_units * T * 64;
-  l.scale = l.sum + (has_offset ? groups * NT * 32 : 0);
-  // a row's scales start at an element whose index is a multiple of 8
-  l.pitch = (groups + 7 + 7) / 8 * 8 + 8;
-  l.offset = l.scale + kCh * l.pitch * 2;
-  l.bytes = std::max(l.offset + (has_offset ? kCh * l.pitch * 2 : 0), NT * 8 * kCh * 4);   // and the CTA's sums at the end
-  return l;
+  l.pass_units = std::min(kActBytes / (T * 64), units);   // both multiples of a stage
+  for (;; l.pass_units -= kStageUnits) {
+    const int groups = l.pass_units / GU;
+    l.b = kWarps * kStages * kStageBytes;
+    l.sum = l.b + l.pass_units * T * 64;
+    l.scale = l.sum + (has_offset ? groups * 32 : 0);
+    // a row's scales start at an element whose index is a multiple of 8
+    l.pitch = (groups + 7 + 7) / 8 * 8 + 8;
+    l.offset = l.scale + kCh * l.pitch * 2;
+    l.bytes = std::max(l.offset + (has_offset ? kCh * l.pitch * 2 : 0), 8 * kCh * 4);   // and the CTA's sums at the end
+    if (l.bytes <= kMaxBytes || l.pass_units <= kStageUnits) return l;
+  }
 }
 
 // d = a b where first, else d += a b.
 template <bool kFirst>
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if (kFirst) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
   } else {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -102,6 +105,27 @@ __device__ __forceinline__ float half_bits_to_float(uint16_t h) {
   asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(h));
   return f;
 }
+// The binary16 scales of N consecutive groups, read at once.
+template <int N>
+struct Scales {
+  uint32_t w[(N + 1) / 2];
+  __device__ __forceinline__ explicit Scales(const uint16_t* p) {
+    if constexpr (N == 8) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (N == 4) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    } else if constexpr (N == 2) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      w[0] = *p;
+    }
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    return half_bits_to_float(static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16)));
+  }
+};
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
 }
@@ -113,11 +137,30 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// T: token rows held, NT tiles of 8.  GU: units of a group.  kOff: with offsets.
+// The slices' sums (s_y: [token][channel] in each CTA of the cluster), added in
+// slice order; every CTA takes its share of the tile's outputs.
+template <int kCh>
+__device__ __forceinline__ void join_slices(const W4gArgs& a, uint32_t s_y, int rank, int slices, int64_t m0, int held,
+                                            int64_t n_cta, int tid, int threads) {
+  cluster_sync();
+  const int rows = static_cast<int>(min(static_cast<int64_t>(held), a.M - m0));
+  for (int i = rank * threads + tid; i < rows * kCh; i += slices * threads) {
+    const int64_t m = m0 + i / kCh, n = n_cta + i % kCh;
+    float v = 0.0f;
+    for (int r = 0; r < slices; ++r) v = __fadd_rn(v, ld_cluster(s_y + i * 4, r));
+    if (n < a.N) {
+      v = __fmul_rn(v, __ldg(a.a_scale + m));
+      if (a.residual != nullptr) v = __fadd_rn(v, bf16_bits_to_float(a.residual[m * a.ldr + n]));
+      a.out[m * a.ldo + n] = static_cast<uint16_t>(float_to_bf16_rne(v));
+    }
+  }
+  cluster_sync();   // no CTA leaves while its sums are read
+}
+
+// ---- up to 8 rows.  T: token rows held.  GU: units of a group.  kOff: with offsets.
 template <int T, int GU, bool kOff>
-__global__ void __launch_bounds__(kWarps<T> * 32, T <= 8 ? 4 : T <= 40 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, 4)
     w4g_kernel(const __grid_constant__ W4gArgs a, const __grid_constant__ Layout l, int slices, int slice_units) {
-  constexpr int NT = (T + 7) / 8, kThreads = kWarps<T> * 32, kCh = kWarps<T> * 16;
   extern __shared__ __align__(128) uint8_t smem[];
   uint4* s_b = reinterpret_cast<uint4*>(smem + l.b);          // [unit][T][4]: the B fragments of a unit
   float* s_sum = reinterpret_cast<float*>(smem + l.sum);      // [group][NT * 8]: sum of q
@@ -154,14 +197,12 @@ __global__ void __launch_bounds__(kWarps<T> * 32, T <= 8 ? 4 : T <= 40 ? 2 : 1)
 #pragma unroll
   for (int st = 0; st < kStages - 1; ++st) issue(st);
 
-  float y[NT][4];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) y[t][0] = y[t][1] = y[t][2] = y[t][3] = 0.0f;
+  float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 
   // ---- activations as B fragments: 16 codes of a token are a piece, in the
   // order (group, token, unit, half); a thread's pieces of the next pass are
   // read ahead
-  constexpr int kPieces = ((NT == 1 ? 12288 : NT <= 5 ? NT * 8192 : NT * 4096) / 32 + kThreads - 1) / kThreads;
+  constexpr int kPieces = kActBytes / 32 / kThreads;
   uint4 w[kPieces];
   auto load_q = [&](int p0) {
     const int total = min(l.pass_units, units - p0) * T * 2;
@@ -219,64 +260,26 @@ __global__ void __launch_bounds__(kWarps<T> * 32, T <= 8 ? 4 : T <= 40 ? 2 : 1)
         sum = __dp4a(static_cast<int>(w[j].z), 0x01010101, __dp4a(static_cast<int>(w[j].w), 0x01010101, sum));
 #pragma unroll
         for (int o = 1; o < 2 * GU; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (live && half == 0 && u == 0) s_sum[g * (NT * 8) + tok] = static_cast<float>(sum);
+        if (live && half == 0 && u == 0) s_sum[g * 8 + tok] = static_cast<float>(sum);
       }
     }
     cp_async_wait<0>();
     __syncthreads();
     if (p0 + l.pass_units < units) load_q(p0 + l.pass_units);
 
-    // ---- a unit: 2 weight words of a lane (rows r, r + 8), 2 NT instructions
+    // ---- a unit: 2 weight words of a lane (rows r, r + 8), 2 instructions
     const int bl = T < 8 ? min(lr, T - 1) : lr;   // a column past the tokens repeats the last one and is not stored
     const uint16_t* sp = s_scale + (warp * 16 + lr) * l.pitch + shift;
     const uint16_t* op = s_off + (warp * 16 + lr) * l.pitch + shift;
-    float acc[NT][4];
-    auto unit = [&](const uint8_t* wb, int ul, int g, auto first, auto last) {   // unit ul of group g in this pass
+    float acc[4];
+    auto unit = [&](const uint8_t* wb, int ul, auto first) {   // unit ul of this pass
       const uint32_t w0 = *reinterpret_cast<const uint32_t*>(wb);
       const uint32_t w1 = *reinterpret_cast<const uint32_t*>(wb + 8 * kPitch);
       const uint32_t ae[4] = {even_codes(w0), even_codes(w1), even_codes(w0 >> 8), even_codes(w1 >> 8)};
       const uint32_t ao[4] = {odd_codes(w0), odd_codes(w1), odd_codes(w0 >> 8), odd_codes(w1 >> 8)};
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint4 b = s_b[(ul * T + t * 8 + bl) * 4 + lc];
-        mma_f16_16816<decltype(first)::value>(acc[t], ae, b.x, b.y);
-        mma_f16_16816<false>(acc[t], ao, b.z, b.w);
-      }
-      if constexpr (decltype(last)::value) {
-        const float s0 = half_bits_to_float(sp[g]), s1 = half_bits_to_float(sp[8 * l.pitch + g]);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          y[t][0] = __fmaf_rn(acc[t][0], s0, y[t][0]);
-          y[t][1] = __fmaf_rn(acc[t][1], s0, y[t][1]);
-          y[t][2] = __fmaf_rn(acc[t][2], s1, y[t][2]);
-          y[t][3] = __fmaf_rn(acc[t][3], s1, y[t][3]);
-        }
-        if constexpr (kOff) {
-          const float o0 = half_bits_to_float(op[g]), o1 = half_bits_to_float(op[8 * l.pitch + g]);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const float2 q = *reinterpret_cast<const float2*>(s_sum + g * (NT * 8) + t * 8 + 2 * lc);
-            y[t][0] = __fmaf_rn(q.x, o0, y[t][0]);
-            y[t][1] = __fmaf_rn(q.y, o0, y[t][1]);
-            y[t][2] = __fmaf_rn(q.x, o1, y[t][2]);
-            y[t][3] = __fmaf_rn(q.y, o1, y[t][3]);
-          }
-        }
-      }
-    };
-    auto group = [&](const uint8_t* wb, int ul, int g) {
-#pragma unroll
-      for (int u = 0; u < GU; ++u) {
-        if constexpr (GU == 1) {
-          unit(wb, ul, g, std::true_type{}, std::true_type{});
-        } else if (u == 0) {
-          unit(wb, ul, g, std::true_type{}, std::false_type{});
-        } else if (u == GU - 1) {
-          unit(wb + u * 16, ul + u, g, std::false_type{}, std::true_type{});
-        } else {
-          unit(wb + u * 16, ul + u, g, std::false_type{}, std::false_type{});
-        }
-      }
+      const uint4 b = s_b[(ul * T + bl) * 4 + lc];
+      mma_f16_16816<decltype(first)::value>(acc, ae, b.x, b.y);
+      mma_f16_16816<false>(acc, ao, b.z, b.w);
     };
     const int st0 = p0 / kStageUnits, st_end = (p0 + pu + kStageUnits - 1) / kStageUnits;
     for (int st = st0; st < st_end; ++st) {
@@ -284,12 +287,32 @@ __global__ void __launch_bounds__(kWarps<T> * 32, T <= 8 ? 4 : T <= 40 ? 2 : 1)
       cp_async_wait<kStages - 1>();
       __syncwarp();
       const uint8_t* wb = smem + (warp * kStages + st % kStages) * kStageBytes + lr * kPitch + lc * 4;
-      const int ul = (st - st0) * kStageUnits, gl = (st - st0) * (kStageUnits / GU), n = pu - ul;
+      constexpr int GV = kStageUnits / GU;   // groups of a stage
+      const int ul = (st - st0) * kStageUnits, gl = (st - st0) * GV, n = pu - ul;
+      const Scales<GV> s0(sp + gl), s1(sp + 8 * l.pitch + gl), o0(kOff ? op + gl : sp), o1(kOff ? op + 8 * l.pitch + gl : sp);
+      auto group = [&](int g) {
+        unit(wb + g * GU * 16, ul + g * GU, std::true_type{});
+#pragma unroll
+        for (int u = 1; u < GU; ++u) unit(wb + (g * GU + u) * 16, ul + g * GU + u, std::false_type{});
+        y[0] = __fmaf_rn(acc[0], s0[g], y[0]);
+        y[1] = __fmaf_rn(acc[1], s0[g], y[1]);
+        y[2] = __fmaf_rn(acc[2], s1[g], y[2]);
+        y[3] = __fmaf_rn(acc[3], s1[g], y[3]);
+        if constexpr (kOff) {
+          const float2 q = *reinterpret_cast<const float2*>(s_sum + (gl + g) * 8 + 2 * lc);
+          y[0] = __fmaf_rn(q.x, o0[g], y[0]);
+          y[1] = __fmaf_rn(q.y, o0[g], y[1]);
+          y[2] = __fmaf_rn(q.x, o1[g], y[2]);
+          y[3] = __fmaf_rn(q.y, o1[g], y[3]);
+        }
+      };
       if (n >= kStageUnits) {
 #pragma unroll
-        for (int u = 0; u < kStageUnits; u += GU) group(wb + u * 16, ul + u, gl + u / GU);
+        for (int g = 0; g < GV; ++g) group(g);
       } else {
-        for (int u = 0; u < n; u += GU) group(wb + u * 16, ul + u, gl + u / GU);
+#pragma unroll
+        for (int g = 0; g < GV; ++g)
+          if (g * GU < n) group(g);
       }
       __syncwarp();   // the stage is free for the copy that the next turn issues
     }
@@ -300,42 +323,259 @@ __global__ void __launch_bounds__(kWarps<T> * 32, T <= 8 ? 4 : T <= 40 ? 2 : 1)
   __syncthreads();
   float* s_y = reinterpret_cast<float*>(smem);   // [token][channel]
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s_y[(t * 8 + 2 * lc + (e & 1)) * kCh + warp * 16 + lr + 8 * (e >> 1)] = y[t][e];
-  cluster_sync();
-  const int rows = static_cast<int>(min(static_cast<int64_t>(NT * 8), a.M - m0));
-  for (int i = rank * kThreads + tid; i < rows * kCh; i += slices * kThreads) {
-    const int64_t m = m0 + i / kCh, n = n_cta + i % kCh;
-    const uint32_t at = smem_u32(s_y + i);
-    float v = 0.0f;
-    for (int r = 0; r < slices; ++r) v = __fadd_rn(v, ld_cluster(at, r));
-    if (n < a.N) {
-      v = __fmul_rn(v, __ldg(a.a_scale + m));
-      if (a.residual != nullptr) v = __fadd_rn(v, bf16_bits_to_float(a.residual[m * a.ldr + n]));
-      a.out[m * a.ldo + n] = static_cast<uint16_t>(float_to_bf16_rne(v));
-    }
-  }
-  cluster_sync();   // no CTA leaves while its sums are read
+  for (int e = 0; e < 4; ++e) s_y[(2 * lc + (e & 1)) * kCh + warp * 16 + lr + 8 * (e >> 1)] = y[e];
+  join_slices<kCh>(a, smem_u32(smem), rank, slices, m0, 8, n_cta, tid, kThreads);
+}
+
+// ---- 9 and more rows.  A CTA owns 128 channels: four warps of 32 channels, so
+// that a B fragment read from shared memory serves two instructions' rows, and
+// two warps that lay chunks of CU units of activations (and their scales) into
+// one of two buffers while the other is used.  Named barriers pass the buffers
+// on: kFull + b when buffer b is laid out, kEmpty + b when it has been read.
+constexpr int kWideWarps = 4, kSideWarps = 2;
+constexpr int kWideThreads = (kWideWarps + kSideWarps) * 32, kSide = kSideWarps * 32;
+constexpr int kWideStages = 3;
+constexpr int kWideCh = kWideWarps * 32;
+constexpr int kWideStage = 32 * kPitch;
+enum : int { kFull = 1, kEmpty = 3 };
+
+__device__ __forceinline__ void named_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kWideThreads) : "memory"); }
+__device__ __forceinline__ void named_arrive(int id) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kWideThreads) : "memory");
 }
 
 template <int T, int GU, bool kOff>
-cudaError_t launch_t(const W4gArgs& a, cudaStream_t stream) {
-  // Slices of K: as many as let four CTAs of 64 channels on every SM run at
-  // once, at most a cluster of eight; whole groups of any size (4 units) each.
-  // A rule on N, K and the group alone: a row's sums do not depend on M.
-  constexpr int kCh = kWarps<T> * 16;
-  const int64_t tiles = (a.N + kCh - 1) / kCh, tiles64 = (a.N + 63) / 64;
-  const int units = static_cast<int>(a.K >> 5);
-  const int slices = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({4 * sm_count() / tiles64, 8, (units + 3) / 4})));
-  const int slice_units = ((units + slices - 1) / slices + 3) & ~3;
-  const Layout l = layout<T, GU>(slice_units, kOff);
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(w4g_kernel<T, GU, kOff>), kMaxSmem);
+struct Wide {
+  static constexpr int NT = T / 8;
+  static constexpr int CU = T <= 40 ? 8 : 4;                       // units of a chunk: two CTAs fit an SM
+  static constexpr int GC = CU / GU;                               // its groups
+  static constexpr int kB = CU * T * 64, kScale = kWideCh * GC * 2, kSum = GC * T * 4;
+  static constexpr int kBuffer = kB + (kOff ? 2 * kScale + kSum : kScale);
+  static constexpr int kRing = kWideWarps * kWideStages * kWideStage;
+  static constexpr int kBytes = kRing + 2 * kBuffer;
+  static_assert(kBytes >= T * kWideCh * 4, "the CTA's sums at the end");
+  static_assert(2 * (kBytes + 1024) <= 227 * 1024, "two CTAs an SM");
+};
+
+template <int T, int GU, bool kOff>
+__global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_constant__ W4gArgs a, int slices, int slice_units) {
+  using C = Wide<T, GU, kOff>;
+  constexpr int NT = C::NT, CU = C::CU, GC = C::GC;
+  extern __shared__ __align__(128) uint8_t smem[];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lr = lane >> 2, lc = lane & 3;
+  const int rank = blockIdx.x % slices;
+  const int64_t n_cta = static_cast<int64_t>(blockIdx.x / slices) * kWideCh;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kSlabRows;
+  const int all_units = static_cast<int>(a.K >> 5);
+  const int u_begin = min(rank * slice_units, all_units);
+  const int units = min(slice_units, all_units - u_begin), chunks = (units + CU - 1) / CU;
+  auto buffer = [&](int c) { return smem + C::kRing + (c & 1) * C::kBuffer; };   // B fragments, scales, offsets, sums of q
+  float y[2][NT][4];
+#pragma unroll
+  for (int i = 0; i < 2 * NT * 4; ++i) y[i / (NT * 4)][i / 4 % NT][i & 3] = 0.0f;
+
+  if (warp >= kWideWarps) {
+    // ============ activations as B fragments, and the scales ============
+    // 16 codes of a token are a piece, in the order (group, token, unit, half)
+    const int st = tid - kWideWarps * 32, half = st & 1, u = (st >> 1) % GU, pair = st / (2 * GU);
+    constexpr int kPieces = CU * T * 2 / kSide, kPairs = kSide / (2 * GU);
+    static_assert(CU * T * 2 % kSide == 0, "whole turns");
+    const int8_t* q0 = a.q + m0 * a.ldq + static_cast<int64_t>(u_begin + u) * 32 + half * 16;
+    const int live = static_cast<int>(min(static_cast<int64_t>(T), a.M - m0));
+    // scales of a channel's chunk in one access, where they lie on its boundary
+    const bool wide = a.lds % GC == 0 && (reinterpret_cast<uintptr_t>(a.scale) & (GC * 2 - 1)) == 0 &&
+                      (!kOff || (a.ldb % GC == 0 && (reinterpret_cast<uintptr_t>(a.offset) & (GC * 2 - 1)) == 0));
+    using Vec = std::conditional_t<GC == 8, uint4, std::conditional_t<GC == 4, uint2, std::conditional_t<GC == 2, uint32_t, uint16_t>>>;
+    constexpr int kRows = kWideCh / kSide;
+    uint4 w[kPieces];
+    Vec sc[kRows], of[kOff ? kRows : 1];
+    auto load = [&](int c) {
+      const int left = units - c * CU;
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int i = pair + j * kPairs, g = i / T, tok = i - g * T;
+        w[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (g * GU < left && tok < live)
+          w[j] = __ldg(reinterpret_cast<const uint4*>(q0 + tok * a.ldq + (c * CU + g * GU) * 32));
+      }
+      const int g0 = (u_begin + c * CU) / GU;
+      const bool whole = wide && left >= CU;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const int64_t n = min(n_cta + st + r * kSide, a.N - 1);   // rows past N repeat the last one
+        const uint16_t *sp = a.scale + n * a.lds + g0, *op = kOff ? a.offset + n * a.ldb + g0 : nullptr;
+        if (whole) {
+          sc[r] = __ldg(reinterpret_cast<const Vec*>(sp));
+          if (kOff) of[r] = __ldg(reinterpret_cast<const Vec*>(op));
+        } else {
+          alignas(16) uint16_t e[GC], f[GC];
+#pragma unroll
+          for (int g = 0; g < GC; ++g) {
+            e[g] = g * GU < left ? __ldg(sp + g) : static_cast<uint16_t>(0);
+            f[g] = kOff && g * GU < left ? __ldg(op + g) : static_cast<uint16_t>(0);
+          }
+          memcpy(&sc[r], e, sizeof(Vec));
+          if (kOff) memcpy(&of[r], f, sizeof(Vec));
+        }
+      }
+    };
+    if (chunks > 0) load(0);
+    for (int c = 0; c < chunks; ++c) {
+      if (c >= 2) named_sync(kEmpty + (c & 1));
+      uint8_t* buf = buffer(c);
+      Vec* s_scale = reinterpret_cast<Vec*>(buf + C::kB);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        s_scale[st + r * kSide] = sc[r];
+        if (kOff) s_scale[kWideCh + st + r * kSide] = of[r];
+      }
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int i = pair + j * kPairs, g = i / T, tok = i - g * T;
+        // [unit][even, odd][token][4 pairs of words]: the even codes' words of two lanes, then the odd ones'
+        uint4* dst = reinterpret_cast<uint4*>(buf) + ((g * GU + u) * 2 * T + tok) * 2 + half;
+        const uint32_t x0 = __byte_perm(w[j].x, w[j].y, 0x5140u) ^ 0x80808080u;   // codes 0, 4, 1, 5
+        const uint32_t x1 = __byte_perm(w[j].x, w[j].y, 0x7362u) ^ 0x80808080u;   // codes 2, 6, 3, 7
+        const uint32_t z0 = __byte_perm(w[j].z, w[j].w, 0x5140u) ^ 0x80808080u;
+        const uint32_t z1 = __byte_perm(w[j].z, w[j].w, 0x7362u) ^ 0x80808080u;
+        dst[0] = make_uint4(widen(x0, 0x4140u), widen(x1, 0x4140u), widen(z0, 0x4140u), widen(z1, 0x4140u));
+        dst[2 * T] = make_uint4(widen(x0, 0x4342u), widen(x1, 0x4342u), widen(z0, 0x4342u), widen(z1, 0x4342u));
+        if constexpr (kOff) {   // the group's sum of q: its 2 GU pieces lie in neighbouring lanes
+          int sum = __dp4a(static_cast<int>(w[j].x), 0x01010101, __dp4a(static_cast<int>(w[j].y), 0x01010101, 0));
+          sum = __dp4a(static_cast<int>(w[j].z), 0x01010101, __dp4a(static_cast<int>(w[j].w), 0x01010101, sum));
+#pragma unroll
+          for (int o = 1; o < 2 * GU; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (half == 0 && u == 0) reinterpret_cast<float*>(buf + C::kB + 2 * C::kScale)[i] = static_cast<float>(sum);
+        }
+      }
+      named_arrive(kFull + (c & 1));
+      if (c + 1 < chunks) load(c + 1);
+    }
+  } else {
+    // ============ contraction ============
+    // this warp's weight ring: 32 rows x 8 units a stage, 16-byte piece i * 32 +
+    // lane.  Rows past N repeat the last one and are not stored.
+    const uint32_t ring = smem_u32(smem) + warp * kWideStages * kWideStage + (lane >> 3) * kPitch + (lane & 7) * 16;
+    const int64_t row0 = n_cta + warp * 32 + (lane >> 3);
+    const uint8_t* wp = a.w4 + (static_cast<int64_t>(u_begin) + (lane & 7)) * 16;
+    auto issue = [&](int st) {
+      if (st * kStageUnits + (lane & 7) < units) {
+        const uint32_t dst = ring + (st % kWideStages) * kWideStage;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          cp_async_16(dst + 4 * i * kPitch, wp + min(row0 + 4 * i, a.N - 1) * a.ldw4 + st * (kStageUnits * 16), 16);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int st = 0; st < kWideStages - 1; ++st) issue(st);
+    float acc[2][NT][4];
+    for (int c = 0; c < chunks; ++c) {
+      constexpr int kPer = kStageUnits / CU;
+      const int st = c / kPer;
+      if (c % kPer == 0) {
+        issue(st + kWideStages - 1);
+        cp_async_wait<kWideStages - 1>();
+        __syncwarp();
+      }
+      const uint8_t* wb = smem + (warp * kWideStages + st % kWideStages) * kWideStage + (c % kPer) * (CU * 16) + lr * kPitch + lc * 4;
+      named_sync(kFull + (c & 1));
+      const uint8_t* buf = buffer(c);
+      const uint2* s_b = reinterpret_cast<const uint2*>(buf) + lr * 4 + lc;
+      const uint16_t* sp = reinterpret_cast<const uint16_t*>(buf + C::kB) + (warp * 32 + lr) * GC;
+      const float* qs = reinterpret_cast<const float*>(buf + C::kB + 2 * C::kScale) + 2 * lc;
+      const uint16_t* op = kOff ? sp + kWideCh * GC : sp;
+      const Scales<GC> sv[4] = {Scales<GC>(sp), Scales<GC>(sp + 8 * GC), Scales<GC>(sp + 16 * GC), Scales<GC>(sp + 24 * GC)};
+      const Scales<GC> ov[4] = {Scales<GC>(op), Scales<GC>(op + 8 * GC), Scales<GC>(op + 16 * GC), Scales<GC>(op + 24 * GC)};
+      auto unit = [&](int u, auto first) {
+        uint32_t ae[2][4], ao[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(wb + i * 16 * kPitch + u * 16);
+          const uint32_t w1 = *reinterpret_cast<const uint32_t*>(wb + (i * 16 + 8) * kPitch + u * 16);
+          ae[i][0] = even_codes(w0), ae[i][1] = even_codes(w1), ae[i][2] = even_codes(w0 >> 8), ae[i][3] = even_codes(w1 >> 8);
+          ao[i][0] = odd_codes(w0), ao[i][1] = odd_codes(w1), ao[i][2] = odd_codes(w0 >> 8), ao[i][3] = odd_codes(w1 >> 8);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const uint2 b = s_b[(u * 2 * T + t * 8) * 4];
+          mma_f16_16816<decltype(first)::value>(acc[0][t], ae[0], b.x, b.y);
+          mma_f16_16816<decltype(first)::value>(acc[1][t], ae[1], b.x, b.y);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {   // an accumulator's next instruction comes 2 NT later
+          const uint2 b = s_b[((u * 2 + 1) * T + t * 8) * 4];
+          mma_f16_16816<false>(acc[0][t], ao[0], b.x, b.y);
+          mma_f16_16816<false>(acc[1][t], ao[1], b.x, b.y);
+        }
+      };
+      auto group = [&](int g) {
+        unit(g * GU, std::true_type{});
+#pragma unroll
+        for (int u = 1; u < GU; ++u) unit(g * GU + u, std::false_type{});
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            y[i][t][0] = __fmaf_rn(acc[i][t][0], sv[i * 2][g], y[i][t][0]);
+            y[i][t][1] = __fmaf_rn(acc[i][t][1], sv[i * 2][g], y[i][t][1]);
+            y[i][t][2] = __fmaf_rn(acc[i][t][2], sv[i * 2 + 1][g], y[i][t][2]);
+            y[i][t][3] = __fmaf_rn(acc[i][t][3], sv[i * 2 + 1][g], y[i][t][3]);
+          }
+          if constexpr (kOff) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const float2 q = *reinterpret_cast<const float2*>(qs + g * T + t * 8);
+              y[i][t][0] = __fmaf_rn(q.x, ov[i * 2][g], y[i][t][0]);
+              y[i][t][1] = __fmaf_rn(q.y, ov[i * 2][g], y[i][t][1]);
+              y[i][t][2] = __fmaf_rn(q.x, ov[i * 2 + 1][g], y[i][t][2]);
+              y[i][t][3] = __fmaf_rn(q.y, ov[i * 2 + 1][g], y[i][t][3]);
+            }
+          }
+        }
+      };
+      const int n = units - c * CU;
+      if (n >= CU) {
+#pragma unroll
+        for (int g = 0; g < GC; ++g) group(g);
+      } else {
+#pragma unroll
+        for (int g = 0; g < GC; ++g)
+          if (g * GU < n) group(g);
+      }
+      if (c + 2 < chunks) named_arrive(kEmpty + (c & 1));
+      __syncwarp();   // the stage is free for the copy that the next turn issues
+    }
+    cp_async_wait<0>();
+  }
+
+  __syncthreads();
+  if (warp < kWideWarps) {
+    float* s_y = reinterpret_cast<float*>(smem);   // [token][channel]
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          s_y[(t * 8 + 2 * lc + (e & 1)) * kWideCh + warp * 32 + i * 16 + lr + 8 * (e >> 1)] = y[i][t][e];
+  }
+  join_slices<kWideCh>(a, smem_u32(smem), rank, slices, m0, T, n_cta, tid, kWideThreads);
+}
+
+template <class... P, class... A>
+cudaError_t launch_slices(void (*kernel)(P...), int channels, int threads, int bytes, int slices, const W4gArgs& a,
+                          cudaStream_t stream, const A&... rest) {
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), bytes);
   if (e != cudaSuccess) return e;
+  const int64_t tiles = (a.N + channels - 1) / channels;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * slices), static_cast<unsigned>((a.M + kSlabRows - 1) / kSlabRows));
-  cfg.blockDim = dim3(kWarps<T> * 32);
-  cfg.dynamicSmemBytes = static_cast<size_t>(l.bytes);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -346,19 +586,36 @@ cudaError_t launch_t(const W4gArgs& a, cudaStream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, w4g_kernel<T, GU, kOff>, a, l, slices, slice_units);
+  return cudaLaunchKernelEx(&cfg, kernel, a, rest...);
 }
 
 template <int GU, bool kOff>
 cudaError_t launch_gu(const W4gArgs& a, cudaStream_t stream) {
-  if (a.M <= 1) return launch_t<1, GU, kOff>(a, stream);
-  if (a.M <= 2) return launch_t<2, GU, kOff>(a, stream);
-  if (a.M <= 4) return launch_t<4, GU, kOff>(a, stream);
-  if (a.M <= 8) return launch_t<8, GU, kOff>(a, stream);
-  if (a.M <= 16) return launch_t<16, GU, kOff>(a, stream);
-  if (a.M <= 24) return launch_t<24, GU, kOff>(a, stream);
-  if (a.M <= 40) return launch_t<40, GU, kOff>(a, stream);
-  return launch_t<64, GU, kOff>(a, stream);
+  // Slices of K: as many as let four CTAs of 64 channels (two of 128) on every
+  // SM run at once, at most a cluster of eight; each a multiple of a stage.  A
+  // rule on N and K alone: a row's sums do not depend on M.
+  const int64_t tiles64 = (a.N + 63) / 64;
+  const int units = static_cast<int>(a.K >> 5), stages = (units + kStageUnits - 1) / kStageUnits;
+  const int slices = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({4 * sm_count() / tiles64, 8, stages})));
+  const int slice_units = (stages + slices - 1) / slices * kStageUnits;
+  auto few = [&](auto t) {
+    constexpr int T = decltype(t)::value;
+    const Layout l = layout<T, GU>(slice_units, kOff);
+    return launch_slices(w4g_kernel<T, GU, kOff>, kCh, kThreads, l.bytes, slices, a, stream, l, slices, slice_units);
+  };
+  auto wide = [&](auto t) {
+    constexpr int T = decltype(t)::value;
+    return launch_slices(w4g_wide_kernel<T, GU, kOff>, kWideCh, kWideThreads, Wide<T, GU, kOff>::kBytes, slices, a, stream,
+                         slices, slice_units);
+  };
+  if (a.M <= 1) return few(std::integral_constant<int, 1>{});
+  if (a.M <= 2) return few(std::integral_constant<int, 2>{});
+  if (a.M <= 4) return few(std::integral_constant<int, 4>{});
+  if (a.M <= 8) return few(std::integral_constant<int, 8>{});
+  if (a.M <= 16) return wide(std::integral_constant<int, 16>{});
+  if (a.M <= 24) return wide(std::integral_constant<int, 24>{});
+  if (a.M <= 40) return wide(std::integral_constant<int, 40>{});
+  return wide(std::integral_constant<int, 64>{});
 }
 
 template <bool kOff>

@@ -21,7 +21,7 @@ struct AttrEntry {
   const void* kernel;
   int bytes;
 };
-constexpr int kMaxKernels = 32;
+constexpr int kMaxKernels = 128;
 AttrEntry g_attr[kMaxDevices][kMaxKernels];
 int g_attr_n[kMaxDevices];
 
