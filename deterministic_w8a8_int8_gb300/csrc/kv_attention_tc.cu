@@ -100,7 +100,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } s_item;
   __shared__ int s_scan[kThreads];
   __shared__ int s_warp[kThreads / 32];
-  __shared__ float s_max[kThreads / 32];
+  __shared__ float s_max[kConvWarps];                        // largest value scale of a warp's pages
+  __shared__ int s_bad[kConvWarps];                          // an invalid one among them
+  __shared__ float s_unit[kWideRows];                        // a row's scale
   __shared__ float s_top[2][2][kWideRows], s_l[kWideRows];   // the halves' maxima (by the block's parity); one half's sum
   __shared__ float s_ks[kUnitSlots][U], s_vr[kUnitSlots][U];
   // completions: K, V converted; scales in place; S formed (K free); P formed; O added to (V, P free); queries; the end
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int64_t item = blockIdx.x;; item += gridDim.x, ++items) {
     {
       Walk walk = s_item.walk;
-      SeqPlan plan;
+      SeqPlan plan = s_item.plan;
       if (!find_item<true, kWideRows, kThreads>(a, item, walk, s_scan, s_warp, plan)) break;
       __syncthreads();               // everyone has read s_item
       if (tid == 0) {
@@ -170,32 +172,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int blocks = k_end > k_begin ? (k_end - k_begin + KB - 1) / KB : 0;
     const int32_t* table = c.table + s_item.walk.s * c.ld_table;
 
-    // ---- the piece's largest value scale, and its pages' validity
-    bool bad_page = false;
-    float v_top = 0.0f;
-    if (blocks > 0) {
-      for (int32_t i = (k_begin >> c.block_shift) + tid; i <= (k_end - 1) >> c.block_shift; i += kThreads) {
-        const int32_t page = table[i];
-        if (page < 0 || page >= c.num_pages) {
-          bad_page = true;
-        } else {
-          v_top = fmaxf(v_top, c.v_scale[static_cast<int64_t>(page) * c.H + hk]);
-        }
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v_top = fmaxf(v_top, __shfl_xor_sync(0xffffffffu, v_top, o));
-    if (lane == 0) s_max[warp] = v_top;
-    const bool bad = __syncthreads_or(bad_page);
-    v_top = s_max[0];
-#pragma unroll
-    for (int i = 1; i < kThreads / 32; ++i) v_top = fmaxf(v_top, s_max[i]);
-    const float v_inv = v_top >= 0x1p-126f ? __frcp_rn(v_top) : 0.0f;
-
     if (warp >= kSoftWarps && warp < kSoftWarps + kConvWarps) {
       // ============================ converters ==============================
       const bool is_v = warp >= kSoftWarps + kConvWarps / 2;
       const int ct = (tid - kSoft) & (kSide - 1);
+      // ---- the piece's largest value scale, and its pages' validity
+      bool bad = false;
+      float v_top = 0.0f;
+      if (blocks > 0) {
+        for (int32_t i = (k_begin >> c.block_shift) + tid - kSoft; i <= (k_end - 1) >> c.block_shift; i += kConv) {
+          const int32_t page = table[i];
+          if (page < 0 || page >= c.num_pages) {
+            bad = true;
+          } else {
+            v_top = fmaxf(v_top, c.v_scale[static_cast<int64_t>(page) * c.H + hk]);
+          }
+        }
+      }
+      bad = __any_sync(0xffffffffu, bad);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v_top = fmaxf(v_top, __shfl_xor_sync(0xffffffffu, v_top, o));
+      if (lane == 0) {
+        s_max[warp - kSoftWarps] = v_top;
+        s_bad[warp - kSoftWarps] = bad;
+      }
       const bool mine = ct < C::kItems;
       // the thread's item, keys 8 kg .. + 7 and channels 16 ch .. + 15.  K: the
       // pieces of a row side by side; V: eight key groups of a channel, whose
@@ -233,6 +233,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         scales = unit_scales(0, u0);
         next_scales = unit_scales(1, u1);
       }
+      named_barrier(5, kConv);
+      v_top = s_max[0];
+#pragma unroll
+      for (int i = 1; i < kConvWarps; ++i) v_top = fmaxf(v_top, s_max[i]);
+      const float v_inv = v_top >= 0x1p-126f ? __frcp_rn(v_top) : 0.0f;
       for (int j = 0; j < blocks; ++j) {
         const uint32_t g = g0 + j, ph = (g >> 1) & 1;
         if (!is_v) {
@@ -350,37 +355,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         t = p.sp.b + tok;
         h = hk * a.G + row - tok * a.G;
       };
-      // ---- the tile's queries as binary16, K-major: row r, a half of its channels
-      float unit;
-      {
-        int64_t t;
-        int h;
-        place(t, h);
-        const uint16_t* qp = a.q + t * a.ldq_t + static_cast<int64_t>(h) * a.ldq_h;
-        float amax = 0.0f;
-#pragma unroll 8
-        for (int i = 0; i < D / 8; ++i) {
-          if (live) {
-            const uint4 v = *reinterpret_cast<const uint4*>(qp + i * 8);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      // ---- the tile's queries as binary16, K-major: a warp takes 16 of its
+      // quarter's rows, a row's 16-byte pieces side by side
+      constexpr int kRowLanes = D / 8, kTurnRows = 32 / kRowLanes, kTurns = 16 / kTurnRows, kAhead = kTurns < 8 ? kTurns : 8;
+      const int q_row = (warp & 3) * 32 + half * 16 + lane / kRowLanes, q_piece = lane % kRowLanes;
+      auto load_q = [&](int turn) {
+        const int row = keys.row0 + q_row + turn * kTurnRows, tok = row / a.G;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (q_row + turn * kTurnRows < keys.n_rows)
+          v = __ldg(reinterpret_cast<const uint4*>(a.q + (p.sp.b + tok) * a.ldq_t +
+                                                   static_cast<int64_t>(hk * a.G + row - tok * a.G) * a.ldq_h + q_piece * 8));
+        return v;
+      };
+      uint4 qv[kAhead];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
-          }
+      for (int i = 0; i < kAhead; ++i) qv[i] = load_q(i);
+#pragma unroll
+      for (int t0 = 0; t0 < kTurns; t0 += kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const uint4 v = qv[i];
+          if (t0 + kAhead < kTurns) qv[i] = load_q(t0 + kAhead + i);
+          const int row = q_row + (t0 + i) * kTurnRows;
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          float amax = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+#pragma unroll
+          for (int o = 1; o < kRowLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          const int fe = query_exponent(amax);
+          const float f = __uint_as_float(static_cast<uint32_t>(fe) << 23);
+          if (q_piece == 0) s_unit[row] = __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) * a.scale_log2;
+          *reinterpret_cast<uint4*>(s_q + (q_piece >> 3) * (kWideRows * 128) + row * 128 + (((q_piece & 7) ^ (row & 7)) << 4)) =
+              make_uint4(half2_bits(bf16_lo(v.x) * f, bf16_hi(v.x) * f), half2_bits(bf16_lo(v.y) * f, bf16_hi(v.y) * f),
+                         half2_bits(bf16_lo(v.z) * f, bf16_hi(v.z) * f), half2_bits(bf16_lo(v.w) * f, bf16_hi(v.w) * f));
         }
-        const int fe = query_exponent(amax);
-        const float f = __uint_as_float(static_cast<uint32_t>(fe) << 23);
-        unit = __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) * a.scale_log2;
-#pragma unroll 8
-        for (int i = half * (D / 16); i < (half + 1) * (D / 16); ++i) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (live) v = *reinterpret_cast<const uint4*>(qp + i * 8);
-          const uint4 q = make_uint4(half2_bits(bf16_lo(v.x) * f, bf16_hi(v.x) * f), half2_bits(bf16_lo(v.y) * f, bf16_hi(v.y) * f),
-                                     half2_bits(bf16_lo(v.z) * f, bf16_hi(v.z) * f), half2_bits(bf16_lo(v.w) * f, bf16_hi(v.w) * f));
-          *reinterpret_cast<uint4*>(s_q + (i >> 3) * (kWideRows * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4)) = q;
-        }
-        tc::fence_proxy_async();
-        if (blocks > 0) tc::mbar_arrive(bar_q);
       }
+      tc::fence_proxy_async();
+      if (blocks > 0) tc::mbar_arrive(bar_q);
+      named_barrier(1 + (warp & 3), 64);
+      const float unit = s_unit[r];
       const int32_t row_hi = keys.hi(r), my_lo = keys.lo(row_hi), my_hi = min(row_hi, k_end);
       const int32_t all_lo = keys.a_lo, all_hi = min(keys.a_hi, k_end);   // the keys that every row sees here
       float m = -INFINITY, l = 0.0f;
@@ -483,6 +497,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // ---- the row's output, or its piece
+      bool bad = false;
+      float v_top = 0.0f;
+      if (blocks > 0) {   // in place since the first block's scales are
+#pragma unroll
+        for (int i = 0; i < kConvWarps; ++i) {
+          bad |= s_bad[i] != 0;
+          v_top = fmaxf(v_top, s_max[i]);
+        }
+      }
       if (half == 1) s_l[r] = l;
       named_barrier(1 + (warp & 3), 64);
       if (half == 0) s_l[r] = l + s_l[r];
@@ -497,29 +520,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* ps = static_cast<float*>(a.ws) +
                   ((static_cast<int64_t>(s_item.walk.s) * c.H + hk) * part_stride + s_item.walk.split * p.rows + keys.row0 + r) * (D + 4);
       const float scale = !some ? 0.0f : p.splits == 1 ? v_top / l : v_top;
+      // a warp's 32 rows, 32 channels at a time, pass through its 4 KB of the
+      // (now unused) K stages, 16-byte pieces swizzled: rows are written whole
+      float* turn = reinterpret_cast<float*>(s_k) + warp * 1024;
+      const bool final = p.splits == 1;
+      const bool spoilt = bad && final;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t o[16] = {};
+      for (int i = 0; i < D / 64; ++i) {
+        uint32_t o[2][16] = {};
         if (blocks > 0) {
-          tc::tmem_ld16(t_o + i * 16, o);
+          tc::tmem_ld16(t_o + i * 32, o[0]);
+          tc::tmem_ld16(t_o + i * 32 + 16, o[1]);
           tc::tmem_wait_ld();
         }
-        const int d = half * (D / 2) + i * 16;
-        float y[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] = some ? __uint_as_float(o[e]) * scale : 0.0f;
-        if (live && p.splits == 1) {
-          uint32_t w[8];
+        for (int e = 0; e < 32; e += 4) {
+          float y[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            w[e] = bad ? kBf16NaN * 0x10001u : float_to_bf16_rne(y[2 * e]) | float_to_bf16_rne(y[2 * e + 1]) << 16;
-          uint4* dst = reinterpret_cast<uint4*>(a.out + t * a.ldo_t + h * a.ldo_h + d);
-          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        } else if (live) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(ps + 4 + d + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+          for (int k = 0; k < 4; ++k)
+            y[k] = spoilt ? nanf : some ? __uint_as_float(o[(e + k) >> 4][(e + k) & 15]) * scale : 0.0f;
+          *reinterpret_cast<float4*>(turn + lane * 32 + (((e >> 2) ^ (lane & 7)) << 2)) = make_float4(y[0], y[1], y[2], y[3]);
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int k = 0; k < 8; ++k) {
+          const int rl = k * 4 + (lane >> 3), piece = lane & 7, rr = (warp & 3) * 32 + rl;   // the row of the tile
+          const float4 v = *reinterpret_cast<const float4*>(turn + rl * 32 + ((piece ^ (rl & 7)) << 2));
+          const int d = half * (D / 2) + i * 32 + piece * 4;
+          if (rr < keys.n_rows) {
+            if (final) {
+              const int row = keys.row0 + rr, tok = row / a.G;
+              *reinterpret_cast<uint2*>(a.out + (p.sp.b + tok) * a.ldo_t +
+                                        static_cast<int64_t>(hk * a.G + row - tok * a.G) * a.ldo_h + d) =
+                  make_uint2(float_to_bf16_rne(v.x) | float_to_bf16_rne(v.y) << 16,
+                             float_to_bf16_rne(v.z) | float_to_bf16_rne(v.w) << 16);
+            } else {
+              *reinterpret_cast<float4*>(ps + static_cast<int64_t>(rr - r) * (D + 4) + 4 + d) = v;
+            }
+          }
         }
         __syncwarp();
       }

@@ -34,15 +34,16 @@ __host__ __device__ __forceinline__ int split_count(int64_t keys, int64_t rows, 
     const int64_t cap = kFillFew / H;
     return static_cast<int>(most > cap ? (cap < 1 ? 1 : cap) : most);
   }
-  const int64_t one = (rows + kWideRows - 1) / kWideRows * H;      // items with one piece
-  int64_t best = 1, best_n = 0, best_d = 1;                        // share of the turns in use, as a fraction
-  for (int64_t k = one >= kSms ? 1 : (kSms * 4 / 5 + one - 1) / one, i = 0; i < 8; ++k, ++i) {
-    if (k > most) k = most, i = 8;
-    const int64_t items = k * one, d = (items + kSms - 1) / kSms * kSms;
+  if ((rows + kWideRows - 1) / kWideRows * H >= 4 * kSms) return 1;   // one piece uses four fifths
+  const int one = static_cast<int>((rows + kWideRows - 1) / kWideRows * H);   // items with one piece
+  int best = 1, best_n = 0, best_d = 1;                                       // share of the turns in use, as a fraction
+  for (int k = one >= kSms ? 1 : (kSms * 4 / 5 + one - 1) / one, i = 0; i < 8; ++k, ++i) {
+    if (k > most) k = static_cast<int>(most), i = 8;
+    const int items = k * one, d = (items + kSms - 1) / kSms * kSms;
     if (items * best_d > best_n * d) best = k, best_n = items, best_d = d;
     if (items * 5 >= d * 4) break;
   }
-  return static_cast<int>(best);
+  return best;
 }
 // The most rows of one (sequence, KV head) that can be cut into pieces, and
 // its most (row, piece) pairs.  Fewer keys never make more pieces.
@@ -101,8 +102,8 @@ struct Walk {
   int items;                   // items in it
   int tile, split, hk, s;      // the item found
 };
-__device__ __forceinline__ Walk new_walk() { return Walk{0, 0, 0, 0, 0, 0, 0, 0}; }
-// Finds `item`; false past the last one.  All kThreads threads; s_scan
+__device__ __forceinline__ Walk new_walk() { return Walk{0, 0, 0, 0, 0, 0, 0, -1}; }
+// Finds `item`, and the plan of its sequence (p keeps the one of w.s); false past the last one.  All kThreads threads; s_scan
 // [kThreads] and s_warp [kThreads / 32] are free again after the caller's next
 // barrier.  kThreads <= 1023.
 template <bool kWide, int kTileRows, int kThreads>
@@ -137,8 +138,10 @@ __device__ __forceinline__ bool find_item(const KvAttentionArgs& a, int64_t item
 #pragma unroll
   for (int o = 512; o > 0; o >>= 1)
     if (at + o <= kThreads && s_scan[at + o - 1] <= local) at += o;
-  w.s = w.s0 + at;
-  seq_items<kWide, kTileRows>(a, w.s, p);
+  if (w.s != w.s0 + at) {
+    w.s = w.s0 + at;
+    seq_items<kWide, kTileRows>(a, w.s, p);
+  }
   int rest = local - (at > 0 ? s_scan[at - 1] : 0);
   w.tile = rest % p.tiles;
   rest /= p.tiles;
