@@ -486,13 +486,14 @@ __device__ __forceinline__ void store_row(const KvAttentionArgs& a, const SeqPla
     a.lse[t * a.Hq + h] = nan ? __uint_as_float(0x7fc00000u) : mx == -INFINITY ? mx : (mx - kPShift + log2f(sum)) * kLn2;
 }
 
-// Joins the pieces of rows of one (sequence, KV head).  Up to kWarpPieces
+// Joins the pieces of rows of one (sequence, KV head).  Many rows: a row a
+// warp, tiles in eighths.  Few rows, up to kWarpPieces
 // pieces: a row a warp, each lane D / 32 channels.  More: a row a CTA; thread i
 // weighs piece i, then D / 4 columns of threads by 1024 / D groups add every
 // group-th piece in order, and the groups are added in order.
 constexpr int kWarpPieces = 16;
 
-template <int D>
+template <int D, bool kMany>   // kMany: a sequence may have many rows
 __global__ void __launch_bounds__(kJoinThreads)
     kv_combine_kernel(const __grid_constant__ KvAttentionArgs a, int64_t part_stride) {
   constexpr int kCols = D / 4, kGroups = kJoinThreads / kCols, kJoinWarps = kJoinThreads / 32, E = D / 32;
@@ -500,12 +501,57 @@ __global__ void __launch_bounds__(kJoinThreads)
   __shared__ float4 s_o[kJoinThreads];
   static_assert(kMaxSplit <= kJoinThreads, "a thread for each piece");
   pdl_trigger();
-  pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int s = blockIdx.x, hk = blockIdx.y;
+  // the plan is made while the previous kernel ends: its inputs are older
   SeqPlan p;
-  if (seq_items<false, 1>(a, s, p) < 0 || p.bad || p.splits == 1) return;
+  if (seq_items<false, 1, kMany>(a, s, p) < 0 || p.bad || p.splits == 1) return;
+  if (!kMany || p.rows <= kFewRows) pdl_wait();
   const float* base = static_cast<const float*>(a.ws) + (static_cast<int64_t>(s) * a.c.H + hk) * part_stride * (D + 4);
+  if constexpr (kMany) if (p.rows > kFewRows) {
+    __shared__ int64_t s_line[kJoinThreads], s_warp64[kJoinWarps];
+    lay_line<kJoinThreads>(a, p, s_line, s_warp64);
+    pdl_wait();
+    const Cuts cuts(s_line[kJoinThreads - 1], p.splits);
+    const int tiles = (p.rows + kWideRows - 1) / kWideRows;
+    for (int u = blockIdx.z; u < tiles * 8; u += gridDim.z) {
+      const TileSpan t = tile_span<kJoinThreads>(a, p, s_line, u >> 3);
+      const int first = cuts.range_of(t.x), last = cuts.range_of(t.x + t.blocks - 1);
+      if (first == last) continue;   // in one piece: answered
+      for (int i = (u & 7) * (kWideRows / 8) + warp; i < (u & 7) * (kWideRows / 8) + kWideRows / 8; i += kJoinWarps) {
+        const int r = (u >> 3) * kWideRows + i;
+        if (r >= p.rows) break;
+        auto piece = [&](int range) { return base + (static_cast<int64_t>(2 * range + (range == first)) * kWideRows + i) * (D + 4); };
+        float mx = -INFINITY;
+        bool nan = false;
+        for (int range = first + lane; range <= last; range += 32) {
+          const float m = piece(range)[0];
+          nan |= m != m;
+          mx = fmaxf(mx, m);
+        }
+        nan = __any_sync(0xffffffffu, nan);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        float sum = 0.0f, y[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = 0.0f;
+#pragma unroll 4
+        for (int range = first; range <= last; ++range) {
+          const float* v = piece(range);
+          const float w = v[0] == -INFINITY ? 0.0f : ex2(v[0] - mx);
+          sum = fmaf(w, v[1], sum);
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const float2 x = *reinterpret_cast<const float2*>(v + 4 + lane * E + e);
+            y[e] = fmaf(w, x.x, y[e]);
+            y[e + 1] = fmaf(w, x.y, y[e + 1]);
+          }
+        }
+        store_row<E>(a, p, hk, r, lane * E, y, sum, mx, nan);
+      }
+    }
+    return;
+  }
   const int64_t step = static_cast<int64_t>(p.rows) * (D + 4);
   if (p.splits <= kWarpPieces) {
     for (int r = blockIdx.z * kJoinWarps + warp; r < p.rows; r += gridDim.z * kJoinWarps) {
@@ -613,23 +659,25 @@ cudaError_t launch_few(const KvAttentionArgs& a, int64_t part_stride, cudaStream
 template <int D>
 cudaError_t launch_d(const KvAttentionArgs& a, cudaStream_t stream) {
   const int64_t rows = a.max_q * a.G;
-  int64_t split_rows;
-  const int64_t part_stride = max_split_rows(a.max_q, a.G, a.c.max_pages << a.c.block_shift, a.c.H, &split_rows);
+  const int64_t part_stride = max_split_rows(a.max_q, a.G, a.c.max_pages << a.c.block_shift, a.c.H, D);
   cudaError_t e = rows <= 8                 ? launch_few<D, 1>(a, part_stride, stream)
                   : rows <= 16 || D == 256  ? launch_few<D, 2>(a, part_stride, stream)
                                             : launch_few<D, D == 256 ? 2 : 4>(a, part_stride, stream);
   if (e == cudaSuccess && rows > kFewRows) e = launch_kv_attention_wide(a, part_stride, stream);
   if (e != cudaSuccess || part_stride == 0) return e;
-  const dim3 grid(a.c.S, a.c.H, static_cast<unsigned>(std::min<int64_t>(split_rows, 128)));
-  return launch_kernel(kv_combine_kernel<D>, grid, dim3(kJoinThreads), 0, stream, false, a, part_stride);
+  // CTAs of a (sequence, KV head): a row each of few, an eighth of a tile each
+  // of many, in one turn of the four that an SM holds
+  const int64_t want = rows <= kFewRows ? rows : (rows + kWideRows - 1) / kWideRows * 8;
+  const int64_t most = rows <= kFewRows ? kFewRows : std::max<int64_t>(1, 4 * sm_count() / (static_cast<int64_t>(a.c.S) * a.c.H));
+  const dim3 grid(a.c.S, a.c.H, static_cast<unsigned>(std::min<int64_t>(want, most)));
+  return launch_kernel(rows <= kFewRows ? kv_combine_kernel<D, false> : kv_combine_kernel<D, true>, grid, dim3(kJoinThreads), 0, stream, rows > kFewRows, a, part_stride);
 }
 
 }  // namespace
 
 size_t kv_attention_workspace_bytes(int64_t S, int64_t, int64_t max_q, int64_t max_pages, int64_t Hq, int64_t Hkv,
                                     int64_t D, int64_t block) {
-  int64_t rows;
-  return static_cast<size_t>(S * Hkv * max_split_rows(max_q, Hq / Hkv, max_pages * block, Hkv, &rows)) * (D + 4) * 4;
+  return static_cast<size_t>(S * Hkv * max_split_rows(max_q, Hq / Hkv, max_pages * block, Hkv, D)) * (D + 4) * 4;
 }
 
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream) {

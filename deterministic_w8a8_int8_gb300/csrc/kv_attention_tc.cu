@@ -29,6 +29,8 @@
 // status bit; every warp then runs its loops out without waiting (so that the
 // named barriers still meet), the instructions in flight complete, and the
 // kernel returns.
+#include <type_traits>
+
 #include "kv_plan.cuh"
 #include "tc_common.cuh"
 
@@ -97,9 +99,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk walk;
     SeqPlan plan;
     TileKeys keys;
+    int64_t x, x_end, tile_x;    // the range's blocks not yet in work; the first of tile walk.tile
+    int slot;                    // of the tile's piece; -1: the whole tile
   } s_item;
   __shared__ int s_scan[kThreads];
   __shared__ int s_warp[kThreads / 32];
+  __shared__ int64_t s_line[kThreads], s_warp64[kThreads / 32];   // of sequence walk.s
   __shared__ float s_max[kConvWarps];                        // largest value scale of a warp's pages
   __shared__ int s_bad[kConvWarps];                          // an invalid one among them
   __shared__ float s_unit[kWideRows];                        // a row's scale
@@ -148,24 +153,50 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::tc_fence_after();
   const uint32_t tmem = s_tmem;
   pdl_trigger();
-  pdl_wait();
+  // Launched ahead of the end of the few-row kernel, whose start ends what the
+  // inputs come from; neither needs the other's results.  The wait stands at the end,
+  // so that this kernel's end is also the other's.
   const KvPages& c = a.c;
   uint32_t g0 = 0, items = 0;      // blocks and items before this item: the phases of the mbarriers
-  if (tid == 0) s_item.walk = new_walk();
+  if (tid == 0) {
+    s_item.walk = new_walk();
+    s_item.x = s_item.x_end = 0;
+  }
   __syncthreads();
 
-  for (int64_t item = blockIdx.x;; item += gridDim.x, ++items) {
-    {
+  for (int64_t item = blockIdx.x;; ++items) {   // one tile's part of a range a turn
+    if (s_item.x >= s_item.x_end) {
       Walk walk = s_item.walk;
       SeqPlan plan = s_item.plan;
+      const int before = walk.s;
       if (!find_item<true, kWideRows, kThreads>(a, item, walk, s_scan, s_warp, plan)) break;
+      item += gridDim.x;
+      if (walk.s != before) lay_line<kThreads>(a, plan, s_line, s_warp64);
       __syncthreads();               // everyone has read s_item
       if (tid == 0) {
+        const Cuts cuts(s_line[kThreads - 1], plan.splits);
+        s_item.x = cuts.cut(walk.split);
+        s_item.x_end = cuts.cut(walk.split + 1);
+        if (s_item.x < s_item.x_end) walk.tile = tile_at<kThreads>(a, plan, s_line, s_item.x);
+        if (s_item.x < s_item.x_end) s_item.tile_x = tile_span<kThreads>(a, plan, s_line, walk.tile).x;
         s_item.walk = walk;
         s_item.plan = plan;
-        s_item.keys = TileKeys(a, plan, walk, kWideRows);
       }
-      __syncthreads();
+    }
+    if (tid == 0 && s_item.x < s_item.x_end) {
+      TileKeys k(a, s_item.plan, s_item.walk, kWideRows);
+      const int n = max(1, (k.t_hi - (k.t_lo & ~63) + KB - 1) / KB);   // the tile's blocks
+      const int x = static_cast<int>(s_item.x - s_item.tile_x);
+      const int end = static_cast<int>(min(static_cast<int64_t>(n), s_item.x_end - s_item.tile_x));
+      k.k_begin = (k.t_lo & ~63) + x * KB;
+      k.k_end = static_cast<int32_t>(min(static_cast<int64_t>(k.t_hi), static_cast<int64_t>(k.t_lo & ~63) + static_cast<int64_t>(end) * KB));
+      s_item.slot = end - x == n ? -1 : 2 * s_item.walk.split + (x == 0);
+      s_item.keys = k;
+    }
+    __syncthreads();
+    if (s_item.x >= s_item.x_end) {   // fewer blocks than ranges
+      --items;
+      continue;
     }
     const int hk = s_item.walk.hk;
     const int32_t k_begin = s_item.keys.k_begin, k_end = s_item.keys.k_end;
@@ -176,26 +207,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ============================ converters ==============================
       const bool is_v = warp >= kSoftWarps + kConvWarps / 2;
       const int ct = (tid - kSoft) & (kSide - 1);
-      // ---- the piece's largest value scale, and its pages' validity
-      bool bad = false;
-      float v_top = 0.0f;
-      if (blocks > 0) {
-        for (int32_t i = (k_begin >> c.block_shift) + tid - kSoft; i <= (k_end - 1) >> c.block_shift; i += kConv) {
-          const int32_t page = table[i];
-          if (page < 0 || page >= c.num_pages) {
-            bad = true;
-          } else {
-            v_top = fmaxf(v_top, c.v_scale[static_cast<int64_t>(page) * c.H + hk]);
-          }
-        }
-      }
-      bad = __any_sync(0xffffffffu, bad);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v_top = fmaxf(v_top, __shfl_xor_sync(0xffffffffu, v_top, o));
-      if (lane == 0) {
-        s_max[warp - kSoftWarps] = v_top;
-        s_bad[warp - kSoftWarps] = bad;
-      }
       const bool mine = ct < C::kItems;
       // the thread's item, keys 8 kg .. + 7 and channels 16 ch .. + 15.  K: the
       // pieces of a row side by side; V: eight key groups of a channel, whose
@@ -232,6 +243,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mine) load(0, page);
         scales = unit_scales(0, u0);
         next_scales = unit_scales(1, u1);
+      }
+      // ---- the piece's largest value scale, and its pages' validity
+      bool bad = false;
+      float v_top = 0.0f;
+      if (blocks > 0) {
+        for (int32_t i = (k_begin >> c.block_shift) + tid - kSoft; i <= (k_end - 1) >> c.block_shift; i += kConv) {
+          const int32_t page = table[i];
+          if (page < 0 || page >= c.num_pages) {
+            bad = true;
+          } else {
+            v_top = fmaxf(v_top, c.v_scale[static_cast<int64_t>(page) * c.H + hk]);
+          }
+        }
+      }
+      bad = __any_sync(0xffffffffu, bad);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v_top = fmaxf(v_top, __shfl_xor_sync(0xffffffffu, v_top, o));
+      if (lane == 0) {
+        s_max[warp - kSoftWarps] = v_top;
+        s_bad[warp - kSoftWarps] = bad;
       }
       named_barrier(5, kConv);
       v_top = s_max[0];
@@ -350,21 +381,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp & 3) << 21);
       const uint32_t t_o = t_lane + 2 * KB + half * (D / 2);
       const bool live = r < keys.n_rows;
-      auto place = [&](int64_t& t, int& h) {   // the row's token and head
-        const int row = keys.row0 + r, tok = row / a.G;
-        t = p.sp.b + tok;
-        h = hk * a.G + row - tok * a.G;
+      const int my_tok = (keys.row0 + r) / a.G, my_h = hk * a.G + keys.row0 + r - my_tok * a.G;   // the row's token and head
+      auto of_row = [&](int lane_of, int64_t ld_t, int64_t ld_h) {   // a row of this warp's 32
+        const int tok = __shfl_sync(0xffffffffu, my_tok, lane_of), h = __shfl_sync(0xffffffffu, my_h, lane_of);
+        return (p.sp.b + tok) * ld_t + h * ld_h;
       };
       // ---- the tile's queries as binary16, K-major: a warp takes 16 of its
       // quarter's rows, a row's 16-byte pieces side by side
       constexpr int kRowLanes = D / 8, kTurnRows = 32 / kRowLanes, kTurns = 16 / kTurnRows, kAhead = kTurns < 8 ? kTurns : 8;
       const int q_row = (warp & 3) * 32 + half * 16 + lane / kRowLanes, q_piece = lane % kRowLanes;
       auto load_q = [&](int turn) {
-        const int row = keys.row0 + q_row + turn * kTurnRows, tok = row / a.G;
+        const int64_t at = of_row((q_row + turn * kTurnRows) & 31, a.ldq_t, a.ldq_h) + q_piece * 8;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (q_row + turn * kTurnRows < keys.n_rows)
-          v = __ldg(reinterpret_cast<const uint4*>(a.q + (p.sp.b + tok) * a.ldq_t +
-                                                   static_cast<int64_t>(hk * a.G + row - tok * a.G) * a.ldq_h + q_piece * 8));
+        if (q_row + turn * kTurnRows < keys.n_rows) v = __ldg(reinterpret_cast<const uint4*>(a.q + at));
         return v;
       };
       uint4 qv[kAhead];
@@ -410,30 +439,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* ks = s_ks[g & (kUnitSlots - 1)] + half * UH;
         const float* vs = s_vr[g & (kUnitSlots - 1)] + half * UH;
         float top = -INFINITY;
+        // rolled, and blocks with masked scores apart: three kinds of warps share the instruction cache
+        auto pass_a = [&](auto masked) {
+#pragma unroll 1
+          for (int u = 0; u < UH; u += 2) {
+            uint32_t x[2][16];
+            tc::tmem_ld16(t_s + u * 16, x[0]);
+            tc::tmem_ld16(t_s + u * 16 + 16, x[1]);
+            tc::tmem_wait_ld();
+            if constexpr (decltype(masked)::value) {
 #pragma unroll
-        for (int u = 0; u < UH; u += 2) {
-          uint32_t x[2][16];
-          tc::tmem_ld16(t_s + u * 16, x[0]);
-          tc::tmem_ld16(t_s + u * 16 + 16, x[1]);
-          tc::tmem_wait_ld();
-          if (edge) {
+              for (int e = 0; e < 32; ++e) {
+                const int32_t key = my_key + u * 16 + e;
+                if (key < my_lo || key >= my_hi) x[e >> 4][e & 15] = 0xff800000u;   // -inf
+              }
+            }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int32_t key = my_key + u * 16 + e;
-              if (key < my_lo || key >= my_hi) x[e >> 4][e & 15] = 0xff800000u;   // -inf
+            for (int v = 0; v < 2; ++v) {
+              float t0 = __uint_as_float(x[v][0]), t1 = __uint_as_float(x[v][1]);
+#pragma unroll
+              for (int e = 2; e < 16; e += 2) {
+                t0 = fmaxf(t0, __uint_as_float(x[v][e]));
+                t1 = fmaxf(t1, __uint_as_float(x[v][e + 1]));
+              }
+              t0 = fmaxf(t0, t1);
+              if (t0 > -INFINITY) top = fmaxf(top, t0 * (ks[u + v] * unit));
             }
           }
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            float t0 = __uint_as_float(x[v][0]), t1 = __uint_as_float(x[v][1]);
-#pragma unroll
-            for (int e = 2; e < 16; e += 2) {
-              t0 = fmaxf(t0, __uint_as_float(x[v][e]));
-              t1 = fmaxf(t1, __uint_as_float(x[v][e + 1]));
-            }
-            t0 = fmaxf(t0, t1);
-            if (t0 > -INFINITY) top = fmaxf(top, t0 * (ks[u + v] * unit));
-          }
+        };
+        if (edge) {
+          pass_a(std::true_type{});
+        } else {
+          pass_a(std::false_type{});
         }
         s_top[g & 1][half][r] = top;
         named_barrier(1 + (warp & 3), 64);
@@ -456,35 +493,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         l *= al;
         const float base = m == -INFINITY ? 0.0f : m - kShift;
+        auto pass_b = [&](auto masked) {
+#pragma unroll 1
+          for (int u = 0; u < UH; u += 2) {
+            uint32_t x[2][16], pk[16];
+            tc::tmem_ld16(t_s + u * 16, x[0]);
+            tc::tmem_ld16(t_s + u * 16 + 16, x[1]);
+            tc::tmem_wait_ld();
 #pragma unroll
-        for (int u = 0; u < UH; u += 2) {
-          uint32_t x[2][16], pk[16];
-          tc::tmem_ld16(t_s + u * 16, x[0]);
-          tc::tmem_ld16(t_s + u * 16 + 16, x[1]);
-          tc::tmem_wait_ld();
+            for (int v = 0; v < 2; ++v) {
+              const float f = ks[u + v] * unit, vf = vs[u + v];
+              float q[16];
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const float f = ks[u + v] * unit, vf = vs[u + v];
-            float q[16];
+              for (int e = 0; e < 16; ++e) q[e] = ex2(__fmaf_rn(__uint_as_float(x[v][e]), f, -base));
+              if constexpr (decltype(masked)::value) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) q[e] = ex2(__fmaf_rn(__uint_as_float(x[v][e]), f, -base));
-            if (edge) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int32_t key = my_key + (u + v) * 16 + e;
-                if (key < my_lo || key >= my_hi) q[e] = 0.0f;
+                for (int e = 0; e < 16; ++e) {
+                  const int32_t key = my_key + (u + v) * 16 + e;
+                  if (key < my_lo || key >= my_hi) q[e] = 0.0f;
+                }
               }
-            }
-            float l0 = 0.0f, l1 = 0.0f;
+              float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              l0 += q[e];
-              l1 += q[e + 1];
-              pk[v * 8 + e / 2] = half2_bits(q[e] * vf, q[e + 1] * vf);
+              for (int e = 0; e < 16; e += 2) {
+                l0 += q[e];
+                l1 += q[e + 1];
+                pk[v * 8 + e / 2] = half2_bits(q[e] * vf, q[e + 1] * vf);
+              }
+              l += l0 + l1;
             }
-            l += l0 + l1;
+            tc::tmem_st16(t_s + u * 8, pk);   // over scores that this thread has read
           }
-          tc::tmem_st16(t_s + u * 8, pk);   // over scores that this thread has read
+        };
+        if (edge) {
+          pass_b(std::true_type{});
+        } else {
+          pass_b(std::false_type{});
         }
         tc::tmem_wait_st();
         tc::tc_fence_before();
@@ -513,19 +557,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       l = s_l[r];
       if (bad && tid == 0 && a.err != nullptr) atomicOr(a.err, PRISM_DEV_ERR_PAGE_RANGE);
       const float nanf = __uint_as_float(0x7fc00000u);
-      int64_t t;
-      int h;
-      place(t, h);
       const bool some = m > -INFINITY || l != l;   // saw a key (or a NaN score)
       float* ps = static_cast<float*>(a.ws) +
-                  ((static_cast<int64_t>(s_item.walk.s) * c.H + hk) * part_stride + s_item.walk.split * p.rows + keys.row0 + r) * (D + 4);
-      const float scale = !some ? 0.0f : p.splits == 1 ? v_top / l : v_top;
+                  ((static_cast<int64_t>(s_item.walk.s) * c.H + hk) * part_stride + static_cast<int64_t>(max(s_item.slot, 0)) * kWideRows + r) * (D + 4);
+      const bool final = s_item.slot < 0;
+      const float scale = !some ? 0.0f : final ? v_top / l : v_top;
       // a warp's 32 rows, 32 channels at a time, pass through its 4 KB of the
       // (now unused) K stages, 16-byte pieces swizzled: rows are written whole
       float* turn = reinterpret_cast<float*>(s_k) + warp * 1024;
-      const bool final = p.splits == 1;
       const bool spoilt = bad && final;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < D / 64; ++i) {
         uint32_t o[2][16] = {};
         if (blocks > 0) {
@@ -547,11 +588,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int rl = k * 4 + (lane >> 3), piece = lane & 7, rr = (warp & 3) * 32 + rl;   // the row of the tile
           const float4 v = *reinterpret_cast<const float4*>(turn + rl * 32 + ((piece ^ (rl & 7)) << 2));
           const int d = half * (D / 2) + i * 32 + piece * 4;
+          const int64_t at = of_row(rl, a.ldo_t, a.ldo_h) + d;
           if (rr < keys.n_rows) {
             if (final) {
-              const int row = keys.row0 + rr, tok = row / a.G;
-              *reinterpret_cast<uint2*>(a.out + (p.sp.b + tok) * a.ldo_t +
-                                        static_cast<int64_t>(hk * a.G + row - tok * a.G) * a.ldo_h + d) =
+              *reinterpret_cast<uint2*>(a.out + at) =
                   make_uint2(float_to_bf16_rne(v.x) | float_to_bf16_rne(v.y) << 16,
                              float_to_bf16_rne(v.z) | float_to_bf16_rne(v.w) << 16);
             } else {
@@ -563,21 +603,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (live && half == 0) {
         const float mx = some ? m - kShift + kPShift : -INFINITY;   // the weights' common form
-        if (p.splits > 1) {
+        if (!final) {
           ps[0] = bad ? nanf : mx;
           ps[1] = l;
         } else if (a.lse != nullptr) {
-          a.lse[t * a.Hq + h] = bad ? nanf : !some ? mx : (mx - kPShift + log2f(l)) * kLn2;
+          a.lse[(p.sp.b + my_tok) * static_cast<int64_t>(a.Hq) + my_h] = bad ? nanf : !some ? mx : (mx - kPShift + log2f(l)) * kLn2;
         }
       }
     }
     if (blocks == 0) --items;          // the queries' mbarrier did not turn
     g0 += blocks;
     tc::tc_fence_before();
-    __syncthreads();   // the queries, s_item, s_scan, s_max and the output's columns are free again
+    __syncthreads();   // the queries, s_scan, s_max and the output's columns are free again
     tc::tc_fence_after();
+    if (tid == 0) {    // on to the range's next tile
+      const int64_t n = max(1, (s_item.keys.t_hi - (s_item.keys.t_lo & ~63) + KB - 1) / KB);
+      s_item.tile_x += n;
+      s_item.x = s_item.tile_x;
+      ++s_item.walk.tile;
+    }
+    __syncthreads();
   }
 
+  pdl_wait();
   // ---- every instruction in flight completes before the columns are given back
   if (tid == kSoft + kConv) {   // the issuing thread
     tc::tc_commit(bar_end);
@@ -596,10 +644,9 @@ cudaError_t launch_d(const KvAttentionArgs& a, int64_t part_stride, cudaStream_t
   using C = Tc<D>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kv_attention_tc_kernel<D>), C::kBytes);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = a.T * a.G / kWideRows + a.c.S;
-  const int64_t items = (tiles + part_stride / kFewRows * a.c.S) * a.c.H;
+  const int64_t items = (a.T * a.G / kWideRows + a.c.S + part_stride / kWideRows * a.c.S) * a.c.H;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sm_count()));
-  return launch_kernel(kv_attention_tc_kernel<D>, dim3(grid), dim3(kThreads), C::kBytes, stream, false, a, part_stride);
+  return launch_kernel(kv_attention_tc_kernel<D>, dim3(grid), dim3(kThreads), C::kBytes, stream, true, a, part_stride);
 }
 
 }  // namespace

@@ -3,12 +3,14 @@
 //
 // A sequence's n queries times its G query heads per KV head are rows.  Up to
 // kFewRows rows (decode steps, a few drafted tokens) go to the kernel that
-// streams keys through the warp-level tensor instructions, more rows to the
-// one on the tcgen05 tensor cores.  The keys of either are cut into pieces of
-// at least kMinChunk; the choice and the cut depend on the sequence's own rows
-// and length (and the number of KV heads) alone, so that its result does not
-// depend on the rest of the batch.  The pieces of a row are joined in piece
-// order.
+// streams keys through the warp-level tensor instructions: an item is a tile of
+// rows and a piece of the keys.  More rows go to the one on the tcgen05 tensor
+// cores: the blocks of keys of one tile of 128 rows after the other form a line,
+// which is cut into ranges of equal length, an item each; a tile is in pieces
+// where a cut falls into it.  The choice and the cuts depend on the sequence's
+// own rows and length (and the number of KV heads) alone, so that its result
+// does not depend on the rest of the batch.  The pieces of a row are joined in
+// the order of their keys.
 #pragma once
 
 #include "decode.cuh"
@@ -22,44 +24,46 @@ constexpr int kMinChunk = 1024;        // keys of a piece at least
 constexpr int kMaxSplit = 128;         // pieces of a row at most
 constexpr int kFillFew = 456;          // items that one sequence is cut into where it has the keys: three on each of 152 SMs
 constexpr int kSms = 152;              // one wide item on each at a time
+// Blocks of a range at least, where a line has more ranges than tiles: a part of
+// a tile costs about eight blocks' time besides its blocks (80 rows, 8 KV heads,
+// 8208 keys, with 6, 10 and 16 at least: one sequence 37.8, 40.1 and 48.1 us,
+// three 60.5, 44.4 and 52.5, eight 123, 99 and 92).
+constexpr int kMinBlocks = 10;
+__host__ __device__ constexpr int wide_shift(int D) { return D == 256 ? 6 : 7; }
+__host__ __device__ constexpr int wide_keys(int D) { return 1 << wide_shift(D); }   // keys of a block of the tcgen05 kernel
 constexpr float kPShift = 12.0f;       // pieces keep their maximum m with 2^(x - m + 12) as the weight of score x
 constexpr float kLn2 = 0.69314718055994531f;
 
-// Pieces of the keys of a sequence with so many rows, H KV heads: for few rows
-// as many as fill the SMs, for more the fewest that leave at most a fifth of
-// the SMs' turns empty (or the best of eight).
-__host__ __device__ __forceinline__ int split_count(int64_t keys, int64_t rows, int64_t H) {
+// Pieces of the keys of a sequence of few rows, H KV heads: as many as fill the SMs.
+__host__ __device__ __forceinline__ int split_count(int64_t keys, int64_t H) {
   const int64_t n = (keys + kMinChunk - 1) / kMinChunk, most = n < 1 ? 1 : n > kMaxSplit ? kMaxSplit : n;
-  if (rows <= kFewRows) {
-    const int64_t cap = kFillFew / H;
-    return static_cast<int>(most > cap ? (cap < 1 ? 1 : cap) : most);
-  }
-  if ((rows + kWideRows - 1) / kWideRows * H >= 4 * kSms) return 1;   // one piece uses four fifths
-  const int one = static_cast<int>((rows + kWideRows - 1) / kWideRows * H);   // items with one piece
-  int best = 1, best_n = 0, best_d = 1;                                       // share of the turns in use, as a fraction
-  for (int k = one >= kSms ? 1 : (kSms * 4 / 5 + one - 1) / one, i = 0; i < 8; ++k, ++i) {
-    if (k > most) k = static_cast<int>(most), i = 8;
-    const int items = k * one, d = (items + kSms - 1) / kSms * kSms;
-    if (items * best_d > best_n * d) best = k, best_n = items, best_d = d;
-    if (items * 5 >= d * 4) break;
-  }
-  return best;
+  const int cap = kFillFew / static_cast<int>(H);
+  return most > cap ? (cap < 1 ? 1 : cap) : static_cast<int>(most);
 }
-// The most rows of one (sequence, KV head) that can be cut into pieces, and
-// its most (row, piece) pairs.  Fewer keys never make more pieces.
-inline int64_t max_split_rows(int64_t max_q, int64_t G, int64_t max_keys, int64_t H, int64_t* rows) {
-  int64_t most = 0;
-  *rows = 0;
-  auto take = [&](int64_t r) {
-    const int64_t splits = split_count(max_keys, r, H);
-    if (splits <= 1) return;
-    *rows = std::max(*rows, r);
-    most = std::max(most, splits * r);
-  };
-  take(std::min<int64_t>(kFewRows, max_q * G));
-  for (int64_t tiles = 1; max_q * G > kFewRows; ++tiles) {
-    take(std::min(tiles * kWideRows, max_q * G));
-    if (tiles * kWideRows >= max_q * G || tiles * H >= 4 * kSms) break;   // beyond: one piece uses four fifths
+// Ranges of each KV head's line of so many tiles and blocks: as many as fill the
+// SMs in the fewest turns that leave at most a tenth of them empty (or the best
+// of four).
+__host__ __device__ __forceinline__ int range_count(int64_t tiles, int64_t blocks, int H) {
+  int best = 1, best_turns = 0;
+  for (int turns = (H + kSms - 1) / kSms, i = 0; i < 4; ++turns, ++i) {
+    const int n = kSms * turns / H;
+    if (best_turns == 0 || n * best_turns > best * turns) best = n, best_turns = turns;
+    if (n * H * 10 >= kSms * turns * 9) break;
+  }
+  const int64_t most = tiles > blocks / kMinBlocks ? tiles : blocks / kMinBlocks;
+  return most < best ? static_cast<int>(most) : best;
+}
+// The most (row, piece) pairs of one (sequence, KV head).  A range has at most
+// two tiles in pieces: the one that it begins inside of (slot 2 range), and one
+// that begins in it (slot 2 range + 1).  Fewer keys never make more of either.
+inline int64_t max_split_rows(int64_t max_q, int64_t G, int64_t max_keys, int64_t H, int64_t D) {
+  const int64_t rows = max_q * G, few = std::min<int64_t>(kFewRows, rows);
+  const int64_t splits = split_count(max_keys, H);
+  int64_t most = splits > 1 ? splits * few : 0;
+  if (rows > kFewRows) {
+    const int64_t tiles = (rows + kWideRows - 1) / kWideRows, blocks = (max_keys + wide_keys(static_cast<int>(D)) - 1) >> wide_shift(static_cast<int>(D));
+    const int64_t n = range_count(tiles, tiles * blocks, static_cast<int>(H));
+    if (n > 1) most = std::max(most, 2 * n * kWideRows);
   }
   return most;
 }
@@ -67,14 +71,14 @@ inline int64_t max_split_rows(int64_t max_q, int64_t G, int64_t max_keys, int64_
 // A sequence's plan: its rows, key range and pieces.
 struct SeqPlan {
   SeqSpan sp;
-  int32_t rows, tiles, splits;
+  int32_t rows, tiles, splits;   // splits: pieces of a tile, or ranges
   int32_t lo, chunk;     // first key seen by any of its queries (rounded down to 64), keys of a piece
   bool bad;              // malformed length: its rows get NaN
 };
-// The sequence's items (tiles x pieces x KV heads) of the kernel that asks, 0
+// The sequence's items (tiles x pieces or ranges, x KV heads) of the kernel that asks, 0
 // where the other one has it; -1 for malformed offsets (no rows to answer
 // for).  A malformed length is the few-row kernel's.
-template <bool kWide, int kTileRows>
+template <bool kWide, int kTileRows, bool kJoin = false>   // kJoin: the plan of either kind
 __device__ __forceinline__ int seq_items(const KvAttentionArgs& a, int s, SeqPlan& p) {
   const bool ok = seq_span(a.c, a.cu_q, a.T, s, true, p.sp);
   if (p.sp.b < 0 || p.sp.n < 0 || static_cast<int64_t>(p.sp.b) + p.sp.n > a.T) return -1;
@@ -87,11 +91,19 @@ __device__ __forceinline__ int seq_items(const KvAttentionArgs& a, int s, SeqPla
     const int64_t first = a.window > 0 ? p.sp.len - p.sp.n + 1 - a.window : 0;
     p.lo = first > 0 ? static_cast<int32_t>(first) & ~63 : 0;
     const int64_t keys = p.sp.len - p.lo;
-    p.splits = split_count(keys, p.rows, a.c.H);
-    p.chunk = static_cast<int32_t>((((keys + p.splits - 1) / p.splits) + 63) & ~63ll);
+    if (p.rows <= kFewRows) {
+      if constexpr (!kWide) {
+        p.splits = split_count(keys, a.c.H);
+        p.chunk = static_cast<int32_t>(((static_cast<uint32_t>(keys) + p.splits - 1) / p.splits + 63) & ~63u);
+      }
+    } else if constexpr (kWide || kJoin) {
+      const int shift = wide_shift(a.c.D);
+      const int64_t tiles = (static_cast<int64_t>(p.rows) + kWideRows - 1) / kWideRows;
+      p.splits = range_count(tiles, tiles * ((keys + (1 << shift) - 1) >> shift), a.c.H);
+    }
   }
   if (kWide ? p.bad || p.rows <= kFewRows : !p.bad && p.rows > kFewRows) return 0;
-  return p.tiles * p.splits * a.c.H;
+  return (kWide ? 1 : p.tiles) * p.splits * a.c.H;
 }
 
 // Walks a CTA's items: sequences are counted a window of one a thread at a
@@ -143,8 +155,10 @@ __device__ __forceinline__ bool find_item(const KvAttentionArgs& a, int64_t item
     seq_items<kWide, kTileRows>(a, w.s, p);
   }
   int rest = local - (at > 0 ? s_scan[at - 1] : 0);
-  w.tile = rest % p.tiles;
-  rest /= p.tiles;
+  if (!kWide) {
+    w.tile = rest % p.tiles;
+    rest /= p.tiles;
+  }
   w.split = rest % p.splits;
   w.hk = rest / p.splits;
   return true;
@@ -179,6 +193,88 @@ struct TileKeys {
     return r >= n_rows || none ? 0 : causal ? max(0, first_pos + (row0 + r) / G + 1) : len;
   }
   __device__ __forceinline__ int32_t lo(int32_t hi) const { return window > 0 && hi > window ? hi - window : 0; }
+};
+
+// The lines of a wide sequence.  A tile's blocks: the first begins at the first
+// key that any of its rows sees, rounded down to 64; at least one.
+__device__ __forceinline__ int tile_blocks(const KvAttentionArgs& a, const SeqPlan& p, int tile) {
+  Walk w = new_walk();
+  w.tile = tile;
+  const TileKeys k(a, p, w, kWideRows);
+  const int shift = wide_shift(a.c.D);
+  return max(1, (k.t_hi - (k.t_lo & ~63) + (1 << shift) - 1) >> shift);
+}
+// Blocks up to the end of each thread's tiles (tiles_a_thread of them) in s_line
+// [kThreads]; s_warp64 [kThreads / 32].  All threads, ends with a barrier.
+template <int kThreads>
+__device__ __forceinline__ void lay_line(const KvAttentionArgs& a, const SeqPlan& p, int64_t* s_line, int64_t* s_warp64) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tiles = (p.rows + kWideRows - 1) / kWideRows, each = (tiles + kThreads - 1) / kThreads;
+  int64_t n = 0;
+  for (int t = tid * each; t < min(tiles, (tid + 1) * each); ++t) n += tile_blocks(a, p, t);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, n, o);
+    if (lane >= o) n += v;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp64[warp] = n;
+  __syncthreads();
+  for (int i = 0; i < warp; ++i) n += s_warp64[i];
+  s_line[tid] = n;
+  __syncthreads();
+}
+// A tile's place in its line: its first block and its number of blocks.
+struct TileSpan {
+  int64_t x;
+  int blocks;
+};
+template <int kThreads>
+__device__ __forceinline__ TileSpan tile_span(const KvAttentionArgs& a, const SeqPlan& p, const int64_t* s_line, int tile) {
+  const int tiles = (p.rows + kWideRows - 1) / kWideRows, each = (tiles + kThreads - 1) / kThreads, at = tile / each;
+  TileSpan t{at > 0 ? s_line[at - 1] : 0, 0};
+  if (each == 1) {
+    t.blocks = static_cast<int>(s_line[at] - t.x);
+    return t;
+  }
+  for (int i = at * each; i < tile; ++i) t.x += tile_blocks(a, p, i);
+  t.blocks = tile_blocks(a, p, tile);
+  return t;
+}
+// The tile that block x lies in.
+template <int kThreads>
+__device__ __forceinline__ int tile_at(const KvAttentionArgs& a, const SeqPlan& p, const int64_t* s_line, int64_t x) {
+  const int tiles = (p.rows + kWideRows - 1) / kWideRows, each = (tiles + kThreads - 1) / kThreads;
+  int at = 0;
+#pragma unroll
+  for (int o = 512; o > 0; o >>= 1)
+    if (at + o < kThreads && s_line[at + o - 1] <= x) at += o;
+  int tile = at * each;
+  if (each == 1) return tile;
+  for (int64_t y = at > 0 ? s_line[at - 1] : 0;; ++tile) {
+    y += tile_blocks(a, p, tile);
+    if (y > x || tile + 1 >= tiles) return tile;
+  }
+}
+// The line of `blocks` in `ranges`: range r is [cut(r), cut(r + 1)), none empty.
+struct Cuts {
+  int64_t blocks;
+  int ranges;
+  int64_t whole;
+  int rest;              // blocks = whole * ranges + rest
+  __device__ __forceinline__ Cuts(int64_t blocks, int most)
+      : blocks(blocks), ranges(static_cast<int>(min(blocks, static_cast<int64_t>(most)))) {
+    whole = blocks >> 31 == 0 ? static_cast<int>(blocks) / ranges : blocks / ranges;
+    rest = static_cast<int>(blocks - whole * ranges);
+  }
+  __device__ __forceinline__ int64_t cut(int r) const {
+    r = min(r, ranges);
+    return whole * r + rest * r / ranges;   // ranges^2 stays below 2^31
+  }
+  __device__ __forceinline__ int range_of(int64_t x) const {
+    const int64_t n = (x + 1) * ranges - 1;
+    return static_cast<int>(blocks >> 20 == 0 ? static_cast<int>(n) / static_cast<int>(blocks) : n / blocks);   // ranges < 2^11
+  }
 };
 
 __device__ __forceinline__ float ex2(float x) {
