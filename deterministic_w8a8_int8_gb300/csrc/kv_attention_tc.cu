@@ -53,12 +53,12 @@ template <int D>
 struct Tc {
   static constexpr int kKeys = D == 256 ? 64 : 128;            // keys of a block
   static constexpr int kUnits = kKeys / 16;
-  static constexpr int kCols = 512;                            // S twice and O
+  static constexpr int kCols = 512;                            // S twice, O, P twice
   static constexpr int kQ = kWideRows * D * 2, kK = kKeys * D * 2, kV = kKeys * D * 2;
   static constexpr int kBytes = kQ + 2 * (kK + kV) + 1024;     // operands start on 1024-byte boundaries
   static constexpr int kItems = kKeys / 8 * (D / 16);          // 8 keys x 16 channels, one a thread
   static_assert(kItems <= kSide, "an item a thread");
-  static_assert(2 * kKeys + D <= kCols, "tensor memory");
+  static_assert(3 * kKeys + D <= kCols, "tensor memory");
 };
 
 // One answer for the warp, whose lanes are together again afterwards.
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ float s_max[kConvWarps];                        // largest value scale of a warp's pages
   __shared__ int s_bad[kConvWarps];                          // an invalid one among them
   __shared__ float s_unit[kWideRows];                        // a row's scale
-  __shared__ float s_top[2][2][kWideRows], s_l[kWideRows];   // the halves' maxima (by the block's parity); one half's sum
+  __shared__ float s_top[2][2][kWideRows], s_l[kWideRows];   // the halves' maxima, exchanged in turn; one half's sum
   __shared__ float s_ks[kUnitSlots][U], s_vr[kUnitSlots][U];
   // completions: K, V converted; scales in place; S formed (K free); P formed; O added to (V, P free); queries; the end
   __shared__ __align__(8) uint64_t s_bar[6 * 2 + kUnitSlots + 2];
@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < blocks; ++j) {
         const uint32_t g = g0 + j, ph = (g >> 1) & 1;
         if (!is_v) {
-          // Q K^T of block g - 2 is complete: so the output of block g - 4 is
-          // (its P lay where that S went), and the units' slot is free
+          // Q K^T of block g - 2 is complete: it was issued after P of block
+          // g - 4 was formed, so the units' slot is free
           wait(bar_kfree(g), ph ^ 1u, &s_abort);
           if (has_unit) {
             s_ks[g & (kUnitSlots - 1)][ct] = scales.x;
@@ -336,9 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id_s = tc::idesc_f16_f32(KB), id_o = tc::idesc_f16_f32(D);
       const uint64_t qd = tc::smem_desc_sw128(smem_u32(s_q));
       bool ok = blocks == 0 || wait(bar_q, items & 1u, &s_abort);
-      auto issue_scores = [&](uint32_t g) {       // S of block g, into its buffer
+      auto issue_scores = [&](uint32_t g) {       // S of block g; block g - 2's was read: its P was waited for
         ok = ok && wait(bar_k(g), (g >> 1) & 1, &s_abort);
-        ok = ok && wait(bar_o(g), ((g >> 1) & 1) ^ 1u, &s_abort);   // P of block g - 2 was read there
         if (ok) {
           tc::tc_fence_after();
           const uint64_t kd = tc::smem_desc_sw128(smem_u32(s_k + (g & 1) * C::kK));
@@ -363,10 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
           tc::tc_fence_after();
           const uint64_t vd = tc::smem_desc_sw128(smem_u32(s_v + (g & 1) * C::kV));
-          const uint32_t pt = tmem + (g & 1) * KB;
+          const uint32_t pt = tmem + 2 * KB + D + (g & 1) * (KB / 2);
 #pragma unroll
           for (int k = 0; k < KB / 16; ++k)
-            mma_ta_if(lead, tmem + 2 * KB, pt + k / UH * (KB / 2) + k % UH * 8, vd + (k >> 2) * (D * 8) + 2 * (k & 3), id_o,
+            mma_ta_if(lead, tmem + 2 * KB, pt + k * 8, vd + (k >> 2) * (D * 8) + 2 * (k & 3), id_o,
                       (j | k) != 0 ? 1u : 0u);
           if (lead) tc::tc_commit(bar_o(g));
         }
@@ -427,108 +426,99 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t row_hi = keys.hi(r), my_lo = keys.lo(row_hi), my_hi = min(row_hi, k_end);
       const int32_t all_lo = keys.a_lo, all_hi = min(keys.a_hi, k_end);   // the keys that every row sees here
       float m = -INFINITY, l = 0.0f;
+      int swaps = 0;
       for (int j = 0; j < blocks; ++j) {
         const uint32_t g = g0 + j;
         wait(bar_u(g), (g / kUnitSlots) & 1, &s_abort);
         wait(bar_s(g), (g >> 1) & 1, &s_abort);
         tc::tc_fence_after();
-        const uint32_t t_s = t_lane + (g & 1) * KB + half * (KB / 2);
+        const uint32_t t_s = t_lane + (g & 1) * KB + half * (KB / 2), t_p = t_lane + 2 * KB + D + (g & 1) * (KB / 2) + half * (KB / 4);
         const int32_t key0 = k_begin + j * KB, my_key = key0 + half * (KB / 2);
         // some row does not see all of the block, or the next piece has its end
         const bool edge = key0 < all_lo || key0 + KB > all_hi;
         const float* ks = s_ks[g & (kUnitSlots - 1)] + half * UH;
         const float* vs = s_vr[g & (kUnitSlots - 1)] + half * UH;
-        float top = -INFINITY;
-        // rolled, and blocks with masked scores apart: three kinds of warps share the instruction cache
-        auto pass_a = [&](auto masked) {
+        wait(bar_o(g), ((g >> 1) & 1) ^ 1u, &s_abort);   // P of block g - 2 was read
+        // Probabilities against the reference at hand; again against the row's
+        // maximum where that stands too far above it (in a first block always)
+        for (;;) {
+          const float base = m == -INFINITY ? 0.0f : m - kShift;
+          float top = -INFINITY, sum = 0.0f;
+          // rolled, and blocks with masked scores apart: three kinds of warps share the instruction cache
+          auto pass = [&](auto masked) {
 #pragma unroll 1
-          for (int u = 0; u < UH; u += 2) {
-            uint32_t x[2][16];
-            tc::tmem_ld16(t_s + u * 16, x[0]);
-            tc::tmem_ld16(t_s + u * 16 + 16, x[1]);
-            tc::tmem_wait_ld();
-            if constexpr (decltype(masked)::value) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const int32_t key = my_key + u * 16 + e;
-                if (key < my_lo || key >= my_hi) x[e >> 4][e & 15] = 0xff800000u;   // -inf
-              }
-            }
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              float t0 = __uint_as_float(x[v][0]), t1 = __uint_as_float(x[v][1]);
-#pragma unroll
-              for (int e = 2; e < 16; e += 2) {
-                t0 = fmaxf(t0, __uint_as_float(x[v][e]));
-                t1 = fmaxf(t1, __uint_as_float(x[v][e + 1]));
-              }
-              t0 = fmaxf(t0, t1);
-              if (t0 > -INFINITY) top = fmaxf(top, t0 * (ks[u + v] * unit));
-            }
-          }
-        };
-        if (edge) {
-          pass_a(std::true_type{});
-        } else {
-          pass_a(std::false_type{});
-        }
-        s_top[g & 1][half][r] = top;
-        named_barrier(1 + (warp & 3), 64);
-        top = fmaxf(top, s_top[g & 1][half ^ 1][r]);
-        const float old = m;
-        if (top > m + kSlack || m == -INFINITY) m = top;
-        const float al = old == m ? 1.0f : ex2(old - m);   // old = -inf: nothing to keep
-        if (__any_sync(0xffffffffu, al != 1.0f) && j > 0) {
-          wait(bar_o(g - 1), ((g - 1) >> 1) & 1, &s_abort);
-          tc::tc_fence_after();
-#pragma unroll 1
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t o[16];
-            tc::tmem_ld16(t_o + i * 16, o);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-            tc::tmem_st16(t_o + i * 16, o);
-          }
-        }
-        l *= al;
-        const float base = m == -INFINITY ? 0.0f : m - kShift;
-        auto pass_b = [&](auto masked) {
-#pragma unroll 1
-          for (int u = 0; u < UH; u += 2) {
-            uint32_t x[2][16], pk[16];
-            tc::tmem_ld16(t_s + u * 16, x[0]);
-            tc::tmem_ld16(t_s + u * 16 + 16, x[1]);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              const float f = ks[u + v] * unit, vf = vs[u + v];
-              float q[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) q[e] = ex2(__fmaf_rn(__uint_as_float(x[v][e]), f, -base));
+            for (int u = 0; u < UH; u += 2) {
+              uint32_t x[2][16], pk[16];
+              tc::tmem_ld16(t_s + u * 16, x[0]);
+              tc::tmem_ld16(t_s + u * 16 + 16, x[1]);
+              tc::tmem_wait_ld();
               if constexpr (decltype(masked)::value) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const int32_t key = my_key + (u + v) * 16 + e;
-                  if (key < my_lo || key >= my_hi) q[e] = 0.0f;
+                for (int e = 0; e < 32; ++e) {
+                  const int32_t key = my_key + u * 16 + e;
+                  if (key < my_lo || key >= my_hi) x[e >> 4][e & 15] = 0xff800000u;   // -inf
                 }
               }
-              float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                l0 += q[e];
-                l1 += q[e + 1];
-                pk[v * 8 + e / 2] = half2_bits(q[e] * vf, q[e + 1] * vf);
+              for (int v = 0; v < 2; ++v) {
+                const float f = ks[u + v] * unit, vf = vs[u + v];
+                float t0 = __uint_as_float(x[v][0]), t1 = __uint_as_float(x[v][1]), q[16];
+#pragma unroll
+                for (int e = 2; e < 16; e += 2) {
+                  t0 = fmaxf(t0, __uint_as_float(x[v][e]));
+                  t1 = fmaxf(t1, __uint_as_float(x[v][e + 1]));
+                }
+                t0 = fmaxf(t0, t1);
+                if (t0 > -INFINITY) top = fmaxf(top, t0 * f);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) q[e] = ex2(__fmaf_rn(__uint_as_float(x[v][e]), f, -base));
+                if constexpr (decltype(masked)::value) {
+#pragma unroll
+                  for (int e = 0; e < 16; ++e)
+                    if (x[v][e] == 0xff800000u) q[e] = 0.0f;   // with f = 0 too
+                }
+                float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                  l0 += q[e];
+                  l1 += q[e + 1];
+                  pk[v * 8 + e / 2] = half2_bits(q[e] * vf, q[e + 1] * vf);
+                }
+                sum += l0 + l1;
               }
-              l += l0 + l1;
+              tc::tmem_st16(t_p + u * 8, pk);
             }
-            tc::tmem_st16(t_s + u * 8, pk);   // over scores that this thread has read
+          };
+          if (edge) {
+            pass(std::true_type{});
+          } else {
+            pass(std::false_type{});
           }
-        };
-        if (edge) {
-          pass_b(std::true_type{});
-        } else {
-          pass_b(std::false_type{});
+          s_top[swaps & 1][half][r] = top;
+          named_barrier(1 + (warp & 3), 64);
+          top = fmaxf(top, s_top[swaps & 1][half ^ 1][r]);
+          ++swaps;
+          const bool far = top > m + kSlack;    // m = -inf: nothing seen yet
+          if (!__any_sync(0xffffffffu, far)) {
+            l += sum;
+            break;
+          }
+          const float al = far ? ex2(m - top) : 1.0f;
+          if (far) m = top;
+          l *= al;
+          if (j > 0) {
+            wait(bar_o(g - 1), ((g - 1) >> 1) & 1, &s_abort);
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+              uint32_t o[16];
+              tc::tmem_ld16(t_o + i * 16, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+              tc::tmem_st16(t_o + i * 16, o);
+            }
+          }
         }
         tc::tmem_wait_st();
         tc::tc_fence_before();
