@@ -66,23 +66,12 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
   return __all_sync(0xffffffffu, tc::mbar_wait_bounded(bar, parity, abort_flag, kWaitNs, &g_kv_status,
                                                        PRISM_DEVSTATUS_WAIT_TIMEOUT));
 }
-// tc::tc_mma and tc::tc_mma_ta of the lane with `lead`, in code that the whole
-// warp runs.
-__device__ __forceinline__ void mma_if(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, l;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 l, %5, 0;\n"
-      " @l tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ta_if(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, l;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 l, %5, 0;\n"
-      " @l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
-      : "memory");
+// True in one lane of the warp, in a way that lets the compiler issue the
+// tensor instructions of that lane from uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
 }
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -331,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kSoftWarps + kConvWarps) {
       // ============================ issuer ==================================
-      // the whole warp forms the descriptors (uniform registers), one lane issues
-      const uint32_t lead = lane == 0 ? 1u : 0u;
+      // the whole warp forms the descriptors, one lane issues
+      const bool lead = elect_one();
       const uint32_t id_s = tc::idesc_f16_f32(KB), id_o = tc::idesc_f16_f32(D);
       const uint64_t qd = tc::smem_desc_sw128(smem_u32(s_q));
       bool ok = blocks == 0 || wait(bar_q, items & 1u, &s_abort);
@@ -342,11 +331,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tc_fence_after();
           const uint64_t kd = tc::smem_desc_sw128(smem_u32(s_k + (g & 1) * C::kK));
           const uint32_t dt = tmem + (g & 1) * KB;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_if(lead, dt, qd + (k >> 2) * (kWideRows * 8) + 2 * (k & 3), kd + (k >> 2) * (KB * 8) + 2 * (k & 3), id_s,
-                   k != 0 ? 1u : 0u);
           if (lead) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              tc::tc_mma(dt, qd + (k >> 2) * (kWideRows * 8) + 2 * (k & 3), kd + (k >> 2) * (KB * 8) + 2 * (k & 3), id_s,
+                         k != 0 ? 1u : 0u);
             tc::tc_commit(bar_s(g));
             tc::tc_commit(bar_kfree(g));
           }
@@ -363,11 +352,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tc_fence_after();
           const uint64_t vd = tc::smem_desc_sw128(smem_u32(s_v + (g & 1) * C::kV));
           const uint32_t pt = tmem + 2 * KB + D + (g & 1) * (KB / 2);
+          if (lead) {
 #pragma unroll
-          for (int k = 0; k < KB / 16; ++k)
-            mma_ta_if(lead, tmem + 2 * KB, pt + k * 8, vd + (k >> 2) * (D * 8) + 2 * (k & 3), id_o,
-                      (j | k) != 0 ? 1u : 0u);
-          if (lead) tc::tc_commit(bar_o(g));
+            for (int k = 0; k < KB / 16; ++k)
+              tc::tc_mma_ta(tmem + 2 * KB, pt + k * 8, vd + (k >> 2) * (D * 8) + 2 * (k & 3), id_o, (j | k) != 0 ? 1u : 0u);
+            tc::tc_commit(bar_o(g));
+          }
         }
         __syncwarp();
       }
@@ -617,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   pdl_wait();
   // ---- every instruction in flight completes before the columns are given back
-  if (tid == kSoft + kConv) {   // the issuing thread
+  if (warp == kSoftWarps + kConvWarps && elect_one()) {   // the issuing thread
     tc::tc_commit(bar_end);
     tc::mbar_wait_drain_bounded(bar_end, 0, kWaitNs, &g_kv_status, PRISM_DEVSTATUS_WAIT_TIMEOUT);
   }
