@@ -1,8 +1,10 @@
-"""Build libprism.so in-tree for sm_103a (nvcc only; no cmake, no torch build).
+"""Build libprism.so in-tree for sm_103a (nvcc and gcc; no cmake, no torch build).
 
 Each ``csrc/*.cu`` translation unit is compiled in parallel with
 ``-gencode arch=compute_103a,code=sm_103a`` and linked into
 ``deterministic_w8a8_int8_gb300/libprism.so`` against the shared CUDA runtime.
+``csrc/decode_py.c``, the Python side of the decode-step entry points, becomes
+the extension module ``_decode.so`` beside it (gcc, Python's headers).
 Set ``PRISM_PTXAS_VERBOSE=1`` to print ptxas register and spill reports.
 """
 from __future__ import annotations
@@ -12,6 +14,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libprism.so")
+MODULE_SRC = os.path.join(CSRC, "decode_py.c")
+MODULE_PATH = os.path.join(PKG, "_decode.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -47,10 +52,24 @@ def _deps() -> list[str]:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(MODULE_PATH):
         return False
     t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return all(os.path.getmtime(p) <= t for p in _deps()) and os.path.getmtime(MODULE_PATH) >= max(
+        os.path.getmtime(MODULE_SRC), os.path.getmtime(os.path.join(INCLUDE, "prism.h")))
+
+
+def _build_module() -> None:
+    cc = next((c for c in (os.environ.get("CC"), shutil.which("gcc"), shutil.which("cc")) if c), None)
+    if cc is None:
+        raise RuntimeError("gcc not found")
+    tmp = MODULE_PATH + f".tmp{os.getpid()}"
+    cmd = [cc, "-O2", "-Wall", "-shared", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], MODULE_SRC,
+           "-o", tmp, "-L", PKG, "-lprism", "-lm", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("gcc failed on decode_py.c:\n" + r.stderr)
+    os.replace(tmp, MODULE_PATH)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -83,6 +102,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stderr)
     os.replace(tmp, LIB_PATH)
+    _build_module()
     return LIB_PATH
 
 
