@@ -1,16 +1,17 @@
-"""Build libprism.so in-tree for sm_103a (nvcc and gcc; no cmake, no torch build).
+"""Build libprism.so in-tree for sm_103a (nvcc and g++; no cmake).
 
 Each ``csrc/*.cu`` translation unit is compiled in parallel with
 ``-gencode arch=compute_103a,code=sm_103a`` and linked into
 ``deterministic_w8a8_int8_gb300/libprism.so`` against the shared CUDA runtime.
-``csrc/decode_py.c``, the Python side of the decode-step entry points, becomes
-the extension module ``_decode.so`` beside it (gcc, Python's headers).
+``csrc/decode_py.cpp``, the Python side of the decode-step entry points, becomes
+the extension module ``_decode.so`` beside it (g++; Python's and torch's headers).
 Set ``PRISM_PTXAS_VERBOSE=1`` to print ptxas register and spill reports.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -22,7 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libprism.so")
-MODULE_SRC = os.path.join(CSRC, "decode_py.c")
+MODULE_SRC = os.path.join(CSRC, "decode_py.cpp")
 MODULE_PATH = os.path.join(PKG, "_decode.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -32,6 +33,13 @@ def _nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def _cxx() -> str:
+    for cand in (os.environ.get("CXX"), shutil.which("g++"), shutil.which("c++")):
+        if cand:
+            return cand
+    raise RuntimeError("g++ not found")
 
 
 def _cuda_lib_dir(nvcc: str) -> str:
@@ -59,16 +67,35 @@ def up_to_date() -> bool:
         os.path.getmtime(MODULE_SRC), os.path.getmtime(os.path.join(INCLUDE, "prism.h")))
 
 
-def _build_module() -> None:
-    cc = next((c for c in (os.environ.get("CC"), shutil.which("gcc"), shutil.which("cc")) if c), None)
-    if cc is None:
-        raise RuntimeError("gcc not found")
-    tmp = MODULE_PATH + f".tmp{os.getpid()}"
-    cmd = [cc, "-O2", "-Wall", "-shared", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], MODULE_SRC,
-           "-o", tmp, "-L", PKG, "-lprism", "-lm", "-Wl,-rpath,$ORIGIN"]
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch not found")
+    return spec.submodule_search_locations[0]
+
+
+def _run(what: str, cmd: list[str]) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("gcc failed on decode_py.c:\n" + r.stderr)
+        raise RuntimeError(f"{what} failed:\n{r.stderr}")
+
+
+def _compile_module(nvcc: str) -> str:
+    obj = os.path.join(BUILD_DIR, "decode_py.o")
+    torch_include = os.path.join(_torch_dir(), "include")
+    dirs = [INCLUDE, torch_include, os.path.join(torch_include, "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")]
+    _run("g++ on decode_py.cpp", [_cxx(), "-O2", "-std=c++17", "-fPIC", *(a for d in dirs for a in ("-I", d)),
+                                  "-c", MODULE_SRC, "-o", obj])
+    return obj
+
+
+def _link_module(obj: str, libdir: str) -> None:
+    torch_lib = os.path.join(_torch_dir(), "lib")
+    tmp = MODULE_PATH + f".tmp{os.getpid()}"
+    _run("link of _decode.so", [_cxx(), "-shared", obj, "-o", tmp, "-L", PKG, "-lprism", "-L", torch_lib, "-lc10", "-lc10_cuda",
+                                "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
+                                f"-Wl,-rpath,$ORIGIN:{torch_lib}:{libdir},-rpath-link,{libdir}"])
     os.replace(tmp, MODULE_PATH)
 
 
@@ -92,7 +119,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        module = ex.submit(_compile_module, nvcc)
         objs = list(ex.map(compile_one, srcs))
     libdir = _cuda_lib_dir(nvcc)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
@@ -102,7 +130,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stderr)
     os.replace(tmp, LIB_PATH)
-    _build_module()
+    _link_module(module.result(), libdir)
     return LIB_PATH
 
 

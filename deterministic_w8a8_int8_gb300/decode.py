@@ -17,12 +17,12 @@ import torch
 
 from . import _check, lib
 
-_BF16, _F16, _F32, _I8, _U8, _I32 = (torch.bfloat16, torch.float16, torch.float32, torch.int8, torch.uint8, torch.int32)
+_BF16, _F32, _I8 = torch.bfloat16, torch.float32, torch.int8
 
 lib()   # one loaded library for both bindings; says what to do where it is not built
-from . import _decode  # noqa: E402  (csrc/decode_py.c: checks, outputs and the calls)
+from . import _decode  # noqa: E402  (csrc/decode_py.cpp: checks, outputs and the calls)
 
-_decode.setup(torch.Tensor, _BF16, _F16, _F32, _I8, _U8, _I32, torch.empty, torch._C._cuda_getCurrentRawStream, _check)
+_decode.setup(_check)
 
 
 class KvCache(NamedTuple):

@@ -1,4 +1,4 @@
-"""The Python side of the decode-step entry points (csrc/decode_py.c): what it
+"""The Python side of the decode-step entry points (csrc/decode_py.cpp): what it
 refuses, what it passes on, and that it keeps nothing."""
 import gc
 import sys
