@@ -31,22 +31,24 @@ __device__ __forceinline__ float page_scale(float amax) {
 __device__ __forceinline__ float code_factor(float amax) {
   return amax >= 0x1p-120f ? __fmul_rn(__frcp_rn(amax), 127.0f) : 0.0f;
 }
-__device__ __forceinline__ float max8(const uint4& v, float m) {
+// The larger magnitudes of m's two bf16 halves and the even and odd channels of v.
+__device__ __forceinline__ uint32_t max8(const uint4& v, uint32_t m) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+  for (int i = 0; i < 4; ++i) asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(w[i] & 0x7fff7fffu));
   return m;
+}
+// rint(x f) for |x f| < 2^22 by the addition of 1.5 * 2^23, whose low byte is
+// then the code; |x f| <= 127 (1 + 2^-22), so nothing needs a clamp.
+__device__ __forceinline__ uint32_t code_bits(float x, float f) {
+  return __float_as_uint(__fadd_rn(__fmul_rn(x, f), 12582912.0f));
 }
 __device__ __forceinline__ uint2 codes8(const uint4& v, float f) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t c[2] = {0u, 0u};
+  uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int lo = max(-127, min(127, __float2int_rn(__fmul_rn(bf16_lo(w[i]), f))));
-    const int hi = max(-127, min(127, __float2int_rn(__fmul_rn(bf16_hi(w[i]), f))));
-    c[i >> 1] |= ((static_cast<uint32_t>(lo) & 0xffu) | ((static_cast<uint32_t>(hi) & 0xffu) << 8)) << (16 * (i & 1));
-  }
-  return make_uint2(c[0], c[1]);
+  for (int i = 0; i < 4; ++i) c[i] = __byte_perm(code_bits(bf16_lo(w[i]), f), code_bits(bf16_hi(w[i]), f), 0x0040u);
+  return make_uint2(__byte_perm(c[0], c[1], 0x5410u), __byte_perm(c[2], c[3], 0x5410u));
 }
 
 // NV: 16-byte pieces of a page's bf16 rows per thread.
@@ -81,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     const int n_rows = static_cast<int>(min(static_cast<int64_t>(c.block), after - p0));
     const int32_t page = c.table[s * c.ld_table + first + j];
     uint4 x[NV];
-    float amax = 0.0f;
+    uint32_t most = 0u;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int r = (i * kThreads + tid) >> row_shift;
@@ -92,8 +94,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     const int64_t ph = static_cast<int64_t>(page) * c.H + h;
     const float old_scale = page_ok && n_old > 0 ? scales[ph] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) amax = max8(x[i], amax);
-    auto block_max = [&](float m) {
+    for (int i = 0; i < NV; ++i) most = max8(x[i], most);
+    auto block_max = [&](uint32_t pair) {
+      float m = fmaxf(bf16_lo(pair), bf16_hi(pair));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       __syncthreads();
@@ -104,14 +107,14 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
       for (int w = 1; w < kThreads / 32; ++w) m = fmaxf(m, s_red[w]);
       return m;
     };
-    amax = block_max(amax);
+    float amax = block_max(most);
     int from = n_old;                     // first row whose codes are written
     if (n_old > 0 && page_ok) {
       if (open_page == first && page_scale(amax) <= old_scale) {
         amax = bf16_bits_to_float(static_cast<uint16_t>(float_to_bf16_rne(__fmul_rn(old_scale, 127.0f))));
       } else {                            // the page's earlier rows again
         from = 0;
-        float old = 0.0f;
+        uint32_t old = 0u;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int r = (i * kThreads + tid) >> row_shift;

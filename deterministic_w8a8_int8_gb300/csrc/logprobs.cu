@@ -216,31 +216,28 @@ __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3)
 
   // ---- 1. a part at a time: the thread's maximum and sums
   for (int part = rank; part < parts; part += ctas) {
-    float limit = -INFINITY, ref = 0.0f, s = 0.0f, e = 0.0f, p_max = -INFINITY;
+    float limit = -INFINITY, ref = 0.0f, p_max = -INFINITY;
+    float2 s2 = make_float2(0.0f, 0.0f), e2 = s2;   // of the even and the odd logits
     each(range(part), [&](Piece<F32> p, int) {
       const float m = p.top();
       p_max = fmaxf(p_max, m);
       if (m > limit && fabsf(m) < kFar) {      // the first finite piece, or one far above the reference
         const float to = __fmul_rn(m, kLog2e), d = limit == -INFINITY ? 0.0f : ref - to, f = ex2(d);
-        e = f * __fmaf_rn(s, d, e);
-        s *= f;
+        e2 = mul2(make_float2(f, f), fma2(s2, make_float2(d, d), e2));
+        s2 = mul2(make_float2(f, f), s2);
         ref = to;
         limit = m + kSlack;
       }
       p.lift();
-      float s2 = 0.0f, e2 = 0.0f;
 #pragma unroll
       for (int i = 0; i < kVec; i += 2) {
-        const float y0 = __fmaf_rn(p.get(i), kLog2e, -ref), y1 = __fmaf_rn(p.get(i + 1), kLog2e, -ref);
-        const float q0 = ex2(y0), q1 = ex2(y1);
-        s = __fadd_rn(s, q0);
-        s2 = __fadd_rn(s2, q1);
-        e = __fmaf_rn(q0, y0, e);
-        e2 = __fmaf_rn(q1, y1, e2);
+        const float2 y = fma2(make_float2(p.get(i), p.get(i + 1)), make_float2(kLog2e, kLog2e), make_float2(-ref, -ref));
+        const float2 q = make_float2(ex2(y.x), ex2(y.y));
+        s2 = add2(s2, q);
+        e2 = fma2(q, y, e2);
       }
-      s = __fadd_rn(s, s2);
-      e = __fadd_rn(e, e2);
     });
+    float s = __fadd_rn(s2.x, s2.y), e = __fadd_rn(e2.x, e2.y);
     s_top[part >> log_ctas][tid] = p_max;
     // the group's maximum (128 groups a row), and the warp's reference and sums
     const int g_lanes = 4 * parts;             // lanes of a group

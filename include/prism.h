@@ -547,17 +547,22 @@ int prism_kv_append(const void *k_bf16, int64_t ldk_t, int64_t ldk_h,
  * (causal only).  Query head h reads KV head h / (H_q / H_kv):
  *   out[t, h] = bf16( sum_j softmax_j(sm_scale * q[t, h] . k_j) * v_j )
  *   lse[t, h] = ln sum_j exp(sm_scale * q[t, h] . k_j)
- * A query that sees no key gives 0 and -inf.  Scores, the softmax's maximum
- * and sum, and the weighted sums are binary32; the probabilities enter the
- * tensor cores as binary16 (scaled by 2^12 below the running maximum), the
- * codes exactly.  A sequence's outputs depend on its own queries, keys and
- * lengths only, not on the other sequences of the call.
+ * A query that sees no key gives 0 and -inf.  Scores, the softmax's reference
+ * and sum, and the weighted sums are binary32; the codes enter the tensor
+ * cores exactly, the queries as binary16 of the row's largest channel (bf16
+ * channels far below it lose bits), the probabilities as binary16 scaled so
+ * that the largest lie between 2^9 and 2^15.  A sequence's outputs depend on
+ * its own queries, keys and lengths (and on H_kv) only, not on the other
+ * sequences of the call.
  *   q_bf16, out_bf16  [T, H_q, D] bf16, strides as in prism_kv_append
  *   lse               [T, H_q] float32 dense, or NULL
  *   cu_q              [S + 1] int32 query offsets; NULL: one query each
  *                     (T == S).  Rows of no sequence are not written.
  *   max_q             the most queries of one sequence (1 <= max_q); a
- *                     sequence with more sets PRISM_DEV_ERR_SEQ_RANGE
+ *                     sequence with more sets PRISM_DEV_ERR_SEQ_RANGE.
+ *                     Sequences of more than 32 rows (queries x H_q / H_kv)
+ *                     run on tcgen05, whose bounded waits report through
+ *                     prism_device_status
  *   workspace         prism_kv_attention_workspace_bytes(...) bytes, 256-byte
  *                     aligned, any contents
  * A sequence with a malformed length or offsets, or a page index outside
@@ -587,8 +592,8 @@ int prism_kv_attention(const void *q_bf16, int64_t ldq_t, int64_t ldq_h,
  *   out[m, n] = bf16( a_scale[m] * sum_k q[m, k] w[n, k] + residual[m, n] )
  * The sums over a group, sum_k q * code and sum_k q, are exact integers; they
  * are scaled and added over the groups in binary32, in an order that depends
- * on K and group alone.  Meant for the few token rows of decode steps; more
- * rows are taken 64 at a time.
+ * on N, K and group alone.  Meant for the few token rows of decode steps; more
+ * rows are taken 64 at a time (M <= 64 * 65535).
  *   q, ldq         [M, K] int8 codes in [-127, 127], a_scale [M] float32
  *                  (prism_quant_act); ldq % 16 == 0, 16-byte aligned
  *   w4, ldw4       [N, K / 2] packed bytes as in prism_w4a8_linear
