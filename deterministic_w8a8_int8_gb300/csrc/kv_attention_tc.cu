@@ -433,7 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // maximum where that stands too far above it (in a first block always)
         for (;;) {
           const float base = m == -INFINITY ? 0.0f : m - kShift;
-          float top = -INFINITY, sum = 0.0f;
+          float top = -INFINITY;
+          float2 sum = make_float2(0.0f, 0.0f);
           // rolled, and blocks with masked scores apart: three kinds of warps share the instruction cache
           auto pass = [&](auto masked) {
 #pragma unroll 1
@@ -461,20 +462,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 t0 = fmaxf(t0, t1);
                 if (t0 > -INFINITY) top = fmaxf(top, t0 * f);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) q[e] = ex2(__fmaf_rn(__uint_as_float(x[v][e]), f, -base));
+                for (int e = 0; e < 16; e += 2) {
+                  const float2 y = fma2(make_float2(__uint_as_float(x[v][e]), __uint_as_float(x[v][e + 1])),
+                                        make_float2(f, f), make_float2(-base, -base));
+                  q[e] = ex2(y.x);
+                  q[e + 1] = ex2(y.y);
+                }
                 if constexpr (decltype(masked)::value) {
 #pragma unroll
                   for (int e = 0; e < 16; ++e)
                     if (x[v][e] == 0xff800000u) q[e] = 0.0f;   // with f = 0 too
                 }
-                float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
-                  l0 += q[e];
-                  l1 += q[e + 1];
-                  pk[v * 8 + e / 2] = half2_bits(q[e] * vf, q[e + 1] * vf);
+                  const float2 two = make_float2(q[e], q[e + 1]), w = mul2(two, make_float2(vf, vf));
+                  sum = add2(sum, two);
+                  pk[v * 8 + e / 2] = half2_bits(w.x, w.y);
                 }
-                sum += l0 + l1;
               }
               tc::tmem_st16(t_p + u * 8, pk);
             }
@@ -490,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++swaps;
           const bool far = top > m + kSlack;    // m = -inf: nothing seen yet
           if (!__any_sync(0xffffffffu, far)) {
-            l += sum;
+            l += sum.x + sum.y;
             break;
           }
           const float al = far ? ex2(m - top) : 1.0f;

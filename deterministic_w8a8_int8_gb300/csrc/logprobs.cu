@@ -156,7 +156,7 @@ __device__ __forceinline__ Piece<F32> load_piece(const void* row, int64_t at, in
 }
 
 template <bool F32>
-__global__ void __launch_bounds__(kThreads, F32 ? 2 : 3)
+__global__ void __launch_bounds__(kThreads, 2)
     logprobs_kernel(const __grid_constant__ LogprobArgs a, int log_parts, int log_ctas) {
   __shared__ __align__(16) float s_max[kGroups];
   __shared__ __align__(16) u64 s_list[kList];
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3)
   };
   // f(piece, number) over the thread's pieces, kAhead of them in flight
   auto each = [&](const Range& g, auto f) {
-    constexpr int kWords = F32 ? 2 : 1, kAhead = 4;
+    constexpr int kWords = F32 ? 2 : 1, kAhead = F32 ? 4 : 8;
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + g.first * (F32 ? 4 : 2));
     const int64_t step = stride * (F32 ? 4 : 2) / 16;
     for (int i0 = 0; i0 < g.whole; i0 += kAhead) {
