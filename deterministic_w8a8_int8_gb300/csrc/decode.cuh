@@ -74,6 +74,8 @@ struct W4gArgs {
   int32_t group;
 };
 cudaError_t launch_w4g(const W4gArgs& a, cudaStream_t stream);
+// Device status bits of its bounded waits.
+cudaError_t read_and_clear_w4g_status(uint32_t* out);
 
 struct LogprobArgs {
   const void* logits;

@@ -15,24 +15,32 @@
 // A CTA owns 64 channels (up to 8 rows) or 128 and one slice of K; the CTAs of a
 // cluster hold the slices of one channel tile and add their sums through
 // distributed shared memory in slice order.  Each warp streams its weight rows
-// through a private ring of cp.async copies (128 bytes of a row a step); the
-// activations are widened once per CTA into shared memory, in the order that the
+// through a private ring (128 bytes of a row a step); the activations are widened once per CTA into shared memory, in the order that the
 // weight words want.
 //
 // Up to 8 rows the issue slots bound it: a weight word costs nine instructions
 // for eight codes, and half of the slots are taken (deeper rings change nothing:
 // 5120 x 34816, one row, 3, 4, 5 stages: 25.4, 26.7, 27.6 us, 3.5 TB/s of weights).
 // With more rows the instructions themselves (608 TFLOP/s at best) take 40 % of
-// the time and the slots 45 %: 37 rows of 5120 x 34816 take 69 us.  The same on
+// the time and the slots 45 %: 37 rows of 5120 x 34816 take 64.7 us.  The same on
 // tcgen05 (weights widened into swizzled shared memory, group sums read back from
 // tensor memory) took 75 us, and 50 us against 36 with 12 rows: every weight then
 // passes through shared memory twice.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <type_traits>
 
 #include "decode.cuh"
+#include "tc_common.cuh"
 
 namespace prism {
+
+__device__ uint32_t g_w4g_status = 0;
+
 namespace {
+
+constexpr unsigned long long kWaitNs = 2000000000ull;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kCh = kWarps * 16;   // of a CTA with up to 8 rows; its channels
 constexpr int kStageUnits = 8;            // a unit is 32 input channels: 16 bytes of a weight row
@@ -336,8 +344,48 @@ constexpr int kWideWarps = 4, kSideWarps = 2;
 constexpr int kWideThreads = (kWideWarps + kSideWarps) * 32, kSide = kSideWarps * 32;
 constexpr int kWideStages = 3;
 constexpr int kWideCh = kWideWarps * 32;
-constexpr int kWideStage = 32 * kPitch;
+constexpr int kWidePitch = kStageUnits * 16, kWideStage = 32 * kWidePitch;
 enum : int { kFull = 1, kEmpty = 3 };
+
+// A warp's weight rows on their way to shared memory: boxes of 32 rows by
+// kStageUnits units, a stage each, their 16-byte pieces swizzled (piece u of row
+// r at u ^ (r & 7)); rows past N and units past K read as zero.  One lane asks
+// for a stage: as cp.async copies of all lanes it cost a fifth of the warp's time
+// (37 rows of 5120 x 34816: 69 us so, 64.7 us with boxes; with up to 8 rows boxes
+// are no faster: one row 25.4 and 26.3 us).
+struct Ring {
+  const CUtensorMap* map;
+  uint32_t stage0, bar0;          // shared addresses: stages (1024-byte boundaries), mbarriers
+  int32_t x0, y;
+  int units;
+  __device__ __forceinline__ Ring(const CUtensorMap* map, uint32_t stages, uint32_t bars, int64_t n0, int u_begin, int units,
+                                  int lane)
+      : map(map), stage0(stages), bar0(bars), x0(u_begin * 16), y(static_cast<int32_t>(n0)), units(units) {
+    if (lane < kWideStages) tc::mbar_init(bar0 + 8 * lane, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
+  }
+  // the stage that st takes the place of has been read by the whole warp
+  __device__ __forceinline__ void issue(int st, int lane) const {
+    if (st * kStageUnits >= units || lane != 0) return;
+    const uint32_t bar = bar0 + 8 * (st % kWideStages);
+    tc::mbar_expect_tx(bar, kWideStage);
+    tc::tma_load_2d(stage0 + (st % kWideStages) * kWideStage, map, x0 + st * kWidePitch, y, bar);
+  }
+  // Bounded: where it runs out, the status bit says that the outputs are not valid.
+  __device__ __forceinline__ void wait(int st, volatile int* abort_flag) const {
+    tc::mbar_wait_bounded(bar0 + 8 * (st % kWideStages), (st / kWideStages) & 1, abort_flag, kWaitNs, &g_w4g_status,
+                          PRISM_DEVSTATUS_WAIT_TIMEOUT);
+    __syncwarp();
+  }
+  // After a wait that ran out: the boxes still under way land before the CTA ends.
+  __device__ __forceinline__ void drain() const {
+    const int stages = (units + kStageUnits - 1) / kStageUnits;
+    for (int st = max(0, stages - kWideStages); st < stages; ++st)
+      tc::mbar_wait_drain_bounded(bar0 + 8 * (st % kWideStages), (st / kWideStages) & 1, kWaitNs, &g_w4g_status,
+                                  PRISM_DEVSTATUS_WAIT_TIMEOUT);
+  }
+};
 
 __device__ __forceinline__ void named_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kWideThreads) : "memory"); }
 __device__ __forceinline__ void named_arrive(int id) {
@@ -352,16 +400,22 @@ struct Wide {
   static constexpr int kB = CU * T * 64, kScale = kWideCh * GC * 2, kSum = GC * T * 4;
   static constexpr int kBuffer = kB + (kOff ? 2 * kScale + kSum : kScale);
   static constexpr int kRing = kWideWarps * kWideStages * kWideStage;
-  static constexpr int kBytes = kRing + 2 * kBuffer;
+  static constexpr int kBytes = 1024 + kRing + 2 * kBuffer;
   static_assert(kBytes >= T * kWideCh * 4, "the CTA's sums at the end");
   static_assert(2 * (kBytes + 1024) <= 227 * 1024, "two CTAs an SM");
 };
 
 template <int T, int GU, bool kOff>
-__global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_constant__ W4gArgs a, int slices, int slice_units) {
+__global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_constant__ W4gArgs a, const __grid_constant__ CUtensorMap w_map, int slices,
+                                                                   int slice_units) {
   using C = Wide<T, GU, kOff>;
   constexpr int NT = C::NT, CU = C::CU, GC = C::GC;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t s_bar[kWideWarps * kWideStages];
+  __shared__ int s_abort;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);   // the ring's boxes start on 1024-byte boundaries
+  if (threadIdx.x == 0) s_abort = 0;
+  __syncthreads();
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -456,32 +510,19 @@ __global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_
     }
   } else {
     // ============ contraction ============
-    // this warp's weight ring: 32 rows x 8 units a stage, 16-byte piece i * 32 +
-    // lane.  Rows past N repeat the last one and are not stored.
-    const uint32_t ring = smem_u32(smem) + warp * kWideStages * kWideStage + (lane >> 3) * kPitch + (lane & 7) * 16;
-    const int64_t row0 = n_cta + warp * 32 + (lane >> 3);
-    const uint8_t* wp = a.w4 + (static_cast<int64_t>(u_begin) + (lane & 7)) * 16;
-    auto issue = [&](int st) {
-      if (st * kStageUnits + (lane & 7) < units) {
-        const uint32_t dst = ring + (st % kWideStages) * kWideStage;
+    const Ring ring(&w_map, smem_u32(smem) + warp * kWideStages * kWideStage, smem_u32(s_bar) + warp * kWideStages * 8,
+                    n_cta + warp * 32, u_begin, units, lane);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          cp_async_16(dst + 4 * i * kPitch, wp + min(row0 + 4 * i, a.N - 1) * a.ldw4 + st * (kStageUnits * 16), 16);
-      }
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int st = 0; st < kWideStages - 1; ++st) issue(st);
+    for (int st = 0; st < kWideStages - 1; ++st) ring.issue(st, lane);
     float acc[2][NT][4];
     for (int c = 0; c < chunks; ++c) {
       constexpr int kPer = kStageUnits / CU;
       const int st = c / kPer;
       if (c % kPer == 0) {
-        issue(st + kWideStages - 1);
-        cp_async_wait<kWideStages - 1>();
-        __syncwarp();
+        ring.issue(st + kWideStages - 1, lane);
+        ring.wait(st, &s_abort);
       }
-      const uint8_t* wb = smem + (warp * kWideStages + st % kWideStages) * kWideStage + (c % kPer) * (CU * 16) + lr * kPitch + lc * 4;
+      const uint8_t* wb = smem + (warp * kWideStages + st % kWideStages) * kWideStage + lr * kWidePitch + lc * 4;
       named_sync(kFull + (c & 1));
       const uint8_t* buf = buffer(c);
       const uint2* s_b = reinterpret_cast<const uint2*>(buf) + lr * 4 + lc;
@@ -494,8 +535,9 @@ __global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_
         uint32_t ae[2][4], ao[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(wb + i * 16 * kPitch + u * 16);
-          const uint32_t w1 = *reinterpret_cast<const uint32_t*>(wb + (i * 16 + 8) * kPitch + u * 16);
+          const uint8_t* at = wb + i * 16 * kWidePitch + (((c % kPer * CU + u) * 16) ^ (lr * 16));
+          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(at);
+          const uint32_t w1 = *reinterpret_cast<const uint32_t*>(at + 8 * kWidePitch);
           ae[i][0] = even_codes(w0), ae[i][1] = even_codes(w1), ae[i][2] = even_codes(w0 >> 8), ae[i][3] = even_codes(w1 >> 8);
           ao[i][0] = odd_codes(w0), ao[i][1] = odd_codes(w1), ao[i][2] = odd_codes(w0 >> 8), ao[i][3] = odd_codes(w1 >> 8);
         }
@@ -549,7 +591,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_
       if (c + 2 < chunks) named_arrive(kEmpty + (c & 1));
       __syncwarp();   // the stage is free for the copy that the next turn issues
     }
-    cp_async_wait<0>();
+    if (*static_cast<volatile int*>(&s_abort) != 0) ring.drain();
   }
 
   __syncthreads();
@@ -564,6 +606,24 @@ __global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_
           s_y[(t * 8 + 2 * lc + (e & 1)) * kWideCh + warp * 32 + i * 16 + lr + 8 * (e >> 1)] = y[i][t][e];
   }
   join_slices<kWideCh>(a, smem_u32(smem), rank, slices, m0, T, n_cta, tid, kWideThreads);
+}
+
+// The packed weights in the wide kernel's boxes.
+cudaError_t weight_map(CUtensorMap* m, const W4gArgs& a) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(e == cudaSuccess && q == cudaDriverEntryPointSuccess ? f : nullptr);
+  }();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.K / 2), static_cast<cuuint64_t>(a.N)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.ldw4)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kWidePitch), 32}, step[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.w4), dims, strides, box, step,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <class... P, class... A>
@@ -605,8 +665,11 @@ cudaError_t launch_gu(const W4gArgs& a, cudaStream_t stream) {
   };
   auto wide = [&](auto t) {
     constexpr int T = decltype(t)::value;
+    CUtensorMap map;
+    const cudaError_t e = weight_map(&map, a);
+    if (e != cudaSuccess) return e;
     return launch_slices(w4g_wide_kernel<T, GU, kOff>, kWideCh, kWideThreads, Wide<T, GU, kOff>::kBytes, slices, a, stream,
-                         slices, slice_units);
+                         map, slices, slice_units);
   };
   if (a.M <= 1) return few(std::integral_constant<int, 1>{});
   if (a.M <= 2) return few(std::integral_constant<int, 2>{});
@@ -629,6 +692,18 @@ cudaError_t launch_off(const W4gArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_w4g(const W4gArgs& a, cudaStream_t stream) {
   return a.offset != nullptr ? launch_off<true>(a, stream) : launch_off<false>(a, stream);
+}
+
+cudaError_t read_and_clear_w4g_status(uint32_t* out) {
+  uint32_t v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_w4g_status, sizeof v);
+  if (e != cudaSuccess) return e;
+  if (v != 0) {
+    const uint32_t zero = 0;
+    e = cudaMemcpyToSymbol(g_w4g_status, &zero, sizeof zero);
+  }
+  *out = v;
+  return e;
 }
 
 }  // namespace prism

@@ -280,11 +280,12 @@ int prism_w8a8_kernel_kind(int64_t M, int64_t N, int64_t K) { return prism::line
 
 int prism_device_status(uint32_t* flags) {
   if (flags == nullptr) return PRISM_ERR_INVALID_ARG;
-  uint32_t a = 0, b = 0, c = 0;
+  uint32_t a = 0, b = 0, c = 0, d = 0;
   int st = prism::record_cuda(prism::read_and_clear_kernel_error(&a));
   if (st == PRISM_OK) st = prism::record_cuda(prism::read_and_clear_f16_status(&b));
   if (st == PRISM_OK) st = prism::record_cuda(prism::read_and_clear_kv_status(&c));
-  *flags = a | b | c;
+  if (st == PRISM_OK) st = prism::record_cuda(prism::read_and_clear_w4g_status(&d));
+  *flags = a | b | c | d;
   return st;
 }
 

@@ -593,7 +593,9 @@ int prism_kv_attention(const void *q_bf16, int64_t ldq_t, int64_t ldq_h,
  * The sums over a group, sum_k q * code and sum_k q, are exact integers; they
  * are scaled and added over the groups in binary32, in an order that depends
  * on N, K and group alone.  Meant for the few token rows of decode steps; more
- * rows are taken 64 at a time (M <= 64 * 65535).
+ * rows are taken 64 at a time (M <= 64 * 65535).  With more than 8 rows the
+ * weights arrive by tensor copies, whose bounded waits report through
+ * prism_device_status.
  *   q, ldq         [M, K] int8 codes in [-127, 127], a_scale [M] float32
  *                  (prism_quant_act); ldq % 16 == 0, 16-byte aligned
  *   w4, ldw4       [N, K / 2] packed bytes as in prism_w4a8_linear
