@@ -22,7 +22,7 @@
 // for eight codes, and half of the slots are taken (deeper rings change nothing:
 // 5120 x 34816, one row, 3, 4, 5 stages: 25.4, 26.7, 27.6 us, 3.5 TB/s of weights).
 // With more rows the instructions themselves (608 TFLOP/s at best) take 40 % of
-// the time and the slots 45 %: 37 rows of 5120 x 34816 take 64.7 us.  The same on
+// the time and the slots 45 %: 37 rows of 5120 x 34816 take 61 us.  The same on
 // tcgen05 (weights widened into swizzled shared memory, group sums read back from
 // tensor memory) took 75 us, and 50 us against 36 with 12 rows: every weight then
 // passes through shared memory twice.
@@ -337,15 +337,15 @@ __global__ void __launch_bounds__(kThreads, 4)
 
 // ---- 9 and more rows.  A CTA owns 128 channels: four warps of 32 channels, so
 // that a B fragment read from shared memory serves two instructions' rows, and
-// two warps that lay chunks of CU units of activations (and their scales) into
+// four warps that lay chunks of CU units of activations (and their scales) into
 // one of two buffers while the other is used.  Named barriers pass the buffers
 // on: kFull + b when buffer b is laid out, kEmpty + b when it has been read.
-constexpr int kWideWarps = 4, kSideWarps = 2;
+constexpr int kWideWarps = 4, kSideWarps = 4;       // a warpgroup each
 constexpr int kWideThreads = (kWideWarps + kSideWarps) * 32, kSide = kSideWarps * 32;
 constexpr int kWideStages = 3;
 constexpr int kWideCh = kWideWarps * 32;
 constexpr int kWidePitch = kStageUnits * 16, kWideStage = 32 * kWidePitch;
-enum : int { kFull = 1, kEmpty = 3 };
+enum : int { kFull = 1, kEmpty = 3, kDone = 5 };
 
 // A warp's weight rows on their way to shared memory: boxes of 32 rows by
 // kStageUnits units, a stage each, their 16-byte pieces swizzled (piece u of row
@@ -387,6 +387,18 @@ struct Ring {
   }
 };
 
+// The two warpgroups share the registers that the CTA was launched with: 128 a
+// thread, by the launch bounds.  (Two warps laying out, 168 registers for all:
+// 37 rows of 17408 x 5120 58.7 us, 64 rows of 5120 x 34816 100; four warps and
+// 168 + 88: 55.4 and 96, with spills; 184 + 72: 51.3 and 90.)
+constexpr int kLaunchRegs = 128, kWideRegs = 184, kSideRegs = 72;
+static_assert(kWideWarps * kWideRegs + kSideWarps * kSideRegs <= (kWideWarps + kSideWarps) * kLaunchRegs, "the launch's registers");
+static_assert(2 * kWideThreads * kLaunchRegs <= 65536, "two CTAs an SM");
+template <int n>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n)); }
+template <int n>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n)); }
+
 __device__ __forceinline__ void named_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kWideThreads) : "memory"); }
 __device__ __forceinline__ void named_arrive(int id) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kWideThreads) : "memory");
@@ -427,11 +439,8 @@ __global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_
   const int u_begin = min(rank * slice_units, all_units);
   const int units = min(slice_units, all_units - u_begin), chunks = (units + CU - 1) / CU;
   auto buffer = [&](int c) { return smem + C::kRing + (c & 1) * C::kBuffer; };   // B fragments, scales, offsets, sums of q
-  float y[2][NT][4];
-#pragma unroll
-  for (int i = 0; i < 2 * NT * 4; ++i) y[i / (NT * 4)][i / 4 % NT][i & 3] = 0.0f;
-
   if (warp >= kWideWarps) {
+    fewer_registers<kSideRegs>();
     // ============ activations as B fragments, and the scales ============
     // 16 codes of a token are a piece, in the order (group, token, unit, half)
     const int st = tid - kWideWarps * 32, half = st & 1, u = (st >> 1) % GU, pair = st / (2 * GU);
@@ -508,12 +517,18 @@ __global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_
       named_arrive(kFull + (c & 1));
       if (c + 1 < chunks) load(c + 1);
     }
+    named_sync(kDone);
+    more_registers<kLaunchRegs>();
   } else {
+    more_registers<kWideRegs>();
     // ============ contraction ============
     const Ring ring(&w_map, smem_u32(smem) + warp * kWideStages * kWideStage, smem_u32(s_bar) + warp * kWideStages * 8,
                     n_cta + warp * 32, u_begin, units, lane);
 #pragma unroll
     for (int st = 0; st < kWideStages - 1; ++st) ring.issue(st, lane);
+    float y[2][NT][4];
+#pragma unroll
+    for (int i = 0; i < 2 * NT * 4; ++i) y[i / (NT * 4)][i / 4 % NT][i & 3] = 0.0f;
     float acc[2][NT][4];
     for (int c = 0; c < chunks; ++c) {
       constexpr int kPer = kStageUnits / CU;
@@ -592,10 +607,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_
       __syncwarp();   // the stage is free for the copy that the next turn issues
     }
     if (*static_cast<volatile int*>(&s_abort) != 0) ring.drain();
-  }
-
-  __syncthreads();
-  if (warp < kWideWarps) {
+    named_sync(kDone);
     float* s_y = reinterpret_cast<float*>(smem);   // [token][channel]
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -604,6 +616,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           s_y[(t * 8 + 2 * lc + (e & 1)) * kWideCh + warp * 32 + i * 16 + lr + 8 * (e >> 1)] = y[i][t][e];
+    fewer_registers<kLaunchRegs>();
   }
   join_slices<kWideCh>(a, smem_u32(smem), rank, slices, m0, T, n_cta, tid, kWideThreads);
 }
