@@ -22,7 +22,7 @@
 // for eight codes, and half of the slots are taken (deeper rings change nothing:
 // 5120 x 34816, one row, 3, 4, 5 stages: 25.4, 26.7, 27.6 us, 3.5 TB/s of weights).
 // With more rows the instructions themselves (608 TFLOP/s at best) take 40 % of
-// the time and the slots 45 %: 37 rows of 5120 x 34816 take 61 us.  The same on
+// the time and the slots 45 %: 37 rows of 5120 x 34816 take 60 us.  The same on
 // tcgen05 (weights widened into swizzled shared memory, group sums read back from
 // tensor memory) took 75 us, and 50 us against 36 with 12 rows: every weight then
 // passes through shared memory twice.
@@ -337,55 +337,21 @@ __global__ void __launch_bounds__(kThreads, 4)
 
 // ---- 9 and more rows.  A CTA owns 128 channels: four warps of 32 channels, so
 // that a B fragment read from shared memory serves two instructions' rows, and
-// four warps that lay chunks of CU units of activations (and their scales) into
-// one of two buffers while the other is used.  Named barriers pass the buffers
-// on: kFull + b when buffer b is laid out, kEmpty + b when it has been read.
+// four warps that lay chunks of 8 units of activations (and their scales) into
+// one of two buffers while the other is used.  A chunk's weights come as one
+// tensor copy, a box of 128 rows by 128 bytes whose 16-byte pieces are swizzled
+// (piece u of row r at u ^ (r & 7)); rows past N and units past K read as zero.
+// Chunk c's mbarrier counts the box's bytes and the laying threads; the named
+// barrier kEmpty + (c & 1) says that chunk c has been read.  (The weights as
+// cp.async copies of the contracting lanes cost a fifth of their time: 37 rows of
+// 5120 x 34816 69 us; a box of 32 rows for each warp 61, one for the CTA asked
+// for by the laying warps 60.  With up to 8 rows boxes are no faster: one row
+// 25.4 and 26.3 us.)
 constexpr int kWideWarps = 4, kSideWarps = 4;       // a warpgroup each
 constexpr int kWideThreads = (kWideWarps + kSideWarps) * 32, kSide = kSideWarps * 32;
-constexpr int kWideStages = 3;
 constexpr int kWideCh = kWideWarps * 32;
-constexpr int kWidePitch = kStageUnits * 16, kWideStage = 32 * kWidePitch;
-enum : int { kFull = 1, kEmpty = 3, kDone = 5 };
-
-// A warp's weight rows on their way to shared memory: boxes of 32 rows by
-// kStageUnits units, a stage each, their 16-byte pieces swizzled (piece u of row
-// r at u ^ (r & 7)); rows past N and units past K read as zero.  One lane asks
-// for a stage: as cp.async copies of all lanes it cost a fifth of the warp's time
-// (37 rows of 5120 x 34816: 69 us so, 64.7 us with boxes; with up to 8 rows boxes
-// are no faster: one row 25.4 and 26.3 us).
-struct Ring {
-  const CUtensorMap* map;
-  uint32_t stage0, bar0;          // shared addresses: stages (1024-byte boundaries), mbarriers
-  int32_t x0, y;
-  int units;
-  __device__ __forceinline__ Ring(const CUtensorMap* map, uint32_t stages, uint32_t bars, int64_t n0, int u_begin, int units,
-                                  int lane)
-      : map(map), stage0(stages), bar0(bars), x0(u_begin * 16), y(static_cast<int32_t>(n0)), units(units) {
-    if (lane < kWideStages) tc::mbar_init(bar0 + 8 * lane, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    __syncwarp();
-  }
-  // the stage that st takes the place of has been read by the whole warp
-  __device__ __forceinline__ void issue(int st, int lane) const {
-    if (st * kStageUnits >= units || lane != 0) return;
-    const uint32_t bar = bar0 + 8 * (st % kWideStages);
-    tc::mbar_expect_tx(bar, kWideStage);
-    tc::tma_load_2d(stage0 + (st % kWideStages) * kWideStage, map, x0 + st * kWidePitch, y, bar);
-  }
-  // Bounded: where it runs out, the status bit says that the outputs are not valid.
-  __device__ __forceinline__ void wait(int st, volatile int* abort_flag) const {
-    tc::mbar_wait_bounded(bar0 + 8 * (st % kWideStages), (st / kWideStages) & 1, abort_flag, kWaitNs, &g_w4g_status,
-                          PRISM_DEVSTATUS_WAIT_TIMEOUT);
-    __syncwarp();
-  }
-  // After a wait that ran out: the boxes still under way land before the CTA ends.
-  __device__ __forceinline__ void drain() const {
-    const int stages = (units + kStageUnits - 1) / kStageUnits;
-    for (int st = max(0, stages - kWideStages); st < stages; ++st)
-      tc::mbar_wait_drain_bounded(bar0 + 8 * (st % kWideStages), (st / kWideStages) & 1, kWaitNs, &g_w4g_status,
-                                  PRISM_DEVSTATUS_WAIT_TIMEOUT);
-  }
-};
+constexpr int kWidePitch = kStageUnits * 16, kWideStage = kWideCh * kWidePitch;
+enum : int { kEmpty = 1, kDone = 3 };
 
 // The two warpgroups share the registers that the CTA was launched with: 128 a
 // thread, by the launch bounds.  (Two warps laying out, 168 registers for all:
@@ -407,11 +373,12 @@ __device__ __forceinline__ void named_arrive(int id) {
 template <int T, int GU, bool kOff>
 struct Wide {
   static constexpr int NT = T / 8;
-  static constexpr int CU = T <= 40 ? 8 : 4;                       // units of a chunk: two CTAs fit an SM
+  static constexpr int CU = kStageUnits;                           // units of a chunk
+  static constexpr int NS = T <= 40 ? 3 : 2;                       // chunks of weights held: two CTAs fit an SM
   static constexpr int GC = CU / GU;                               // its groups
   static constexpr int kB = CU * T * 64, kScale = kWideCh * GC * 2, kSum = GC * T * 4;
   static constexpr int kBuffer = kB + (kOff ? 2 * kScale + kSum : kScale);
-  static constexpr int kRing = kWideWarps * kWideStages * kWideStage;
+  static constexpr int kRing = NS * kWideStage;
   static constexpr int kBytes = 1024 + kRing + 2 * kBuffer;
   static_assert(kBytes >= T * kWideCh * 4, "the CTA's sums at the end");
   static_assert(2 * (kBytes + 1024) <= 227 * 1024, "two CTAs an SM");
@@ -421,12 +388,17 @@ template <int T, int GU, bool kOff>
 __global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_constant__ W4gArgs a, const __grid_constant__ CUtensorMap w_map, int slices,
                                                                    int slice_units) {
   using C = Wide<T, GU, kOff>;
-  constexpr int NT = C::NT, CU = C::CU, GC = C::GC;
+  constexpr int NT = C::NT, CU = C::CU, GC = C::GC, NS = C::NS;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[kWideWarps * kWideStages];
+  __shared__ __align__(8) uint64_t s_bar[NS];
   __shared__ int s_abort;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);   // the ring's boxes start on 1024-byte boundaries
-  if (threadIdx.x == 0) s_abort = 0;
+  const uint32_t bars = smem_u32(s_bar);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) tc::mbar_init(bars + 8 * i, kSide + 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   __syncthreads();
   pdl_trigger();
   pdl_wait();
@@ -485,9 +457,22 @@ __global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_
         }
       }
     };
+    // chunk c's weights, into the place of chunk c - NS
+    auto ask = [&](int c) {
+      if (st == 0 && c < chunks) {
+        const uint32_t bar = bars + 8 * (c % NS);
+        tc::mbar_expect_tx(bar, kWideStage);
+        tc::tma_load_2d(smem_u32(smem) + (c % NS) * kWideStage, &w_map, u_begin * 16 + c * kWidePitch, static_cast<int32_t>(n_cta), bar);
+      }
+    };
+#pragma unroll
+    for (int c = 0; c < NS; ++c) ask(c);
     if (chunks > 0) load(0);
     for (int c = 0; c < chunks; ++c) {
-      if (c >= 2) named_sync(kEmpty + (c & 1));
+      if (c >= 2) {
+        named_sync(kEmpty + (c & 1));   // chunk c - 2 was read
+        ask(c - 2 + NS);
+      }
       uint8_t* buf = buffer(c);
       Vec* s_scale = reinterpret_cast<Vec*>(buf + C::kB);
 #pragma unroll
@@ -514,31 +499,29 @@ __global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_
           if (half == 0 && u == 0) reinterpret_cast<float*>(buf + C::kB + 2 * C::kScale)[i] = static_cast<float>(sum);
         }
       }
-      named_arrive(kFull + (c & 1));
+      tc::mbar_arrive(bars + 8 * (c % NS));
       if (c + 1 < chunks) load(c + 1);
     }
     named_sync(kDone);
+    // after a wait that ran out: the boxes still under way land before the CTA ends
+    if (st == 0 && *static_cast<volatile int*>(&s_abort) != 0) {
+      for (int c = max(0, chunks - NS); c < chunks; ++c)
+        tc::mbar_wait_drain_bounded(bars + 8 * (c % NS), (c / NS) & 1, kWaitNs, &g_w4g_status, PRISM_DEVSTATUS_WAIT_TIMEOUT);
+    }
+    __syncwarp();
     more_registers<kLaunchRegs>();
   } else {
     more_registers<kWideRegs>();
     // ============ contraction ============
-    const Ring ring(&w_map, smem_u32(smem) + warp * kWideStages * kWideStage, smem_u32(s_bar) + warp * kWideStages * 8,
-                    n_cta + warp * 32, u_begin, units, lane);
-#pragma unroll
-    for (int st = 0; st < kWideStages - 1; ++st) ring.issue(st, lane);
     float y[2][NT][4];
 #pragma unroll
     for (int i = 0; i < 2 * NT * 4; ++i) y[i / (NT * 4)][i / 4 % NT][i & 3] = 0.0f;
     float acc[2][NT][4];
     for (int c = 0; c < chunks; ++c) {
-      constexpr int kPer = kStageUnits / CU;
-      const int st = c / kPer;
-      if (c % kPer == 0) {
-        ring.issue(st + kWideStages - 1, lane);
-        ring.wait(st, &s_abort);
-      }
-      const uint8_t* wb = smem + (warp * kWideStages + st % kWideStages) * kWideStage + lr * kWidePitch + lc * 4;
-      named_sync(kFull + (c & 1));
+      // bounded: where it runs out, the status bit says that the outputs are not valid
+      tc::mbar_wait_bounded(bars + 8 * (c % NS), (c / NS) & 1, &s_abort, kWaitNs, &g_w4g_status, PRISM_DEVSTATUS_WAIT_TIMEOUT);
+      __syncwarp();
+      const uint8_t* wb = smem + (c % NS) * kWideStage + (warp * 32 + lr) * kWidePitch + lc * 4;
       const uint8_t* buf = buffer(c);
       const uint2* s_b = reinterpret_cast<const uint2*>(buf) + lr * 4 + lc;
       const uint16_t* sp = reinterpret_cast<const uint16_t*>(buf + C::kB) + (warp * 32 + lr) * GC;
@@ -550,7 +533,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_
         uint32_t ae[2][4], ao[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint8_t* at = wb + i * 16 * kWidePitch + (((c % kPer * CU + u) * 16) ^ (lr * 16));
+          const uint8_t* at = wb + i * 16 * kWidePitch + ((u * 16) ^ (lr * 16));
           const uint32_t w0 = *reinterpret_cast<const uint32_t*>(at);
           const uint32_t w1 = *reinterpret_cast<const uint32_t*>(at + 8 * kWidePitch);
           ae[i][0] = even_codes(w0), ae[i][1] = even_codes(w1), ae[i][2] = even_codes(w0 >> 8), ae[i][3] = even_codes(w1 >> 8);
@@ -604,9 +587,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_
           if (g * GU < n) group(g);
       }
       if (c + 2 < chunks) named_arrive(kEmpty + (c & 1));
-      __syncwarp();   // the stage is free for the copy that the next turn issues
     }
-    if (*static_cast<volatile int*>(&s_abort) != 0) ring.drain();
     named_sync(kDone);
     float* s_y = reinterpret_cast<float*>(smem);   // [token][channel]
 #pragma unroll
@@ -632,7 +613,7 @@ cudaError_t weight_map(CUtensorMap* m, const W4gArgs& a) {
   if (fn == nullptr) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.K / 2), static_cast<cuuint64_t>(a.N)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.ldw4)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kWidePitch), 32}, step[2] = {1, 1};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kWidePitch), kWideCh}, step[2] = {1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.w4), dims, strides, box, step,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
