@@ -511,7 +511,10 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int s = blockIdx.x, hk = blockIdx.y;
   // the plan is made while the previous kernel ends: its inputs are older
   SeqPlan p;
-  if (seq_items<false, 1, kMany>(a, s, p) < 0 || p.bad || p.splits == 1) return;
+  if (seq_items<false, 1, kMany>(a, s, p) < 0 || p.bad || p.splits == 1) {
+    pdl_wait();   // this kernel ends no earlier than the one before it
+    return;
+  }
   if (!kMany || p.rows <= kFewRows) pdl_wait();
   const float* base = static_cast<const float*>(a.ws) + (static_cast<int64_t>(s) * a.c.H + hk) * part_stride * (D + 4);
   if constexpr (kMany) if (p.rows > kFewRows) {
