@@ -29,9 +29,9 @@
 // page's vs enters as its ratio to the largest vs seen so far.  Maxima, sums
 // and outputs are binary32.
 //
-// It reads the codes once: 64 sequences of 5 to 12000 tokens (287 MB of codes
-// and scales, 40 heads on 8) take 62 us, 4.6 TB/s; a single one of 131071 tokens
-// 60 us, 4.5 TB/s.  HBM is at 62 % then, the ALU pipe (widening, byte permutes)
+// It reads the codes once: 64 sequences of 300 to 4096 tokens (289 MB, 40 heads
+// on 8 of 128) take 62 us, 4.7 TB/s; a single one of 131071 tokens (32 heads on 4
+// of 256) 60 us, 4.5 TB/s.  HBM is at 62 % then, the ALU pipe (widening, byte permutes)
 // at half its rate: neither is full, what is left is the wait for a warp's next
 // step with 12 warps an SM (three CTAs, by registers).
 #include <cuda_fp16.h>

@@ -14,9 +14,9 @@
 //
 // A CTA owns 64 channels (up to 8 rows) or 128 and one slice of K; the CTAs of a
 // cluster hold the slices of one channel tile and add their sums through
-// distributed shared memory in slice order.  Each warp streams its weight rows
-// through a private ring (128 bytes of a row a step); the activations are widened once per CTA into shared memory, in the order that the
-// weight words want.
+// distributed shared memory in slice order.  The weights pass through a ring in
+// shared memory (128 bytes of a row a step); the activations are widened once
+// per CTA into shared memory, in the order that the weight words want.
 //
 // Up to 8 rows the issue slots bound it: a weight word costs nine instructions
 // for eight codes, and half of the slots are taken (deeper rings change nothing:
