@@ -108,7 +108,6 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
   __shared__ float s_scale[kWarps][kStages][U][2];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ float2 s_q[kRows];          // unit and start value of a row's scores
-  pdl_trigger();
   pdl_wait();
   const KvPages& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -472,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
     }
     __syncthreads();   // s_m, s_l, s_q, the ring and s_scan are free again
   }
+  pdl_trigger();       // not before: a join that waits takes the places of CTAs that work
 }
 
 // A joined row's output and lse: y and sum against the reference mx.
@@ -654,8 +654,10 @@ cudaError_t launch_few(const KvAttentionArgs& a, int64_t part_stride, cudaStream
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kv_attention_kernel<D, NQ>), M::kBytes);
   if (e != cudaSuccess) return e;
   // Persistent: as many CTAs as the SMs hold, or as the call can have items.
-  // Not launched ahead of the previous kernel's end: a join that waits for
-  // these CTAs takes their places (64 ragged sequences: 85 us so, 65 us not).
+  // Not launched ahead of the previous kernel's end: that brought nothing (one
+  // query, 271 keys: 8.0 us, 8.4 so).  The join is launched as these CTAs end:
+  // allowed from their start it took their places (64 sequences: 85 us), after
+  // the kernel it came later (eight of 4096 keys: 24.2 us, 23.4 so).
   const int64_t tiles = std::min<int64_t>(a.T * a.G, static_cast<int64_t>(a.c.S) * kFewRows) / M::kRows + a.c.S;
   const int64_t items = (tiles + (part_stride / M::kRows + kMaxSplit) * a.c.S) * a.c.H;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sm_count() * M::kCtas));
@@ -679,7 +681,8 @@ cudaError_t launch_d(const KvAttentionArgs& a, cudaStream_t stream) {
   const int64_t want = rows <= kFewRows ? rows : (rows + kWideRows - 1) / kWideRows * 8;
   const int64_t most = rows <= kFewRows ? kFewRows : std::max<int64_t>(1, 4 * sm_count() / (static_cast<int64_t>(a.c.S) * a.c.H));
   const dim3 grid(a.c.S, a.c.H, static_cast<unsigned>(std::min<int64_t>(want, most)));
-  return launch_kernel(rows <= kFewRows ? kv_combine_kernel<D, false> : kv_combine_kernel<D, true>, grid, dim3(kJoinThreads), 0, stream, rows > kFewRows, a, part_stride);
+  return launch_kernel(rows <= kFewRows ? kv_combine_kernel<D, false> : kv_combine_kernel<D, true>, grid,
+                       dim3(kJoinThreads), 0, stream, true, a, part_stride);
 }
 
 }  // namespace
