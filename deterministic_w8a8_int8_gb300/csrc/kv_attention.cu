@@ -506,7 +506,6 @@ __global__ void __launch_bounds__(kJoinThreads)
   __shared__ float s_f[kJoinThreads], s_red[kJoinWarps], s_sum[kJoinWarps];
   __shared__ float4 s_o[kJoinThreads];
   static_assert(kMaxSplit <= kJoinThreads, "a thread for each piece");
-  pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int s = blockIdx.x, hk = blockIdx.y;
   // the plan is made while the previous kernel ends: its inputs are older
@@ -654,14 +653,15 @@ cudaError_t launch_few(const KvAttentionArgs& a, int64_t part_stride, cudaStream
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kv_attention_kernel<D, NQ>), M::kBytes);
   if (e != cudaSuccess) return e;
   // Persistent: as many CTAs as the SMs hold, or as the call can have items.
-  // Not launched ahead of the previous kernel's end: that brought nothing (one
-  // query, 271 keys: 8.0 us, 8.4 so).  The join is launched as these CTAs end:
-  // allowed from their start it took their places (64 sequences: 85 us), after
-  // the kernel it came later (eight of 4096 keys: 24.2 us, 23.4 so).
+  // Each of a call's kernels is launched as the CTAs of the one before it end
+  // (calls in a row, one query on 271 keys: 10.3 us without, 7.9 so; 131071 keys:
+  // 65 and 59); allowed from their start, a join takes the places of CTAs that
+  // work (64 sequences: 85 us), and the next call's CTAs those of a join (64
+  // sequences of 500 to 3000 keys: 58.2 us, 53.2 so).
   const int64_t tiles = std::min<int64_t>(a.T * a.G, static_cast<int64_t>(a.c.S) * kFewRows) / M::kRows + a.c.S;
   const int64_t items = (tiles + (part_stride / M::kRows + kMaxSplit) * a.c.S) * a.c.H;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sm_count() * M::kCtas));
-  return launch_kernel(kv_attention_kernel<D, NQ>, dim3(grid), dim3(kThreads), M::kBytes, stream, false, a, part_stride);
+  return launch_kernel(kv_attention_kernel<D, NQ>, dim3(grid), dim3(kThreads), M::kBytes, stream, true, a, part_stride);
 }
 
 // Rows of a tile: as many as a sequence of this kernel can have in this call

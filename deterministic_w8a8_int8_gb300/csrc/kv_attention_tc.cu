@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::tc_fence_after();
   const uint32_t tmem = s_tmem;
   pdl_trigger();
-  // Launched ahead of the end of the few-row kernel, whose start ends what the
-  // inputs come from; neither needs the other's results.  The wait stands at the end,
+  // Launched ahead of the end of the few-row kernel, all of whose CTAs have waited
+  // for what the inputs come from; neither needs the other's results.  The wait stands at the end,
   // so that this kernel's end is also the other's.
   const KvPages& c = a.c;
   uint32_t g0 = 0, items = 0;      // blocks and items before this item: the phases of the mbarriers
