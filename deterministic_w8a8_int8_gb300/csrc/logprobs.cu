@@ -42,7 +42,13 @@ constexpr int kMaxParts = 8;
 constexpr int kGroups = 128;                  // group maxima of a row
 constexpr int kList = 1024;                   // candidates the first CTA can take
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
-constexpr float kFar = 1e37f;                 // beyond it x * log2(e) could leave binary32's range
+// A thread's reference is RN(L m), so its terms are off by a common factor of 2^
+// (half a step of L m), which the join takes back: below kFar that is 2^(1/16) at
+// most (at 1e10 it would be 2^440).  Pieces at -kFar and below are masked ones,
+// without a reference: their terms are zero.  That holds for rows whose maximum
+// is well above -kFar; other rows, and those above kFarRow, are summed again by
+// differences.
+constexpr float kFar = 0x1p20f, kFarRow = 0x1p19f;
 constexpr float kSlack = 27.0f;               // e^27 over the reference: far from binary32's limits
 
 typedef unsigned long long u64;
@@ -379,8 +385,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     const float top = s_row_sum[0];
     float rr = s_row_sum[1], sum = s_row_sum[2], ent = s_row_sum[3];
-    const bool far = top > -INFINITY && top < INFINITY && !(fabsf(top) < kFar);
-    if (far) {   // a maximum near binary32's limits: the row once more, differences first
+    const bool far = top > -INFINITY && top < INFINITY && !(fabsf(top) < kFarRow);
+    if (far) {   // the row once more, differences first
       float fs = 0.0f, fe = 0.0f;
       for (int64_t v = tid; v < a.V; v += kThreads) {
         const float x = F32 ? static_cast<const float*>(row)[v] : bf16_bits_to_float(static_cast<const uint16_t*>(row)[v]);
