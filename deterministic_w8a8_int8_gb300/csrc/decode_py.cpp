@@ -8,6 +8,7 @@
 // call took 12.8 us, through Python's C API alone 9.4 (torch.empty takes 5 us
 // of it after a launch), and here 3.4; token log probabilities 15.2, 14.4, 6.1.
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -128,16 +129,22 @@ at::Tensor empty(at::ScalarType type, int64_t device, int n, const int64_t* shap
                                            c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(device)), std::nullopt));
 }
 
-bool stream_of(PyObject* stream, int64_t device, void** out) {
+// The stream of a call, made torch's current one for as long as `guard` lives:
+// outputs and workspaces taken from torch's allocator meanwhile belong to the
+// stream that uses them, so that no other stream's work is given their memory.
+bool use_stream(PyObject* stream, int64_t device, c10::cuda::OptionalCUDAStreamGuard* guard, void** out) {
+  const auto index = static_cast<c10::DeviceIndex>(device);
   if (stream == Py_None) {
-    *out = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
+    *out = c10::cuda::getCurrentCUDAStream(index).stream();
     return true;
   }
   PyObject* v = PyObject_GetAttrString(stream, "cuda_stream");
   if (v == nullptr) return false;
   *out = PyLong_AsVoidPtr(v);
   Py_DECREF(v);
-  return PyErr_Occurred() == nullptr;
+  if (PyErr_Occurred() != nullptr) return false;
+  guard->reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(*out), index));
+  return true;
 }
 
 bool integer(PyObject* v, int64_t* out) {
@@ -216,6 +223,7 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Operand k, v, ko, vo;
   Cache c;
   void *cu, *err, *stream;
+  c10::cuda::OptionalCUDAStreamGuard guard;
   if (!first_operand(a[0], "k", 3, &device, first)) return nullptr;
   const Items cache(a[2], "cache must be a sequence of tensors");
   if (cache.seq == nullptr || !read_cache(cache, a[3], a[4], device, &c)) return nullptr;
@@ -232,7 +240,7 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return nullptr;
   max_new = cu == nullptr || rows < 1 ? 1 : rows;
   if (a[6] != Py_None && !integer(a[6], &max_new)) return nullptr;
-  if (!optional(a[7], "err", at::kInt, device, 1, &kOne, &err) || !stream_of(a[8], device, &stream)) return nullptr;
+  if (!optional(a[7], "err", at::kInt, device, 1, &kOne, &err) || !use_stream(a[8], device, &guard, &stream)) return nullptr;
   int status;
   Py_BEGIN_ALLOW_THREADS
   status = prism_kv_append(k.ptr, k.stride[0], k.stride[1], v.ptr, v.stride[0], v.stride[1],
@@ -254,6 +262,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Operand q, o;
   Cache c;
   void *cu, *lse, *err, *stream, *ws = nullptr;
+  c10::cuda::OptionalCUDAStreamGuard guard;
   if (!first_operand(a[0], "q", 3, &device, first)) return nullptr;
   const Items cache(a[1], "cache must be a sequence of tensors");
   if (cache.seq == nullptr || !read_cache(cache, a[2], a[3], device, &c)) return nullptr;
@@ -272,7 +281,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (PyErr_Occurred() != nullptr || !integer(a[8], &window)) return nullptr;
   if (a[9] != Py_None && !operand(a[9], "out", at::kBFloat16, device, 3, shape, false, &o)) return nullptr;
   if (!optional(a[10], "lse", at::kFloat, device, 2, lse_shape, &lse)) return nullptr;
-  if (!optional(a[12], "err", at::kInt, device, 1, &kOne, &err) || !stream_of(a[13], device, &stream)) return nullptr;
+  if (!optional(a[12], "err", at::kInt, device, 1, &kOne, &err) || !use_stream(a[13], device, &guard, &stream)) return nullptr;
   at::Tensor held, made;
   if (a[11] != Py_None) {
     const at::Tensor* w = tensor(a[11], "workspace");
@@ -318,6 +327,7 @@ PyObject* py_w4g(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   int64_t device, first[2], group_shape[2];
   Operand q, as, w, s, b, r, o;
   void* stream;
+  c10::cuda::OptionalCUDAStreamGuard guard;
   if (!first_operand(a[0], "q", 2, &device, first) || !shape_of(a[3], "group_scale", 2, group_shape)) return nullptr;
   const int64_t m = first[0], k = first[1], n = group_shape[0], groups = group_shape[1];
   if (groups == 0 || k % groups || k % 2) {
@@ -332,7 +342,7 @@ PyObject* py_w4g(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       (a[4] != Py_None && !operand(a[4], "group_offset", at::kHalf, device, 2, group_shape, false, &b)) ||
       (a[5] != Py_None && !operand(a[5], "residual", at::kBFloat16, device, 2, out_shape, false, &r)) ||
       (a[6] != Py_None && !operand(a[6], "out", at::kBFloat16, device, 2, out_shape, false, &o)) ||
-      !stream_of(a[7], device, &stream))
+      !use_stream(a[7], device, &guard, &stream))
     return nullptr;
   at::Tensor made;
   if (a[6] == Py_None) {
@@ -359,6 +369,7 @@ PyObject* py_logprobs(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   int64_t device, first[2], ids_shape[2], top_k;
   Operand x, ids;
   void *stream, *err;
+  c10::cuda::OptionalCUDAStreamGuard guard;
   if (!first_operand(a[0], "logits", 2, &device, first) || !shape_of(a[1], "token_ids", 2, ids_shape) ||
       !integer(a[2], &top_k))
     return nullptr;
@@ -374,7 +385,7 @@ PyObject* py_logprobs(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   }
   if (!operand(a[0], "logits", type, device, 2, first, false, &x) ||
       !operand(a[1], "token_ids", at::kInt, device, 2, ids_shape, false, &ids) ||
-      !optional(a[4], "err", at::kInt, device, 1, &kOne, &err) || !stream_of(a[5], device, &stream))
+      !optional(a[4], "err", at::kInt, device, 1, &kOne, &err) || !use_stream(a[5], device, &guard, &stream))
     return nullptr;
   at::Tensor lp = empty(at::kFloat, device, 2, lp_shape), ent, ti, tl;
   if (want_entropy) ent = empty(at::kFloat, device, 1, &rows);

@@ -8,6 +8,9 @@ Entry points (same names as the C ABI):
   prism_kv_attention(q, cache, page_table, seq_lens, ...)        -> out
   prism_w4g_linear(q, a_scale, w4, group_scale, ...)             -> out
   prism_token_logprobs(logits, token_ids, top_k=...)             -> (logprobs, entropy, top_ids, top_logprobs)
+
+Each takes ``stream`` (default: torch's current one); the outputs and the
+workspace that a call allocates belong to that stream.
 """
 from __future__ import annotations
 
