@@ -129,13 +129,16 @@ at::Tensor empty(at::ScalarType type, int64_t device, int n, const int64_t* shap
                                            c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(device)), std::nullopt));
 }
 
-// The stream of a call, made torch's current one for as long as `guard` lives:
-// outputs and workspaces taken from torch's allocator meanwhile belong to the
-// stream that uses them, so that no other stream's work is given their memory.
+// The stream of a call and the operands' device, torch's current ones for as long
+// as `guard` lives: the kernels are launched on that device, and outputs and
+// workspaces taken from torch's allocator meanwhile belong to the stream that
+// uses them, so that no other stream's work is given their memory.
 bool use_stream(PyObject* stream, int64_t device, c10::cuda::OptionalCUDAStreamGuard* guard, void** out) {
   const auto index = static_cast<c10::DeviceIndex>(device);
   if (stream == Py_None) {
-    *out = c10::cuda::getCurrentCUDAStream(index).stream();
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(index);
+    *out = current.stream();
+    guard->reset_stream(current);
     return true;
   }
   PyObject* v = PyObject_GetAttrString(stream, "cuda_stream");
@@ -143,6 +146,16 @@ bool use_stream(PyObject* stream, int64_t device, c10::cuda::OptionalCUDAStreamG
   *out = PyLong_AsVoidPtr(v);
   Py_DECREF(v);
   if (PyErr_Occurred() != nullptr) return false;
+  v = PyObject_GetAttrString(stream, "device_index");
+  if (v == nullptr) return false;
+  const int64_t of = PyLong_AsLongLong(v);
+  Py_DECREF(v);
+  if (PyErr_Occurred() != nullptr) return false;
+  if (of != device) {
+    PyErr_Format(PyExc_ValueError, "stream must be of cuda:%lld, got one of cuda:%lld", static_cast<long long>(device),
+                 static_cast<long long>(of));
+    return false;
+  }
   guard->reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(*out), index));
   return true;
 }
