@@ -3,22 +3,21 @@
 //
 // A page's codes and scale are a function of its rows: amax over the rows, one
 // scale, codes by one factor.  The rows of a sequence's open page are kept in
-// bf16 as well: a row that raises amax is followed by a fresh quantisation of
-// the whole page, and so is the row that completes it.  Any other row (all but
-// ln(block) of a page's rows, for values in random order) leaves the earlier
-// codes as they are: then only the new rows are written, and the page's amax
-// is read back from its scale (a bf16 number; amax * RN(1/127) keeps 23 bits
-// of it).
+// bf16 as well and looked at again whenever rows are added: a scale that differs
+// from the one in place (amax raised, or its row dropped by a sequence set back)
+// is followed by a fresh quantisation of the whole page, and so is the row that
+// completes it.  Where the scale stays (all but ln(block) of a page's rows, for
+// values in random order) the earlier codes do, and only the new rows' are written.
 //
 // Bytes: 2 in and 1 out per value, 2 more out for the rows of a page that
-// stays open -- HBM-bound for prompts; one generated token is a chain of four
-// dependent reads (offsets, page, scale, rows of a raised page).  One CTA per
-// (sequence, page, head, K or V): a page's rows stay in registers between the
-// maximum and the codes.  64 clients' rows of one token take 5.4 us; prompts of
-// 24 million values 19.3 us, 3.7 TB/s, bound by the issue slots (11 instructions
-// a value before magnitudes were taken in pairs and codes rounded by an addition:
-// 21.5 us).  CTAs that walk several pages and read the next one ahead: 20.7 us,
-// and 7.4 us for single tokens.
+// stays open -- HBM-bound for prompts; one generated token is a chain of three
+// dependent reads (offsets, page and rows, scale).  One CTA per (sequence, page,
+// head, K or V): a page's rows stay in registers between the maximum and the
+// codes.  64 clients' rows of one token take 5.2 us; prompts of 24 million values
+// 19.7 us, 3.7 TB/s, bound by the issue slots (11 instructions a value before
+// magnitudes were taken in pairs and codes rounded by an addition: 21.5 us).
+// CTAs that walk several pages and read the next one ahead: 20.7 us, and 7.4 us
+// for single tokens.
 #include "decode.cuh"
 
 namespace prism {
@@ -94,42 +93,29 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
       x[i] = make_uint4(0u, 0u, 0u, 0u);
       if (r >= n_old && r < n_rows) x[i] = *reinterpret_cast<const uint4*>(rows + (p0 + r - before) * ld_t + col);
     }
+    if (n_old > 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int r = (i * kThreads + tid) >> row_shift;
+        if (r < n_old) x[i] = *reinterpret_cast<const uint4*>(open + r * c.D + col);
+      }
+    }
     const bool page_ok = page >= 0 && page < c.num_pages;
     const int64_t ph = static_cast<int64_t>(page) * c.H + h;
     const float old_scale = page_ok && n_old > 0 ? scales[ph] : 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) most = max8(x[i], most);
-    auto block_max = [&](uint32_t pair) {
-      float m = fmaxf(bf16_lo(pair), bf16_hi(pair));
+    float amax = fmaxf(bf16_lo(most), bf16_hi(most));
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      __syncthreads();
-      if (lane == 0) s_red[warp] = m;
-      __syncthreads();
-      m = s_red[0];
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    __syncthreads();
+    if (lane == 0) s_red[warp] = amax;
+    __syncthreads();
+    amax = s_red[0];
 #pragma unroll
-      for (int w = 1; w < kThreads / 32; ++w) m = fmaxf(m, s_red[w]);
-      return m;
-    };
-    float amax = block_max(most);
-    int from = n_old;                     // first row whose codes are written
-    if (n_old > 0 && page_ok) {
-      if (open_page == first && page_scale(amax) <= old_scale) {
-        amax = bf16_bits_to_float(static_cast<uint16_t>(float_to_bf16_rne(__fmul_rn(old_scale, 127.0f))));
-      } else {                            // the page's earlier rows again
-        from = 0;
-        uint32_t old = 0u;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int r = (i * kThreads + tid) >> row_shift;
-          if (r < n_old) {
-            x[i] = *reinterpret_cast<const uint4*>(open + r * c.D + col);
-            old = max8(x[i], old);
-          }
-        }
-        amax = fmaxf(amax, block_max(old));
-      }
-    }
+    for (int w = 1; w < kThreads / 32; ++w) amax = fmaxf(amax, s_red[w]);
+    // first row whose codes are written: those of the same scale stand already
+    const int from = n_old > 0 && open_page == first && page_scale(amax) == old_scale ? n_old : 0;
     if (page_ok) {
       const float f = code_factor(amax);
       if (tid == 0 && from == 0) scales[ph] = page_scale(amax);
@@ -143,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
       atomicOr(a.err, PRISM_DEV_ERR_PAGE_RANGE);
     }
     // ---- the open page's rows, by the CTA of the first page: only it reads
-    // the open buffer, and it has (block_max's barriers come after its reads)
+    // the open buffer, and it has (the barriers come after its reads)
     if (j == 0) {
       const int64_t o0 = open_page << c.block_shift;
       const int begin = open_page == first ? n_old : 0, end = static_cast<int>(after - o0);

@@ -517,6 +517,10 @@ size_t prism_readout_workspace_bytes(int64_t P, int64_t T, int64_t K);
  * RN(x * f)), -127, 127) with f = RN(127 * RN(1 / amax)); amax < 2^-120 gives
  * scale 0 and codes 0.
  * Rows past the sequence's end are left as they are.
+ * seq_lens may be set back between calls, to drop rows, as far as the start of
+ * the open page (the bf16 rows of a page that was completed are not kept) or to
+ * the start of any page; the next call's codes and scale are then those of the
+ * rows that are left and the new ones.
  *   k_bf16, v_bf16    [T, H_kv, D] bf16, token stride ld?_t, head stride
  *                     ld?_h (multiples of 8, 16-byte aligned bases)
  *   seq_lens          tokens in the cache BEFORE the call (not changed)
