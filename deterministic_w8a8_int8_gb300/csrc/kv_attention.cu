@@ -97,7 +97,7 @@ struct Smem {
 
 template <int D, int NQ>
 __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
-    kv_attention_kernel(const __grid_constant__ KvAttentionArgs a, int64_t part_stride) {
+    kv_attention_kernel(const __grid_constant__ KvAttentionArgs a, const __grid_constant__ Parts parts) {
   constexpr int U = kUnits<D>;
   constexpr int kSteps16 = D / 16;       // k16 steps of S^T, m16 tiles of O^T
   constexpr bool kQSmem = Smem<D, NQ>::kQ;
@@ -463,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
         if (d == 0 && a.lse != nullptr)
           a.lse[t * a.Hq + h] = bad ? nanf : mx == -INFINITY ? mx : (mx - kPShift + log2f(sum)) * kLn2;
       } else {
-        const int64_t slot = (static_cast<int64_t>(s) * c.H + hk) * part_stride + split * p.rows + row0 + r;
-        float* ps = part + slot * (D + 4);
+        const int64_t at = first_part(parts, p, s, hk) + static_cast<int64_t>(split) * p.rows + row0 + r;
+        float* ps = part + at * (D + 4);
         *reinterpret_cast<float4*>(ps + 4 + d) = y;
         if (d == 0) ps[0] = bad ? nanf : mx, ps[1] = sum;
       }
@@ -501,7 +501,7 @@ constexpr int kWarpPieces = 16;
 
 template <int D, bool kMany>   // kMany: a sequence may have many rows
 __global__ void __launch_bounds__(kJoinThreads)
-    kv_combine_kernel(const __grid_constant__ KvAttentionArgs a, int64_t part_stride) {
+    kv_combine_kernel(const __grid_constant__ KvAttentionArgs a, const __grid_constant__ Parts parts) {
   constexpr int kCols = D / 4, kGroups = kJoinThreads / kCols, kJoinWarps = kJoinThreads / 32, E = D / 32;
   __shared__ float s_f[kJoinThreads], s_red[kJoinWarps], s_sum[kJoinWarps];
   __shared__ float4 s_o[kJoinThreads];
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     return;
   }
   if (!kMany || p.rows <= kFewRows) pdl_wait();
-  const float* base = static_cast<const float*>(a.ws) + (static_cast<int64_t>(s) * a.c.H + hk) * part_stride * (D + 4);
+  const float* base = static_cast<const float*>(a.ws) + first_part(parts, p, s, hk) * (D + 4);
   if constexpr (kMany) if (p.rows > kFewRows) {
     __shared__ int64_t s_line[kJoinThreads], s_warp64[kJoinWarps];
     lay_line<kJoinThreads>(a, p, s_line, s_warp64);
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kJoinThreads)
       for (int i = (u & 7) * (kWideRows / 8) + warp; i < (u & 7) * (kWideRows / 8) + kWideRows / 8; i += kJoinWarps) {
         const int r = (u >> 3) * kWideRows + i;
         if (r >= p.rows) break;
-        auto piece = [&](int range) { return base + (static_cast<int64_t>(2 * range + (range == first)) * kWideRows + i) * (D + 4); };
+        auto piece = [&](int range) { return base + (wide_part(p, range, u >> 3, range == first) + i) * (D + 4); };
         float mx = -INFINITY;
         bool nan = false;
         for (int range = first + lane; range <= last; range += 32) {
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 }
 
 template <int D, int NQ>
-cudaError_t launch_few(const KvAttentionArgs& a, int64_t part_stride, cudaStream_t stream) {
+cudaError_t launch_few(const KvAttentionArgs& a, const Parts& parts, cudaStream_t stream) {
   using M = Smem<D, NQ>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kv_attention_kernel<D, NQ>), M::kBytes);
   if (e != cudaSuccess) return e;
@@ -659,9 +659,9 @@ cudaError_t launch_few(const KvAttentionArgs& a, int64_t part_stride, cudaStream
   // work (64 sequences: 85 us), and the next call's CTAs those of a join (64
   // sequences of 500 to 3000 keys: 58.2 us, 53.2 so).
   const int64_t tiles = std::min<int64_t>(a.T * a.G, static_cast<int64_t>(a.c.S) * kFewRows) / M::kRows + a.c.S;
-  const int64_t items = (tiles + (part_stride / M::kRows + kMaxSplit) * a.c.S) * a.c.H;
+  const int64_t items = (tiles + (parts.few / M::kRows + kMaxSplit) * a.c.S) * a.c.H;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sm_count() * M::kCtas));
-  return launch_kernel(kv_attention_kernel<D, NQ>, dim3(grid), dim3(kThreads), M::kBytes, stream, true, a, part_stride);
+  return launch_kernel(kv_attention_kernel<D, NQ>, dim3(grid), dim3(kThreads), M::kBytes, stream, true, a, parts);
 }
 
 // Rows of a tile: as many as a sequence of this kernel can have in this call
@@ -670,26 +670,26 @@ cudaError_t launch_few(const KvAttentionArgs& a, int64_t part_stride, cudaStream
 template <int D>
 cudaError_t launch_d(const KvAttentionArgs& a, cudaStream_t stream) {
   const int64_t rows = a.max_q * a.G;
-  const int64_t part_stride = max_split_rows(a.max_q, a.G, a.c.max_pages << a.c.block_shift, a.c.H, D);
-  cudaError_t e = rows <= 8                 ? launch_few<D, 1>(a, part_stride, stream)
-                  : rows <= 16 || D == 256  ? launch_few<D, 2>(a, part_stride, stream)
-                                            : launch_few<D, D == 256 ? 2 : 4>(a, part_stride, stream);
-  if (e == cudaSuccess && rows > kFewRows) e = launch_kv_attention_wide(a, part_stride, stream);
-  if (e != cudaSuccess || part_stride == 0) return e;
+  const Parts parts = parts_of(a.c.S, a.T, a.max_q, a.G, a.c.max_pages << a.c.block_shift, a.c.H, D);
+  cudaError_t e = rows <= 8                 ? launch_few<D, 1>(a, parts, stream)
+                  : rows <= 16 || D == 256  ? launch_few<D, 2>(a, parts, stream)
+                                            : launch_few<D, D == 256 ? 2 : 4>(a, parts, stream);
+  if (e == cudaSuccess && rows > kFewRows) e = launch_kv_attention_wide(a, parts, stream);
+  if (e != cudaSuccess || parts.rows == 0) return e;
   // CTAs of a (sequence, KV head): a row each of few, an eighth of a tile each
   // of many, in one turn of the four that an SM holds
   const int64_t want = rows <= kFewRows ? rows : (rows + kWideRows - 1) / kWideRows * 8;
   const int64_t most = rows <= kFewRows ? kFewRows : std::max<int64_t>(1, 4 * sm_count() / (static_cast<int64_t>(a.c.S) * a.c.H));
   const dim3 grid(a.c.S, a.c.H, static_cast<unsigned>(std::min<int64_t>(want, most)));
   return launch_kernel(rows <= kFewRows ? kv_combine_kernel<D, false> : kv_combine_kernel<D, true>, grid,
-                       dim3(kJoinThreads), 0, stream, true, a, part_stride);
+                       dim3(kJoinThreads), 0, stream, true, a, parts);
 }
 
 }  // namespace
 
-size_t kv_attention_workspace_bytes(int64_t S, int64_t, int64_t max_q, int64_t max_pages, int64_t Hq, int64_t Hkv,
+size_t kv_attention_workspace_bytes(int64_t S, int64_t T, int64_t max_q, int64_t max_pages, int64_t Hq, int64_t Hkv,
                                     int64_t D, int64_t block) {
-  return static_cast<size_t>(S * Hkv * max_split_rows(max_q, Hq / Hkv, max_pages * block, Hkv, D)) * (D + 4) * 4;
+  return static_cast<size_t>(Hkv * parts_of(S, T, max_q, Hq / Hkv, max_pages * block, Hkv, D).rows) * (D + 4) * 4;
 }
 
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream) {

@@ -89,7 +89,7 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    kv_attention_tc_kernel(const __grid_constant__ KvAttentionArgs a, int64_t part_stride) {
+    kv_attention_tc_kernel(const __grid_constant__ KvAttentionArgs a, const __grid_constant__ Parts parts) {
   using C = Tc<D>;
   constexpr int KB = C::kKeys, U = C::kUnits, UH = U / 2;
   extern __shared__ uint8_t smem_raw[];
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     SeqPlan plan;
     TileKeys keys;
     int64_t x, x_end, tile_x;    // the range's blocks not yet in work; the first of tile walk.tile
-    int slot;                    // of the tile's piece; -1: the whole tile
+    int64_t part;                // the piece's first row among the sequence's pieces; -1: the whole tile
   } s_item;
   __shared__ int s_scan[kThreads];
   __shared__ int s_warp[kThreads / 32];
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int end = static_cast<int>(min(static_cast<int64_t>(n), s_item.x_end - s_item.tile_x));
       k.k_begin = (k.t_lo & ~63) + x * KB;
       k.k_end = static_cast<int32_t>(min(static_cast<int64_t>(k.t_hi), static_cast<int64_t>(k.t_lo & ~63) + static_cast<int64_t>(end) * KB));
-      s_item.slot = end - x == n ? -1 : 2 * s_item.walk.split + (x == 0);
+      s_item.part = end - x == n ? -1 : wide_part(s_item.plan, s_item.walk.split, s_item.walk.tile, x == 0);
       s_item.keys = k;
     }
     __syncthreads();
@@ -553,8 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float nanf = __uint_as_float(0x7fc00000u);
       const bool some = m > -INFINITY || l != l;   // saw a key (or a NaN score)
       float* ps = static_cast<float*>(a.ws) +
-                  ((static_cast<int64_t>(s_item.walk.s) * c.H + hk) * part_stride + static_cast<int64_t>(max(s_item.slot, 0)) * kWideRows + r) * (D + 4);
-      const bool final = s_item.slot < 0;
+                  (first_part(parts, p, s_item.walk.s, hk) + max(s_item.part, static_cast<int64_t>(0)) + r) * (D + 4);
+      const bool final = s_item.part < 0;
       const float scale = !some ? 0.0f : final ? v_top / l : v_top;
       // a warp's 32 rows, 32 channels at a time, pass through its 4 KB of the
       // (now unused) K stages, 16-byte pieces swizzled: rows are written whole
@@ -634,21 +634,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D>
-cudaError_t launch_d(const KvAttentionArgs& a, int64_t part_stride, cudaStream_t stream) {
+cudaError_t launch_d(const KvAttentionArgs& a, const Parts& parts, cudaStream_t stream) {
   using C = Tc<D>;
   cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kv_attention_tc_kernel<D>), C::kBytes);
   if (e != cudaSuccess) return e;
-  const int64_t items = (a.T * a.G / kWideRows + a.c.S + part_stride / kWideRows * a.c.S) * a.c.H;
+  const int64_t items = (a.T * a.G / kWideRows + a.c.S + 2 * parts.ranges * a.c.S) * a.c.H;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sm_count()));
-  return launch_kernel(kv_attention_tc_kernel<D>, dim3(grid), dim3(kThreads), C::kBytes, stream, true, a, part_stride);
+  return launch_kernel(kv_attention_tc_kernel<D>, dim3(grid), dim3(kThreads), C::kBytes, stream, true, a, parts);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_attention_wide(const KvAttentionArgs& a, int64_t part_stride, cudaStream_t stream) {
-  return a.c.D == 64    ? launch_d<64>(a, part_stride, stream)
-         : a.c.D == 128 ? launch_d<128>(a, part_stride, stream)
-                        : launch_d<256>(a, part_stride, stream);
+cudaError_t launch_kv_attention_wide(const KvAttentionArgs& a, const kv::Parts& parts, cudaStream_t stream) {
+  return a.c.D == 64    ? launch_d<64>(a, parts, stream)
+         : a.c.D == 128 ? launch_d<128>(a, parts, stream)
+                        : launch_d<256>(a, parts, stream);
 }
 
 cudaError_t read_and_clear_kv_status(uint32_t* out) {

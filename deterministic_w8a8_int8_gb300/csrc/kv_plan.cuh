@@ -57,19 +57,50 @@ __host__ __device__ __forceinline__ int range_count(int64_t tiles, int64_t block
   const int64_t most = tiles > blocks / kMinBlocks ? tiles : blocks / kMinBlocks;
   return most < best ? static_cast<int>(most) : best;
 }
-// The most (row, piece) pairs of one (sequence, KV head).  A range has at most
-// two tiles in pieces: the one that it begins inside of (slot 2 range), and one
-// that begins in it (slot 2 range + 1).  Fewer keys never make more of either.
-inline int64_t max_split_rows(int64_t max_q, int64_t G, int64_t max_keys, int64_t H, int64_t D) {
-  const int64_t rows = max_q * G, few = std::min<int64_t>(kFewRows, rows);
-  const int64_t splits = split_count(max_keys, H);
-  int64_t most = splits > 1 ? splits * few : 0;
+// Pieces of a wide sequence, in slots of as many rows as its tiles have: a range
+// has at most two tiles in pieces, the one that it begins inside of and one that
+// begins in it, and along the line a next piece has a next range or a next tile.
+__host__ __device__ __forceinline__ int64_t wide_slots(int64_t tiles, int64_t ranges) {
+  return tiles <= ranges ? ranges + tiles - 1 : 2 * ranges;
+}
+__host__ __device__ __forceinline__ int64_t wide_slot(int64_t tiles, int64_t ranges, int64_t range, int64_t tile, bool begins) {
+  return tiles <= ranges ? range + tile : 2 * range + (begins ? 1 : 0);
+}
+
+// A call's workspace: (D + 4) floats for a (row, piece) pair.  Its place depends on
+// the sequence or on its first query alone, whichever takes less for the call:
+// where sequences are long and few, so many pairs as one has at most for each; in
+// a batch of many, so many for each query as it has at most.
+struct Parts {
+  int64_t rows = 0;                      // pairs of one KV head
+  int64_t per_seq = 0, per_query = 0;    // one of them is 0
+  int64_t few = 0, ranges = 0;           // pairs of a sequence of few rows; ranges of a wide one: at most
+};
+// The most of everything; fewer rows or keys of a sequence never take more.  A
+// wide sequence of t tiles has at least 128 (t - 1) + 1 rows (33), and at most
+// max(t, t blocks / kMinBlocks) ranges: 1 + max(2, blocks / 5) pairs a row.
+inline Parts parts_of(int64_t S, int64_t T, int64_t max_q, int64_t G, int64_t max_keys, int64_t H, int64_t D) {
+  static_assert(kMinBlocks == 10, "the bound of a row's pairs");
+  Parts p;
+  const int64_t rows = max_q * G, splits = split_count(max_keys, H);
+  int64_t of_seq = 0, of_row = 0;
+  if (splits > 1) of_seq = p.few = splits * std::min<int64_t>(kFewRows, rows), of_row = splits;
   if (rows > kFewRows) {
     const int64_t tiles = (rows + kWideRows - 1) / kWideRows, blocks = (max_keys + wide_keys(static_cast<int>(D)) - 1) >> wide_shift(static_cast<int>(D));
-    const int64_t n = range_count(tiles, tiles * blocks, static_cast<int>(H));
-    if (n > 1) most = std::max(most, 2 * n * kWideRows);
+    p.ranges = range_count(tiles, tiles * blocks, static_cast<int>(H));
+    if (p.ranges > 1) {
+      of_seq = std::max(of_seq, wide_slots(tiles, p.ranges) * std::min<int64_t>(kWideRows, rows));
+      of_row = std::max(of_row, 1 + std::min(p.ranges, std::max<int64_t>(2, (blocks + 4) / 5)));
+    }
   }
-  return most;
+  if (S * of_seq <= T * G * of_row) {
+    p.per_seq = of_seq;
+    p.rows = S * of_seq;
+  } else {
+    p.per_query = G * of_row;
+    p.rows = T * p.per_query;
+  }
+  return p;
 }
 
 // A sequence's plan: its rows, key range and pieces.
@@ -108,6 +139,15 @@ __device__ __forceinline__ int seq_items(const KvAttentionArgs& a, int s, SeqPla
   }
   if (kWide ? p.bad || p.rows <= kFewRows : !p.bad && p.rows > kFewRows) return 0;
   return (kWide ? 1 : p.tiles) * p.splits * a.c.H;
+}
+
+// The sequence's first pair in the workspace, in pairs.
+__device__ __forceinline__ int64_t first_part(const Parts& w, const SeqPlan& p, int s, int hk) {
+  return hk * w.rows + s * w.per_seq + p.sp.b * w.per_query;
+}
+// The first row of a piece of tile `tile`, from there.
+__device__ __forceinline__ int64_t wide_part(const SeqPlan& p, int range, int tile, bool begins) {
+  return wide_slot((p.rows + kWideRows - 1) / kWideRows, p.splits, range, tile, begins) * min(p.rows, kWideRows);
 }
 
 // Walks a CTA's items: sequences are counted a window of one a thread at a
@@ -308,5 +348,5 @@ __device__ __forceinline__ int query_exponent(float amax) {
 }  // namespace kv
 
 // The tcgen05 kernel (kv_attention_tc.cu): sequences of more than kv::kFewRows rows.
-cudaError_t launch_kv_attention_wide(const KvAttentionArgs& a, int64_t part_stride, cudaStream_t stream);
+cudaError_t launch_kv_attention_wide(const KvAttentionArgs& a, const kv::Parts& parts, cudaStream_t stream);
 }  // namespace prism
