@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
     const int s = walk.s, hk = walk.hk, split = walk.split;
     const TileKeys keys(a, p, walk, kRows);
     const int row0 = keys.row0, n_rows = keys.n_rows;
-    const int32_t k_begin = keys.k_begin, k_end = keys.k_end;
+    const int32_t k_begin = keys.k_begin, k_first = keys.k_first, k_end = keys.k_end;
     const int steps = k_end > k_begin ? (k_end - k_begin + kStepKeys<D> - 1) / kStepKeys<D> : 0;
     const int my_steps = (steps - warp + kWarps - 1) / kWarps;   // steps warp, warp + 4, ...
 
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
       const int u = lane % U, j = st + lane / U;
       const int32_t key = k_begin + (warp + kWarps * j) * kStepKeys<D> + u * 16;
       page_l = 0;
-      if (j < my_steps && key < k_end) {
+      if (j < my_steps && key >= k_first && key < k_end) {
         page_l = table[key >> c.block_shift];
         if (page_l < 0 || page_l >= c.num_pages) {
           bad_page = true;
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
         for (int u = 0; u < U; ++u) {
           const int32_t page = __shfl_sync(0xffffffffu, page_l, (st % (32 / U)) * U + u);
           const int32_t key = key0 + u * 16;
-          const int bytes = key < k_end ? 16 : 0;   // units past the end: zeros
+          const int bytes = key >= k_first && key < k_end ? 16 : 0;   // units that no row sees: zeros
           const int64_t ph = static_cast<int64_t>(page) * c.H + hk;
           const int64_t off = (ph * c.block + (key & (c.block - 1))) * D + lane * 16;
           const int8_t* ks = c.k_codes + off;

@@ -214,7 +214,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ch = is_v ? ct / 8 % (D / 16) : ct % (D / 16);
       const bool has_unit = !is_v && ct < U;            // passes on the scales of unit ct
       // a page id is read ahead and looked at when it is used
-      auto page_at = [&](int32_t key, bool live) { return live && key < k_end ? table[key >> c.block_shift] : 0; };
+      const int32_t k_first = max(k_begin, s_item.keys.k_first);
+      auto page_at = [&](int32_t key, bool live) { return live && key >= k_first && key < k_end ? table[key >> c.block_shift] : 0; };
       auto code_page = [&](int j) { return page_at(k_begin + j * KB + kg * 8, mine); };
       auto unit_page = [&](int j) { return page_at(k_begin + j * KB + ct * 16, has_unit); };
       auto row = [&](int32_t page) {          // an invalid page (the rows get NaN) or none: page 0, in its stead
@@ -222,8 +223,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto unit_scales = [&](int j, int32_t page) {     // vs not yet divided
         const int64_t at = row(page);
-        return has_unit && k_begin + j * KB + ct * 16 < k_end ? make_float2(c.k_scale[at], c.v_scale[at])
-                                                              : make_float2(0.0f, 0.0f);
+        const int32_t key = k_begin + j * KB + ct * 16;
+        return has_unit && key >= k_first && key < k_end ? make_float2(c.k_scale[at], c.v_scale[at]) : make_float2(0.0f, 0.0f);
       };
       uint4 raw[8];
       auto load = [&](int j, int32_t page) {
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool bad = false;
       float v_top = 0.0f;
       if (blocks > 0) {
-        for (int32_t i = (k_begin >> c.block_shift) + tid - kSoft; i <= (k_end - 1) >> c.block_shift; i += kConv) {
+        for (int32_t i = (k_first >> c.block_shift) + tid - kSoft; i <= (k_end - 1) >> c.block_shift; i += kConv) {
           const int32_t page = table[i];
           if (page < 0 || page >= c.num_pages) {
             bad = true;

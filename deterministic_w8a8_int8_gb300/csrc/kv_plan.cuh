@@ -215,6 +215,7 @@ struct TileKeys {
   int32_t row0, n_rows, first_pos, len, G, window;
   bool causal, none;
   int32_t a_hi, t_hi, t_lo, a_lo, k_begin, k_end;
+  int32_t k_first;             // no row sees a key of the 16-key units before it: their pages may be gone
   TileKeys() = default;
   __device__ __forceinline__ TileKeys(const KvAttentionArgs& a, const SeqPlan& p, const Walk& w, int tile_rows) {
     row0 = w.tile * tile_rows;
@@ -230,6 +231,7 @@ struct TileKeys {
     t_lo = lo(a_hi);
     a_lo = lo(t_hi);
     k_begin = max(p.lo + w.split * p.chunk, t_lo & ~63);
+    k_first = t_lo & ~15;
     const int64_t piece_end = static_cast<int64_t>(p.lo) + static_cast<int64_t>(w.split + 1) * p.chunk;
     k_end = static_cast<int32_t>(min(static_cast<int64_t>(t_hi), piece_end));
   }

@@ -502,7 +502,8 @@ size_t prism_readout_workspace_bytes(int64_t P, int64_t T, int64_t K);
  *                     sequence's tokens [i * block, (i + 1) * block).  Full
  *                     pages may be shared by several sequences (the branches
  *                     of one evidence text); entries past a sequence's last
- *                     token are not read.
+ *                     token, and those of pages wholly before the windows of
+ *                     all its queries, are not read.
  *   seq_lens          [S] int32 token counts
  *   block in {16, 32, 64, 128}, D in {64, 128, 256}, H_kv >= 1.
  * The last page of a sequence is open while it holds fewer than `block`
