@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
         const int64_t t = p.sp.b + tok;
         *reinterpret_cast<uint2*>(a.out + t * a.ldo_t + h * a.ldo_h + d) = w;
         if (d == 0 && a.lse != nullptr)
-          a.lse[t * a.Hq + h] = bad ? nanf : mx == -INFINITY ? mx : (mx - kPShift + log2f(sum)) * kLn2;
+          a.lse[t * a.Hq + h] = bad ? nanf : mx == -INFINITY ? mx + sum : (mx - kPShift + log2f(sum)) * kLn2;   // no key: sum 0; only NaN scores: NaN
       } else {
         const int64_t at = first_part(parts, p, s, hk) + static_cast<int64_t>(split) * p.rows + row0 + r;
         float* ps = part + at * (D + 4);
@@ -489,7 +489,7 @@ __device__ __forceinline__ void store_row(const KvAttentionArgs& a, const SeqPla
 #pragma unroll
   for (int e = 0; e < E / 2; ++e) dst[e] = w[e];
   if (d == 0 && a.lse != nullptr)
-    a.lse[t * a.Hq + h] = nan ? __uint_as_float(0x7fc00000u) : mx == -INFINITY ? mx : (mx - kPShift + log2f(sum)) * kLn2;
+    a.lse[t * a.Hq + h] = nan ? __uint_as_float(0x7fc00000u) : mx == -INFINITY ? mx + sum : (mx - kPShift + log2f(sum)) * kLn2;
 }
 
 // Joins the pieces of rows of one (sequence, KV head).  Many rows: a row a
