@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const float unit = __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) * a.scale_log2 * 0x1p24f;
+      const float unit = __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) * a.scale_log2;
       const float start = sum * -0x1p-17f;   // -128 * 2^-24
       if constexpr (kQSmem) {
         if (lc == 0) s_q[r] = make_float2(unit, start);
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, Smem<D, NQ>::kCtas)
             }
           }
         }
-        const float ks = s_scale[warp][stage][u][0];
+        const float ks = s_scale[warp][stage][u][0] * 0x1p24f;   // of code * 2^-24; beside q_unit it could leave binary32's range
         vs[u] = s_scale[warp][stage][u][1];
         v_top = fmaxf(v_top, vs[u]);
 #pragma unroll
