@@ -7,6 +7,9 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 constexpr int64_t kInt31 = (1LL << 31) - 1;
+// Tokens of a sequence at most: the attention's 32-bit positions run up to some
+// thousand past a text's end (pages that are looked up ahead).
+constexpr int64_t kMaxTokens = (1LL << 31) - (1LL << 14);
 
 // The cache's own arguments.  Fills c where they are sound.
 int check_cache(const int8_t* k_codes, const int8_t* v_codes, const float* k_scale, const float* v_scale,
@@ -20,7 +23,7 @@ int check_cache(const int8_t* k_codes, const int8_t* v_codes, const float* k_sca
   while ((1LL << shift) < block && shift < 8) ++shift;
   if ((1LL << shift) != block || block < 16 || block > 128) return PRISM_ERR_UNSUPPORTED;
   if (D != 64 && D != 128 && D != 256) return PRISM_ERR_UNSUPPORTED;
-  if (S > (1 << 24) || H > 32767 || num_pages > kInt31 || max_pages > (kInt31 >> shift)) return PRISM_ERR_UNSUPPORTED;
+  if (S > (1 << 24) || H > 32767 || num_pages > kInt31 || max_pages > (kMaxTokens >> shift)) return PRISM_ERR_UNSUPPORTED;
   if (!aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
       !aligned(page_table, 4) || !aligned(seq_lens, 4))
     return PRISM_ERR_ALIGNMENT;
@@ -111,7 +114,7 @@ int prism_kv_attention(const void* q_bf16, int64_t ldq_t, int64_t ldq_h, const i
   int st = check_cache(k_codes, v_codes, k_scale, v_scale, page_table, ld_table, seq_lens, S, num_pages, max_pages,
                        H_kv, D, block, a.c);
   if (st != PRISM_OK) return st;
-  if (H_q > (1 << 16) || T * H_q > kInt31) return PRISM_ERR_UNSUPPORTED;
+  if (H_q > (1 << 16) || T > kInt31 || T * H_q > kInt31) return PRISM_ERR_UNSUPPORTED;
   if ((st = check_rows(q_bf16, ldq_t, ldq_h, T, H_q, D)) != PRISM_OK) return st;
   if ((st = check_rows(out_bf16, ldo_t, ldo_h, T, H_q, D)) != PRISM_OK) return st;
   if (!aligned(lse, 4) || !aligned(cu_q, 4) || !aligned(dev_error_word, 4)) return PRISM_ERR_ALIGNMENT;

@@ -506,6 +506,7 @@ size_t prism_readout_workspace_bytes(int64_t P, int64_t T, int64_t K);
  *                     all its queries, are not read.
  *   seq_lens          [S] int32 token counts
  *   block in {16, 32, 64, 128}, D in {64, 128, 256}, H_kv >= 1.
+ *   max_pages * block <= 2^31 - 2^14.
  * The last page of a sequence is open while it holds fewer than `block`
  * tokens; its rows are also kept in bf16,
  *   k_open, v_open    [S, H_kv, block, D] bf16, dense, 16-byte aligned,
