@@ -7,6 +7,10 @@
 
 namespace prism {
 
+// SMs that work is cut for, whatever the device has: the order of sums follows the
+// cuts, so results are those of a call's sizes alone.
+constexpr int kSms = 152;
+
 // A paged cache as the kernels see it (dense [num_pages, H, block, D] codes).
 struct KvPages {
   int8_t* k_codes;

@@ -26,8 +26,7 @@ constexpr int kWideRows = 128;         // rows of a tile of the tcgen05 kernel: 
 // 45.4 and 41.9.
 constexpr int kMinChunk = 1024;
 constexpr int kMaxSplit = 128;         // pieces of a row at most
-constexpr int kFillFew = 456;          // items that one sequence is cut into where it has the keys: three on each of 152 SMs
-constexpr int kSms = 152;              // one wide item on each at a time
+constexpr int kFillFew = 3 * kSms;     // items that one sequence is cut into where it has the keys: three on each SM
 // Blocks of a range at least, where a line has more ranges than tiles: a part of
 // a tile costs about eight blocks' time besides its blocks (80 rows, 8 KV heads,
 // 8208 keys, with 6, 10 and 16 at least: one sequence 37.8, 40.1 and 48.1 us,

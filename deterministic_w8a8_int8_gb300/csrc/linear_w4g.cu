@@ -645,12 +645,12 @@ cudaError_t launch_slices(void (*kernel)(P...), int channels, int threads, int b
 
 template <int GU, bool kOff>
 cudaError_t launch_gu(const W4gArgs& a, cudaStream_t stream) {
-  // Slices of K: as many as let four CTAs of 64 channels (two of 128) on every
-  // SM run at once, at most a cluster of eight; each a multiple of a stage.  A
-  // rule on N and K alone: a row's sums do not depend on M.
+  // Slices of K: as many as let four CTAs of 64 channels (two of 128) on each of
+  // kSms SMs run at once, at most a cluster of eight; each a multiple of a stage.
+  // A rule on N and K alone: a row's sums do not depend on M, or on the device.
   const int64_t tiles64 = (a.N + 63) / 64;
   const int units = static_cast<int>(a.K >> 5), stages = (units + kStageUnits - 1) / kStageUnits;
-  const int slices = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({4 * sm_count() / tiles64, 8, stages})));
+  const int slices = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({4 * kSms / tiles64, 8, stages})));
   const int slice_units = (stages + slices - 1) / slices * kStageUnits;
   auto few = [&](auto t) {
     constexpr int T = decltype(t)::value;
