@@ -5,6 +5,7 @@ Each ``csrc/*.cu`` translation unit is compiled in parallel with
 ``deterministic_w8a8_int8_gb300/libprism.so`` against the shared CUDA runtime.
 ``csrc/decode_py.cpp``, the Python side of the decode-step entry points, becomes
 the extension module ``_decode.so`` beside it (g++; Python's and torch's headers).
+Without these the library is built all the same, with a warning.
 Set ``PRISM_PTXAS_VERBOSE=1`` to print ptxas register and spill reports.
 """
 from __future__ import annotations
@@ -16,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +27,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libprism.so")
 MODULE_SRC = os.path.join(CSRC, "decode_py.cpp")
 MODULE_PATH = os.path.join(PKG, "_decode.so")
+STAMP_PATH = os.path.join(BUILD_DIR, "decode_py.stamp")   # what the module was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -35,11 +38,11 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _cxx() -> str:
+def _cxx() -> str | None:
     for cand in (os.environ.get("CXX"), shutil.which("g++"), shutil.which("c++")):
         if cand:
             return cand
-    raise RuntimeError("g++ not found")
+    return None
 
 
 def _cuda_lib_dir(nvcc: str) -> str:
@@ -59,19 +62,41 @@ def _deps() -> list[str]:
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+def _torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec is not None and spec.submodule_search_locations else None
+
+
+def _module_lacks() -> str | None:
+    """What is missing here that the extension module cannot be built without."""
+    if _cxx() is None:
+        return "g++"
+    torch_dir = _torch_dir()
+    if torch_dir is None or not os.path.isdir(os.path.join(torch_dir, "include", "torch", "csrc")):
+        return "torch's headers"
+    return None if os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")) else "Python's headers"
+
+
+def _module_stamp() -> str:
+    """The torch and the Python that the module is built for."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return f"{sysconfig.get_config_var('EXT_SUFFIX')}\n{_torch_dir()}\n{f.read()}"
+
+
+def _module_up_to_date() -> bool:
+    if not os.path.exists(MODULE_PATH) or not os.path.exists(STAMP_PATH):
+        return False
+    with open(STAMP_PATH) as f:
+        if f.read() != _module_stamp():
+            return False
+    return os.path.getmtime(MODULE_PATH) >= max(os.path.getmtime(MODULE_SRC), os.path.getmtime(os.path.join(INCLUDE, "prism.h")))
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(MODULE_PATH):
+    if not os.path.exists(LIB_PATH):
         return False
     t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(p) <= t for p in _deps()) and os.path.getmtime(MODULE_PATH) >= max(
-        os.path.getmtime(MODULE_SRC), os.path.getmtime(os.path.join(INCLUDE, "prism.h")))
-
-
-def _torch_dir() -> str:
-    spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("torch not found")
-    return spec.submodule_search_locations[0]
+    return all(os.path.getmtime(p) <= t for p in _deps()) and (_module_lacks() is not None or _module_up_to_date())
 
 
 def _run(what: str, cmd: list[str]) -> None:
@@ -97,6 +122,8 @@ def _link_module(obj: str, libdir: str) -> None:
                                 "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
                                 f"-Wl,-rpath,$ORIGIN:{torch_lib}:{libdir},-rpath-link,{libdir}"])
     os.replace(tmp, MODULE_PATH)
+    with open(STAMP_PATH, "w") as f:
+        f.write(_module_stamp())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -118,9 +145,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stderr, end="")
         return obj
 
+    lacks = _module_lacks()
+    if lacks is not None:
+        warnings.warn(f"_decode.so is not built, for want of {lacks}: the decode-step entry points need it")
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        module = ex.submit(_compile_module, nvcc)
+        module = ex.submit(_compile_module, nvcc) if lacks is None else None
         objs = list(ex.map(compile_one, srcs))
     libdir = _cuda_lib_dir(nvcc)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
@@ -130,7 +160,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stderr)
     os.replace(tmp, LIB_PATH)
-    _link_module(module.result(), libdir)
+    if module is not None:
+        _link_module(module.result(), libdir)
     return LIB_PATH
 
 

@@ -23,7 +23,11 @@ from . import _check, lib
 _BF16, _F32, _I8 = torch.bfloat16, torch.float32, torch.int8
 
 lib()   # one loaded library for both bindings; says what to do where it is not built
-from . import _decode  # noqa: E402  (csrc/decode_py.cpp: checks, outputs and the calls)
+try:
+    from . import _decode  # (csrc/decode_py.cpp: checks, outputs and the calls)
+except ImportError as e:
+    raise ImportError("_decode.so is not built, or for another torch; run deterministic_w8a8_int8_gb300.build.build() "
+                      "(needs nvcc, g++, and torch's and Python's headers)") from e
 
 _decode.setup(_check)
 
