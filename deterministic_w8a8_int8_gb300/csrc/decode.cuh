@@ -57,8 +57,9 @@ struct KvAttentionArgs {
 size_t kv_attention_workspace_bytes(int64_t S, int64_t T, int64_t max_q, int64_t max_pages, int64_t Hq, int64_t Hkv,
                                     int64_t D, int64_t block);
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t stream);
-// Device status bits of its bounded waits.
+// Device status bits of its bounded waits, and their test mode (prism_debug_wait_expiry).
 cudaError_t read_and_clear_kv_status(uint32_t* out);
+cudaError_t set_kv_wait_expiry(unsigned long long limit_ns, int withhold);
 
 struct W4gArgs {
   const int8_t* q;
@@ -78,8 +79,9 @@ struct W4gArgs {
   int32_t group;
 };
 cudaError_t launch_w4g(const W4gArgs& a, cudaStream_t stream);
-// Device status bits of its bounded waits.
+// Device status bits of its bounded waits, and their test mode (prism_debug_wait_expiry).
 cudaError_t read_and_clear_w4g_status(uint32_t* out);
+cudaError_t set_w4g_wait_expiry(unsigned long long limit_ns, int withhold);
 
 struct LogprobArgs {
   const void* logits;

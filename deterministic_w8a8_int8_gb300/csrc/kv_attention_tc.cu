@@ -35,8 +35,8 @@
 // binary16 with 2^kShift as the value of the reference (2^15 at most), times vs
 // relative to the part's largest; sums and outputs are binary32.
 //
-// Every wait on an mbarrier is bounded: after 2 s the kernel sets the device
-// status bit; every warp then runs its loops out without waiting (so that the
+// Every wait on an mbarrier is bounded: after 2 s (prism_debug_wait_expiry shortens
+// that for tests) the kernel sets the device status bit; every warp then runs its loops out without waiting (so that the
 // named barriers still meet), the instructions in flight complete, and the
 // kernel returns.
 #include <type_traits>
@@ -47,12 +47,16 @@
 namespace prism {
 
 __device__ uint32_t g_kv_status = 0;
+// Test mode (prism_debug_wait_expiry): the waits' limit, and whether each CTA's
+// issuer withholds the signal that its first block's scores are formed.
+__device__ unsigned long long g_kv_wait_limit_ns = 2000000000ull;
+__device__ int g_kv_withhold = 0;
 
 namespace {
 
 using namespace kv;
 
-constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr unsigned long long kDrainNs = 2000000000ull;
 constexpr float kShift = 9.0f, kSlack = 6.0f;
 constexpr int kSoftWarps = 8, kConvWarps = 8;
 constexpr int kThreads = (kSoftWarps + kConvWarps + 1) * 32;
@@ -73,7 +77,7 @@ struct Tc {
 
 // One answer for the warp, whose lanes are together again afterwards.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  return __all_sync(0xffffffffu, tc::mbar_wait_bounded(bar, parity, abort_flag, kWaitNs, &g_kv_status,
+  return __all_sync(0xffffffffu, tc::mbar_wait_bounded(bar, parity, abort_flag, &g_kv_wait_limit_ns, &g_kv_status,
                                                        PRISM_DEVSTATUS_WAIT_TIMEOUT));
 }
 // True in one lane of the warp, in a way that lets the compiler issue the
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < D / 16; ++k)
               tc::tc_mma(dt, qd + (k >> 2) * (kWideRows * 8) + 2 * (k & 3), kd + (k >> 2) * (KB * 8) + 2 * (k & 3), id_s,
                          k != 0 ? 1u : 0u);
-            tc::tc_commit(bar_s(g));
+            if (g != 0 || *static_cast<volatile int*>(&g_kv_withhold) == 0) tc::tc_commit(bar_s(g));
             tc::tc_commit(bar_kfree(g));
           }
         }
@@ -624,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- every instruction in flight completes before the columns are given back
   if (warp == kSoftWarps + kConvWarps && elect_one()) {   // the issuing thread
     tc::tc_commit(bar_end);
-    tc::mbar_wait_drain_bounded(bar_end, 0, kWaitNs, &g_kv_status, PRISM_DEVSTATUS_WAIT_TIMEOUT);
+    tc::mbar_wait_drain_bounded(bar_end, 0, kDrainNs, &g_kv_status, PRISM_DEVSTATUS_WAIT_TIMEOUT);
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -661,6 +665,12 @@ cudaError_t read_and_clear_kv_status(uint32_t* out) {
     e = cudaMemcpyToSymbol(g_kv_status, &zero, sizeof zero);
   }
   *out = v;
+  return e;
+}
+
+cudaError_t set_kv_wait_expiry(unsigned long long limit_ns, int withhold) {
+  cudaError_t e = cudaMemcpyToSymbol(g_kv_wait_limit_ns, &limit_ns, sizeof limit_ns);
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_kv_withhold, &withhold, sizeof withhold);
   return e;
 }
 

@@ -37,10 +37,14 @@
 namespace prism {
 
 __device__ uint32_t g_w4g_status = 0;
+// Test mode (prism_debug_wait_expiry): the waits' limit, and whether a laying thread
+// of each CTA withholds its arrival for the first chunk until the CTA has run out.
+__device__ unsigned long long g_w4g_wait_limit_ns = 2000000000ull;
+__device__ int g_w4g_withhold = 0;
 
 namespace {
 
-constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr unsigned long long kDrainNs = 2000000000ull;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kCh = kWarps * 16;   // of a CTA with up to 8 rows; its channels
 constexpr int kStageUnits = 8;            // a unit is 32 input channels: 16 bytes of a weight row
@@ -465,12 +469,31 @@ __global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_
         tc::tma_load_2d(smem_u32(smem) + (c % NS) * kWideStage, &w_map, u_begin * 16 + c * kWidePitch, static_cast<int32_t>(n_cta), bar);
       }
     };
+    // Once a wait has run out no more is asked for, and only chunks that were
+    // asked for are arrived for, so that no phase of an mbarrier gets another's
+    // arrivals; the boxes still under way land before the CTA ends.
+    auto withheld = [&] { return st == 0 && *static_cast<volatile int*>(&g_w4g_withhold) != 0; };
+    auto aborted = [&] { return __any_sync(0xffffffffu, *static_cast<volatile int*>(&s_abort)) != 0; };   // one answer for the warp
+    auto drain = [&](int asked) {
+      if (withheld()) tc::mbar_arrive(bars);
+      for (int c = max(0, asked - NS); c < min(asked, chunks) && st == 0; ++c)
+        tc::mbar_wait_drain_bounded(bars + 8 * (c % NS), (c / NS) & 1, kDrainNs, &g_w4g_status, PRISM_DEVSTATUS_WAIT_TIMEOUT);
+    };
 #pragma unroll
     for (int c = 0; c < NS; ++c) ask(c);
     if (chunks > 0) load(0);
-    for (int c = 0; c < chunks; ++c) {
+    int c = 0;
+    for (; c < chunks; ++c) {
       if (c >= 2) {
         named_sync(kEmpty + (c & 1));   // chunk c - 2 was read
+        if (aborted()) {
+          for (int k = c; k < chunks; ++k) {
+            if (k > c) named_sync(kEmpty + (k & 1));
+            if (k < c - 2 + NS) tc::mbar_arrive(bars + 8 * (k % NS));
+          }
+          drain(c - 2 + NS);
+          break;
+        }
         ask(c - 2 + NS);
       }
       uint8_t* buf = buffer(c);
@@ -499,15 +522,11 @@ __global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_
           if (half == 0 && u == 0) reinterpret_cast<float*>(buf + C::kB + 2 * C::kScale)[i] = static_cast<float>(sum);
         }
       }
-      tc::mbar_arrive(bars + 8 * (c % NS));
+      if (c != 0 || !withheld()) tc::mbar_arrive(bars + 8 * (c % NS));
       if (c + 1 < chunks) load(c + 1);
     }
     named_sync(kDone);
-    // after a wait that ran out: the boxes still under way land before the CTA ends
-    if (st == 0 && *static_cast<volatile int*>(&s_abort) != 0) {
-      for (int c = max(0, chunks - NS); c < chunks; ++c)
-        tc::mbar_wait_drain_bounded(bars + 8 * (c % NS), (c / NS) & 1, kWaitNs, &g_w4g_status, PRISM_DEVSTATUS_WAIT_TIMEOUT);
-    }
+    if (c == chunks && chunks > 0 && aborted()) drain(chunks);   // after the last chunk was asked for
     __syncwarp();
     more_registers<kLaunchRegs>();
   } else {
@@ -519,7 +538,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) w4g_wide_kernel(const __grid_
     float acc[2][NT][4];
     for (int c = 0; c < chunks; ++c) {
       // bounded: where it runs out, the status bit says that the outputs are not valid
-      tc::mbar_wait_bounded(bars + 8 * (c % NS), (c / NS) & 1, &s_abort, kWaitNs, &g_w4g_status, PRISM_DEVSTATUS_WAIT_TIMEOUT);
+      tc::mbar_wait_bounded(bars + 8 * (c % NS), (c / NS) & 1, &s_abort, &g_w4g_wait_limit_ns, &g_w4g_status, PRISM_DEVSTATUS_WAIT_TIMEOUT);
       __syncwarp();
       const uint8_t* wb = smem + (c % NS) * kWideStage + (warp * 32 + lr) * kWidePitch + lc * 4;
       const uint8_t* buf = buffer(c);
@@ -703,6 +722,12 @@ cudaError_t read_and_clear_w4g_status(uint32_t* out) {
     e = cudaMemcpyToSymbol(g_w4g_status, &zero, sizeof zero);
   }
   *out = v;
+  return e;
+}
+
+cudaError_t set_w4g_wait_expiry(unsigned long long limit_ns, int withhold) {
+  cudaError_t e = cudaMemcpyToSymbol(g_w4g_wait_limit_ns, &limit_ns, sizeof limit_ns);
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_w4g_withhold, &withhold, sizeof withhold);
   return e;
 }
 

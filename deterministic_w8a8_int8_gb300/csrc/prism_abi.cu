@@ -294,6 +294,8 @@ int prism_debug_wait_expiry(uint64_t limit_ns) {
   const int withhold = limit_ns != 0 ? 1 : 0;
   int st = prism::record_cuda(prism::set_tc_wait_expiry(v, withhold));
   if (st == PRISM_OK) st = prism::record_cuda(prism::set_f16_wait_expiry(v, withhold));
+  if (st == PRISM_OK) st = prism::record_cuda(prism::set_kv_wait_expiry(v, withhold));
+  if (st == PRISM_OK) st = prism::record_cuda(prism::set_w4g_wait_expiry(v, withhold));
   return st;
 }
 

@@ -69,6 +69,24 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     }
   }
 }
+// The same with a limit in memory, looked up beside the clock.
+__device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                  const volatile unsigned long long* limit_ns, uint32_t* status,
+                                                  uint32_t status_bit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  unsigned long long t0 = globaltimer();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0u) {
+      if (*abort_flag) return false;
+      if (wait_expired(t0, i, *limit_ns)) {
+        *abort_flag = 1;
+        atomicOr(status, status_bit);
+        return false;
+      }
+    }
+  }
+}
 // Teardown wait (for copies and MMAs already issued): bounded by limit_ns,
 // blind to any abort flag; expiry only ORs status_bit into *status.
 __device__ __forceinline__ void mbar_wait_drain_bounded(uint32_t bar, uint32_t parity, unsigned long long limit_ns,

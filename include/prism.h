@@ -683,15 +683,19 @@ int prism_device_status(uint32_t *flags);
 
 /*
  * Diagnostics for the bounded on-chip waits of the tensor-core kernels
- * (prism_w8a8_linear's, prism_w8a8_linear_f16's) on the current device.
+ * (prism_w8a8_linear's, prism_w8a8_linear_f16's, prism_kv_attention's for many
+ * rows, prism_w4g_linear's for more than 8) on the current device.
  * limit_ns > 0 arms a test mode for the calls that follow: every pipeline
  * wait is limited to limit_ns, and each CTA withholds its first
- * chunk-complete signal, so the wait for it cannot complete and expires.
+ * chunk-complete signal (the attention: that its first scores are formed; the
+ * 4-bit linear: an arrival for its first weights), so the wait for it cannot
+ * complete and expires.
  * The kernel then raises PRISM_DEVSTATUS_WAIT_TIMEOUT, lets every copy it
  * started land and every MMA it issued complete, releases its tensor memory
  * and returns.  limit_ns = 0 disarms the mode (the default: a 2 s limit,
  * every signal sent).  The outputs of any call that raised the bit are
- * invalid, and a workspace it used must be zeroed again before its next use.
+ * invalid, and a workspace of the first two must be zeroed again before its
+ * next use.
  */
 int prism_debug_wait_expiry(uint64_t limit_ns);
 
