@@ -32,6 +32,8 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 import threading
 
@@ -158,6 +160,25 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _under_its_stream(fn):
+    """``fn`` with its ``stream`` as torch's current one: the outputs and the
+    workspaces that it allocates (and zeroes) belong to the stream that uses them."""
+    place = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        stream = args[place] if len(args) > place else kwargs.get("stream")
+        if stream is None:
+            return fn(*args, **kwargs)
+        import torch
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+
+    return call
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -229,6 +250,7 @@ def prism_version() -> int:
     return int(lib().prism_version())
 
 
+@_under_its_stream
 def prism_quant_act(x, inv_s=None, q=None, a_scale=None, stream=None):
     """Per-token quantisation of bf16 ``x`` [M, K] -> (int8 q [M, K], float32 a_scale [M])."""
     import torch
@@ -248,6 +270,7 @@ def prism_quant_act(x, inv_s=None, q=None, a_scale=None, stream=None):
     return q, a_scale
 
 
+@_under_its_stream
 def prism_smooth_requant(q, d, smooth=None, w=None, w_scale=None, stream=None):
     """Requantise Q8_0 weights with SmoothQuant factors folded in.
 
@@ -284,6 +307,7 @@ def new_workspace(M: int, N: int, K: int, split_k: int = 0, device=None):
     return torch.zeros((n,), dtype=torch.uint8, device=device)
 
 
+@_under_its_stream
 def prism_w8a8_linear(q, a_scale, w, w_scale, residual=None, out=None, acc_out=None,
                       split_k: int = 0, workspace=None, stream=None):
     """out[M, N] (bf16) = epilogue(q @ w^T) with exact int32 accumulation.
@@ -307,6 +331,7 @@ def prism_w8a8_linear(q, a_scale, w, w_scale, residual=None, out=None, acc_out=N
     return out
 
 
+@_under_its_stream
 def prism_quant_act_rows(x, rows, inv_s=None, q=None, a_scale=None, err=None, stream=None):
     """Quantisation of the rows ``rows`` (int32 [n]) of bf16 ``x`` [M_x, K]
     -> (int8 q [n, K], float32 a_scale [n]).  ``err``: optional int32 [1]
@@ -332,6 +357,7 @@ def prism_quant_act_rows(x, rows, inv_s=None, q=None, a_scale=None, err=None, st
     return q, a_scale
 
 
+@_under_its_stream
 def prism_w8a8_linear_rows(q, a_scale, w, w_scale, residual, residual_rows, out=None, acc_out=None,
                            split_k: int = 0, workspace=None, err=None, stream=None):
     """prism_w8a8_linear whose residual row for output row m is
@@ -375,6 +401,7 @@ def prism_w4a8_workspace_bytes(M: int, N: int, K: int, split_k: int = 0) -> int:
     return int(lib().prism_w4a8_workspace_bytes(M, N, K, split_k))
 
 
+@_under_its_stream
 def prism_w4a8_linear(q, a_scale, w4, w_scale, residual=None, out=None, acc_out=None, split_k: int = 0,
                       workspace=None, stream=None):
     """The W8A8 linear on packed 4-bit weights ``w4`` uint8 [N, K/2] (code
@@ -408,6 +435,7 @@ def prism_w4a8_linear(q, a_scale, w4, w_scale, residual=None, out=None, acc_out=
     return out
 
 
+@_under_its_stream
 def prism_unpack_w4(w4, K: int, w=None, stream=None):
     """Packed 4-bit codes uint8 [N, K/2] -> int8 [N, K]."""
     import torch
@@ -421,6 +449,7 @@ def prism_unpack_w4(w4, K: int, w=None, stream=None):
     return w
 
 
+@_under_its_stream
 def prism_act_amax(x, inv_s=None, amax=None, stream=None):
     """Row maxima max_k |x * inv_s| of bf16 ``x`` [M, K] -> float32 [M]."""
     import torch
@@ -436,6 +465,7 @@ def prism_act_amax(x, inv_s=None, amax=None, stream=None):
     return amax
 
 
+@_under_its_stream
 def prism_quant_act_amax(x, inv_s, amax, q=None, a_scale=None, stream=None):
     """prism_quant_act with given row maxima ``amax`` [M] -> (q, a_scale)."""
     import torch
@@ -455,6 +485,7 @@ def prism_quant_act_amax(x, inv_s, amax, q=None, a_scale=None, stream=None):
     return q, a_scale
 
 
+@_under_its_stream
 def prism_w8a8_gemm_s32(q, w, acc=None, split_k: int = 0, workspace=None, stream=None):
     """Exact int32 ``q @ w^T`` -> dense int32 [M, N] (no scaling)."""
     import torch
@@ -477,6 +508,7 @@ def prism_w8a8_gemm_s32(q, w, acc=None, split_k: int = 0, workspace=None, stream
     return acc
 
 
+@_under_its_stream
 def prism_w8a8_epilogue(acc, a_scale, w_scale, residual=None, out=None, stream=None):
     """bf16 out[M, N] from int32 ``acc`` [M, N] with the linear's epilogue."""
     import torch
@@ -526,6 +558,7 @@ def tp_row_parallel_linear(x, inv_s, w, w_scale, residual=None, group=None, ops=
     return ops.epilogue(acc, a_scale, w_scale, residual)
 
 
+@_under_its_stream
 def prism_w8a8_linear_noalloc(q, a_scale, w, w_scale, residual=None, out=None, acc_out=None,
                               split_k: int = 0, stream=None):
     """prism_w8a8_linear for callers that cannot supply scratch memory: split-K
@@ -547,6 +580,7 @@ def prism_readout_workspace_bytes(P: int, T: int, K: int) -> int:
     return int(lib().prism_readout_workspace_bytes(P, T, K))
 
 
+@_under_its_stream
 def prism_candidate_readout(hidden, inv_s, lm_head, lm_scale, cand_offsets, cand_ids,
                             logits=None, probs=None, err=None, workspace=None, stream=None):
     """Candidate-restricted read-out -> (logits float32 [T], probs float32 [T]).
@@ -588,6 +622,7 @@ def prism_candidate_readout(hidden, inv_s, lm_head, lm_scale, cand_offsets, cand
     return logits, probs
 
 
+@_under_its_stream
 def prism_candidate_logits(hidden, inv_s, lm_shard, lm_scale_shard, v0: int, V: int, cand_offsets, cand_ids,
                            logits=None, err=None, stream=None):
     """Logits float32 [T] of the candidates held by one vocabulary shard
@@ -622,6 +657,7 @@ def prism_candidate_logits(hidden, inv_s, lm_shard, lm_scale_shard, v0: int, V: 
     return logits
 
 
+@_under_its_stream
 def prism_candidate_softmax(logits, cand_offsets, probs=None, err=None, stream=None):
     """The read-out's candidate softmax on given logits -> probs float32 [T]."""
     import torch
@@ -672,6 +708,7 @@ def prism_debug_wait_expiry(limit_ns: int) -> None:
     _check("prism_debug_wait_expiry", lib().prism_debug_wait_expiry(int(limit_ns)))
 
 
+@_under_its_stream
 def prism_quant_act_f16(x, inv_s=None, qh=None, a_scale=None, stream=None):
     """prism_quant_act with the codes stored as float16 values (exact integers
     in [-127, 127]): bf16 ``x`` [M, K] -> (float16 qh [M, K], float32 a_scale [M])."""
@@ -694,6 +731,7 @@ def prism_quant_act_f16(x, inv_s=None, qh=None, a_scale=None, stream=None):
     return qh, a_scale
 
 
+@_under_its_stream
 def prism_codes_to_f16(w, wh=None, stream=None):
     """int8 codes [N, K] -> the same codes as float16 [N, K] (exact; the weight
     operand of prism_w8a8_linear_f16, made once at load time)."""
@@ -723,6 +761,7 @@ def new_workspace_f16(M: int, N: int, K: int, split_k: int = 0, device=None):
     return torch.zeros((n,), dtype=torch.uint8, device=device)
 
 
+@_under_its_stream
 def prism_w8a8_linear_f16(qh, a_scale, wh, w_scale, residual=None, out=None, acc_out=None,
                           split_k: int = 0, workspace=None, stream=None):
     """prism_w8a8_linear with the codes given as float16 values: ``qh`` [M, K]
