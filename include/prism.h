@@ -519,10 +519,11 @@ size_t prism_readout_workspace_bytes(int64_t P, int64_t T, int64_t K);
  * RN(x * f)), -127, 127) with f = RN(127 * RN(1 / amax)); amax < 2^-120 gives
  * scale 0 and codes 0.
  * Rows past the sequence's end are left as they are.
- * seq_lens may be set back between calls, to drop rows, as far as the start of
- * the open page (the bf16 rows of a page that was completed are not kept) or to
- * the start of any page; the next call's codes and scale are then those of the
- * rows that are left and the new ones.
+ * seq_lens may be set back between calls, to drop rows: to the start of any
+ * page; into the open page; and, while the next page has no row, to where the
+ * call that completed a page began (the bf16 rows of a completed page are not
+ * kept any longer).  The next call's codes and scale are then those of the rows
+ * that are left and the new ones.
  *   k_bf16, v_bf16    [T, H_kv, D] bf16, token stride ld?_t, head stride
  *                     ld?_h (multiples of 8, 16-byte aligned bases)
  *   seq_lens          tokens in the cache BEFORE the call (not changed)
@@ -633,6 +634,8 @@ int prism_w4g_linear(const int8_t *q, int64_t ldq, const float *a_scale,
  *              token
  *   token_ids  [R, n_ids] int32, row stride ld_ids; an id outside [0, V) sets
  *              PRISM_DEV_ERR_ID_RANGE and gives NaN
+ * Sums are binary32, of exponentials good to 2^-21; finite logits of any size
+ * (a finite fill for masked tokens among them) count as what they are.
  * A row without a finite maximum (all -inf, a NaN or +inf among its logits)
  * gives NaN and top_ids -1.  A row's outputs do not depend on the other rows.
  *   0 <= top_k <= min(V, PRISM_MAX_TOP_K); V < 2^31; R < 2^31 / 8.

@@ -64,3 +64,21 @@ def test_a_step_tried_again(cuda_device):
             codes, scales = du.quantise_block(torch.cat((head[side], row[side])).float().numpy())
             assert np.array_equal(cache[side][0, :, :7].cpu().numpy(), codes.transpose(1, 0, 2))
             assert np.array_equal(cache[2 + side][0].cpu().numpy(), scales)
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+def test_a_step_that_completed_a_page_tried_again(cuda_device, rows):
+    """The rows before it are still held while the next page has none."""
+    rng = np.random.default_rng(rows)
+    heads, d, block = 2, 64, 16
+    cache = prism.new_kv_cache(1, heads, d, block, 1)
+    table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    head = _rows(rng, block - rows, heads, d, 1.0)
+    _append(cache, table, [head], [0])
+    for n, scale in ((rows, 30.0), (rows, 0.5), (1, 0.25)):
+        new = _rows(rng, n, heads, d, scale)
+        _append(cache, table, [new], [block - rows])
+        for side in range(2):
+            codes, scales = du.quantise_block(torch.cat((head[side], new[side])).float().numpy())
+            assert np.array_equal(cache[side][0, :, :len(codes)].cpu().numpy(), codes.transpose(1, 0, 2))
+            assert np.array_equal(cache[2 + side][0].cpu().numpy(), scales)
