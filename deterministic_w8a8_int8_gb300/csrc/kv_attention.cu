@@ -30,10 +30,13 @@
 // and outputs are binary32.
 //
 // It reads the codes once: 64 sequences of 300 to 4096 tokens (289 MB, 40 heads
-// on 8 of 128) take 62 us, 4.7 TB/s; a single one of 131071 tokens (32 heads on 4
-// of 256) 60 us, 4.5 TB/s.  HBM is at 62 % then, the ALU pipe (widening, byte permutes)
-// at half its rate: neither is full, what is left is the wait for a warp's next
-// step with 12 warps an SM (three CTAs, by registers).
+// on 8 of 128) take 61 us, 4.7 TB/s; a single one of 131071 tokens (32 heads on 4
+// of 256) 59 us, 4.6 TB/s.  No unit is full then: HBM at 64 %, the ALU pipe
+// (widening, byte permutes) and the issue slots at half their rate, and the copies
+// under way (8 KB a warp, 12 warps an SM) are enough for more.  Within a warp a
+// step is a chain -- scores, their maximum over lanes, exponentials, transposition,
+// second product -- with two other warps of the scheduler beside it (three CTAs an
+// SM, by registers).
 #include <cuda_fp16.h>
 
 #include "kv_plan.cuh"

@@ -18,11 +18,15 @@
 // shared memory (128 bytes of a row a step); the activations are widened once
 // per CTA into shared memory, in the order that the weight words want.
 //
-// Up to 8 rows the issue slots bound it: a weight word costs nine instructions
-// for eight codes, and half of the slots are taken (deeper rings change nothing:
-// 5120 x 34816, one row, 3, 4, 5 stages: 25.4, 26.7, 27.6 us, 3.5 TB/s of weights).
-// With more rows the instructions themselves (608 TFLOP/s at best) take 40 % of
-// the time and the slots 45 %: 37 rows of 5120 x 34816 take 60 us.  The same on
+// Up to 8 rows no unit is full: half of the issue slots are taken (a weight word
+// costs nine instructions for eight codes), HBM is at 28 to 50 %, and the stalls
+// are at barriers and on loads -- each pass waits for its own scales at its head
+// and with them for all of the ring (8 rows of 17408 x 5120 21.8 us; 5120 x 34816,
+// one row, rings of 3, 4, 5 stages: 25.4, 26.7, 27.6 us, 3.5 TB/s of weights).
+// With more rows the instructions themselves (608 TFLOP/s at best) take 42 % of
+// the time and the slots 48 %, the contracting warps (two a scheduler) waiting at
+// barriers: 37 rows of 5120 x 34816 take 61 us.  More than 64 rows stream and widen
+// the weights again for every 64 (256 rows 353 us).  The same on
 // tcgen05 (weights widened into swizzled shared memory, group sums read back from
 // tensor memory) took 75 us, and 50 us against 36 with 12 rows: every weight then
 // passes through shared memory twice.

@@ -10,9 +10,11 @@
 // arrive.  With few rows each part is a CTA of the row's cluster; with many, a
 // CTA takes several parts or all of them in turn (a part's sums are the same
 // either way, so a row's bits do not depend on the call): 768 rows of 248000
-// took 185 us with eight CTAs a row, one row 7 us against 30 with one.  Now 95
-// us (4.0 TB/s; three quarters of the issue slots are taken: eight instructions
-// a logit) and 7.7 us.
+// took 185 us with eight CTAs a row, one row 7 us against 30 with one.  Now 96
+// us (4.0 TB/s, 62 % of the issue slots, eleven instructions a logit, in 2.5 turns
+// of the CTAs) and 7.4 us.  Rows off 16-byte boundaries (7 of 8 where V is odd) are
+// read by single logits: 768 of 248001 take 248 us.  Rows whose maximum is beyond
+// kFarRow are read twice: 178 us.
 //   Sums: a thread adds 2^y and y 2^y, y = x L - r, L = log2 e, against a
 // reference r = RN(L m), m the maximum of its first piece that has one -- one
 // fused multiply-add and one ex2 a logit, x L itself being exact inside the
