@@ -146,15 +146,17 @@ bool use_stream(PyObject* stream, int64_t device, c10::cuda::OptionalCUDAStreamG
   *out = PyLong_AsVoidPtr(v);
   Py_DECREF(v);
   if (PyErr_Occurred() != nullptr) return false;
-  v = PyObject_GetAttrString(stream, "device_index");
-  if (v == nullptr) return false;
-  const int64_t of = PyLong_AsLongLong(v);
-  Py_DECREF(v);
-  if (PyErr_Occurred() != nullptr) return false;
-  if (of != device) {
-    PyErr_Format(PyExc_ValueError, "stream must be of cuda:%lld, got one of cuda:%lld", static_cast<long long>(device),
-                 static_cast<long long>(of));
-    return false;
+  if (PyObject_HasAttrString(stream, "device_index")) {   // torch's streams know theirs; a handle alone is taken as it is
+    v = PyObject_GetAttrString(stream, "device_index");
+    if (v == nullptr) return false;
+    const int64_t of = PyLong_AsLongLong(v);
+    Py_DECREF(v);
+    if (PyErr_Occurred() != nullptr) return false;
+    if (of != device) {
+      PyErr_Format(PyExc_ValueError, "stream must be of cuda:%lld, got one of cuda:%lld", static_cast<long long>(device),
+                   static_cast<long long>(of));
+      return false;
+    }
   }
   guard->reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(*out), index));
   return true;

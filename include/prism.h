@@ -564,7 +564,8 @@ int prism_kv_append(const void *k_bf16, int64_t ldk_t, int64_t ldk_h,
  *   q_bf16, out_bf16  [T, H_q, D] bf16, strides as in prism_kv_append
  *   lse               [T, H_q] float32 dense, or NULL
  *   cu_q              [S + 1] int32 query offsets; NULL: one query each
- *                     (T == S).  Rows of no sequence are not written.
+ *                     (T == S).  Rows of no sequence are not written; where
+ *                     sequences overlap, theirs are undefined.
  *   max_q             the most queries of one sequence (1 <= max_q); a
  *                     sequence with more sets PRISM_DEV_ERR_SEQ_RANGE.
  *                     Sequences of more than 32 rows (queries x H_q / H_kv)

@@ -32,5 +32,6 @@ def test_a_stream_of_another_device_is_refused(cuda_device, i):
         call(stream=SimpleNamespace(cuda_stream=0, device_index=1))   # no such stream is ever used
     call(stream=torch.cuda.current_stream())
     call(stream=torch.cuda.ExternalStream(torch.cuda.current_stream().cuda_stream))
+    call(stream=SimpleNamespace(cuda_stream=torch.cuda.current_stream().cuda_stream))
     assert torch.cuda.current_device() == 0
     torch.cuda.synchronize()
