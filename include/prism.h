@@ -558,7 +558,9 @@ int prism_kv_append(const void *k_bf16, int64_t ldk_t, int64_t ldk_h,
  * and sum, and the weighted sums are binary32; the codes enter the tensor
  * cores exactly, the queries as binary16 of the row's largest channel (bf16
  * channels far below it lose bits), the probabilities as binary16 scaled so
- * that the largest lie between 2^9 and 2^15.  A sequence's outputs depend on
+ * that the largest lie between 2^9 and 2^15, times the page's v_scale over the
+ * largest v_scale among the keys read (pages far below it, from about 2^-20 on,
+ * lose bits beside it).  A sequence's outputs depend on
  * its own queries, keys and lengths (and on H_kv) only, not on the other
  * sequences of the call.
  *   q_bf16, out_bf16  [T, H_q, D] bf16, strides as in prism_kv_append
