@@ -168,16 +168,21 @@ def _codes(y, form):
     return dict(q=q.to(torch.int8 if form == "int8" else torch.float16), a_scale=scale)
 
 
+def _fma(a, b, c):
+    """a * b + c rounded once (the product of two 32-bit values is exact in 64)."""
+    return (a.double() * b + c).float()
+
+
 def _exp(x):
     """exp of x <= 0: x = n ln 2 + r, the series of e^r to r^7, times 2^n; each
-    step one operation in 32 bits.  Below 2^-126: 0."""
-    n = torch.round(x * 1.4426950216293335)
-    r = x - n * 0.693359375
-    r = r - n * -2.121944417012855e-04
-    p = torch.full_like(r, 1.98412701138295233e-04)
-    for a in (1.38888892251998186e-03, 8.33333376795053482e-03, 4.16666679084300995e-02, 1.66666671633720398e-01, 0.5, 1.0, 1.0):
-        p = p * r
-        p = p + a
+    step one fused operation in 32 bits.  Below 2^-126: 0."""
+    n = torch.round(x.double() * 1.44269502162933349609375).clamp_(min=-200.0).float()
+    r = _fma(n, -0.693359375, x)
+    r = _fma(n, 2.12194441701285541057586669921875e-4, r)
+    p = torch.full_like(r, 1.98412701138295233249664306640625e-4)
+    for a in (1.388888922519981861114501953125e-3, 8.333333767950534820556640625e-3, 4.16666679084300994873046875e-2,
+              0.16666667163372039794921875, 0.5, 1.0, 1.0):
+        p = _fma(p, r, a)
     two_n = ((n.clamp(min=-126.0).to(torch.int32) + 127) << 23).view(torch.float32)
     return torch.where(n >= -126.0, p * two_n, 0.0)
 
