@@ -28,11 +28,14 @@ Entry points (same names as the C ABI):
   prism_w8a8_linear_f16(qh, a_scale, wh, w_scale, ...) -> out   codes given as float16
   prism_kv_append, prism_kv_attention, prism_w4g_linear, prism_token_logprobs
                                                  the decode step (decode.py)
+  prism_norm_quant, prism_head_norm_quant, prism_glu_quant, prism_linear_attention
+                                                 between a layer's linears (layer.py)
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import importlib
 import inspect
 import os
 import threading
@@ -58,7 +61,12 @@ PRISM_DEV_ERR_DUPLICATE = 8
 PRISM_DEV_ERR_ROW_RANGE = 16
 PRISM_DEV_ERR_PAGE_RANGE = 32
 PRISM_DEV_ERR_SEQ_RANGE = 64
+PRISM_DEV_ERR_STATE_RANGE = 128
 PRISM_MAX_TOP_K = 32
+PRISM_FORM_INT8 = 0
+PRISM_FORM_F16 = 1
+PRISM_FORM_BF16 = 2
+PRISM_MAX_ROW = 32768
 PRISM_DEVSTATUS_WAIT_TIMEOUT = 1
 
 # (restype, argtypes) of every symbol the header declares
@@ -103,6 +111,14 @@ SIGNATURES = {
     "prism_w4g_linear": (_I32, [_P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64,
                                 _I64, _P]),
     "prism_token_logprobs": (_I32, [_P, _I32, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P]),
+    "prism_norm_quant": (_I32, [_P, _I64, _P, _I64, ctypes.c_float, _P, _P, ctypes.c_float, _I64, _I64, _P, _I64, _I32,
+                                _P, _I64, _P, _P]),
+    "prism_head_norm_quant": (_I32, [_P, _I64, _P, _P, _I64, _P, ctypes.c_float, _I64, _I64, _I64, _I32, _P, _I64, _P, _P]),
+    "prism_glu_quant": (_I32, [_P, _I64, _P, _I64, _I64, _I32, _P, _I64, _P, _P]),
+    "prism_linear_attention_workspace_bytes": (_SZ, [_I64] * 6),
+    "prism_linear_attention": (_I32, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64,
+                                      _I64, ctypes.c_float, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _P, _SZ, _P,
+                                      _P]),
     "prism_status_string": (ctypes.c_char_p, [_I32]),
     "prism_version": (_I32, []),
     "prism_w8a8_kernel_kind": (_I32, [_I64, _I64, _I64]),
@@ -803,14 +819,18 @@ def prism_w8a8_linear_f16(qh, a_scale, wh, w_scale, residual=None, out=None, acc
 
 _DECODE = ("KvCache", "new_kv_cache", "prism_kv_append", "prism_kv_attention", "prism_kv_attention_workspace_bytes",
            "prism_w4g_linear", "prism_token_logprobs")
+_LAYER = ("prism_norm_quant", "prism_head_norm_quant", "prism_glu_quant", "prism_linear_attention",
+          "prism_linear_attention_workspace_bytes")
 
 
 def __getattr__(name):
-    """The decode-step entry points live in decode.py, which imports torch; like
-    the functions above, that happens at their first use."""
-    if name in _DECODE:
-        from . import decode
-        for n in _DECODE:
-            globals()[n] = getattr(decode, n)
-        return globals()[name]
+    """The decode-step entry points live in decode.py and those between a layer's
+    linears in layer.py, which import torch; like the functions above, that happens
+    at their first use."""
+    for names, module in ((_DECODE, "decode"), (_LAYER, "layer")):
+        if name in names:
+            found = importlib.import_module("." + module, __name__)
+            for n in names:
+                globals()[n] = getattr(found, n)
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

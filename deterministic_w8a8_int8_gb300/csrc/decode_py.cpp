@@ -1,5 +1,5 @@
-// decode_py.cpp -- the Python side of the decode-step entry points, as an
-// extension module over libprism.so's C ABI (include/prism.h): reads the
+// decode_py.cpp -- the Python side of the decode-step entry points and of those
+// between a layer's linears, as an extension module over libprism.so's C ABI (include/prism.h): reads the
 // tensors' addresses, shapes and strides, checks them, allocates outputs and
 // workspaces from torch's allocator, and calls.
 //
@@ -425,6 +425,253 @@ PyObject* py_logprobs(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------- between a layer's linears ---
+// The rows' codes (or values): allocated, [M, K], with their scales.
+struct Codes {
+  int form;
+  at::Tensor q, scale;
+  int64_t ldq;
+};
+
+bool read_form(PyObject* obj, Codes* c) {
+  const char* name = PyUnicode_Check(obj) ? PyUnicode_AsUTF8(obj) : "";
+  if (name == nullptr) return false;
+  const std::string form = name;
+  c->form = form == "int8" ? PRISM_FORM_INT8 : form == "f16" ? PRISM_FORM_F16 : form == "bf16" ? PRISM_FORM_BF16 : -1;
+  if (c->form < 0) PyErr_SetString(PyExc_ValueError, "form must be \"int8\", \"f16\" or \"bf16\"");
+  return c->form >= 0;
+}
+
+void make_codes(Codes* c, int64_t m, int64_t k, int64_t device) {
+  const int64_t shape[2] = {m, k};
+  c->ldq = k;
+  c->q = empty(c->form == PRISM_FORM_INT8 ? at::kChar : c->form == PRISM_FORM_F16 ? at::kHalf : at::kBFloat16, device, 2, shape);
+  if (c->form != PRISM_FORM_BF16) c->scale = empty(at::kFloat, device, 1, &m);
+}
+
+void* address(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+// (q, a_scale) or (q, a_scale, last); None for a tensor that is not there.
+PyObject* tuple_of(Codes* c, PyObject* last) {
+  PyObject* tuple = PyTuple_New(last != nullptr ? 3 : 2);
+  PyObject* items[3] = {tuple != nullptr ? THPVariable_Wrap(std::move(c->q)) : nullptr, nullptr, last};
+  if (items[0] != nullptr) items[1] = c->scale.defined() ? THPVariable_Wrap(std::move(c->scale)) : Py_NewRef(Py_None);
+  if (items[1] == nullptr) {
+    Py_XDECREF(tuple);
+    Py_XDECREF(items[0]);
+    Py_XDECREF(last);
+    return nullptr;
+  }
+  for (int i = 0; i < (last != nullptr ? 3 : 2); ++i) PyTuple_SET_ITEM(tuple, i, items[i]);
+  return tuple;
+}
+
+// The address of a dense operand.
+bool dense(PyObject* obj, const char* name, at::ScalarType type, int64_t device, int n, const int64_t* shape, void** ptr) {
+  Operand o;
+  if (!operand(obj, name, type, device, n, shape, true, &o)) return false;
+  *ptr = o.ptr;
+  return true;
+}
+
+// norm_quant(x, weight, delta, alpha, post_weight, eps, h, form, stream) -> (q, a_scale, h)
+PyObject* py_norm_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!argc_is(n, 9)) return nullptr;
+  int64_t device, shape[2];
+  Operand x, d, h;
+  void *weight, *post, *stream;
+  Codes c;
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  if (!first_operand(a[0], "x", 2, &device, shape) || !operand(a[0], "x", at::kBFloat16, device, 2, shape, false, &x) ||
+      !dense(a[1], "weight", at::kFloat, device, 1, shape + 1, &weight) ||
+      (a[2] != Py_None && !operand(a[2], "delta", at::kBFloat16, device, 2, shape, false, &d)) ||
+      !optional(a[4], "post_weight", at::kFloat, device, 1, shape + 1, &post) ||
+      (a[6] != Py_None && !operand(a[6], "h", at::kBFloat16, device, 2, shape, false, &h)))
+    return nullptr;
+  const double alpha = PyFloat_AsDouble(a[3]), eps = PyFloat_AsDouble(a[5]);
+  if (PyErr_Occurred() != nullptr || !read_form(a[7], &c) || !use_stream(a[8], device, &guard, &stream)) return nullptr;
+  make_codes(&c, shape[0], shape[1], device);
+  at::Tensor made;
+  if (a[2] != Py_None && a[6] == Py_None) {
+    made = empty(at::kBFloat16, device, 2, shape);
+    h.ptr = made.data_ptr();
+    h.stride[0] = shape[1];
+  }
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = prism_norm_quant(x.ptr, x.stride[0], d.ptr, d.stride[0], static_cast<float>(alpha), static_cast<float*>(post),
+                            static_cast<float*>(weight), static_cast<float>(eps), shape[0], shape[1], h.ptr, h.stride[0],
+                            c.form, c.q.data_ptr(), c.ldq, static_cast<float*>(address(c.scale)), stream);
+  Py_END_ALLOW_THREADS
+  if (!accepted("prism_norm_quant", status)) return nullptr;
+  PyObject* last = made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(a[2] == Py_None ? a[0] : a[6]);
+  return last == nullptr ? nullptr : tuple_of(&c, last);
+  END_HANDLE_TH_ERRORS
+}
+
+// A [M, H, D] or [M, H * D] bf16 operand as rows of H * D values: its heads lie side by side.
+bool rows_operand(PyObject* obj, const char* name, int64_t device, int dims, const int64_t* shape, Operand* o) {
+  if (!operand(obj, name, at::kBFloat16, device, dims, shape, false, o)) return false;
+  if (dims == 3 && shape[1] > 1 && o->stride[1] != shape[2]) {
+    PyErr_Format(PyExc_ValueError, "%s's heads must lie side by side", name);
+    return false;
+  }
+  return true;
+}
+
+// head_norm_quant(x, weight, gate, inv_s, eps, form, stream) -> (q, a_scale)
+PyObject* py_head_norm_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!argc_is(n, 7)) return nullptr;
+  int64_t device, shape[3], d;
+  Operand x, z;
+  void *weight, *inv, *stream;
+  Codes c;
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  if (!shape_of(a[1], "weight", 1, &d) || !first_operand(a[0], "x", 3, &device, shape)) return nullptr;
+  const int64_t m = shape[0], h = shape[1], k = h * d;
+  shape[2] = d;
+  if (!rows_operand(a[0], "x", device, 3, shape, &x) || !dense(a[1], "weight", at::kFloat, device, 1, &d, &weight) ||
+      (a[2] != Py_None && !rows_operand(a[2], "gate", device, 3, shape, &z)) ||
+      !optional(a[3], "inv_s", at::kFloat, device, 1, &k, &inv))
+    return nullptr;
+  const double eps = PyFloat_AsDouble(a[4]);
+  if (PyErr_Occurred() != nullptr || !read_form(a[5], &c) || !use_stream(a[6], device, &guard, &stream)) return nullptr;
+  make_codes(&c, m, k, device);
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = prism_head_norm_quant(x.ptr, x.stride[0], static_cast<float*>(weight), z.ptr, z.stride[0],
+                                 static_cast<float*>(inv), static_cast<float>(eps), m, h, d, c.form, c.q.data_ptr(), c.ldq,
+                                 static_cast<float*>(address(c.scale)), stream);
+  Py_END_ALLOW_THREADS
+  if (!accepted("prism_head_norm_quant", status)) return nullptr;
+  return tuple_of(&c, nullptr);
+  END_HANDLE_TH_ERRORS
+}
+
+// glu_quant(gate_up, inv_s, form, stream) -> (q, a_scale)
+PyObject* py_glu_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!argc_is(n, 4)) return nullptr;
+  int64_t device, shape[2];
+  Operand x;
+  void *inv, *stream;
+  Codes c;
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  if (!first_operand(a[0], "gate_up", 2, &device, shape)) return nullptr;
+  const int64_t m = shape[0], f = shape[1] / 2;
+  if (shape[1] % 2) {
+    PyErr_SetString(PyExc_ValueError, "gate_up must be [M, 2 F]");
+    return nullptr;
+  }
+  if (!operand(a[0], "gate_up", at::kBFloat16, device, 2, shape, false, &x) ||
+      !optional(a[1], "inv_s", at::kFloat, device, 1, &f, &inv) || !read_form(a[2], &c) ||
+      !use_stream(a[3], device, &guard, &stream))
+    return nullptr;
+  make_codes(&c, m, f, device);
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = prism_glu_quant(x.ptr, x.stride[0], static_cast<float*>(inv), m, f, c.form, c.q.data_ptr(), c.ldq,
+                           static_cast<float*>(address(c.scale)), stream);
+  Py_END_ALLOW_THREADS
+  if (!accepted("prism_glu_quant", status)) return nullptr;
+  return tuple_of(&c, nullptr);
+  END_HANDLE_TH_ERRORS
+}
+
+// linear_attention(q, k, v, log_decay, state, state_in, state_out, cu, max_len, scale, out, workspace, err, stream) -> out
+PyObject* py_linear_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (!argc_is(n, 14)) return nullptr;
+  int64_t device, qs[3], vs[3], max_len, num_states = 0, ws_bytes = 0;
+  Operand q, k, v, g, o;
+  void *state, *in, *out, *cu, *err, *stream, *ws = nullptr;
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  if (!first_operand(a[0], "q", 3, &device, qs) || !shape_of(a[2], "v", 3, vs)) return nullptr;
+  const int64_t rows = qs[0], dk = qs[2], heads = vs[1], dv = vs[2];
+  vs[0] = rows;
+  const at::Tensor* decay = tensor(a[3], "log_decay");
+  if (decay == nullptr) return nullptr;
+  const int64_t g_shape[2] = {rows, heads};
+  const bool per_token = decay->dim() != 1;
+  if (!operand(a[0], "q", at::kBFloat16, device, 3, qs, false, &q) ||
+      !operand(a[1], "k", at::kBFloat16, device, 3, qs, false, &k) ||
+      !operand(a[2], "v", at::kBFloat16, device, 3, vs, false, &v))
+    return nullptr;
+  if (per_token && decay->dim() != 2) {
+    PyErr_SetString(PyExc_ValueError, "log_decay must be [T, H_v] or [H_v]");
+    return nullptr;
+  }
+  if (!operand(a[3], "log_decay", at::kFloat, device, per_token ? 2 : 1, per_token ? g_shape : &heads, false, &g)) return nullptr;
+  const int64_t ldd = !per_token ? 0 : rows > 1 ? g.stride[0] : heads;
+  if (a[4] != Py_None) {
+    int64_t shape[4];
+    if (!shape_of(a[4], "state", 4, shape)) return nullptr;
+    num_states = shape[0], shape[1] = heads, shape[2] = dk, shape[3] = dv;
+    if (!optional(a[4], "state", at::kFloat, device, 4, shape, &state)) return nullptr;
+  } else {
+    state = nullptr;
+  }
+  // the number of sequences: that of the states' indices, of the offsets, or one for each token
+  int64_t seqs = rows, offsets = 0;
+  if (a[7] != Py_None) {
+    if (!shape_of(a[7], "cu", 1, &offsets)) return nullptr;
+    if (offsets < 1) {
+      PyErr_SetString(PyExc_ValueError, "cu must be [S + 1]");
+      return nullptr;
+    }
+    seqs = offsets - 1;
+  }
+  if (!optional(a[7], "cu", at::kInt, device, 1, &offsets, &cu) ||
+      !optional(a[5], "state_in", at::kInt, device, 1, &seqs, &in) ||
+      !optional(a[6], "state_out", at::kInt, device, 1, &seqs, &out))
+    return nullptr;
+  if (state == nullptr && (in != nullptr || out != nullptr)) {
+    PyErr_SetString(PyExc_ValueError, "state_in and state_out need state");
+    return nullptr;
+  }
+  max_len = cu == nullptr || rows < 1 ? 1 : rows;
+  if (a[8] != Py_None && !integer(a[8], &max_len)) return nullptr;
+  const double scale = a[9] == Py_None ? std::pow(static_cast<double>(dk), -0.5) : PyFloat_AsDouble(a[9]);
+  if (PyErr_Occurred() != nullptr) return nullptr;
+  if (a[10] != Py_None && !operand(a[10], "out", at::kBFloat16, device, 3, vs, false, &o)) return nullptr;
+  if (!optional(a[12], "err", at::kInt, device, 1, &kOne, &err) || !use_stream(a[13], device, &guard, &stream)) return nullptr;
+  at::Tensor held, made;
+  if (a[11] != Py_None) {
+    const at::Tensor* w = tensor(a[11], "workspace");
+    if (w == nullptr) return nullptr;
+    if (index_of(*w) != device || !w->is_contiguous()) {
+      PyErr_Format(PyExc_ValueError, "workspace must be a contiguous tensor on cuda:%lld", static_cast<long long>(device));
+      return nullptr;
+    }
+    ws = w->data_ptr();
+    ws_bytes = static_cast<int64_t>(w->nbytes());
+  } else {
+    ws_bytes = static_cast<int64_t>(prism_linear_attention_workspace_bytes(seqs, rows, max_len, heads, dk, dv));
+    if (ws_bytes > 0) {
+      held = empty(at::kByte, device, 1, &ws_bytes);
+      ws = held.data_ptr();
+    }
+  }
+  if (a[10] == Py_None) {
+    made = empty(at::kBFloat16, device, 3, vs);
+    o.ptr = made.data_ptr();
+    o.stride[0] = heads * dv, o.stride[1] = dv;
+  }
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = prism_linear_attention(q.ptr, q.stride[0], q.stride[1], k.ptr, k.stride[0], k.stride[1], v.ptr, v.stride[0],
+                                  v.stride[1], static_cast<float*>(g.ptr), ldd, static_cast<float*>(state),
+                                  static_cast<int32_t*>(in), static_cast<int32_t*>(out), static_cast<int32_t*>(cu), o.ptr,
+                                  o.stride[0], o.stride[1], static_cast<float>(scale), seqs, rows, max_len, num_states, qs[1],
+                                  heads, dk, dv, ws, static_cast<size_t>(ws_bytes), static_cast<int32_t*>(err), stream);
+  Py_END_ALLOW_THREADS
+  if (!accepted("prism_linear_attention", status)) return nullptr;
+  return a[10] == Py_None ? THPVariable_Wrap(std::move(made)) : Py_NewRef(a[10]);
+  END_HANDLE_TH_ERRORS
+}
+
 // setup(check): check(name, status) raises for a status
 PyObject* py_setup(PyObject*, PyObject* check) {
   Py_XSETREF(g_check, Py_NewRef(check));
@@ -441,6 +688,10 @@ PyMethodDef methods[] = {{"setup", py_setup, METH_O, nullptr},
                          {"attention", fast(py_attention), METH_FASTCALL, nullptr},
                          {"w4g_linear", fast(py_w4g), METH_FASTCALL, nullptr},
                          {"token_logprobs", fast(py_logprobs), METH_FASTCALL, nullptr},
+                         {"norm_quant", fast(py_norm_quant), METH_FASTCALL, nullptr},
+                         {"head_norm_quant", fast(py_head_norm_quant), METH_FASTCALL, nullptr},
+                         {"glu_quant", fast(py_glu_quant), METH_FASTCALL, nullptr},
+                         {"linear_attention", fast(py_linear_attention), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_decode", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

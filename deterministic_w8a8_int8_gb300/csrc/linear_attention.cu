@@ -1,0 +1,571 @@
+// linear_attention.cu -- linear attention with a decay for each head:
+//   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale * q_t S_t
+// with a state S [Dk, Dv] in binary32 for each (sequence, value head).
+//
+// Up to kFewTokens tokens of a sequence (decode steps, drafted tokens): the
+// recurrence as it stands.  The state is read once into registers, every token
+// updates it and reads it out, and it is written once: bytes, 8 Dk Dv a head,
+// bound it.
+//
+// More tokens: chunks of 64.  With G_i the sum of the chunk's decays up to token
+// i, w_ij = e^{G_i - G_j} and S the state that enters,
+//   o_i = scale * (e^{G_i} q_i S + sum_{j <= i} w_ij (q_i . k_j) v_j)
+//   S   = e^{G_C} S + sum_j e^{G_C - G_j} k_j v_j^T
+// on the tensor cores (mma.sync m16n8k16, bf16 operands, binary32 sums).  Each warp
+// keeps 16 columns of the state in registers, transposed: the result of its
+// update, S^T += (w v)^T k, is laid out among the lanes as the operand that q S
+// wants.  What is not bf16 already is split into bf16 parts: scores and the state
+// where it is read out into two (2^-17 of the value), the decayed values of the
+// update into three (2^-25), so that states are as good as binary32 sums.  Sums
+// of decays are kept as two binary32 numbers (from a scan in 64 bits): their
+// differences decide.
+//
+// A long sequence is cut into segments (by its length and the number of heads
+// alone, so that a sequence's bits do not depend on the batch): a first kernel
+// forms each segment's own state from zero, and the second starts each segment
+// from the states and decays of those before it.
+#include <type_traits>
+
+#include "layer.cuh"
+
+namespace prism {
+namespace {
+
+constexpr int kFewTokens = 16;
+constexpr int kChunk = 64;
+constexpr int kGroups = 8;            // rows of the state are divided among as many groups of threads (few tokens)
+constexpr int kSegChunks = 4;         // chunks of a segment at least
+constexpr int kFillCtas = 304;        // segments times heads of one sequence at most: two CTAs on each of 152 SMs
+constexpr float kMinDecay = -16384.0f;   // e^x = 0 from far above it; sums of 64 stay finite
+
+// Segments that a sequence of n tokens is cut into at most, the chunks of each,
+// and as many as that makes.
+__host__ __device__ __forceinline__ int64_t most_segments(int64_t n, int64_t Hv) {
+  const int64_t cap = kFillCtas / Hv, segs = n / (kSegChunks * kChunk);
+  return segs > cap ? (cap < 1 ? 1 : cap) : segs < 1 ? 1 : segs;
+}
+__host__ __device__ __forceinline__ int64_t segment_chunks(int64_t n, int64_t Hv) {
+  const int64_t chunks = (n + kChunk - 1) / kChunk, segs = most_segments(n, Hv);
+  return (chunks + segs - 1) / segs;
+}
+__host__ __device__ __forceinline__ int64_t segment_count(int64_t n, int64_t Hv) {
+  const int64_t chunks = (n + kChunk - 1) / kChunk, each = segment_chunks(n, Hv);
+  return (chunks + each - 1) / each;
+}
+// A sequence in segments has a place in the workspace for each but the last, and
+// one for the state that it starts from: no more than whole lengths of
+// kSegChunks chunks among its tokens.
+__host__ __device__ __forceinline__ int64_t first_place(int64_t first_token) { return first_token / (kSegChunks * kChunk); }
+
+struct Span {
+  int64_t b, n;
+  int64_t in, out;     // states: -1 for none
+  bool bad;            // its rows get NaN, its state is not written
+};
+// Sequence s; false where its offsets are malformed (no rows to answer for).
+__device__ __forceinline__ bool span_of(const LinAttnArgs& a, int64_t s, bool report, Span& p) {
+  const int64_t b = a.cu != nullptr ? a.cu[s] : s, e = a.cu != nullptr ? a.cu[s + 1] : s + 1;
+  p.b = b;
+  p.n = e - b;
+  p.in = a.state_in != nullptr ? a.state_in[s] : -1;
+  p.out = a.state_out != nullptr ? a.state_out[s] : -1;
+  const bool offsets = b >= 0 && e >= b && e <= a.T;
+  const bool states = p.in >= -1 && p.in < a.num_states && p.out >= -1 && p.out < a.num_states;
+  const bool length = p.n <= a.max_len;
+  if (report && a.err != nullptr) {
+    if (!offsets || !length) atomicOr(a.err, PRISM_DEV_ERR_SEQ_RANGE);
+    if (!states) atomicOr(a.err, PRISM_DEV_ERR_STATE_RANGE);
+  }
+  p.bad = !states || !length;
+  return offsets;
+}
+
+__device__ __forceinline__ float decay_of(const LinAttnArgs& a, int64_t token, int h) {
+  const float g = __ldg(a.decay + token * a.ldd_t + h);
+  return g < kMinDecay ? kMinDecay : g;
+}
+
+// ------------------------------------------------------------- few tokens ---
+// One (sequence, head) and `width` of its columns from c0 on: kGroups groups of
+// threads, group g on rows [g R, (g + 1) R), a thread on 4 columns.  Column sums
+// are added in the order of the rows, whatever the width.
+template <int DK>
+__device__ __forceinline__ void few_tokens(const LinAttnArgs& a, const Span& p, int hv, int c0, int width, float* smem) {
+  constexpr int R = DK / kGroups;
+  float* s_q = smem;                               // [kFewTokens][DK]
+  float* s_k = s_q + kFewTokens * DK;
+  float* s_o = s_k + kFewTokens * DK;              // [2][kGroups][width]
+  const int lanes = width >> 2, tid = threadIdx.x, group = tid / lanes, col = (tid % lanes) * 4;
+  const int n = static_cast<int>(p.n), hk = hv / a.G;
+  const int64_t plane = static_cast<int64_t>(DK) * a.Dv;
+  float4 st[R];
+  if (p.in >= 0 && !p.bad) {
+    const float* src = a.state + (p.in * a.Hv + hv) * plane + static_cast<int64_t>(group * R) * a.Dv + c0 + col;
+#pragma unroll
+    for (int i = 0; i < R; ++i) st[i] = __ldcs(reinterpret_cast<const float4*>(src + static_cast<int64_t>(i) * a.Dv));
+  } else {
+    const float x = p.bad ? __uint_as_float(0x7fc00000u) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) st[i] = make_float4(x, x, x, x);
+  }
+  for (int i = tid; i < n * (DK / 8); i += blockDim.x) {
+    const int t = i / (DK / 8), c = i % (DK / 8) * 8;
+    const uint4 qv = *reinterpret_cast<const uint4*>(a.q + (p.b + t) * a.ldq_t + hk * a.ldq_h + c);
+    const uint4 kv = *reinterpret_cast<const uint4*>(a.k + (p.b + t) * a.ldk_t + hk * a.ldk_h + c);
+    float4* qd = reinterpret_cast<float4*>(s_q + t * DK + c);
+    float4* kd = reinterpret_cast<float4*>(s_k + t * DK + c);
+    qd[0] = make_float4(bf16_lo(qv.x), bf16_hi(qv.x), bf16_lo(qv.y), bf16_hi(qv.y));
+    qd[1] = make_float4(bf16_lo(qv.z), bf16_hi(qv.z), bf16_lo(qv.w), bf16_hi(qv.w));
+    kd[0] = make_float4(bf16_lo(kv.x), bf16_hi(kv.x), bf16_lo(kv.y), bf16_hi(kv.y));
+    kd[1] = make_float4(bf16_lo(kv.z), bf16_hi(kv.z), bf16_lo(kv.w), bf16_hi(kv.w));
+  }
+  __syncthreads();
+  for (int t = 0; t < n; ++t) {
+    const float d = expf(decay_of(a, p.b + t, hv));
+    const uint2 vv = *reinterpret_cast<const uint2*>(a.v + (p.b + t) * a.ldv_t + hv * a.ldv_h + c0 + col);
+    const float4 v = make_float4(bf16_lo(vv.x), bf16_hi(vv.x), bf16_lo(vv.y), bf16_hi(vv.y));
+    const float* q = s_q + t * DK + group * R;
+    const float* k = s_k + t * DK + group * R;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float ki = k[i], qi = q[i];
+      st[i].x = fmaf(ki, v.x, d * st[i].x);
+      st[i].y = fmaf(ki, v.y, d * st[i].y);
+      st[i].z = fmaf(ki, v.z, d * st[i].z);
+      st[i].w = fmaf(ki, v.w, d * st[i].w);
+      o.x = fmaf(qi, st[i].x, o.x);
+      o.y = fmaf(qi, st[i].y, o.y);
+      o.z = fmaf(qi, st[i].z, o.z);
+      o.w = fmaf(qi, st[i].w, o.w);
+    }
+    float* red = s_o + (t & 1) * kGroups * width;
+    *reinterpret_cast<float4*>(red + group * width + col) = o;
+    __syncthreads();   // the other half was read before the last barrier
+    for (int c = tid; c < width; c += blockDim.x) {
+      float sum = red[c];
+#pragma unroll
+      for (int g = 1; g < kGroups; ++g) sum += red[g * width + c];
+      a.out[(p.b + t) * a.ldo_t + hv * a.ldo_h + c0 + c] = static_cast<uint16_t>(float_to_bf16_rne(sum * a.scale));
+    }
+  }
+  if (p.out >= 0 && !p.bad) {
+    float* dst = a.state + (p.out * a.Hv + hv) * plane + static_cast<int64_t>(group * R) * a.Dv + c0 + col;
+#pragma unroll
+    for (int i = 0; i < R; ++i) __stcs(reinterpret_cast<float4*>(dst + static_cast<int64_t>(i) * a.Dv), st[i]);
+  }
+}
+constexpr int few_smem(int DK, int width) { return (2 * kFewTokens * DK + 2 * kGroups * width) * 4; }
+
+// The rows of a sequence that cannot be answered.
+__device__ __forceinline__ void spoil(const LinAttnArgs& a, const Span& p, int hv, int c0, int width) {
+  for (int64_t i = threadIdx.x; i < p.n * width; i += blockDim.x)
+    a.out[(p.b + i / width) * a.ldo_t + hv * a.ldo_h + c0 + i % width] = static_cast<uint16_t>(kBf16NaN);
+}
+
+// Calls without longer sequences: a CTA for each `width` columns of a (sequence, head).
+template <int DK>
+__global__ void __launch_bounds__(256) linear_few_kernel(const __grid_constant__ LinAttnArgs a, int width) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  pdl_wait();
+  const int slices = a.Dv / width, c0 = static_cast<int>(blockIdx.x % slices) * width;
+  const int64_t s = blockIdx.x / slices;
+  Span p;
+  if (span_of(a, s, blockIdx.y == 0 && c0 == 0 && threadIdx.x == 0, p)) {
+    if (p.n > kFewTokens) {   // only where it is malformed
+      spoil(a, p, blockIdx.y, c0, width);
+    } else {
+      few_tokens<DK>(a, p, blockIdx.y, c0, width, reinterpret_cast<float*>(smem));
+    }
+  }
+  pdl_trigger();
+}
+
+// ----------------------------------------------------------------- chunks ---
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two values as a pair of bf16, and what that leaves of them.
+__device__ __forceinline__ uint32_t split_bf16(float& lo, float& hi) {
+  const uint32_t r = pack_bf16(lo, hi);
+  lo -= bf16_lo(r);
+  hi -= bf16_hi(r);
+  return r;
+}
+// Place of 16-byte piece `ch` of row `row` in a tile of rows of W values: the
+// eight rows of a matrix touch all banks.
+template <int W>
+__device__ __forceinline__ uint32_t piece(int row, int ch) {
+  return static_cast<uint32_t>(row * (W * 2) + ((ch ^ (row & 7)) << 4));
+}
+
+// Scores lie in blocks of 16 rows and 16 columns, those on and below the diagonal alone.
+constexpr int kScoreBlocks = kChunk / 16 * (kChunk / 16 + 1) / 2;
+__device__ __forceinline__ uint32_t score_place(int row, int ch) {
+  const int m = row >> 4, r = row & 15;
+  return static_cast<uint32_t>((m * (m + 1) / 2 + (ch >> 1)) * 512 + r * 32 + (((ch ^ (r >> 2)) & 1) << 4));
+}
+
+template <int DK, int DV>
+struct Tile {
+  static constexpr int kWarps = DV / 16, kThreads = kWarps * 32;
+  static constexpr int kQ = kChunk * DK * 2, kV = kChunk * DV * 2, kP = kScoreBlocks * 512;
+  static constexpr int kStage = 2 * kQ + kV;
+  static constexpr int kBytes = 2 * kStage + 2 * kP;
+  static constexpr int kLocalBytes = 2 * (kQ + kV);
+};
+
+// Segment `blockIdx.x % segs` of a (sequence, head).  kLocal: its state from
+// zero, into the workspace.
+template <int DK, int DV, bool kLocal>
+__global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
+    linear_chunk_kernel(const __grid_constant__ LinAttnArgs a, int max_segs) {
+  using L = Tile<DK, DV>;
+  constexpr int kWarps = L::kWarps, kThreads = L::kThreads, NT = DK / 8;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 s_g[2][kChunk];              // decays summed up to a token, in two parts
+  __shared__ float s_eg[2][kChunk], s_w[2][kChunk], s_tot[2];   // e^{G_i}, e^{G_C - G_i}, e^{G_C}
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, lr = lane >> 2, lc = lane & 3;
+  const int hv = blockIdx.y, hk = hv / a.G;
+  const int64_t s = blockIdx.x / max_segs;
+  const int seg = static_cast<int>(blockIdx.x % max_segs);
+  Span p;
+  const bool ok = span_of(a, s, !kLocal && seg == 0 && hv == 0 && tid == 0, p);
+  if (!ok) return;
+  if (p.bad || p.n <= kFewTokens) {
+    if (kLocal || seg != 0) return;
+    if (p.n > kFewTokens) {
+      spoil(a, p, hv, 0, DV);
+    } else {
+      few_tokens<DK>(a, p, hv, 0, DV, reinterpret_cast<float*>(smem));
+    }
+    return;
+  }
+  const int64_t each = segment_chunks(p.n, a.Hv);
+  const int segs = static_cast<int>(segment_count(p.n, a.Hv));
+  if (seg >= segs || (kLocal && seg + 1 == segs)) return;   // nothing comes after the last one
+  const int64_t t0 = seg * each * kChunk, t1 = min(p.n, t0 + each * kChunk);
+  const int chunks = static_cast<int>((t1 - t0 + kChunk - 1) / kChunk);
+
+  // the state, transposed: warp w has columns 16 w .. of it, lane (r, c) of tile t
+  // columns r, r + 8 of those and rows 8 t + 2 c, + 1
+  float st[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) st[t][0] = st[t][1] = st[t][2] = st[t][3] = 0.0f;
+  constexpr int64_t kPart = DK * DV + 4;
+  float* part = a.ws + (first_place(p.b) * a.Hv + hv) * kPart;   // of the sequence's first segment
+  const int64_t part_step = a.Hv * kPart;
+  const int64_t at = (static_cast<int64_t>(2 * lc)) * DV + warp * 16 + lr;
+  auto read_part = [&](const float* ps) {
+    const float d = ps[DK * DV];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float4 x = *reinterpret_cast<const float4*>(ps + (t * kThreads + tid) * 4);
+      st[t][0] = fmaf(d, st[t][0], x.x);
+      st[t][1] = fmaf(d, st[t][1], x.y);
+      st[t][2] = fmaf(d, st[t][2], x.z);
+      st[t][3] = fmaf(d, st[t][3], x.w);
+    }
+  };
+  auto write_part = [&](float* ps, float d) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      *reinterpret_cast<float4*>(ps + (t * kThreads + tid) * 4) = make_float4(st[t][0], st[t][1], st[t][2], st[t][3]);
+    if (tid == 0) ps[DK * DV] = d;
+  };
+  // The first place holds the state that the sequence starts from: with several
+  // segments, the last may have written the state back before another begins.
+  if (kLocal ? seg == 0 : segs == 1) {
+    if (p.in >= 0) {
+      const float* src = a.state + (p.in * a.Hv + hv) * (DK * DV) + at;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        st[t][0] = src[8 * t * DV];
+        st[t][1] = src[(8 * t + 1) * DV];
+        st[t][2] = src[8 * t * DV + 8];
+        st[t][3] = src[(8 * t + 1) * DV + 8];
+      }
+    }
+    if constexpr (kLocal) {
+      write_part(part, 0.0f);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) st[t][0] = st[t][1] = st[t][2] = st[t][3] = 0.0f;
+    }
+  } else if constexpr (!kLocal) {
+    for (int i = 0; i <= seg; ++i) read_part(part + i * part_step);
+  }
+
+  const uint32_t base = smem_u32(smem);
+  auto stage_k = [&](int c) { return base + (c & 1) * (kLocal ? L::kQ + L::kV : L::kStage); };
+  auto stage_v = [&](int c) { return stage_k(c) + L::kQ; };
+  auto stage_q = [&](int c) { return stage_v(c) + L::kV; };
+  const uint32_t p_hi = base + 2 * L::kStage, p_lo = p_hi + L::kP;
+  auto copy = [&](int c) {
+    if (c < chunks) {
+      const int64_t r0 = t0 + static_cast<int64_t>(c) * kChunk;
+      auto rows = [&](auto width, uint32_t dst, const uint16_t* src, int64_t ld) {
+        constexpr int W = decltype(width)::value;
+#pragma unroll
+        for (int i = tid; i < kChunk * W / 8; i += kThreads) {
+          const int row = i / (W / 8), ch = i % (W / 8);
+          const bool live = r0 + row < t1;
+          cp_async_16(dst + piece<W>(row, ch), src + (live ? r0 + row : r0) * ld + ch * 8, live ? 16 : 0);
+        }
+      };
+      rows(std::integral_constant<int, DK>(), stage_k(c), a.k + p.b * a.ldk_t + hk * a.ldk_h, a.ldk_t);
+      rows(std::integral_constant<int, DV>(), stage_v(c), a.v + p.b * a.ldv_t + hv * a.ldv_h, a.ldv_t);
+      if constexpr (!kLocal) rows(std::integral_constant<int, DK>(), stage_q(c), a.q + p.b * a.ldq_t + hk * a.ldq_h, a.ldq_t);
+    }
+    cp_async_commit();
+  };
+  // a chunk's decays: warp 0, two tokens a lane
+  float dec[2];
+  auto load_decay = [&](int c) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int64_t i = t0 + static_cast<int64_t>(c) * kChunk + 2 * lane + e;
+      dec[e] = i < t1 ? decay_of(a, p.b + i, hv) : 0.0f;
+    }
+  };
+  double log_total = 0.0;     // of the segment so far (warp 0)
+  auto lay_decay = [&](int c) {
+    double sum = static_cast<double>(dec[0]) + dec[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    const double total = __shfl_sync(0xffffffffu, sum, 31), g[2] = {sum - dec[1], sum};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float hi = static_cast<float>(g[e]);
+      s_g[c & 1][2 * lane + e] = make_float2(hi, static_cast<float>(g[e] - hi));
+      s_eg[c & 1][2 * lane + e] = expf(hi);
+      s_w[c & 1][2 * lane + e] = expf(static_cast<float>(total - g[e]));
+    }
+    if (lane == 0) s_tot[c & 1] = expf(static_cast<float>(total));
+    log_total += total;
+  };
+
+  copy(0);
+  if (warp == 0) {
+    load_decay(0);
+    lay_decay(0);
+    load_decay(1);
+  }
+  for (int c = 0; c < chunks; ++c) {
+    copy(c + 1);
+    cp_async_wait<1>();
+    __syncthreads();     // the chunk's rows and decays are there
+    const uint32_t sk = stage_k(c), sv = stage_v(c), sq = stage_q(c);
+    const int64_t r0 = t0 + static_cast<int64_t>(c) * kChunk;
+
+    if constexpr (!kLocal) {
+      // ---- scores of 16 rows and kCols columns a warp, decayed, into two bf16 parts
+      constexpr int kCols = kChunk * kChunk / 16 / kWarps, kN = kCols / 8;
+      const int m0 = kWarps == 8 ? (warp >> 1) * 16 : warp * 16, n0 = kWarps == 8 ? (warp & 1) * kCols : 0;
+      float x[kN][4];
+#pragma unroll
+      for (int n = 0; n < kN; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.0f;
+      if (n0 <= m0 + 15) {
+#pragma unroll
+        for (int kk = 0; kk < DK / 16; ++kk) {
+          uint32_t qa[4];
+          ldmatrix_x4(sq + piece<DK>(m0 + (lane & 15), 2 * kk + (lane >> 4)), qa[0], qa[1], qa[2], qa[3]);
+#pragma unroll
+          for (int n = 0; n < kN; n += 2) {
+            if (n0 + n * 8 > m0 + 15) continue;
+            uint32_t kb[4];
+            ldmatrix_x4(sk + piece<DK>(n0 + n * 8 + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1)), kb[0],
+                        kb[1], kb[2], kb[3]);
+            mma_bf16(x[n], qa, kb[0], kb[1]);
+            mma_bf16(x[n + 1], qa, kb[2], kb[3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = m0 + lr + 8 * e;
+        const float2 gi = s_g[c & 1][i];
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          const int j = n0 + n * 8 + 2 * lc;
+          float y[2];
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const float2 gj = s_g[c & 1][j + f];
+            y[f] = j + f <= i ? x[n][2 * e + f] * expf((gi.x - gj.x) + (gi.y - gj.y)) : 0.0f;
+          }
+          if (j > m0 + 15) continue;
+          const uint32_t at_p = score_place(i, j >> 3) + (j & 7) * 2;
+          const uint32_t hi = split_bf16(y[0], y[1]), lo = pack_bf16(y[0], y[1]);
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_hi + at_p), "r"(hi) : "memory");
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_lo + at_p), "r"(lo) : "memory");
+        }
+      }
+      __syncthreads();
+    }
+    // next chunk's decays: their place was read before the barrier that began this chunk
+    if (warp == 0 && c + 1 < chunks) {
+      lay_decay(c + 1);
+      load_decay(c + 2);
+    }
+
+    // the warp's 16 columns of V: k16 steps of 16 tokens
+    uint32_t vf[kChunk / 16][4];
+#pragma unroll
+    for (int kk = 0; kk < kChunk / 16; ++kk)
+      ldmatrix_x4_trans(sv + piece<DV>(kk * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * warp + ((lane >> 3) & 1)), vf[kk]);
+
+    if constexpr (!kLocal) {
+      // ---- outputs: q S, decayed, and the scores times V
+      float o[kChunk / 16][2][4];
+#pragma unroll
+      for (int m = 0; m < kChunk / 16; ++m)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.0f;
+#pragma unroll
+      for (int kk = 0; kk < DK / 16; ++kk) {
+        uint32_t bh[2][2], bl[2][2];   // [column half][k half]
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float lo = st[2 * kk + k][2 * n], hi = st[2 * kk + k][2 * n + 1];
+            bh[n][k] = split_bf16(lo, hi);
+            bl[n][k] = pack_bf16(lo, hi);
+          }
+#pragma unroll
+        for (int m = 0; m < kChunk / 16; ++m) {
+          uint32_t qa[4];
+          ldmatrix_x4(sq + piece<DK>(m * 16 + (lane & 15), 2 * kk + (lane >> 4)), qa[0], qa[1], qa[2], qa[3]);
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            mma_bf16(o[m][n], qa, bh[n][0], bh[n][1]);
+            mma_bf16(o[m][n], qa, bl[n][0], bl[n][1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < kChunk / 16; ++m) {
+        const float e0 = s_eg[c & 1][m * 16 + lr], e1 = s_eg[c & 1][m * 16 + lr + 8];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) o[m][n][0] *= e0, o[m][n][1] *= e0, o[m][n][2] *= e1, o[m][n][3] *= e1;
+#pragma unroll
+        for (int kk = 0; kk <= m; ++kk) {
+          uint32_t ph[4], pl[4];
+          const uint32_t at_p = score_place(m * 16 + (lane & 15), 2 * kk + (lane >> 4));
+          ldmatrix_x4(p_hi + at_p, ph[0], ph[1], ph[2], ph[3]);
+          ldmatrix_x4(p_lo + at_p, pl[0], pl[1], pl[2], pl[3]);
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            mma_bf16(o[m][n], ph, vf[kk][n], vf[kk][2 + n]);
+            mma_bf16(o[m][n], pl, vf[kk][n], vf[kk][2 + n]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int64_t i = r0 + m * 16 + lr + 8 * e;
+          if (i >= t1) continue;
+          uint16_t* dst = a.out + (p.b + i) * a.ldo_t + hv * a.ldo_h + warp * 16 + 2 * lc;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            *reinterpret_cast<uint32_t*>(dst + 8 * n) = pack_bf16(o[m][n][2 * e] * a.scale, o[m][n][2 * e + 1] * a.scale);
+        }
+      }
+    }
+
+    // ---- the state after the chunk
+    const float tot = s_tot[c & 1];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) st[t][0] *= tot, st[t][1] *= tot, st[t][2] *= tot, st[t][3] *= tot;
+#pragma unroll
+    for (int kk = 0; kk < kChunk / 16; ++kk) {
+      uint32_t va[3][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = kk * 16 + 2 * lc + 8 * (i >> 1);   // tokens of the operand's register
+        float lo = bf16_lo(vf[kk][i]) * s_w[c & 1][j], hi = bf16_hi(vf[kk][i]) * s_w[c & 1][j + 1];
+        va[0][i] = split_bf16(lo, hi);
+        va[1][i] = split_bf16(lo, hi);
+        va[2][i] = pack_bf16(lo, hi);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; t += 2) {
+        uint32_t kb[4];
+        ldmatrix_x4_trans(sk + piece<DK>(kk * 16 + (lane & 15), t + (lane >> 4)), kb);
+#pragma unroll
+        for (int f = 0; f < 3; ++f) {
+          mma_bf16(st[t], va[f], kb[0], kb[1]);
+          mma_bf16(st[t + 1], va[f], kb[2], kb[3]);
+        }
+      }
+    }
+    __syncthreads();     // the chunk's stage and scores are free
+  }
+  cp_async_wait<0>();
+
+  if constexpr (kLocal) {
+    write_part(part + (seg + 1) * part_step, expf(static_cast<float>(log_total)));
+  } else if (seg + 1 == segs && p.out >= 0) {
+    float* dst = a.state + (p.out * a.Hv + hv) * (DK * DV) + at;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      dst[8 * t * DV] = st[t][0];
+      dst[(8 * t + 1) * DV] = st[t][1];
+      dst[8 * t * DV + 8] = st[t][2];
+      dst[(8 * t + 1) * DV + 8] = st[t][3];
+    }
+  }
+}
+
+template <int DK, int DV>
+cudaError_t launch_shape(const LinAttnArgs& a, cudaStream_t stream) {
+  using L = Tile<DK, DV>;
+  if (a.max_len <= kFewTokens) {
+    // narrow slices where whole heads leave SMs empty
+    const int width = a.S * a.Hv >= kFillCtas ? DV : 32;
+    const dim3 grid(static_cast<unsigned>(a.S * (DV / width)), a.Hv);
+    return launch_kernel(linear_few_kernel<DK>, grid, dim3(kGroups * width / 4), few_smem(DK, width), stream, true, a, width);
+  }
+  const int segs = static_cast<int>(most_segments(a.max_len, a.Hv));
+  const dim3 grid(static_cast<unsigned>(a.S * segs), a.Hv);
+  cudaError_t e = cudaSuccess;
+  if (segs > 1) {
+    e = ensure_smem_attr(reinterpret_cast<const void*>(linear_chunk_kernel<DK, DV, true>), L::kLocalBytes);
+    if (e == cudaSuccess)
+      e = launch_kernel(linear_chunk_kernel<DK, DV, true>, grid, dim3(L::kThreads), L::kLocalBytes, stream, true, a, segs);
+  }
+  static_assert(few_smem(DK, DV) <= L::kBytes, "few tokens in the same memory");
+  if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(linear_chunk_kernel<DK, DV, false>), L::kBytes);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(linear_chunk_kernel<DK, DV, false>, grid, dim3(L::kThreads), L::kBytes, stream, true, a, segs);
+}
+
+}  // namespace
+
+size_t linear_attention_workspace_bytes(int64_t T, int64_t max_len, int64_t Hv, int64_t Dk, int64_t Dv) {
+  if (most_segments(max_len, Hv) <= 1) return 0;
+  return static_cast<size_t>(first_place(T) * Hv * (Dk * Dv + 4)) * 4;
+}
+
+cudaError_t launch_linear_attention(const LinAttnArgs& a, cudaStream_t stream) {
+  if (a.Dk == 64) return a.Dv == 64 ? launch_shape<64, 64>(a, stream) : launch_shape<64, 128>(a, stream);
+  return a.Dv == 64 ? launch_shape<128, 64>(a, stream) : launch_shape<128, 128>(a, stream);
+}
+
+}  // namespace prism

@@ -85,6 +85,7 @@ typedef enum {
 #define PRISM_DEV_ERR_ROW_RANGE 16u /* a row index outside the indexed matrix */
 #define PRISM_DEV_ERR_PAGE_RANGE 32u /* a page index outside [0, num_pages)   */
 #define PRISM_DEV_ERR_SEQ_RANGE 64u /* a sequence's length or offsets bad     */
+#define PRISM_DEV_ERR_STATE_RANGE 128u /* a state index outside [-1, num_states) */
 
 /* Largest top_k accepted by prism_token_logprobs. */
 #define PRISM_MAX_TOP_K 32
@@ -649,6 +650,121 @@ int prism_token_logprobs(const void *logits, int logits_f32, int64_t ldl,
                          float *logprobs, float *entropy, int32_t *top_ids,
                          float *top_logprobs, int32_t *dev_error_word,
                          void *cuda_stream);
+
+/*
+ * ---- Between a layer's linears (StartLux-Prism: per layer a norm, the
+ * projections, attention or linear attention, the output projection and its
+ * residual, a norm, gate/up, the activation, the down projection).
+ *
+ * The first three turn a bf16 row into the operand of the next linear.  `form`
+ * says which:
+ *   PRISM_FORM_INT8   codes of prism_quant_act, [M, K] int8 (ldq % 16 == 0)
+ *   PRISM_FORM_F16    the same codes as binary16 (prism_quant_act_f16; ldq % 8 == 0)
+ *   PRISM_FORM_BF16   the values themselves rounded to bf16 (ldq % 8 == 0),
+ *                     without a scale (a_scale NULL)
+ * with a_scale [M] float32 and the quantiser's definition applied to the binary32
+ * values y of a row.  Every step named below is one binary32 operation rounded
+ * to nearest even, in the order of the brackets.  The reciprocal root
+ *   r(v) = RN((sum_k v_k^2 / n + eps)^(-1/2))
+ * is formed to about 2^-40 and rounded once, so that codes are the same bits
+ * for any batch and device.  silu(z) = z * ((z >= 0 ? 1 : e) / (1 + e)) with
+ * e = exp(-|z|) as in the read-out, but each product and the sum that follows it
+ * one fused operation (and n = rint of the exact product).
+ * Inputs must be finite, with magnitudes below 2^40.  q 16-byte aligned; rows of
+ * bf16 16-byte aligned, their strides multiples of 8; weights 16-byte aligned;
+ * 1e-20 <= eps <= 1; 16 <= K <= PRISM_MAX_ROW, K % 16 == 0.  M == 0 enqueues
+ * nothing.
+ *
+ * prism_norm_quant -- the residual stream, its RMS norm, and codes:
+ *   h = bf16(x + (alpha * d)), d = delta, or (delta * r(delta)) * post_weight
+ *   y = (h * r(h)) * weight
+ *   delta_bf16    the last block's output [M, K], or NULL: h = x, and h_bf16
+ *                 and post_weight must be NULL
+ *   h_bf16, ldh   [M, K] out, the stream after the addition; may be x or delta
+ *                 itself (the same pointer and stride)
+ *   weight        [K] float32: the norm's weight (times prism_quant_act's
+ *                 inv_smooth where the linear's input is smoothed)
+ *   post_weight   [K] float32: the block's output has a norm of its own; or NULL
+ *
+ * prism_head_norm_quant -- the norm of each head of an attention's output:
+ *   y = (((x * r(x's head)) * weight) * silu(gate)) * inv_smooth
+ *   x_bf16, gate_bf16   [M, H * D]; gate may be NULL (no factor)
+ *   weight [D] float32; inv_smooth [H * D] float32 or NULL (no factor)
+ *   D in {64, 128, 256}; K = H * D.
+ *
+ * prism_glu_quant -- the FFN's activation:
+ *   y = (silu(gate) * up) * inv_smooth
+ *   gate_up_bf16  [M, 2 F]: gate, then up (the gate/up projection's output)
+ *   inv_smooth    [F] float32 or NULL (no factor); K = F.
+ */
+#define PRISM_FORM_INT8 0
+#define PRISM_FORM_F16 1
+#define PRISM_FORM_BF16 2
+#define PRISM_MAX_ROW 32768
+int prism_norm_quant(const void *x_bf16, int64_t ldx, const void *delta_bf16,
+                     int64_t ldd, float alpha, const float *post_weight,
+                     const float *weight, float eps, int64_t M, int64_t K,
+                     void *h_bf16, int64_t ldh, int form, void *q, int64_t ldq,
+                     float *a_scale, void *cuda_stream);
+int prism_head_norm_quant(const void *x_bf16, int64_t ldx, const float *weight,
+                          const void *gate_bf16, int64_t ldg,
+                          const float *inv_smooth, float eps, int64_t M,
+                          int64_t H, int64_t D, int form, void *q, int64_t ldq,
+                          float *a_scale, void *cuda_stream);
+int prism_glu_quant(const void *gate_up_bf16, int64_t ldx,
+                    const float *inv_smooth, int64_t M, int64_t F, int form,
+                    void *q, int64_t ldq, float *a_scale, void *cuda_stream);
+
+/*
+ * prism_linear_attention -- linear attention with a decay for each head, over
+ * states in slots.  For each sequence and value head (key head h / (H_v / H_k)),
+ * token by token from the state S that the sequence starts from:
+ *   S = e^g S + k v^T          [D_k, D_v] float32
+ *   out = bf16(scale * q S)
+ *   q, k          [T, H_k, D_k] bf16, v, out [T, H_v, D_v] bf16; strides as in
+ *                 prism_kv_append
+ *   log_decay     float32 g: [T, H_v], token stride ldd_t >= H_v, or one for
+ *                 each head, [H_v] with ldd_t = 0.  Below -16384 (-inf among
+ *                 them: the state is forgotten) counts as -16384.
+ *   state         [num_states, H_v, D_k, D_v] float32, dense, 16-byte aligned
+ *   state_in      [S] int32: the slot that a sequence starts from (a branch: its
+ *                 parent's, which several may share), -1 or NULL: zeros
+ *   state_out     [S] int32: the slot that its last state goes to (its own again,
+ *                 or another), -1 or NULL: none.  A slot that one sequence
+ *                 writes is undefined afterwards where another of the same call
+ *                 writes it too, and so are the outputs of another that starts
+ *                 from it.  A sequence without tokens passes its state on.
+ *   cu            [S + 1] int32: sequence s has rows cu[s] .. cu[s + 1] - 1; NULL:
+ *                 row s (T == S).  Rows of no sequence are not written; where
+ *                 sequences overlap, theirs are undefined.
+ *   max_len       the most tokens of one sequence; a sequence with more sets
+ *                 PRISM_DEV_ERR_SEQ_RANGE
+ *   workspace     prism_linear_attention_workspace_bytes(...) bytes, 256-byte
+ *                 aligned, any contents
+ * Inputs must be finite (log_decay: not NaN or +inf).  States and sums are binary32; products of the
+ * chunked form (more than 16 tokens) enter the tensor cores as sums of two or
+ * three bf16 parts, to 2^-17 of a score or a state that is read out and 2^-25 of what
+ * is added to a state.  A sequence's results depend on its own tokens and state
+ * (and on H_v and how its tokens are divided among calls) only.
+ * A malformed sequence (too many tokens, a state index outside [-1, num_states):
+ * PRISM_DEV_ERR_STATE_RANGE) gets NaN rows and writes no state; one with
+ * malformed offsets has no rows.
+ *   D_k, D_v in {64, 128}; H_v a multiple of H_k, H_v <= 65535.
+ */
+size_t prism_linear_attention_workspace_bytes(int64_t S, int64_t T,
+                                              int64_t max_len, int64_t H_v,
+                                              int64_t D_k, int64_t D_v);
+int prism_linear_attention(const void *q_bf16, int64_t ldq_t, int64_t ldq_h,
+                           const void *k_bf16, int64_t ldk_t, int64_t ldk_h,
+                           const void *v_bf16, int64_t ldv_t, int64_t ldv_h,
+                           const float *log_decay, int64_t ldd_t, float *state,
+                           const int32_t *state_in, const int32_t *state_out,
+                           const int32_t *cu, void *out_bf16, int64_t ldo_t,
+                           int64_t ldo_h, float scale, int64_t S, int64_t T,
+                           int64_t max_len, int64_t num_states, int64_t H_k,
+                           int64_t H_v, int64_t D_k, int64_t D_v,
+                           void *workspace, size_t workspace_bytes,
+                           int32_t *dev_error_word, void *cuda_stream);
 
 /* Human-readable text for a prism_status value (static storage). */
 const char *prism_status_string(int status);
