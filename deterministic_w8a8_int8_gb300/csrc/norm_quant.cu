@@ -24,6 +24,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "decode.cuh"
 #include "layer.cuh"
 
@@ -32,6 +34,8 @@ namespace {
 
 constexpr int kMaxTeam = 512;
 constexpr int kWarps = kMaxTeam / 32;
+
+__device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
 
 // A sum of binary32 numbers as the rounded sum and its error.
 struct Sum {
@@ -42,19 +46,33 @@ __device__ __forceinline__ Sum join(Sum a, Sum b) {
   const float e = __fadd_rn(__fsub_rn(a.h, __fsub_rn(s, t)), __fsub_rn(b.h, t));
   return Sum{s, __fadd_rn(e, __fadd_rn(a.l, b.l))};
 }
-// Two sums side by side.
-struct Sum2 {
+// Sums of squares of bf16 values, two side by side.  They begin at the largest
+// square of the thread's, which is taken off again at the end: with no addend
+// above the sum, the error of an addition is what its difference leaves of the
+// addend, three operations instead of six (Dekker's form).
+struct Squares {
   float2 h, l;
+  float top;
+  __device__ __forceinline__ explicit Squares(float largest) : l(make_float2(0.0f, 0.0f)), top(largest * largest) {
+    h = make_float2(top, top);
+  }
+  __device__ __forceinline__ void add(float2 v) {
+    const float2 s = fma2(v, v, h);
+    l = add2(l, fma2(v, v, fma2(s, twice(-1.0f), h)));
+    h = s;
+  }
+  __device__ __forceinline__ Sum sum() const {
+    return join(join(Sum{h.x, l.x}, Sum{h.y, l.y}), Sum{-2.0f * top, 0.0f});
+  }
 };
-__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
-__device__ __forceinline__ void add_square(Sum2& a, float2 v) {
-  const float2 p = mul2(v, v);
-  const float2 s = add2(a.h, p), t = add2(s, neg2(a.h));
-  const float2 e = add2(add2(a.h, neg2(add2(s, neg2(t)))), add2(p, neg2(t)));
-  a.h = s;
-  a.l = add2(a.l, e);
+// The largest magnitude of a vector's values, and of what was there.
+__device__ __forceinline__ __nv_bfloat162 larger(__nv_bfloat162 m, const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
+  return m;
 }
-__device__ __forceinline__ Sum both(const Sum2& a) { return join(Sum{a.h.x, a.l.x}, Sum{a.h.y, a.l.y}); }
+__device__ __forceinline__ float largest(__nv_bfloat162 m) { return fmaxf(__low2float(m), __high2float(m)); }
 
 // (s / n + eps)^(-1/2): the reciprocal root's approximation and one step of
 // Newton's iteration whose residual is formed from the rounding errors too.
@@ -72,33 +90,39 @@ __device__ __forceinline__ float inverse_root(Sum s, float inv_n, float inv_n_lo
   return __fmaf_rn(__fmul_rn(0.5f, r), d, r);
 }
 
+// n / d rounded to nearest for 1 <= d <= 2: Markstein's quotient (1990).  The
+// reciprocal's approximation and one step of Newton's iteration, and the
+// remainder, which one fused operation forms exactly, put back.  There are 2^16
+// gates, and the tests compare each one's result.
+__device__ __forceinline__ float2 divide2(float2 n, float2 d) {
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+  const float2 minus = mul2(d, twice(-1.0f));
+  r = fma2(fma2(minus, r, twice(1.0f)), r, r);
+  const float2 q = mul2(n, r);
+  return fma2(fma2(minus, q, n), r, q);
+}
+
 // silu of two values: z / (1 + exp(-z)) as z * ((1 or e) / (1 + e)), e = exp(-|z|)
 // by n ln 2 + r (ln 2 in two parts), the series of e^r to r^7 in fused steps, times
-// 2^n; e = 0 for n < -126.
+// 2^n.  From |z| = 88 on n would be -127 or less, and 2^n counts as 0.
 __device__ __forceinline__ float2 silu2(float2 z) {
-  constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: its unit is 1
-  auto two = [](float v) { return make_float2(v, v); };
-  const float2 x = make_float2(-fabsf(z.x), -fabsf(z.y));
-  float2 t = fma2(x, two(0x1.715476p+0f), two(kMagic));
-  t = make_float2(fmaxf(t.x, kMagic - 200.0f), fmaxf(t.y, kMagic - 200.0f));
-  const float2 n = add2(t, two(-kMagic));
-  float2 r = fma2(n, two(-0x1.63p-1f), x);
-  r = fma2(n, two(0x1.bd0106p-13f), r);
-  float2 p = two(0x1.a01a02p-13f);
-  p = fma2(p, r, two(0x1.6c16c2p-10f));
-  p = fma2(p, r, two(0x1.111112p-7f));
-  p = fma2(p, r, two(0x1.555556p-5f));
-  p = fma2(p, r, two(0x1.555556p-3f));
-  p = fma2(p, r, two(0x1p-1f));
-  p = fma2(p, r, two(1.0f));
-  p = fma2(p, r, two(1.0f));
-  const float2 scale = make_float2(__uint_as_float((__float_as_uint(t.x) + 127u) << 23),
-                                   __uint_as_float((__float_as_uint(t.y) + 127u) << 23));
-  p = mul2(p, scale);
-  const float2 e = make_float2(n.x >= -126.0f ? p.x : 0.0f, n.y >= -126.0f ? p.y : 0.0f);
-  const float2 d = add2(e, two(1.0f));
-  const float2 s = make_float2(__fdiv_rn(z.x >= 0.0f ? 1.0f : e.x, d.x), __fdiv_rn(z.y >= 0.0f ? 1.0f : e.y, d.y));
-  return mul2(z, s);
+  constexpr float kMagic = 12582912.0f + 127.0f;   // 1.5 * 2^23, whose unit is 1, and the exponent's bias
+  const float2 x = make_float2(fmaxf(-fabsf(z.x), -88.0f), fmaxf(-fabsf(z.y), -88.0f));
+  const float2 t = fma2(x, twice(0x1.715476p+0f), twice(kMagic)), n = add2(t, twice(-kMagic));
+  float2 r = fma2(n, twice(-0x1.63p-1f), x);
+  r = fma2(n, twice(0x1.bd0106p-13f), r);
+  float2 p = fma2(twice(0x1.a01a02p-13f), r, twice(0x1.6c16c2p-10f));
+  p = fma2(p, r, twice(0x1.111112p-7f));
+  p = fma2(p, r, twice(0x1.555556p-5f));
+  p = fma2(p, r, twice(0x1.555556p-3f));
+  p = fma2(p, r, twice(0x1p-1f));
+  p = fma2(p, r, twice(1.0f));
+  p = fma2(p, r, twice(1.0f));
+  const float2 e = mul2(p, make_float2(__uint_as_float(__float_as_uint(t.x) << 23), __uint_as_float(__float_as_uint(t.y) << 23)));
+  const float2 top = make_float2(z.x >= 0.0f ? 1.0f : e.x, z.y >= 0.0f ? 1.0f : e.y);
+  return mul2(z, divide2(top, add2(e, twice(1.0f))));
 }
 
 __device__ __forceinline__ float2 pair(uint32_t v) { return make_float2(bf16_lo(v), bf16_hi(v)); }
@@ -123,13 +147,12 @@ __device__ __forceinline__ Sum team_sum(Sum s, Sum* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.h, o), __shfl_xor_sync(0xffffffffu, s.l, o)});
+  if (warps == 1) return s;
   if (lane == 0) red[threadIdx.x >> 5] = s;
   __syncthreads();
-  s = lane < warps ? red[lane] : Sum{0.0f, 0.0f};
-#pragma unroll
-  for (int o = kWarps / 2; o > 0; o >>= 1)
-    s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.h, o), __shfl_xor_sync(0xffffffffu, s.l, o)});
-  return Sum{__shfl_sync(0xffffffffu, s.h, 0), __shfl_sync(0xffffffffu, s.l, 0)};
+  s = red[0];
+  for (int i = 1; i < warps; ++i) s = join(s, red[i]);
+  return s;
 }
 
 // The row's values y, 8 C a thread (0 past the row's end), as codes.
@@ -168,7 +191,7 @@ __device__ __forceinline__ void store_codes(const RowCodes& o, int64_t row, int 
     float2 t[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      t[e] = mul2(y[i][e], make_float2(inv, inv));
+      t[e] = mul2(y[i][e], twice(inv));
       t[e] = make_float2(__fadd_rn(t[e].x, kMagic), __fadd_rn(t[e].y, kMagic));   // scalar: never merged into a multiply-add
     }
     if (o.form == PRISM_FORM_F16) {
@@ -189,50 +212,72 @@ __device__ __forceinline__ void store_codes(const RowCodes& o, int64_t row, int 
   }
 }
 
-// A row's values are read once.  Not through the read-only path: a row may be
-// written back in place.
-__device__ __forceinline__ uint4 load_once_16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
-template <int C>
-struct Row {
-  uint4 v[C];
-  // Vectors of the thread; zeros past the row's end.
-  __device__ __forceinline__ void load(const uint16_t* row, int nvec) {
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int j = threadIdx.x + i * static_cast<int>(blockDim.x);
-      v[i] = j < nvec ? load_once_16(reinterpret_cast<const uint4*>(row) + j) : make_uint4(0u, 0u, 0u, 0u);
-    }
+// A thread's vectors of one operand's next row, on their way through shared
+// memory: each thread copies and reads its own, so that no barrier is needed, and
+// refills a place as soon as it has read it.
+struct Ahead {
+  uint32_t at;             // of vector 0
+  int nvec;
+  __device__ __forceinline__ Ahead(const uint8_t* smem, int operand, int vectors, int nvec)
+      : at(smem_u32(smem) + (operand * vectors * blockDim.x + threadIdx.x) * 16), nvec(nvec) {}
+  __device__ __forceinline__ int index(int i) const { return threadIdx.x + i * static_cast<int>(blockDim.x); }
+  __device__ __forceinline__ void fill(const uint16_t* row, int i) const {
+    if (index(i) < nvec) cp_async_16(at + i * blockDim.x * 16, row + index(i) * 8, 16);
+  }
+  __device__ __forceinline__ uint4 read(int i) const {   // zeros past the row's end
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (index(i) < nvec)
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "r"(at + i * blockDim.x * 16)
+                   : "memory");
+    return v;
   }
 };
 
 template <int C, bool kDelta>
 __global__ void __launch_bounds__(kMaxTeam) norm_kernel(const __grid_constant__ NormArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Sum s_sum[2][kWarps], s_post[2][kWarps];
   __shared__ uint32_t s_top[2][kWarps];
   pdl_trigger();
   pdl_wait();
   const int team = blockDim.x, lt = threadIdx.x, nvec = static_cast<int>(a.K >> 3);
-  Row<C> x, d;
+  const Ahead ax(smem, 0, C, nvec), ad(smem, 1, C, nvec);
   int64_t row = blockIdx.x;
-  x.load(a.x + row * a.ldx, nvec);
-  if constexpr (kDelta) d.load(a.delta + row * a.ldd, nvec);
+  auto fill = [&](int64_t r) {
+    if (r < a.M) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        ax.fill(a.x + r * a.ldx, i);
+        if constexpr (kDelta) ad.fill(a.delta + r * a.ldd, i);
+      }
+    }
+    cp_async_commit();
+  };
+  fill(row);
   for (int par = 0; row < a.M; row += gridDim.x, par ^= 1) {
+    cp_async_wait<0>();
+    uint4 x[C], d[kDelta ? C : 1];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      x[i] = ax.read(i);
+      if constexpr (kDelta) d[i] = ad.read(i);
+    }
+    fill(row + gridDim.x);
+    __nv_bfloat162 m = __floats2bfloat162_rn(0.0f, 0.0f);
     if constexpr (kDelta) {
       float r = 1.0f;
       if (a.post != nullptr) {
-        Sum2 s{};
+#pragma unroll
+        for (int i = 0; i < C; ++i) m = larger(m, d[i]);
+        Squares s(largest(m));
 #pragma unroll
         for (int i = 0; i < C; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) add_square(s, pair(word(d.v[i], e)));
-        r = inverse_root(team_sum(both(s), s_post[par]), a.inv_n, a.inv_n_low, a.eps);
+          for (int e = 0; e < 4; ++e) s.add(pair(word(d[i], e)));
+        r = inverse_root(team_sum(s.sum(), s_post[par]), a.inv_n, a.inv_n_low, a.eps);
+        m = __floats2bfloat162_rn(0.0f, 0.0f);
       }
 #pragma unroll
       for (int i = 0; i < C; ++i) {
@@ -242,187 +287,263 @@ __global__ void __launch_bounds__(kMaxTeam) norm_kernel(const __grid_constant__ 
         if (a.post != nullptr) {
           const Weights p(a.post, j);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = mul2(mul2(pair(word(d.v[i], e)), make_float2(r, r)), p[e]);
+          for (int e = 0; e < 4; ++e) w[e] = mul2(mul2(pair(word(d[i], e)), twice(r)), p[e]);
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = pair(word(d.v[i], e));
+          for (int e = 0; e < 4; ++e) w[e] = pair(word(d[i], e));
         }
         uint32_t h[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 add = mul2(w[e], make_float2(a.alpha, a.alpha)), v = pair(word(x.v[i], e));
+          const float2 add = mul2(w[e], twice(a.alpha)), v = pair(word(x[i], e));
           h[e] = bf16x2(make_float2(__fadd_rn(v.x, add.x), __fadd_rn(v.y, add.y)));   // scalar: not merged with the product
         }
-        x.v[i] = make_uint4(h[0], h[1], h[2], h[3]);
-        reinterpret_cast<uint4*>(a.h + row * a.ldh)[j] = x.v[i];
+        x[i] = make_uint4(h[0], h[1], h[2], h[3]);
+        reinterpret_cast<uint4*>(a.h + row * a.ldh)[j] = x[i];
       }
     }
-    float2 y[C][4];
-    Sum2 s{};
+#pragma unroll
+    for (int i = 0; i < C; ++i) m = larger(m, x[i]);
+    Squares s(largest(m));
 #pragma unroll
     for (int i = 0; i < C; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[i][e] = pair(word(x.v[i], e));
-        add_square(s, y[i][e]);
-      }
-    const int64_t next = row + gridDim.x;
-    if (next < a.M) {
-      x.load(a.x + next * a.ldx, nvec);
-      if constexpr (kDelta) d.load(a.delta + next * a.ldd, nvec);
-    }
-    const float r = inverse_root(team_sum(both(s), s_sum[par]), a.inv_n, a.inv_n_low, a.eps);
+      for (int e = 0; e < 4; ++e) s.add(pair(word(x[i], e)));
+    const float r = inverse_root(team_sum(s.sum(), s_sum[par]), a.inv_n, a.inv_n_low, a.eps);
+    float2 y[C][4];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int j = lt + i * team;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[i][e] = mul2(pair(word(x[i], e)), twice(r));
       if (j >= nvec) continue;
       const Weights w(a.weight, j);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[i][e] = mul2(mul2(y[i][e], make_float2(r, r)), w[e]);
+      for (int e = 0; e < 4; ++e) y[i][e] = mul2(y[i][e], w[e]);
     }
     store_codes<C>(a.o, row, nvec, y, s_top[par]);
+  }
+  cp_async_wait<0>();
+}
+
+// CTAs of an SM at least, by registers.
+constexpr int ctas_of(int C) { return C <= 5 ? 2 : 1; }
+
+// A head's channels lie in D / 8 = `lanes` neighbouring lanes, and the sums of a
+// thread's N vectors belong to N heads: with each exchange the lanes of one half
+// take over half of the sums and the others the rest, until each lane has one,
+// whose root it forms, and the roots are handed round.
+template <int N>
+__device__ __forceinline__ void head_roots(const Sum (&t)[N], int lanes, const NormArgs& a, float (&r)[N]) {
+  const int lane = threadIdx.x & 31;
+  auto exchanged = [&](Sum s, int o) {
+    return Sum{__shfl_xor_sync(0xffffffffu, s.h, o), __shfl_xor_sync(0xffffffffu, s.l, o)};
+  };
+  auto half = [&](Sum s, Sum other, int o) {   // s of the lanes without bit o, the other of those with it
+    const bool upper = lane & o;
+    return join(upper ? other : s, exchanged(upper ? s : other, o));
+  };
+  int o = lanes >> 1;
+  Sum s;
+  if constexpr (N == 4) {
+    const Sum u = half(t[0], t[2], o), v = half(t[1], t[3], o);
+    o >>= 1;
+    s = half(u, v, o);
+    o >>= 1;
+  } else if constexpr (N == 2) {
+    s = half(t[0], t[1], o);
+    o >>= 1;
+  } else {
+    s = t[0];
+  }
+  for (; o > 0; o >>= 1) s = join(s, exchanged(s, o));
+  const float root = inverse_root(s, a.inv_n, a.inv_n_low, a.eps);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int from = N == 4 ? (i >> 1) * (lanes >> 1) + (i & 1) * (lanes >> 2) : N == 2 ? i * (lanes >> 1) : 0;
+    r[i] = N == 1 ? root : __shfl_sync(0xffffffffu, root, (lane & ~(lanes - 1)) + from);
   }
 }
 
-// A head's channels lie in D / 8 neighbouring lanes, whose sums are exchanged by shuffles.
 template <int C, bool kGate>
-__global__ void __launch_bounds__(kMaxTeam) head_norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __maxnreg__(C <= 2 ? 64 : C == 4 ? 80 : 128) head_norm_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int N = C < 4 ? C : 4;
+  static_assert(C % N == 0, "vectors go by in groups");
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t s_top[2][kWarps];
   pdl_trigger();
   pdl_wait();
-  const int team = blockDim.x, lt = threadIdx.x, nvec = static_cast<int>(a.K >> 3), lanes = a.D >> 3;
-  Row<C> x, z;
+  const int nvec = static_cast<int>(a.K >> 3), lanes = a.D >> 3;
+  const Ahead ax(smem, 0, C, nvec), az(smem, 1, C, nvec);
   int64_t row = blockIdx.x;
-  x.load(a.x + row * a.ldx, nvec);
-  if constexpr (kGate) z.load(a.gate + row * a.ldg, nvec);
-  const Weights w(a.weight, lt & (lanes - 1));   // a team is whole heads wide, or the row is one turn
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    ax.fill(a.x + row * a.ldx, i);
+    if constexpr (kGate) az.fill(a.gate + row * a.ldg, i);
+  }
+  const Weights w(a.weight, threadIdx.x & (lanes - 1));   // a team is whole heads wide, or the row is one turn
   for (int par = 0; row < a.M; row += gridDim.x, par ^= 1) {
-    float2 y[C][4];
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int j = lt + i * team;
-      Sum2 s{};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[i][e] = pair(word(x.v[i], e));
-        add_square(s, y[i][e]);
-      }
-      Sum t = both(s);
-      for (int o = lanes >> 1; o > 0; o >>= 1)
-        t = join(t, Sum{__shfl_xor_sync(0xffffffffu, t.h, o), __shfl_xor_sync(0xffffffffu, t.l, o)});
-      const float r = inverse_root(t, a.inv_n, a.inv_n_low, a.eps);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[i][e] = mul2(mul2(y[i][e], make_float2(r, r)), w[e]);
-        if constexpr (kGate) y[i][e] = mul2(y[i][e], silu2(pair(word(z.v[i], e))));
-      }
-      if (a.inv_s != nullptr && j < nvec) {
-        const Weights p(a.inv_s, j);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[i][e] = mul2(y[i][e], p[e]);
-      }
-    }
     const int64_t next = row + gridDim.x;
-    if (next < a.M) {
-      x.load(a.x + next * a.ldx, nvec);
-      if constexpr (kGate) z.load(a.gate + next * a.ldg, nvec);
+    float2 y[C][4];
+    cp_async_commit();
+    cp_async_wait<0>();
+#pragma unroll
+    for (int g = 0; g < C; g += N) {
+      Sum t[N];
+      float r[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint4 x = ax.read(g + i);
+        Squares s(largest(larger(__floats2bfloat162_rn(0.0f, 0.0f), x)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[g + i][e] = pair(word(x, e));
+          s.add(y[g + i][e]);
+        }
+        t[i] = s.sum();
+        if (next < a.M) ax.fill(a.x + next * a.ldx, g + i);
+      }
+      head_roots<N>(t, lanes, a, r);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[g + i][e] = mul2(mul2(y[g + i][e], twice(r[i])), w[e]);
+        if constexpr (kGate) {
+          const uint4 z = az.read(g + i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[g + i][e] = mul2(y[g + i][e], silu2(pair(word(z, e))));
+          if (next < a.M) az.fill(a.gate + next * a.ldg, g + i);
+        }
+        if (a.inv_s != nullptr && ax.index(g + i) < nvec) {
+          const Weights p(a.inv_s, ax.index(g + i));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[g + i][e] = mul2(y[g + i][e], p[e]);
+        }
+      }
     }
     store_codes<C>(a.o, row, nvec, y, s_top[par]);
   }
+  cp_async_wait<0>();
 }
 
 template <int C>
-__global__ void __launch_bounds__(kMaxTeam) glu_kernel(const __grid_constant__ GluArgs a) {
+__global__ void __launch_bounds__(kMaxTeam, ctas_of(C)) glu_kernel(const __grid_constant__ GluArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t s_top[2][kWarps];
   pdl_trigger();
   pdl_wait();
-  const int team = blockDim.x, lt = threadIdx.x, nvec = static_cast<int>(a.F >> 3);
-  Row<C> g, u;
+  const int nvec = static_cast<int>(a.F >> 3);
+  const Ahead ag(smem, 0, C, nvec), au(smem, 1, C, nvec);
   int64_t row = blockIdx.x;
-  g.load(a.x + row * a.ldx, nvec);
-  u.load(a.x + row * a.ldx + a.F, nvec);
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    ag.fill(a.x + row * a.ldx, i);
+    au.fill(a.x + row * a.ldx + a.F, i);
+  }
   for (int par = 0; row < a.M; row += gridDim.x, par ^= 1) {
+    const int64_t next = row + gridDim.x;
     float2 y[C][4];
+    cp_async_commit();
+    cp_async_wait<0>();
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const int j = lt + i * team;
+      const uint4 g = ag.read(i), u = au.read(i);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[i][e] = mul2(silu2(pair(word(g.v[i], e))), pair(word(u.v[i], e)));
-      if (a.inv_s != nullptr && j < nvec) {
-        const Weights p(a.inv_s, j);
+      for (int e = 0; e < 4; ++e) y[i][e] = mul2(silu2(pair(word(g, e))), pair(word(u, e)));
+      if (next < a.M) {
+        ag.fill(a.x + next * a.ldx, i);
+        au.fill(a.x + next * a.ldx + a.F, i);
+      }
+      if (a.inv_s != nullptr && ag.index(i) < nvec) {
+        const Weights p(a.inv_s, ag.index(i));
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[i][e] = mul2(y[i][e], p[e]);
       }
     }
-    const int64_t next = row + gridDim.x;
-    if (next < a.M) {
-      g.load(a.x + next * a.ldx, nvec);
-      u.load(a.x + next * a.ldx + a.F, nvec);
-    }
     store_codes<C>(a.o, row, nvec, y, s_top[par]);
   }
+  cp_async_wait<0>();
 }
 
-// The fewest vectors a thread that keep a row within kMaxTeam threads.  The team
-// follows from the row's length alone, and with it the order of its sums.
-constexpr int vectors_of(int64_t K) {
-  return static_cast<int>((K / 8 + kMaxTeam - 1) / kMaxTeam);
+// Vectors of 8 values a thread: the fewest of 1, 2, 4 (and 5 to 8, for heads 8) with which
+// one warp holds the row, or else kMaxTeam threads.  Sums cost a thread some 100
+// instructions, which many vectors share; more than 4 cost the SM warps (norm of 2048
+// rows of 5120 with 2, 4 and 5: see DESIGN).  The team follows from the
+// row's length alone, and with it the order of its sums.
+constexpr int vectors_of(int64_t K, bool even) {
+  const int64_t n = K / 8;
+  return n <= 32 ? 1 : n <= 64 ? 2 : n <= 4 * kMaxTeam ? 4 : even ? 8 : static_cast<int>((n + kMaxTeam - 1) / kMaxTeam);
 }
 
+// A launch of `operands` rows at a time for each CTA: as many CTAs as the SMs
+// hold, or fewer that have equally many rows each.
 template <class Args>
-cudaError_t launch_rows(void (*kernel)(const Args), const Args& a, int64_t M, int64_t K, cudaStream_t stream) {
-  const int c = vectors_of(K);
+cudaError_t launch_rows(void (*kernel)(const Args), std::atomic<int>* held, const Args& a, int64_t M, int64_t K, int c, int operands,
+                        cudaStream_t stream) {
   const int team = static_cast<int>(32 * ((K / 8 + 32 * c - 1) / (32 * c)));
-  int per_sm = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, team, 0);
+  const int bytes = operands * c * team * 16;
+  cudaError_t e = cudaSuccess;
+  if (bytes > 48 * 1024) e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), operands * c * kMaxTeam * 16);
   if (e != cudaSuccess) return e;
-  // as many rows for each CTA that the SMs hold
-  const int64_t most = static_cast<int64_t>(sm_count()) * std::max(per_sm, 1), each = (M + most - 1) / most;
-  return launch_kernel(kernel, dim3(static_cast<unsigned>((M + each - 1) / each)), dim3(team), 0, stream, true, a);
+  int per_sm = held[team / 32].load(std::memory_order_relaxed);   // a property of the kernel and its team
+  if (per_sm == 0) {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, team, bytes);
+    if (e != cudaSuccess) return e;
+    per_sm = std::max(per_sm, 1);
+    held[team / 32].store(per_sm, std::memory_order_relaxed);
+  }
+  const int64_t most = static_cast<int64_t>(sm_count()) * per_sm, each = (M + most - 1) / most;
+  return launch_kernel(kernel, dim3(static_cast<unsigned>((M + each - 1) / each)), dim3(team), bytes, stream, true, a);
 }
 
-template <class Args, class F>
-cudaError_t with_vectors(int64_t K, const Args& a, int64_t M, cudaStream_t stream, F kernel) {
-  switch (vectors_of(K)) {
-    case 1: return launch_rows<Args>(kernel.template of<1>(), a, M, K, stream);
-    case 2: return launch_rows<Args>(kernel.template of<2>(), a, M, K, stream);
-    case 3: return launch_rows<Args>(kernel.template of<3>(), a, M, K, stream);
-    case 4: return launch_rows<Args>(kernel.template of<4>(), a, M, K, stream);
-    case 5: return launch_rows<Args>(kernel.template of<5>(), a, M, K, stream);
-    case 6: return launch_rows<Args>(kernel.template of<6>(), a, M, K, stream);
-    case 7: return launch_rows<Args>(kernel.template of<7>(), a, M, K, stream);
-    default: return launch_rows<Args>(kernel.template of<8>(), a, M, K, stream);
+template <class F, int C, class Args>
+cudaError_t launch_c(const Args& a, int64_t M, int64_t K, cudaStream_t stream) {
+  static std::atomic<int> held[kWarps + 1];
+  return launch_rows<Args>(F::template of<C>(), held, a, M, K, C, F::kOperands, stream);
+}
+template <class F, class Args>
+cudaError_t launch_any(const Args& a, int64_t M, int64_t K, cudaStream_t stream) {
+  switch (vectors_of(K, F::kEven)) {
+    case 1: return launch_c<F, 1>(a, M, K, stream);
+    case 2: return launch_c<F, 2>(a, M, K, stream);
+    case 4: return launch_c<F, 4>(a, M, K, stream);
+    case 5: return launch_c<F, F::kEven ? 8 : 5>(a, M, K, stream);
+    case 6: return launch_c<F, F::kEven ? 8 : 6>(a, M, K, stream);
+    case 7: return launch_c<F, F::kEven ? 8 : 7>(a, M, K, stream);
+    default: return launch_c<F, 8>(a, M, K, stream);
   }
 }
-static_assert(vectors_of(PRISM_MAX_ROW) == 8, "the longest row");
+static_assert(vectors_of(PRISM_MAX_ROW, false) == 8 && PRISM_MAX_ROW <= 64 * kMaxTeam, "the longest row");
 
 template <bool kDelta>
 struct NormKernel {
+  static constexpr int kOperands = kDelta ? 2 : 1;
+  static constexpr bool kEven = false;
   template <int C>
-  auto of() const { return norm_kernel<C, kDelta>; }
+  static auto of() { return norm_kernel<C, kDelta>; }
 };
 template <bool kGate>
 struct HeadKernel {
+  static constexpr int kOperands = kGate ? 2 : 1;
+  static constexpr bool kEven = true;
   template <int C>
-  auto of() const { return head_norm_kernel<C, kGate>; }
+  static auto of() { return head_norm_kernel<C, kGate>; }
 };
 struct GluKernel {
+  static constexpr int kOperands = 2;
+  static constexpr bool kEven = false;
   template <int C>
-  auto of() const { return glu_kernel<C>; }
+  static auto of() { return glu_kernel<C>; }
 };
 
 }  // namespace
 
 cudaError_t launch_norm_quant(const NormArgs& a, cudaStream_t stream) {
-  return a.delta != nullptr ? with_vectors(a.K, a, a.M, stream, NormKernel<true>())
-                            : with_vectors(a.K, a, a.M, stream, NormKernel<false>());
+  return a.delta != nullptr ? launch_any<NormKernel<true>>(a, a.M, a.K, stream) : launch_any<NormKernel<false>>(a, a.M, a.K, stream);
 }
 cudaError_t launch_head_norm_quant(const NormArgs& a, cudaStream_t stream) {
-  return a.gate != nullptr ? with_vectors(a.K, a, a.M, stream, HeadKernel<true>())
-                           : with_vectors(a.K, a, a.M, stream, HeadKernel<false>());
+  return a.gate != nullptr ? launch_any<HeadKernel<true>>(a, a.M, a.K, stream) : launch_any<HeadKernel<false>>(a, a.M, a.K, stream);
 }
-cudaError_t launch_glu_quant(const GluArgs& a, cudaStream_t stream) {
-  return with_vectors(a.F, a, a.M, stream, GluKernel());
-}
+cudaError_t launch_glu_quant(const GluArgs& a, cudaStream_t stream) { return launch_any<GluKernel>(a, a.M, a.F, stream); }
 
 }  // namespace prism

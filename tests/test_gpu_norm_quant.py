@@ -77,6 +77,9 @@ def test_every_gate():
     x = np.concatenate((z.reshape(16, 4096), np.ones((16, 4096), np.float32)), axis=1)
     for form in ("bf16", "int8"):
         check(prism.prism_glu_quant(dev(x), form=form), u.glu(x), form)
+    for up in (1.0, 1.203125, 1.6640625):       # to the last bits: a row's scale is its one value's, over 127
+        rows = np.stack([z] * 16 + [np.full_like(z, up)] * 16, axis=1)
+        check(prism.prism_glu_quant(dev(rows)), u.glu(rows), "int8")
     exact = z.astype(np.float64) / (1.0 + np.exp(-np.clip(z.astype(np.float64), -700, 700)))
     # the exponential and three more steps: 2^-21 of the value; results below 2^-126 become 0
     assert np.all(np.abs(u.silu(z) - exact) <= 2.0 ** -21 * np.abs(exact) + 2.0 ** -86)
