@@ -37,6 +37,7 @@ constexpr int kGroups = 8;            // rows of the state are divided among as 
 constexpr int kSegChunks = 4;         // chunks of a segment at least
 constexpr int kFillCtas = 304;        // segments times heads of one sequence at most: two CTAs on each of 152 SMs
 constexpr float kMinDecay = -16384.0f;   // e^x = 0 from far above it; sums of 64 stay finite
+constexpr double kLog2e = 1.4426950408889634074;
 
 // Segments that a sequence of n tokens is cut into at most, the chunks of each,
 // and as many as that makes.
@@ -182,6 +183,11 @@ __global__ void __launch_bounds__(256) linear_few_kernel(const __grid_constant__
 }
 
 // ----------------------------------------------------------------- chunks ---
+__device__ __forceinline__ float ex2(float x) {   // to about 2^-22
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -236,8 +242,8 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
   using L = Tile<DK, DV>;
   constexpr int kWarps = L::kWarps, kThreads = L::kThreads, NT = DK / 8;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 s_g[2][kChunk];              // decays summed up to a token, in two parts
-  __shared__ float s_eg[2][kChunk], s_w[2][kChunk], s_tot[2];   // e^{G_i}, e^{G_C - G_i}, e^{G_C}
+  __shared__ float2 s_g[2][kChunk];              // decays summed up to a token, in powers of two, in two parts
+  __shared__ float s_eg[2][kChunk], s_w[2][kChunk], s_tot[2];   // those of G_i, G_C - G_i and G_C
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, lr = lane >> 2, lc = lane & 3;
   const int hv = blockIdx.y, hk = hv / a.G;
@@ -343,21 +349,22 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
   };
   double log_total = 0.0;     // of the segment so far (warp 0)
   auto lay_decay = [&](int c) {
-    double sum = static_cast<double>(dec[0]) + dec[1];
+    const double d0 = dec[0] * kLog2e, d1 = dec[1] * kLog2e;
+    double sum = d0 + d1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const double v = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += v;
     }
-    const double total = __shfl_sync(0xffffffffu, sum, 31), g[2] = {sum - dec[1], sum};
+    const double total = __shfl_sync(0xffffffffu, sum, 31), g[2] = {sum - d1, sum};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const float hi = static_cast<float>(g[e]);
       s_g[c & 1][2 * lane + e] = make_float2(hi, static_cast<float>(g[e] - hi));
-      s_eg[c & 1][2 * lane + e] = expf(hi);
-      s_w[c & 1][2 * lane + e] = expf(static_cast<float>(total - g[e]));
+      s_eg[c & 1][2 * lane + e] = exp2f(hi);
+      s_w[c & 1][2 * lane + e] = exp2f(static_cast<float>(total - g[e]));
     }
-    if (lane == 0) s_tot[c & 1] = expf(static_cast<float>(total));
+    if (lane == 0) s_tot[c & 1] = exp2f(static_cast<float>(total));
     log_total += total;
   };
 
@@ -373,6 +380,7 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
     __syncthreads();     // the chunk's rows and decays are there
     const uint32_t sk = stage_k(c), sv = stage_v(c), sq = stage_q(c);
     const int64_t r0 = t0 + static_cast<int64_t>(c) * kChunk;
+    const int tiles = static_cast<int>(min(static_cast<int64_t>(kChunk), t1 - r0) + 15) >> 4;   // of 16 tokens that there are
 
     if constexpr (!kLocal) {
       // ---- scores of 16 rows and kCols columns a warp, decayed, into two bf16 parts
@@ -381,7 +389,7 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
       float x[kN][4];
 #pragma unroll
       for (int n = 0; n < kN; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.0f;
-      if (n0 <= m0 + 15) {
+      if (n0 <= m0 && m0 < 16 * tiles) {
 #pragma unroll
         for (int kk = 0; kk < DK / 16; ++kk) {
           uint32_t qa[4];
@@ -408,7 +416,7 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
             const float2 gj = s_g[c & 1][j + f];
-            y[f] = j + f <= i ? x[n][2 * e + f] * expf((gi.x - gj.x) + (gi.y - gj.y)) : 0.0f;
+            y[f] = j + f <= i ? x[n][2 * e + f] * ex2((gi.x - gj.x) + (gi.y - gj.y)) : 0.0f;
           }
           if (j > m0 + 15) continue;
           const uint32_t at_p = score_place(i, j >> 3) + (j & 7) * 2;
@@ -451,6 +459,7 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
           }
 #pragma unroll
         for (int m = 0; m < kChunk / 16; ++m) {
+          if (m >= tiles) break;
           uint32_t qa[4];
           ldmatrix_x4(sq + piece<DK>(m * 16 + (lane & 15), 2 * kk + (lane >> 4)), qa[0], qa[1], qa[2], qa[3]);
 #pragma unroll
@@ -462,6 +471,7 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
       }
 #pragma unroll
       for (int m = 0; m < kChunk / 16; ++m) {
+        if (m >= tiles) break;
         const float e0 = s_eg[c & 1][m * 16 + lr], e1 = s_eg[c & 1][m * 16 + lr + 8];
 #pragma unroll
         for (int n = 0; n < 2; ++n) o[m][n][0] *= e0, o[m][n][1] *= e0, o[m][n][2] *= e1, o[m][n][3] *= e1;
@@ -495,6 +505,7 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
     for (int t = 0; t < NT; ++t) st[t][0] *= tot, st[t][1] *= tot, st[t][2] *= tot, st[t][3] *= tot;
 #pragma unroll
     for (int kk = 0; kk < kChunk / 16; ++kk) {
+      if (kk >= tiles) break;
       uint32_t va[3][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -508,11 +519,18 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
       for (int t = 0; t < NT; t += 2) {
         uint32_t kb[4];
         ldmatrix_x4_trans(sk + piece<DK>(kk * 16 + (lane & 15), t + (lane >> 4)), kb);
+        // from zero, the small parts first, and then rounded to nearest: the tensor
+        // cores' additions cut off, and the state would gather that
+        float u[2][4] = {};
 #pragma unroll
-        for (int f = 0; f < 3; ++f) {
-          mma_bf16(st[t], va[f], kb[0], kb[1]);
-          mma_bf16(st[t + 1], va[f], kb[2], kb[3]);
+        for (int f = 2; f >= 0; --f) {
+          mma_bf16(u[0], va[f], kb[0], kb[1]);
+          mma_bf16(u[1], va[f], kb[2], kb[3]);
         }
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) st[t + f][e] += u[f][e];
       }
     }
     __syncthreads();     // the chunk's stage and scores are free
@@ -520,7 +538,7 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
   cp_async_wait<0>();
 
   if constexpr (kLocal) {
-    write_part(part + (seg + 1) * part_step, expf(static_cast<float>(log_total)));
+    write_part(part + (seg + 1) * part_step, exp2f(static_cast<float>(log_total)));
   } else if (seg + 1 == segs && p.out >= 0) {
     float* dst = a.state + (p.out * a.Hv + hv) * (DK * DV) + at;
 #pragma unroll

@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kMaxTeam, ctas_of(C)) glu_kernel(const __grid_
 // row's length alone, and with it the order of its sums.
 constexpr int vectors_of(int64_t K, bool even) {
   const int64_t n = K / 8;
-  return n <= 32 ? 1 : n <= 64 ? 2 : n <= 4 * kMaxTeam ? 4 : even ? 8 : static_cast<int>((n + kMaxTeam - 1) / kMaxTeam);
+  return n <= 32 ? 1 : n <= (even ? 2 * kMaxTeam : 64) ? 2 : n <= 4 * kMaxTeam ? 4 : even ? 8 : static_cast<int>((n + kMaxTeam - 1) / kMaxTeam);
 }
 
 // A launch of `operands` rows at a time for each CTA: as many CTAs as the SMs
