@@ -26,65 +26,14 @@
 // from the states and decays of those before it.
 #include <type_traits>
 
-#include "layer.cuh"
+#include "linear_plan.cuh"
 
 namespace prism {
 namespace {
 
-constexpr int kFewTokens = 16;
-constexpr int kChunk = 64;
+using namespace lin;
+
 constexpr int kGroups = 8;            // rows of the state are divided among as many groups of threads (few tokens)
-constexpr int kSegChunks = 4;         // chunks of a segment at least
-constexpr int kFillCtas = 304;        // segments times heads of one sequence at most: two CTAs on each of 152 SMs
-constexpr float kMinDecay = -16384.0f;   // e^x = 0 from far above it; sums of 64 stay finite
-constexpr double kLog2e = 1.4426950408889634074;
-
-// Segments that a sequence of n tokens is cut into at most, the chunks of each,
-// and as many as that makes.
-__host__ __device__ __forceinline__ int64_t most_segments(int64_t n, int64_t Hv) {
-  const int64_t cap = kFillCtas / Hv, segs = n / (kSegChunks * kChunk);
-  return segs > cap ? (cap < 1 ? 1 : cap) : segs < 1 ? 1 : segs;
-}
-__host__ __device__ __forceinline__ int64_t segment_chunks(int64_t n, int64_t Hv) {
-  const int64_t chunks = (n + kChunk - 1) / kChunk, segs = most_segments(n, Hv);
-  return (chunks + segs - 1) / segs;
-}
-__host__ __device__ __forceinline__ int64_t segment_count(int64_t n, int64_t Hv) {
-  const int64_t chunks = (n + kChunk - 1) / kChunk, each = segment_chunks(n, Hv);
-  return (chunks + each - 1) / each;
-}
-// A sequence in segments has a place in the workspace for each but the last, and
-// one for the state that it starts from: no more than whole lengths of
-// kSegChunks chunks among its tokens.
-__host__ __device__ __forceinline__ int64_t first_place(int64_t first_token) { return first_token / (kSegChunks * kChunk); }
-
-struct Span {
-  int64_t b, n;
-  int64_t in, out;     // states: -1 for none
-  bool bad;            // its rows get NaN, its state is not written
-};
-// Sequence s; false where its offsets are malformed (no rows to answer for).
-__device__ __forceinline__ bool span_of(const LinAttnArgs& a, int64_t s, bool report, Span& p) {
-  const int64_t b = a.cu != nullptr ? a.cu[s] : s, e = a.cu != nullptr ? a.cu[s + 1] : s + 1;
-  p.b = b;
-  p.n = e - b;
-  p.in = a.state_in != nullptr ? a.state_in[s] : -1;
-  p.out = a.state_out != nullptr ? a.state_out[s] : -1;
-  const bool offsets = b >= 0 && e >= b && e <= a.T;
-  const bool states = p.in >= -1 && p.in < a.num_states && p.out >= -1 && p.out < a.num_states;
-  const bool length = p.n <= a.max_len;
-  if (report && a.err != nullptr) {
-    if (!offsets || !length) atomicOr(a.err, PRISM_DEV_ERR_SEQ_RANGE);
-    if (!states) atomicOr(a.err, PRISM_DEV_ERR_STATE_RANGE);
-  }
-  p.bad = !states || !length;
-  return offsets;
-}
-
-__device__ __forceinline__ float decay_of(const LinAttnArgs& a, int64_t token, int h) {
-  const float g = __ldg(a.decay + token * a.ldd_t + h);
-  return g < kMinDecay ? kMinDecay : g;
-}
 
 // ------------------------------------------------------------- few tokens ---
 // One (sequence, head) and `width` of its columns from c0 on: kGroups groups of
@@ -164,7 +113,7 @@ __device__ __forceinline__ void spoil(const LinAttnArgs& a, const Span& p, int h
     a.out[(p.b + i / width) * a.ldo_t + hv * a.ldo_h + c0 + i % width] = static_cast<uint16_t>(kBf16NaN);
 }
 
-// Calls without longer sequences: a CTA for each `width` columns of a (sequence, head).
+// A CTA for each `width` columns of a (sequence, head).
 template <int DK>
 __global__ void __launch_bounds__(256) linear_few_kernel(const __grid_constant__ LinAttnArgs a, int width) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -173,8 +122,8 @@ __global__ void __launch_bounds__(256) linear_few_kernel(const __grid_constant__
   const int64_t s = blockIdx.x / slices;
   Span p;
   if (span_of(a, s, blockIdx.y == 0 && c0 == 0 && threadIdx.x == 0, p)) {
-    if (p.n > kFewTokens) {   // only where it is malformed
-      spoil(a, p, blockIdx.y, c0, width);
+    if (p.n > kFewTokens) {   // another kernel's, unless it is malformed
+      if (p.bad) spoil(a, p, blockIdx.y, c0, width);
     } else {
       few_tokens<DK>(a, p, blockIdx.y, c0, width, reinterpret_cast<float*>(smem));
     }
@@ -183,11 +132,6 @@ __global__ void __launch_bounds__(256) linear_few_kernel(const __grid_constant__
 }
 
 // ----------------------------------------------------------------- chunks ---
-__device__ __forceinline__ float ex2(float x) {   // to about 2^-22
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -198,18 +142,6 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// Two values as a pair of bf16, and what that leaves of them.
-__device__ __forceinline__ uint32_t split_bf16(float& lo, float& hi) {
-  const uint32_t r = pack_bf16(lo, hi);
-  lo -= bf16_lo(r);
-  hi -= bf16_hi(r);
-  return r;
 }
 // Place of 16-byte piece `ch` of row `row` in a tile of rows of W values: the
 // eight rows of a matrix touch all banks.
@@ -261,8 +193,8 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
     }
     return;
   }
-  const int64_t each = segment_chunks(p.n, a.Hv);
-  const int segs = static_cast<int>(segment_count(p.n, a.Hv));
+  const int64_t each = segment_chunks(p.n, a.seg_cap);
+  const int segs = static_cast<int>(segment_count(p.n, a.seg_cap));
   if (seg >= segs || (kLocal && seg + 1 == segs)) return;   // nothing comes after the last one
   const int64_t t0 = seg * each * kChunk, t1 = min(p.n, t0 + each * kChunk);
   const int chunks = static_cast<int>((t1 - t0 + kChunk - 1) / kChunk);
@@ -349,23 +281,7 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
   };
   double log_total = 0.0;     // of the segment so far (warp 0)
   auto lay_decay = [&](int c) {
-    const double d0 = dec[0] * kLog2e, d1 = dec[1] * kLog2e;
-    double sum = d0 + d1;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
-    }
-    const double total = __shfl_sync(0xffffffffu, sum, 31), g[2] = {sum - d1, sum};
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float hi = static_cast<float>(g[e]);
-      s_g[c & 1][2 * lane + e] = make_float2(hi, static_cast<float>(g[e] - hi));
-      s_eg[c & 1][2 * lane + e] = exp2f(hi);
-      s_w[c & 1][2 * lane + e] = exp2f(static_cast<float>(total - g[e]));
-    }
-    if (lane == 0) s_tot[c & 1] = exp2f(static_cast<float>(total));
-    log_total += total;
+    log_total += lay_decays(dec, s_g[c & 1], s_eg[c & 1], s_w[c & 1], &s_tot[c & 1]);
   };
 
   copy(0);
@@ -552,36 +468,46 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
 }
 
 template <int DK, int DV>
+cudaError_t launch_few(const LinAttnArgs& a, cudaStream_t stream) {
+  // narrow slices where whole heads leave SMs empty
+  const int width = a.S * a.Hv >= 2 * kSms ? DV : 32;
+  const dim3 grid(static_cast<unsigned>(a.S * (DV / width)), a.Hv);
+  return launch_kernel(linear_few_kernel<DK>, grid, dim3(kGroups * width / 4), few_smem(DK, width), stream, true, a, width);
+}
+
+template <int DK, int DV>
 cudaError_t launch_shape(const LinAttnArgs& a, cudaStream_t stream) {
-  using L = Tile<DK, DV>;
-  if (a.max_len <= kFewTokens) {
-    // narrow slices where whole heads leave SMs empty
-    const int width = a.S * a.Hv >= kFillCtas ? DV : 32;
-    const dim3 grid(static_cast<unsigned>(a.S * (DV / width)), a.Hv);
-    return launch_kernel(linear_few_kernel<DK>, grid, dim3(kGroups * width / 4), few_smem(DK, width), stream, true, a, width);
+  if (a.max_len <= kFewTokens) return launch_few<DK, DV>(a, stream);
+  if constexpr (DK == 128 && DV == 128) {
+    const cudaError_t e = launch_few<DK, DV>(a, stream);
+    return e == cudaSuccess ? launch_linear_attention_tc(a, stream) : e;
+  } else {
+    using L = Tile<DK, DV>;
+    const int segs = static_cast<int>(most_segments(a.max_len, a.seg_cap));
+    const dim3 grid(static_cast<unsigned>(a.S * segs), a.Hv);
+    cudaError_t e = cudaSuccess;
+    if (segs > 1) {
+      e = ensure_smem_attr(reinterpret_cast<const void*>(linear_chunk_kernel<DK, DV, true>), L::kLocalBytes);
+      if (e == cudaSuccess)
+        e = launch_kernel(linear_chunk_kernel<DK, DV, true>, grid, dim3(L::kThreads), L::kLocalBytes, stream, true, a, segs);
+    }
+    static_assert(few_smem(DK, DV) <= L::kBytes, "few tokens in the same memory");
+    if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(linear_chunk_kernel<DK, DV, false>), L::kBytes);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(linear_chunk_kernel<DK, DV, false>, grid, dim3(L::kThreads), L::kBytes, stream, true, a, segs);
   }
-  const int segs = static_cast<int>(most_segments(a.max_len, a.Hv));
-  const dim3 grid(static_cast<unsigned>(a.S * segs), a.Hv);
-  cudaError_t e = cudaSuccess;
-  if (segs > 1) {
-    e = ensure_smem_attr(reinterpret_cast<const void*>(linear_chunk_kernel<DK, DV, true>), L::kLocalBytes);
-    if (e == cudaSuccess)
-      e = launch_kernel(linear_chunk_kernel<DK, DV, true>, grid, dim3(L::kThreads), L::kLocalBytes, stream, true, a, segs);
-  }
-  static_assert(few_smem(DK, DV) <= L::kBytes, "few tokens in the same memory");
-  if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(linear_chunk_kernel<DK, DV, false>), L::kBytes);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(linear_chunk_kernel<DK, DV, false>, grid, dim3(L::kThreads), L::kBytes, stream, true, a, segs);
 }
 
 }  // namespace
 
 size_t linear_attention_workspace_bytes(int64_t T, int64_t max_len, int64_t Hv, int64_t Dk, int64_t Dv) {
-  if (most_segments(max_len, Hv) <= 1) return 0;
+  if (most_segments(max_len, segment_cap(Hv)) <= 1) return 0;
   return static_cast<size_t>(first_place(T) * Hv * (Dk * Dv + 4)) * 4;
 }
 
-cudaError_t launch_linear_attention(const LinAttnArgs& a, cudaStream_t stream) {
+cudaError_t launch_linear_attention(const LinAttnArgs& given, cudaStream_t stream) {
+  LinAttnArgs a = given;
+  a.seg_cap = segment_cap(a.Hv);
   if (a.Dk == 64) return a.Dv == 64 ? launch_shape<64, 64>(a, stream) : launch_shape<64, 128>(a, stream);
   return a.Dv == 64 ? launch_shape<128, 64>(a, stream) : launch_shape<128, 128>(a, stream);
 }

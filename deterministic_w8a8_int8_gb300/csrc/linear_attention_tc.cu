@@ -1,0 +1,611 @@
+// linear_attention_tc.cu -- the chunked form of linear attention on the tcgen05
+// tensor cores, for heads of 128 by 128 channels.
+//
+// A chunk's 64 tokens against one head (G, w, S as in linear_attention.cu), each product
+// with 128 rows in the lanes of tensor memory:
+//   A  = Q K^T          64 by 64 scores (the lower 64 lanes)          8 steps of 16
+//   O1 = S^T Q^T        128 channels of v by 64 tokens, S in two bf16 parts   2 * 8
+//   O2 = V^T (w A)^T    the same shape, the scores in two parts               2 * 4
+//   U  = (w V)^T K      128 by 128, V's decayed values in three parts         3 * 4
+// and out = scale * (e^G O1 + O2)^T, S = e^{G_C} S + U^T.  S^T and (w V)^T are
+// operands in tensor memory, formed by the warps that have the values; Q, K and V
+// are read as they lie, by tensor copies in the 128-byte-swizzled layout (K-major
+// for Q and K; for K in U and V in O2 along the tokens, the operand's other
+// major), and w A lies in shared memory beside them.  S stays in the registers of
+// eight warps (lane v channel, 64 key channels a thread) from a sequence's first
+// chunk to its last: U is formed from zero for each chunk, its small parts first,
+// and added to S rounded to nearest, since the tensor cores' additions cut off.
+//
+// One CTA an SM walks the items (sequence, head, segment).  Its warps pass chunks
+// on by mbarriers:
+//   producer (1)   finds items, copies Q, K and V of chunks ahead into three stages,
+//                  with the chunk's decays and what is to be done
+//   issuer (1)     A, U, O1, O2 of a chunk
+//   state (8)      S's two parts; S after the chunk
+//   values (4)     the decayed values' three parts ahead; outputs
+//   scores (4)     w A
+// A's columns are O2's: A of the next chunk waits for the outputs.
+//
+// Every wait on an mbarrier is bounded: after 2 s (prism_debug_wait_expiry
+// shortens that for tests) the kernel sets the device status bit; every warp leaves
+// its loop, the copies and instructions in flight complete, and the kernel returns.
+#include <cudaTypedefs.h>
+
+#include "linear_plan.cuh"
+#include "tc_common.cuh"
+
+namespace prism {
+
+__device__ uint32_t g_lin_status = 0;
+// Test mode (prism_debug_wait_expiry): the waits' limit, and whether each CTA's
+// issuer withholds the signal that its first U is formed.
+__device__ unsigned long long g_lin_wait_limit_ns = 2000000000ull;
+__device__ int g_lin_withhold = 0;
+
+namespace {
+
+using namespace lin;
+
+constexpr unsigned long long kDrainNs = 2000000000ull;
+constexpr int D = 128;
+constexpr int kStages = 3;
+constexpr int kStateWarps = 8, kIssuer = 14, kProducer = 15, kWarps = 18;   // values 8 .. 11; scores 12, 13, 16, 17
+constexpr int kThreads = kWarps * 32, kStateThreads = kStateWarps * 32;
+constexpr int kTile = kChunk * D * 2, kHalf = kTile / 2;     // of q, k or v: halves of 64 channels
+constexpr int kScores = kChunk * kChunk * 2;
+constexpr int kSmem = kStages * 3 * kTile + 2 * kScores + 1024;
+constexpr int kPart = D * D + 4;                             // floats of a segment's state in the workspace
+// columns of tensor memory
+constexpr uint32_t kColU = 0, kColS = 128, kColV = 256, kColO1 = 352, kColO2 = 416;
+
+enum { kFirst = 1, kLast = 2, kEnd = 4 };
+struct Step {          // a chunk's work
+  int64_t row;         // its first token
+  int64_t in, out;     // states: of the sequence's start (kFirst); to write to (kLast), -1 for none
+  int64_t part;        // of the sequence's first place in the workspace and this head
+  int32_t live, hv, flags, seg;   // seg: segments (places) before it that the state is made of; -1: the state slot
+  float left;          // what the segment leaves of the state before it (kLast)
+};
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, tc::mbar_wait_bounded(bar, parity, abort_flag, &g_lin_wait_limit_ns, &g_lin_status,
+                                                       PRISM_DEVSTATUS_WAIT_TIMEOUT));
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
+}
+// One arrival for the warp, after what all of its lanes did.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// A tile of rows of 64 channels, 128-byte swizzled, as an operand whose rows are
+// the contraction's: 64 channels in 128 bytes, eight rows to 1024, the other 64
+// channels a half tile on.
+__device__ __forceinline__ uint64_t desc_along_rows(uint32_t addr) {
+  return (tc::smem_desc_sw128(addr) & ~(static_cast<uint64_t>(0x3fff) << 16)) | (static_cast<uint64_t>(kHalf >> 4) << 16);
+}
+// bf16 operands, binary32 sums, M = 128.
+__device__ __forceinline__ constexpr uint32_t idesc(int n, bool a_along_rows, bool b_along_rows) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_along_rows ? 1u << 15 : 0u) | (b_along_rows ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+template <bool kLocal>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_tc_chunk_kernel(const __grid_constant__ LinAttnArgs a, const __grid_constant__ Maps maps, int max_segs) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Step s_step[kStages];
+  __shared__ float2 s_g[kStages][kChunk];
+  __shared__ __align__(16) float s_eg[kStages][kChunk], s_w[kStages][kChunk];
+  __shared__ float s_tot[kStages];
+  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 9];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t base = smem_u32(smem);
+  auto tile_q = [&](int st) { return base + st * 3 * kTile; };
+  auto tile_k = [&](int st) { return base + st * 3 * kTile + kTile; };
+  auto tile_v = [&](int st) { return base + st * 3 * kTile + 2 * kTile; };
+  const uint32_t scores = base + kStages * 3 * kTile;       // high parts, then low ones
+  const uint32_t bars = smem_u32(s_bar);
+  auto bar_full = [&](int st) { return bars + 8 * st; };
+  auto bar_free = [&](int st) { return bars + 8 * (kStages + st); };
+  const uint32_t bar_a = bars + 16 * kStages, bar_p = bar_a + 8, bar_v = bar_a + 16, bar_u = bar_a + 24, bar_ufree = bar_a + 32,
+                 bar_s = bar_a + 40, bar_o = bar_a + 48, bar_ofree = bar_a + 56, bar_end = bar_a + 64;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(bar_full(i), 1);
+      tc::mbar_init(bar_free(i), kLocal ? 1 + 4 + kStateWarps : 1 + 4 + 4 + kStateWarps);
+    }
+    tc::mbar_init(bar_a, 1);
+    tc::mbar_init(bar_p, 4);
+    tc::mbar_init(bar_v, 4);
+    tc::mbar_init(bar_u, 1);
+    tc::mbar_init(bar_ufree, kStateWarps);
+    tc::mbar_init(bar_s, kStateWarps);
+    tc::mbar_init(bar_o, 1);
+    tc::mbar_init(bar_ofree, 4);
+    tc::mbar_init(bar_end, 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = s_tmem, t_lane = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+  pdl_wait();
+  uint32_t in_flight = 0;          // stages that the producer filled, where it does not come to the end
+
+  if (warp == kProducer) {
+    // ============================ producer ================================
+    const int64_t per_seq = static_cast<int64_t>(max_segs) * a.Hv, total = a.S * per_seq;
+    bool ok = true;
+    int st = 0;
+    uint32_t round = 0, issued = 0;
+    auto turn = [&] {
+      ++issued;
+      if (++st == kStages) st = 0, ++round;
+    };
+    for (int64_t at = blockIdx.x; ok && at < total; at += 32 * static_cast<int64_t>(gridDim.x)) {
+      // 32 items at a time, one a lane: heads go by fastest, sequences slowest
+      const int64_t item = at + lane * static_cast<int64_t>(gridDim.x);
+      Span p{};
+      int hv = 0, seg = 0, segs = 0;
+      int64_t each = 0;
+      bool mine = false;
+      if (item < total) {
+        const int64_t s = item / per_seq;
+        const int rest = static_cast<int>(item - s * per_seq);
+        seg = rest / a.Hv;
+        hv = rest - seg * a.Hv;
+        mine = span_of(a, s, false, p) && !p.bad && p.n > kFewTokens;
+        if (mine) {
+          each = segment_chunks(p.n, a.seg_cap);
+          segs = static_cast<int>(segment_count(p.n, a.seg_cap));
+          mine = seg < (kLocal ? segs - 1 : segs);   // nothing comes after the last one
+        }
+      }
+      uint32_t todo = __ballot_sync(0xffffffffu, mine);
+      while (ok && todo != 0) {
+        const int from = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int64_t b = __shfl_sync(0xffffffffu, p.b, from), n = __shfl_sync(0xffffffffu, p.n, from);
+        const int64_t in = __shfl_sync(0xffffffffu, p.in, from), out = __shfl_sync(0xffffffffu, p.out, from);
+        const int64_t chunks_each = __shfl_sync(0xffffffffu, each, from);
+        const int h = __shfl_sync(0xffffffffu, hv, from), sg = __shfl_sync(0xffffffffu, seg, from);
+        const int sgs = __shfl_sync(0xffffffffu, segs, from);
+        const int64_t t0 = sg * chunks_each * kChunk, t1 = min(n, t0 + chunks_each * kChunk);
+        const int chunks = static_cast<int>((t1 - t0 + kChunk - 1) / kChunk), hk = h / a.G;
+        float dec[2];
+        auto load_decay = [&](int c) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int64_t i = t0 + static_cast<int64_t>(c) * kChunk + 2 * lane + e;
+            dec[e] = i < t1 ? decay_of(a, b + i, h) : 0.0f;
+          }
+        };
+        load_decay(0);
+        double log_total = 0.0;
+        for (int c = 0; c < chunks; ++c) {
+          ok = wait(bar_free(st), (round & 1) ^ 1u, &s_abort);
+          if (!ok) break;
+          const int32_t row = static_cast<int32_t>(b + t0 + static_cast<int64_t>(c) * kChunk);
+          log_total += lay_decays(dec, s_g[st], s_eg[st], s_w[st], &s_tot[st]);
+          if (lane == 0) {
+            Step& w = s_step[st];
+            w.row = row;
+            w.live = static_cast<int>(min(static_cast<int64_t>(kChunk), t1 - t0 - static_cast<int64_t>(c) * kChunk));
+            w.hv = h;
+            w.flags = (c == 0 ? kFirst : 0) | (c + 1 == chunks ? kLast : 0);
+            w.in = in;
+            w.out = kLocal ? sg + 1 : sg + 1 == sgs ? out : -1;
+            w.part = (first_place(b) * a.Hv + h) * kPart;
+            w.seg = kLocal ? sg : sgs == 1 ? -1 : sg;
+            w.left = c + 1 == chunks ? exp2f(static_cast<float>(log_total)) : 0.0f;
+          }
+          __syncwarp();
+          if (elect_one()) {
+            const uint32_t bar = bar_full(st);
+            tc::mbar_expect_tx(bar, (kLocal ? 2 : 3) * kTile);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if constexpr (!kLocal) tma_load_3d(tile_q(st) + half * kHalf, &maps.q, half * 64, hk, row, bar);
+              tma_load_3d(tile_k(st) + half * kHalf, &maps.k, half * 64, hk, row, bar);
+              tma_load_3d(tile_v(st) + half * kHalf, &maps.v, half * 64, h, row, bar);
+            }
+          }
+          __syncwarp();
+          if (c + 1 < chunks) load_decay(c + 1);
+          turn();
+        }
+      }
+    }
+    if (ok && wait(bar_free(st), (round & 1) ^ 1u, &s_abort)) {
+      if (lane == 0) {
+        s_step[st].flags = kEnd;
+        tc::mbar_arrive(bar_full(st));
+      }
+      __syncwarp();
+    } else {
+      in_flight = issued;
+    }
+  } else if (warp == kIssuer) {
+    // ============================ issuer ==================================
+    const bool lead = elect_one();
+    int st = 0;
+    uint32_t round = 0;
+    for (uint32_t g = 0;; ++g) {
+      if (!wait(bar_full(st), round & 1, &s_abort) || (s_step[st].flags & kEnd)) break;
+      if constexpr (!kLocal) {
+        if (g > 0 && !wait(bar_ofree, (g - 1) & 1, &s_abort)) break;
+        tc::tc_fence_after();
+        if (lead) {
+          const uint64_t qd = tc::smem_desc_sw128(tile_q(st)), kd = tc::smem_desc_sw128(tile_k(st));
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)   // rows 64 .. of Q's tile are not its: those lanes are not read
+            tc::tc_mma(tmem + kColO2, qd + (k >> 2) * (kHalf >> 4) + 2 * (k & 3), kd + (k >> 2) * (kHalf >> 4) + 2 * (k & 3),
+                       idesc(kChunk, false, false), k != 0 ? 1u : 0u);
+          tc::tc_commit(bar_a);
+        }
+        __syncwarp();
+      }
+      if (!wait(bar_v, g & 1, &s_abort)) break;
+      if (g > 0 && !wait(bar_ufree, (g - 1) & 1, &s_abort)) break;
+      tc::tc_fence_after();
+      if (lead) {
+        const uint64_t kd = desc_along_rows(tile_k(st));
+#pragma unroll
+        for (int part = 2; part >= 0; --part)   // the small parts first
+#pragma unroll
+          for (int k = 0; k < kChunk / 16; ++k)
+            tc::tc_mma_ta(tmem + kColU, tmem + kColV + part * 32 + k * 8, kd + k * (16 * 128 >> 4), idesc(D, false, true),
+                          part != 2 || k != 0 ? 1u : 0u);
+        if (g != 0 || *static_cast<volatile int*>(&g_lin_withhold) == 0) tc::tc_commit(bar_u);
+      }
+      __syncwarp();
+      if constexpr (!kLocal) {
+        if (!wait(bar_s, g & 1, &s_abort)) break;
+        tc::tc_fence_after();
+        if (lead) {
+          const uint64_t qd = tc::smem_desc_sw128(tile_q(st));
+#pragma unroll
+          for (int part = 1; part >= 0; --part)
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              tc::tc_mma_ta(tmem + kColO1, tmem + kColS + part * 64 + k * 8, qd + (k >> 2) * (kHalf >> 4) + 2 * (k & 3),
+                            idesc(kChunk, false, false), part != 1 || k != 0 ? 1u : 0u);
+        }
+        __syncwarp();
+        if (!wait(bar_p, g & 1, &s_abort)) break;
+        tc::tc_fence_after();
+        if (lead) {
+          const uint64_t vd = desc_along_rows(tile_v(st)), pd = tc::smem_desc_sw128(scores);
+#pragma unroll
+          for (int part = 1; part >= 0; --part)
+#pragma unroll
+            for (int k = 0; k < kChunk / 16; ++k)
+              tc::tc_mma(tmem + kColO2, vd + k * (16 * 128 >> 4), pd + part * (kScores >> 4) + 2 * k, idesc(kChunk, true, false),
+                         part != 1 || k != 0 ? 1u : 0u);
+          tc::tc_commit(bar_o);
+        }
+        __syncwarp();
+      }
+      if (lead) tc::tc_commit(bar_free(st));
+      __syncwarp();
+      if (++st == kStages) st = 0, ++round;
+    }
+  } else if (warp < kStateWarps) {
+    // ============================ state ===================================
+    const int half = warp >> 2, dv = (warp & 3) * 32 + lane;
+    float S[64];
+    int st = 0;
+    uint32_t round = 0;
+    for (uint32_t g = 0;; ++g) {
+      if (!wait(bar_full(st), round & 1, &s_abort)) break;
+      const Step& w = s_step[st];
+      const int flags = w.flags;
+      if (flags & kEnd) break;
+      if (flags & kFirst) {
+        const float* src = a.state + (w.in * a.Hv + w.hv) * (D * D) + half * 64 * D + dv;
+        const float* part = a.ws + w.part + tid;
+        const int64_t part_step = static_cast<int64_t>(a.Hv) * kPart;
+        const bool slot = w.in >= 0 && (kLocal ? w.seg == 0 : w.seg < 0);
+#pragma unroll
+        for (int i = 0; i < 64; ++i) S[i] = slot ? src[i * D] : 0.0f;
+        if constexpr (kLocal) {
+          // the sequence's start has a place of its own: the last segment may write
+          // the state back before another begins
+          if (w.seg == 0) {
+            float* ps = a.ws + w.part;
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+              ps[i * kStateThreads + tid] = S[i];
+              S[i] = 0.0f;
+            }
+          }
+        } else {
+          for (int k = 0; k <= w.seg; ++k) {
+            const float left = k == 0 ? 0.0f : a.ws[w.part + k * part_step + D * D];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) S[i] = fmaf(left, S[i], part[k * part_step + i * kStateThreads]);
+          }
+        }
+      }
+      if constexpr (!kLocal) {
+        if (g > 0 && !wait(bar_o, (g - 1) & 1, &s_abort)) break;   // the parts were read
+        tc::tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float x = S[i * 16 + 2 * e], y = S[i * 16 + 2 * e + 1];
+            hi[e] = split_bf16(x, y);
+            lo[e] = pack_bf16(x, y);
+          }
+          tmem_st8(t_lane + kColS + half * 32 + i * 8, hi);
+          tmem_st8(t_lane + kColS + 64 + half * 32 + i * 8, lo);
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        warp_arrive(bar_s);
+      }
+      const float tot = s_tot[st];
+      if (!wait(bar_u, g & 1, &s_abort)) break;
+      tc::tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {   // 16 at a time, by registers
+        uint32_t u[16];
+        tc::tmem_ld16(t_lane + kColU + half * 64 + i * 16, u);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) S[i * 16 + e] = fmaf(tot, S[i * 16 + e], __uint_as_float(u[e]));
+      }
+      tc::tc_fence_before();
+      warp_arrive(bar_ufree);
+      if (flags & kLast) {
+        if constexpr (kLocal) {
+          float* ps = a.ws + w.part + w.out * (static_cast<int64_t>(a.Hv) * kPart);
+#pragma unroll
+          for (int i = 0; i < 64; ++i) ps[i * kStateThreads + tid] = S[i];
+          if (tid == 0) ps[D * D] = w.left;
+        } else if (w.out >= 0) {
+          float* dst = a.state + (w.out * a.Hv + w.hv) * (D * D) + half * 64 * D + dv;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) dst[i * D] = S[i];
+        }
+      }
+      warp_arrive(bar_free(st));
+      if (++st == kStages) st = 0, ++round;
+    }
+  } else if (warp < kStateWarps + 4) {
+    // ==================== decayed values, and outputs ======================
+    const int dv = (warp & 3) * 32 + lane;
+    int st = 0, before = 0;
+    uint32_t round = 0;
+    for (uint32_t g = 0;; ++g) {
+      if (!wait(bar_full(st), round & 1, &s_abort)) break;
+      const bool end = s_step[st].flags & kEnd;
+      if (!end) {
+        const int live = s_step[st].live;
+        // Behind the sequence's end lies another, or anything: zeros, a warp's own 32
+        // channels of V and of K (eight 16-byte pieces a row).
+        for (int row = live + (lane >> 3); row < kChunk; row += 4) {
+          const uint32_t logical = ((warp & 1) * 4 + (lane & 3)) ^ (row & 7);
+          const uint32_t to = ((lane & 4) ? tile_k(st) : tile_v(st)) + ((warp & 2) ? kHalf : 0) + row * 128 + logical * 16;
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
+        }
+        __syncwarp();
+        if (g > 0 && !wait(bar_u, (g - 1) & 1, &s_abort)) break;   // the parts were read
+        tc::tc_fence_after();
+        const uint32_t v = tile_v(st) + (dv >> 6) * kHalf + (dv & 7) * 2;
+        const uint32_t piece = (dv & 63) >> 3;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t hi[16], mid[16], lo[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int j = i * 32 + 2 * e;
+            uint16_t v0, v1;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v0) : "r"(v + j * 128 + ((piece ^ (j & 7)) << 4)));
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v1) : "r"(v + (j + 1) * 128 + ((piece ^ ((j + 1) & 7)) << 4)));
+            const float2 wj = *reinterpret_cast<const float2*>(&s_w[st][j]);
+            float x = bf16_bits_to_float(v0) * wj.x, y = bf16_bits_to_float(v1) * wj.y;
+            hi[e] = split_bf16(x, y);
+            mid[e] = split_bf16(x, y);
+            lo[e] = pack_bf16(x, y);
+          }
+          tc::tmem_st16(t_lane + kColV + i * 16, hi);
+          tc::tmem_st16(t_lane + kColV + 32 + i * 16, mid);
+          tc::tmem_st16(t_lane + kColV + 64 + i * 16, lo);
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        tc::fence_proxy_async();
+        warp_arrive(bar_v);
+        if constexpr (kLocal) warp_arrive(bar_free(st));
+      }
+      if constexpr (!kLocal) {
+        if (g > 0) {   // the outputs of the chunk before
+          const Step& w = s_step[before];
+          if (!wait(bar_o, (g - 1) & 1, &s_abort)) break;
+          tc::tc_fence_after();
+          uint16_t* dst = a.out + w.row * a.ldo_t + w.hv * a.ldo_h + dv;
+          const int live = w.live;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o1[16], o2[16];
+            tc::tmem_ld16(t_lane + kColO1 + i * 16, o1);
+            tc::tmem_ld16(t_lane + kColO2 + i * 16, o2);
+            tc::tmem_wait_ld();
+            if (i == 3) {
+              tc::tc_fence_before();
+              warp_arrive(bar_ofree);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const int j = i * 16 + e;
+              const float2 eg = *reinterpret_cast<const float2*>(&s_eg[before][j]);
+              const uint32_t y = pack_bf16(fmaf(eg.x, __uint_as_float(o1[e]), __uint_as_float(o2[e])) * a.scale,
+                                           fmaf(eg.y, __uint_as_float(o1[e + 1]), __uint_as_float(o2[e + 1])) * a.scale);
+              if (j < live) dst[j * a.ldo_t] = static_cast<uint16_t>(y);
+              if (j + 1 < live) dst[(j + 1) * a.ldo_t] = static_cast<uint16_t>(y >> 16);
+            }
+          }
+          warp_arrive(bar_free(before));
+        }
+      }
+      if (end) break;
+      before = st;
+      if (++st == kStages) st = 0, ++round;
+    }
+  } else if constexpr (!kLocal) {
+    // ============================ scores ==================================
+    const int i = (warp & 1) * 32 + lane, j0 = warp >= 16 ? 32 : 0;   // row; first of 32 columns
+    int st = 0;
+    uint32_t round = 0;
+    for (uint32_t g = 0;; ++g) {
+      if (!wait(bar_full(st), round & 1, &s_abort) || (s_step[st].flags & kEnd)) break;
+      if (!wait(bar_a, g & 1, &s_abort)) break;
+      tc::tc_fence_after();
+      const float2 gi = s_g[st][i];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t x[16];
+        tc::tmem_ld16(t_lane + kColO2 + j0 + q * 16, x);
+        tc::tmem_wait_ld();
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int j = j0 + q * 16 + 2 * e;
+          float y[2];
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const float2 gj = s_g[st][j + f];
+            const float w = ex2((gi.x - gj.x) + (gi.y - gj.y));
+            y[f] = j + f <= i ? __uint_as_float(x[2 * e + f]) * w : 0.0f;
+          }
+          hi[e] = split_bf16(y[0], y[1]);
+          lo[e] = pack_bf16(y[0], y[1]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const uint32_t to = scores + i * 128 + (((j0 >> 3) + q * 2 + (e >> 2)) ^ (i & 7)) * 16;
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[e]), "r"(hi[e + 1]), "r"(hi[e + 2]), "r"(hi[e + 3])
+                       : "memory");
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + kScores), "r"(lo[e]), "r"(lo[e + 1]), "r"(lo[e + 2]),
+                       "r"(lo[e + 3])
+                       : "memory");
+        }
+      }
+      tc::tc_fence_before();
+      tc::fence_proxy_async();
+      warp_arrive(bar_p);
+      warp_arrive(bar_free(st));
+      if (++st == kStages) st = 0, ++round;
+    }
+  }
+
+  // ---- every copy and instruction in flight completes before memory is given back
+  // (copies: at the end, every one was waited for)
+  if (lane == 0)
+    for (uint32_t i = in_flight > kStages ? in_flight - kStages : 0; i < in_flight; ++i)
+      tc::mbar_wait_drain_bounded(bar_full(i % kStages), (i / kStages) & 1, kDrainNs, &g_lin_status, PRISM_DEVSTATUS_WAIT_TIMEOUT);
+  __syncwarp();
+  if (warp == kIssuer && elect_one()) {
+    tc::tc_commit(bar_end);
+    tc::mbar_wait_drain_bounded(bar_end, 0, kDrainNs, &g_lin_status, PRISM_DEVSTATUS_WAIT_TIMEOUT);
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc::tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+  pdl_trigger();
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const auto fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
+  }();
+  return fn;
+}
+
+// [T, H, 128] bf16 in boxes of 64 tokens of a head by 64 channels; rows past T read 0.
+cudaError_t make_map(CUtensorMap* m, const uint16_t* ptr, int64_t T, int64_t H, int64_t ld_t, int64_t ld_h) {
+  const auto fn = encode_fn();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(H > 1 ? ld_h : D) * 2, static_cast<cuuint64_t>(ld_t) * 2};
+  const cuuint32_t box[3] = {64, 1, kChunk}, steps[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(ptr), dims, strides, box, steps,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_linear_attention_tc(const LinAttnArgs& a, cudaStream_t stream) {
+  Maps maps;
+  cudaError_t e = make_map(&maps.q, a.q, a.T, a.Hk, a.ldq_t, a.ldq_h);
+  if (e == cudaSuccess) e = make_map(&maps.k, a.k, a.T, a.Hk, a.ldk_t, a.ldk_h);
+  if (e == cudaSuccess) e = make_map(&maps.v, a.v, a.T, a.Hv, a.ldv_t, a.ldv_h);
+  if (e != cudaSuccess) return e;
+  const int segs = static_cast<int>(most_segments(a.max_len, a.seg_cap));
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.S * segs * a.Hv, sm_count()));
+  if (segs > 1) {
+    e = ensure_smem_attr(reinterpret_cast<const void*>(linear_tc_chunk_kernel<true>), kSmem);
+    if (e == cudaSuccess)
+      e = launch_kernel(linear_tc_chunk_kernel<true>, dim3(grid), dim3(kThreads), kSmem, stream, true, a, maps, segs);
+  }
+  if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(linear_tc_chunk_kernel<false>), kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(linear_tc_chunk_kernel<false>, dim3(grid), dim3(kThreads), kSmem, stream, true, a, maps, segs);
+}
+
+cudaError_t read_and_clear_linear_status(uint32_t* out) {
+  uint32_t v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_lin_status, sizeof v);
+  if (e != cudaSuccess) return e;
+  if (v != 0) {
+    const uint32_t zero = 0;
+    e = cudaMemcpyToSymbol(g_lin_status, &zero, sizeof zero);
+  }
+  *out = v;
+  return e;
+}
+
+cudaError_t set_linear_wait_expiry(unsigned long long limit_ns, int withhold) {
+  cudaError_t e = cudaMemcpyToSymbol(g_lin_wait_limit_ns, &limit_ns, sizeof limit_ns);
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_lin_withhold, &withhold, sizeof withhold);
+  return e;
+}
+
+}  // namespace prism

@@ -1,0 +1,131 @@
+// linear_plan.cuh -- how a call of linear attention is cut up, and what its
+// kernels share.
+//
+// Up to kFewTokens tokens of a sequence take the recurrence as it stands, more
+// go by in chunks.  A long sequence is cut into segments, by its length and the
+// number of heads alone, so that a sequence's bits do not depend on the batch: a
+// first kernel forms each segment's own state from zero, and the second starts
+// each segment from the states and decays of those before it.
+#pragma once
+
+#include "layer.cuh"
+
+namespace prism {
+namespace lin {
+
+constexpr int kFewTokens = 16;
+constexpr int kChunk = 64;
+constexpr int kSegChunks = 8;         // chunks of a segment at least
+constexpr int kMaxSegments = 24;
+constexpr int kSms = 152;             // that segments are cut for, whatever the device has
+constexpr float kMinDecay = -16384.0f;   // e^x = 0 from far above it; sums of 64 stay finite
+constexpr double kLog2e = 1.4426950408889634074;
+
+// The segments of a long sequence: those with which its heads fill the SMs in the
+// fewest turns for what each then has to do, kMaxSegments at most (a segment reads
+// the states of those before it).  One where more do not save a third: keys and
+// values are read twice.
+inline int64_t segment_cap(int64_t Hv) {
+  const int64_t most = std::max<int64_t>(8, std::min<int64_t>(kMaxSegments, kSms / Hv));
+  auto turns = [&](int64_t n) { return (n * Hv + kSms - 1) / kSms; };
+  int64_t best = 1;
+  for (int64_t n = 2; n <= most; ++n)
+    if (turns(n) * best < turns(best) * n) best = n;
+  return turns(best) * 3 <= turns(1) * best * 2 ? best : 1;
+}
+// Segments that a sequence of n tokens is cut into at most, the chunks of each,
+// and as many as that makes.
+__host__ __device__ __forceinline__ int64_t most_segments(int64_t n, int64_t cap) {
+  const int64_t segs = n / (kSegChunks * kChunk);
+  return segs > cap ? cap : segs < 1 ? 1 : segs;
+}
+__host__ __device__ __forceinline__ int64_t segment_chunks(int64_t n, int64_t cap) {
+  const int64_t chunks = (n + kChunk - 1) / kChunk, segs = most_segments(n, cap);
+  return (chunks + segs - 1) / segs;
+}
+__host__ __device__ __forceinline__ int64_t segment_count(int64_t n, int64_t cap) {
+  const int64_t chunks = (n + kChunk - 1) / kChunk, each = segment_chunks(n, cap);
+  return (chunks + each - 1) / each;
+}
+// A sequence in segments has a place in the workspace for each but the last, and
+// one for the state that it starts from: no more than whole lengths of
+// kSegChunks chunks among its tokens.
+__host__ __device__ __forceinline__ int64_t first_place(int64_t first_token) { return first_token / (kSegChunks * kChunk); }
+
+struct Span {
+  int64_t b, n;
+  int64_t in, out;     // states: -1 for none
+  bool bad;            // its rows get NaN, its state is not written
+};
+// Sequence s; false where its offsets are malformed (no rows to answer for).
+__device__ __forceinline__ bool span_of(const LinAttnArgs& a, int64_t s, bool report, Span& p) {
+  const int64_t b = a.cu != nullptr ? a.cu[s] : s, e = a.cu != nullptr ? a.cu[s + 1] : s + 1;
+  p.b = b;
+  p.n = e - b;
+  p.in = a.state_in != nullptr ? a.state_in[s] : -1;
+  p.out = a.state_out != nullptr ? a.state_out[s] : -1;
+  const bool offsets = b >= 0 && e >= b && e <= a.T;
+  const bool states = p.in >= -1 && p.in < a.num_states && p.out >= -1 && p.out < a.num_states;
+  const bool length = p.n <= a.max_len;
+  if (report && a.err != nullptr) {
+    if (!offsets || !length) atomicOr(a.err, PRISM_DEV_ERR_SEQ_RANGE);
+    if (!states) atomicOr(a.err, PRISM_DEV_ERR_STATE_RANGE);
+  }
+  p.bad = !states || !length;
+  return offsets;
+}
+
+__device__ __forceinline__ float decay_of(const LinAttnArgs& a, int64_t token, int h) {
+  const float g = __ldg(a.decay + token * a.ldd_t + h);
+  return g < kMinDecay ? kMinDecay : g;
+}
+
+// Two values as a pair of bf16, and what that leaves of them.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t split_bf16(float& lo, float& hi) {
+  const uint32_t r = pack_bf16(lo, hi);
+  lo -= bf16_lo(r);
+  hi -= bf16_hi(r);
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {   // to about 2^-22
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The decays of a chunk's 64 tokens, two a lane (0 past the end), summed up:
+// in powers of two up to each token (in two parts), and the factors that these
+// are, that the chunk's end has left of each token, and of the whole chunk.
+// Returns the chunk's sum.
+__device__ __forceinline__ double lay_decays(const float (&dec)[2], float2* g2, float* eg, float* w, float* tot) {
+  const int lane = threadIdx.x & 31;
+  const double d0 = dec[0] * kLog2e, d1 = dec[1] * kLog2e;
+  double sum = d0 + d1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  const double total = __shfl_sync(0xffffffffu, sum, 31), g[2] = {sum - d1, sum};
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float hi = static_cast<float>(g[e]);
+    g2[2 * lane + e] = make_float2(hi, static_cast<float>(g[e] - hi));
+    eg[2 * lane + e] = exp2f(hi);
+    w[2 * lane + e] = exp2f(static_cast<float>(total - g[e]));
+  }
+  if (lane == 0) *tot = exp2f(static_cast<float>(total));
+  return total;
+}
+
+}  // namespace lin
+
+// The tcgen05 kernel (linear_attention_tc.cu): heads of 128 by 128 channels, sequences of
+// more than lin::kFewTokens tokens.
+cudaError_t launch_linear_attention_tc(const LinAttnArgs& a, cudaStream_t stream);
+}  // namespace prism

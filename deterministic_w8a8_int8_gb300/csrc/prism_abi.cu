@@ -4,6 +4,7 @@
 #include <mutex>
 
 #include "decode.cuh"
+#include "layer.cuh"
 
 namespace prism {
 
@@ -280,12 +281,13 @@ int prism_w8a8_kernel_kind(int64_t M, int64_t N, int64_t K) { return prism::line
 
 int prism_device_status(uint32_t* flags) {
   if (flags == nullptr) return PRISM_ERR_INVALID_ARG;
-  uint32_t a = 0, b = 0, c = 0, d = 0;
+  uint32_t a = 0, b = 0, c = 0, d = 0, l = 0;
   int st = prism::record_cuda(prism::read_and_clear_kernel_error(&a));
   if (st == PRISM_OK) st = prism::record_cuda(prism::read_and_clear_f16_status(&b));
   if (st == PRISM_OK) st = prism::record_cuda(prism::read_and_clear_kv_status(&c));
   if (st == PRISM_OK) st = prism::record_cuda(prism::read_and_clear_w4g_status(&d));
-  *flags = a | b | c | d;
+  if (st == PRISM_OK) st = prism::record_cuda(prism::read_and_clear_linear_status(&l));
+  *flags = a | b | c | d | l;
   return st;
 }
 
@@ -296,6 +298,7 @@ int prism_debug_wait_expiry(uint64_t limit_ns) {
   if (st == PRISM_OK) st = prism::record_cuda(prism::set_f16_wait_expiry(v, withhold));
   if (st == PRISM_OK) st = prism::record_cuda(prism::set_kv_wait_expiry(v, withhold));
   if (st == PRISM_OK) st = prism::record_cuda(prism::set_w4g_wait_expiry(v, withhold));
+  if (st == PRISM_OK) st = prism::record_cuda(prism::set_linear_wait_expiry(v, withhold));
   return st;
 }
 

@@ -57,7 +57,7 @@ def check(data, lens, start, got, states, scale=None):
     assert np.all(off <= after_bound), f"state: {np.max(off / after_bound)} of the bound"
 
 
-LENS = [[1], [1, 1, 1], [2, 16, 15], [17], [63, 64, 65], [0, 1, 130, 0, 40, 16], [255, 3, 256, 257], [511], [512], [513, 1], [1100, 700]]
+LENS = [[1], [1, 1, 1], [2, 16, 15], [17], [63, 64, 65], [0, 1, 130, 0, 40, 16], [255, 3, 256, 257], [511], [512], [513, 1], [1100, 1023], [1024], [2600, 17, 1537]]
 
 
 @pytest.mark.parametrize("lens", LENS, ids=lambda x: "-".join(map(str, x)))
@@ -105,22 +105,23 @@ def test_branches_of_one_parent():
 
 def test_a_text_in_pieces():
     """Pieces that hand the state on, against the whole text."""
-    lens = [700]
+    lens = [2300]
     data = make(5, lens, 1, 2, 128, 128)
     dstate = torch.zeros((1, 2, 128, 128), device="cuda")
     outs, at = [], 0
-    for n in (1, 130, 16, 17, 300, 236):
+    for n in (1, 130, 16, 17, 1500, 636):
         piece = tuple(x[at:at + n] for x in data)
         outs.append(run(piece, [n], dstate, index([0]), index([0])))
         at += n
-    assert at == 700
+    assert at == 2300
     check(data, lens, np.zeros((1, 2, 128, 128)), torch.cat(outs), dstate)
 
 
 @pytest.mark.parametrize("kind", ["-inf", "strong", "mixed", "growing", "none"])
-@pytest.mark.parametrize("lens", [[9], [200], [600]], ids=str)
-def test_decays(lens, kind):
-    data = list(make(6, lens, 1, 3, 64, 64))
+@pytest.mark.parametrize("lens", [[9], [200], [1200]], ids=str)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_decays(lens, kind, dim):
+    data = list(make(6, lens, 1, 3, dim, dim))
     g = data[3]
     if kind == "-inf":
         g[::7] = -np.inf
@@ -133,32 +134,33 @@ def test_decays(lens, kind):
         g[:] = 0.01
     else:
         g[:] = 0.0
-    state = np.random.default_rng(4).standard_normal((1, 3, 64, 64)).astype(np.float32)
+    state = np.random.default_rng(4).standard_normal((1, 3, dim, dim)).astype(np.float32)
     dstate = dev(state, torch.float32)
     got = run(data, lens, dstate, index([0]), index([0]))
     check(data, lens, state, got, dstate)
 
 
-def test_strides_scale_and_rows_past_the_end():
+@pytest.mark.parametrize("dk", [64, 128])
+def test_strides_scale_and_rows_past_the_end(dk):
     lens = [70, 5]
-    q, k, v, g = make(7, lens, 2, 4, 64, 128)
+    q, k, v, g = make(7, lens, 2, 4, dk, 128)
     t = sum(lens)
-    buf = torch.full((t, 2, 3 * 64 + 8), math.nan, dtype=torch.bfloat16, device="cuda")     # q and k of wider rows
-    buf[..., :64], buf[..., 128:192] = dev(q), dev(k)
+    buf = torch.full((t, 2, 3 * dk + 8), math.nan, dtype=torch.bfloat16, device="cuda")     # q and k of wider rows
+    buf[..., :dk], buf[..., 2 * dk:3 * dk] = dev(q), dev(k)
     vb = torch.full((4, t, 136), math.nan, dtype=torch.bfloat16, device="cuda")              # heads outermost
     vb[..., :128] = dev(v).transpose(0, 1)
     gb = torch.full((t, 9), math.nan, device="cuda")
     gb[:, :4] = dev(g, torch.float32)
     ob = torch.full((t, 4, 160), 5.0, dtype=torch.bfloat16, device="cuda")
-    out = prism.prism_linear_attention(buf[..., :64], buf[..., 128:192], vb[..., :128].transpose(0, 1), gb[:, :4],
+    out = prism.prism_linear_attention(buf[..., :dk], buf[..., 2 * dk:3 * dk], vb[..., :128].transpose(0, 1), gb[:, :4],
                                        cu=offsets(lens), max_len=70, scale=-0.3, out=ob[..., :128])
     assert bool((ob[..., 128:] == 5).all())
-    want, bound, *_ = u.linear_attention(q, k, v, g, np.zeros((2, 4, 64, 128)), lens, -0.3)
+    want, bound, *_ = u.linear_attention(q, k, v, g, np.zeros((2, 4, dk, 128)), lens, -0.3)
     assert np.all(np.abs(out.double().cpu().numpy() - want) <= bound)
 
 
 def test_bits_do_not_depend_on_the_batch():
-    lens = [5, 900, 17, 64, 300, 16, 0, 1]
+    lens = [5, 1900, 17, 64, 300, 16, 0, 1]
     data = make(8, lens, 2, 4, 128, 128)
     state = dev(np.random.default_rng(5).standard_normal((8, 4, 128, 128)), torch.float32)
     own = index(list(range(8)))
@@ -168,7 +170,7 @@ def test_bits_do_not_depend_on_the_batch():
     for i, n in enumerate(lens):
         alone = state.clone()
         piece = tuple(x[at:at + n] for x in data)
-        for most in {max(n, 1), 16 if n <= 16 else n, 900}:
+        for most in {max(n, 1), 16 if n <= 16 else n, 1900}:
             alone = state.clone()
             one = run(piece, [n], alone, index([i]), index([i]), max_len=most)
             assert torch.equal(one, got[at:at + n]) and torch.equal(alone[i], all_state[i])
@@ -189,10 +191,11 @@ def test_many_sequences_of_few_tokens():
     check(data, lens, state.cpu().numpy(), got, many)
 
 
-def test_errors():
+@pytest.mark.parametrize("dim", [64, 128])
+def test_errors(dim):
     lens = [20, 3, 40, 2, 300]
-    data = make(10, lens, 1, 2, 64, 64)
-    state = np.random.default_rng(7).standard_normal((5, 2, 64, 64)).astype(np.float32)
+    data = make(10, lens, 1, 2, dim, dim)
+    state = np.random.default_rng(7).standard_normal((5, 2, dim, dim)).astype(np.float32)
     for first, last, most, bit, bad in (
             ([0, 5, 2, 3, 4], [0, 1, 2, 3, 4], 300, 128, [1]), ([0, 1, -2, 3, 4], [0, 1, 2, 3, 4], 300, 128, [2]),
             ([0, 1, 2, 3, 4], [0, 1, 2, 3, 1 << 30], 300, 128, [4]), ([0, 1, 2, 3, 4], [-7, 1, 2, 3, 4], 300, 128, [0]),
@@ -209,7 +212,7 @@ def test_errors():
             at += n
     cu = index([0, 20, 10, 400, 65, 365])      # two that end before they begin or behind the rows
     err, dstate = index([0]), dev(state, torch.float32)
-    out = torch.full((365, 2, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((365, 2, dim), 5.0, dtype=torch.bfloat16, device="cuda")
     own = index([0, 1, 2, 3, 4])
     prism.prism_linear_attention(*(dev(x) for x in data[:3]), dev(data[3], torch.float32), dstate, own, own, cu=cu,
                                  max_len=300, out=out, err=err)
@@ -218,26 +221,26 @@ def test_errors():
 
 
 def test_streams_graphs_and_given_workspaces():
-    lens = [600, 30]
+    lens = [1600, 30]
     data = make(11, lens, 2, 4, 128, 128)
     args = [dev(x) for x in data[:3]] + [dev(data[3], torch.float32)]
     state = dev(np.random.default_rng(8).standard_normal((2, 4, 128, 128)), torch.float32)
     own, cu = index([0, 1]), offsets(lens)
     want_state = state.clone()
-    want = prism.prism_linear_attention(*args, want_state, own, own, cu=cu, max_len=600)
-    size = prism.prism_linear_attention_workspace_bytes(2, 630, 600, 4, 128, 128)
+    want = prism.prism_linear_attention(*args, want_state, own, own, cu=cu, max_len=1600)
+    size = prism.prism_linear_attention_workspace_bytes(2, 1630, 1600, 4, 128, 128)
     ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")       # any contents
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     mine = state.clone()
     side.wait_stream(torch.cuda.current_stream())
-    got = prism.prism_linear_attention(*args, mine, own, own, cu=cu, max_len=600, workspace=ws, stream=side)
+    got = prism.prism_linear_attention(*args, mine, own, own, cu=cu, max_len=1600, workspace=ws, stream=side)
     side.synchronize()
     assert torch.equal(got, want) and torch.equal(mine, want_state)
     graph = torch.cuda.CUDAGraph()
     buf = state.clone()
     with torch.cuda.graph(graph):
-        out = prism.prism_linear_attention(*args, buf, own, own, cu=cu, max_len=600)
+        out = prism.prism_linear_attention(*args, buf, own, own, cu=cu, max_len=1600)
     for _ in range(2):
         buf.copy_(state)
         graph.replay()
@@ -258,12 +261,12 @@ def test_states_without_tokens():
     dict(state_in=index, state=None), dict(max_len=0), dict(log_decay="wide"), dict(cu="short"), dict(state="small"),
     dict(out="float"), dict(workspace="small"), dict(scale=math.nan), dict(k="short")])
 def test_refusals(kw):
-    q = torch.zeros((600, 2, 64), dtype=torch.bfloat16, device="cuda")
-    g = torch.zeros((600, 2), device="cuda")
-    d = dict(k=q, state=torch.zeros((2, 2, 64, 64), device="cuda"), state_in=None, state_out=None, cu=index([0, 600]), max_len=600)
+    q = torch.zeros((1600, 2, 64), dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros((1600, 2), device="cuda")
+    d = dict(k=q, state=torch.zeros((2, 2, 64, 64), device="cuda"), state_in=None, state_out=None, cu=index([0, 1600]), max_len=1600)
     d.update(kw)
     if d.get("log_decay") == "wide":
-        g = torch.zeros((600, 3), device="cuda")
+        g = torch.zeros((1600, 3), device="cuda")
     d.pop("log_decay", None)
     if d["cu"] == "short" if isinstance(d["cu"], str) else False:
         d["cu"] = index([])

@@ -36,7 +36,7 @@ def glu(L, **kw):
 
 def linear(L, **kw):
     d = dict(q=A, ldq_t=256, ldq_h=128, k=A, ldk_t=256, ldk_h=128, v=A, ldv_t=512, ldv_h=128, g=A, ldd=4, state=A, si=A, so=A,
-             cu=A, out=A, ldo_t=512, ldo_h=128, scale=0.1, S=3, T=900, max_len=900, slots=5, hk=2, hv=4, dk=128, dv=128, ws=A,
+             cu=A, out=A, ldo_t=512, ldo_h=128, scale=0.1, S=3, T=2000, max_len=2000, slots=5, hk=2, hv=4, dk=128, dv=128, ws=A,
              bytes=1 << 40, err=None)
     d.update(kw)
     return L.prism_linear_attention(d["q"], d["ldq_t"], d["ldq_h"], d["k"], d["ldk_t"], d["ldk_h"], d["v"], d["ldv_t"],
@@ -93,13 +93,13 @@ def test_nothing_to_do(L):
 
 
 def test_workspace(L):
-    """None for calls that are not cut into segments; else a place of states for each 256 tokens at most."""
+    """None for calls that are not cut into segments; else a place of states for each 512 tokens at most."""
     f = L.prism_linear_attention_workspace_bytes
-    assert f(64, 64, 1, 40, 128, 128) == 0 and f(1, 511, 511, 40, 128, 128) == 0 and f(0, 0, 1, 40, 128, 128) == 0
-    assert f(1, 512, 512, 40, 128, 96) == 0
+    assert f(64, 64, 1, 40, 128, 128) == 0 and f(1, 1023, 1023, 40, 128, 128) == 0 and f(0, 0, 1, 40, 128, 128) == 0
+    assert f(1, 1024, 1024, 40, 128, 96) == 0
     one = 40 * (128 * 128 + 4) * 4
-    assert f(1, 512, 512, 40, 128, 128) == 2 * one
-    assert f(3, 8191, 8191, 40, 128, 128) <= 32 * one
+    assert f(1, 1024, 1024, 40, 128, 128) == 2 * one
+    assert f(3, 8191, 8191, 40, 128, 128) <= 16 * one
     assert f(1, 1 << 20, 1 << 20, 400, 128, 128) == 0     # heads enough
 
 
