@@ -403,6 +403,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kStateWarps + 4) {
     // ==================== decayed values, and outputs ======================
     const int dv = (warp & 3) * 32 + lane;
+    uint32_t swizzled[8];      // place of the thread's channel in a row, by the row's number within eight
+#pragma unroll
+    for (int r = 0; r < 8; ++r) swizzled[r] = r * 128 + ((((dv & 63) >> 3) ^ r) << 4);
     int st = 0, before = 0;
     uint32_t round = 0;
     for (uint32_t g = 0;; ++g) {
@@ -421,25 +424,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (g > 0 && !wait(bar_u, (g - 1) & 1, &s_abort)) break;   // the parts were read
         tc::tc_fence_after();
         const uint32_t v = tile_v(st) + (dv >> 6) * kHalf + (dv & 7) * 2;
-        const uint32_t piece = (dv & 63) >> 3;
+        // rolled: the kinds of warps share the instruction cache
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          uint32_t hi[8], mid[8], lo[8];
+          float4 wj[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t hi[16], mid[16], lo[16];
+          for (int e = 0; e < 4; ++e) wj[e] = *reinterpret_cast<const float4*>(&s_w[st][i * 16 + e * 4]);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int j = i * 32 + 2 * e;
+          for (int e = 0; e < 8; ++e) {
             uint16_t v0, v1;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v0) : "r"(v + j * 128 + ((piece ^ (j & 7)) << 4)));
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v1) : "r"(v + (j + 1) * 128 + ((piece ^ ((j + 1) & 7)) << 4)));
-            const float2 wj = *reinterpret_cast<const float2*>(&s_w[st][j]);
-            float x = bf16_bits_to_float(v0) * wj.x, y = bf16_bits_to_float(v1) * wj.y;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v0) : "r"(v + i * 2048 + (e >> 2) * 1024 + swizzled[2 * e & 7]));
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v1) : "r"(v + i * 2048 + (e >> 2) * 1024 + swizzled[(2 * e & 7) + 1]));
+            const float4 w4 = wj[e >> 1];
+            float x = bf16_bits_to_float(v0) * (e & 1 ? w4.z : w4.x), y = bf16_bits_to_float(v1) * (e & 1 ? w4.w : w4.y);
             hi[e] = split_bf16(x, y);
             mid[e] = split_bf16(x, y);
             lo[e] = pack_bf16(x, y);
           }
-          tc::tmem_st16(t_lane + kColV + i * 16, hi);
-          tc::tmem_st16(t_lane + kColV + 32 + i * 16, mid);
-          tc::tmem_st16(t_lane + kColV + 64 + i * 16, lo);
+          tmem_st8(t_lane + kColV + i * 8, hi);
+          tmem_st8(t_lane + kColV + 32 + i * 8, mid);
+          tmem_st8(t_lane + kColV + 64 + i * 8, lo);
         }
         tc::tmem_wait_st();
         tc::tc_fence_before();
@@ -454,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tc_fence_after();
           uint16_t* dst = a.out + w.row * a.ldo_t + w.hv * a.ldo_h + dv;
           const int live = w.live;
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             uint32_t o1[16], o2[16];
             tc::tmem_ld16(t_lane + kColO1 + i * 16, o1);
@@ -464,14 +469,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::tc_fence_before();
               warp_arrive(bar_ofree);
             }
+            const int here = live - i * 16;
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              const int j = i * 16 + e;
-              const float2 eg = *reinterpret_cast<const float2*>(&s_eg[before][j]);
+              const float2 eg = *reinterpret_cast<const float2*>(&s_eg[before][i * 16 + e]);
               const uint32_t y = pack_bf16(fmaf(eg.x, __uint_as_float(o1[e]), __uint_as_float(o2[e])) * a.scale,
                                            fmaf(eg.y, __uint_as_float(o1[e + 1]), __uint_as_float(o2[e + 1])) * a.scale);
-              if (j < live) dst[j * a.ldo_t] = static_cast<uint16_t>(y);
-              if (j + 1 < live) dst[(j + 1) * a.ldo_t] = static_cast<uint16_t>(y >> 16);
+              if (e < here) *dst = static_cast<uint16_t>(y);
+              dst += a.ldo_t;
+              if (e + 1 < here) *dst = static_cast<uint16_t>(y >> 16);
+              dst += a.ldo_t;
             }
           }
           warp_arrive(bar_free(before));
@@ -491,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(bar_a, g & 1, &s_abort)) break;
       tc::tc_fence_after();
       const float2 gi = s_g[st][i];
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < 2; ++q) {
         uint32_t x[16];
         tc::tmem_ld16(t_lane + kColO2 + j0 + q * 16, x);
