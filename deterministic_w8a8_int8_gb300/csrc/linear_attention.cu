@@ -17,7 +17,7 @@
 // wants.  What is not bf16 already is split into bf16 parts: scores and the state
 // where it is read out into two (2^-17 of the value), the decayed values of the
 // update into three (2^-25), so that states are as good as binary32 sums.  Sums
-// of decays are kept as two binary32 numbers (from a scan in 64 bits): their
+// of decays are kept as two binary32 numbers (and added as such): their
 // differences decide.
 //
 // A long sequence is cut into segments (by its length and the number of heads
@@ -279,9 +279,9 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
       dec[e] = i < t1 ? decay_of(a, p.b + i, hv) : 0.0f;
     }
   };
-  double log_total = 0.0;     // of the segment so far (warp 0)
+  Sum log_total{0.0f, 0.0f};  // of the segment so far (warp 0)
   auto lay_decay = [&](int c) {
-    log_total += lay_decays(dec, s_g[c & 1], s_eg[c & 1], s_w[c & 1], &s_tot[c & 1]);
+    log_total = join(log_total, lay_decays(dec, s_g[c & 1], s_eg[c & 1], s_w[c & 1], &s_tot[c & 1]));
   };
 
   copy(0);
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
   cp_async_wait<0>();
 
   if constexpr (kLocal) {
-    write_part(part + (seg + 1) * part_step, exp2f(static_cast<float>(log_total)));
+    write_part(part + (seg + 1) * part_step, exp2f(log_total.h + log_total.l));
   } else if (seg + 1 == segs && p.out >= 0) {
     float* dst = a.state + (p.out * a.Hv + hv) * (DK * DV) + at;
 #pragma unroll

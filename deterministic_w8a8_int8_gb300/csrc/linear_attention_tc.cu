@@ -21,9 +21,9 @@
 //   producer (1)   finds items, copies Q, K and V of chunks ahead into three stages,
 //                  with the chunk's decays and what is to be done
 //   issuer (1)     A, U, O1, O2 of a chunk
-//   state (8)      S's two parts; S after the chunk
-//   values (4)     the decayed values' three parts ahead; outputs
+//   state (8)      the decayed values' three parts, S's two parts; S after the chunk
 //   scores (4)     w A
+//   outputs (4)
 // A's columns are O2's: A of the next chunk waits for the outputs.
 //
 // Every wait on an mbarrier is bounded: after 2 s (prism_debug_wait_expiry
@@ -49,7 +49,7 @@ using namespace lin;
 constexpr unsigned long long kDrainNs = 2000000000ull;
 constexpr int D = 128;
 constexpr int kStages = 3;
-constexpr int kStateWarps = 8, kIssuer = 14, kProducer = 15, kWarps = 18;   // values 8 .. 11; scores 12, 13, 16, 17
+constexpr int kStateWarps = 8, kIssuer = 14, kProducer = 15, kWarps = 18;   // outputs 8 .. 11; scores 12, 13, 16, 17
 constexpr int kThreads = kWarps * 32, kStateThreads = kStateWarps * 32;
 constexpr int kTile = kChunk * D * 2, kHalf = kTile / 2;     // of q, k or v: halves of 64 channels
 constexpr int kScores = kChunk * kChunk * 2;
@@ -79,6 +79,9 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t one;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
   return one != 0;
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]));
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
@@ -132,12 +135,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                  bar_s = bar_a + 40, bar_o = bar_a + 48, bar_ofree = bar_a + 56, bar_end = bar_a + 64;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      tc::mbar_init(bar_full(i), 1);
-      tc::mbar_init(bar_free(i), kLocal ? 1 + 4 + kStateWarps : 1 + 4 + 4 + kStateWarps);
+      tc::mbar_init(bar_full(i), 2);   // the copies, and what the producer writes itself
+      tc::mbar_init(bar_free(i), kLocal ? 1 + kStateWarps : 1 + kStateWarps + 4 + 4);
     }
     tc::mbar_init(bar_a, 1);
     tc::mbar_init(bar_p, 4);
-    tc::mbar_init(bar_v, 4);
+    tc::mbar_init(bar_v, kStateWarps);
     tc::mbar_init(bar_u, 1);
     tc::mbar_init(bar_ufree, kStateWarps);
     tc::mbar_init(bar_s, kStateWarps);
@@ -198,34 +201,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int sgs = __shfl_sync(0xffffffffu, segs, from);
         const int64_t t0 = sg * chunks_each * kChunk, t1 = min(n, t0 + chunks_each * kChunk);
         const int chunks = static_cast<int>((t1 - t0 + kChunk - 1) / kChunk), hk = h / a.G;
-        float dec[2];
-        auto load_decay = [&](int c) {
+        float dec[2], ahead[2];      // of the next chunk and the one after
+        auto load_decay = [&](int c, float (&to)[2]) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int64_t i = t0 + static_cast<int64_t>(c) * kChunk + 2 * lane + e;
-            dec[e] = i < t1 ? decay_of(a, b + i, h) : 0.0f;
+            to[e] = i < t1 ? decay_of(a, b + i, h) : 0.0f;
           }
         };
-        load_decay(0);
-        double log_total = 0.0;
+        load_decay(0, dec);
+        load_decay(1, ahead);
+        Sum log_total{0.0f, 0.0f};
         for (int c = 0; c < chunks; ++c) {
           ok = wait(bar_free(st), (round & 1) ^ 1u, &s_abort);
           if (!ok) break;
           const int32_t row = static_cast<int32_t>(b + t0 + static_cast<int64_t>(c) * kChunk);
-          log_total += lay_decays(dec, s_g[st], s_eg[st], s_w[st], &s_tot[st]);
-          if (lane == 0) {
-            Step& w = s_step[st];
-            w.row = row;
-            w.live = static_cast<int>(min(static_cast<int64_t>(kChunk), t1 - t0 - static_cast<int64_t>(c) * kChunk));
-            w.hv = h;
-            w.flags = (c == 0 ? kFirst : 0) | (c + 1 == chunks ? kLast : 0);
-            w.in = in;
-            w.out = kLocal ? sg + 1 : sg + 1 == sgs ? out : -1;
-            w.part = (first_place(b) * a.Hv + h) * kPart;
-            w.seg = kLocal ? sg : sgs == 1 ? -1 : sg;
-            w.left = c + 1 == chunks ? exp2f(static_cast<float>(log_total)) : 0.0f;
-          }
-          __syncwarp();
           if (elect_one()) {
             const uint32_t bar = bar_full(st);
             tc::mbar_expect_tx(bar, (kLocal ? 2 : 3) * kTile);
@@ -237,7 +227,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           __syncwarp();
-          if (c + 1 < chunks) load_decay(c + 1);
+          log_total = join(log_total, lay_decays(dec, s_g[st], s_eg[st], s_w[st], &s_tot[st]));
+          if (lane == 0) {
+            Step& w = s_step[st];
+            w.row = row;
+            w.live = static_cast<int>(min(static_cast<int64_t>(kChunk), t1 - t0 - static_cast<int64_t>(c) * kChunk));
+            w.hv = h;
+            w.flags = (c == 0 ? kFirst : 0) | (c + 1 == chunks ? kLast : 0);
+            w.in = in;
+            w.out = kLocal ? sg + 1 : sg + 1 == sgs ? out : -1;
+            w.part = (first_place(b) * a.Hv + h) * kPart;
+            w.seg = kLocal ? sg : sgs == 1 ? -1 : sg;
+            w.left = exp2f(log_total.h + log_total.l);
+          }
+          warp_arrive(bar_full(st));
+          dec[0] = ahead[0], dec[1] = ahead[1];
+          load_decay(c + 2, ahead);
           turn();
         }
       }
@@ -245,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && wait(bar_free(st), (round & 1) ^ 1u, &s_abort)) {
       if (lane == 0) {
         s_step[st].flags = kEnd;
+        tc::mbar_arrive(bar_full(st));
         tc::mbar_arrive(bar_full(st));
       }
       __syncwarp();
@@ -353,6 +359,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      {
+        // ---- the decayed values of half of the chunk's tokens, in three parts (their
+        // columns are free: U of the chunk before is in S)
+        const int live = w.live - half * 32;
+        // Behind the sequence's end lies another, or anything: zeros, a warp's own 32
+        // channels of V and of K (eight 16-byte pieces a row).
+        for (int row = max(live, 0) + (lane >> 3); row < 32; row += 4) {
+          const uint32_t logical = ((warp & 1) * 4 + (lane & 3)) ^ (row & 7);
+          const uint32_t to = ((lane & 4) ? tile_k(st) : tile_v(st)) + ((warp & 2) ? kHalf : 0) + (half * 32 + row) * 128 + logical * 16;
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
+        }
+        __syncwarp();
+        // a row's place of the thread's channel: its piece by the row's number within eight
+        const uint32_t v = tile_v(st) + (dv >> 6) * kHalf + half * 4096 + ((dv & 63) >> 3) * 16 + (dv & 7) * 2;
+        // rolled: the kinds of warps share the instruction cache
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          uint32_t hi[4], mid[4], lo[4];
+          const float4 w0 = *reinterpret_cast<const float4*>(&s_w[st][half * 32 + i * 8]);
+          const float4 w1 = *reinterpret_cast<const float4*>(&s_w[st][half * 32 + i * 8 + 4]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint16_t v0, v1;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v0) : "r"(((v + i * 1024) ^ (2 * e << 4)) + 2 * e * 128));
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v1) : "r"(((v + i * 1024) ^ ((2 * e + 1) << 4)) + (2 * e + 1) * 128));
+            const float4 w4 = e < 2 ? w0 : w1;
+            float x = bf16_bits_to_float(v0) * (e & 1 ? w4.z : w4.x), y = bf16_bits_to_float(v1) * (e & 1 ? w4.w : w4.y);
+            hi[e] = split_bf16(x, y);
+            mid[e] = split_bf16(x, y);
+            lo[e] = pack_bf16(x, y);
+          }
+          const uint32_t to = t_lane + kColV + half * 16 + i * 4;
+          tmem_st4(to, hi);
+          tmem_st4(to + 32, mid);
+          tmem_st4(to + 64, lo);
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        tc::fence_proxy_async();
+        warp_arrive(bar_v);
+      }
       if constexpr (!kLocal) {
         if (g > 0 && !wait(bar_o, (g - 1) & 1, &s_abort)) break;   // the parts were read
         tc::tc_fence_after();
@@ -401,92 +448,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (++st == kStages) st = 0, ++round;
     }
   } else if (warp < kStateWarps + 4) {
-    // ==================== decayed values, and outputs ======================
-    const int dv = (warp & 3) * 32 + lane;
-    uint32_t swizzled[8];      // place of the thread's channel in a row, by the row's number within eight
-#pragma unroll
-    for (int r = 0; r < 8; ++r) swizzled[r] = r * 128 + ((((dv & 63) >> 3) ^ r) << 4);
-    int st = 0, before = 0;
-    uint32_t round = 0;
-    for (uint32_t g = 0;; ++g) {
-      if (!wait(bar_full(st), round & 1, &s_abort)) break;
-      const bool end = s_step[st].flags & kEnd;
-      if (!end) {
-        const int live = s_step[st].live;
-        // Behind the sequence's end lies another, or anything: zeros, a warp's own 32
-        // channels of V and of K (eight 16-byte pieces a row).
-        for (int row = live + (lane >> 3); row < kChunk; row += 4) {
-          const uint32_t logical = ((warp & 1) * 4 + (lane & 3)) ^ (row & 7);
-          const uint32_t to = ((lane & 4) ? tile_k(st) : tile_v(st)) + ((warp & 2) ? kHalf : 0) + row * 128 + logical * 16;
-          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
-        }
-        __syncwarp();
-        if (g > 0 && !wait(bar_u, (g - 1) & 1, &s_abort)) break;   // the parts were read
+    // ============================ outputs =================================
+    if constexpr (!kLocal) {
+      const int dv = (warp & 3) * 32 + lane;
+      int st = 0;
+      uint32_t round = 0;
+      for (uint32_t g = 0;; ++g) {
+        if (!wait(bar_full(st), round & 1, &s_abort) || (s_step[st].flags & kEnd)) break;
+        const Step& w = s_step[st];
+        uint16_t* dst = a.out + w.row * a.ldo_t + w.hv * a.ldo_h + dv;
+        const int live = w.live;
+        if (!wait(bar_o, g & 1, &s_abort)) break;
         tc::tc_fence_after();
-        const uint32_t v = tile_v(st) + (dv >> 6) * kHalf + (dv & 7) * 2;
         // rolled: the kinds of warps share the instruction cache
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
-          uint32_t hi[8], mid[8], lo[8];
-          float4 wj[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) wj[e] = *reinterpret_cast<const float4*>(&s_w[st][i * 16 + e * 4]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            uint16_t v0, v1;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v0) : "r"(v + i * 2048 + (e >> 2) * 1024 + swizzled[2 * e & 7]));
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v1) : "r"(v + i * 2048 + (e >> 2) * 1024 + swizzled[(2 * e & 7) + 1]));
-            const float4 w4 = wj[e >> 1];
-            float x = bf16_bits_to_float(v0) * (e & 1 ? w4.z : w4.x), y = bf16_bits_to_float(v1) * (e & 1 ? w4.w : w4.y);
-            hi[e] = split_bf16(x, y);
-            mid[e] = split_bf16(x, y);
-            lo[e] = pack_bf16(x, y);
+          uint32_t o1[16], o2[16];
+          tc::tmem_ld16(t_lane + kColO1 + i * 16, o1);
+          tc::tmem_ld16(t_lane + kColO2 + i * 16, o2);
+          tc::tmem_wait_ld();
+          if (i == 3) {
+            tc::tc_fence_before();
+            warp_arrive(bar_ofree);
           }
-          tmem_st8(t_lane + kColV + i * 8, hi);
-          tmem_st8(t_lane + kColV + 32 + i * 8, mid);
-          tmem_st8(t_lane + kColV + 64 + i * 8, lo);
-        }
-        tc::tmem_wait_st();
-        tc::tc_fence_before();
-        tc::fence_proxy_async();
-        warp_arrive(bar_v);
-        if constexpr (kLocal) warp_arrive(bar_free(st));
-      }
-      if constexpr (!kLocal) {
-        if (g > 0) {   // the outputs of the chunk before
-          const Step& w = s_step[before];
-          if (!wait(bar_o, (g - 1) & 1, &s_abort)) break;
-          tc::tc_fence_after();
-          uint16_t* dst = a.out + w.row * a.ldo_t + w.hv * a.ldo_h + dv;
-          const int live = w.live;
-#pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            uint32_t o1[16], o2[16];
-            tc::tmem_ld16(t_lane + kColO1 + i * 16, o1);
-            tc::tmem_ld16(t_lane + kColO2 + i * 16, o2);
-            tc::tmem_wait_ld();
-            if (i == 3) {
-              tc::tc_fence_before();
-              warp_arrive(bar_ofree);
-            }
-            const int here = live - i * 16;
+          const int here = live - i * 16;
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const float2 eg = *reinterpret_cast<const float2*>(&s_eg[before][i * 16 + e]);
-              const uint32_t y = pack_bf16(fmaf(eg.x, __uint_as_float(o1[e]), __uint_as_float(o2[e])) * a.scale,
-                                           fmaf(eg.y, __uint_as_float(o1[e + 1]), __uint_as_float(o2[e + 1])) * a.scale);
-              if (e < here) *dst = static_cast<uint16_t>(y);
-              dst += a.ldo_t;
-              if (e + 1 < here) *dst = static_cast<uint16_t>(y >> 16);
-              dst += a.ldo_t;
-            }
+          for (int e = 0; e < 16; e += 2) {
+            const float2 eg = *reinterpret_cast<const float2*>(&s_eg[st][i * 16 + e]);
+            const uint32_t y = pack_bf16(fmaf(eg.x, __uint_as_float(o1[e]), __uint_as_float(o2[e])) * a.scale,
+                                         fmaf(eg.y, __uint_as_float(o1[e + 1]), __uint_as_float(o2[e + 1])) * a.scale);
+            if (e < here) *dst = static_cast<uint16_t>(y);
+            dst += a.ldo_t;
+            if (e + 1 < here) *dst = static_cast<uint16_t>(y >> 16);
+            dst += a.ldo_t;
           }
-          warp_arrive(bar_free(before));
         }
+        warp_arrive(bar_free(st));
+        if (++st == kStages) st = 0, ++round;
       }
-      if (end) break;
-      before = st;
-      if (++st == kStages) st = 0, ++round;
     }
   } else if constexpr (!kLocal) {
     // ============================ scores ==================================

@@ -19,7 +19,6 @@ constexpr int kSegChunks = 8;         // chunks of a segment at least
 constexpr int kMaxSegments = 24;
 constexpr int kSms = 152;             // that segments are cut for, whatever the device has
 constexpr float kMinDecay = -16384.0f;   // e^x = 0 from far above it; sums of 64 stay finite
-constexpr double kLog2e = 1.4426950408889634074;
 
 // The segments of a long sequence: those with which its heads fill the SMs in the
 // fewest turns for what each then has to do, kMaxSegments at most (a segment reads
@@ -98,28 +97,44 @@ __device__ __forceinline__ float ex2(float x) {   // to about 2^-22
   return y;
 }
 
+// A sum of binary32 numbers as the rounded sum and what is missing of it.
+struct Sum {
+  float h, l;
+};
+__device__ __forceinline__ Sum join(Sum a, Sum b) {
+  const float s = __fadd_rn(a.h, b.h), t = __fsub_rn(s, a.h);
+  const float e = __fadd_rn(__fsub_rn(a.h, __fsub_rn(s, t)), __fsub_rn(b.h, t));
+  return Sum{s, __fadd_rn(e, __fadd_rn(a.l, b.l))};
+}
+
 // The decays of a chunk's 64 tokens, two a lane (0 past the end), summed up:
 // in powers of two up to each token (in two parts), and the factors that these
 // are, that the chunk's end has left of each token, and of the whole chunk.
-// Returns the chunk's sum.
-__device__ __forceinline__ double lay_decays(const float (&dec)[2], float2* g2, float* eg, float* w, float* tot) {
+// Returns the chunk's sum.  (Sums in binary64 took the warp some 2000 cycles.)
+__device__ __forceinline__ Sum lay_decays(const float (&dec)[2], float2* g2, float* eg, float* w, float* tot) {
+  constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596299e-8f;
   const int lane = threadIdx.x & 31;
-  const double d0 = dec[0] * kLog2e, d1 = dec[1] * kLog2e;
-  double sum = d0 + d1;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double v = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += v;
-  }
-  const double total = __shfl_sync(0xffffffffu, sum, 31), g[2] = {sum - d1, sum};
+  Sum d[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const float hi = static_cast<float>(g[e]);
-    g2[2 * lane + e] = make_float2(hi, static_cast<float>(g[e] - hi));
-    eg[2 * lane + e] = exp2f(hi);
-    w[2 * lane + e] = exp2f(static_cast<float>(total - g[e]));
+    d[e].h = __fmul_rn(dec[e], kLog2e);
+    d[e].l = fmaf(dec[e], kLog2eLow, fmaf(dec[e], kLog2e, -d[e].h));
   }
-  if (lane == 0) *tot = exp2f(static_cast<float>(total));
+  Sum sum = join(d[0], d[1]);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Sum v{__shfl_up_sync(0xffffffffu, sum.h, o), __shfl_up_sync(0xffffffffu, sum.l, o)};
+    if (lane >= o) sum = join(sum, v);
+  }
+  const Sum total{__shfl_sync(0xffffffffu, sum.h, 31), __shfl_sync(0xffffffffu, sum.l, 31)};
+  const Sum g[2] = {join(sum, Sum{-d[1].h, -d[1].l}), sum};
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    g2[2 * lane + e] = make_float2(g[e].h, g[e].l);
+    eg[2 * lane + e] = exp2f(__fadd_rn(g[e].h, g[e].l));
+    w[2 * lane + e] = exp2f(__fadd_rn(__fsub_rn(total.h, g[e].h), __fsub_rn(total.l, g[e].l)));
+  }
+  if (lane == 0) *tot = exp2f(__fadd_rn(total.h, total.l));
   return total;
 }
 
