@@ -174,8 +174,8 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
   using L = Tile<DK, DV>;
   constexpr int kWarps = L::kWarps, kThreads = L::kThreads, NT = DK / 8;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 s_g[2][kChunk];              // decays summed up to a token, in powers of two, in two parts
-  __shared__ float s_eg[2][kChunk], s_w[2][kChunk], s_tot[2];   // those of G_i, G_C - G_i and G_C
+  __shared__ __align__(8) float s_gh[2][kChunk], s_gl[2][kChunk];   // decays summed up to a token, in powers of two, in two parts
+  __shared__ __align__(8) float s_eg[2][kChunk], s_w[2][kChunk], s_tot[2];   // those of G_i, G_C - G_i and G_C
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, lr = lane >> 2, lc = lane & 3;
   const int hv = blockIdx.y, hk = hv / a.G;
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
   };
   Sum log_total{0.0f, 0.0f};  // of the segment so far (warp 0)
   auto lay_decay = [&](int c) {
-    log_total = join(log_total, lay_decays(dec, s_g[c & 1], s_eg[c & 1], s_w[c & 1], &s_tot[c & 1]));
+    log_total = join(log_total, lay_decays(dec, s_gh[c & 1], s_gl[c & 1], s_eg[c & 1], s_w[c & 1], &s_tot[c & 1]));
   };
 
   copy(0);
@@ -324,19 +324,16 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = m0 + lr + 8 * e;
-        const float2 gi = s_g[c & 1][i];
+        const float2 gi = make_float2(s_gh[c & 1][i], s_gl[c & 1][i]);
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
           const int j = n0 + n * 8 + 2 * lc;
-          float y[2];
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const float2 gj = s_g[c & 1][j + f];
-            y[f] = j + f <= i ? x[n][2 * e + f] * ex2((gi.x - gj.x) + (gi.y - gj.y)) : 0.0f;
-          }
+          const float2 gh = *reinterpret_cast<const float2*>(&s_gh[c & 1][j]), gl = *reinterpret_cast<const float2*>(&s_gl[c & 1][j]);
+          float2 y = make_float2(j <= i ? x[n][2 * e] * ex2((gi.x - gh.x) + (gi.y - gl.x)) : 0.0f,
+                                 j + 1 <= i ? x[n][2 * e + 1] * ex2((gi.x - gh.y) + (gi.y - gl.y)) : 0.0f);
           if (j > m0 + 15) continue;
           const uint32_t at_p = score_place(i, j >> 3) + (j & 7) * 2;
-          const uint32_t hi = split_bf16(y[0], y[1]), lo = pack_bf16(y[0], y[1]);
+          const uint32_t hi = split_bf16(y), lo = pack_bf16(y.x, y.y);
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_hi + at_p), "r"(hi) : "memory");
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(p_lo + at_p), "r"(lo) : "memory");
         }
@@ -369,9 +366,9 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float lo = st[2 * kk + k][2 * n], hi = st[2 * kk + k][2 * n + 1];
-            bh[n][k] = split_bf16(lo, hi);
-            bl[n][k] = pack_bf16(lo, hi);
+            float2 v = make_float2(st[2 * kk + k][2 * n], st[2 * kk + k][2 * n + 1]);
+            bh[n][k] = split_bf16(v);
+            bl[n][k] = pack_bf16(v.x, v.y);
           }
 #pragma unroll
         for (int m = 0; m < kChunk / 16; ++m) {
@@ -426,10 +423,10 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int j = kk * 16 + 2 * lc + 8 * (i >> 1);   // tokens of the operand's register
-        float lo = bf16_lo(vf[kk][i]) * s_w[c & 1][j], hi = bf16_hi(vf[kk][i]) * s_w[c & 1][j + 1];
-        va[0][i] = split_bf16(lo, hi);
-        va[1][i] = split_bf16(lo, hi);
-        va[2][i] = pack_bf16(lo, hi);
+        float2 v = mul2(make_float2(bf16_lo(vf[kk][i]), bf16_hi(vf[kk][i])), *reinterpret_cast<const float2*>(&s_w[c & 1][j]));
+        va[0][i] = split_bf16(v);
+        va[1][i] = split_bf16(v);
+        va[2][i] = pack_bf16(v.x, v.y);
       }
 #pragma unroll
       for (int t = 0; t < NT; t += 2) {

@@ -7,11 +7,11 @@
 //   O1 = S^T Q^T        128 channels of v by 64 tokens, S in two bf16 parts   2 * 8
 //   O2 = V^T (w A)^T    the same shape, the scores in two parts               2 * 4
 //   U  = (w V)^T K      128 by 128, V's decayed values in three parts         3 * 4
-// and out = scale * (e^G O1 + O2)^T, S = e^{G_C} S + U^T.  S^T and (w V)^T are
-// operands in tensor memory, formed by the warps that have the values; Q, K and V
-// are read as they lie, by tensor copies in the 128-byte-swizzled layout (K-major
-// for Q and K; for K in U and V in O2 along the tokens, the operand's other
-// major), and w A lies in shared memory beside them.  S stays in the registers of
+// and out = scale * (e^G O1 + O2)^T, S = e^{G_C} S + U^T.  S^T is an operand in
+// tensor memory, formed by the warps that have it; Q, K and V are read as they lie,
+// by tensor copies in the 128-byte-swizzled layout (K-major for Q and K; for K in U
+// and V in O2 along the tokens, the operand's other major); w A and (w V)^T lie in
+// shared memory beside them.  S stays in the registers of
 // eight warps (lane v channel, 64 key channels a thread) from a sequence's first
 // chunk to its last: U is formed from zero for each chunk, its small parts first,
 // and added to S rounded to nearest, since the tensor cores' additions cut off.
@@ -20,11 +20,10 @@
 // on by mbarriers:
 //   producer (1)   finds items, copies Q, K and V of chunks ahead into three stages,
 //                  with the chunk's decays and what is to be done
-//   issuer (1)     A, U, O1, O2 of a chunk
-//   state (8)      the decayed values' three parts, S's two parts; S after the chunk
-//   scores (4)     w A
-//   outputs (4)
-// A's columns are O2's: A of the next chunk waits for the outputs.
+//   issuer (1)     U, O1, O2 of a chunk, A of the next
+//   state (8)      S's two parts; S after the chunk
+//   values (4)     the decayed values' three parts; the outputs of the chunk before
+//   scores (2)     w A, its weights ready before A is
 //
 // Every wait on an mbarrier is bounded: after 2 s (prism_debug_wait_expiry
 // shortens that for tests) the kernel sets the device status bit; every warp leaves
@@ -49,14 +48,16 @@ using namespace lin;
 constexpr unsigned long long kDrainNs = 2000000000ull;
 constexpr int D = 128;
 constexpr int kStages = 3;
-constexpr int kStateWarps = 8, kIssuer = 14, kProducer = 15, kWarps = 18;   // outputs 8 .. 11; scores 12, 13, 16, 17
+constexpr int kStateWarps = 8, kIssuer = 14, kProducer = 15, kWarps = 16;   // values and outputs 8 .. 11; scores 12, 13
 constexpr int kThreads = kWarps * 32, kStateThreads = kStateWarps * 32;
 constexpr int kTile = kChunk * D * 2, kHalf = kTile / 2;     // of q, k or v: halves of 64 channels
 constexpr int kScores = kChunk * kChunk * 2;
-constexpr int kSmem = kStages * 3 * kTile + 2 * kScores + 1024;
+constexpr int kTurn = 32 * 32 * 2;                           // a warp's turn of outputs
+constexpr int kSmem = kStages * 3 * kTile + 2 * kScores + 3 * kTile + 4 * kTurn + 1024;
+constexpr int kAhead = 4;                                    // chunks whose decays are held, three on their way
 constexpr int kPart = D * D + 4;                             // floats of a segment's state in the workspace
 // columns of tensor memory
-constexpr uint32_t kColU = 0, kColS = 128, kColV = 256, kColO1 = 352, kColO2 = 416;
+constexpr uint32_t kColU = 0, kColS = 128, kColA = 256, kColO1 = 320, kColO2 = 384;
 
 enum { kFirst = 1, kLast = 2, kEnd = 4 };
 struct Step {          // a chunk's work
@@ -80,8 +81,9 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
   return one != 0;
 }
-__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]));
+__device__ __forceinline__ void store_matrices(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
@@ -97,6 +99,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+__device__ __forceinline__ void copy_4(uint32_t dst, const float* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 // A tile of rows of 64 channels, 128-byte swizzled, as an operand whose rows are
 // the contraction's: 64 channels in 128 bytes, eight rows to 1024, the other 64
@@ -115,10 +120,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     linear_tc_chunk_kernel(const __grid_constant__ LinAttnArgs a, const __grid_constant__ Maps maps, int max_segs) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Step s_step[kStages];
-  __shared__ float2 s_g[kStages][kChunk];
-  __shared__ __align__(16) float s_eg[kStages][kChunk], s_w[kStages][kChunk];
+  __shared__ __align__(16) float s_gh[kStages][kChunk], s_gl[kStages][kChunk], s_eg[kStages][kChunk], s_w[kStages][kChunk];
+  __shared__ __align__(8) float s_dec[kAhead][kChunk];
   __shared__ float s_tot[kStages];
-  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 9];
+  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 11];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -128,22 +133,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tile_k = [&](int st) { return base + st * 3 * kTile + kTile; };
   auto tile_v = [&](int st) { return base + st * 3 * kTile + 2 * kTile; };
   const uint32_t scores = base + kStages * 3 * kTile;       // high parts, then low ones
+  // the decayed values, [128 channels][64 tokens] a part; kLocal: two of them in turn, the
+  // second where Q would lie
+  auto values = [&](uint32_t g, int part) { return kLocal && (g & 1) ? tile_q(part) : scores + 2 * kScores + part * kTile; };
   const uint32_t bars = smem_u32(s_bar);
   auto bar_full = [&](int st) { return bars + 8 * st; };
   auto bar_free = [&](int st) { return bars + 8 * (kStages + st); };
-  const uint32_t bar_a = bars + 16 * kStages, bar_p = bar_a + 8, bar_v = bar_a + 16, bar_u = bar_a + 24, bar_ufree = bar_a + 32,
-                 bar_s = bar_a + 40, bar_o = bar_a + 48, bar_ofree = bar_a + 56, bar_end = bar_a + 64;
+  const uint32_t bar_a = bars + 16 * kStages, bar_p = bar_a + 8, bar_v = bar_a + 16, bar_ufree = bar_a + 24,
+                 bar_s = bar_a + 32, bar_q = bar_a + 40, bar_o = bar_a + 48, bar_ofree = bar_a + 56, bar_end = bar_a + 64;
+  // two in turn: kLocal, the values of chunk g wait for U of chunk g - 2 when that of g - 1 may be formed
+  auto bar_u = [&](uint32_t g) { return bar_a + 72 + 8 * (g & 1); };
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(bar_full(i), 2);   // the copies, and what the producer writes itself
-      tc::mbar_init(bar_free(i), kLocal ? 1 + kStateWarps : 1 + kStateWarps + 4 + 4);
+      tc::mbar_init(bar_free(i), kLocal ? 1 + kStateWarps + 4 : 1 + kStateWarps + 4 + 2);
     }
     tc::mbar_init(bar_a, 1);
-    tc::mbar_init(bar_p, 4);
-    tc::mbar_init(bar_v, kStateWarps);
-    tc::mbar_init(bar_u, 1);
+    tc::mbar_init(bar_p, 2);
+    tc::mbar_init(bar_v, 4);
+    tc::mbar_init(bar_u(0), 1);
+    tc::mbar_init(bar_u(1), 1);
     tc::mbar_init(bar_ufree, kStateWarps);
     tc::mbar_init(bar_s, kStateWarps);
+    tc::mbar_init(bar_q, 1);
     tc::mbar_init(bar_o, 1);
     tc::mbar_init(bar_ofree, 4);
     tc::mbar_init(bar_end, 1);
@@ -154,6 +166,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // the scores of tokens 0 .. 31 with tokens 32 .. 63 are 0 for good
+  if (!kLocal && warp == 12)
+    for (int p = 4; p < 8; ++p)
+      for (int part = 0; part < 2; ++part)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(scores + part * kScores + lane * 128 + ((p ^ (lane & 7)) << 4)), "r"(0)
+                     : "memory");
+  tc::fence_proxy_async();
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -201,16 +220,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int sgs = __shfl_sync(0xffffffffu, segs, from);
         const int64_t t0 = sg * chunks_each * kChunk, t1 = min(n, t0 + chunks_each * kChunk);
         const int chunks = static_cast<int>((t1 - t0 + kChunk - 1) / kChunk), hk = h / a.G;
-        float dec[2], ahead[2];      // of the next chunk and the one after
-        auto load_decay = [&](int c, float (&to)[2]) {
+        // decays by way of shared memory, three chunks ahead
+        auto copy_decays = [&](int c) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int64_t i = t0 + static_cast<int64_t>(c) * kChunk + 2 * lane + e;
-            to[e] = i < t1 ? decay_of(a, b + i, h) : 0.0f;
+            const bool there = c < chunks && i < t1;
+            copy_4(smem_u32(&s_dec[c & (kAhead - 1)][2 * lane + e]), a.decay + (there ? (b + i) * a.ldd_t : 0) + h, there ? 4 : 0);
           }
+          cp_async_commit();
         };
-        load_decay(0, dec);
-        load_decay(1, ahead);
+        cp_async_wait<0>();        // the copies of the item before
+        if (lane == 0 && in >= 0 && (kLocal ? sg == 0 : sgs == 1))
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.state + (in * a.Hv + h) * (D * D)), "r"(D * D * 4) : "memory");
+        for (int c = 0; c < kAhead - 1; ++c) copy_decays(c);
         Sum log_total{0.0f, 0.0f};
         for (int c = 0; c < chunks; ++c) {
           ok = wait(bar_free(st), (round & 1) ^ 1u, &s_abort);
@@ -227,7 +250,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           __syncwarp();
-          log_total = join(log_total, lay_decays(dec, s_g[st], s_eg[st], s_w[st], &s_tot[st]));
+          copy_decays(c + kAhead - 1);
+          cp_async_wait<kAhead - 1>();
+          const float2 g2 = *reinterpret_cast<const float2*>(&s_dec[c & (kAhead - 1)][2 * lane]);
+          const float dec[2] = {bounded_decay(g2.x), bounded_decay(g2.y)};
+          log_total = join(log_total, lay_decays(dec, s_gh[st], s_gl[st], s_eg[st], s_w[st], &s_tot[st]));
           if (lane == 0) {
             Step& w = s_step[st];
             w.row = row;
@@ -241,8 +268,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             w.left = exp2f(log_total.h + log_total.l);
           }
           warp_arrive(bar_full(st));
-          dec[0] = ahead[0], dec[1] = ahead[1];
-          load_decay(c + 2, ahead);
           turn();
         }
       }
@@ -262,37 +287,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool lead = elect_one();
     int st = 0;
     uint32_t round = 0;
-    for (uint32_t g = 0;; ++g) {
-      if (!wait(bar_full(st), round & 1, &s_abort) || (s_step[st].flags & kEnd)) break;
-      if constexpr (!kLocal) {
-        if (g > 0 && !wait(bar_ofree, (g - 1) & 1, &s_abort)) break;
-        tc::tc_fence_after();
-        if (lead) {
-          const uint64_t qd = tc::smem_desc_sw128(tile_q(st)), kd = tc::smem_desc_sw128(tile_k(st));
+    bool more = wait(bar_full(0), 0, &s_abort) && !(s_step[0].flags & kEnd);
+    auto issue_scores = [&] {
+      if (lead) {
+        const uint64_t qd = tc::smem_desc_sw128(tile_q(st)), kd = tc::smem_desc_sw128(tile_k(st));
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)   // rows 64 .. of Q's tile are not its: those lanes are not read
-            tc::tc_mma(tmem + kColO2, qd + (k >> 2) * (kHalf >> 4) + 2 * (k & 3), kd + (k >> 2) * (kHalf >> 4) + 2 * (k & 3),
-                       idesc(kChunk, false, false), k != 0 ? 1u : 0u);
-          tc::tc_commit(bar_a);
-        }
-        __syncwarp();
+        for (int k = 0; k < D / 16; ++k)   // rows 64 .. of Q's tile are not its: those lanes are not read
+          tc::tc_mma(tmem + kColA, qd + (k >> 2) * (kHalf >> 4) + 2 * (k & 3), kd + (k >> 2) * (kHalf >> 4) + 2 * (k & 3),
+                     idesc(kChunk, false, false), k != 0 ? 1u : 0u);
+        tc::tc_commit(bar_a);
       }
+      __syncwarp();
+    };
+    if (!kLocal && more) issue_scores();
+    for (uint32_t g = 0; more; ++g) {
       if (!wait(bar_v, g & 1, &s_abort)) break;
       if (g > 0 && !wait(bar_ufree, (g - 1) & 1, &s_abort)) break;
       tc::tc_fence_after();
       if (lead) {
         const uint64_t kd = desc_along_rows(tile_k(st));
 #pragma unroll
-        for (int part = 2; part >= 0; --part)   // the small parts first
+        for (int part = 2; part >= 0; --part) {   // the small parts first
+          const uint64_t vd = tc::smem_desc_sw128(values(g, part));
 #pragma unroll
           for (int k = 0; k < kChunk / 16; ++k)
-            tc::tc_mma_ta(tmem + kColU, tmem + kColV + part * 32 + k * 8, kd + k * (16 * 128 >> 4), idesc(D, false, true),
-                          part != 2 || k != 0 ? 1u : 0u);
-        if (g != 0 || *static_cast<volatile int*>(&g_lin_withhold) == 0) tc::tc_commit(bar_u);
+            tc::tc_mma(tmem + kColU, vd + 2 * k, kd + k * (16 * 128 >> 4), idesc(D, false, true), part != 2 || k != 0 ? 1u : 0u);
+        }
+        if (g != 0 || *static_cast<volatile int*>(&g_lin_withhold) == 0) tc::tc_commit(bar_u(g));
       }
       __syncwarp();
       if constexpr (!kLocal) {
         if (!wait(bar_s, g & 1, &s_abort)) break;
+        if (g > 0 && !wait(bar_ofree, (g - 1) & 1, &s_abort)) break;
         tc::tc_fence_after();
         if (lead) {
           const uint64_t qd = tc::smem_desc_sw128(tile_q(st));
@@ -302,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < D / 16; ++k)
               tc::tc_mma_ta(tmem + kColO1, tmem + kColS + part * 64 + k * 8, qd + (k >> 2) * (kHalf >> 4) + 2 * (k & 3),
                             idesc(kChunk, false, false), part != 1 || k != 0 ? 1u : 0u);
+          tc::tc_commit(bar_q);
         }
         __syncwarp();
         if (!wait(bar_p, g & 1, &s_abort)) break;
@@ -321,11 +348,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lead) tc::tc_commit(bar_free(st));
       __syncwarp();
       if (++st == kStages) st = 0, ++round;
+      more = wait(bar_full(st), round & 1, &s_abort) && !(s_step[st].flags & kEnd);
+      if (!kLocal && more) issue_scores();   // A was read: w A of this chunk was waited for
     }
   } else if (warp < kStateWarps) {
     // ============================ state ===================================
     const int half = warp >> 2, dv = (warp & 3) * 32 + lane;
-    float S[64];
+    float2 S[32];      // key channels 64 half + 2 i, + 1
     int st = 0;
     uint32_t round = 0;
     for (uint32_t g = 0;; ++g) {
@@ -335,82 +364,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (flags & kEnd) break;
       if (flags & kFirst) {
         const float* src = a.state + (w.in * a.Hv + w.hv) * (D * D) + half * 64 * D + dv;
-        const float* part = a.ws + w.part + tid;
         const int64_t part_step = static_cast<int64_t>(a.Hv) * kPart;
         const bool slot = w.in >= 0 && (kLocal ? w.seg == 0 : w.seg < 0);
 #pragma unroll
-        for (int i = 0; i < 64; ++i) S[i] = slot ? src[i * D] : 0.0f;
+        for (int i = 0; i < 32; ++i) S[i] = slot ? make_float2(src[2 * i * D], src[(2 * i + 1) * D]) : make_float2(0.0f, 0.0f);
         if constexpr (kLocal) {
           // the sequence's start has a place of its own: the last segment may write
           // the state back before another begins
           if (w.seg == 0) {
-            float* ps = a.ws + w.part;
+            float2* ps = reinterpret_cast<float2*>(a.ws + w.part) + tid;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) {
-              ps[i * kStateThreads + tid] = S[i];
-              S[i] = 0.0f;
+            for (int i = 0; i < 32; ++i) {
+              ps[i * kStateThreads] = S[i];
+              S[i] = make_float2(0.0f, 0.0f);
             }
           }
         } else {
           for (int k = 0; k <= w.seg; ++k) {
-            const float left = k == 0 ? 0.0f : a.ws[w.part + k * part_step + D * D];
+            const float* ps = a.ws + w.part + k * part_step;
+            const float left = k == 0 ? 0.0f : ps[D * D];
+            const float2* from = reinterpret_cast<const float2*>(ps) + tid;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) S[i] = fmaf(left, S[i], part[k * part_step + i * kStateThreads]);
+            for (int i = 0; i < 32; ++i) S[i] = fma2(make_float2(left, left), S[i], from[i * kStateThreads]);
           }
         }
-      }
-      {
-        // ---- the decayed values of half of the chunk's tokens, in three parts (their
-        // columns are free: U of the chunk before is in S)
-        const int live = w.live - half * 32;
-        // Behind the sequence's end lies another, or anything: zeros, a warp's own 32
-        // channels of V and of K (eight 16-byte pieces a row).
-        for (int row = max(live, 0) + (lane >> 3); row < 32; row += 4) {
-          const uint32_t logical = ((warp & 1) * 4 + (lane & 3)) ^ (row & 7);
-          const uint32_t to = ((lane & 4) ? tile_k(st) : tile_v(st)) + ((warp & 2) ? kHalf : 0) + (half * 32 + row) * 128 + logical * 16;
-          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
-        }
-        __syncwarp();
-        // a row's place of the thread's channel: its piece by the row's number within eight
-        const uint32_t v = tile_v(st) + (dv >> 6) * kHalf + half * 4096 + ((dv & 63) >> 3) * 16 + (dv & 7) * 2;
-        // rolled: the kinds of warps share the instruction cache
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          uint32_t hi[4], mid[4], lo[4];
-          const float4 w0 = *reinterpret_cast<const float4*>(&s_w[st][half * 32 + i * 8]);
-          const float4 w1 = *reinterpret_cast<const float4*>(&s_w[st][half * 32 + i * 8 + 4]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint16_t v0, v1;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v0) : "r"(((v + i * 1024) ^ (2 * e << 4)) + 2 * e * 128));
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v1) : "r"(((v + i * 1024) ^ ((2 * e + 1) << 4)) + (2 * e + 1) * 128));
-            const float4 w4 = e < 2 ? w0 : w1;
-            float x = bf16_bits_to_float(v0) * (e & 1 ? w4.z : w4.x), y = bf16_bits_to_float(v1) * (e & 1 ? w4.w : w4.y);
-            hi[e] = split_bf16(x, y);
-            mid[e] = split_bf16(x, y);
-            lo[e] = pack_bf16(x, y);
-          }
-          const uint32_t to = t_lane + kColV + half * 16 + i * 4;
-          tmem_st4(to, hi);
-          tmem_st4(to + 32, mid);
-          tmem_st4(to + 64, lo);
-        }
-        tc::tmem_wait_st();
-        tc::tc_fence_before();
-        tc::fence_proxy_async();
-        warp_arrive(bar_v);
       }
       if constexpr (!kLocal) {
-        if (g > 0 && !wait(bar_o, (g - 1) & 1, &s_abort)) break;   // the parts were read
+        if (g > 0 && !wait(bar_q, (g - 1) & 1, &s_abort)) break;   // the parts were read
         tc::tc_fence_after();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t hi[8], lo[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            float x = S[i * 16 + 2 * e], y = S[i * 16 + 2 * e + 1];
-            hi[e] = split_bf16(x, y);
-            lo[e] = pack_bf16(x, y);
+            float2 x = S[i * 8 + e];
+            hi[e] = split_bf16(x);
+            lo[e] = pack_bf16(x.x, x.y);
           }
           tmem_st8(t_lane + kColS + half * 32 + i * 8, hi);
           tmem_st8(t_lane + kColS + 64 + half * 32 + i * 8, lo);
@@ -420,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(bar_s);
       }
       const float tot = s_tot[st];
-      if (!wait(bar_u, g & 1, &s_abort)) break;
+      if (!wait(bar_u(g), (g >> 1) & 1, &s_abort)) break;
       tc::tc_fence_after();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {   // 16 at a time, by registers
@@ -428,7 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_ld16(t_lane + kColU + half * 64 + i * 16, u);
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) S[i * 16 + e] = fmaf(tot, S[i * 16 + e], __uint_as_float(u[e]));
+        for (int e = 0; e < 8; ++e)
+          S[i * 8 + e] = fma2(make_float2(tot, tot), S[i * 8 + e], make_float2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1])));
       }
       tc::tc_fence_before();
       warp_arrive(bar_ufree);
@@ -436,101 +426,186 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kLocal) {
           float* ps = a.ws + w.part + w.out * (static_cast<int64_t>(a.Hv) * kPart);
 #pragma unroll
-          for (int i = 0; i < 64; ++i) ps[i * kStateThreads + tid] = S[i];
+          for (int i = 0; i < 32; ++i) reinterpret_cast<float2*>(ps)[i * kStateThreads + tid] = S[i];
           if (tid == 0) ps[D * D] = w.left;
         } else if (w.out >= 0) {
           float* dst = a.state + (w.out * a.Hv + w.hv) * (D * D) + half * 64 * D + dv;
 #pragma unroll
-          for (int i = 0; i < 64; ++i) dst[i * D] = S[i];
+          for (int i = 0; i < 32; ++i) dst[2 * i * D] = S[i].x, dst[(2 * i + 1) * D] = S[i].y;
         }
       }
       warp_arrive(bar_free(st));
       if (++st == kStages) st = 0, ++round;
     }
   } else if (warp < kStateWarps + 4) {
-    // ============================ outputs =================================
-    if constexpr (!kLocal) {
-      const int dv = (warp & 3) * 32 + lane;
+    // ==================== decayed values, and outputs ======================
+    int st = 0, before = 0;
+    uint32_t round = 0;
+    for (uint32_t g = 0;; ++g) {
+      if (!wait(bar_full(st), round & 1, &s_abort)) break;
+      const bool end = s_step[st].flags & kEnd;
+      if (!end) {
+        // ---- 32 channels of v, in three parts, transposed
+        const int live = s_step[st].live;
+        const uint32_t half = (warp & 2) ? kHalf : 0, first = (warp & 1) * 4;   // of the row's pieces of 8 channels
+        // Behind the sequence's end lies another, or anything: zeros, a warp's own
+        // channels of V and as many of K.
+        for (int row = live + (lane >> 3); row < kChunk; row += 4) {
+          const uint32_t to = ((lane & 4) ? tile_k(st) : tile_v(st)) + half + row * 128 + (((first + (lane & 3)) ^ (row & 7)) << 4);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
+        }
+        __syncwarp();
+        // the parts were read: of the chunk before, or (kLocal) the one before that
+        constexpr uint32_t kBack = kLocal ? 2 : 1;
+        if (g >= kBack && !wait(bar_u(g - kBack), ((g - kBack) >> 1) & 1, &s_abort)) break;
+        float2 w[8];                                  // of the tokens 8 i + 2 c, + 1, c = lane % 4
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const float2*>(&s_w[st][i * 8 + (lane & 3) * 2]);
+        const int r8 = lane & 7;
+#pragma unroll 1
+        for (int p = 0; p < 4; ++p) {
+          const uint32_t from = tile_v(st) + half + lane * 128 + (((first + p) ^ r8) << 4);   // token 32 t + lane
+          const int row = (warp & 3) * 32 + p * 8 + r8;                                     // channel, for the parts' addresses
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            uint32_t x[4], hi[4], mid[4], lo[4];
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                         : "r"(from + t * 4096)
+                         : "memory");
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float2 y = mul2(make_float2(bf16_lo(x[i]), bf16_hi(x[i])), w[t * 4 + i]);
+              hi[i] = split_bf16(y);
+              mid[i] = split_bf16(y);
+              lo[i] = pack_bf16(y.x, y.y);
+            }
+            const uint32_t to = row * 128 + (((t * 4 + (lane >> 3)) ^ (row & 7)) << 4);
+            store_matrices(values(g, 0) + to, hi);
+            store_matrices(values(g, 1) + to, mid);
+            store_matrices(values(g, 2) + to, lo);
+          }
+        }
+        tc::fence_proxy_async();
+        warp_arrive(bar_v);
+        if constexpr (kLocal) warp_arrive(bar_free(st));
+      }
+      if constexpr (!kLocal) {
+        if (g > 0) {   // ---- the outputs of the chunk before
+          const Step& w = s_step[before];
+          if (!wait(bar_o, (g - 1) & 1, &s_abort)) break;
+          tc::tc_fence_after();
+          uint32_t y[32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o1[16], o2[16];
+            tc::tmem_ld16(t_lane + kColO1 + i * 16, o1);
+            tc::tmem_ld16(t_lane + kColO2 + i * 16, o2);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float2 eg = *reinterpret_cast<const float2*>(&s_eg[before][i * 16 + e]);
+              const float2 o = mul2(fma2(eg, make_float2(__uint_as_float(o1[e]), __uint_as_float(o1[e + 1])),
+                                         make_float2(__uint_as_float(o2[e]), __uint_as_float(o2[e + 1]))),
+                                    make_float2(a.scale, a.scale));
+              y[i * 8 + e / 2] = pack_bf16(o.x, o.y);
+            }
+          }
+          tc::tc_fence_before();
+          warp_arrive(bar_ofree);
+          // through the warp's own shared memory, 32 tokens at a time: 64 bytes of a token side by side
+          const uint32_t turn = scores + 2 * kScores + 3 * kTile + (warp & 3) * kTurn;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t * 32 >= w.live) break;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(turn + e * 64 + lane * 2),
+                           "h"(static_cast<uint16_t>(y[t * 16 + e / 2] >> (16 * (e & 1))))
+                           : "memory");
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int token = t * 32 + k * 8 + (lane >> 2);
+              uint4 v;
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                           : "r"(turn + k * 512 + lane * 16)
+                           : "memory");
+              if (token < w.live)
+                *reinterpret_cast<uint4*>(a.out + (w.row + token) * a.ldo_t + w.hv * a.ldo_h + (warp & 3) * 32 + (lane & 3) * 8) = v;
+            }
+            __syncwarp();
+          }
+          warp_arrive(bar_free(before));
+        }
+      }
+      if (end) break;
+      before = st;
+      if (++st == kStages) st = 0, ++round;
+    }
+  } else if constexpr (!kLocal) {
+    // ============================ scores ==================================
+    // rows 0 .. 31 (warp 12), 32 .. 63 (13); blocks of 32 columns, the last on the diagonal
+    if (warp <= 13) {
+      const int rows = warp & 1, i = rows * 32 + lane;
       int st = 0;
       uint32_t round = 0;
       for (uint32_t g = 0;; ++g) {
         if (!wait(bar_full(st), round & 1, &s_abort) || (s_step[st].flags & kEnd)) break;
-        const Step& w = s_step[st];
-        uint16_t* dst = a.out + w.row * a.ldo_t + w.hv * a.ldo_h + dv;
-        const int live = w.live;
-        if (!wait(bar_o, g & 1, &s_abort)) break;
-        tc::tc_fence_after();
-        // rolled: the kinds of warps share the instruction cache
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          uint32_t o1[16], o2[16];
-          tc::tmem_ld16(t_lane + kColO1 + i * 16, o1);
-          tc::tmem_ld16(t_lane + kColO2 + i * 16, o2);
-          tc::tmem_wait_ld();
-          if (i == 3) {
-            tc::tc_fence_before();
-            warp_arrive(bar_ofree);
-          }
-          const int here = live - i * 16;
+        float2 w[2][16];      // ready before the scores are: of the diagonal block, of the other
+        const float2 gih = make_float2(s_gh[st][i], s_gh[st][i]), gil = make_float2(s_gl[st][i], s_gl[st][i]);
+        const float2 minus = make_float2(-1.0f, -1.0f);
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float2 eg = *reinterpret_cast<const float2*>(&s_eg[st][i * 16 + e]);
-            const uint32_t y = pack_bf16(fmaf(eg.x, __uint_as_float(o1[e]), __uint_as_float(o2[e])) * a.scale,
-                                         fmaf(eg.y, __uint_as_float(o1[e + 1]), __uint_as_float(o2[e + 1])) * a.scale);
-            if (e < here) *dst = static_cast<uint16_t>(y);
-            dst += a.ldo_t;
-            if (e + 1 < here) *dst = static_cast<uint16_t>(y >> 16);
-            dst += a.ldo_t;
+        for (int k = 0; k < 2; ++k) {
+          if (k > rows) break;
+          const int j0 = (rows - k) * 32;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 gh = *reinterpret_cast<const float2*>(&s_gh[st][j0 + 2 * e]);
+            const float2 gl = *reinterpret_cast<const float2*>(&s_gl[st][j0 + 2 * e]);
+            const float2 x = add2(fma2(gh, minus, gih), fma2(gl, minus, gil));
+            w[k][e] = make_float2(ex2(x.x), ex2(x.y));
           }
         }
+        if (!wait(bar_a, g & 1, &s_abort)) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (k > rows) break;
+          const int j0 = (rows - k) * 32;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t x[16];
+            tc::tmem_ld16(t_lane + kColA + j0 + q * 16, x);
+            tc::tmem_wait_ld();
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float2 y = mul2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), w[k][q * 8 + e]);
+              if (k == 0)      // scores with later tokens may be anything
+                y = make_float2(q * 16 + 2 * e <= lane ? y.x : 0.0f, q * 16 + 2 * e + 1 <= lane ? y.y : 0.0f);
+              hi[e] = split_bf16(y);
+              lo[e] = pack_bf16(y.x, y.y);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+              const uint32_t to = scores + i * 128 + (((j0 >> 3) + q * 2 + (e >> 2)) ^ (i & 7)) * 16;
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[e]), "r"(hi[e + 1]), "r"(hi[e + 2]),
+                           "r"(hi[e + 3])
+                           : "memory");
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + kScores), "r"(lo[e]), "r"(lo[e + 1]), "r"(lo[e + 2]),
+                           "r"(lo[e + 3])
+                           : "memory");
+            }
+          }
+        }
+        tc::tc_fence_before();
+        tc::fence_proxy_async();
+        warp_arrive(bar_p);
         warp_arrive(bar_free(st));
         if (++st == kStages) st = 0, ++round;
       }
-    }
-  } else if constexpr (!kLocal) {
-    // ============================ scores ==================================
-    const int i = (warp & 1) * 32 + lane, j0 = warp >= 16 ? 32 : 0;   // row; first of 32 columns
-    int st = 0;
-    uint32_t round = 0;
-    for (uint32_t g = 0;; ++g) {
-      if (!wait(bar_full(st), round & 1, &s_abort) || (s_step[st].flags & kEnd)) break;
-      if (!wait(bar_a, g & 1, &s_abort)) break;
-      tc::tc_fence_after();
-      const float2 gi = s_g[st][i];
-#pragma unroll 1
-      for (int q = 0; q < 2; ++q) {
-        uint32_t x[16];
-        tc::tmem_ld16(t_lane + kColO2 + j0 + q * 16, x);
-        tc::tmem_wait_ld();
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int j = j0 + q * 16 + 2 * e;
-          float y[2];
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const float2 gj = s_g[st][j + f];
-            const float w = ex2((gi.x - gj.x) + (gi.y - gj.y));
-            y[f] = j + f <= i ? __uint_as_float(x[2 * e + f]) * w : 0.0f;
-          }
-          hi[e] = split_bf16(y[0], y[1]);
-          lo[e] = pack_bf16(y[0], y[1]);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          const uint32_t to = scores + i * 128 + (((j0 >> 3) + q * 2 + (e >> 2)) ^ (i & 7)) * 16;
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[e]), "r"(hi[e + 1]), "r"(hi[e + 2]), "r"(hi[e + 3])
-                       : "memory");
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + kScores), "r"(lo[e]), "r"(lo[e + 1]), "r"(lo[e + 2]),
-                       "r"(lo[e + 3])
-                       : "memory");
-        }
-      }
-      tc::tc_fence_before();
-      tc::fence_proxy_async();
-      warp_arrive(bar_p);
-      warp_arrive(bar_free(st));
-      if (++st == kStages) st = 0, ++round;
     }
   }
 

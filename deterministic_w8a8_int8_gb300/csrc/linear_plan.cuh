@@ -8,6 +8,7 @@
 // each segment from the states and decays of those before it.
 #pragma once
 
+#include "decode.cuh"
 #include "layer.cuh"
 
 namespace prism {
@@ -17,7 +18,6 @@ constexpr int kFewTokens = 16;
 constexpr int kChunk = 64;
 constexpr int kSegChunks = 8;         // chunks of a segment at least
 constexpr int kMaxSegments = 24;
-constexpr int kSms = 152;             // that segments are cut for, whatever the device has
 constexpr float kMinDecay = -16384.0f;   // e^x = 0 from far above it; sums of 64 stay finite
 
 // The segments of a long sequence: those with which its heads fill the SMs in the
@@ -74,9 +74,9 @@ __device__ __forceinline__ bool span_of(const LinAttnArgs& a, int64_t s, bool re
   return offsets;
 }
 
+__device__ __forceinline__ float bounded_decay(float g) { return g < kMinDecay ? kMinDecay : g; }
 __device__ __forceinline__ float decay_of(const LinAttnArgs& a, int64_t token, int h) {
-  const float g = __ldg(a.decay + token * a.ldd_t + h);
-  return g < kMinDecay ? kMinDecay : g;
+  return bounded_decay(__ldg(a.decay + token * a.ldd_t + h));
 }
 
 // Two values as a pair of bf16, and what that leaves of them.
@@ -85,10 +85,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint32_t split_bf16(float& lo, float& hi) {
-  const uint32_t r = pack_bf16(lo, hi);
-  lo -= bf16_lo(r);
-  hi -= bf16_hi(r);
+__device__ __forceinline__ uint32_t split_bf16(float2& v) {
+  const uint32_t r = pack_bf16(v.x, v.y);
+  v = fma2(make_float2(bf16_lo(r), bf16_hi(r)), make_float2(-1.0f, -1.0f), v);
   return r;
 }
 __device__ __forceinline__ float ex2(float x) {   // to about 2^-22
@@ -111,7 +110,7 @@ __device__ __forceinline__ Sum join(Sum a, Sum b) {
 // in powers of two up to each token (in two parts), and the factors that these
 // are, that the chunk's end has left of each token, and of the whole chunk.
 // Returns the chunk's sum.  (Sums in binary64 took the warp some 2000 cycles.)
-__device__ __forceinline__ Sum lay_decays(const float (&dec)[2], float2* g2, float* eg, float* w, float* tot) {
+__device__ __forceinline__ Sum lay_decays(const float (&dec)[2], float* gh, float* gl, float* eg, float* w, float* tot) {
   constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596299e-8f;
   const int lane = threadIdx.x & 31;
   Sum d[2];
@@ -130,7 +129,8 @@ __device__ __forceinline__ Sum lay_decays(const float (&dec)[2], float2* g2, flo
   const Sum g[2] = {join(sum, Sum{-d[1].h, -d[1].l}), sum};
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    g2[2 * lane + e] = make_float2(g[e].h, g[e].l);
+    gh[2 * lane + e] = g[e].h;
+    gl[2 * lane + e] = g[e].l;
     eg[2 * lane + e] = exp2f(__fadd_rn(g[e].h, g[e].l));
     w[2 * lane + e] = exp2f(__fadd_rn(__fsub_rn(total.h, g[e].h), __fsub_rn(total.l, g[e].l)));
   }
