@@ -21,8 +21,8 @@
 //   producer (1)   finds items, copies Q, K and V of chunks ahead into three stages,
 //                  with the chunk's decays and what is to be done
 //   issuer (1)     U, O1, O2 of a chunk, A of the next
-//   state (8)      S's two parts; S after the chunk
-//   values (4)     the decayed values' three parts; the outputs of the chunk before
+//   state (8)      S's two parts; outputs of the chunk before; S after the chunk
+//   values (4)     the decayed values' three parts
 //   scores (2)     w A, its weights ready before A is
 //
 // Every wait on an mbarrier is bounded: after 2 s (prism_debug_wait_expiry
@@ -48,12 +48,13 @@ using namespace lin;
 constexpr unsigned long long kDrainNs = 2000000000ull;
 constexpr int D = 128;
 constexpr int kStages = 3;
-constexpr int kStateWarps = 8, kIssuer = 14, kProducer = 15, kWarps = 16;   // values and outputs 8 .. 11; scores 12, 13
-constexpr int kThreads = kWarps * 32, kStateThreads = kStateWarps * 32;
+constexpr int kStateWarps = 8, kIssuer = 14, kProducer = 15;   // values 8 .. 11 (kLocal: and 16 .. 19); scores 12, 13
+constexpr int threads_of(bool local) { return local ? 640 : 512; }
+constexpr int kStateThreads = kStateWarps * 32;
 constexpr int kTile = kChunk * D * 2, kHalf = kTile / 2;     // of q, k or v: halves of 64 channels
 constexpr int kScores = kChunk * kChunk * 2;
-constexpr int kTurn = 32 * 32 * 2;                           // a warp's turn of outputs
-constexpr int kSmem = kStages * 3 * kTile + 2 * kScores + 3 * kTile + 4 * kTurn + 1024;
+constexpr int kTurn = 32 * 16 * 2;                           // a warp's turn of outputs
+constexpr int kSmem = kStages * 3 * kTile + 2 * kScores + 3 * kTile + kStateWarps * kTurn + 1024;
 constexpr int kAhead = 4;                                    // chunks whose decays are held, three on their way
 constexpr int kPart = D * D + 4;                             // floats of a segment's state in the workspace
 // columns of tensor memory
@@ -84,6 +85,17 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void store_matrices(uint32_t addr, const uint32_t (&r)[4]) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
                : "memory");
+}
+// Four 8 by 8 matrices, each written transposed.
+__device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// 16 lanes by 32 columns, in the fragments of an m16n8 result for each 8 columns.
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                 "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
@@ -116,14 +128,14 @@ __device__ __forceinline__ constexpr uint32_t idesc(int n, bool a_along_rows, bo
 }
 
 template <bool kLocal>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(kLocal), 1)
     linear_tc_chunk_kernel(const __grid_constant__ LinAttnArgs a, const __grid_constant__ Maps maps, int max_segs) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Step s_step[kStages];
   __shared__ __align__(16) float s_gh[kStages][kChunk], s_gl[kStages][kChunk], s_eg[kStages][kChunk], s_w[kStages][kChunk];
   __shared__ __align__(8) float s_dec[kAhead][kChunk];
   __shared__ float s_tot[kStages];
-  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 11];
+  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 12];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -139,25 +151,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bars = smem_u32(s_bar);
   auto bar_full = [&](int st) { return bars + 8 * st; };
   auto bar_free = [&](int st) { return bars + 8 * (kStages + st); };
-  const uint32_t bar_a = bars + 16 * kStages, bar_p = bar_a + 8, bar_v = bar_a + 16, bar_ufree = bar_a + 24,
-                 bar_s = bar_a + 32, bar_q = bar_a + 40, bar_o = bar_a + 48, bar_ofree = bar_a + 56, bar_end = bar_a + 64;
-  // two in turn: kLocal, the values of chunk g wait for U of chunk g - 2 when that of g - 1 may be formed
-  auto bar_u = [&](uint32_t g) { return bar_a + 72 + 8 * (g & 1); };
+  const uint32_t bar_a = bars + 16 * kStages, bar_p = bar_a + 8, bar_ufree = bar_a + 16,
+                 bar_s = bar_a + 24, bar_q = bar_a + 32, bar_o = bar_a + 40, bar_ofree = bar_a + 48, bar_end = bar_a + 56;
+  // two in turn: kLocal, the values of chunk g wait for U of chunk g - 2 alone, when that of
+  // g - 1 may be formed already, or a warp of them still be at those of g - 1
+  auto bar_u = [&](uint32_t g) { return bar_a + 64 + 8 * (g & 1); };
+  auto bar_v = [&](uint32_t g) { return bar_a + 80 + 8 * (g & 1); };
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(bar_full(i), 2);   // the copies, and what the producer writes itself
-      tc::mbar_init(bar_free(i), kLocal ? 1 + kStateWarps + 4 : 1 + kStateWarps + 4 + 2);
+      tc::mbar_init(bar_free(i), kLocal ? 1 + kStateWarps + 8 : 1 + kStateWarps + 4 + 2);
     }
     tc::mbar_init(bar_a, 1);
     tc::mbar_init(bar_p, 2);
-    tc::mbar_init(bar_v, 4);
+    tc::mbar_init(bar_v(0), kLocal ? 8 : 4);
+    tc::mbar_init(bar_v(1), kLocal ? 8 : 4);
     tc::mbar_init(bar_u(0), 1);
     tc::mbar_init(bar_u(1), 1);
     tc::mbar_init(bar_ufree, kStateWarps);
     tc::mbar_init(bar_s, kStateWarps);
     tc::mbar_init(bar_q, 1);
     tc::mbar_init(bar_o, 1);
-    tc::mbar_init(bar_ofree, 4);
+    tc::mbar_init(bar_ofree, kStateWarps);
     tc::mbar_init(bar_end, 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -301,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (!kLocal && more) issue_scores();
     for (uint32_t g = 0; more; ++g) {
-      if (!wait(bar_v, g & 1, &s_abort)) break;
+      if (!wait(bar_v(g), (g >> 1) & 1, &s_abort)) break;
       if (g > 0 && !wait(bar_ufree, (g - 1) & 1, &s_abort)) break;
       tc::tc_fence_after();
       if (lead) {
@@ -355,13 +370,69 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ============================ state ===================================
     const int half = warp >> 2, dv = (warp & 3) * 32 + lane;
     float2 S[32];      // key channels 64 half + 2 i, + 1
-    int st = 0;
+    // ---- outputs of chunk g (stage `of`): the warp's 32 channels, its half of the
+    // tokens, 16 channels at a time by way of its own shared memory
+    auto outputs = [&](uint32_t g, int of) {
+      const Step& w = s_step[of];
+      if (!wait(bar_o, g & 1, &s_abort)) return false;
+      tc::tc_fence_after();
+      const uint32_t turn = scores + 2 * kScores + 3 * kTile + warp * kTurn;
+      const int lr = lane & 7, token = lane >> 1;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t o1[16], o2[16], y[8];      // column groups of 8 tokens: channels c / 4 and c / 4 + 8, tokens 2 (c % 4), + 1
+        tmem_ld_16x256b(t_lane + (16u * k << 16) + kColO1 + half * 32, o1);
+        tmem_ld_16x256b(t_lane + (16u * k << 16) + kColO2 + half * 32, o2);
+        tc::tmem_wait_ld();
+        if (k == 1) {
+          tc::tc_fence_before();
+          warp_arrive(bar_ofree);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 eg = *reinterpret_cast<const float2*>(&s_eg[of][half * 32 + i * 8 + (lane & 3) * 2]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 4 * i + 2 * e;
+            const float2 o = mul2(fma2(eg, make_float2(__uint_as_float(o1[r]), __uint_as_float(o1[r + 1])),
+                                       make_float2(__uint_as_float(o2[r]), __uint_as_float(o2[r + 1]))),
+                                  make_float2(a.scale, a.scale));
+            y[2 * i + e] = pack_bf16(o.x, o.y);
+          }
+        }
+        // rows of 32 bytes, a token's 16 channels; two tokens' groups at a time
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const int row = (i + (lane >> 4)) * 8 + lr;
+          store_transposed(turn + row * 32 + ((((lane >> 3) & 1) ^ ((row >> 2) & 1)) << 4), y[2 * i], y[2 * i + 1], y[2 * i + 2], y[2 * i + 3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = i * 16 + token, at = half * 32 + row;
+          uint4 v;
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "r"(turn + row * 32 + (((lane & 1) ^ ((row >> 2) & 1)) << 4))
+                       : "memory");
+          if (at < w.live)
+            *reinterpret_cast<uint4*>(a.out + (w.row + at) * a.ldo_t + w.hv * a.ldo_h + (warp & 3) * 32 + k * 16 + (lane & 1) * 8) = v;
+        }
+        __syncwarp();
+      }
+      warp_arrive(bar_free(of));
+      return true;
+    };
+    int st = 0, before = 0;
     uint32_t round = 0;
     for (uint32_t g = 0;; ++g) {
       if (!wait(bar_full(st), round & 1, &s_abort)) break;
       const Step& w = s_step[st];
       const int flags = w.flags;
-      if (flags & kEnd) break;
+      if (flags & kEnd) {
+        if (!kLocal && g > 0) outputs(g - 1, before);
+        break;
+      }
       if (flags & kFirst) {
         const float* src = a.state + (w.in * a.Hv + w.hv) * (D * D) + half * 64 * D + dv;
         const int64_t part_step = static_cast<int64_t>(a.Hv) * kPart;
@@ -407,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_wait_st();
         tc::tc_fence_before();
         warp_arrive(bar_s);
+        if (g > 0 && !outputs(g - 1, before)) break;
       }
       const float tot = s_tot[st];
       if (!wait(bar_u(g), (g >> 1) & 1, &s_abort)) break;
@@ -434,114 +506,69 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i) dst[2 * i * D] = S[i].x, dst[(2 * i + 1) * D] = S[i].y;
         }
       }
-      warp_arrive(bar_free(st));
+      if constexpr (kLocal) warp_arrive(bar_free(st));
+      before = st;
       if (++st == kStages) st = 0, ++round;
     }
-  } else if (warp < kStateWarps + 4) {
-    // ==================== decayed values, and outputs ======================
-    int st = 0, before = 0;
+  } else if (warp < kStateWarps + 4 || warp >= 16) {
+    // ========================= decayed values ==============================
+    // 32 channels of v a warp, in three parts, transposed; kLocal: half of the tokens
+    constexpr int kT = kLocal ? 1 : 2;
+    const int t0 = kLocal && warp >= 16 ? 1 : 0;
+    const uint32_t half = (warp & 2) ? kHalf : 0, first = (warp & 1) * 4;   // of the row's pieces of 8 channels
+    const int r8 = lane & 7;
+    int st = 0;
     uint32_t round = 0;
     for (uint32_t g = 0;; ++g) {
       if (!wait(bar_full(st), round & 1, &s_abort)) break;
-      const bool end = s_step[st].flags & kEnd;
-      if (!end) {
-        // ---- 32 channels of v, in three parts, transposed
-        const int live = s_step[st].live;
-        const uint32_t half = (warp & 2) ? kHalf : 0, first = (warp & 1) * 4;   // of the row's pieces of 8 channels
-        // Behind the sequence's end lies another, or anything: zeros, a warp's own
-        // channels of V and as many of K.
-        for (int row = live + (lane >> 3); row < kChunk; row += 4) {
+      const Step& s = s_step[st];
+      if (s.flags & kEnd) break;
+      // Behind the sequence's end lies another, or anything: zeros, the warp's own
+      // channels and tokens of V, and as many of K.
+      if (s.live < kChunk)
+        for (int row = max(s.live, t0 * 32) + (lane >> 3); row < (t0 + kT) * 32; row += 4) {
           const uint32_t to = ((lane & 4) ? tile_k(st) : tile_v(st)) + half + row * 128 + (((first + (lane & 3)) ^ (row & 7)) << 4);
           asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
         }
-        __syncwarp();
-        // the parts were read: of the chunk before, or (kLocal) the one before that
-        constexpr uint32_t kBack = kLocal ? 2 : 1;
-        if (g >= kBack && !wait(bar_u(g - kBack), ((g - kBack) >> 1) & 1, &s_abort)) break;
-        float2 w[8];                                  // of the tokens 8 i + 2 c, + 1, c = lane % 4
+      __syncwarp();
+      uint32_t part[3][4][kT][4];     // ready before their place is free
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const float2*>(&s_w[st][i * 8 + (lane & 3) * 2]);
-        const int r8 = lane & 7;
-#pragma unroll 1
+      for (int t = 0; t < kT; ++t) {
+        float2 w[4];                  // of the tokens 32 t + 8 i + 2 c, + 1, c = lane % 4
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float2*>(&s_w[st][(t0 + t) * 32 + i * 8 + (lane & 3) * 2]);
+#pragma unroll
         for (int p = 0; p < 4; ++p) {
-          const uint32_t from = tile_v(st) + half + lane * 128 + (((first + p) ^ r8) << 4);   // token 32 t + lane
-          const int row = (warp & 3) * 32 + p * 8 + r8;                                     // channel, for the parts' addresses
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            uint32_t x[4], hi[4], mid[4], lo[4];
-            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                         : "r"(from + t * 4096)
-                         : "memory");
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float2 y = mul2(make_float2(bf16_lo(x[i]), bf16_hi(x[i])), w[t * 4 + i]);
-              hi[i] = split_bf16(y);
-              mid[i] = split_bf16(y);
-              lo[i] = pack_bf16(y.x, y.y);
-            }
-            const uint32_t to = row * 128 + (((t * 4 + (lane >> 3)) ^ (row & 7)) << 4);
-            store_matrices(values(g, 0) + to, hi);
-            store_matrices(values(g, 1) + to, mid);
-            store_matrices(values(g, 2) + to, lo);
-          }
-        }
-        tc::fence_proxy_async();
-        warp_arrive(bar_v);
-        if constexpr (kLocal) warp_arrive(bar_free(st));
-      }
-      if constexpr (!kLocal) {
-        if (g > 0) {   // ---- the outputs of the chunk before
-          const Step& w = s_step[before];
-          if (!wait(bar_o, (g - 1) & 1, &s_abort)) break;
-          tc::tc_fence_after();
-          uint32_t y[32];
+          uint32_t x[4];
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                       : "r"(tile_v(st) + half + ((t0 + t) * 32 + lane) * 128 + (((first + p) ^ r8) << 4))
+                       : "memory");
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t o1[16], o2[16];
-            tc::tmem_ld16(t_lane + kColO1 + i * 16, o1);
-            tc::tmem_ld16(t_lane + kColO2 + i * 16, o2);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const float2 eg = *reinterpret_cast<const float2*>(&s_eg[before][i * 16 + e]);
-              const float2 o = mul2(fma2(eg, make_float2(__uint_as_float(o1[e]), __uint_as_float(o1[e + 1])),
-                                         make_float2(__uint_as_float(o2[e]), __uint_as_float(o2[e + 1]))),
-                                    make_float2(a.scale, a.scale));
-              y[i * 8 + e / 2] = pack_bf16(o.x, o.y);
-            }
+            float2 y = mul2(make_float2(bf16_lo(x[i]), bf16_hi(x[i])), w[i]);
+            part[0][p][t][i] = split_bf16(y);
+            part[1][p][t][i] = split_bf16(y);
+            part[2][p][t][i] = pack_bf16(y.x, y.y);
           }
-          tc::tc_fence_before();
-          warp_arrive(bar_ofree);
-          // through the warp's own shared memory, 32 tokens at a time: 64 bytes of a token side by side
-          const uint32_t turn = scores + 2 * kScores + 3 * kTile + (warp & 3) * kTurn;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (t * 32 >= w.live) break;
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              asm volatile("st.shared.u16 [%0], %1;" ::"r"(turn + e * 64 + lane * 2),
-                           "h"(static_cast<uint16_t>(y[t * 16 + e / 2] >> (16 * (e & 1))))
-                           : "memory");
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int token = t * 32 + k * 8 + (lane >> 2);
-              uint4 v;
-              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                           : "r"(turn + k * 512 + lane * 16)
-                           : "memory");
-              if (token < w.live)
-                *reinterpret_cast<uint4*>(a.out + (w.row + token) * a.ldo_t + w.hv * a.ldo_h + (warp & 3) * 32 + (lane & 3) * 8) = v;
-            }
-            __syncwarp();
-          }
-          warp_arrive(bar_free(before));
         }
       }
-      if (end) break;
-      before = st;
+      // free: the parts of the chunk before were read, or (kLocal) of the one before that
+      constexpr uint32_t kBack = kLocal ? 2 : 1;
+      if (g >= kBack && !wait(bar_u(g - kBack), ((g - kBack) >> 1) & 1, &s_abort)) break;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const int row = (warp & 3) * 32 + p * 8 + r8;    // channel, for the parts' addresses
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          const uint32_t to = row * 128 + ((((t0 + t) * 4 + (lane >> 3)) ^ (row & 7)) << 4);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) store_matrices(values(g, k) + to, part[k][p][t]);
+        }
+      }
+      tc::fence_proxy_async();
+      warp_arrive(bar_v(g));
+      warp_arrive(bar_free(st));
       if (++st == kStages) st = 0, ++round;
     }
   } else if constexpr (!kLocal) {
@@ -664,11 +691,11 @@ cudaError_t launch_linear_attention_tc(const LinAttnArgs& a, cudaStream_t stream
   if (segs > 1) {
     e = ensure_smem_attr(reinterpret_cast<const void*>(linear_tc_chunk_kernel<true>), kSmem);
     if (e == cudaSuccess)
-      e = launch_kernel(linear_tc_chunk_kernel<true>, dim3(grid), dim3(kThreads), kSmem, stream, true, a, maps, segs);
+      e = launch_kernel(linear_tc_chunk_kernel<true>, dim3(grid), dim3(threads_of(true)), kSmem, stream, true, a, maps, segs);
   }
   if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(linear_tc_chunk_kernel<false>), kSmem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(linear_tc_chunk_kernel<false>, dim3(grid), dim3(kThreads), kSmem, stream, true, a, maps, segs);
+  return launch_kernel(linear_tc_chunk_kernel<false>, dim3(grid), dim3(threads_of(false)), kSmem, stream, true, a, maps, segs);
 }
 
 cudaError_t read_and_clear_linear_status(uint32_t* out) {

@@ -85,23 +85,22 @@ def linear_attention(q, k, v, decay, starts, lens, scale):
     each and those over 64 scores by 2^-17, besides the state's own error, the
     exponentials' 2^-21 and the rounding to bf16: under 2^-14 of A in all."""
     T, hv, dv = v.shape
-    hk, dk = q.shape[1], q.shape[2]
-    g = np.broadcast_to(np.maximum(decay.astype(np.float64), -16384.0), (T, hv))
-    out, size = np.zeros((T, hv, dv)), np.zeros((T, hv, dv))
-    states, bounds = starts.astype(np.float64).copy(), np.zeros(starts.shape)
-    rep = hv // hk
+    rep = hv // q.shape[1]
+    q, k, v, decay, starts = (torch.from_numpy(np.ascontiguousarray(x)).double().cuda() for x in (q, k, v, decay, starts))
+    gain = torch.exp(decay.clamp(min=-16384.0)).expand(T, hv)[..., None, None]
+    q, k = (x.repeat_interleave(rep, dim=1) for x in (q, k))
+    out, size = torch.zeros((T, hv, dv)).double().cuda(), torch.zeros((T, hv, dv)).double().cuda()
+    states, bounds = starts.clone(), torch.zeros_like(starts)
     at = 0
     for s, n in enumerate(lens):
-        S, A = states[s], np.abs(states[s])
+        both = torch.stack((states[s], states[s].abs()))       # S and A
         for t in range(at, at + n):
-            e = np.exp(g[t])[:, None, None]
-            kk, qq = np.repeat(k[t].astype(np.float64), rep, 0), np.repeat(q[t].astype(np.float64), rep, 0)
-            kv = kk[:, :, None] * v[t].astype(np.float64)[:, None, :]
-            S = e * S + kv
-            A = e * A + np.abs(kv)
-            out[t] = np.einsum("hd,hde->he", qq, S) * scale
-            size[t] = np.einsum("hd,hde->he", np.abs(qq), A) * abs(scale)
-        states[s] = S
-        bounds[s] = A * (2.0 ** -17 + 2.0 ** -22 * (2 + n // 64))
+            kv = k[t][:, :, None] * v[t][:, None, :]
+            both = gain[t] * both + torch.stack((kv, kv.abs()))
+            o = torch.stack((q[t], q[t].abs()))[:, :, None, :] @ both
+            out[t], size[t] = o[0, :, 0] * scale, o[1, :, 0] * abs(scale)
+        states[s] = both[0]
+        bounds[s] = both[1] * (2.0 ** -17 + 2.0 ** -22 * (2 + n // 64))
         at += n
-    return out, HALF_BF16 * np.abs(out) + 2.0 ** -14 * size + 1e-38, states, bounds + 1e-38
+    bound = HALF_BF16 * out.abs() + 2.0 ** -14 * size + 1e-38
+    return tuple(x.cpu().numpy() for x in (out, bound, states, bounds + 1e-38))

@@ -191,6 +191,17 @@ def test_many_sequences_of_few_tokens():
     check(data, lens, state.cpu().numpy(), got, many)
 
 
+def test_more_work_than_places():
+    """More items (sequence, head, segment) than SMs: each CTA has several, of several chunks."""
+    lens = [2100, 70, 1100, 3]
+    data = make(12, lens, 6, 48, 128, 128)
+    state = np.random.default_rng(10).standard_normal((4, 48, 128, 128)).astype(np.float32)
+    dstate = dev(state, torch.float32)
+    own = index([3, 1, 0, 2])
+    got = run(data, lens, dstate, own, own)
+    check(data, lens, state[[3, 1, 0, 2]], got, dstate[own.long()])
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 def test_errors(dim):
     lens = [20, 3, 40, 2, 300]
