@@ -22,8 +22,8 @@
 //                  with the chunk's decays and what is to be done
 //   issuer (1)     U, O1, O2 of a chunk, A of the next
 //   state (8)      S's two parts; outputs of the chunk before; S after the chunk
-//   values (4)     the decayed values' three parts
-//   scores (2)     w A, its weights ready before A is
+//   values (8)     the decayed values' three parts
+//   scores (2)     w A
 //
 // Every wait on an mbarrier is bounded: after 2 s (prism_debug_wait_expiry
 // shortens that for tests) the kernel sets the device status bit; every warp leaves
@@ -48,12 +48,12 @@ using namespace lin;
 constexpr unsigned long long kDrainNs = 2000000000ull;
 constexpr int D = 128;
 constexpr int kStages = 3;
-constexpr int kStateWarps = 8, kIssuer = 14, kProducer = 15;   // values 8 .. 11 (kLocal: and 16 .. 19); scores 12, 13
-constexpr int threads_of(bool local) { return local ? 640 : 512; }
+constexpr int kStateWarps = 8, kIssuer = 14, kProducer = 15;   // values 8 .. 11, 16 .. 19; scores 12, 13
+constexpr int kThreads = 640;
 constexpr int kStateThreads = kStateWarps * 32;
 constexpr int kTile = kChunk * D * 2, kHalf = kTile / 2;     // of q, k or v: halves of 64 channels
 constexpr int kScores = kChunk * kChunk * 2;
-constexpr int kTurn = 32 * 16 * 2;                           // a warp's turn of outputs
+constexpr int kTurn = 16 * 16 * 2;                           // a warp's turn of outputs
 constexpr int kSmem = kStages * 3 * kTile + 2 * kScores + 3 * kTile + kStateWarps * kTurn + 1024;
 constexpr int kAhead = 4;                                    // chunks whose decays are held, three on their way
 constexpr int kPart = D * D + 4;                             // floats of a segment's state in the workspace
@@ -73,9 +73,27 @@ struct Maps {
   CUtensorMap q, k, v;
 };
 
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  return __all_sync(0xffffffffu, tc::mbar_wait_bounded(bar, parity, abort_flag, &g_lin_wait_limit_ns, &g_lin_status,
-                                                       PRISM_DEVSTATUS_WAIT_TIMEOUT));
+// A CTA's waits: their limit in cycles, and whether one has run out.
+struct Limit {
+  long long cycles;
+  int abort;
+};
+// Compact, since it stands in many places and the kinds of warps share the
+// instruction cache.  One answer for the warp.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile Limit* limit) {
+  bool ok = tc::mbar_try_wait(bar, parity);
+  if (!__all_sync(0xffffffffu, ok)) {
+    const long long end = clock64() + limit->cycles;
+    while (!ok && limit->abort == 0) {
+      ok = tc::mbar_try_wait(bar, parity);
+      if (!ok && clock64() > end) {
+        limit->abort = 1;
+        atomicOr(&g_lin_status, PRISM_DEVSTATUS_WAIT_TIMEOUT);
+      }
+    }
+    ok = __all_sync(0xffffffffu, ok);
+  }
+  return ok;
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
@@ -90,11 +108,10 @@ __device__ __forceinline__ void store_matrices(uint32_t addr, const uint32_t (&r
 __device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-// 16 lanes by 32 columns, in the fragments of an m16n8 result for each 8 columns.
-__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-                 "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+// 16 lanes by 16 columns, in the fragments of an m16n8 result for each 8 columns.
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -128,7 +145,7 @@ __device__ __forceinline__ constexpr uint32_t idesc(int n, bool a_along_rows, bo
 }
 
 template <bool kLocal>
-__global__ void __launch_bounds__(threads_of(kLocal), 1)
+__global__ void __launch_bounds__(kThreads, 1)
     linear_tc_chunk_kernel(const __grid_constant__ LinAttnArgs a, const __grid_constant__ Maps maps, int max_segs) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Step s_step[kStages];
@@ -137,7 +154,7 @@ __global__ void __launch_bounds__(threads_of(kLocal), 1)
   __shared__ float s_tot[kStages];
   __shared__ __align__(8) uint64_t s_bar[2 * kStages + 12];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
+  __shared__ Limit s_limit;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(smem);
@@ -160,12 +177,12 @@ __global__ void __launch_bounds__(threads_of(kLocal), 1)
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(bar_full(i), 2);   // the copies, and what the producer writes itself
-      tc::mbar_init(bar_free(i), kLocal ? 1 + kStateWarps + 8 : 1 + kStateWarps + 4 + 2);
+      tc::mbar_init(bar_free(i), 1 + kStateWarps + 8 + (kLocal ? 0 : 2));
     }
     tc::mbar_init(bar_a, 1);
     tc::mbar_init(bar_p, 2);
-    tc::mbar_init(bar_v(0), kLocal ? 8 : 4);
-    tc::mbar_init(bar_v(1), kLocal ? 8 : 4);
+    tc::mbar_init(bar_v(0), 8);
+    tc::mbar_init(bar_v(1), 8);
     tc::mbar_init(bar_u(0), 1);
     tc::mbar_init(bar_u(1), 1);
     tc::mbar_init(bar_ufree, kStateWarps);
@@ -174,7 +191,8 @@ __global__ void __launch_bounds__(threads_of(kLocal), 1)
     tc::mbar_init(bar_o, 1);
     tc::mbar_init(bar_ofree, kStateWarps);
     tc::mbar_init(bar_end, 1);
-    s_abort = 0;
+    s_limit.abort = 0;
+    s_limit.cycles = static_cast<long long>(*static_cast<volatile unsigned long long*>(&g_lin_wait_limit_ns)) * 2;   // of 2 GHz
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -251,7 +269,7 @@ __global__ void __launch_bounds__(threads_of(kLocal), 1)
         for (int c = 0; c < kAhead - 1; ++c) copy_decays(c);
         Sum log_total{0.0f, 0.0f};
         for (int c = 0; c < chunks; ++c) {
-          ok = wait(bar_free(st), (round & 1) ^ 1u, &s_abort);
+          ok = wait(bar_free(st), (round & 1) ^ 1u, &s_limit);
           if (!ok) break;
           const int32_t row = static_cast<int32_t>(b + t0 + static_cast<int64_t>(c) * kChunk);
           if (elect_one()) {
@@ -287,7 +305,7 @@ __global__ void __launch_bounds__(threads_of(kLocal), 1)
         }
       }
     }
-    if (ok && wait(bar_free(st), (round & 1) ^ 1u, &s_abort)) {
+    if (ok && wait(bar_free(st), (round & 1) ^ 1u, &s_limit)) {
       if (lane == 0) {
         s_step[st].flags = kEnd;
         tc::mbar_arrive(bar_full(st));
@@ -302,7 +320,7 @@ __global__ void __launch_bounds__(threads_of(kLocal), 1)
     const bool lead = elect_one();
     int st = 0;
     uint32_t round = 0;
-    bool more = wait(bar_full(0), 0, &s_abort) && !(s_step[0].flags & kEnd);
+    bool more = wait(bar_full(0), 0, &s_limit) && !(s_step[0].flags & kEnd);
     auto issue_scores = [&] {
       if (lead) {
         const uint64_t qd = tc::smem_desc_sw128(tile_q(st)), kd = tc::smem_desc_sw128(tile_k(st));
@@ -316,12 +334,12 @@ __global__ void __launch_bounds__(threads_of(kLocal), 1)
     };
     if (!kLocal && more) issue_scores();
     for (uint32_t g = 0; more; ++g) {
-      if (!wait(bar_v(g), (g >> 1) & 1, &s_abort)) break;
-      if (g > 0 && !wait(bar_ufree, (g - 1) & 1, &s_abort)) break;
+      if (!wait(bar_v(g), (g >> 1) & 1, &s_limit)) break;
+      if (g > 0 && !wait(bar_ufree, (g - 1) & 1, &s_limit)) break;
       tc::tc_fence_after();
       if (lead) {
         const uint64_t kd = desc_along_rows(tile_k(st));
-#pragma unroll
+#pragma unroll 1
         for (int part = 2; part >= 0; --part) {   // the small parts first
           const uint64_t vd = tc::smem_desc_sw128(values(g, part));
 #pragma unroll
@@ -332,12 +350,12 @@ __global__ void __launch_bounds__(threads_of(kLocal), 1)
       }
       __syncwarp();
       if constexpr (!kLocal) {
-        if (!wait(bar_s, g & 1, &s_abort)) break;
-        if (g > 0 && !wait(bar_ofree, (g - 1) & 1, &s_abort)) break;
+        if (!wait(bar_s, g & 1, &s_limit)) break;
+        if (g > 0 && !wait(bar_ofree, (g - 1) & 1, &s_limit)) break;
         tc::tc_fence_after();
         if (lead) {
           const uint64_t qd = tc::smem_desc_sw128(tile_q(st));
-#pragma unroll
+#pragma unroll 1
           for (int part = 1; part >= 0; --part)
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
@@ -346,11 +364,11 @@ __global__ void __launch_bounds__(threads_of(kLocal), 1)
           tc::tc_commit(bar_q);
         }
         __syncwarp();
-        if (!wait(bar_p, g & 1, &s_abort)) break;
+        if (!wait(bar_p, g & 1, &s_limit)) break;
         tc::tc_fence_after();
         if (lead) {
           const uint64_t vd = desc_along_rows(tile_v(st)), pd = tc::smem_desc_sw128(scores);
-#pragma unroll
+#pragma unroll 1
           for (int part = 1; part >= 0; --part)
 #pragma unroll
             for (int k = 0; k < kChunk / 16; ++k)
@@ -363,7 +381,7 @@ __global__ void __launch_bounds__(threads_of(kLocal), 1)
       if (lead) tc::tc_commit(bar_free(st));
       __syncwarp();
       if (++st == kStages) st = 0, ++round;
-      more = wait(bar_full(st), round & 1, &s_abort) && !(s_step[st].flags & kEnd);
+      more = wait(bar_full(st), round & 1, &s_limit) && !(s_step[st].flags & kEnd);
       if (!kLocal && more) issue_scores();   // A was read: w A of this chunk was waited for
     }
   } else if (warp < kStateWarps) {
@@ -374,50 +392,40 @@ __global__ void __launch_bounds__(threads_of(kLocal), 1)
     // tokens, 16 channels at a time by way of its own shared memory
     auto outputs = [&](uint32_t g, int of) {
       const Step& w = s_step[of];
-      if (!wait(bar_o, g & 1, &s_abort)) return false;
+      if (!wait(bar_o, g & 1, &s_limit)) return false;
       tc::tc_fence_after();
       const uint32_t turn = scores + 2 * kScores + 3 * kTile + warp * kTurn;
-      const int lr = lane & 7, token = lane >> 1;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t o1[16], o2[16], y[8];      // column groups of 8 tokens: channels c / 4 and c / 4 + 8, tokens 2 (c % 4), + 1
-        tmem_ld_16x256b(t_lane + (16u * k << 16) + kColO1 + half * 32, o1);
-        tmem_ld_16x256b(t_lane + (16u * k << 16) + kColO2 + half * 32, o2);
+      // where the lane writes a row of its matrix, and reads a piece: rows of 32 bytes, a token's 16 channels
+      const int row_w = ((lane >> 4) << 3) + (lane & 7), row_r = lane >> 1;
+      const uint32_t to = turn + row_w * 32 + ((((lane >> 3) ^ (row_w >> 2)) & 1) << 4);
+      const uint32_t from = turn + row_r * 32 + (((lane ^ (row_r >> 2)) & 1) << 4);
+      const int live = w.live - half * 32 - row_r;
+      uint16_t* dst = a.out + (w.row + half * 32 + row_r) * a.ldo_t + w.hv * a.ldo_h + (warp & 3) * 32 + (lane & 1) * 8;
+      // 16 channels by 16 tokens a turn; rolled: the kinds of warps share the instruction cache
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const int t = i & 1, k = i >> 1;
+        uint32_t o1[8], o2[8], y[4];      // for each 8 tokens: channels c / 4 and c / 4 + 8, tokens 2 (c % 4), + 1
+        tmem_ld_16x256b(t_lane + (16u * k << 16) + kColO1 + half * 32 + t * 16, o1);
+        tmem_ld_16x256b(t_lane + (16u * k << 16) + kColO2 + half * 32 + t * 16, o2);
         tc::tmem_wait_ld();
-        if (k == 1) {
+        if (i == 3) {
           tc::tc_fence_before();
           warp_arrive(bar_ofree);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 eg = *reinterpret_cast<const float2*>(&s_eg[of][half * 32 + i * 8 + (lane & 3) * 2]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = 4 * i + 2 * e;
-            const float2 o = mul2(fma2(eg, make_float2(__uint_as_float(o1[r]), __uint_as_float(o1[r + 1])),
-                                       make_float2(__uint_as_float(o2[r]), __uint_as_float(o2[r + 1]))),
-                                  make_float2(a.scale, a.scale));
-            y[2 * i + e] = pack_bf16(o.x, o.y);
-          }
+        for (int e = 0; e < 4; ++e) {
+          const float2 eg = *reinterpret_cast<const float2*>(&s_eg[of][half * 32 + t * 16 + (e >> 1) * 8 + (lane & 3) * 2]);
+          const float2 o = mul2(fma2(eg, make_float2(__uint_as_float(o1[2 * e]), __uint_as_float(o1[2 * e + 1])),
+                                     make_float2(__uint_as_float(o2[2 * e]), __uint_as_float(o2[2 * e + 1]))),
+                                make_float2(a.scale, a.scale));
+          y[e] = pack_bf16(o.x, o.y);
         }
-        // rows of 32 bytes, a token's 16 channels; two tokens' groups at a time
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          const int row = (i + (lane >> 4)) * 8 + lr;
-          store_transposed(turn + row * 32 + ((((lane >> 3) & 1) ^ ((row >> 2) & 1)) << 4), y[2 * i], y[2 * i + 1], y[2 * i + 2], y[2 * i + 3]);
-        }
+        store_transposed(to, y[0], y[1], y[2], y[3]);
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = i * 16 + token, at = half * 32 + row;
-          uint4 v;
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                       : "r"(turn + row * 32 + (((lane & 1) ^ ((row >> 2) & 1)) << 4))
-                       : "memory");
-          if (at < w.live)
-            *reinterpret_cast<uint4*>(a.out + (w.row + at) * a.ldo_t + w.hv * a.ldo_h + (warp & 3) * 32 + k * 16 + (lane & 1) * 8) = v;
-        }
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
+        if (t * 16 < live) *reinterpret_cast<uint4*>(dst + t * 16 * a.ldo_t + k * 16) = v;
         __syncwarp();
       }
       warp_arrive(bar_free(of));
@@ -426,14 +434,11 @@ __global__ void __launch_bounds__(threads_of(kLocal), 1)
     int st = 0, before = 0;
     uint32_t round = 0;
     for (uint32_t g = 0;; ++g) {
-      if (!wait(bar_full(st), round & 1, &s_abort)) break;
+      if (!wait(bar_full(st), round & 1, &s_limit)) break;
       const Step& w = s_step[st];
       const int flags = w.flags;
-      if (flags & kEnd) {
-        if (!kLocal && g > 0) outputs(g - 1, before);
-        break;
-      }
-      if (flags & kFirst) {
+      const bool end = flags & kEnd;
+      if (!end && (flags & kFirst)) {
         const float* src = a.state + (w.in * a.Hv + w.hv) * (D * D) + half * 64 * D + dv;
         const int64_t part_step = static_cast<int64_t>(a.Hv) * kPart;
         const bool slot = w.in >= 0 && (kLocal ? w.seg == 0 : w.seg < 0);
@@ -460,8 +465,8 @@ __global__ void __launch_bounds__(threads_of(kLocal), 1)
           }
         }
       }
-      if constexpr (!kLocal) {
-        if (g > 0 && !wait(bar_q, (g - 1) & 1, &s_abort)) break;   // the parts were read
+      if (!kLocal && !end) {
+        if (g > 0 && !wait(bar_q, (g - 1) & 1, &s_limit)) break;   // the parts were read
         tc::tc_fence_after();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -478,10 +483,11 @@ __global__ void __launch_bounds__(threads_of(kLocal), 1)
         tc::tmem_wait_st();
         tc::tc_fence_before();
         warp_arrive(bar_s);
-        if (g > 0 && !outputs(g - 1, before)) break;
       }
+      if (!kLocal && g > 0 && !outputs(g - 1, before)) break;
+      if (end) break;
       const float tot = s_tot[st];
-      if (!wait(bar_u(g), (g >> 1) & 1, &s_abort)) break;
+      if (!wait(bar_u(g), (g >> 1) & 1, &s_limit)) break;
       tc::tc_fence_after();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {   // 16 at a time, by registers
@@ -512,59 +518,50 @@ __global__ void __launch_bounds__(threads_of(kLocal), 1)
     }
   } else if (warp < kStateWarps + 4 || warp >= 16) {
     // ========================= decayed values ==============================
-    // 32 channels of v a warp, in three parts, transposed; kLocal: half of the tokens
-    constexpr int kT = kLocal ? 1 : 2;
-    const int t0 = kLocal && warp >= 16 ? 1 : 0;
+    // 32 channels of v and half of the tokens a warp, in three parts, transposed
+    const int t0 = warp >= 16 ? 32 : 0;
     const uint32_t half = (warp & 2) ? kHalf : 0, first = (warp & 1) * 4;   // of the row's pieces of 8 channels
     const int r8 = lane & 7;
     int st = 0;
     uint32_t round = 0;
     for (uint32_t g = 0;; ++g) {
-      if (!wait(bar_full(st), round & 1, &s_abort)) break;
+      if (!wait(bar_full(st), round & 1, &s_limit)) break;
       const Step& s = s_step[st];
       if (s.flags & kEnd) break;
       // Behind the sequence's end lies another, or anything: zeros, the warp's own
       // channels and tokens of V, and as many of K.
       if (s.live < kChunk)
-        for (int row = max(s.live, t0 * 32) + (lane >> 3); row < (t0 + kT) * 32; row += 4) {
+        for (int row = max(s.live, t0) + (lane >> 3); row < t0 + 32; row += 4) {
           const uint32_t to = ((lane & 4) ? tile_k(st) : tile_v(st)) + half + row * 128 + (((first + (lane & 3)) ^ (row & 7)) << 4);
           asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
         }
       __syncwarp();
-      uint32_t part[3][4][kT][4];     // ready before their place is free
+      float2 w[4];                    // of the tokens 8 i + 2 c, + 1, c = lane % 4
 #pragma unroll
-      for (int t = 0; t < kT; ++t) {
-        float2 w[4];                  // of the tokens 32 t + 8 i + 2 c, + 1, c = lane % 4
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float2*>(&s_w[st][(t0 + t) * 32 + i * 8 + (lane & 3) * 2]);
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          uint32_t x[4];
-          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                       : "r"(tile_v(st) + half + ((t0 + t) * 32 + lane) * 128 + (((first + p) ^ r8) << 4))
-                       : "memory");
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float2 y = mul2(make_float2(bf16_lo(x[i]), bf16_hi(x[i])), w[i]);
-            part[0][p][t][i] = split_bf16(y);
-            part[1][p][t][i] = split_bf16(y);
-            part[2][p][t][i] = pack_bf16(y.x, y.y);
-          }
-        }
-      }
-      // free: the parts of the chunk before were read, or (kLocal) of the one before that
+      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float2*>(&s_w[st][t0 + i * 8 + (lane & 3) * 2]);
+      // their place is free: the parts of the chunk before were read, or (kLocal) of the one before that
       constexpr uint32_t kBack = kLocal ? 2 : 1;
-      if (g >= kBack && !wait(bar_u(g - kBack), ((g - kBack) >> 1) & 1, &s_abort)) break;
-#pragma unroll
+      if (g >= kBack && !wait(bar_u(g - kBack), ((g - kBack) >> 1) & 1, &s_limit)) break;
+      // rolled: the kinds of warps share the instruction cache
+#pragma unroll 1
       for (int p = 0; p < 4; ++p) {
-        const int row = (warp & 3) * 32 + p * 8 + r8;    // channel, for the parts' addresses
+        uint32_t x[4], hi[4], mid[4], lo[4];
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                     : "r"(tile_v(st) + half + (t0 + lane) * 128 + (((first + p) ^ r8) << 4))
+                     : "memory");
 #pragma unroll
-        for (int t = 0; t < kT; ++t) {
-          const uint32_t to = row * 128 + ((((t0 + t) * 4 + (lane >> 3)) ^ (row & 7)) << 4);
-#pragma unroll
-          for (int k = 0; k < 3; ++k) store_matrices(values(g, k) + to, part[k][p][t]);
+        for (int i = 0; i < 4; ++i) {
+          float2 y = mul2(make_float2(bf16_lo(x[i]), bf16_hi(x[i])), w[i]);
+          hi[i] = split_bf16(y);
+          mid[i] = split_bf16(y);
+          lo[i] = pack_bf16(y.x, y.y);
         }
+        const int row = (warp & 3) * 32 + p * 8 + r8;    // channel, for the parts' addresses
+        const uint32_t to = row * 128 + ((((t0 >> 3) + (lane >> 3)) ^ r8) << 4);
+        store_matrices(values(g, 0) + to, hi);
+        store_matrices(values(g, 1) + to, mid);
+        store_matrices(values(g, 2) + to, lo);
       }
       tc::fence_proxy_async();
       warp_arrive(bar_v(g));
@@ -573,58 +570,48 @@ __global__ void __launch_bounds__(threads_of(kLocal), 1)
     }
   } else if constexpr (!kLocal) {
     // ============================ scores ==================================
-    // rows 0 .. 31 (warp 12), 32 .. 63 (13); blocks of 32 columns, the last on the diagonal
+    // rows 0 .. 31 (warp 12), 32 .. 63 (13)
     if (warp <= 13) {
       const int rows = warp & 1, i = rows * 32 + lane;
       int st = 0;
       uint32_t round = 0;
       for (uint32_t g = 0;; ++g) {
-        if (!wait(bar_full(st), round & 1, &s_abort) || (s_step[st].flags & kEnd)) break;
-        float2 w[2][16];      // ready before the scores are: of the diagonal block, of the other
+        if (!wait(bar_full(st), round & 1, &s_limit) || (s_step[st].flags & kEnd)) break;
         const float2 gih = make_float2(s_gh[st][i], s_gh[st][i]), gil = make_float2(s_gl[st][i], s_gl[st][i]);
-        const float2 minus = make_float2(-1.0f, -1.0f);
+        if (!wait(bar_a, g & 1, &s_limit)) break;
+        tc::tc_fence_after();
+        // 16 columns at a time; rolled: the kinds of warps share the instruction cache
+#pragma unroll 1
+        for (int j0 = 0; j0 < (rows + 1) * 32; j0 += 16) {
+          uint32_t x[16], hi[8], lo[8];
+          tc::tmem_ld16(t_lane + kColA + j0, x);
+          float2 w[8];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if (k > rows) break;
-          const int j0 = (rows - k) * 32;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < 8; ++e) {
             const float2 gh = *reinterpret_cast<const float2*>(&s_gh[st][j0 + 2 * e]);
             const float2 gl = *reinterpret_cast<const float2*>(&s_gl[st][j0 + 2 * e]);
-            const float2 x = add2(fma2(gh, minus, gih), fma2(gl, minus, gil));
-            w[k][e] = make_float2(ex2(x.x), ex2(x.y));
+            const float2 d = add2(fma2(gh, make_float2(-1.0f, -1.0f), gih), fma2(gl, make_float2(-1.0f, -1.0f), gil));
+            w[e] = make_float2(ex2(d.x), ex2(d.y));
           }
-        }
-        if (!wait(bar_a, g & 1, &s_abort)) break;
-        tc::tc_fence_after();
+          tc::tmem_wait_ld();
+          const int ahead = i - j0;      // columns that the row sees, less one: the others' scores may be anything
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if (k > rows) break;
-          const int j0 = (rows - k) * 32;
+          for (int e = 0; e < 8; ++e) {
+            float2 y = mul2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), w[e]);
+            y = make_float2(2 * e <= ahead ? y.x : 0.0f, 2 * e + 1 <= ahead ? y.y : 0.0f);
+            hi[e] = split_bf16(y);
+            lo[e] = pack_bf16(y.x, y.y);
+          }
+          const uint32_t to = scores + i * 128;
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t x[16];
-            tc::tmem_ld16(t_lane + kColA + j0 + q * 16, x);
-            tc::tmem_wait_ld();
-            uint32_t hi[8], lo[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float2 y = mul2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), w[k][q * 8 + e]);
-              if (k == 0)      // scores with later tokens may be anything
-                y = make_float2(q * 16 + 2 * e <= lane ? y.x : 0.0f, q * 16 + 2 * e + 1 <= lane ? y.y : 0.0f);
-              hi[e] = split_bf16(y);
-              lo[e] = pack_bf16(y.x, y.y);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-              const uint32_t to = scores + i * 128 + (((j0 >> 3) + q * 2 + (e >> 2)) ^ (i & 7)) * 16;
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[e]), "r"(hi[e + 1]), "r"(hi[e + 2]),
-                           "r"(hi[e + 3])
-                           : "memory");
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + kScores), "r"(lo[e]), "r"(lo[e + 1]), "r"(lo[e + 2]),
-                           "r"(lo[e + 3])
-                           : "memory");
-            }
+          for (int e = 0; e < 8; e += 4) {
+            const uint32_t piece = (((j0 >> 3) + (e >> 2)) ^ (i & 7)) * 16;
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + piece), "r"(hi[e]), "r"(hi[e + 1]), "r"(hi[e + 2]),
+                         "r"(hi[e + 3])
+                         : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + piece + kScores), "r"(lo[e]), "r"(lo[e + 1]),
+                         "r"(lo[e + 2]), "r"(lo[e + 3])
+                         : "memory");
           }
         }
         tc::tc_fence_before();
@@ -691,11 +678,11 @@ cudaError_t launch_linear_attention_tc(const LinAttnArgs& a, cudaStream_t stream
   if (segs > 1) {
     e = ensure_smem_attr(reinterpret_cast<const void*>(linear_tc_chunk_kernel<true>), kSmem);
     if (e == cudaSuccess)
-      e = launch_kernel(linear_tc_chunk_kernel<true>, dim3(grid), dim3(threads_of(true)), kSmem, stream, true, a, maps, segs);
+      e = launch_kernel(linear_tc_chunk_kernel<true>, dim3(grid), dim3(kThreads), kSmem, stream, true, a, maps, segs);
   }
   if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(linear_tc_chunk_kernel<false>), kSmem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(linear_tc_chunk_kernel<false>, dim3(grid), dim3(threads_of(false)), kSmem, stream, true, a, maps, segs);
+  return launch_kernel(linear_tc_chunk_kernel<false>, dim3(grid), dim3(kThreads), kSmem, stream, true, a, maps, segs);
 }
 
 cudaError_t read_and_clear_linear_status(uint32_t* out) {

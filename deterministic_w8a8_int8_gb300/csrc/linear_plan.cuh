@@ -131,8 +131,8 @@ __device__ __forceinline__ Sum lay_decays(const float (&dec)[2], float* gh, floa
   for (int e = 0; e < 2; ++e) {
     gh[2 * lane + e] = g[e].h;
     gl[2 * lane + e] = g[e].l;
-    eg[2 * lane + e] = exp2f(__fadd_rn(g[e].h, g[e].l));
-    w[2 * lane + e] = exp2f(__fadd_rn(__fsub_rn(total.h, g[e].h), __fsub_rn(total.l, g[e].l)));
+    eg[2 * lane + e] = ex2(__fadd_rn(g[e].h, g[e].l));
+    w[2 * lane + e] = ex2(__fadd_rn(__fsub_rn(total.h, g[e].h), __fsub_rn(total.l, g[e].l)));
   }
   if (lane == 0) *tot = exp2f(__fadd_rn(total.h, total.l));
   return total;
