@@ -281,7 +281,17 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
   };
   Sum log_total{0.0f, 0.0f};  // of the segment so far (warp 0)
   auto lay_decay = [&](int c) {
-    log_total = join(log_total, lay_decays(dec, s_gh[c & 1], s_gl[c & 1], s_eg[c & 1], s_w[c & 1], &s_tot[c & 1]));
+    const Decays d = sum_decays(dec);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = 2 * lane + e;
+      s_gh[c & 1][i] = d.g[e].h;
+      s_gl[c & 1][i] = d.g[e].l;
+      s_eg[c & 1][i] = ex2(__fadd_rn(d.g[e].h, d.g[e].l));
+      s_w[c & 1][i] = left_of(d, e);
+    }
+    if (lane == 0) s_tot[c & 1] = exp2f(__fadd_rn(d.total.h, d.total.l));
+    log_total = join(log_total, d.total);
   };
 
   copy(0);

@@ -1,17 +1,20 @@
 // linear_attention_tc.cu -- the chunked form of linear attention on the tcgen05
 // tensor cores, for heads of 128 by 128 channels.
 //
-// A chunk's 64 tokens against one head (G, w, S as in linear_attention.cu), each product
-// with 128 rows in the lanes of tensor memory:
-//   A  = Q K^T          64 by 64 scores (the lower 64 lanes)          8 steps of 16
-//   O1 = S^T Q^T        128 channels of v by 64 tokens, S in two bf16 parts   2 * 8
-//   O2 = V^T (w A)^T    the same shape, the scores in two parts               2 * 4
-//   U  = (w V)^T K      128 by 128, V's decayed values in three parts         3 * 4
-// and out = scale * (e^G O1 + O2)^T, S = e^{G_C} S + U^T.  S^T is an operand in
+// A chunk's 64 tokens against one head (G and S as in linear_attention.cu, in
+// powers of two), each product with 128 rows in the lanes of tensor memory:
+//   A  = Q K^T                   64 by 64 scores (the lower 64 lanes)       8 steps of 16
+//   O  = S^T Q^T                 128 channels of v by 64 tokens, S in two bf16 parts  2 * 8
+//      + V^T (2^{-G_j} A)^T      the scores in two parts                     2 * 4
+//   U  = (2^{G_C - G_j} V)^T K   128 by 128, V's decayed values in three parts  3 * 4
+// and out = scale * 2^{G_i} O^T, S = 2^{G_C} S + U^T.  The scores' weights are those
+// of a column alone.  Where a chunk's decays go below 2^-80 (kDeep), G_i stops there
+// for the outputs, and the scores of those rows make up for it: what 2^-80 is left
+// of in the state that entered counts as 2^-80 of it.  S^T is an operand in
 // tensor memory, formed by the warps that have it; Q, K and V are read as they lie,
 // by tensor copies in the 128-byte-swizzled layout (K-major for Q and K; for K in U
-// and V in O2 along the tokens, the operand's other major); w A and (w V)^T lie in
-// shared memory beside them.  S stays in the registers of
+// and V in O along the tokens, the operand's other major); the weighted scores and
+// values lie in shared memory beside them.  S stays in the registers of
 // eight warps (lane v channel, 64 key channels a thread) from a sequence's first
 // chunk to its last: U is formed from zero for each chunk, its small parts first,
 // and added to S rounded to nearest, since the tensor cores' additions cut off.
@@ -20,10 +23,10 @@
 // on by mbarriers:
 //   producer (1)   finds items, copies Q, K and V of chunks ahead into three stages,
 //                  with the chunk's decays and what is to be done
-//   issuer (1)     U, O1, O2 of a chunk, A of the next
-//   state (8)      S's two parts; outputs of the chunk before; S after the chunk
-//   values (8)     the decayed values' three parts
-//   scores (2)     w A
+//   issuer (1)     U and O of a chunk, A of the next
+//   state (8)      S's two parts; S after the chunk
+//   values (8)     the decayed values' three parts; outputs of the chunk before
+//   scores (2)     the weighted scores
 //
 // Every wait on an mbarrier is bounded: after 2 s (prism_debug_wait_expiry
 // shortens that for tests) the kernel sets the device status bit; every warp leaves
@@ -58,9 +61,10 @@ constexpr int kSmem = kStages * 3 * kTile + 2 * kScores + 3 * kTile + kStateWarp
 constexpr int kAhead = 4;                                    // chunks whose decays are held, three on their way
 constexpr int kPart = D * D + 4;                             // floats of a segment's state in the workspace
 // columns of tensor memory
-constexpr uint32_t kColU = 0, kColS = 128, kColA = 256, kColO1 = 320, kColO2 = 384;
+constexpr uint32_t kColU = 0, kColS = 128, kColA = 256, kColO = 320;   // O of two chunks in turn
 
-enum { kFirst = 1, kLast = 2, kEnd = 4 };
+constexpr float kDeepest = 80.0f;
+enum { kFirst = 1, kLast = 2, kEnd = 4, kDeep = 8 };
 struct Step {          // a chunk's work
   int64_t row;         // its first token
   int64_t in, out;     // states: of the sequence's start (kFirst); to write to (kLast), -1 for none
@@ -149,10 +153,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     linear_tc_chunk_kernel(const __grid_constant__ LinAttnArgs a, const __grid_constant__ Maps maps, int max_segs) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Step s_step[kStages];
-  __shared__ __align__(16) float s_gh[kStages][kChunk], s_gl[kStages][kChunk], s_eg[kStages][kChunk], s_w[kStages][kChunk];
+  __shared__ __align__(16) float s_gh[kStages][kChunk], s_gl[kStages][kChunk];   // G, in two parts (kDeep)
+  // 2^G times the scale, 2^-G, 2^{G_C - G}
+  __shared__ __align__(16) float s_out[kStages][kChunk], s_in[kStages][kChunk], s_w[kStages][kChunk];
   __shared__ __align__(8) float s_dec[kAhead][kChunk];
   __shared__ float s_tot[kStages];
-  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 12];
+  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 14];
   __shared__ uint32_t s_tmem;
   __shared__ Limit s_limit;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -169,11 +175,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar_full = [&](int st) { return bars + 8 * st; };
   auto bar_free = [&](int st) { return bars + 8 * (kStages + st); };
   const uint32_t bar_a = bars + 16 * kStages, bar_p = bar_a + 8, bar_ufree = bar_a + 16,
-                 bar_s = bar_a + 24, bar_q = bar_a + 32, bar_o = bar_a + 40, bar_ofree = bar_a + 48, bar_end = bar_a + 56;
+                 bar_s = bar_a + 24, bar_q = bar_a + 32, bar_end = bar_a + 40;
   // two in turn: kLocal, the values of chunk g wait for U of chunk g - 2 alone, when that of
   // g - 1 may be formed already, or a warp of them still be at those of g - 1
-  auto bar_u = [&](uint32_t g) { return bar_a + 64 + 8 * (g & 1); };
-  auto bar_v = [&](uint32_t g) { return bar_a + 80 + 8 * (g & 1); };
+  auto bar_u = [&](uint32_t g) { return bar_a + 48 + 8 * (g & 1); };
+  auto bar_v = [&](uint32_t g) { return bar_a + 64 + 8 * (g & 1); };
+  auto bar_o = [&](uint32_t g) { return bar_a + 80 + 8 * (g & 1); };
+  auto bar_ofree = [&](uint32_t g) { return bar_a + 96 + 8 * (g & 1); };
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(bar_full(i), 2);   // the copies, and what the producer writes itself
@@ -188,8 +196,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(bar_ufree, kStateWarps);
     tc::mbar_init(bar_s, kStateWarps);
     tc::mbar_init(bar_q, 1);
-    tc::mbar_init(bar_o, 1);
-    tc::mbar_init(bar_ofree, kStateWarps);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar_o(i), 1);
+      tc::mbar_init(bar_ofree(i), 8);
+    }
     tc::mbar_init(bar_end, 1);
     s_limit.abort = 0;
     s_limit.cycles = static_cast<long long>(*static_cast<volatile unsigned long long*>(&g_lin_wait_limit_ns)) * 2;   // of 2 GHz
@@ -287,13 +297,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           cp_async_wait<kAhead - 1>();
           const float2 g2 = *reinterpret_cast<const float2*>(&s_dec[c & (kAhead - 1)][2 * lane]);
           const float dec[2] = {bounded_decay(g2.x), bounded_decay(g2.y)};
-          log_total = join(log_total, lay_decays(dec, s_gh[st], s_gl[st], s_eg[st], s_w[st], &s_tot[st]));
+          const Decays d = sum_decays(dec);
+          log_total = join(log_total, d.total);
+          const bool deep = d.total.h < -kDeepest;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int i = 2 * lane + e;
+            const float G = __fadd_rn(d.g[e].h, d.g[e].l);
+            if constexpr (!kLocal) {
+              s_out[st][i] = ex2(fmaxf(G, -kDeepest)) * a.scale;
+              s_in[st][i] = ex2(fminf(-G, kDeepest));
+              if (deep) s_gh[st][i] = d.g[e].h, s_gl[st][i] = d.g[e].l;
+            }
+            s_w[st][i] = left_of(d, e);
+          }
+          if (lane == 0) s_tot[st] = exp2f(__fadd_rn(d.total.h, d.total.l));
           if (lane == 0) {
             Step& w = s_step[st];
             w.row = row;
             w.live = static_cast<int>(min(static_cast<int64_t>(kChunk), t1 - t0 - static_cast<int64_t>(c) * kChunk));
             w.hv = h;
-            w.flags = (c == 0 ? kFirst : 0) | (c + 1 == chunks ? kLast : 0);
+            w.flags = (c == 0 ? kFirst : 0) | (c + 1 == chunks ? kLast : 0) | (deep ? kDeep : 0);
             w.in = in;
             w.out = kLocal ? sg + 1 : sg + 1 == sgs ? out : -1;
             w.part = (first_place(b) * a.Hv + h) * kPart;
@@ -351,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if constexpr (!kLocal) {
         if (!wait(bar_s, g & 1, &s_limit)) break;
-        if (g > 0 && !wait(bar_ofree, (g - 1) & 1, &s_limit)) break;
+        if (g > 1 && !wait(bar_ofree(g), ((g - 2) >> 1) & 1, &s_limit)) break;
         tc::tc_fence_after();
         if (lead) {
           const uint64_t qd = tc::smem_desc_sw128(tile_q(st));
@@ -359,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int part = 1; part >= 0; --part)
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-              tc::tc_mma_ta(tmem + kColO1, tmem + kColS + part * 64 + k * 8, qd + (k >> 2) * (kHalf >> 4) + 2 * (k & 3),
+              tc::tc_mma_ta(tmem + kColO + (g & 1) * kChunk, tmem + kColS + part * 64 + k * 8, qd + (k >> 2) * (kHalf >> 4) + 2 * (k & 3),
                             idesc(kChunk, false, false), part != 1 || k != 0 ? 1u : 0u);
           tc::tc_commit(bar_q);
         }
@@ -372,9 +396,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int part = 1; part >= 0; --part)
 #pragma unroll
             for (int k = 0; k < kChunk / 16; ++k)
-              tc::tc_mma(tmem + kColO2, vd + k * (16 * 128 >> 4), pd + part * (kScores >> 4) + 2 * k, idesc(kChunk, true, false),
-                         part != 1 || k != 0 ? 1u : 0u);
-          tc::tc_commit(bar_o);
+              tc::tc_mma(tmem + kColO + (g & 1) * kChunk, vd + k * (16 * 128 >> 4), pd + part * (kScores >> 4) + 2 * k,
+                         idesc(kChunk, true, false), 1u);
+          tc::tc_commit(bar_o(g));
         }
         __syncwarp();
       }
@@ -388,57 +412,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ============================ state ===================================
     const int half = warp >> 2, dv = (warp & 3) * 32 + lane;
     float2 S[32];      // key channels 64 half + 2 i, + 1
-    // ---- outputs of chunk g (stage `of`): the warp's 32 channels, its half of the
-    // tokens, 16 channels at a time by way of its own shared memory
-    auto outputs = [&](uint32_t g, int of) {
-      const Step& w = s_step[of];
-      if (!wait(bar_o, g & 1, &s_limit)) return false;
-      tc::tc_fence_after();
-      const uint32_t turn = scores + 2 * kScores + 3 * kTile + warp * kTurn;
-      // where the lane writes a row of its matrix, and reads a piece: rows of 32 bytes, a token's 16 channels
-      const int row_w = ((lane >> 4) << 3) + (lane & 7), row_r = lane >> 1;
-      const uint32_t to = turn + row_w * 32 + ((((lane >> 3) ^ (row_w >> 2)) & 1) << 4);
-      const uint32_t from = turn + row_r * 32 + (((lane ^ (row_r >> 2)) & 1) << 4);
-      const int live = w.live - half * 32 - row_r;
-      uint16_t* dst = a.out + (w.row + half * 32 + row_r) * a.ldo_t + w.hv * a.ldo_h + (warp & 3) * 32 + (lane & 1) * 8;
-      // 16 channels by 16 tokens a turn; rolled: the kinds of warps share the instruction cache
-#pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        const int t = i & 1, k = i >> 1;
-        uint32_t o1[8], o2[8], y[4];      // for each 8 tokens: channels c / 4 and c / 4 + 8, tokens 2 (c % 4), + 1
-        tmem_ld_16x256b(t_lane + (16u * k << 16) + kColO1 + half * 32 + t * 16, o1);
-        tmem_ld_16x256b(t_lane + (16u * k << 16) + kColO2 + half * 32 + t * 16, o2);
-        tc::tmem_wait_ld();
-        if (i == 3) {
-          tc::tc_fence_before();
-          warp_arrive(bar_ofree);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 eg = *reinterpret_cast<const float2*>(&s_eg[of][half * 32 + t * 16 + (e >> 1) * 8 + (lane & 3) * 2]);
-          const float2 o = mul2(fma2(eg, make_float2(__uint_as_float(o1[2 * e]), __uint_as_float(o1[2 * e + 1])),
-                                     make_float2(__uint_as_float(o2[2 * e]), __uint_as_float(o2[2 * e + 1]))),
-                                make_float2(a.scale, a.scale));
-          y[e] = pack_bf16(o.x, o.y);
-        }
-        store_transposed(to, y[0], y[1], y[2], y[3]);
-        __syncwarp();
-        uint4 v;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
-        if (t * 16 < live) *reinterpret_cast<uint4*>(dst + t * 16 * a.ldo_t + k * 16) = v;
-        __syncwarp();
-      }
-      warp_arrive(bar_free(of));
-      return true;
-    };
-    int st = 0, before = 0;
+    int st = 0;
     uint32_t round = 0;
     for (uint32_t g = 0;; ++g) {
       if (!wait(bar_full(st), round & 1, &s_limit)) break;
       const Step& w = s_step[st];
       const int flags = w.flags;
-      const bool end = flags & kEnd;
-      if (!end && (flags & kFirst)) {
+      if (flags & kEnd) break;
+      if (flags & kFirst) {
         const float* src = a.state + (w.in * a.Hv + w.hv) * (D * D) + half * 64 * D + dv;
         const int64_t part_step = static_cast<int64_t>(a.Hv) * kPart;
         const bool slot = w.in >= 0 && (kLocal ? w.seg == 0 : w.seg < 0);
@@ -465,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!kLocal && !end) {
+      if constexpr (!kLocal) {
         if (g > 0 && !wait(bar_q, (g - 1) & 1, &s_limit)) break;   // the parts were read
         tc::tc_fence_after();
 #pragma unroll
@@ -484,8 +465,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tc_fence_before();
         warp_arrive(bar_s);
       }
-      if (!kLocal && g > 0 && !outputs(g - 1, before)) break;
-      if (end) break;
       const float tot = s_tot[st];
       if (!wait(bar_u(g), (g >> 1) & 1, &s_limit)) break;
       tc::tc_fence_after();
@@ -512,8 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i) dst[2 * i * D] = S[i].x, dst[(2 * i + 1) * D] = S[i].y;
         }
       }
-      if constexpr (kLocal) warp_arrive(bar_free(st));
-      before = st;
+      warp_arrive(bar_free(st));
       if (++st == kStages) st = 0, ++round;
     }
   } else if (warp < kStateWarps + 4 || warp >= 16) {
@@ -522,12 +500,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t0 = warp >= 16 ? 32 : 0;
     const uint32_t half = (warp & 2) ? kHalf : 0, first = (warp & 1) * 4;   // of the row's pieces of 8 channels
     const int r8 = lane & 7;
-    int st = 0;
+    // ---- outputs of chunk g (stage `of`): the warp's 32 channels and half of the
+    // tokens, 16 channels by 16 tokens at a time by way of its own shared memory
+    auto outputs = [&](uint32_t g, int of) {
+      const Step& w = s_step[of];
+      if (!wait(bar_o(g), (g >> 1) & 1, &s_limit)) return false;
+      tc::tc_fence_after();
+      const uint32_t turn = scores + 2 * kScores + 3 * kTile + ((warp & 3) + (t0 >> 3)) * kTurn;
+      // where the lane writes a row of its matrix, and reads a piece: rows of 32 bytes, a token's 16 channels
+      const int row_w = ((lane >> 4) << 3) + (lane & 7), row_r = lane >> 1;
+      const uint32_t to = turn + row_w * 32 + ((((lane >> 3) ^ (row_w >> 2)) & 1) << 4);
+      const uint32_t from = turn + row_r * 32 + (((lane ^ (row_r >> 2)) & 1) << 4);
+      const int live = w.live - t0 - row_r;
+      uint16_t* dst = a.out + (w.row + t0 + row_r) * a.ldo_t + w.hv * a.ldo_h + (warp & 3) * 32 + (lane & 1) * 8;
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const int t = i & 1, k = i >> 1;
+        uint32_t o[8], y[4];      // for each 8 tokens: channels c / 4 and c / 4 + 8, tokens 2 (c % 4), + 1
+        tmem_ld_16x256b(t_lane + (16u * k << 16) + kColO + (g & 1) * kChunk + t0 + t * 16, o);
+        const float2 e0 = *reinterpret_cast<const float2*>(&s_out[of][t0 + t * 16 + (lane & 3) * 2]);
+        const float2 e1 = *reinterpret_cast<const float2*>(&s_out[of][t0 + t * 16 + 8 + (lane & 3) * 2]);
+        tc::tmem_wait_ld();
+        if (i == 3) {
+          tc::tc_fence_before();
+          warp_arrive(bar_ofree(g));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 x = mul2(e < 2 ? e0 : e1, make_float2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])));
+          y[e] = pack_bf16(x.x, x.y);
+        }
+        store_transposed(to, y[0], y[1], y[2], y[3]);
+        __syncwarp();
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
+        if (t * 16 < live) *reinterpret_cast<uint4*>(dst + t * 16 * a.ldo_t + k * 16) = v;
+        __syncwarp();
+      }
+      warp_arrive(bar_free(of));
+      return true;
+    };
+    int st = 0, before = 0;
     uint32_t round = 0;
     for (uint32_t g = 0;; ++g) {
       if (!wait(bar_full(st), round & 1, &s_limit)) break;
       const Step& s = s_step[st];
-      if (s.flags & kEnd) break;
+      if (s.flags & kEnd) {
+        if (!kLocal && g > 0) outputs(g - 1, before);
+        break;
+      }
       // Behind the sequence's end lies another, or anything: zeros, the warp's own
       // channels and tokens of V, and as many of K.
       if (s.live < kChunk)
@@ -565,7 +586,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc::fence_proxy_async();
       warp_arrive(bar_v(g));
-      warp_arrive(bar_free(st));
+      if constexpr (kLocal) warp_arrive(bar_free(st));
+      if (!kLocal && g > 0 && !outputs(g - 1, before)) break;
+      before = st;
       if (++st == kStages) st = 0, ++round;
     }
   } else if constexpr (!kLocal) {
@@ -577,7 +600,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t round = 0;
       for (uint32_t g = 0;; ++g) {
         if (!wait(bar_full(st), round & 1, &s_limit) || (s_step[st].flags & kEnd)) break;
-        const float2 gih = make_float2(s_gh[st][i], s_gh[st][i]), gil = make_float2(s_gl[st][i], s_gl[st][i]);
+        const bool deep = s_step[st].flags & kDeep;
+        // (kDeep) what the row's outputs are short of, in two parts
+        const float under = deep ? s_gh[st][i] + kDeepest : 0.0f;
+        const float2 dh = make_float2(fminf(under, 0.0f), fminf(under, 0.0f));
+        const float dl1 = under < 0.0f ? s_gl[st][i] : 0.0f;
         if (!wait(bar_a, g & 1, &s_limit)) break;
         tc::tc_fence_after();
         // 16 columns at a time; rolled: the kinds of warps share the instruction cache
@@ -586,12 +613,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t x[16], hi[8], lo[8];
           tc::tmem_ld16(t_lane + kColA + j0, x);
           float2 w[8];
+          if (!deep) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 gh = *reinterpret_cast<const float2*>(&s_gh[st][j0 + 2 * e]);
-            const float2 gl = *reinterpret_cast<const float2*>(&s_gl[st][j0 + 2 * e]);
-            const float2 d = add2(fma2(gh, make_float2(-1.0f, -1.0f), gih), fma2(gl, make_float2(-1.0f, -1.0f), gil));
-            w[e] = make_float2(ex2(d.x), ex2(d.y));
+            for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const float2*>(&s_in[st][j0 + 2 * e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 gh = *reinterpret_cast<const float2*>(&s_gh[st][j0 + 2 * e]);
+              const float2 gl = *reinterpret_cast<const float2*>(&s_gl[st][j0 + 2 * e]);
+              w[e] = make_float2(ex2((dh.x - gh.x) + (dl1 - gl.x)), ex2((dh.y - gh.y) + (dl1 - gl.y)));
+            }
           }
           tc::tmem_wait_ld();
           const int ahead = i - j0;      // columns that the row sees, less one: the others' scores may be anything

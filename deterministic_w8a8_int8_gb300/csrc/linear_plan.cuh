@@ -74,7 +74,7 @@ __device__ __forceinline__ bool span_of(const LinAttnArgs& a, int64_t s, bool re
   return offsets;
 }
 
-__device__ __forceinline__ float bounded_decay(float g) { return g < kMinDecay ? kMinDecay : g; }
+__device__ __forceinline__ float bounded_decay(float g) { return g < kMinDecay ? kMinDecay : g > 0.0f ? 0.0f : g; }
 __device__ __forceinline__ float decay_of(const LinAttnArgs& a, int64_t token, int h) {
   return bounded_decay(__ldg(a.decay + token * a.ldd_t + h));
 }
@@ -106,11 +106,13 @@ __device__ __forceinline__ Sum join(Sum a, Sum b) {
   return Sum{s, __fadd_rn(e, __fadd_rn(a.l, b.l))};
 }
 
-// The decays of a chunk's 64 tokens, two a lane (0 past the end), summed up:
-// in powers of two up to each token (in two parts), and the factors that these
-// are, that the chunk's end has left of each token, and of the whole chunk.
-// Returns the chunk's sum.  (Sums in binary64 took the warp some 2000 cycles.)
-__device__ __forceinline__ Sum lay_decays(const float (&dec)[2], float* gh, float* gl, float* eg, float* w, float* tot) {
+// The decays of a chunk's 64 tokens, two a lane (0 past the end), summed up to
+// each token and over the chunk, in powers of two.  (In binary64 this took the
+// warp some 2000 cycles.)
+struct Decays {
+  Sum g[2], total;
+};
+__device__ __forceinline__ Decays sum_decays(const float (&dec)[2]) {
   constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596299e-8f;
   const int lane = threadIdx.x & 31;
   Sum d[2];
@@ -125,17 +127,15 @@ __device__ __forceinline__ Sum lay_decays(const float (&dec)[2], float* gh, floa
     const Sum v{__shfl_up_sync(0xffffffffu, sum.h, o), __shfl_up_sync(0xffffffffu, sum.l, o)};
     if (lane >= o) sum = join(sum, v);
   }
-  const Sum total{__shfl_sync(0xffffffffu, sum.h, 31), __shfl_sync(0xffffffffu, sum.l, 31)};
-  const Sum g[2] = {join(sum, Sum{-d[1].h, -d[1].l}), sum};
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    gh[2 * lane + e] = g[e].h;
-    gl[2 * lane + e] = g[e].l;
-    eg[2 * lane + e] = ex2(__fadd_rn(g[e].h, g[e].l));
-    w[2 * lane + e] = ex2(__fadd_rn(__fsub_rn(total.h, g[e].h), __fsub_rn(total.l, g[e].l)));
-  }
-  if (lane == 0) *tot = exp2f(__fadd_rn(total.h, total.l));
-  return total;
+  Decays r;
+  r.total = Sum{__shfl_sync(0xffffffffu, sum.h, 31), __shfl_sync(0xffffffffu, sum.l, 31)};
+  r.g[0] = join(sum, Sum{-d[1].h, -d[1].l});
+  r.g[1] = sum;
+  return r;
+}
+// What the chunk's end has left of a token.
+__device__ __forceinline__ float left_of(const Decays& d, int e) {
+  return ex2(__fadd_rn(__fsub_rn(d.total.h, d.g[e].h), __fsub_rn(d.total.l, d.g[e].l)));
 }
 
 }  // namespace lin

@@ -725,7 +725,7 @@ int prism_glu_quant(const void *gate_up_bf16, int64_t ldx,
  *                 prism_kv_append
  *   log_decay     float32 g: [T, H_v], token stride ldd_t >= H_v, or one for
  *                 each head, [H_v] with ldd_t = 0.  Below -16384 (-inf among
- *                 them: the state is forgotten) counts as -16384.
+ *                 them: the state is forgotten) counts as -16384, above 0 as 0.
  *   state         [num_states, H_v, D_k, D_v] float32, dense, 16-byte aligned
  *   state_in      [S] int32: the slot that a sequence starts from (a branch: its
  *                 parent's, which several may share), -1 or NULL: zeros

@@ -87,7 +87,7 @@ def linear_attention(q, k, v, decay, starts, lens, scale):
     T, hv, dv = v.shape
     rep = hv // q.shape[1]
     q, k, v, decay, starts = (torch.from_numpy(np.ascontiguousarray(x)).double().cuda() for x in (q, k, v, decay, starts))
-    gain = torch.exp(decay.clamp(min=-16384.0)).expand(T, hv)[..., None, None]
+    gain = torch.exp(decay.clamp(-16384.0, 0.0)).expand(T, hv)[..., None, None]
     q, k = (x.repeat_interleave(rep, dim=1) for x in (q, k))
     out, size = torch.zeros((T, hv, dv)).double().cuda(), torch.zeros((T, hv, dv)).double().cuda()
     states, bounds = starts.clone(), torch.zeros_like(starts)
