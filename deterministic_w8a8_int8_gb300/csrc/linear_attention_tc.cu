@@ -21,8 +21,9 @@
 //
 // One CTA an SM walks the items (sequence, head, segment).  Its warps pass chunks
 // on by mbarriers:
-//   producer (1)   finds items, copies Q, K and V of chunks ahead into three stages,
-//                  with the chunk's decays and what is to be done
+//   producer (1)   finds items, copies Q, K and V of chunks ahead into a ring of stages;
+//                  the chunks' decays and what is to be done, in a longer one:
+//                  at most five chunks are in work when one is begun
 //   issuer (1)     U and O of a chunk, A of the next
 //   state (8)      S's two parts; S after the chunk
 //   values (8)     the decayed values' three parts; outputs of the chunk before
@@ -50,14 +51,17 @@ using namespace lin;
 
 constexpr unsigned long long kDrainNs = 2000000000ull;
 constexpr int D = 128;
-constexpr int kStages = 3;
+constexpr int kInfo = 6;             // chunks whose decays and work are held
 constexpr int kStateWarps = 8, kIssuer = 14, kProducer = 15;   // values 8 .. 11, 16 .. 19; scores 12, 13
 constexpr int kThreads = 640;
 constexpr int kStateThreads = kStateWarps * 32;
 constexpr int kTile = kChunk * D * 2, kHalf = kTile / 2;     // of q, k or v: halves of 64 channels
 constexpr int kScores = kChunk * kChunk * 2;
 constexpr int kTurn = 16 * 16 * 2;                           // a warp's turn of outputs
-constexpr int kSmem = kStages * 3 * kTile + 2 * kScores + 3 * kTile + kStateWarps * kTurn + 1024;
+template <bool kLocal>
+constexpr int kStagesOf = kLocal ? 5 : 3;
+template <bool kLocal>
+constexpr int kSmemOf = kStagesOf<kLocal> * (kLocal ? 2 : 3) * kTile + 3 * kTile + (kLocal ? 0 : 2 * kScores + kStateWarps * kTurn) + 1024;
 constexpr int kAhead = 4;                                    // chunks whose decays are held, three on their way
 constexpr int kPart = D * D + 4;                             // floats of a segment's state in the workspace
 // columns of tensor memory
@@ -151,48 +155,42 @@ __device__ __forceinline__ constexpr uint32_t idesc(int n, bool a_along_rows, bo
 template <bool kLocal>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tc_chunk_kernel(const __grid_constant__ LinAttnArgs a, const __grid_constant__ Maps maps, int max_segs) {
+  constexpr int kStages = kStagesOf<kLocal>, kTiles = kLocal ? 2 : 3;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Step s_step[kStages];
-  __shared__ __align__(16) float s_gh[kStages][kChunk], s_gl[kStages][kChunk];   // G, in two parts (kDeep)
+  __shared__ Step s_step[kInfo];
+  __shared__ __align__(16) float s_gh[kInfo][kChunk], s_gl[kInfo][kChunk];   // G, in two parts (kDeep)
   // 2^G times the scale, 2^-G, 2^{G_C - G}
-  __shared__ __align__(16) float s_out[kStages][kChunk], s_in[kStages][kChunk], s_w[kStages][kChunk];
+  __shared__ __align__(16) float s_out[kInfo][kChunk], s_in[kInfo][kChunk], s_w[kInfo][kChunk];
   __shared__ __align__(8) float s_dec[kAhead][kChunk];
-  __shared__ float s_tot[kStages];
-  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 14];
+  __shared__ float s_tot[kInfo];
+  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 12];
   __shared__ uint32_t s_tmem;
   __shared__ Limit s_limit;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(smem);
-  auto tile_q = [&](int st) { return base + st * 3 * kTile; };
-  auto tile_k = [&](int st) { return base + st * 3 * kTile + kTile; };
-  auto tile_v = [&](int st) { return base + st * 3 * kTile + 2 * kTile; };
-  const uint32_t scores = base + kStages * 3 * kTile;       // high parts, then low ones
-  // the decayed values, [128 channels][64 tokens] a part; kLocal: two of them in turn, the
-  // second where Q would lie
-  auto values = [&](uint32_t g, int part) { return kLocal && (g & 1) ? tile_q(part) : scores + 2 * kScores + part * kTile; };
+  auto tile_k = [&](int st) { return base + st * kTiles * kTile; };
+  auto tile_v = [&](int st) { return base + st * kTiles * kTile + kTile; };
+  auto tile_q = [&](int st) { return base + st * kTiles * kTile + 2 * kTile; };
+  auto values = [&](int part) { return base + (kStages * kTiles + part) * kTile; };   // [128 channels][64 tokens] a part
+  const uint32_t scores = values(3), turns = scores + 2 * kScores;                    // high parts, then low ones
   const uint32_t bars = smem_u32(s_bar);
   auto bar_full = [&](int st) { return bars + 8 * st; };
   auto bar_free = [&](int st) { return bars + 8 * (kStages + st); };
   const uint32_t bar_a = bars + 16 * kStages, bar_p = bar_a + 8, bar_ufree = bar_a + 16,
-                 bar_s = bar_a + 24, bar_q = bar_a + 32, bar_end = bar_a + 40;
-  // two in turn: kLocal, the values of chunk g wait for U of chunk g - 2 alone, when that of
-  // g - 1 may be formed already, or a warp of them still be at those of g - 1
-  auto bar_u = [&](uint32_t g) { return bar_a + 48 + 8 * (g & 1); };
-  auto bar_v = [&](uint32_t g) { return bar_a + 64 + 8 * (g & 1); };
-  auto bar_o = [&](uint32_t g) { return bar_a + 80 + 8 * (g & 1); };
-  auto bar_ofree = [&](uint32_t g) { return bar_a + 96 + 8 * (g & 1); };
+                 bar_s = bar_a + 24, bar_q = bar_a + 32, bar_end = bar_a + 40, bar_u = bar_a + 48, bar_v = bar_a + 56;
+  // two in turn: O of chunk g + 1 may be formed before a warp looks for that of g
+  auto bar_o = [&](uint32_t g) { return bar_a + 64 + 8 * (g & 1); };
+  auto bar_ofree = [&](uint32_t g) { return bar_a + 80 + 8 * (g & 1); };
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(bar_full(i), 2);   // the copies, and what the producer writes itself
-      tc::mbar_init(bar_free(i), 1 + kStateWarps + 8 + (kLocal ? 0 : 2));
+      tc::mbar_init(bar_free(i), 1 + 8);
     }
     tc::mbar_init(bar_a, 1);
     tc::mbar_init(bar_p, 2);
-    tc::mbar_init(bar_v(0), 8);
-    tc::mbar_init(bar_v(1), 8);
-    tc::mbar_init(bar_u(0), 1);
-    tc::mbar_init(bar_u(1), 1);
+    tc::mbar_init(bar_v, 8);
+    tc::mbar_init(bar_u, 1);
     tc::mbar_init(bar_ufree, kStateWarps);
     tc::mbar_init(bar_s, kStateWarps);
     tc::mbar_init(bar_q, 1);
@@ -227,10 +225,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ============================ producer ================================
     const int64_t per_seq = static_cast<int64_t>(max_segs) * a.Hv, total = a.S * per_seq;
     bool ok = true;
-    int st = 0;
+    int st = 0, in_slot = 0;
     uint32_t round = 0, issued = 0;
     auto turn = [&] {
       ++issued;
+      if (++in_slot == kInfo) in_slot = 0;
       if (++st == kStages) st = 0, ++round;
     };
     for (int64_t at = blockIdx.x; ok && at < total; at += 32 * static_cast<int64_t>(gridDim.x)) {
@@ -305,15 +304,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int i = 2 * lane + e;
             const float G = __fadd_rn(d.g[e].h, d.g[e].l);
             if constexpr (!kLocal) {
-              s_out[st][i] = ex2(fmaxf(G, -kDeepest)) * a.scale;
-              s_in[st][i] = ex2(fminf(-G, kDeepest));
-              if (deep) s_gh[st][i] = d.g[e].h, s_gl[st][i] = d.g[e].l;
+              s_out[in_slot][i] = ex2(fmaxf(G, -kDeepest)) * a.scale;
+              s_in[in_slot][i] = ex2(fminf(-G, kDeepest));
+              if (deep) s_gh[in_slot][i] = d.g[e].h, s_gl[in_slot][i] = d.g[e].l;
             }
-            s_w[st][i] = left_of(d, e);
+            s_w[in_slot][i] = left_of(d, e);
           }
-          if (lane == 0) s_tot[st] = exp2f(__fadd_rn(d.total.h, d.total.l));
+          if (lane == 0) s_tot[in_slot] = exp2f(__fadd_rn(d.total.h, d.total.l));
           if (lane == 0) {
-            Step& w = s_step[st];
+            Step& w = s_step[in_slot];
             w.row = row;
             w.live = static_cast<int>(min(static_cast<int64_t>(kChunk), t1 - t0 - static_cast<int64_t>(c) * kChunk));
             w.hv = h;
@@ -331,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok && wait(bar_free(st), (round & 1) ^ 1u, &s_limit)) {
       if (lane == 0) {
-        s_step[st].flags = kEnd;
+        s_step[in_slot].flags = kEnd;
         tc::mbar_arrive(bar_full(st));
         tc::mbar_arrive(bar_full(st));
       }
@@ -342,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kIssuer) {
     // ============================ issuer ==================================
     const bool lead = elect_one();
-    int st = 0;
+    int st = 0, info = 0;
     uint32_t round = 0;
     bool more = wait(bar_full(0), 0, &s_limit) && !(s_step[0].flags & kEnd);
     auto issue_scores = [&] {
@@ -358,19 +357,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (!kLocal && more) issue_scores();
     for (uint32_t g = 0; more; ++g) {
-      if (!wait(bar_v(g), (g >> 1) & 1, &s_limit)) break;
+      if (!wait(bar_v, g & 1, &s_limit)) break;
       if (g > 0 && !wait(bar_ufree, (g - 1) & 1, &s_limit)) break;
       tc::tc_fence_after();
       if (lead) {
         const uint64_t kd = desc_along_rows(tile_k(st));
 #pragma unroll 1
         for (int part = 2; part >= 0; --part) {   // the small parts first
-          const uint64_t vd = tc::smem_desc_sw128(values(g, part));
+          const uint64_t vd = tc::smem_desc_sw128(values(part));
 #pragma unroll
           for (int k = 0; k < kChunk / 16; ++k)
             tc::tc_mma(tmem + kColU, vd + 2 * k, kd + k * (16 * 128 >> 4), idesc(D, false, true), part != 2 || k != 0 ? 1u : 0u);
         }
-        if (g != 0 || *static_cast<volatile int*>(&g_lin_withhold) == 0) tc::tc_commit(bar_u(g));
+        if (g != 0 || *static_cast<volatile int*>(&g_lin_withhold) == 0) tc::tc_commit(bar_u);
       }
       __syncwarp();
       if constexpr (!kLocal) {
@@ -405,18 +404,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lead) tc::tc_commit(bar_free(st));
       __syncwarp();
       if (++st == kStages) st = 0, ++round;
-      more = wait(bar_full(st), round & 1, &s_limit) && !(s_step[st].flags & kEnd);
+      if (++info == kInfo) info = 0;
+      more = wait(bar_full(st), round & 1, &s_limit) && !(s_step[info].flags & kEnd);
       if (!kLocal && more) issue_scores();   // A was read: w A of this chunk was waited for
     }
   } else if (warp < kStateWarps) {
     // ============================ state ===================================
     const int half = warp >> 2, dv = (warp & 3) * 32 + lane;
     float2 S[32];      // key channels 64 half + 2 i, + 1
-    int st = 0;
+    int st = 0, info = 0;
     uint32_t round = 0;
     for (uint32_t g = 0;; ++g) {
       if (!wait(bar_full(st), round & 1, &s_limit)) break;
-      const Step& w = s_step[st];
+      const Step& w = s_step[info];
       const int flags = w.flags;
       if (flags & kEnd) break;
       if (flags & kFirst) {
@@ -465,8 +465,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tc_fence_before();
         warp_arrive(bar_s);
       }
-      const float tot = s_tot[st];
-      if (!wait(bar_u(g), (g >> 1) & 1, &s_limit)) break;
+      const float tot = s_tot[info], left = w.left;
+      const int64_t last_out = w.out, last_part = w.part;
+      const int hv = w.hv;
+      if (!wait(bar_u, g & 1, &s_limit)) break;
       tc::tc_fence_after();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {   // 16 at a time, by registers
@@ -481,18 +483,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(bar_ufree);
       if (flags & kLast) {
         if constexpr (kLocal) {
-          float* ps = a.ws + w.part + w.out * (static_cast<int64_t>(a.Hv) * kPart);
+          float* ps = a.ws + last_part + last_out * (static_cast<int64_t>(a.Hv) * kPart);
 #pragma unroll
           for (int i = 0; i < 32; ++i) reinterpret_cast<float2*>(ps)[i * kStateThreads + tid] = S[i];
-          if (tid == 0) ps[D * D] = w.left;
-        } else if (w.out >= 0) {
-          float* dst = a.state + (w.out * a.Hv + w.hv) * (D * D) + half * 64 * D + dv;
+          if (tid == 0) ps[D * D] = left;
+        } else if (last_out >= 0) {
+          float* dst = a.state + (last_out * a.Hv + hv) * (D * D) + half * 64 * D + dv;
 #pragma unroll
           for (int i = 0; i < 32; ++i) dst[2 * i * D] = S[i].x, dst[(2 * i + 1) * D] = S[i].y;
         }
       }
-      warp_arrive(bar_free(st));
       if (++st == kStages) st = 0, ++round;
+      if (++info == kInfo) info = 0;
     }
   } else if (warp < kStateWarps + 4 || warp >= 16) {
     // ========================= decayed values ==============================
@@ -500,13 +502,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t0 = warp >= 16 ? 32 : 0;
     const uint32_t half = (warp & 2) ? kHalf : 0, first = (warp & 1) * 4;   // of the row's pieces of 8 channels
     const int r8 = lane & 7;
-    // ---- outputs of chunk g (stage `of`): the warp's 32 channels and half of the
+    // ---- outputs of chunk g (place `of`): the warp's 32 channels and half of the
     // tokens, 16 channels by 16 tokens at a time by way of its own shared memory
     auto outputs = [&](uint32_t g, int of) {
       const Step& w = s_step[of];
       if (!wait(bar_o(g), (g >> 1) & 1, &s_limit)) return false;
       tc::tc_fence_after();
-      const uint32_t turn = scores + 2 * kScores + 3 * kTile + ((warp & 3) + (t0 >> 3)) * kTurn;
+      const uint32_t turn = turns + ((warp & 3) + (t0 >> 3)) * kTurn;
       // where the lane writes a row of its matrix, and reads a piece: rows of 32 bytes, a token's 16 channels
       const int row_w = ((lane >> 4) << 3) + (lane & 7), row_r = lane >> 1;
       const uint32_t to = turn + row_w * 32 + ((((lane >> 3) ^ (row_w >> 2)) & 1) << 4);
@@ -537,14 +539,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t * 16 < live) *reinterpret_cast<uint4*>(dst + t * 16 * a.ldo_t + k * 16) = v;
         __syncwarp();
       }
-      warp_arrive(bar_free(of));
       return true;
     };
-    int st = 0, before = 0;
+    int st = 0, info = 0, before = 0;
     uint32_t round = 0;
     for (uint32_t g = 0;; ++g) {
       if (!wait(bar_full(st), round & 1, &s_limit)) break;
-      const Step& s = s_step[st];
+      const Step& s = s_step[info];
       if (s.flags & kEnd) {
         if (!kLocal && g > 0) outputs(g - 1, before);
         break;
@@ -559,14 +560,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       float2 w[4];                    // of the tokens 8 i + 2 c, + 1, c = lane % 4
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float2*>(&s_w[st][t0 + i * 8 + (lane & 3) * 2]);
-      // their place is free: the parts of the chunk before were read, or (kLocal) of the one before that
-      constexpr uint32_t kBack = kLocal ? 2 : 1;
-      if (g >= kBack && !wait(bar_u(g - kBack), ((g - kBack) >> 1) & 1, &s_limit)) break;
-      // rolled: the kinds of warps share the instruction cache
-#pragma unroll 1
-      for (int p = 0; p < 4; ++p) {
-        uint32_t x[4], hi[4], mid[4], lo[4];
+      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float2*>(&s_w[info][t0 + i * 8 + (lane & 3) * 2]);
+      auto form = [&](int p, uint32_t (&parts)[3][4]) {     // 8 channels
+        uint32_t x[4];
         asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
                      : "r"(tile_v(st) + half + (t0 + lane) * 128 + (((first + p) ^ r8) << 4))
@@ -574,37 +570,55 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float2 y = mul2(make_float2(bf16_lo(x[i]), bf16_hi(x[i])), w[i]);
-          hi[i] = split_bf16(y);
-          mid[i] = split_bf16(y);
-          lo[i] = pack_bf16(y.x, y.y);
+          parts[0][i] = split_bf16(y);
+          parts[1][i] = split_bf16(y);
+          parts[2][i] = pack_bf16(y.x, y.y);
         }
-        const int row = (warp & 3) * 32 + p * 8 + r8;    // channel, for the parts' addresses
-        const uint32_t to = row * 128 + ((((t0 >> 3) + (lane >> 3)) ^ r8) << 4);
-        store_matrices(values(g, 0) + to, hi);
-        store_matrices(values(g, 1) + to, mid);
-        store_matrices(values(g, 2) + to, lo);
+      };
+      auto keep = [&](int p, const uint32_t (&parts)[3][4]) {
+        const uint32_t to = ((warp & 3) * 32 + p * 8 + r8) * 128 + ((((t0 >> 3) + (lane >> 3)) ^ r8) << 4);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) store_matrices(values(k) + to, parts[k]);
+      };
+      if constexpr (kLocal) {      // formed before their place is free
+        uint32_t parts[4][3][4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) form(p, parts[p]);
+        if (g > 0 && !wait(bar_u, (g - 1) & 1, &s_limit)) break;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) keep(p, parts[p]);
+      } else {
+        if (g > 0 && !wait(bar_u, (g - 1) & 1, &s_limit)) break;   // the parts of the chunk before were read
+        // rolled: the kinds of warps share the instruction cache
+#pragma unroll 1
+        for (int p = 0; p < 4; ++p) {
+          uint32_t parts[3][4];
+          form(p, parts);
+          keep(p, parts);
+        }
       }
       tc::fence_proxy_async();
-      warp_arrive(bar_v(g));
-      if constexpr (kLocal) warp_arrive(bar_free(st));
+      warp_arrive(bar_v);
+      warp_arrive(bar_free(st));
       if (!kLocal && g > 0 && !outputs(g - 1, before)) break;
-      before = st;
+      before = info;
       if (++st == kStages) st = 0, ++round;
+      if (++info == kInfo) info = 0;
     }
   } else if constexpr (!kLocal) {
     // ============================ scores ==================================
     // rows 0 .. 31 (warp 12), 32 .. 63 (13)
     if (warp <= 13) {
       const int rows = warp & 1, i = rows * 32 + lane;
-      int st = 0;
+      int st = 0, info = 0;
       uint32_t round = 0;
       for (uint32_t g = 0;; ++g) {
-        if (!wait(bar_full(st), round & 1, &s_limit) || (s_step[st].flags & kEnd)) break;
-        const bool deep = s_step[st].flags & kDeep;
+        if (!wait(bar_full(st), round & 1, &s_limit) || (s_step[info].flags & kEnd)) break;
+        const bool deep = s_step[info].flags & kDeep;
         // (kDeep) what the row's outputs are short of, in two parts
-        const float under = deep ? s_gh[st][i] + kDeepest : 0.0f;
+        const float under = deep ? s_gh[info][i] + kDeepest : 0.0f;
         const float2 dh = make_float2(fminf(under, 0.0f), fminf(under, 0.0f));
-        const float dl1 = under < 0.0f ? s_gl[st][i] : 0.0f;
+        const float dl1 = under < 0.0f ? s_gl[info][i] : 0.0f;
         if (!wait(bar_a, g & 1, &s_limit)) break;
         tc::tc_fence_after();
         // 16 columns at a time; rolled: the kinds of warps share the instruction cache
@@ -615,12 +629,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           float2 w[8];
           if (!deep) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const float2*>(&s_in[st][j0 + 2 * e]);
+            for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const float2*>(&s_in[info][j0 + 2 * e]);
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float2 gh = *reinterpret_cast<const float2*>(&s_gh[st][j0 + 2 * e]);
-              const float2 gl = *reinterpret_cast<const float2*>(&s_gl[st][j0 + 2 * e]);
+              const float2 gh = *reinterpret_cast<const float2*>(&s_gh[info][j0 + 2 * e]);
+              const float2 gl = *reinterpret_cast<const float2*>(&s_gl[info][j0 + 2 * e]);
               w[e] = make_float2(ex2((dh.x - gh.x) + (dl1 - gl.x)), ex2((dh.y - gh.y) + (dl1 - gl.y)));
             }
           }
@@ -648,8 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tc_fence_before();
         tc::fence_proxy_async();
         warp_arrive(bar_p);
-        warp_arrive(bar_free(st));
         if (++st == kStages) st = 0, ++round;
+        if (++info == kInfo) info = 0;
       }
     }
   }
@@ -707,13 +721,13 @@ cudaError_t launch_linear_attention_tc(const LinAttnArgs& a, cudaStream_t stream
   const int segs = static_cast<int>(most_segments(a.max_len, a.seg_cap));
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.S * segs * a.Hv, sm_count()));
   if (segs > 1) {
-    e = ensure_smem_attr(reinterpret_cast<const void*>(linear_tc_chunk_kernel<true>), kSmem);
+    e = ensure_smem_attr(reinterpret_cast<const void*>(linear_tc_chunk_kernel<true>), kSmemOf<true>);
     if (e == cudaSuccess)
-      e = launch_kernel(linear_tc_chunk_kernel<true>, dim3(grid), dim3(kThreads), kSmem, stream, true, a, maps, segs);
+      e = launch_kernel(linear_tc_chunk_kernel<true>, dim3(grid), dim3(kThreads), kSmemOf<true>, stream, true, a, maps, segs);
   }
-  if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(linear_tc_chunk_kernel<false>), kSmem);
+  if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(linear_tc_chunk_kernel<false>), kSmemOf<false>);
   if (e != cudaSuccess) return e;
-  return launch_kernel(linear_tc_chunk_kernel<false>, dim3(grid), dim3(kThreads), kSmem, stream, true, a, maps, segs);
+  return launch_kernel(linear_tc_chunk_kernel<false>, dim3(grid), dim3(kThreads), kSmemOf<false>, stream, true, a, maps, segs);
 }
 
 cudaError_t read_and_clear_linear_status(uint32_t* out) {
