@@ -61,11 +61,12 @@ constexpr int kTurn = 16 * 16 * 2;                           // a warp's turn of
 template <bool kLocal>
 constexpr int kStagesOf = kLocal ? 5 : 3;
 template <bool kLocal>
-constexpr int kSmemOf = kStagesOf<kLocal> * (kLocal ? 2 : 3) * kTile + 3 * kTile + (kLocal ? 0 : 2 * kScores + kStateWarps * kTurn) + 1024;
+constexpr int kSmemOf = kStagesOf<kLocal> * (kLocal ? 2 : 3) * kTile + (kLocal ? 0 : 3 * kTile + 2 * kScores + kStateWarps * kTurn) + 1024;
 constexpr int kAhead = 4;                                    // chunks whose decays are held, three on their way
 constexpr int kPart = D * D + 4;                             // floats of a segment's state in the workspace
 // columns of tensor memory
 constexpr uint32_t kColU = 0, kColS = 128, kColA = 256, kColO = 320;   // O of two chunks in turn
+constexpr uint32_t kColV = 128;      // kLocal: the decayed values, of two chunks in turn
 
 constexpr float kDeepest = 80.0f;
 enum { kFirst = 1, kLast = 2, kEnd = 4, kDeep = 8 };
@@ -122,6 +123,11 @@ __device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[8]
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
+// 16 lanes by 16 columns in such fragments, lanes 0 .. 7 and 8 .. 15: lane c / 4, column c % 4 of each four.
+__device__ __forceinline__ void tmem_st_16x128b(uint32_t taddr, const uint32_t (&a)[4], const uint32_t (&b)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(a[0]), "r"(b[0]),
+               "r"(a[1]), "r"(b[1]), "r"(a[2]), "r"(b[2]), "r"(a[3]), "r"(b[3]));
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
@@ -163,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(16) float s_out[kInfo][kChunk], s_in[kInfo][kChunk], s_w[kInfo][kChunk];
   __shared__ __align__(8) float s_dec[kAhead][kChunk];
   __shared__ float s_tot[kInfo];
-  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 12];
+  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 14];
   __shared__ uint32_t s_tmem;
   __shared__ Limit s_limit;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -178,8 +184,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar_full = [&](int st) { return bars + 8 * st; };
   auto bar_free = [&](int st) { return bars + 8 * (kStages + st); };
   const uint32_t bar_a = bars + 16 * kStages, bar_p = bar_a + 8, bar_ufree = bar_a + 16,
-                 bar_s = bar_a + 24, bar_q = bar_a + 32, bar_end = bar_a + 40, bar_u = bar_a + 48, bar_v = bar_a + 56;
-  // two in turn: O of chunk g + 1 may be formed before a warp looks for that of g
+                 bar_s = bar_a + 24, bar_q = bar_a + 32, bar_end = bar_a + 40;
+  auto bar_u = [&](uint32_t g) { return bar_a + 48 + 8 * (g & 1); };
+  auto bar_v = [&](uint32_t g) { return bar_a + 96 + 8 * (g & 1); };
+  // two in turn: O of chunk g + 1 may be formed before a warp looks for that of g; kLocal: U
+  // too, and a warp may have the values of g + 1 when another is still at those of g
   auto bar_o = [&](uint32_t g) { return bar_a + 64 + 8 * (g & 1); };
   auto bar_ofree = [&](uint32_t g) { return bar_a + 80 + 8 * (g & 1); };
   if (tid == 0) {
@@ -189,12 +198,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc::mbar_init(bar_a, 1);
     tc::mbar_init(bar_p, 2);
-    tc::mbar_init(bar_v, 8);
-    tc::mbar_init(bar_u, 1);
     tc::mbar_init(bar_ufree, kStateWarps);
     tc::mbar_init(bar_s, kStateWarps);
     tc::mbar_init(bar_q, 1);
     for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar_u(i), 1);
+      tc::mbar_init(bar_v(i), 8);
       tc::mbar_init(bar_o(i), 1);
       tc::mbar_init(bar_ofree(i), 8);
     }
@@ -357,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (!kLocal && more) issue_scores();
     for (uint32_t g = 0; more; ++g) {
-      if (!wait(bar_v, g & 1, &s_limit)) break;
+      if (!wait(bar_v(g), (g >> 1) & 1, &s_limit)) break;
       if (g > 0 && !wait(bar_ufree, (g - 1) & 1, &s_limit)) break;
       tc::tc_fence_after();
       if (lead) {
@@ -366,10 +375,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int part = 2; part >= 0; --part) {   // the small parts first
           const uint64_t vd = tc::smem_desc_sw128(values(part));
 #pragma unroll
-          for (int k = 0; k < kChunk / 16; ++k)
-            tc::tc_mma(tmem + kColU, vd + 2 * k, kd + k * (16 * 128 >> 4), idesc(D, false, true), part != 2 || k != 0 ? 1u : 0u);
+          for (int k = 0; k < kChunk / 16; ++k) {
+            const uint32_t more_of = part != 2 || k != 0 ? 1u : 0u;
+            if constexpr (kLocal) {
+              tc::tc_mma_ta(tmem + kColU, tmem + kColV + (g & 1) * 96 + part * 32 + k * 8, kd + k * (16 * 128 >> 4),
+                            idesc(D, false, true), more_of);
+            } else {
+              tc::tc_mma(tmem + kColU, vd + 2 * k, kd + k * (16 * 128 >> 4), idesc(D, false, true), more_of);
+            }
+          }
         }
-        if (g != 0 || *static_cast<volatile int*>(&g_lin_withhold) == 0) tc::tc_commit(bar_u);
+        if (g != 0 || *static_cast<volatile int*>(&g_lin_withhold) == 0) tc::tc_commit(bar_u(g));
       }
       __syncwarp();
       if constexpr (!kLocal) {
@@ -468,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float tot = s_tot[info], left = w.left;
       const int64_t last_out = w.out, last_part = w.part;
       const int hv = w.hv;
-      if (!wait(bar_u, g & 1, &s_limit)) break;
+      if (!wait(bar_u(g), (g >> 1) & 1, &s_limit)) break;
       tc::tc_fence_after();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {   // 16 at a time, by registers
@@ -561,7 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2 w[4];                    // of the tokens 8 i + 2 c, + 1, c = lane % 4
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float2*>(&s_w[info][t0 + i * 8 + (lane & 3) * 2]);
-      auto form = [&](int p, uint32_t (&parts)[3][4]) {     // 8 channels
+      // 8 channels of them: lane c / 4 has a channel, c % 4 two tokens of each eight
+      auto form = [&](int p, uint32_t (&parts)[3][4]) {
         uint32_t x[4];
         asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
@@ -575,30 +592,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           parts[2][i] = pack_bf16(y.x, y.y);
         }
       };
-      auto keep = [&](int p, const uint32_t (&parts)[3][4]) {
-        const uint32_t to = ((warp & 3) * 32 + p * 8 + r8) * 128 + ((((t0 >> 3) + (lane >> 3)) ^ r8) << 4);
+      if constexpr (kLocal) {      // in tensor memory, where there is room for two chunks'
+        if (g > 1 && !wait(bar_u(g), ((g - 2) >> 1) & 1, &s_limit)) break;
+        tc::tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 3; ++k) store_matrices(values(k) + to, parts[k]);
-      };
-      if constexpr (kLocal) {      // formed before their place is free
-        uint32_t parts[4][3][4];
+        for (int k = 0; k < 2; ++k) {
+          uint32_t lower[3][4], upper[3][4];
+          form(2 * k, lower);
+          form(2 * k + 1, upper);
 #pragma unroll
-        for (int p = 0; p < 4; ++p) form(p, parts[p]);
-        if (g > 0 && !wait(bar_u, (g - 1) & 1, &s_limit)) break;
-#pragma unroll
-        for (int p = 0; p < 4; ++p) keep(p, parts[p]);
+          for (int i = 0; i < 3; ++i)
+            tmem_st_16x128b(t_lane + (16u * k << 16) + kColV + (g & 1) * 96 + i * 32 + (t0 >> 1), lower[i], upper[i]);
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
       } else {
-        if (g > 0 && !wait(bar_u, (g - 1) & 1, &s_limit)) break;   // the parts of the chunk before were read
+        if (g > 0 && !wait(bar_u(g - 1), ((g - 1) >> 1) & 1, &s_limit)) break;   // the parts of the chunk before were read
         // rolled: the kinds of warps share the instruction cache
 #pragma unroll 1
         for (int p = 0; p < 4; ++p) {
           uint32_t parts[3][4];
           form(p, parts);
-          keep(p, parts);
+          const uint32_t to = ((warp & 3) * 32 + p * 8 + r8) * 128 + ((((t0 >> 3) + (lane >> 3)) ^ r8) << 4);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) store_matrices(values(k) + to, parts[k]);
         }
       }
       tc::fence_proxy_async();
-      warp_arrive(bar_v);
+      warp_arrive(bar_v(g));
       warp_arrive(bar_free(st));
       if (!kLocal && g > 0 && !outputs(g - 1, before)) break;
       before = info;
@@ -622,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(bar_a, g & 1, &s_limit)) break;
         tc::tc_fence_after();
         // 16 columns at a time; rolled: the kinds of warps share the instruction cache
-#pragma unroll 1
+#pragma unroll 2
         for (int j0 = 0; j0 < (rows + 1) * 32; j0 += 16) {
           uint32_t x[16], hi[8], lo[8];
           tc::tmem_ld16(t_lane + kColA + j0, x);
