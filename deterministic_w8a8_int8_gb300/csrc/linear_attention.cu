@@ -33,86 +33,6 @@ namespace {
 
 using namespace lin;
 
-constexpr int kGroups = 8;            // rows of the state are divided among as many groups of threads (few tokens)
-
-// ------------------------------------------------------------- few tokens ---
-// One (sequence, head) and `width` of its columns from c0 on: kGroups groups of
-// threads, group g on rows [g R, (g + 1) R), a thread on 4 columns.  Column sums
-// are added in the order of the rows, whatever the width.
-template <int DK>
-__device__ __forceinline__ void few_tokens(const LinAttnArgs& a, const Span& p, int hv, int c0, int width, float* smem) {
-  constexpr int R = DK / kGroups;
-  float* s_q = smem;                               // [kFewTokens][DK]
-  float* s_k = s_q + kFewTokens * DK;
-  float* s_o = s_k + kFewTokens * DK;              // [2][kGroups][width]
-  const int lanes = width >> 2, tid = threadIdx.x, group = tid / lanes, col = (tid % lanes) * 4;
-  const int n = static_cast<int>(p.n), hk = hv / a.G;
-  const int64_t plane = static_cast<int64_t>(DK) * a.Dv;
-  float4 st[R];
-  if (p.in >= 0 && !p.bad) {
-    const float* src = a.state + (p.in * a.Hv + hv) * plane + static_cast<int64_t>(group * R) * a.Dv + c0 + col;
-#pragma unroll
-    for (int i = 0; i < R; ++i) st[i] = __ldcs(reinterpret_cast<const float4*>(src + static_cast<int64_t>(i) * a.Dv));
-  } else {
-    const float x = p.bad ? __uint_as_float(0x7fc00000u) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < R; ++i) st[i] = make_float4(x, x, x, x);
-  }
-  for (int i = tid; i < n * (DK / 8); i += blockDim.x) {
-    const int t = i / (DK / 8), c = i % (DK / 8) * 8;
-    const uint4 qv = *reinterpret_cast<const uint4*>(a.q + (p.b + t) * a.ldq_t + hk * a.ldq_h + c);
-    const uint4 kv = *reinterpret_cast<const uint4*>(a.k + (p.b + t) * a.ldk_t + hk * a.ldk_h + c);
-    float4* qd = reinterpret_cast<float4*>(s_q + t * DK + c);
-    float4* kd = reinterpret_cast<float4*>(s_k + t * DK + c);
-    qd[0] = make_float4(bf16_lo(qv.x), bf16_hi(qv.x), bf16_lo(qv.y), bf16_hi(qv.y));
-    qd[1] = make_float4(bf16_lo(qv.z), bf16_hi(qv.z), bf16_lo(qv.w), bf16_hi(qv.w));
-    kd[0] = make_float4(bf16_lo(kv.x), bf16_hi(kv.x), bf16_lo(kv.y), bf16_hi(kv.y));
-    kd[1] = make_float4(bf16_lo(kv.z), bf16_hi(kv.z), bf16_lo(kv.w), bf16_hi(kv.w));
-  }
-  __syncthreads();
-  for (int t = 0; t < n; ++t) {
-    const float d = expf(decay_of(a, p.b + t, hv));
-    const uint2 vv = *reinterpret_cast<const uint2*>(a.v + (p.b + t) * a.ldv_t + hv * a.ldv_h + c0 + col);
-    const float4 v = make_float4(bf16_lo(vv.x), bf16_hi(vv.x), bf16_lo(vv.y), bf16_hi(vv.y));
-    const float* q = s_q + t * DK + group * R;
-    const float* k = s_k + t * DK + group * R;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const float ki = k[i], qi = q[i];
-      st[i].x = fmaf(ki, v.x, d * st[i].x);
-      st[i].y = fmaf(ki, v.y, d * st[i].y);
-      st[i].z = fmaf(ki, v.z, d * st[i].z);
-      st[i].w = fmaf(ki, v.w, d * st[i].w);
-      o.x = fmaf(qi, st[i].x, o.x);
-      o.y = fmaf(qi, st[i].y, o.y);
-      o.z = fmaf(qi, st[i].z, o.z);
-      o.w = fmaf(qi, st[i].w, o.w);
-    }
-    float* red = s_o + (t & 1) * kGroups * width;
-    *reinterpret_cast<float4*>(red + group * width + col) = o;
-    __syncthreads();   // the other half was read before the last barrier
-    for (int c = tid; c < width; c += blockDim.x) {
-      float sum = red[c];
-#pragma unroll
-      for (int g = 1; g < kGroups; ++g) sum += red[g * width + c];
-      a.out[(p.b + t) * a.ldo_t + hv * a.ldo_h + c0 + c] = static_cast<uint16_t>(float_to_bf16_rne(sum * a.scale));
-    }
-  }
-  if (p.out >= 0 && !p.bad) {
-    float* dst = a.state + (p.out * a.Hv + hv) * plane + static_cast<int64_t>(group * R) * a.Dv + c0 + col;
-#pragma unroll
-    for (int i = 0; i < R; ++i) __stcs(reinterpret_cast<float4*>(dst + static_cast<int64_t>(i) * a.Dv), st[i]);
-  }
-}
-constexpr int few_smem(int DK, int width) { return (2 * kFewTokens * DK + 2 * kGroups * width) * 4; }
-
-// The rows of a sequence that cannot be answered.
-__device__ __forceinline__ void spoil(const LinAttnArgs& a, const Span& p, int hv, int c0, int width) {
-  for (int64_t i = threadIdx.x; i < p.n * width; i += blockDim.x)
-    a.out[(p.b + i / width) * a.ldo_t + hv * a.ldo_h + c0 + i % width] = static_cast<uint16_t>(kBf16NaN);
-}
-
 // A CTA for each `width` columns of a (sequence, head).
 template <int DK>
 __global__ void __launch_bounds__(256) linear_few_kernel(const __grid_constant__ LinAttnArgs a, int width) {
@@ -122,8 +42,8 @@ __global__ void __launch_bounds__(256) linear_few_kernel(const __grid_constant__
   const int64_t s = blockIdx.x / slices;
   Span p;
   if (span_of(a, s, blockIdx.y == 0 && c0 == 0 && threadIdx.x == 0, p)) {
-    if (p.n > kFewTokens) {   // another kernel's, unless it is malformed
-      if (p.bad) spoil(a, p, blockIdx.y, c0, width);
+    if (p.n > kFewTokens) {   // only where it is malformed
+      spoil(a, p, blockIdx.y, c0, width);
     } else {
       few_tokens<DK>(a, p, blockIdx.y, c0, width, reinterpret_cast<float*>(smem));
     }
@@ -486,8 +406,7 @@ template <int DK, int DV>
 cudaError_t launch_shape(const LinAttnArgs& a, cudaStream_t stream) {
   if (a.max_len <= kFewTokens) return launch_few<DK, DV>(a, stream);
   if constexpr (DK == 128 && DV == 128) {
-    const cudaError_t e = launch_few<DK, DV>(a, stream);
-    return e == cudaSuccess ? launch_linear_attention_tc(a, stream) : e;
+    return launch_linear_attention_tc(a, stream);
   } else {
     using L = Tile<DK, DV>;
     const int segs = static_cast<int>(most_segments(a.max_len, a.seg_cap));

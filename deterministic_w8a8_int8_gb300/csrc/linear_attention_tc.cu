@@ -74,7 +74,7 @@ struct Step {          // a chunk's work
   int64_t row;         // its first token
   int64_t in, out;     // states: of the sequence's start (kFirst); to write to (kLast), -1 for none
   int64_t part;        // of the sequence's first place in the workspace and this head
-  int32_t live, hv, flags, seg;   // seg: segments (places) before it that the state is made of; -1: the state slot
+  int32_t live, hv, flags, seg;   // seg: the place of the state that the segment starts from; -1: the state slot
   float left;          // what the segment leaves of the state before it (kLast)
 };
 
@@ -158,6 +158,37 @@ __device__ __forceinline__ constexpr uint32_t idesc(int n, bool a_along_rows, bo
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
 
+// Sequences of few tokens, and malformed ones, after the chunks: found kThreads at a
+// time, their heads dealt out to the CTAs.
+__device__ void few_sequences(const LinAttnArgs& a, uint8_t* smem, uint32_t (&found)[kThreads / 32]) {
+  const int tid = threadIdx.x;
+  int64_t item = 0;
+  for (int64_t s0 = 0; s0 < a.S; s0 += kThreads) {
+    Span p;
+    const int64_t s = s0 + tid;
+    const bool few = s < a.S && span_of(a, s, blockIdx.x == 0, p) && (p.bad || p.n <= kFewTokens);
+    const uint32_t mask = __ballot_sync(0xffffffffu, few);
+    __syncthreads();
+    if ((tid & 31) == 0) found[tid >> 5] = mask;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w)
+      for (uint32_t rest = found[w]; rest != 0; rest &= rest - 1) {
+        // heads hv with (item + hv) % gridDim.x == blockIdx.x
+        const int64_t first = (static_cast<int64_t>(blockIdx.x) + gridDim.x - item % gridDim.x) % gridDim.x;
+        for (int64_t hv = first; hv < a.Hv; hv += gridDim.x) {
+          span_of(a, s0 + w * 32 + __ffs(rest) - 1, false, p);
+          if (p.n > kFewTokens) {
+            spoil(a, p, static_cast<int>(hv), 0, D);
+          } else {
+            __syncthreads();       // shared memory is free again
+            few_tokens<D>(a, p, static_cast<int>(hv), 0, D, reinterpret_cast<float*>(smem));
+          }
+        }
+        item += a.Hv;
+      }
+  }
+}
+
 template <bool kLocal>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tc_chunk_kernel(const __grid_constant__ LinAttnArgs a, const __grid_constant__ Maps maps, int max_segs) {
@@ -172,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t s_bar[2 * kStages + 14];
   __shared__ uint32_t s_tmem;
   __shared__ Limit s_limit;
+  __shared__ uint32_t s_few[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(smem);
@@ -438,9 +470,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (flags & kFirst) {
         const float* src = a.state + (w.in * a.Hv + w.hv) * (D * D) + half * 64 * D + dv;
         const int64_t part_step = static_cast<int64_t>(a.Hv) * kPart;
+        const float2* place = reinterpret_cast<const float2*>(a.ws + w.part + w.seg * part_step) + tid;
         const bool slot = w.in >= 0 && (kLocal ? w.seg == 0 : w.seg < 0);
+        if (!kLocal && w.seg >= 0) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) S[i] = slot ? make_float2(src[2 * i * D], src[(2 * i + 1) * D]) : make_float2(0.0f, 0.0f);
+          for (int i = 0; i < 32; ++i) S[i] = place[i * kStateThreads];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) S[i] = slot ? make_float2(src[2 * i * D], src[(2 * i + 1) * D]) : make_float2(0.0f, 0.0f);
+        }
         if constexpr (kLocal) {
           // the sequence's start has a place of its own: the last segment may write
           // the state back before another begins
@@ -451,14 +489,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               ps[i * kStateThreads] = S[i];
               S[i] = make_float2(0.0f, 0.0f);
             }
-          }
-        } else {
-          for (int k = 0; k <= w.seg; ++k) {
-            const float* ps = a.ws + w.part + k * part_step;
-            const float left = k == 0 ? 0.0f : ps[D * D];
-            const float2* from = reinterpret_cast<const float2*>(ps) + tid;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) S[i] = fma2(make_float2(left, left), S[i], from[i * kStateThreads]);
           }
         }
       }
@@ -705,6 +735,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   }
+  if constexpr (!kLocal) few_sequences(a, smem, s_few);
+  pdl_trigger();
+}
+
+// The states that the segments start from, place by place: place 0 holds the
+// sequence's, place k + 1 what segment k makes of none.  A CTA for 1024 values.
+constexpr int kScanThreads = 256, kSlices = D * D / (4 * kScanThreads);
+__global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const __grid_constant__ LinAttnArgs a) {
+  pdl_wait();
+  const int64_t s = blockIdx.x / kSlices;
+  const int hv = blockIdx.y;
+  Span p;
+  if (span_of(a, s, false, p) && !p.bad && p.n > kFewTokens) {
+    const int segs = static_cast<int>(segment_count(p.n, a.seg_cap));
+    const int64_t step = static_cast<int64_t>(a.Hv) * kPart;
+    float* place = a.ws + (first_place(p.b) * a.Hv + hv) * kPart;
+    const int at = static_cast<int>(blockIdx.x % kSlices) * 4 * kScanThreads + threadIdx.x * 4;
+    if (segs > 1) {
+      float4 x = *reinterpret_cast<const float4*>(place + at);
+#pragma unroll 4
+      for (int k = 1; k < segs; ++k) {
+        float4* here = reinterpret_cast<float4*>(place + k * step + at);
+        const float left = place[k * step + D * D];
+        const float4 y = *here;
+        x = make_float4(fmaf(left, x.x, y.x), fmaf(left, x.y, y.y), fmaf(left, x.z, y.z), fmaf(left, x.w, y.w));
+        *here = x;
+      }
+    }
+  }
   pdl_trigger();
 }
 
@@ -745,6 +804,8 @@ cudaError_t launch_linear_attention_tc(const LinAttnArgs& a, cudaStream_t stream
     e = ensure_smem_attr(reinterpret_cast<const void*>(linear_tc_chunk_kernel<true>), kSmemOf<true>);
     if (e == cudaSuccess)
       e = launch_kernel(linear_tc_chunk_kernel<true>, dim3(grid), dim3(kThreads), kSmemOf<true>, stream, true, a, maps, segs);
+    if (e == cudaSuccess)
+      e = launch_kernel(linear_scan_kernel, dim3(static_cast<unsigned>(a.S * kSlices), a.Hv), dim3(kScanThreads), 0, stream, true, a);
   }
   if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(linear_tc_chunk_kernel<false>), kSmemOf<false>);
   if (e != cudaSuccess) return e;

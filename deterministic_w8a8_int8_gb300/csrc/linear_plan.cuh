@@ -79,6 +79,90 @@ __device__ __forceinline__ float decay_of(const LinAttnArgs& a, int64_t token, i
   return bounded_decay(__ldg(a.decay + token * a.ldd_t + h));
 }
 
+// ------------------------------------------------------------- few tokens ---
+// One (sequence, head) and `width` of its columns from c0 on: kGroups groups of
+// threads, group g on rows [g R, (g + 1) R), a thread on 4 columns.  Column sums
+// are added in the order of the rows, whatever the width.  All of the CTA's threads
+// take part, those past the groups' (kGroups * width / 4) at the barriers alone.
+constexpr int kGroups = 8;
+template <int DK>
+__device__ __forceinline__ void few_tokens(const LinAttnArgs& a, const Span& p, int hv, int c0, int width, float* smem) {
+  constexpr int R = DK / kGroups;
+  float* s_q = smem;                               // [kFewTokens][DK]
+  float* s_k = s_q + kFewTokens * DK;
+  float* s_o = s_k + kFewTokens * DK;              // [2][kGroups][width]
+  const int lanes = width >> 2, tid = threadIdx.x, group = tid / lanes, col = (tid % lanes) * 4;
+  const bool in = group < kGroups;
+  const int n = static_cast<int>(p.n), hk = hv / a.G;
+  const int64_t plane = static_cast<int64_t>(DK) * a.Dv;
+  float4 st[R];
+  if (p.in >= 0 && !p.bad && in) {
+    const float* src = a.state + (p.in * a.Hv + hv) * plane + static_cast<int64_t>(group * R) * a.Dv + c0 + col;
+#pragma unroll
+    for (int i = 0; i < R; ++i) st[i] = __ldcs(reinterpret_cast<const float4*>(src + static_cast<int64_t>(i) * a.Dv));
+  } else {
+    const float x = p.bad ? __uint_as_float(0x7fc00000u) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) st[i] = make_float4(x, x, x, x);
+  }
+  for (int i = tid; i < n * (DK / 8); i += blockDim.x) {
+    const int t = i / (DK / 8), c = i % (DK / 8) * 8;
+    const uint4 qv = *reinterpret_cast<const uint4*>(a.q + (p.b + t) * a.ldq_t + hk * a.ldq_h + c);
+    const uint4 kv = *reinterpret_cast<const uint4*>(a.k + (p.b + t) * a.ldk_t + hk * a.ldk_h + c);
+    float4* qd = reinterpret_cast<float4*>(s_q + t * DK + c);
+    float4* kd = reinterpret_cast<float4*>(s_k + t * DK + c);
+    qd[0] = make_float4(bf16_lo(qv.x), bf16_hi(qv.x), bf16_lo(qv.y), bf16_hi(qv.y));
+    qd[1] = make_float4(bf16_lo(qv.z), bf16_hi(qv.z), bf16_lo(qv.w), bf16_hi(qv.w));
+    kd[0] = make_float4(bf16_lo(kv.x), bf16_hi(kv.x), bf16_lo(kv.y), bf16_hi(kv.y));
+    kd[1] = make_float4(bf16_lo(kv.z), bf16_hi(kv.z), bf16_lo(kv.w), bf16_hi(kv.w));
+  }
+  __syncthreads();
+  for (int t = 0; t < n; ++t) {
+    const float d = expf(decay_of(a, p.b + t, hv));
+    float* red = s_o + (t & 1) * kGroups * width;
+    if (in) {
+      const uint2 vv = *reinterpret_cast<const uint2*>(a.v + (p.b + t) * a.ldv_t + hv * a.ldv_h + c0 + col);
+      const float4 v = make_float4(bf16_lo(vv.x), bf16_hi(vv.x), bf16_lo(vv.y), bf16_hi(vv.y));
+      const float* q = s_q + t * DK + group * R;
+      const float* k = s_k + t * DK + group * R;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float ki = k[i], qi = q[i];
+        st[i].x = fmaf(ki, v.x, d * st[i].x);
+        st[i].y = fmaf(ki, v.y, d * st[i].y);
+        st[i].z = fmaf(ki, v.z, d * st[i].z);
+        st[i].w = fmaf(ki, v.w, d * st[i].w);
+        o.x = fmaf(qi, st[i].x, o.x);
+        o.y = fmaf(qi, st[i].y, o.y);
+        o.z = fmaf(qi, st[i].z, o.z);
+        o.w = fmaf(qi, st[i].w, o.w);
+      }
+      *reinterpret_cast<float4*>(red + group * width + col) = o;
+    }
+    __syncthreads();   // the other half was read before the last barrier
+    for (int c = tid; c < width; c += blockDim.x) {
+      float sum = red[c];
+#pragma unroll
+      for (int g = 1; g < kGroups; ++g) sum += red[g * width + c];
+      a.out[(p.b + t) * a.ldo_t + hv * a.ldo_h + c0 + c] = static_cast<uint16_t>(float_to_bf16_rne(sum * a.scale));
+    }
+  }
+  if (p.out >= 0 && !p.bad && in) {
+    float* dst = a.state + (p.out * a.Hv + hv) * plane + static_cast<int64_t>(group * R) * a.Dv + c0 + col;
+#pragma unroll
+    for (int i = 0; i < R; ++i) __stcs(reinterpret_cast<float4*>(dst + static_cast<int64_t>(i) * a.Dv), st[i]);
+  }
+}
+constexpr int few_smem(int DK, int width) { return (2 * kFewTokens * DK + 2 * kGroups * width) * 4; }
+
+// The rows of a sequence that cannot be answered.
+__device__ __forceinline__ void spoil(const LinAttnArgs& a, const Span& p, int hv, int c0, int width) {
+  for (int64_t i = threadIdx.x; i < p.n * width; i += blockDim.x)
+    a.out[(p.b + i / width) * a.ldo_t + hv * a.ldo_h + c0 + i % width] = static_cast<uint16_t>(kBf16NaN);
+}
+
+// ----------------------------------------------------------------- chunks ---
 // Two values as a pair of bf16, and what that leaves of them.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
