@@ -65,14 +65,13 @@ struct Squares {
     return join(join(Sum{h.x, l.x}, Sum{h.y, l.y}), Sum{-2.0f * top, 0.0f});
   }
 };
-// The largest magnitude of a vector's values, and of what was there.
-__device__ __forceinline__ __nv_bfloat162 larger(__nv_bfloat162 m, const uint4& v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
-  return m;
+// The largest magnitude of a vector's values, and of what was there: bf16 pairs,
+// whose magnitudes are ordered as their bits are.
+__device__ __forceinline__ uint32_t larger(uint32_t m, const uint4& v) {
+  constexpr uint32_t kMagnitude = 0x7fff7fffu;
+  return __vimax3_u16x2(__vimax3_u16x2(m, v.x & kMagnitude, v.y & kMagnitude), v.z & kMagnitude, v.w & kMagnitude);
 }
-__device__ __forceinline__ float largest(__nv_bfloat162 m) { return fmaxf(__low2float(m), __high2float(m)); }
+__device__ __forceinline__ float largest(uint32_t m) { return fmaxf(bf16_lo(m), bf16_hi(m)); }
 
 // (s / n + eps)^(-1/2): the reciprocal root's approximation and one step of
 // Newton's iteration whose residual is formed from the rounding errors too.
@@ -90,15 +89,14 @@ __device__ __forceinline__ float inverse_root(Sum s, float inv_n, float inv_n_lo
   return __fmaf_rn(__fmul_rn(0.5f, r), d, r);
 }
 
-// n / d rounded to nearest for 1 <= d <= 2: Markstein's quotient (1990).  The
-// reciprocal's approximation and one step of Newton's iteration, and the
-// remainder, which one fused operation forms exactly, put back.  There are 2^16
+// n / d rounded to nearest for d = -minus, 1 <= d <= 2: Markstein's quotient
+// (1990).  The reciprocal's approximation and one step of Newton's iteration, and
+// the remainder, which one fused operation forms exactly, put back.  There are 2^16
 // gates, and the tests compare each one's result.
-__device__ __forceinline__ float2 divide2(float2 n, float2 d) {
+__device__ __forceinline__ float2 divide2(float2 n, float2 minus) {
   float2 r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
-  const float2 minus = mul2(d, twice(-1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(-minus.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(-minus.y));
   r = fma2(fma2(minus, r, twice(1.0f)), r, r);
   const float2 q = mul2(n, r);
   return fma2(fma2(minus, q, n), r, q);
@@ -122,7 +120,7 @@ __device__ __forceinline__ float2 silu2(float2 z) {
   p = fma2(p, r, twice(1.0f));
   const float2 e = mul2(p, make_float2(__uint_as_float(__float_as_uint(t.x) << 23), __uint_as_float(__float_as_uint(t.y) << 23)));
   const float2 top = make_float2(z.x >= 0.0f ? 1.0f : e.x, z.y >= 0.0f ? 1.0f : e.y);
-  return mul2(z, divide2(top, add2(e, twice(1.0f))));
+  return mul2(z, divide2(top, fma2(e, twice(-1.0f), twice(-1.0f))));
 }
 
 __device__ __forceinline__ float2 pair(uint32_t v) { return make_float2(bf16_lo(v), bf16_hi(v)); }
@@ -235,8 +233,11 @@ struct Ahead {
   }
 };
 
+// CTAs of an SM at least, by registers.
+constexpr int ctas_of(int C) { return C <= 5 ? 2 : 1; }
+
 template <int C, bool kDelta>
-__global__ void __launch_bounds__(kMaxTeam) norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __maxnreg__(C <= 4 ? 56 : C <= 6 ? 80 : 128) norm_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Sum s_sum[2][kWarps], s_post[2][kWarps];
   __shared__ uint32_t s_top[2][kWarps];
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(kMaxTeam) norm_kernel(const __grid_constant__ 
       if constexpr (kDelta) d[i] = ad.read(i);
     }
     fill(row + gridDim.x);
-    __nv_bfloat162 m = __floats2bfloat162_rn(0.0f, 0.0f);
+    uint32_t m = 0;
     if constexpr (kDelta) {
       float r = 1.0f;
       if (a.post != nullptr) {
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kMaxTeam) norm_kernel(const __grid_constant__ 
 #pragma unroll
           for (int e = 0; e < 4; ++e) s.add(pair(word(d[i], e)));
         r = inverse_root(team_sum(s.sum(), s_post[par]), a.inv_n, a.inv_n_low, a.eps);
-        m = __floats2bfloat162_rn(0.0f, 0.0f);
+        m = 0;
       }
 #pragma unroll
       for (int i = 0; i < C; ++i) {
@@ -325,9 +326,6 @@ __global__ void __launch_bounds__(kMaxTeam) norm_kernel(const __grid_constant__ 
   }
   cp_async_wait<0>();
 }
-
-// CTAs of an SM at least, by registers.
-constexpr int ctas_of(int C) { return C <= 5 ? 2 : 1; }
 
 // A head's channels lie in D / 8 = `lanes` neighbouring lanes, and the sums of a
 // thread's N vectors belong to N heads: with each exchange the lanes of one half
@@ -394,7 +392,7 @@ __global__ void __maxnreg__(C <= 2 ? 64 : C == 4 ? 80 : 128) head_norm_kernel(co
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const uint4 x = ax.read(g + i);
-        Squares s(largest(larger(__floats2bfloat162_rn(0.0f, 0.0f), x)));
+        Squares s(largest(larger(0u, x)));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           y[g + i][e] = pair(word(x, e));
@@ -475,8 +473,7 @@ constexpr int vectors_of(int64_t K, bool even) {
   return n <= 32 ? 1 : n <= (even ? 2 * kMaxTeam : 64) ? 2 : n <= 4 * kMaxTeam ? 4 : even ? 8 : static_cast<int>((n + kMaxTeam - 1) / kMaxTeam);
 }
 
-// A launch of `operands` rows at a time for each CTA: as many CTAs as the SMs
-// hold, or fewer that have equally many rows each.
+// A launch with as many CTAs as the SMs hold, each with `operands` vectors' rows ahead.
 template <class Args>
 cudaError_t launch_rows(void (*kernel)(const Args), std::atomic<int>* held, const Args& a, int64_t M, int64_t K, int c, int operands,
                         cudaStream_t stream) {
@@ -492,8 +489,8 @@ cudaError_t launch_rows(void (*kernel)(const Args), std::atomic<int>* held, cons
     per_sm = std::max(per_sm, 1);
     held[team / 32].store(per_sm, std::memory_order_relaxed);
   }
-  const int64_t most = static_cast<int64_t>(sm_count()) * per_sm, each = (M + most - 1) / most;
-  return launch_kernel(kernel, dim3(static_cast<unsigned>((M + each - 1) / each)), dim3(team), bytes, stream, true, a);
+  const int64_t most = static_cast<int64_t>(sm_count()) * per_sm;
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(std::min(M, most))), dim3(team), bytes, stream, true, a);
 }
 
 template <class F, int C, class Args>
