@@ -59,6 +59,8 @@ int prism_norm_quant(const void* x_bf16, int64_t ldx, const void* delta_bf16, in
   if (delta_bf16 != nullptr &&
       ((st = check_matrix(delta_bf16, ldd, K)) != PRISM_OK || (st = check_matrix(h_bf16, ldh, K)) != PRISM_OK))
     return st;
+  if (h_bf16 != nullptr && ((h_bf16 == x_bf16 && ldh != ldx) || (h_bf16 == delta_bf16 && ldh != ldd)))
+    return PRISM_ERR_INVALID_ARG;
   a.x = static_cast<const uint16_t*>(x_bf16);
   a.ldx = ldx;
   a.delta = static_cast<const uint16_t*>(delta_bf16);

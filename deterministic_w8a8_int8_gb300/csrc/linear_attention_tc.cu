@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             float2 y = mul2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), w[e]);
-            y = make_float2(2 * e <= ahead ? y.x : 0.0f, 2 * e + 1 <= ahead ? y.y : 0.0f);
+            if (j0 >= rows * 32) y = make_float2(2 * e <= ahead ? y.x : 0.0f, 2 * e + 1 <= ahead ? y.y : 0.0f);
             hi[e] = split_bf16(y);
             lo[e] = pack_bf16(y.x, y.y);
           }

@@ -673,7 +673,7 @@ int prism_token_logprobs(const void *logits, int logits_f32, int64_t ldl,
  * Inputs must be finite, with magnitudes below 2^40.  q 16-byte aligned; rows of
  * bf16 16-byte aligned, their strides multiples of 8; weights 16-byte aligned;
  * 1e-20 <= eps <= 1; 16 <= K <= PRISM_MAX_ROW, K % 16 == 0.  M == 0 enqueues
- * nothing.
+ * nothing.  Outputs overlap no input but where that is said.
  *
  * prism_norm_quant -- the residual stream, its RMS norm, and codes:
  *   h = bf16(x + (alpha * d)), d = delta, or (delta * r(delta)) * post_weight
@@ -681,7 +681,7 @@ int prism_token_logprobs(const void *logits, int logits_f32, int64_t ldl,
  *   delta_bf16    the last block's output [M, K], or NULL: h = x, and h_bf16
  *                 and post_weight must be NULL
  *   h_bf16, ldh   [M, K] out, the stream after the addition; may be x or delta
- *                 itself (the same pointer and stride)
+ *                 itself (the same pointer and stride; no other overlap)
  *   weight        [K] float32: the norm's weight (times prism_quant_act's
  *                 inv_smooth where the linear's input is smoothed)
  *   post_weight   [K] float32: the block's output has a norm of its own; or NULL
@@ -741,11 +741,15 @@ int prism_glu_quant(const void *gate_up_bf16, int64_t ldx,
  *                 PRISM_DEV_ERR_SEQ_RANGE
  *   workspace     prism_linear_attention_workspace_bytes(...) bytes, 256-byte
  *                 aligned, any contents
- * Inputs must be finite (log_decay: not NaN or +inf).  States and sums are binary32; products of the
- * chunked form (more than 16 tokens) enter the tensor cores as sums of two or
- * three bf16 parts, to 2^-17 of a score or a state that is read out and 2^-25 of what
- * is added to a state.  A sequence's results depend on its own tokens and state
- * (and on H_v and how its tokens are divided among calls) only.
+ * Inputs must be finite (log_decay: not NaN or +inf); out overlaps no input.  States
+ * and sums are binary32.  More than 16 tokens of a sequence go by in chunks of 64,
+ * whose products enter the tensor cores as sums of two or three bf16 parts: to 2^-17
+ * of a score or a state that is read out, and 2^-25 of what is added to a state.  With
+ * D_k = D_v = 128 what a chunk's decays leave of the state that it begins with, in
+ * its outputs, counts as 2^-80 of it at least; those heads run on tcgen05, whose
+ * bounded waits report through prism_device_status.
+ * A sequence's results depend on its own tokens and state (and on H_v and how its
+ * tokens are divided among calls) only.
  * A malformed sequence (too many tokens, a state index outside [-1, num_states):
  * PRISM_DEV_ERR_STATE_RANGE) gets NaN rows and writes no state; one with
  * malformed offsets has no rows.
@@ -806,11 +810,13 @@ int prism_device_status(uint32_t *flags);
 /*
  * Diagnostics for the bounded on-chip waits of the tensor-core kernels
  * (prism_w8a8_linear's, prism_w8a8_linear_f16's, prism_kv_attention's for many
- * rows, prism_w4g_linear's for more than 8) on the current device.
+ * rows, prism_w4g_linear's for more than 8, prism_linear_attention's for more
+ * than 16 tokens) on the current device.
  * limit_ns > 0 arms a test mode for the calls that follow: every pipeline
  * wait is limited to limit_ns, and each CTA withholds its first
  * chunk-complete signal (the attention: that its first scores are formed; the
- * 4-bit linear: an arrival for its first weights), so the wait for it cannot
+ * 4-bit linear: an arrival for its first weights; linear attention: that the first
+ * chunk's addition to a state is formed), so the wait for it cannot
  * complete and expires.
  * The kernel then raises PRISM_DEVSTATUS_WAIT_TIMEOUT, lets every copy it
  * started land and every MMA it issued complete, releases its tensor memory

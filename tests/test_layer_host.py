@@ -15,7 +15,7 @@ def L():
 
 
 def norm(L, **kw):
-    d = dict(x=A, ldx=256, delta=A, ldd=256, alpha=1.0, post=None, w=A, eps=1e-6, M=3, K=256, h=A, ldh=256, form=0, q=A, ldq=256, s=A)
+    d = dict(x=A, ldx=256, delta=2 * A, ldd=256, alpha=1.0, post=None, w=A, eps=1e-6, M=3, K=256, h=A, ldh=256, form=0, q=A, ldq=256, s=A)
     d.update(kw)
     return L.prism_norm_quant(d["x"], d["ldx"], d["delta"], d["ldd"], d["alpha"], d["post"], d["w"], d["eps"], d["M"], d["K"],
                               d["h"], d["ldh"], d["form"], d["q"], d["ldq"], d["s"], None)
@@ -55,7 +55,7 @@ CODES = [(dict(q=None), -1), (dict(s=None), -1), (dict(form=2), -1), (dict(form=
     (dict(ldx=248), -1), (dict(ldx=260), -2), (dict(w=None), -1), (dict(w=A + 4), -2), (dict(eps=0.0), -1), (dict(eps=2.0), -1),
     (dict(eps=float("nan")), -1), (dict(alpha=float("nan")), -1), (dict(alpha=float("inf")), -1), (dict(h=None), -1),
     (dict(delta=None), -1), (dict(delta=None, h=None, post=A), -1), (dict(post=A + 8), -2), (dict(ldd=200), -1),
-    (dict(ldh=200), -1), (dict(delta=A + 2), -2), (dict(h=A + 8), -2), (dict(ldh=260), -2)])
+    (dict(ldh=200), -1), (dict(ldh=264), -1), (dict(h=2 * A, ldh=264), -1), (dict(delta=A + 2), -2), (dict(h=A + 8), -2), (dict(ldh=260), -2)])
 def test_norm_refusals(L, kw, status):
     assert norm(L, **kw) == status
 
