@@ -14,7 +14,10 @@
 namespace prism {
 namespace lin {
 
-constexpr int kFewTokens = 16;
+// Tokens that take the recurrence.  40 heads of 128 by 128, 2, 4, 8 and 16 tokens by the
+// recurrence: one sequence 3.8, 4.5, 6.3 and 9.7 us, 64 of them 60, 70, 92 and 136;
+// in chunks 9.3 and 83 whatever the number.
+constexpr int kFewTokens = 8;
 constexpr int kChunk = 64;
 constexpr int kSegChunks = 8;         // chunks of a segment at least
 constexpr int kMaxSegments = 24;
@@ -84,61 +87,72 @@ __device__ __forceinline__ float decay_of(const LinAttnArgs& a, int64_t token, i
 // threads, group g on rows [g R, (g + 1) R), a thread on 4 columns.  Column sums
 // are added in the order of the rows, whatever the width.  All of the CTA's threads
 // take part, those past the groups' (kGroups * width / 4) at the barriers alone.
+// What the tokens bring lies in shared memory before the first.
 constexpr int kGroups = 8;
 template <int DK>
 __device__ __forceinline__ void few_tokens(const LinAttnArgs& a, const Span& p, int hv, int c0, int width, float* smem) {
   constexpr int R = DK / kGroups;
   float* s_q = smem;                               // [kFewTokens][DK]
   float* s_k = s_q + kFewTokens * DK;
-  float* s_o = s_k + kFewTokens * DK;              // [2][kGroups][width]
+  float* s_v = s_k + kFewTokens * DK;              // [kFewTokens][width]
+  float* s_o = s_v + kFewTokens * width;           // [2][kGroups][width]
+  float* s_d = s_o + 2 * kGroups * width;          // [kFewTokens]
   const int lanes = width >> 2, tid = threadIdx.x, group = tid / lanes, col = (tid % lanes) * 4;
   const bool in = group < kGroups;
   const int n = static_cast<int>(p.n), hk = hv / a.G;
   const int64_t plane = static_cast<int64_t>(DK) * a.Dv;
-  float4 st[R];
+  float2 st[R][2];
   if (p.in >= 0 && !p.bad && in) {
     const float* src = a.state + (p.in * a.Hv + hv) * plane + static_cast<int64_t>(group * R) * a.Dv + c0 + col;
 #pragma unroll
-    for (int i = 0; i < R; ++i) st[i] = __ldcs(reinterpret_cast<const float4*>(src + static_cast<int64_t>(i) * a.Dv));
+    for (int i = 0; i < R; ++i) {
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(src + static_cast<int64_t>(i) * a.Dv));
+      st[i][0] = make_float2(x.x, x.y);
+      st[i][1] = make_float2(x.z, x.w);
+    }
   } else {
     const float x = p.bad ? __uint_as_float(0x7fc00000u) : 0.0f;
 #pragma unroll
-    for (int i = 0; i < R; ++i) st[i] = make_float4(x, x, x, x);
+    for (int i = 0; i < R; ++i) st[i][0] = st[i][1] = make_float2(x, x);
   }
+  auto widen8 = [](float* dst, const uint16_t* src) {
+    const uint4 v = *reinterpret_cast<const uint4*>(src);
+    reinterpret_cast<float4*>(dst)[0] = make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
+    reinterpret_cast<float4*>(dst)[1] = make_float4(bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w));
+  };
   for (int i = tid; i < n * (DK / 8); i += blockDim.x) {
     const int t = i / (DK / 8), c = i % (DK / 8) * 8;
-    const uint4 qv = *reinterpret_cast<const uint4*>(a.q + (p.b + t) * a.ldq_t + hk * a.ldq_h + c);
-    const uint4 kv = *reinterpret_cast<const uint4*>(a.k + (p.b + t) * a.ldk_t + hk * a.ldk_h + c);
-    float4* qd = reinterpret_cast<float4*>(s_q + t * DK + c);
-    float4* kd = reinterpret_cast<float4*>(s_k + t * DK + c);
-    qd[0] = make_float4(bf16_lo(qv.x), bf16_hi(qv.x), bf16_lo(qv.y), bf16_hi(qv.y));
-    qd[1] = make_float4(bf16_lo(qv.z), bf16_hi(qv.z), bf16_lo(qv.w), bf16_hi(qv.w));
-    kd[0] = make_float4(bf16_lo(kv.x), bf16_hi(kv.x), bf16_lo(kv.y), bf16_hi(kv.y));
-    kd[1] = make_float4(bf16_lo(kv.z), bf16_hi(kv.z), bf16_lo(kv.w), bf16_hi(kv.w));
+    widen8(s_q + t * DK + c, a.q + (p.b + t) * a.ldq_t + hk * a.ldq_h + c);
+    widen8(s_k + t * DK + c, a.k + (p.b + t) * a.ldk_t + hk * a.ldk_h + c);
   }
+  for (int i = tid; i < n * (width / 8); i += blockDim.x) {
+    const int t = i / (width / 8), c = i % (width / 8) * 8;
+    widen8(s_v + t * width + c, a.v + (p.b + t) * a.ldv_t + hv * a.ldv_h + c0 + c);
+  }
+  if (tid < n) s_d[tid] = expf(decay_of(a, p.b + tid, hv));
   __syncthreads();
   for (int t = 0; t < n; ++t) {
-    const float d = expf(decay_of(a, p.b + t, hv));
     float* red = s_o + (t & 1) * kGroups * width;
     if (in) {
-      const uint2 vv = *reinterpret_cast<const uint2*>(a.v + (p.b + t) * a.ldv_t + hv * a.ldv_h + c0 + col);
-      const float4 v = make_float4(bf16_lo(vv.x), bf16_hi(vv.x), bf16_lo(vv.y), bf16_hi(vv.y));
-      const float* q = s_q + t * DK + group * R;
-      const float* k = s_k + t * DK + group * R;
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const float2 d = make_float2(s_d[t], s_d[t]);
+      const float4 vv = *reinterpret_cast<const float4*>(s_v + t * width + col);
+      const float2 v[2] = {make_float2(vv.x, vv.y), make_float2(vv.z, vv.w)};
+      float2 o[2] = {};
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const float ki = k[i], qi = q[i];
-        st[i].x = fmaf(ki, v.x, d * st[i].x);
-        st[i].y = fmaf(ki, v.y, d * st[i].y);
-        st[i].z = fmaf(ki, v.z, d * st[i].z);
-        st[i].w = fmaf(ki, v.w, d * st[i].w);
-        o.x = fmaf(qi, st[i].x, o.x);
-        o.y = fmaf(qi, st[i].y, o.y);
-        o.z = fmaf(qi, st[i].z, o.z);
-        o.w = fmaf(qi, st[i].w, o.w);
+      for (int i = 0; i < R; i += 4) {
+        const float4 k4 = *reinterpret_cast<const float4*>(s_k + t * DK + group * R + i);
+        const float4 q4 = *reinterpret_cast<const float4*>(s_q + t * DK + group * R + i);
+        const float ks[4] = {k4.x, k4.y, k4.z, k4.w}, qs[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            float2& x = st[i + e][f];
+            x = fma2(make_float2(ks[e], ks[e]), v[f], mul2(d, x));
+            o[f] = fma2(make_float2(qs[e], qs[e]), x, o[f]);
+          }
       }
-      *reinterpret_cast<float4*>(red + group * width + col) = o;
+      *reinterpret_cast<float4*>(red + group * width + col) = make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
     }
     __syncthreads();   // the other half was read before the last barrier
     for (int c = tid; c < width; c += blockDim.x) {
@@ -151,10 +165,12 @@ __device__ __forceinline__ void few_tokens(const LinAttnArgs& a, const Span& p, 
   if (p.out >= 0 && !p.bad && in) {
     float* dst = a.state + (p.out * a.Hv + hv) * plane + static_cast<int64_t>(group * R) * a.Dv + c0 + col;
 #pragma unroll
-    for (int i = 0; i < R; ++i) __stcs(reinterpret_cast<float4*>(dst + static_cast<int64_t>(i) * a.Dv), st[i]);
+    for (int i = 0; i < R; ++i)
+      __stcs(reinterpret_cast<float4*>(dst + static_cast<int64_t>(i) * a.Dv),
+             make_float4(st[i][0].x, st[i][0].y, st[i][1].x, st[i][1].y));
   }
 }
-constexpr int few_smem(int DK, int width) { return (2 * kFewTokens * DK + 2 * kGroups * width) * 4; }
+constexpr int few_smem(int DK, int width) { return (kFewTokens * (2 * DK + width + 1) + 2 * kGroups * width) * 4; }
 
 // The rows of a sequence that cannot be answered.
 __device__ __forceinline__ void spoil(const LinAttnArgs& a, const Span& p, int hv, int c0, int width) {

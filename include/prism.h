@@ -742,7 +742,7 @@ int prism_glu_quant(const void *gate_up_bf16, int64_t ldx,
  *   workspace     prism_linear_attention_workspace_bytes(...) bytes, 256-byte
  *                 aligned, any contents
  * Inputs must be finite (log_decay: not NaN or +inf); out overlaps no input.  States
- * and sums are binary32.  More than 16 tokens of a sequence go by in chunks of 64,
+ * and sums are binary32.  More than 8 tokens of a sequence go by in chunks of 64,
  * whose products enter the tensor cores as sums of two or three bf16 parts: to 2^-17
  * of a score or a state that is read out, and 2^-25 of what is added to a state.  With
  * D_k = D_v = 128 what a chunk's decays leave of the state that it begins with, in
@@ -811,7 +811,7 @@ int prism_device_status(uint32_t *flags);
  * Diagnostics for the bounded on-chip waits of the tensor-core kernels
  * (prism_w8a8_linear's, prism_w8a8_linear_f16's, prism_kv_attention's for many
  * rows, prism_w4g_linear's for more than 8, prism_linear_attention's for more
- * than 16 tokens) on the current device.
+ * than 8 tokens) on the current device.
  * limit_ns > 0 arms a test mode for the calls that follow: every pipeline
  * wait is limited to limit_ns, and each CTA withholds its first
  * chunk-complete signal (the attention: that its first scores are formed; the

@@ -57,7 +57,7 @@ def check(data, lens, start, got, states, scale=None):
     assert np.all(off <= after_bound), f"state: {np.max(off / after_bound)} of the bound"
 
 
-LENS = [[1], [1, 1, 1], [2, 16, 15], [17], [63, 64, 65], [0, 1, 130, 0, 40, 16], [255, 3, 256, 257], [511], [512], [513, 1], [1100, 1023], [1024], [2600, 17, 1537]]
+LENS = [[1], [1, 1, 1], [2, 8, 7], [9], [2, 16, 15], [17], [63, 64, 65], [0, 1, 130, 0, 40, 16], [255, 3, 256, 257], [511], [512], [513, 1], [1100, 1023], [1024], [2600, 17, 1537]]
 
 
 @pytest.mark.parametrize("lens", LENS, ids=lambda x: "-".join(map(str, x)))
@@ -160,17 +160,17 @@ def test_strides_scale_and_rows_past_the_end(dk):
 
 
 def test_bits_do_not_depend_on_the_batch():
-    lens = [5, 1900, 17, 64, 300, 16, 0, 1]
+    lens = [5, 1900, 17, 64, 300, 8, 0, 1, 9]
     data = make(8, lens, 2, 4, 128, 128)
-    state = dev(np.random.default_rng(5).standard_normal((8, 4, 128, 128)), torch.float32)
-    own = index(list(range(8)))
+    state = dev(np.random.default_rng(5).standard_normal((9, 4, 128, 128)), torch.float32)
+    own = index(list(range(9)))
     all_state = state.clone()
     got = run(data, lens, all_state, own, own)
     at = 0
     for i, n in enumerate(lens):
         alone = state.clone()
         piece = tuple(x[at:at + n] for x in data)
-        for most in {max(n, 1), 16 if n <= 16 else n, 1900}:
+        for most in {max(n, 1), 8 if n <= 8 else n, 1900}:
             alone = state.clone()
             one = run(piece, [n], alone, index([i]), index([i]), max_len=most)
             assert torch.equal(one, got[at:at + n]) and torch.equal(alone[i], all_state[i])
@@ -179,7 +179,7 @@ def test_bits_do_not_depend_on_the_batch():
 
 def test_many_sequences_of_few_tokens():
     """Enough of them that a head is one CTA's, and few, in slices: the same bits."""
-    lens = [1, 3, 16, 0] * 30
+    lens = [1, 3, 8, 0] * 30
     data = make(9, lens, 4, 4, 128, 128)
     state = dev(np.random.default_rng(6).standard_normal((120, 4, 128, 128)), torch.float32)
     own = index(list(range(120)))
