@@ -479,8 +479,8 @@ cudaError_t launch_rows(void (*kernel)(const Args), std::atomic<int>* held, cons
                         cudaStream_t stream) {
   const int team = static_cast<int>(32 * ((K / 8 + 32 * c - 1) / (32 * c)));
   const int bytes = operands * c * team * 16;
-  cudaError_t e = cudaSuccess;
-  if (bytes > 48 * 1024) e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), operands * c * kMaxTeam * 16);
+  cudaError_t e = cudaSuccess;   // 48 KB need no attribute, the kernel's own arrays among them
+  if (bytes > 40 * 1024) e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), operands * c * kMaxTeam * 16);
   if (e != cudaSuccess) return e;
   int per_sm = held[team / 32].load(std::memory_order_relaxed);   // a property of the kernel and its team
   if (per_sm == 0) {

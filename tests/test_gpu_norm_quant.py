@@ -69,6 +69,19 @@ def test_glu(m, f, form):
         check(prism.prism_glu_quant(dev(x), dev(kw.get("inv"), torch.float32), form=form), u.glu(x, **kw), form)
 
 
+def test_rows_at_48_kb_of_shared_memory():
+    """Two operands' rows of 12288 channels ahead, and a kernel's own arrays."""
+    rng = np.random.default_rng(48)
+    x, d, w = normal(rng, (3, 12288), 2.0), normal(rng, (3, 12288)), rng.uniform(0.3, 2.0, 12288).astype(np.float32)
+    y, h = u.norm(x, w, delta=d)
+    q, scale, got_h = prism.prism_norm_quant(dev(x), dev(w, torch.float32), delta=dev(d))
+    check((q, scale), y, "int8")
+    assert np.array_equal(got_h.float().cpu().numpy(), h)
+    check(prism.prism_glu_quant(dev(np.concatenate((x, d), axis=1))), u.glu(np.concatenate((x, d), axis=1)), "int8")
+    x, d, w = x.reshape(3, 96, 128), d.reshape(3, 96, 128), w[:128]
+    check(prism.prism_head_norm_quant(dev(x), dev(w, torch.float32), gate=dev(d)), u.head_norm(x, w, gate=d), "int8")
+
+
 def test_every_gate():
     """silu of every finite bf16 gate of magnitude below 2^40."""
     bits = np.arange(1 << 16, dtype=np.uint32)
