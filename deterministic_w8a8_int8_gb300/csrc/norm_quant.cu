@@ -102,10 +102,9 @@ __device__ __forceinline__ float2 divide2(float2 n, float2 minus) {
   return fma2(fma2(minus, q, n), r, q);
 }
 
-// silu of two values: z / (1 + exp(-z)) as z * ((1 or e) / (1 + e)), e = exp(-|z|)
-// by n ln 2 + r (ln 2 in two parts), the series of e^r to r^7 in fused steps, times
+// 1 / (1 + exp(-z)) of two values as (1 or e) / (1 + e), e = exp(-|z|) by n ln 2 + r (ln 2 in two parts), the series of e^r to r^7 in fused steps, times
 // 2^n.  From |z| = 88 on n would be -127 or less, and 2^n counts as 0.
-__device__ __forceinline__ float2 silu2(float2 z) {
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
   constexpr float kMagic = 12582912.0f + 127.0f;   // 1.5 * 2^23, whose unit is 1, and the exponent's bias
   const float2 x = make_float2(fmaxf(-fabsf(z.x), -88.0f), fmaxf(-fabsf(z.y), -88.0f));
   const float2 t = fma2(x, twice(0x1.715476p+0f), twice(kMagic)), n = add2(t, twice(-kMagic));
@@ -120,7 +119,7 @@ __device__ __forceinline__ float2 silu2(float2 z) {
   p = fma2(p, r, twice(1.0f));
   const float2 e = mul2(p, make_float2(__uint_as_float(__float_as_uint(t.x) << 23), __uint_as_float(__float_as_uint(t.y) << 23)));
   const float2 top = make_float2(z.x >= 0.0f ? 1.0f : e.x, z.y >= 0.0f ? 1.0f : e.y);
-  return mul2(z, divide2(top, fma2(e, twice(-1.0f), twice(-1.0f))));
+  return divide2(top, fma2(e, twice(-1.0f), twice(-1.0f)));
 }
 
 __device__ __forceinline__ float2 pair(uint32_t v) { return make_float2(bf16_lo(v), bf16_hi(v)); }
@@ -129,9 +128,39 @@ __device__ __forceinline__ uint32_t bf16x2(float2 v) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+// z * sigmoid(z), rounded once more.
+__device__ __forceinline__ float2 silu2(uint32_t gates) {
+  const float2 z = pair(gates);
+  return mul2(z, sigmoid2(z));
+}
+// The sigmoids of all gates in shared memory: bf16 values whose magnitudes lie from
+// 2^-25, up to where exp(-|z|) rounds to 1, to 88, from where on it counts as 0.
+// The magnitudes' bits are the places, those with the sign behind the others.
+struct SigmoidTable {
+  static constexpr uint32_t kFirst = 0x3300u, kLast = 0x42b0u, kNegative = 0x4000u;   // bits of 2^-25 and 88; bytes
+  static constexpr int kBytes = 2 * kNegative;
+  static_assert((kLast - kFirst + 1) * 4 <= kNegative, "places of one sign");
+  const uint8_t* at;
+  __device__ __forceinline__ void build(uint8_t* smem) {   // the caller's barrier follows
+    at = smem;
+    for (uint32_t i = threadIdx.x; i <= kLast - kFirst; i += blockDim.x) {
+      const float z = bf16_lo(kFirst + i);
+      const float2 v = sigmoid2(make_float2(z, -z));
+      *reinterpret_cast<float*>(smem + 4 * i) = v.x;
+      *reinterpret_cast<float*>(smem + kNegative + 4 * i) = v.y;
+    }
+  }
+  __device__ __forceinline__ float2 silu2(uint32_t gates) const {
+    const uint32_t m = __vminu2(__vmaxu2(gates & 0x7fff7fffu, kFirst * 0x10001u), kLast * 0x10001u);
+    const uint32_t place = (m + ((gates >> 3) & (kNegative / 4 * 0x10001u)) - kFirst * 0x10001u) << 2;
+    return mul2(pair(gates), make_float2(*reinterpret_cast<const float*>(at + (place & 0xffffu)),
+                                         *reinterpret_cast<const float*>(at + (place >> 16))));
+  }
+};
 // Weights of the four pairs of channels 8 j .. 8 j + 7.
 struct Weights {
   float4 a, b;
+  Weights() = default;
   __device__ __forceinline__ Weights(const float* w, int j)
       : a(__ldg(reinterpret_cast<const float4*>(w) + 2 * j)), b(__ldg(reinterpret_cast<const float4*>(w) + 2 * j + 1)) {}
   __device__ __forceinline__ float2 operator[](int i) const {
@@ -363,22 +392,26 @@ __device__ __forceinline__ void head_roots(const Sum (&t)[N], int lanes, const N
   }
 }
 
-template <int C, bool kGate>
+template <int C, bool kGate, bool kTable>
 __global__ void __maxnreg__(C <= 2 ? 64 : C == 4 ? 80 : 128) head_norm_kernel(const __grid_constant__ NormArgs a) {
   constexpr int N = C < 4 ? C : 4;
   static_assert(C % N == 0, "vectors go by in groups");
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t s_top[2][kWarps];
   pdl_trigger();
+  SigmoidTable table;
+  if constexpr (kTable) table.build(smem);
   pdl_wait();
+  constexpr int kRows = kTable ? SigmoidTable::kBytes : 0;
   const int nvec = static_cast<int>(a.K >> 3), lanes = a.D >> 3;
-  const Ahead ax(smem, 0, C, nvec), az(smem, 1, C, nvec);
+  const Ahead ax(smem + kRows, 0, C, nvec), az(smem + kRows, 1, C, nvec);
   int64_t row = blockIdx.x;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     ax.fill(a.x + row * a.ldx, i);
     if constexpr (kGate) az.fill(a.gate + row * a.ldg, i);
   }
+  if constexpr (kTable) __syncthreads();
   const Weights w(a.weight, threadIdx.x & (lanes - 1));   // a team is whole heads wide, or the row is one turn
   for (int par = 0; row < a.M; row += gridDim.x, par ^= 1) {
     const int64_t next = row + gridDim.x;
@@ -406,14 +439,16 @@ __global__ void __maxnreg__(C <= 2 ? 64 : C == 4 ? 80 : 128) head_norm_kernel(co
       for (int i = 0; i < N; ++i) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[g + i][e] = mul2(mul2(y[g + i][e], twice(r[i])), w[e]);
+        const bool smooth = a.inv_s != nullptr && ax.index(g + i) < nvec;
+        Weights p;
+        if (smooth) p = Weights(a.inv_s, ax.index(g + i));
         if constexpr (kGate) {
           const uint4 z = az.read(g + i);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[g + i][e] = mul2(y[g + i][e], silu2(pair(word(z, e))));
+          for (int e = 0; e < 4; ++e) y[g + i][e] = mul2(y[g + i][e], kTable ? table.silu2(word(z, e)) : silu2(word(z, e)));
           if (next < a.M) az.fill(a.gate + next * a.ldg, g + i);
         }
-        if (a.inv_s != nullptr && ax.index(g + i) < nvec) {
-          const Weights p(a.inv_s, ax.index(g + i));
+        if (smooth) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[g + i][e] = mul2(y[g + i][e], p[e]);
         }
@@ -424,20 +459,24 @@ __global__ void __maxnreg__(C <= 2 ? 64 : C == 4 ? 80 : 128) head_norm_kernel(co
   cp_async_wait<0>();
 }
 
-template <int C>
+template <int C, bool kTable>
 __global__ void __launch_bounds__(kMaxTeam, ctas_of(C)) glu_kernel(const __grid_constant__ GluArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t s_top[2][kWarps];
   pdl_trigger();
+  SigmoidTable table;
+  if constexpr (kTable) table.build(smem);
   pdl_wait();
+  constexpr int kRows = kTable ? SigmoidTable::kBytes : 0;
   const int nvec = static_cast<int>(a.F >> 3);
-  const Ahead ag(smem, 0, C, nvec), au(smem, 1, C, nvec);
+  const Ahead ag(smem + kRows, 0, C, nvec), au(smem + kRows, 1, C, nvec);
   int64_t row = blockIdx.x;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     ag.fill(a.x + row * a.ldx, i);
     au.fill(a.x + row * a.ldx + a.F, i);
   }
+  if constexpr (kTable) __syncthreads();
   for (int par = 0; row < a.M; row += gridDim.x, par ^= 1) {
     const int64_t next = row + gridDim.x;
     float2 y[C][4];
@@ -446,14 +485,16 @@ __global__ void __launch_bounds__(kMaxTeam, ctas_of(C)) glu_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const uint4 g = ag.read(i), u = au.read(i);
+      const bool smooth = a.inv_s != nullptr && ag.index(i) < nvec;
+      Weights p;
+      if (smooth) p = Weights(a.inv_s, ag.index(i));   // on its way beside the sigmoids
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[i][e] = mul2(silu2(pair(word(g, e))), pair(word(u, e)));
+      for (int e = 0; e < 4; ++e) y[i][e] = mul2(kTable ? table.silu2(word(g, e)) : silu2(word(g, e)), pair(word(u, e)));
       if (next < a.M) {
         ag.fill(a.x + next * a.ldx, i);
         au.fill(a.x + next * a.ldx + a.F, i);
       }
-      if (a.inv_s != nullptr && ag.index(i) < nvec) {
-        const Weights p(a.inv_s, ag.index(i));
+      if (smooth) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[i][e] = mul2(y[i][e], p[e]);
       }
@@ -465,22 +506,26 @@ __global__ void __launch_bounds__(kMaxTeam, ctas_of(C)) glu_kernel(const __grid_
 
 // Vectors of 8 values a thread: the fewest of 1, 2, 4 (and 5 to 8, for heads 8) with which
 // one warp holds the row, or else kMaxTeam threads.  Sums cost a thread some 100
-// instructions, which many vectors share; more than 4 cost the SM warps (norm of 2048
-// rows of 5120 with 2, 4 and 5: see DESIGN).  The team follows from the
-// row's length alone, and with it the order of its sums.
+// instructions, which many vectors share (norm of 2048 rows of 5120: 24 us with 2, 19
+// with 4); more than 4 cost the SM warps.  Heads' sums are each thread's own whatever
+// the number, and 2 leave it registers.  The team follows from the row's length alone,
+// and with it the order of its sums.
 constexpr int vectors_of(int64_t K, bool even) {
   const int64_t n = K / 8;
   return n <= 32 ? 1 : n <= (even ? 2 * kMaxTeam : 64) ? 2 : n <= 4 * kMaxTeam ? 4 : even ? 8 : static_cast<int>((n + kMaxTeam - 1) / kMaxTeam);
 }
 
-// A launch with as many CTAs as the SMs hold, each with `operands` vectors' rows ahead.
+constexpr int team_of(int64_t K, int c) { return static_cast<int>(32 * ((K / 8 + 32 * c - 1) / (32 * c))); }
+
+// A launch with as many CTAs as the SMs hold, each with `operands` vectors' rows ahead
+// and `more` bytes of shared memory in front of them.
 template <class Args>
 cudaError_t launch_rows(void (*kernel)(const Args), std::atomic<int>* held, const Args& a, int64_t M, int64_t K, int c, int operands,
-                        cudaStream_t stream) {
-  const int team = static_cast<int>(32 * ((K / 8 + 32 * c - 1) / (32 * c)));
-  const int bytes = operands * c * team * 16;
+                        int more, cudaStream_t stream) {
+  const int team = team_of(K, c);
+  const int bytes = operands * c * team * 16 + more;
   cudaError_t e = cudaSuccess;   // 48 KB need no attribute, the kernel's own arrays among them
-  if (bytes > 40 * 1024) e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), operands * c * kMaxTeam * 16);
+  if (bytes > 40 * 1024) e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), operands * c * kMaxTeam * 16 + more);
   if (e != cudaSuccess) return e;
   int per_sm = held[team / 32].load(std::memory_order_relaxed);   // a property of the kernel and its team
   if (per_sm == 0) {
@@ -493,10 +538,24 @@ cudaError_t launch_rows(void (*kernel)(const Args), std::atomic<int>* held, cons
   return launch_kernel(kernel, dim3(static_cast<unsigned>(std::min(M, most))), dim3(team), bytes, stream, true, a);
 }
 
+// Whether CTAs make themselves a table of sigmoids: it costs each as much as 8034
+// gates, about 1 us behind another kernel, and its shared memory costs an SM CTAs
+// where they are small.  glu without and with it, 304 rows of 8192 behind a copy 5.7
+// and 6.1 us, of 17408 10.0 and 9.7, 2048 rows of 17408 52.9 and 43.4; heads, 304
+// rows of 8192 6.3 and 6.6, 8192 rows of 5120 74 and 57, 1536 rows of 2048 (128
+// threads) 7.5 and 8.1, 4096 of them 15.9 and 14.2.
+inline bool worth_table(int64_t M, int64_t K, int team) {
+  return team >= 128 && M * K >= static_cast<int64_t>(sm_count()) * 32768;
+}
+
 template <class F, int C, class Args>
 cudaError_t launch_c(const Args& a, int64_t M, int64_t K, cudaStream_t stream) {
-  static std::atomic<int> held[kWarps + 1];
-  return launch_rows<Args>(F::template of<C>(), held, a, M, K, C, F::kOperands, stream);
+  static std::atomic<int> held[2][kWarps + 1];
+  if constexpr (F::kSigmoids && C > 1) {
+    if (worth_table(M, K, team_of(K, C)))
+      return launch_rows<Args>(F::template of<C, true>(), held[1], a, M, K, C, F::kOperands, SigmoidTable::kBytes, stream);
+  }
+  return launch_rows<Args>(F::template of<C, false>(), held[0], a, M, K, C, F::kOperands, 0, stream);
 }
 template <class F, class Args>
 cudaError_t launch_any(const Args& a, int64_t M, int64_t K, cudaStream_t stream) {
@@ -515,22 +574,22 @@ static_assert(vectors_of(PRISM_MAX_ROW, false) == 8 && PRISM_MAX_ROW <= 64 * kMa
 template <bool kDelta>
 struct NormKernel {
   static constexpr int kOperands = kDelta ? 2 : 1;
-  static constexpr bool kEven = false;
-  template <int C>
+  static constexpr bool kEven = false, kSigmoids = false;
+  template <int C, bool kTable>
   static auto of() { return norm_kernel<C, kDelta>; }
 };
 template <bool kGate>
 struct HeadKernel {
   static constexpr int kOperands = kGate ? 2 : 1;
-  static constexpr bool kEven = true;
-  template <int C>
-  static auto of() { return head_norm_kernel<C, kGate>; }
+  static constexpr bool kEven = true, kSigmoids = kGate;
+  template <int C, bool kTable>
+  static auto of() { return head_norm_kernel<C, kGate, kTable>; }
 };
 struct GluKernel {
   static constexpr int kOperands = 2;
-  static constexpr bool kEven = false;
-  template <int C>
-  static auto of() { return glu_kernel<C>; }
+  static constexpr bool kEven = false, kSigmoids = true;
+  template <int C, bool kTable>
+  static auto of() { return glu_kernel<C, kTable>; }
 };
 
 }  // namespace

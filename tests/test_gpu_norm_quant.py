@@ -98,6 +98,27 @@ def test_every_gate():
     assert np.all(np.abs(u.silu(z) - exact) <= 2.0 ** -21 * np.abs(exact) + 2.0 ** -86)
 
 
+@pytest.mark.parametrize("k", [2048, 4096])
+def test_every_gate_of_many_rows(k):
+    """The same codes where CTAs look the sigmoids up."""
+    z = (np.arange(1 << 16, dtype=np.uint32) << 16).view(np.float32)
+    z = np.where(np.abs(z) < 2.0 ** 40, z, 0).astype(np.float32).reshape(-1, k)
+    m, rng = z.shape[0], np.random.default_rng(9)
+    times = -(-5200000 // (m * k)) + 1
+    up, x, w = normal(rng, (m, k)), normal(rng, (m, k // 128, 128)), rng.uniform(0.3, 2.0, 128).astype(np.float32)
+    for form in ("bf16", "int8"):
+        few = prism.prism_glu_quant(dev(np.concatenate((z, up), axis=1)), form=form)
+        many = prism.prism_glu_quant(dev(np.tile(np.concatenate((z, up), axis=1), (times, 1))), form=form)
+        check(few, u.glu(np.concatenate((z, up), axis=1)), form)
+        assert torch.equal(many[0], few[0].repeat(times, 1)) and (form == "bf16" or torch.equal(many[1], few[1].repeat(times)))
+        gate = z.reshape(x.shape)
+        few = prism.prism_head_norm_quant(dev(x), dev(w, torch.float32), gate=dev(gate), form=form)
+        many = prism.prism_head_norm_quant(dev(np.tile(x, (times, 1, 1))), dev(w, torch.float32), gate=dev(np.tile(gate, (times, 1, 1))),
+                                           form=form)
+        check(few, u.head_norm(x, w, gate=gate), form)
+        assert torch.equal(many[0], few[0].repeat(times, 1)) and (form == "bf16" or torch.equal(many[1], few[1].repeat(times)))
+
+
 def test_strides_and_in_place():
     rng = np.random.default_rng(5)
     m, k = 19, 272
