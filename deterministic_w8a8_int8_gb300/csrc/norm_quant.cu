@@ -151,8 +151,9 @@ struct SigmoidTable {
     }
   }
   __device__ __forceinline__ float2 silu2(uint32_t gates) const {
-    const uint32_t m = __vminu2(__vmaxu2(gates & 0x7fff7fffu, kFirst * 0x10001u), kLast * 0x10001u);
-    const uint32_t place = (m + ((gates >> 3) & (kNegative / 4 * 0x10001u)) - kFirst * 0x10001u) << 2;
+    // max(min(magnitude - kFirst, kLast - kFirst), 0) of both
+    const uint32_t m = __viaddmin_s16x2_relu(gates & 0x7fff7fffu, (0x10000u - kFirst) * 0x10001u, (kLast - kFirst) * 0x10001u);
+    const uint32_t place = (m | ((gates >> 3) & (kNegative / 4 * 0x10001u))) << 2;
     return mul2(pair(gates), make_float2(*reinterpret_cast<const float*>(at + (place & 0xffffu)),
                                          *reinterpret_cast<const float*>(at + (place >> 16))));
   }
@@ -182,6 +183,12 @@ __device__ __forceinline__ Sum team_sum(Sum s, Sum* red) {
   return s;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float v;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
+  return v;
+}
+
 // The row's values y, 8 C a thread (0 past the row's end), as codes.
 template <int C>
 __device__ __forceinline__ void store_codes(const RowCodes& o, int64_t row, int nvec, const float2 (&y)[C][4], uint32_t* red) {
@@ -200,7 +207,7 @@ __device__ __forceinline__ void store_codes(const RowCodes& o, int64_t row, int 
 #pragma unroll
   for (int i = 0; i < C; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(y[i][e].x), fabsf(y[i][e].y)));
+    for (int e = 0; e < 4; ++e) top = max3(top, fabsf(y[i][e].x), fabsf(y[i][e].y));
   // magnitudes are ordered as their bits are
   const uint32_t wm = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
   if (lane == 0) red[lt >> 5] = wm;
@@ -504,17 +511,22 @@ __global__ void __launch_bounds__(kMaxTeam, ctas_of(C)) glu_kernel(const __grid_
   cp_async_wait<0>();
 }
 
-// Vectors of 8 values a thread: the fewest of 1, 2, 4 (and 5 to 8, for heads 8) with which
-// one warp holds the row, or else kMaxTeam threads.  Sums cost a thread some 100
-// instructions, which many vectors share (norm of 2048 rows of 5120: 24 us with 2, 19
-// with 4); more than 4 cost the SM warps.  Heads' sums are each thread's own whatever
-// the number, and 2 leave it registers.  The team follows from the row's length alone,
-// and with it the order of its sums.
-constexpr int vectors_of(int64_t K, bool even) {
+// Vectors of 8 values a thread.  Sums cost a thread some 100 instructions, which many
+// vectors share (norm of 2048 rows of 5120: 24 us with 2, 19 with 4); more than 4 cost
+// the SM warps, and only rows beyond kMaxTeam threads have them (heads 8, which go by in
+// fours).  A gate's steps fill the time that sums leave: gated heads have 2 vectors up
+// to 8192 channels (8192 rows of 5120: 55.8 us, with 4 56.4; 304 of them 4.1 and 4.8;
+// without a gate 39.2 and 34.0, 3.3 and 2.75).  The team follows from the row's length
+// alone, and with it the order of its sums.
+enum Rows { kNormRows, kHeadRows, kGatedHeadRows };
+constexpr int vectors_of(int64_t K, Rows rows) {
   const int64_t n = K / 8;
-  return n <= 32 ? 1 : n <= (even ? 2 * kMaxTeam : 64) ? 2 : n <= 4 * kMaxTeam ? 4 : even ? 8 : static_cast<int>((n + kMaxTeam - 1) / kMaxTeam);
+  return n <= 32                                            ? 1
+         : n <= (rows == kGatedHeadRows ? 2 * kMaxTeam : 64) ? 2
+         : n <= 4 * kMaxTeam                                 ? 4
+         : rows != kNormRows                                 ? 8
+                                                             : static_cast<int>((n + kMaxTeam - 1) / kMaxTeam);
 }
-
 constexpr int team_of(int64_t K, int c) { return static_cast<int>(32 * ((K / 8 + 32 * c - 1) / (32 * c))); }
 
 // A launch with as many CTAs as the SMs hold, each with `operands` vectors' rows ahead
@@ -559,35 +571,38 @@ cudaError_t launch_c(const Args& a, int64_t M, int64_t K, cudaStream_t stream) {
 }
 template <class F, class Args>
 cudaError_t launch_any(const Args& a, int64_t M, int64_t K, cudaStream_t stream) {
-  switch (vectors_of(K, F::kEven)) {
+  switch (vectors_of(K, F::kRows)) {
     case 1: return launch_c<F, 1>(a, M, K, stream);
     case 2: return launch_c<F, 2>(a, M, K, stream);
     case 4: return launch_c<F, 4>(a, M, K, stream);
-    case 5: return launch_c<F, F::kEven ? 8 : 5>(a, M, K, stream);
-    case 6: return launch_c<F, F::kEven ? 8 : 6>(a, M, K, stream);
-    case 7: return launch_c<F, F::kEven ? 8 : 7>(a, M, K, stream);
+    case 5: return launch_c<F, F::kRows != kNormRows ? 8 : 5>(a, M, K, stream);
+    case 6: return launch_c<F, F::kRows != kNormRows ? 8 : 6>(a, M, K, stream);
+    case 7: return launch_c<F, F::kRows != kNormRows ? 8 : 7>(a, M, K, stream);
     default: return launch_c<F, 8>(a, M, K, stream);
   }
 }
-static_assert(vectors_of(PRISM_MAX_ROW, false) == 8 && PRISM_MAX_ROW <= 64 * kMaxTeam, "the longest row");
+static_assert(vectors_of(PRISM_MAX_ROW, kNormRows) == 8 && PRISM_MAX_ROW <= 64 * kMaxTeam, "the longest row");
 
 template <bool kDelta>
 struct NormKernel {
   static constexpr int kOperands = kDelta ? 2 : 1;
-  static constexpr bool kEven = false, kSigmoids = false;
+  static constexpr Rows kRows = kNormRows;
+  static constexpr bool kSigmoids = false;
   template <int C, bool kTable>
   static auto of() { return norm_kernel<C, kDelta>; }
 };
 template <bool kGate>
 struct HeadKernel {
   static constexpr int kOperands = kGate ? 2 : 1;
-  static constexpr bool kEven = true, kSigmoids = kGate;
+  static constexpr Rows kRows = kGate ? kGatedHeadRows : kHeadRows;
+  static constexpr bool kSigmoids = kGate;
   template <int C, bool kTable>
   static auto of() { return head_norm_kernel<C, kGate, kTable>; }
 };
 struct GluKernel {
   static constexpr int kOperands = 2;
-  static constexpr bool kEven = false, kSigmoids = true;
+  static constexpr Rows kRows = kNormRows;
+  static constexpr bool kSigmoids = true;
   template <int C, bool kTable>
   static auto of() { return glu_kernel<C, kTable>; }
 };
