@@ -108,7 +108,10 @@ bool operand(PyObject* obj, const char* name, at::ScalarType type, int64_t devic
     PyErr_Format(PyExc_ValueError, "%s must be contiguous", name);
     return false;
   }
-  for (int i = 0; i < n; ++i) o->shape[i] = shape[i], o->stride[i] = t->stride(i);
+  for (int i = n - 1; i >= 0; --i) {   // where there is one row its stride says nothing
+    o->shape[i] = shape[i];
+    o->stride[i] = shape[i] != 1 ? t->stride(i) : i + 1 < n ? shape[i + 1] * o->stride[i + 1] : 1;
+  }
   o->ptr = t->data_ptr();
   return true;
 }

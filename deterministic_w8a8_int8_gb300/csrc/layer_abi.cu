@@ -141,6 +141,7 @@ int prism_linear_attention(const void* q_bf16, int64_t ldq_t, int64_t ldq_h, con
   if (!(scale > -3e38f && scale < 3e38f)) return PRISM_ERR_INVALID_ARG;
   if ((D_k != 64 && D_k != 128) || (D_v != 64 && D_v != 128)) return PRISM_ERR_UNSUPPORTED;
   if (S > (1 << 24) || T > kInt31 || H_v > 65535 || num_states > kInt31) return PRISM_ERR_UNSUPPORTED;
+  if (S * H_v > (1 << 28)) return PRISM_ERR_UNSUPPORTED;   // searched for work within the kernels' bounded waits
   if ((state_in != nullptr || state_out != nullptr) && (state == nullptr || num_states == 0)) return PRISM_ERR_INVALID_ARG;
   int st;
   if (T > 0) {   // no token: states are passed on alone

@@ -557,7 +557,7 @@ cudaError_t launch_rows(void (*kernel)(const Args), std::atomic<int>* held, cons
 // rows of 8192 6.3 and 6.6, 8192 rows of 5120 74 and 57, 1536 rows of 2048 (128
 // threads) 7.5 and 8.1, 4096 of them 15.9 and 14.2.
 inline bool worth_table(int64_t M, int64_t K, int team) {
-  return team >= 128 && M * K >= static_cast<int64_t>(sm_count()) * 32768;
+  return team >= 128 && M >= (static_cast<int64_t>(sm_count()) * 32768 + K - 1) / K;
 }
 
 template <class F, int C, class Args>

@@ -753,7 +753,8 @@ int prism_glu_quant(const void *gate_up_bf16, int64_t ldx,
  * A malformed sequence (too many tokens, a state index outside [-1, num_states):
  * PRISM_DEV_ERR_STATE_RANGE) gets NaN rows and writes no state; one with
  * malformed offsets has no rows.
- *   D_k, D_v in {64, 128}; H_v a multiple of H_k, H_v <= 65535.
+ *   D_k, D_v in {64, 128}; H_v a multiple of H_k, H_v <= 65535, S <= 2^24,
+ *   S * H_v <= 2^28; T, num_states < 2^31.
  */
 size_t prism_linear_attention_workspace_bytes(int64_t S, int64_t T,
                                               int64_t max_len, int64_t H_v,

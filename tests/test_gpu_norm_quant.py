@@ -217,6 +217,19 @@ def test_streams_and_graphs():
         assert torch.equal(q2, glu[0]) and torch.equal(s2, glu[1])
 
 
+def test_one_row_of_any_stride():
+    x = torch.randn((4096, 1), device="cuda").to(torch.bfloat16).t()
+    w = torch.rand((4096,), device="cuda") + 0.5
+    assert x.stride() == (1, 1)
+    got, want = prism.prism_norm_quant(x, w, delta=x), prism.prism_norm_quant(x.contiguous(), w, delta=x.contiguous())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    got, want = prism.prism_glu_quant(x), prism.prism_glu_quant(x.clone(memory_format=torch.contiguous_format))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    heads = x.reshape(32, 1, 128).transpose(0, 1)
+    got, want = prism.prism_head_norm_quant(heads, w[:128]), prism.prism_head_norm_quant(x.reshape(1, 32, 128).contiguous(), w[:128])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_empty():
     w = torch.ones(64, device="cuda")
     x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")

@@ -78,7 +78,7 @@ def test_glu_refusals(L, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(S=-1), -1), (dict(T=-1), -1), (dict(max_len=0), -1), (dict(slots=-1), -1), (dict(cu=None), -1), (dict(hk=0), -1),
     (dict(hv=0), -1), (dict(hk=3), -1), (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(dk=96), -3),
-    (dict(dv=256), -3), (dict(S=1 << 25), -3), (dict(T=1 << 31), -3), (dict(hv=1 << 16, ldd=1 << 16), -3),
+    (dict(dv=256), -3), (dict(S=1 << 25), -3), (dict(S=1 << 24, hv=32, ldd=32), -3), (dict(T=1 << 31), -3), (dict(hv=1 << 16, ldd=1 << 16), -3),
     (dict(slots=1 << 31), -3), (dict(state=None), -1), (dict(slots=0), -1), (dict(state=None, si=None), -1), (dict(q=None), -1),
     (dict(k=None), -1), (dict(v=None), -1), (dict(out=None), -1), (dict(g=None), -1), (dict(ldd=3), -1), (dict(ldd=-1), -1),
     (dict(ldq_t=64), -1), (dict(ldk_h=120), -1), (dict(ldv_t=516), -2), (dict(ldo_h=132), -2), (dict(q=A + 8), -2),
