@@ -226,7 +226,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(bar_full(i), 2);   // the copies, and what the producer writes itself
-      tc::mbar_init(bar_free(i), 1 + 8);
+      // the issuer's instructions, the warps of decayed values; kLocal: the state's warps,
+      // which nothing else keeps from missing a stage's whole turn (else bar_s does)
+      tc::mbar_init(bar_free(i), 1 + 8 + (kLocal ? kStateWarps : 0));
     }
     tc::mbar_init(bar_a, 1);
     tc::mbar_init(bar_p, 2);
@@ -467,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Step& w = s_step[info];
       const int flags = w.flags;
       if (flags & kEnd) break;
+      if constexpr (kLocal) warp_arrive(bar_free(st));   // its turn was seen
       if (flags & kFirst) {
         const float* src = a.state + (w.in * a.Hv + w.hv) * (D * D) + half * 64 * D + dv;
         const int64_t part_step = static_cast<int64_t>(a.Hv) * kPart;

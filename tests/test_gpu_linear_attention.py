@@ -258,6 +258,26 @@ def test_streams_graphs_and_given_workspaces():
         assert torch.equal(out, want) and torch.equal(buf, want_state)
 
 
+def test_no_wait_runs_out_beside_other_work():
+    """Long sequences again and again, while copies on another stream take the memory's time."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    q, k, v = (torch.randn((16383, 8, 128), generator=g, device="cuda").to(torch.bfloat16) for _ in range(3))
+    decay = -torch.rand((16383, 8), generator=g, device="cuda") * 0.1
+    state = torch.zeros((2, 8, 128, 128), device="cuda")
+    out_to = torch.zeros((1,), dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 16383], dtype=torch.int32, device="cuda")
+    big, side = torch.empty((1 << 28,), dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+    to = torch.empty_like(big)
+    prism.prism_device_status()
+    first = prism.prism_linear_attention(q, k, v, decay, state, state_out=out_to, cu=cu)
+    for i in range(300):
+        with torch.cuda.stream(side):
+            to.copy_(big)
+        last = prism.prism_linear_attention(q, k, v, decay, state, state_out=out_to, cu=cu)
+    torch.cuda.synchronize()
+    assert prism.prism_device_status() == 0 and torch.equal(first, last)
+
+
 def test_states_without_tokens():
     state = dev(np.random.default_rng(9).standard_normal((3, 2, 64, 64)), torch.float32)
     keep = state.clone()
