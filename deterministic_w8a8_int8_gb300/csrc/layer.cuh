@@ -45,6 +45,14 @@ struct GluArgs {
 };
 cudaError_t launch_glu_quant(const GluArgs& a, cudaStream_t stream);
 
+namespace lin {
+// How long sequences are cut: `most` segments, of 2^shift tokens at least.
+struct Cut {
+  int64_t most;
+  int32_t shift;
+};
+}  // namespace lin
+
 struct LinAttnArgs {
   const uint16_t* q;
   int64_t ldq_t, ldq_h;
@@ -63,7 +71,7 @@ struct LinAttnArgs {
   float scale;
   int64_t S, T, max_len, num_states;
   int32_t Hk, Hv, Dk, Dv, G;   // G: value heads of a key head
-  int64_t seg_cap;         // segments of a sequence at most (set by the launcher)
+  lin::Cut cut;            // how sequences are cut (set by the launcher)
   float* ws;
   uint32_t* err;
 };

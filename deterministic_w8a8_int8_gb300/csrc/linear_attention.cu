@@ -113,8 +113,8 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
     }
     return;
   }
-  const int64_t each = segment_chunks(p.n, a.seg_cap);
-  const int segs = static_cast<int>(segment_count(p.n, a.seg_cap));
+  const int64_t each = segment_chunks(p.n, a.cut);
+  const int segs = static_cast<int>(segment_count(p.n, a.cut));
   if (seg >= segs || (kLocal && seg + 1 == segs)) return;   // nothing comes after the last one
   const int64_t t0 = seg * each * kChunk, t1 = min(p.n, t0 + each * kChunk);
   const int chunks = static_cast<int>((t1 - t0 + kChunk - 1) / kChunk);
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(Tile<DK, DV>::kThreads, 2)
 #pragma unroll
   for (int t = 0; t < NT; ++t) st[t][0] = st[t][1] = st[t][2] = st[t][3] = 0.0f;
   constexpr int64_t kPart = DK * DV + 4;
-  float* part = a.ws + (first_place(p.b) * a.Hv + hv) * kPart;   // of the sequence's first segment
+  float* part = a.ws + (first_place(p.b, a.cut) * a.Hv + hv) * kPart;   // of the sequence's first segment
   const int64_t part_step = a.Hv * kPart;
   const int64_t at = (static_cast<int64_t>(2 * lc)) * DV + warp * 16 + lr;
   auto read_part = [&](const float* ps) {
@@ -409,7 +409,7 @@ cudaError_t launch_shape(const LinAttnArgs& a, cudaStream_t stream) {
     return launch_linear_attention_tc(a, stream);
   } else {
     using L = Tile<DK, DV>;
-    const int segs = static_cast<int>(most_segments(a.max_len, a.seg_cap));
+    const int segs = static_cast<int>(most_segments(a.max_len, a.cut));
     const dim3 grid(static_cast<unsigned>(a.S * segs), a.Hv);
     cudaError_t e = cudaSuccess;
     if (segs > 1) {
@@ -427,13 +427,14 @@ cudaError_t launch_shape(const LinAttnArgs& a, cudaStream_t stream) {
 }  // namespace
 
 size_t linear_attention_workspace_bytes(int64_t T, int64_t max_len, int64_t Hv, int64_t Dk, int64_t Dv) {
-  if (most_segments(max_len, segment_cap(Hv)) <= 1) return 0;
-  return static_cast<size_t>(first_place(T) * Hv * (Dk * Dv + 4)) * 4;
+  const Cut cut = cut_of(Hv, Dk == 128 && Dv == 128);
+  if (most_segments(max_len, cut) <= 1) return 0;
+  return static_cast<size_t>(first_place(T, cut) * Hv * (Dk * Dv + 4)) * 4;
 }
 
 cudaError_t launch_linear_attention(const LinAttnArgs& given, cudaStream_t stream) {
   LinAttnArgs a = given;
-  a.seg_cap = segment_cap(a.Hv);
+  a.cut = cut_of(a.Hv, a.Dk == 128 && a.Dv == 128);
   if (a.Dk == 64) return a.Dv == 64 ? launch_shape<64, 64>(a, stream) : launch_shape<64, 128>(a, stream);
   return a.Dv == 64 ? launch_shape<128, 64>(a, stream) : launch_shape<128, 128>(a, stream);
 }

@@ -289,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         hv = rest - seg * a.Hv;
         mine = span_of(a, s, false, p) && !p.bad && p.n > kFewTokens;
         if (mine) {
-          each = segment_chunks(p.n, a.seg_cap);
-          segs = static_cast<int>(segment_count(p.n, a.seg_cap));
+          each = segment_chunks(p.n, a.cut);
+          segs = static_cast<int>(segment_count(p.n, a.cut));
           mine = seg < (kLocal ? segs - 1 : segs);   // nothing comes after the last one
         }
       }
@@ -319,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0 && in >= 0 && (kLocal ? sg == 0 : sgs == 1))
           asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.state + (in * a.Hv + h) * (D * D)), "r"(D * D * 4) : "memory");
         for (int c = 0; c < kAhead - 1; ++c) copy_decays(c);
+        const int64_t part = (first_place(b, a.cut) * a.Hv + h) * kPart;
         Sum log_total{0.0f, 0.0f};
         for (int c = 0; c < chunks; ++c) {
           ok = wait(bar_free(st), (round & 1) ^ 1u, &s_limit);
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             w.flags = (c == 0 ? kFirst : 0) | (c + 1 == chunks ? kLast : 0) | (deep ? kDeep : 0);
             w.in = in;
             w.out = kLocal ? sg + 1 : sg + 1 == sgs ? out : -1;
-            w.part = (first_place(b) * a.Hv + h) * kPart;
+            w.part = part;
             w.seg = kLocal ? sg : sgs == 1 ? -1 : sg;
             w.left = exp2f(log_total.h + log_total.l);
           }
@@ -751,9 +752,9 @@ __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const __grid_
   const int hv = blockIdx.y;
   Span p;
   if (span_of(a, s, false, p) && !p.bad && p.n > kFewTokens) {
-    const int segs = static_cast<int>(segment_count(p.n, a.seg_cap));
+    const int segs = static_cast<int>(segment_count(p.n, a.cut));
     const int64_t step = static_cast<int64_t>(a.Hv) * kPart;
-    float* place = a.ws + (first_place(p.b) * a.Hv + hv) * kPart;
+    float* place = a.ws + (first_place(p.b, a.cut) * a.Hv + hv) * kPart;
     const int at = static_cast<int>(blockIdx.x % kSlices) * 4 * kScanThreads + threadIdx.x * 4;
     if (segs > 1) {
       float4 x = *reinterpret_cast<const float4*>(place + at);
@@ -801,7 +802,7 @@ cudaError_t launch_linear_attention_tc(const LinAttnArgs& a, cudaStream_t stream
   if (e == cudaSuccess) e = make_map(&maps.k, a.k, a.T, a.Hk, a.ldk_t, a.ldk_h);
   if (e == cudaSuccess) e = make_map(&maps.v, a.v, a.T, a.Hv, a.ldv_t, a.ldv_h);
   if (e != cudaSuccess) return e;
-  const int segs = static_cast<int>(most_segments(a.max_len, a.seg_cap));
+  const int segs = static_cast<int>(most_segments(a.max_len, a.cut));
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.S * segs * a.Hv, sm_count()));
   if (segs > 1) {
     e = ensure_smem_attr(reinterpret_cast<const void*>(linear_tc_chunk_kernel<true>), kSmemOf<true>);

@@ -19,40 +19,53 @@ namespace lin {
 // in chunks 9.3 and 83 whatever the number.
 constexpr int kFewTokens = 8;
 constexpr int kChunk = 64;
-constexpr int kSegChunks = 8;         // chunks of a segment at least
-constexpr int kMaxSegments = 24;
 constexpr float kMinDecay = -16384.0f;   // e^x = 0 from far above it; sums of 64 stay finite
 
-// The segments of a long sequence: those with which its heads fill the SMs in the
-// fewest turns for what each then has to do, kMaxSegments at most (a segment reads
-// the states of those before it).  One where more do not save a third: keys and
-// values are read twice.
-inline int64_t segment_cap(int64_t Hv) {
-  const int64_t most = std::max<int64_t>(8, std::min<int64_t>(kMaxSegments, kSms / Hv));
-  auto turns = [&](int64_t n) { return (n * Hv + kSms - 1) / kSms; };
+// The segments of a long sequence: those with which its heads fill the places for
+// CTAs in the fewest turns for what each then has to do, and one where more do not save
+// a third: keys and values are read twice.  The tcgen05 kernel has a place on an SM, the
+// other more (8191 tokens of 16 heads of 64 by 64: 103 us by one, 64 by two, 81 by three,
+// of 40 heads 153, 153, 177).  One sequence of 32767 tokens, 2 heads of 128 by 128, cut
+// into 24, 48, 76 and 152 at most: 85, 65, 64 and 64 us, of one head 84, 61, 58 and 61.
+// Segments of fewer tokens pay where a few heads leave SMs empty, and cost a batch the
+// work twice.  2048 tokens, in us:
+//   chunks                                  2      4      8
+//   128 by 128, 8 heads, one sequence      27.3   29.8   38.3
+//               four sequences             57.5   50.3
+//               40 heads, one                     56.5   61.3
+//               four                             180.7  161.0
+//   64 by 64, 8 heads, one                 20.9   31.1   53.3
+//             four                         44.3   38.3
+//             40 heads, one                46.1   46.2   67.2
+//             four                        163.1  163.2  176.3
+constexpr int64_t kMaxSegments = 76;
+inline Cut cut_of(int64_t Hv, bool tc) {
+  const int64_t places = tc ? kSms : 2 * kSms, most = std::max<int64_t>(8, std::min<int64_t>(kMaxSegments, places / Hv));
+  auto turns = [&](int64_t n) { return (n * Hv + places - 1) / places; };
   int64_t best = 1;
   for (int64_t n = 2; n <= most; ++n)
     if (turns(n) * best < turns(best) * n) best = n;
-  return turns(best) * 3 <= turns(1) * best * 2 ? best : 1;
+  if (turns(best) * 3 > turns(1) * best * 2) best = 1;
+  return Cut{best, (tc ? 8 : 7) + (best > 8 ? 0 : 1)};
 }
-// Segments that a sequence of n tokens is cut into at most, the chunks of each,
-// and as many as that makes.
-__host__ __device__ __forceinline__ int64_t most_segments(int64_t n, int64_t cap) {
-  const int64_t segs = n / (kSegChunks * kChunk);
-  return segs > cap ? cap : segs < 1 ? 1 : segs;
+// Segments that a sequence of n tokens is cut into at most (short ones do not earn the
+// first kernel: 512 tokens of 8 heads of 128 by 128 in one 23.6, in two 28 us), the chunks
+// of each, and as many as that makes.
+__host__ __device__ __forceinline__ int64_t most_segments(int64_t n, const Cut& cut) {
+  const int64_t segs = n >> cut.shift;
+  return segs < 2 || (segs < 3 && n < 16 * kChunk) ? 1 : segs > cut.most ? cut.most : segs;
 }
-__host__ __device__ __forceinline__ int64_t segment_chunks(int64_t n, int64_t cap) {
-  const int64_t chunks = (n + kChunk - 1) / kChunk, segs = most_segments(n, cap);
+__host__ __device__ __forceinline__ int64_t segment_chunks(int64_t n, const Cut& cut) {
+  const int64_t chunks = (n + kChunk - 1) / kChunk, segs = most_segments(n, cut);
   return (chunks + segs - 1) / segs;
 }
-__host__ __device__ __forceinline__ int64_t segment_count(int64_t n, int64_t cap) {
-  const int64_t chunks = (n + kChunk - 1) / kChunk, each = segment_chunks(n, cap);
+__host__ __device__ __forceinline__ int64_t segment_count(int64_t n, const Cut& cut) {
+  const int64_t chunks = (n + kChunk - 1) / kChunk, each = segment_chunks(n, cut);
   return (chunks + each - 1) / each;
 }
 // A sequence in segments has a place in the workspace for each but the last, and
-// one for the state that it starts from: no more than whole lengths of
-// kSegChunks chunks among its tokens.
-__host__ __device__ __forceinline__ int64_t first_place(int64_t first_token) { return first_token / (kSegChunks * kChunk); }
+// one for the state that it starts from: no more than 2^shift go into its tokens.
+__host__ __device__ __forceinline__ int64_t first_place(int64_t first_token, const Cut& cut) { return first_token >> cut.shift; }
 
 struct Span {
   int64_t b, n;
