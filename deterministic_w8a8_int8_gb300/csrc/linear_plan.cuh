@@ -48,12 +48,12 @@ inline Cut cut_of(int64_t Hv, bool tc) {
   if (turns(best) * 3 > turns(1) * best * 2) best = 1;
   return Cut{best, (tc ? 8 : 7) + (best > 8 ? 0 : 1)};
 }
-// Segments that a sequence of n tokens is cut into at most (short ones do not earn the
-// first kernel: 512 tokens of 8 heads of 128 by 128 in one 23.6, in two 28 us), the chunks
-// of each, and as many as that makes.
+// Segments that a sequence of n tokens is cut into at most (two as short as may be do not
+// earn the first kernel: 512 tokens of 8 heads of 128 by 128 in one 23.6, in two 28 us, 1024
+// of 40 heads 40.1 and 41.4), the chunks of each, and as many as that makes.
 __host__ __device__ __forceinline__ int64_t most_segments(int64_t n, const Cut& cut) {
   const int64_t segs = n >> cut.shift;
-  return segs < 2 || (segs < 3 && n < 16 * kChunk) ? 1 : segs > cut.most ? cut.most : segs;
+  return segs < 3 ? 1 : segs > cut.most ? cut.most : segs;
 }
 __host__ __device__ __forceinline__ int64_t segment_chunks(int64_t n, const Cut& cut) {
   const int64_t chunks = (n + kChunk - 1) / kChunk, segs = most_segments(n, cut);

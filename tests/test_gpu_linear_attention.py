@@ -57,7 +57,7 @@ def check(data, lens, start, got, states, scale=None):
     assert np.all(off <= after_bound), f"state: {np.max(off / after_bound)} of the bound"
 
 
-LENS = [[1], [1, 1, 1], [2, 8, 7], [9], [2, 16, 15], [17], [63, 64, 65], [0, 1, 130, 0, 40, 16], [255, 3, 256, 257], [511], [512], [513, 1], [1100, 1023], [1024], [2600, 17, 1537]]
+LENS = [[1], [1, 1, 1], [2, 8, 7], [9], [2, 16, 15], [17], [63, 64, 65], [0, 1, 130, 0, 40, 16], [255, 3, 256, 257], [511], [512], [513, 1], [1100, 1023], [1024], [2600, 17, 1537], [1536], [384, 768, 767]]
 
 
 @pytest.mark.parametrize("lens", LENS, ids=lambda x: "-".join(map(str, x)))

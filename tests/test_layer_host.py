@@ -95,12 +95,14 @@ def test_nothing_to_do(L):
 def test_workspace(L):
     """None for calls that are not cut into segments; else a place of states for each 512 tokens at most."""
     f = L.prism_linear_attention_workspace_bytes
-    assert f(64, 64, 1, 40, 128, 128) == 0 and f(1, 1023, 1023, 40, 128, 128) == 0 and f(0, 0, 1, 40, 128, 128) == 0
-    assert f(1, 1024, 1024, 40, 128, 96) == 0
+    assert f(64, 64, 1, 40, 128, 128) == 0 and f(1, 1535, 1535, 40, 128, 128) == 0 and f(0, 0, 1, 40, 128, 128) == 0
+    assert f(1, 1536, 1536, 40, 128, 96) == 0
     one = 40 * (128 * 128 + 4) * 4
-    assert f(1, 1024, 1024, 40, 128, 128) == 2 * one
+    assert f(1, 1536, 1536, 40, 128, 128) == 3 * one
     assert f(3, 8191, 8191, 40, 128, 128) <= 16 * one
     assert f(1, 1 << 20, 1 << 20, 400, 128, 128) == 0     # heads enough
+    assert f(1, 767, 767, 8, 128, 128) == 0 and f(1, 768, 768, 8, 128, 128) == 3 * 8 * (128 * 128 + 4) * 4
+    assert f(1, 383, 383, 8, 64, 64) == 0 and f(1, 384, 384, 8, 64, 64) == 3 * 8 * (64 * 64 + 4) * 4
 
 
 @pytest.mark.parametrize("call,text", [
