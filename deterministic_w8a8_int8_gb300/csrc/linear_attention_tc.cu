@@ -1,8 +1,20 @@
-// linear_attention_tc.cu -- the chunked form of linear attention on the tcgen05
-// tensor cores, for heads of 128 by 128 channels.
+// linear_attention_tc.cu -- the chunked form of linear attention (linear_attention.cu)
+// on the tcgen05 tensor cores.  With G_i the sum of a chunk's decays up to token i,
+// w_ij = e^{G_i - G_j} and S the state that enters,
+//   o_i = scale * (e^{G_i} q_i S + sum_{j <= i} w_ij (q_i . k_j) v_j)
+//   S   = e^{G_C} S + sum_j e^{G_C - G_j} k_j v_j^T
+// What is not bf16 already is split into bf16 parts: scores and the state where it is
+// read out into two (2^-17 of the value), the decayed values of the update into three
+// (2^-25), so that states are as good as binary32 sums.  Sums of decays are kept as two
+// binary32 numbers (and added as such): their differences decide.
 //
-// A chunk's 64 tokens against one head (G and S as in linear_attention.cu, in
-// powers of two), each product with 128 rows in the lanes of tensor memory:
+// A long sequence is cut into segments (by its length and the number of heads alone, so
+// that a sequence's bits do not depend on the batch): a first kernel forms each
+// segment's own state from zero, a scan adds up what each then starts from, and the
+// second kernel has the outputs.
+//
+// A chunk's 64 tokens against one head of 128 by 128 channels (decays in powers of
+// two), each product with 128 rows in the lanes of tensor memory:
 //   A  = Q K^T                   64 by 64 scores (the lower 64 lanes)       8 steps of 16
 //   O  = S^T Q^T                 128 channels of v by 64 tokens, S in two bf16 parts  2 * 8
 //      + V^T (2^{-G_j} A)^T      the scores in two parts                     2 * 4
@@ -16,7 +28,9 @@
 // and V in O along the tokens, the operand's other major); the weighted scores and
 // values lie in shared memory beside them.  S stays in the registers of
 // eight warps (lane v channel, 64 key channels a thread) from a sequence's first
-// chunk to its last: U is formed from zero for each chunk, its small parts first,
+// chunk to its last (64 key channels: the first four warps'; 64 value channels: those
+// of the lower lanes, and likewise the values' warps; the other lanes hold anything, and
+// nothing is stored from them; products over key channels take half the steps): U is formed from zero for each chunk, its small parts first,
 // and added to S rounded to nearest, since the tensor cores' additions cut off.
 //
 // One CTA an SM walks the items (sequence, head, segment).  Its warps pass chunks
@@ -33,7 +47,8 @@
 // each, whatever their columns), the rest between the kinds of warps; the segments'
 // kernel 2200, 12 instructions and the splitting of V.  64 sequences of 24
 // to 41 tokens, 40 heads: 84 us (bytes at 6784 GB/s: 57); 8191 tokens of 40 heads
-// 148 us (50): 44 segments, 10 scan, 95 outputs; 3 sequences of 48 tokens at most 9.6 us.
+// 143 us (50): 42 segments, 9 scan, 92 outputs; 3 sequences of 48 tokens at most 9.6 us.
+// 8191 tokens of 40 heads of 64 by 64 129 us, 64 by 128 134, 128 by 64 139.
 //
 // Every wait on an mbarrier is bounded: after 2 s (prism_debug_wait_expiry
 // shortens that for tests) the kernel sets the device status bit; every warp leaves
@@ -69,7 +84,8 @@ constexpr int kStagesOf = kLocal ? 5 : 3;
 template <bool kLocal>
 constexpr int kSmemOf = kStagesOf<kLocal> * (kLocal ? 2 : 3) * kTile + (kLocal ? 0 : 3 * kTile + 2 * kScores + kStateWarps * kTurn) + 1024;
 constexpr int kAhead = 4;                                    // chunks whose decays are held, three on their way
-constexpr int kPart = D * D + 4;                             // floats of a segment's state in the workspace
+template <int DK, int DV>
+constexpr int kPart = DK * DV + 4;                           // floats of a segment's state in the workspace
 // columns of tensor memory
 constexpr uint32_t kColU = 0, kColS = 128, kColA = 256, kColO = 320;   // O of two chunks in turn
 constexpr uint32_t kColV = 128;      // kLocal: the decayed values, of two chunks in turn
@@ -142,6 +158,12 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
+// Predicated, not branched: with a branch here the segments' kernel spills 620 bytes a thread.
+__device__ __forceinline__ void store_if(bool there, float2* to, float2 v) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.s32 p, %0, 0;\n @p st.global.v2.f32 [%1], {%2, %3};\n}\n" ::"r"(static_cast<int>(there)), "l"(to),
+               "f"(v.x), "f"(v.y)
+               : "memory");
+}
 // One arrival for the warp, after what all of its lanes did.
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   __syncwarp();
@@ -170,6 +192,7 @@ __device__ __forceinline__ constexpr uint32_t idesc(int n, bool a_along_rows, bo
 
 // Sequences of few tokens, and malformed ones, after the chunks: found kThreads at a
 // time, their heads dealt out to the CTAs.
+template <int DK, int DV>
 __device__ void few_sequences(const LinAttnArgs& a, uint8_t* smem, uint32_t (&found)[kThreads / 32]) {
   const int tid = threadIdx.x;
   int64_t item = 0;
@@ -188,10 +211,10 @@ __device__ void few_sequences(const LinAttnArgs& a, uint8_t* smem, uint32_t (&fo
         for (int64_t hv = first; hv < a.Hv; hv += gridDim.x) {
           span_of(a, s0 + w * 32 + __ffs(rest) - 1, false, p);
           if (p.n > kFewTokens) {
-            spoil(a, p, static_cast<int>(hv), 0, D);
+            spoil(a, p, static_cast<int>(hv), 0, DV);
           } else {
             __syncthreads();       // shared memory is free again
-            few_tokens<D>(a, p, static_cast<int>(hv), 0, D, reinterpret_cast<float*>(smem));
+            few_tokens<DK>(a, p, static_cast<int>(hv), 0, DV, reinterpret_cast<float*>(smem));
           }
         }
         item += a.Hv;
@@ -199,9 +222,9 @@ __device__ void few_sequences(const LinAttnArgs& a, uint8_t* smem, uint32_t (&fo
   }
 }
 
-template <bool kLocal>
+template <bool kLocal, int DK, int DV>
 __global__ void __launch_bounds__(kThreads, 1)
-    linear_tc_chunk_kernel(const __grid_constant__ LinAttnArgs a, const __grid_constant__ Maps maps, int max_segs) {
+    linear_chunk_kernel(const __grid_constant__ LinAttnArgs a, const __grid_constant__ Maps maps, int max_segs) {
   constexpr int kStages = kStagesOf<kLocal>, kTiles = kLocal ? 2 : 3;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Step s_step[kInfo];
@@ -327,9 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         cp_async_wait<0>();        // the copies of the item before
         if (lane == 0 && in >= 0 && (kLocal ? sg == 0 : sgs == 1))
-          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.state + (in * a.Hv + h) * (D * D)), "r"(D * D * 4) : "memory");
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.state + (in * a.Hv + h) * (DK * DV)), "r"(DK * DV * 4) : "memory");
         for (int c = 0; c < kAhead - 1; ++c) copy_decays(c);
-        const int64_t part = (first_place(b, a.cut) * a.Hv + h) * kPart;
+        const int64_t part = (first_place(b, a.cut) * a.Hv + h) * kPart<DK, DV>;
         Sum log_total{0.0f, 0.0f};
         for (int c = 0; c < chunks; ++c) {
           ok = wait(bar_free(st), (round & 1) ^ 1u, &s_limit);
@@ -337,12 +360,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t row = static_cast<int32_t>(b + t0 + static_cast<int64_t>(c) * kChunk);
           if (elect_one()) {
             const uint32_t bar = bar_full(st);
-            tc::mbar_expect_tx(bar, (kLocal ? 2 : 3) * kTile);
+            tc::mbar_expect_tx(bar, ((kLocal ? 1 : 2) * (DK / 64) + DV / 64) * kHalf);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              if constexpr (!kLocal) tma_load_3d(tile_q(st) + half * kHalf, &maps.q, half * 64, hk, row, bar);
-              tma_load_3d(tile_k(st) + half * kHalf, &maps.k, half * 64, hk, row, bar);
-              tma_load_3d(tile_v(st) + half * kHalf, &maps.v, half * 64, h, row, bar);
+              if (!kLocal && half < DK / 64) tma_load_3d(tile_q(st) + half * kHalf, &maps.q, half * 64, hk, row, bar);
+              if (half < DK / 64) tma_load_3d(tile_k(st) + half * kHalf, &maps.k, half * 64, hk, row, bar);
+              if (half < DV / 64) tma_load_3d(tile_v(st) + half * kHalf, &maps.v, half * 64, h, row, bar);
             }
           }
           __syncwarp();
@@ -402,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lead) {
         const uint64_t qd = tc::smem_desc_sw128(tile_q(st)), kd = tc::smem_desc_sw128(tile_k(st));
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)   // rows 64 .. of Q's tile are not its: those lanes are not read
+        for (int k = 0; k < DK / 16; ++k)   // rows 64 .. of Q's tile are not its: those lanes are not read
           tc::tc_mma(tmem + kColA, qd + (k >> 2) * (kHalf >> 4) + 2 * (k & 3), kd + (k >> 2) * (kHalf >> 4) + 2 * (k & 3),
                      idesc(kChunk, false, false), k != 0 ? 1u : 0u);
         tc::tc_commit(bar_a);
@@ -424,9 +447,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t more_of = part != 2 || k != 0 ? 1u : 0u;
             if constexpr (kLocal) {
               tc::tc_mma_ta(tmem + kColU, tmem + kColV + (g & 1) * 96 + part * 32 + k * 8, kd + k * (16 * 128 >> 4),
-                            idesc(D, false, true), more_of);
+                            idesc(DK, false, true), more_of);
             } else {
-              tc::tc_mma(tmem + kColU, vd + 2 * k, kd + k * (16 * 128 >> 4), idesc(D, false, true), more_of);
+              tc::tc_mma(tmem + kColU, vd + 2 * k, kd + k * (16 * 128 >> 4), idesc(DK, false, true), more_of);
             }
           }
         }
@@ -442,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int part = 1; part >= 0; --part)
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
+            for (int k = 0; k < DK / 16; ++k)
               tc::tc_mma_ta(tmem + kColO + (g & 1) * kChunk, tmem + kColS + part * 64 + k * 8, qd + (k >> 2) * (kHalf >> 4) + 2 * (k & 3),
                             idesc(kChunk, false, false), part != 1 || k != 0 ? 1u : 0u);
           tc::tc_commit(bar_q);
@@ -472,6 +495,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kStateWarps) {
     // ============================ state ===================================
     const int half = warp >> 2, dv = (warp & 3) * 32 + lane;
+    // The others' warps go the same way with anything, which no one reads.
+    const bool own = half < DK / 64 && (warp & 3) < DV / 32;          // of the head's channels
+    constexpr int kOwners = DK * DV / 64;                              // threads that are
+    const int id = own ? half * DV + dv : 0;                           // among them
+    const int at = own ? half * 64 * DV + dv : 0;                      // of the state's values
     float2 S[32];      // key channels 64 half + 2 i, + 1
     int st = 0, info = 0;
     uint32_t round = 0;
@@ -482,27 +510,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (flags & kEnd) break;
       if constexpr (kLocal) warp_arrive(bar_free(st));   // its turn was seen
       if (flags & kFirst) {
-        const float* src = a.state + (w.in * a.Hv + w.hv) * (D * D) + half * 64 * D + dv;
-        const int64_t part_step = static_cast<int64_t>(a.Hv) * kPart;
-        const float2* place = reinterpret_cast<const float2*>(a.ws + w.part + w.seg * part_step) + tid;
+        const float* src = a.state + (w.in * a.Hv + w.hv) * (DK * DV) + at;
+        const int64_t part_step = static_cast<int64_t>(a.Hv) * kPart<DK, DV>;
+        const float2* place = reinterpret_cast<const float2*>(a.ws + w.part + w.seg * part_step) + id;
         const bool slot = w.in >= 0 && (kLocal ? w.seg == 0 : w.seg < 0);
         if (!kLocal && w.seg >= 0) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) S[i] = place[i * kStateThreads];
+          for (int i = 0; i < 32; ++i) S[i] = place[i * kOwners];
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) S[i] = slot ? make_float2(src[2 * i * D], src[(2 * i + 1) * D]) : make_float2(0.0f, 0.0f);
+          for (int i = 0; i < 32; ++i) S[i] = slot ? make_float2(src[2 * i * DV], src[(2 * i + 1) * DV]) : make_float2(0.0f, 0.0f);
         }
         if constexpr (kLocal) {
           // the sequence's start has a place of its own: the last segment may write
           // the state back before another begins
           if (w.seg == 0) {
-            float2* ps = reinterpret_cast<float2*>(a.ws + w.part) + tid;
+            float2* ps = reinterpret_cast<float2*>(a.ws + w.part) + id;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              ps[i * kStateThreads] = S[i];
-              S[i] = make_float2(0.0f, 0.0f);
-            }
+            for (int i = 0; i < 32; ++i) store_if(own, ps + i * kOwners, S[i]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S[i] = make_float2(0.0f, 0.0f);
           }
         }
       }
@@ -543,14 +570,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(bar_ufree);
       if (flags & kLast) {
         if constexpr (kLocal) {
-          float* ps = a.ws + last_part + last_out * (static_cast<int64_t>(a.Hv) * kPart);
+          float* ps = a.ws + last_part + last_out * (static_cast<int64_t>(a.Hv) * kPart<DK, DV>);
+          if (own)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) reinterpret_cast<float2*>(ps)[i * kStateThreads + tid] = S[i];
-          if (tid == 0) ps[D * D] = left;
-        } else if (last_out >= 0) {
-          float* dst = a.state + (last_out * a.Hv + hv) * (D * D) + half * 64 * D + dv;
+            for (int i = 0; i < 32; ++i) reinterpret_cast<float2*>(ps)[i * kOwners + id] = S[i];
+          if (tid == 0) ps[DK * DV] = left;
+        } else if (own && last_out >= 0) {
+          float* dst = a.state + (last_out * a.Hv + hv) * (DK * DV) + at;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) dst[2 * i * D] = S[i].x, dst[(2 * i + 1) * D] = S[i].y;
+          for (int i = 0; i < 32; ++i) dst[2 * i * DV] = S[i].x, dst[(2 * i + 1) * DV] = S[i].y;
         }
       }
       if (++st == kStages) st = 0, ++round;
@@ -562,6 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t0 = warp >= 16 ? 32 : 0;
     const uint32_t half = (warp & 2) ? kHalf : 0, first = (warp & 1) * 4;   // of the row's pieces of 8 channels
     const int r8 = lane & 7;
+    const bool own = (warp & 3) < DV / 32;        // of the head's channels
     // ---- outputs of chunk g (place `of`): the warp's 32 channels and half of the
     // tokens, 16 channels by 16 tokens at a time by way of its own shared memory
     auto outputs = [&](uint32_t g, int of) {
@@ -596,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         uint4 v;
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
-        if (t * 16 < live) *reinterpret_cast<uint4*>(dst + t * 16 * a.ldo_t + k * 16) = v;
+        if (own && t * 16 < live) *reinterpret_cast<uint4*>(dst + t * 16 * a.ldo_t + k * 16) = v;
         __syncwarp();
       }
       return true;
@@ -639,6 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (kLocal) {      // in tensor memory, where there is room for two chunks'
         if (g > 1 && !wait(bar_u(g), ((g - 2) >> 1) & 1, &s_limit)) break;
         tc::tc_fence_after();
+        if (own)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t lower[3][4], upper[3][4];
@@ -653,6 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         if (g > 0 && !wait(bar_u(g - 1), ((g - 1) >> 1) & 1, &s_limit)) break;   // the parts of the chunk before were read
         // rolled: the kinds of warps share the instruction cache
+        if (own)
 #pragma unroll 1
         for (int p = 0; p < 4; ++p) {
           uint32_t parts[3][4];
@@ -749,29 +780,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   }
-  if constexpr (!kLocal) few_sequences(a, smem, s_few);
+  if constexpr (!kLocal) few_sequences<DK, DV>(a, smem, s_few);
   pdl_trigger();
 }
 
 // The states that the segments start from, place by place: place 0 holds the
 // sequence's, place k + 1 what segment k makes of none.  A CTA for 1024 values.
-constexpr int kScanThreads = 256, kSlices = D * D / (4 * kScanThreads);
+constexpr int kScanThreads = 256;
+template <int DK, int DV>
+constexpr int kSlices = DK * DV / (4 * kScanThreads);
+template <int DK, int DV>
 __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const __grid_constant__ LinAttnArgs a) {
   pdl_wait();
-  const int64_t s = blockIdx.x / kSlices;
+  const int64_t s = blockIdx.x / kSlices<DK, DV>;
   const int hv = blockIdx.y;
   Span p;
   if (span_of(a, s, false, p) && !p.bad && p.n > kFewTokens) {
     const int segs = static_cast<int>(segment_count(p.n, a.cut));
-    const int64_t step = static_cast<int64_t>(a.Hv) * kPart;
-    float* place = a.ws + (first_place(p.b, a.cut) * a.Hv + hv) * kPart;
-    const int at = static_cast<int>(blockIdx.x % kSlices) * 4 * kScanThreads + threadIdx.x * 4;
+    const int64_t step = static_cast<int64_t>(a.Hv) * kPart<DK, DV>;
+    float* place = a.ws + (first_place(p.b, a.cut) * a.Hv + hv) * kPart<DK, DV>;
+    const int at = static_cast<int>(blockIdx.x % kSlices<DK, DV>) * 4 * kScanThreads + threadIdx.x * 4;
     if (segs > 1) {
       float4 x = *reinterpret_cast<const float4*>(place + at);
 #pragma unroll 4
       for (int k = 1; k < segs; ++k) {
         float4* here = reinterpret_cast<float4*>(place + k * step + at);
-        const float left = place[k * step + D * D];
+        const float left = place[k * step + DK * DV];
         const float4 y = *here;
         x = make_float4(fmaf(left, x.x, y.x), fmaf(left, x.y, y.y), fmaf(left, x.z, y.z), fmaf(left, x.w, y.w));
         *here = x;
@@ -791,12 +825,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// [T, H, 128] bf16 in boxes of 64 tokens of a head by 64 channels; rows past T read 0.
-cudaError_t make_map(CUtensorMap* m, const uint16_t* ptr, int64_t T, int64_t H, int64_t ld_t, int64_t ld_h) {
+// [T, H, channels] bf16 in boxes of 64 tokens of a head by 64 channels; rows past T read 0.
+cudaError_t make_map(CUtensorMap* m, const uint16_t* ptr, int64_t T, int64_t H, int64_t channels, int64_t ld_t, int64_t ld_h) {
   const auto fn = encode_fn();
   if (fn == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(H > 1 ? ld_h : D) * 2, static_cast<cuuint64_t>(ld_t) * 2};
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(channels), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(H > 1 ? ld_h : channels) * 2, static_cast<cuuint64_t>(ld_t) * 2};
   const cuuint32_t box[3] = {64, 1, kChunk}, steps[3] = {1, 1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(ptr), dims, strides, box, steps,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -806,25 +840,31 @@ cudaError_t make_map(CUtensorMap* m, const uint16_t* ptr, int64_t T, int64_t H, 
 
 }  // namespace
 
-cudaError_t launch_linear_attention_tc(const LinAttnArgs& a, cudaStream_t stream) {
+template <int DK, int DV>
+cudaError_t launch_linear_chunks(const LinAttnArgs& a, cudaStream_t stream) {
   Maps maps;
-  cudaError_t e = make_map(&maps.q, a.q, a.T, a.Hk, a.ldq_t, a.ldq_h);
-  if (e == cudaSuccess) e = make_map(&maps.k, a.k, a.T, a.Hk, a.ldk_t, a.ldk_h);
-  if (e == cudaSuccess) e = make_map(&maps.v, a.v, a.T, a.Hv, a.ldv_t, a.ldv_h);
+  cudaError_t e = make_map(&maps.q, a.q, a.T, a.Hk, DK, a.ldq_t, a.ldq_h);
+  if (e == cudaSuccess) e = make_map(&maps.k, a.k, a.T, a.Hk, DK, a.ldk_t, a.ldk_h);
+  if (e == cudaSuccess) e = make_map(&maps.v, a.v, a.T, a.Hv, DV, a.ldv_t, a.ldv_h);
   if (e != cudaSuccess) return e;
   const int segs = static_cast<int>(most_segments(a.max_len, a.cut));
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.S * segs * a.Hv, sm_count()));
+  const auto first = linear_chunk_kernel<true, DK, DV>, second = linear_chunk_kernel<false, DK, DV>;
   if (segs > 1) {
-    e = ensure_smem_attr(reinterpret_cast<const void*>(linear_tc_chunk_kernel<true>), kSmemOf<true>);
+    e = ensure_smem_attr(reinterpret_cast<const void*>(first), kSmemOf<true>);
+    if (e == cudaSuccess) e = launch_kernel(first, dim3(grid), dim3(kThreads), kSmemOf<true>, stream, true, a, maps, segs);
     if (e == cudaSuccess)
-      e = launch_kernel(linear_tc_chunk_kernel<true>, dim3(grid), dim3(kThreads), kSmemOf<true>, stream, true, a, maps, segs);
-    if (e == cudaSuccess)
-      e = launch_kernel(linear_scan_kernel, dim3(static_cast<unsigned>(a.S * kSlices), a.Hv), dim3(kScanThreads), 0, stream, true, a);
+      e = launch_kernel(linear_scan_kernel<DK, DV>, dim3(static_cast<unsigned>(a.S * kSlices<DK, DV>), a.Hv), dim3(kScanThreads), 0,
+                        stream, true, a);
   }
-  if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(linear_tc_chunk_kernel<false>), kSmemOf<false>);
+  if (e == cudaSuccess) e = ensure_smem_attr(reinterpret_cast<const void*>(second), kSmemOf<false>);
   if (e != cudaSuccess) return e;
-  return launch_kernel(linear_tc_chunk_kernel<false>, dim3(grid), dim3(kThreads), kSmemOf<false>, stream, true, a, maps, segs);
+  return launch_kernel(second, dim3(grid), dim3(kThreads), kSmemOf<false>, stream, true, a, maps, segs);
 }
+template cudaError_t launch_linear_chunks<64, 64>(const LinAttnArgs&, cudaStream_t);
+template cudaError_t launch_linear_chunks<64, 128>(const LinAttnArgs&, cudaStream_t);
+template cudaError_t launch_linear_chunks<128, 64>(const LinAttnArgs&, cudaStream_t);
+template cudaError_t launch_linear_chunks<128, 128>(const LinAttnArgs&, cudaStream_t);
 
 cudaError_t read_and_clear_linear_status(uint32_t* out) {
   uint32_t v = 0;

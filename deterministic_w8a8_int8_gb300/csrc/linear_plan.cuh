@@ -16,37 +16,31 @@ namespace lin {
 
 // Tokens that take the recurrence.  40 heads of 128 by 128, 2, 4, 8 and 16 tokens by the
 // recurrence: one sequence 3.8, 4.5, 6.3 and 9.7 us, 64 of them 60, 70, 92 and 136;
-// in chunks 9.3 and 83 whatever the number.
+// in chunks 9.3 and 83 whatever the number (heads of 64 by 64: 8.5 and 60).
 constexpr int kFewTokens = 8;
 constexpr int kChunk = 64;
 constexpr float kMinDecay = -16384.0f;   // e^x = 0 from far above it; sums of 64 stay finite
 
-// The segments of a long sequence: those with which its heads fill the places for
-// CTAs in the fewest turns for what each then has to do, and one where more do not save
-// a third: keys and values are read twice.  The tcgen05 kernel has a place on an SM, the
-// other more (8191 tokens of 16 heads of 64 by 64: 103 us by one, 64 by two, 81 by three,
-// of 40 heads 153, 153, 177).  One sequence of 32767 tokens, 2 heads of 128 by 128, cut
+// The segments of a long sequence: those with which its heads fill the SMs in the
+// fewest turns for what each then has to do, and one where more do not save a third: keys
+// and values are read twice.  One sequence of 32767 tokens, 2 heads of 128 by 128, cut
 // into 24, 48, 76 and 152 at most: 85, 65, 64 and 64 us, of one head 84, 61, 58 and 61.
 // Segments of fewer tokens pay where a few heads leave SMs empty, and cost a batch the
-// work twice.  2048 tokens, in us:
-//   chunks                                  2      4      8
-//   128 by 128, 8 heads, one sequence      27.3   29.8   38.3
-//               four sequences             57.5   50.3
-//               40 heads, one                     56.5   61.3
-//               four                             180.7  161.0
-//   64 by 64, 8 heads, one                 20.9   31.1   53.3
-//             four                         44.3   38.3
-//             40 heads, one                46.1   46.2   67.2
-//             four                        163.1  163.2  176.3
+// work twice.  2048 tokens, heads of 128 by 128, in us:
+//   chunks                       2      4      8
+//   8 heads, one sequence       27.3   29.8   38.3
+//            four sequences     57.5   50.3
+//   40 heads, one                      56.5   61.3
+//             four                    180.7  161.0
 constexpr int64_t kMaxSegments = 76;
-inline Cut cut_of(int64_t Hv, bool tc) {
-  const int64_t places = tc ? kSms : 2 * kSms, most = std::max<int64_t>(8, std::min<int64_t>(kMaxSegments, places / Hv));
-  auto turns = [&](int64_t n) { return (n * Hv + places - 1) / places; };
+inline Cut cut_of(int64_t Hv) {
+  const int64_t most = std::max<int64_t>(8, std::min<int64_t>(kMaxSegments, kSms / Hv));
+  auto turns = [&](int64_t n) { return (n * Hv + kSms - 1) / kSms; };
   int64_t best = 1;
   for (int64_t n = 2; n <= most; ++n)
     if (turns(n) * best < turns(best) * n) best = n;
   if (turns(best) * 3 > turns(1) * best * 2) best = 1;
-  return Cut{best, (tc ? 8 : 7) + (best > 8 ? 0 : 1)};
+  return Cut{best, best > 8 ? 8 : 9};
 }
 // Segments that a sequence of n tokens is cut into at most (two as short as may be do not
 // earn the first kernel: 512 tokens of 8 heads of 128 by 128 in one 23.6, in two 28 us, 1024
@@ -253,7 +247,7 @@ __device__ __forceinline__ float left_of(const Decays& d, int e) {
 
 }  // namespace lin
 
-// The tcgen05 kernel (linear_attention_tc.cu): heads of 128 by 128 channels, sequences of
-// more than lin::kFewTokens tokens.
-cudaError_t launch_linear_attention_tc(const LinAttnArgs& a, cudaStream_t stream);
+// Sequences of more than lin::kFewTokens tokens (linear_attention_tc.cu).
+template <int DK, int DV>
+cudaError_t launch_linear_chunks(const LinAttnArgs& a, cudaStream_t stream);
 }  // namespace prism

@@ -744,10 +744,10 @@ int prism_glu_quant(const void *gate_up_bf16, int64_t ldx,
  * Inputs must be finite (log_decay: not NaN or +inf); out overlaps no input.  States
  * and sums are binary32.  More than 8 tokens of a sequence go by in chunks of 64,
  * whose products enter the tensor cores as sums of two or three bf16 parts: to 2^-17
- * of a score or a state that is read out, and 2^-25 of what is added to a state.  With
- * D_k = D_v = 128 what a chunk's decays leave of the state that it begins with, in
- * its outputs, counts as 2^-80 of it at least; those heads run on tcgen05, whose
- * bounded waits report through prism_device_status.
+ * of a score or a state that is read out, and 2^-25 of what is added to a state.   What
+ * a chunk's decays leave of the state that it begins with, in its outputs, counts as
+ * 2^-80 of it at least.  Chunks run on tcgen05, whose bounded waits report through
+ * prism_device_status.
  * A sequence's results depend on its own tokens and state (and on H_v and how its
  * tokens are divided among calls) only.
  * A malformed sequence (too many tokens, a state index outside [-1, num_states):

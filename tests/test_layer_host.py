@@ -102,7 +102,7 @@ def test_workspace(L):
     assert f(3, 8191, 8191, 40, 128, 128) <= 16 * one
     assert f(1, 1 << 20, 1 << 20, 400, 128, 128) == 0     # heads enough
     assert f(1, 767, 767, 8, 128, 128) == 0 and f(1, 768, 768, 8, 128, 128) == 3 * 8 * (128 * 128 + 4) * 4
-    assert f(1, 383, 383, 8, 64, 64) == 0 and f(1, 384, 384, 8, 64, 64) == 3 * 8 * (64 * 64 + 4) * 4
+    assert f(1, 767, 767, 8, 64, 64) == 0 and f(1, 768, 768, 8, 64, 64) == 3 * 8 * (64 * 64 + 4) * 4
 
 
 @pytest.mark.parametrize("call,text", [
