@@ -138,7 +138,7 @@ int prism_linear_attention(const void* q_bf16, int64_t ldq_t, int64_t ldq_h, con
   if (S == 0) return PRISM_OK;
   if (max_len < 1 || num_states < 0 || (cu == nullptr && T != S)) return PRISM_ERR_INVALID_ARG;
   if (H_k <= 0 || H_v <= 0 || H_v % H_k != 0) return PRISM_ERR_INVALID_ARG;
-  if (!(scale > -3e38f && scale < 3e38f)) return PRISM_ERR_INVALID_ARG;
+  if (!(scale >= -0x1p64f && scale <= 0x1p64f)) return PRISM_ERR_INVALID_ARG;   // times 2^40 in chunks
   if ((D_k != 64 && D_k != 128) || (D_v != 64 && D_v != 128)) return PRISM_ERR_UNSUPPORTED;
   if (S > (1 << 24) || T > kInt31 || H_v > 65535 || num_states > kInt31) return PRISM_ERR_UNSUPPORTED;
   if (S * H_v > (1 << 28)) return PRISM_ERR_UNSUPPORTED;   // searched for work within the kernels' bounded waits

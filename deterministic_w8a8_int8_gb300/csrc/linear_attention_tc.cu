@@ -22,7 +22,11 @@
 // and out = scale * 2^{G_i} O^T, S = 2^{G_C} S + U^T.  The scores' weights are those
 // of a column alone.  Where a chunk's decays go below 2^-80 (kDeep), G_i stops there
 // for the outputs, and the scores of those rows make up for it: what 2^-80 is left
-// of in the state that entered counts as 2^-80 of it.  S^T is an operand in
+// of in the state that entered counts as 2^-80 of it.  So that weights of up to 2^80 take
+// no sum out of binary32, S and the weights are held 2^-40 times as large, and the
+// outputs' factor has the 2^40: exact, and free but at an item's ends (64 sequences of 24
+// to 41 tokens 86.7 -> 87.8 us; as a factor of S for the chunks alone that need it, 8191
+// tokens took 146 to 150).  S^T is an operand in
 // tensor memory, formed by the warps that have it; Q, K and V are read as they lie,
 // by tensor copies in the 128-byte-swizzled layout (K-major for Q and K; for K in U
 // and V in O along the tokens, the operand's other major); the weighted scores and
@@ -91,6 +95,7 @@ constexpr uint32_t kColU = 0, kColS = 128, kColA = 256, kColO = 320;   // O of t
 constexpr uint32_t kColV = 128;      // kLocal: the decayed values, of two chunks in turn
 
 constexpr float kDeepest = 80.0f;
+constexpr float kUp = 0x1p40f, kDown = 0x1p-40f;            // half of it; the second kernel's S and weights
 enum { kFirst = 1, kLast = 2, kEnd = 4, kDeep = 8 };
 struct Step {          // a chunk's work
   int64_t row;         // its first token
@@ -381,11 +386,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int i = 2 * lane + e;
             const float G = __fadd_rn(d.g[e].h, d.g[e].l);
             if constexpr (!kLocal) {
-              s_out[in_slot][i] = ex2(fmaxf(G, -kDeepest)) * a.scale;
-              s_in[in_slot][i] = ex2(fminf(-G, kDeepest));
+              s_out[in_slot][i] = ex2(fmaxf(G, -kDeepest)) * (a.scale * kUp);
+              s_in[in_slot][i] = ex2(fminf(-G, kDeepest)) * kDown;
               if (deep) s_gh[in_slot][i] = d.g[e].h, s_gl[in_slot][i] = d.g[e].l;
             }
-            s_w[in_slot][i] = left_of(d, e);
+            s_w[in_slot][i] = kLocal ? left_of(d, e) : left_of(d, e) * kDown;
           }
           if (lane == 0) s_tot[in_slot] = exp2f(__fadd_rn(d.total.h, d.total.l));
           if (lane == 0) {
@@ -521,6 +526,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) S[i] = slot ? make_float2(src[2 * i * DV], src[(2 * i + 1) * DV]) : make_float2(0.0f, 0.0f);
         }
+        if constexpr (!kLocal) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) S[i] = mul2(S[i], make_float2(kDown, kDown));
+        }
         if constexpr (kLocal) {
           // the sequence's start has a place of its own: the last segment may write
           // the state back before another begins
@@ -578,7 +587,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (own && last_out >= 0) {
           float* dst = a.state + (last_out * a.Hv + hv) * (DK * DV) + at;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) dst[2 * i * DV] = S[i].x, dst[(2 * i + 1) * DV] = S[i].y;
+          for (int i = 0; i < 32; ++i) {
+            const float2 x = mul2(S[i], make_float2(kUp, kUp));
+            dst[2 * i * DV] = x.x, dst[(2 * i + 1) * DV] = x.y;
+          }
         }
       }
       if (++st == kStages) st = 0, ++round;
@@ -732,6 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float2 gh = *reinterpret_cast<const float2*>(&s_gh[info][j0 + 2 * e]);
               const float2 gl = *reinterpret_cast<const float2*>(&s_gl[info][j0 + 2 * e]);
               w[e] = make_float2(ex2((dh.x - gh.x) + (dl1 - gl.x)), ex2((dh.y - gh.y) + (dl1 - gl.y)));
+              w[e] = mul2(w[e], make_float2(kDown, kDown));
             }
           }
           tc::tmem_wait_ld();

@@ -744,17 +744,20 @@ int prism_glu_quant(const void *gate_up_bf16, int64_t ldx,
  * Inputs must be finite (log_decay: not NaN or +inf); out overlaps no input.  States
  * and sums are binary32.  More than 8 tokens of a sequence go by in chunks of 64,
  * whose products enter the tensor cores as sums of two or three bf16 parts: to 2^-17
- * of a score or a state that is read out, and 2^-25 of what is added to a state.   What
+ * of a score or a state that is read out, and 2^-25 of what is added to a state.  What
  * a chunk's decays leave of the state that it begins with, in its outputs, counts as
- * 2^-80 of it at least.  Chunks run on tcgen05, whose bounded waits report through
+ * 2^-80 of it at least.  The sum of |q.k| |v| over a chunk must stay below 2^87 (below
+ * 2^127 where |q S| and up to 8 tokens are concerned), or outputs are infinities or
+ * NaN; in chunks, scores, states and decayed values of v below 2^-60 count to fewer
+ * bits, or as 0.  Chunks run on tcgen05, whose bounded waits report through
  * prism_device_status.
  * A sequence's results depend on its own tokens and state (and on H_v and how its
  * tokens are divided among calls) only.
  * A malformed sequence (too many tokens, a state index outside [-1, num_states):
  * PRISM_DEV_ERR_STATE_RANGE) gets NaN rows and writes no state; one with
  * malformed offsets has no rows.
- *   D_k, D_v in {64, 128}; H_v a multiple of H_k, H_v <= 65535, S <= 2^24,
- *   S * H_v <= 2^28; T, num_states < 2^31.
+ *   |scale| <= 2^64; D_k, D_v in {64, 128}; H_v a multiple of H_k, H_v <= 65535,
+ *   S <= 2^24, S * H_v <= 2^28; T, num_states < 2^31.
  */
 size_t prism_linear_attention_workspace_bytes(int64_t S, int64_t T,
                                               int64_t max_len, int64_t H_v,
