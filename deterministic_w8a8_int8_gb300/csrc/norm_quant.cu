@@ -192,9 +192,9 @@ __device__ __forceinline__ Sum team_sum(Sum s, Sum* red) {
   return s;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
+__device__ __forceinline__ float max3(float a, float b, float c) {   // NaN where one of them is
   float v;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
   return v;
 }
 
@@ -217,14 +217,14 @@ __device__ __forceinline__ void store_codes(const RowCodes& o, int64_t row, int 
   for (int i = 0; i < C; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) top = max3(top, fabsf(y[i][e].x), fabsf(y[i][e].y));
-  // magnitudes are ordered as their bits are
+  // magnitudes are ordered as their bits are, NaN above all
   const uint32_t wm = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
   if (lane == 0) red[lt >> 5] = wm;
   __syncthreads();
   const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < (team >> 5) ? red[lane] : 0u));
-  const bool zero_row = !(amax >= 0x1p-120f);
-  const float inv = zero_row ? 0.0f : __fdiv_rn(127.0f, amax);
-  if (lt == 0) o.a_scale[row] = zero_row ? 0.0f : __fdiv_rn(amax, 127.0f);
+  const bool finite = amax < __int_as_float(0x7f800000), dead = !finite || amax < 0x1p-120f;
+  const float inv = dead ? 0.0f : __fdiv_rn(127.0f, amax);
+  if (lt == 0) o.a_scale[row] = dead ? __fmul_rn(amax, 0.0f) : __fdiv_rn(amax, 127.0f);
   // t + 1.5 * 2^23 is t rounded to an integer, in the low bits
   constexpr float kMagic = 12582912.0f;
 #pragma unroll
@@ -251,6 +251,16 @@ __device__ __forceinline__ void store_codes(const RowCodes& o, int64_t row, int 
       for (int e = 0; e < 4; ++e) b[e] = __byte_perm(__float_as_uint(t[e].x), __float_as_uint(t[e].y), 0x0040u);
       reinterpret_cast<uint2*>(static_cast<int8_t*>(o.q) + row * o.ldq)[j] =
           make_uint2(__byte_perm(b[0], b[1], 0x5410u), __byte_perm(b[2], b[3], 0x5410u));
+    }
+  }
+  if (!finite) {   // 0 * NaN is no code: the thread's own once more
+#pragma unroll 1
+    for (int j = lt; j < nvec; j += team) {
+      if (o.form == PRISM_FORM_F16) {
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.q) + row * o.ldq)[j] = make_uint4(0u, 0u, 0u, 0u);
+      } else {
+        reinterpret_cast<uint2*>(static_cast<int8_t*>(o.q) + row * o.ldq)[j] = make_uint2(0u, 0u);
+      }
     }
   }
 }

@@ -670,7 +670,9 @@ int prism_token_logprobs(const void *logits, int logits_f32, int64_t ldl,
  * for any batch and device.  silu(z) = z * ((z >= 0 ? 1 : e) / (1 + e)) with
  * e = exp(-|z|) as in the read-out, but each product and the sum that follows it
  * one fused operation (and n = rint of the exact product).
- * Inputs must be finite, with magnitudes below 2^40.  q 16-byte aligned; rows of
+ * Inputs must be finite, with magnitudes below 2^40, and so must h.  A row with a
+ * value y that is not finite (a NaN or an infinity in its inputs) is marked: codes 0,
+ * a_scale NaN, so that a linear on it gives NaN.  q 16-byte aligned; rows of
  * bf16 16-byte aligned, their strides multiples of 8; weights 16-byte aligned;
  * 1e-20 <= eps <= 1; 16 <= K <= PRISM_MAX_ROW, K % 16 == 0.  M == 0 enqueues
  * nothing.  Outputs overlap no input but where that is said.
