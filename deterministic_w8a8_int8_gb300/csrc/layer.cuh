@@ -72,10 +72,11 @@ struct LinAttnArgs {
   int64_t S, T, max_len, num_states;
   int32_t Hk, Hv, Dk, Dv, G;   // G: value heads of a key head
   lin::Cut cut;            // how sequences are cut (set by the launcher)
+  int64_t places_each;     // workspace places of a sequence, or 0: by tokens (set by the launcher)
   float* ws;
   uint32_t* err;
 };
-size_t linear_attention_workspace_bytes(int64_t T, int64_t max_len, int64_t Hv, int64_t Dk, int64_t Dv);
+size_t linear_attention_workspace_bytes(int64_t S, int64_t T, int64_t max_len, int64_t Hv, int64_t Dk, int64_t Dv);
 cudaError_t launch_linear_attention(const LinAttnArgs& a, cudaStream_t stream);
 // Device status bits of its bounded waits, and their test mode (prism_debug_wait_expiry).
 cudaError_t read_and_clear_linear_status(uint32_t* out);

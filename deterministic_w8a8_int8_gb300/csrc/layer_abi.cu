@@ -124,7 +124,7 @@ int prism_glu_quant(const void* gate_up_bf16, int64_t ldx, const float* inv_smoo
 size_t prism_linear_attention_workspace_bytes(int64_t S, int64_t T, int64_t max_len, int64_t H_v, int64_t D_k,
                                               int64_t D_v) {
   if (S <= 0 || T <= 0 || max_len <= 0 || H_v <= 0 || (D_k != 64 && D_k != 128) || (D_v != 64 && D_v != 128)) return 0;
-  return prism::linear_attention_workspace_bytes(T, std::min(max_len, T), H_v, D_k, D_v);
+  return prism::linear_attention_workspace_bytes(S, T, std::min(max_len, T), H_v, D_k, D_v);
 }
 
 int prism_linear_attention(const void* q_bf16, int64_t ldq_t, int64_t ldq_h, const void* k_bf16, int64_t ldk_t,
@@ -155,7 +155,7 @@ int prism_linear_attention(const void* q_bf16, int64_t ldq_t, int64_t ldq_h, con
       !aligned(cu, 4) || !aligned(dev_error_word, 4))
     return PRISM_ERR_ALIGNMENT;
   max_len = std::min(max_len, std::max<int64_t>(T, 1));
-  const size_t need = prism::linear_attention_workspace_bytes(T, max_len, H_v, D_k, D_v);
+  const size_t need = prism::linear_attention_workspace_bytes(S, T, max_len, H_v, D_k, D_v);
   if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need) return PRISM_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return PRISM_ERR_ALIGNMENT;

@@ -49,15 +49,14 @@ cudaError_t launch_shape(const LinAttnArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-size_t linear_attention_workspace_bytes(int64_t T, int64_t max_len, int64_t Hv, int64_t Dk, int64_t Dv) {
-  const Cut cut = cut_of(Hv);
-  if (most_segments(max_len, cut) <= 1) return 0;
-  return static_cast<size_t>(first_place(T, cut) * Hv * (Dk * Dv + 4)) * 4;
+size_t linear_attention_workspace_bytes(int64_t S, int64_t T, int64_t max_len, int64_t Hv, int64_t Dk, int64_t Dv) {
+  return static_cast<size_t>(places_of(S, T, max_len, cut_of(Hv)).total * Hv * (Dk * Dv + 4)) * 4;
 }
 
 cudaError_t launch_linear_attention(const LinAttnArgs& given, cudaStream_t stream) {
   LinAttnArgs a = given;
   a.cut = cut_of(a.Hv);
+  a.places_each = places_of(a.S, a.T, a.max_len, a.cut).each;
   if (a.Dk == 64) return a.Dv == 64 ? launch_shape<64, 64>(a, stream) : launch_shape<64, 128>(a, stream);
   return a.Dv == 64 ? launch_shape<128, 64>(a, stream) : launch_shape<128, 128>(a, stream);
 }

@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t item = at + lane * static_cast<int64_t>(gridDim.x);
       Span p{};
       int hv = 0, seg = 0, segs = 0;
-      int64_t each = 0;
+      int64_t each = 0, place = 0;
       bool mine = false;
       if (item < total) {
         const int64_t s = item / per_seq;
@@ -328,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mine = span_of(a, s, false, p) && !p.bad && p.n > kFewTokens;
         if (mine) {
           each = segment_chunks(p.n, a.cut);
+          place = first_place(a, s, p.b);
           segs = static_cast<int>(segment_count(p.n, a.cut));
           mine = seg < (kLocal ? segs - 1 : segs);   // nothing comes after the last one
         }
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0 && in >= 0 && (kLocal ? sg == 0 : sgs == 1))
           asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.state + (in * a.Hv + h) * (DK * DV)), "r"(DK * DV * 4) : "memory");
         for (int c = 0; c < kAhead - 1; ++c) copy_decays(c);
-        const int64_t part = (first_place(b, a.cut) * a.Hv + h) * kPart<DK, DV>;
+        const int64_t part = (__shfl_sync(0xffffffffu, place, from) * a.Hv + h) * kPart<DK, DV>;
         Sum log_total{0.0f, 0.0f};
         for (int c = 0; c < chunks; ++c) {
           ok = wait(bar_free(st), (round & 1) ^ 1u, &s_limit);
@@ -811,7 +812,7 @@ __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const __grid_
   if (span_of(a, s, false, p) && !p.bad && p.n > kFewTokens) {
     const int segs = static_cast<int>(segment_count(p.n, a.cut));
     const int64_t step = static_cast<int64_t>(a.Hv) * kPart<DK, DV>;
-    float* place = a.ws + (first_place(p.b, a.cut) * a.Hv + hv) * kPart<DK, DV>;
+    float* place = a.ws + (first_place(a, s, p.b) * a.Hv + hv) * kPart<DK, DV>;
     const int at = static_cast<int>(blockIdx.x % kSlices<DK, DV>) * 4 * kScanThreads + threadIdx.x * 4;
     if (segs > 1) {
       float4 x = *reinterpret_cast<const float4*>(place + at);

@@ -58,8 +58,20 @@ __host__ __device__ __forceinline__ int64_t segment_count(int64_t n, const Cut& 
   return (chunks + each - 1) / each;
 }
 // A sequence in segments has a place in the workspace for each but the last, and
-// one for the state that it starts from: no more than 2^shift go into its tokens.
-__host__ __device__ __forceinline__ int64_t first_place(int64_t first_token, const Cut& cut) { return first_token >> cut.shift; }
+// one for the state that it starts from.  They are counted by tokens, 2^shift at least to
+// each, or by the segments that every sequence may have, whichever makes fewer: one text
+// of 131071 tokens and 40 heads has 8 (21 MB), by tokens 255 (669 MB).
+struct Places {
+  int64_t total, each;   // each: a sequence's own; 0 where they go by tokens
+};
+inline Places places_of(int64_t S, int64_t T, int64_t max_len, const Cut& cut) {
+  const int64_t segs = most_segments(max_len, cut), by_tokens = T >> cut.shift;
+  if (segs <= 1) return Places{0, 0};
+  return S * segs < by_tokens ? Places{S * segs, segs} : Places{by_tokens, 0};
+}
+__device__ __forceinline__ int64_t first_place(const LinAttnArgs& a, int64_t s, int64_t first_token) {
+  return a.places_each != 0 ? s * a.places_each : first_token >> a.cut.shift;
+}
 
 struct Span {
   int64_t b, n;
