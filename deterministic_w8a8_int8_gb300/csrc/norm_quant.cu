@@ -17,10 +17,10 @@
 // product and both are to be rounded, the sum is a scalar one.)
 //
 // A row is one CTA's: its values stay in registers from the first read to the
-// codes, 8 to a 16-byte vector, C vectors a thread, the fewest that keep the row
-// within 512 threads.  Two exchanges in shared memory (three with a post norm)
-// stand in the way of a row, the sum's and the largest magnitude's; the next
-// row's loads are under way across them, and the other CTAs of the SM work.
+// codes, 8 to a 16-byte vector, C vectors a thread (vectors_of).  Two exchanges in
+// shared memory (three with a post norm) stand in the way of a row, the sum's and
+// the largest magnitude's; the next row's loads are under way across them, and the
+// other CTAs of the SM work.
 //
 // A call's bytes (each operand once) are its floor; rows of 5120 and 17408, at 6784 GB/s:
 //   norm   8192 rows with a delta 48.2 us (90 % of that rate), 2048 rows with a delta's
@@ -582,7 +582,7 @@ inline bool worth_table(int64_t M, int64_t K, int team) {
 template <class F, int C, class Args>
 cudaError_t launch_c(const Args& a, int64_t M, int64_t K, cudaStream_t stream) {
   static std::atomic<int> held[2][kWarps + 1];
-  if constexpr (F::kSigmoids && C > 1) {
+  if constexpr (C >= F::kTables) {
     if (worth_table(M, K, team_of(K, C)))
       return launch_rows<Args>(F::template of<C, true>(), held[1], a, M, K, C, F::kOperands, SigmoidTable::kBytes, stream);
   }
@@ -602,11 +602,13 @@ cudaError_t launch_any(const Args& a, int64_t M, int64_t K, cudaStream_t stream)
 }
 static_assert(vectors_of(PRISM_MAX_ROW, kNormRows) == 8 && PRISM_MAX_ROW <= 64 * kMaxTeam, "the longest row");
 
+// kTables: vectors a thread from which on a table may pay, where teams can have 128
+// threads (rows of 2 vectors a thread have 32, but for gated heads); 9: none.
 template <bool kDelta>
 struct NormKernel {
   static constexpr int kOperands = kDelta ? 2 : 1;
   static constexpr Rows kRows = kNormRows;
-  static constexpr bool kSigmoids = false;
+  static constexpr int kTables = 9;
   template <int C, bool kTable>
   static auto of() { return norm_kernel<C, kDelta>; }
 };
@@ -614,14 +616,14 @@ template <bool kGate>
 struct HeadKernel {
   static constexpr int kOperands = kGate ? 2 : 1;
   static constexpr Rows kRows = kGate ? kGatedHeadRows : kHeadRows;
-  static constexpr bool kSigmoids = kGate;
+  static constexpr int kTables = kGate ? 2 : 9;
   template <int C, bool kTable>
   static auto of() { return head_norm_kernel<C, kGate, kTable>; }
 };
 struct GluKernel {
   static constexpr int kOperands = 2;
   static constexpr Rows kRows = kNormRows;
-  static constexpr bool kSigmoids = true;
+  static constexpr int kTables = 4;
   template <int C, bool kTable>
   static auto of() { return glu_kernel<C, kTable>; }
 };
