@@ -7,6 +7,16 @@
 
 namespace prism {
 
+// A sum of binary32 numbers as the rounded sum and what is missing of it.
+struct Sum {
+  float h, l;
+};
+__device__ __forceinline__ Sum join(Sum a, Sum b) {
+  const float s = __fadd_rn(a.h, b.h), t = __fsub_rn(s, a.h);
+  const float e = __fadd_rn(__fsub_rn(a.h, __fsub_rn(s, t)), __fsub_rn(b.h, t));
+  return Sum{s, __fadd_rn(e, __fadd_rn(a.l, b.l))};
+}
+
 struct RowCodes {          // where a row's values go (PRISM_FORM_*)
   int32_t form;
   void* q;

@@ -26,16 +26,18 @@
 // no sum out of binary32, S and the weights are held 2^-40 times as large, and the
 // outputs' factor has the 2^40: exact, and free but at an item's ends (64 sequences of 24
 // to 41 tokens 86.7 -> 87.8 us; as a factor of S for the chunks alone that need it, 8191
-// tokens took 146 to 150).  S^T is an operand in
-// tensor memory, formed by the warps that have it; Q, K and V are read as they lie,
-// by tensor copies in the 128-byte-swizzled layout (K-major for Q and K; for K in U
-// and V in O along the tokens, the operand's other major); the weighted scores and
-// values lie in shared memory beside them.  S stays in the registers of
-// eight warps (lane v channel, 64 key channels a thread) from a sequence's first
-// chunk to its last (64 key channels: the first four warps'; 64 value channels: those
-// of the lower lanes, and likewise the values' warps; the other lanes hold anything, and
-// nothing is stored from them; products over key channels take half the steps): U is formed from zero for each chunk, its small parts first,
-// and added to S rounded to nearest, since the tensor cores' additions cut off.
+// tokens took 146 to 150).
+//
+// S^T is an operand in tensor memory, formed by the warps that have it.  Q, K and V are
+// read as they lie, by tensor copies in the 128-byte-swizzled layout (K-major for Q and
+// K; for K in U and V in O along the tokens, the operand's other major); the weighted
+// scores and values lie in shared memory beside them.  S stays in the registers of eight
+// warps (lane v channel, 64 key channels a thread) from a sequence's first chunk to its
+// last.  With 64 key channels the first four of those warps have it, and products over key
+// channels take half the steps; with 64 value channels the warps of the lower lanes, and
+// likewise the values' warps.  The other lanes hold anything, and nothing is stored from
+// them.  U is formed from zero for each chunk, its small parts first, and added to S
+// rounded to nearest, since the tensor cores' additions cut off.
 //
 // One CTA an SM walks the items (sequence, head, segment).  Its warps pass chunks
 // on by mbarriers:
@@ -146,7 +148,8 @@ __device__ __forceinline__ void store_matrices(uint32_t addr, const uint32_t (&r
 }
 // Four 8 by 8 matrices, each written transposed.
 __device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
 }
 // 16 lanes by 16 columns, in the fragments of an m16n8 result for each 8 columns.
 __device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[8]) {
@@ -165,8 +168,9 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 }
 // Predicated, not branched: with a branch here the segments' kernel spills 620 bytes a thread.
 __device__ __forceinline__ void store_if(bool there, float2* to, float2 v) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.s32 p, %0, 0;\n @p st.global.v2.f32 [%1], {%2, %3};\n}\n" ::"r"(static_cast<int>(there)), "l"(to),
-               "f"(v.x), "f"(v.y)
+  asm volatile("{\n .reg .pred p;\n setp.ne.s32 p, %0, 0;\n @p st.global.v2.f32 [%1], {%2, %3};\n}\n" ::"r"(
+                   static_cast<int>(there)),
+               "l"(to), "f"(v.x), "f"(v.y)
                : "memory");
 }
 // One arrival for the warp, after what all of its lanes did.
@@ -292,7 +296,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!kLocal && warp == 12)
     for (int p = 4; p < 8; ++p)
       for (int part = 0; part < 2; ++part)
-        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(scores + part * kScores + lane * 128 + ((p ^ (lane & 7)) << 4)), "r"(0)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(scores + part * kScores + lane * 128 +
+                                                                                   ((p ^ (lane & 7)) << 4)),
+                     "r"(0)
                      : "memory");
   tc::fence_proxy_async();
   tc::tc_fence_before();
@@ -356,7 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         cp_async_wait<0>();        // the copies of the item before
         if (lane == 0 && in >= 0 && (kLocal ? sg == 0 : sgs == 1))
-          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.state + (in * a.Hv + h) * (DK * DV)), "r"(DK * DV * 4) : "memory");
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.state + (in * a.Hv + h) * (DK * DV)), "r"(DK * DV * 4)
+                       : "memory");
         for (int c = 0; c < kAhead - 1; ++c) copy_decays(c);
         const int64_t part = (__shfl_sync(0xffffffffu, place, from) * a.Hv + h) * kPart<DK, DV>;
         Sum log_total{0.0f, 0.0f};

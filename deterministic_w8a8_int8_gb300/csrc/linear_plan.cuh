@@ -60,7 +60,7 @@ __host__ __device__ __forceinline__ int64_t segment_count(int64_t n, const Cut& 
 // A sequence in segments has a place in the workspace for each but the last, and
 // one for the state that it starts from.  They are counted by tokens, 2^shift at least to
 // each, or by the segments that every sequence may have, whichever makes fewer: one text
-// of 131071 tokens and 40 heads has 8 (21 MB), by tokens 255 (669 MB).
+// of 131071 tokens and 40 heads has 7 (18 MB), by tokens 255 (669 MB).
 struct Places {
   int64_t total, each;   // each: a sequence's own; 0 where they go by tokens
 };
@@ -213,16 +213,6 @@ __device__ __forceinline__ float ex2(float x) {   // to about 2^-22
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// A sum of binary32 numbers as the rounded sum and what is missing of it.
-struct Sum {
-  float h, l;
-};
-__device__ __forceinline__ Sum join(Sum a, Sum b) {
-  const float s = __fadd_rn(a.h, b.h), t = __fsub_rn(s, a.h);
-  const float e = __fadd_rn(__fsub_rn(a.h, __fsub_rn(s, t)), __fsub_rn(b.h, t));
-  return Sum{s, __fadd_rn(e, __fadd_rn(a.l, b.l))};
 }
 
 // The decays of a chunk's 64 tokens, two a lane (0 past the end), summed up to

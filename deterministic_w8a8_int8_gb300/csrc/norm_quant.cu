@@ -46,15 +46,6 @@ constexpr int kWarps = kMaxTeam / 32;
 
 __device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
 
-// A sum of binary32 numbers as the rounded sum and its error.
-struct Sum {
-  float h, l;
-};
-__device__ __forceinline__ Sum join(Sum a, Sum b) {
-  const float s = __fadd_rn(a.h, b.h), t = __fsub_rn(s, a.h);
-  const float e = __fadd_rn(__fsub_rn(a.h, __fsub_rn(s, t)), __fsub_rn(b.h, t));
-  return Sum{s, __fadd_rn(e, __fadd_rn(a.l, b.l))};
-}
 // Sums of squares of bf16 values, two side by side.  They begin at the largest
 // square of the thread's, which is taken off again at the end: with no addend
 // above the sum, the error of an addition is what its difference leaves of the
@@ -111,8 +102,9 @@ __device__ __forceinline__ float2 divide2(float2 n, float2 minus) {
   return fma2(fma2(minus, q, n), r, q);
 }
 
-// 1 / (1 + exp(-z)) of two values as (1 or e) / (1 + e), e = exp(-|z|) by n ln 2 + r (ln 2 in two parts), the series of e^r to r^7 in fused steps, times
-// 2^n.  From |z| = 88 on n would be -127 or less, and 2^n counts as 0.
+// 1 / (1 + exp(-z)) of two values as (1 or e) / (1 + e), e = exp(-|z|) by n ln 2 + r
+// (ln 2 in two parts), the series of e^r to r^7 in fused steps, times 2^n.  From
+// |z| = 88 on n would be -127 or less, and 2^n counts as 0.
 __device__ __forceinline__ float2 sigmoid2(float2 z) {
   constexpr float kMagic = 12582912.0f + 127.0f;   // 1.5 * 2^23, whose unit is 1, and the exponent's bias
   const float2 x = make_float2(fmaxf(-fabsf(z.x), -88.0f), fmaxf(-fabsf(z.y), -88.0f));
