@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    cp_async_wait<0>();            // of decays, where it left early
     if (ok && wait(bar_free(st), (round & 1) ^ 1u, &s_limit)) {
       if (lane == 0) {
         s_step[in_slot].flags = kEnd;
