@@ -39,6 +39,9 @@ int check_heads(const void* p, int64_t ld_t, int64_t ld_h, int64_t T, int64_t H,
   return ld_t % 8 != 0 || ld_h % 8 != 0 || !aligned(p, 16) ? PRISM_ERR_ALIGNMENT : PRISM_OK;
 }
 
+// Sizes of linear attention: S * H_v is searched for work within the kernels' bounded waits.
+bool within(int64_t S, int64_t T, int64_t H_v) { return S <= (1 << 24) && T <= kInt31 && H_v <= 65535 && S * H_v <= (1 << 28); }
+
 }  // namespace
 
 extern "C" {
@@ -124,6 +127,7 @@ int prism_glu_quant(const void* gate_up_bf16, int64_t ldx, const float* inv_smoo
 size_t prism_linear_attention_workspace_bytes(int64_t S, int64_t T, int64_t max_len, int64_t H_v, int64_t D_k,
                                               int64_t D_v) {
   if (S <= 0 || T <= 0 || max_len <= 0 || H_v <= 0 || (D_k != 64 && D_k != 128) || (D_v != 64 && D_v != 128)) return 0;
+  if (!within(S, T, H_v)) return 0;   // the call is refused
   return prism::linear_attention_workspace_bytes(S, T, std::min(max_len, T), H_v, D_k, D_v);
 }
 
@@ -140,8 +144,7 @@ int prism_linear_attention(const void* q_bf16, int64_t ldq_t, int64_t ldq_h, con
   if (H_k <= 0 || H_v <= 0 || H_v % H_k != 0) return PRISM_ERR_INVALID_ARG;
   if (!(scale >= -0x1p64f && scale <= 0x1p64f)) return PRISM_ERR_INVALID_ARG;   // times 2^40 in chunks
   if ((D_k != 64 && D_k != 128) || (D_v != 64 && D_v != 128)) return PRISM_ERR_UNSUPPORTED;
-  if (S > (1 << 24) || T > kInt31 || H_v > 65535 || num_states > kInt31) return PRISM_ERR_UNSUPPORTED;
-  if (S * H_v > (1 << 28)) return PRISM_ERR_UNSUPPORTED;   // searched for work within the kernels' bounded waits
+  if (!within(S, T, H_v) || num_states > kInt31) return PRISM_ERR_UNSUPPORTED;
   if ((state_in != nullptr || state_out != nullptr) && (state == nullptr || num_states == 0)) return PRISM_ERR_INVALID_ARG;
   int st;
   if (T > 0) {   // no token: states are passed on alone

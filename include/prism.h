@@ -741,8 +741,8 @@ int prism_glu_quant(const void *gate_up_bf16, int64_t ldx,
  *                 sequences overlap, theirs are undefined.
  *   max_len       the most tokens of one sequence; a sequence with more sets
  *                 PRISM_DEV_ERR_SEQ_RANGE
- *   workspace     prism_linear_attention_workspace_bytes(...) bytes, 256-byte
- *                 aligned, any contents
+ *   workspace     prism_linear_attention_workspace_bytes(...) bytes (0 for sizes
+ *                 that are refused), 256-byte aligned, any contents
  * Inputs must be finite (log_decay: not NaN or +inf); out overlaps no input.  States
  * and sums are binary32.  More than 8 tokens of a sequence go by in chunks of 64,
  * whose products enter the tensor cores as sums of two or three bf16 parts: to 2^-17
