@@ -190,6 +190,22 @@ __device__ __forceinline__ float max3(float a, float b, float c) {   // NaN wher
   return v;
 }
 
+// A row that is not finite: codes 0, and a scale of NaN, which the next linear passes on.
+// Out of the kernels' way (in line, heads without a gate took 35.6 us instead of 34.6, the
+// norm of 8192 rows of 256 6.3 instead of 6.0).
+__device__ __noinline__ void mark_row(const RowCodes& o, int64_t row, int nvec) {
+  const int team = blockDim.x, lt = threadIdx.x;
+  if (lt == 0) o.a_scale[row] = __int_as_float(0x7fffffff);
+#pragma unroll 1   // few registers, which the caller has to give
+  for (int j = lt; j < nvec; j += team) {
+    if (o.form == PRISM_FORM_F16) {
+      reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.q) + row * o.ldq)[j] = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      reinterpret_cast<uint2*>(static_cast<int8_t*>(o.q) + row * o.ldq)[j] = make_uint2(0u, 0u);
+    }
+  }
+}
+
 // The row's values y, 8 C a thread (0 past the row's end), as codes.
 template <int C>
 __device__ __forceinline__ void store_codes(const RowCodes& o, int64_t row, int nvec, const float2 (&y)[C][4], uint32_t* red) {
@@ -214,9 +230,13 @@ __device__ __forceinline__ void store_codes(const RowCodes& o, int64_t row, int 
   if (lane == 0) red[lt >> 5] = wm;
   __syncthreads();
   const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < (team >> 5) ? red[lane] : 0u));
-  const bool finite = amax < __int_as_float(0x7f800000), dead = !finite || amax < 0x1p-120f;
-  const float inv = dead ? 0.0f : __fdiv_rn(127.0f, amax);
-  if (lt == 0) o.a_scale[row] = dead ? __fmul_rn(amax, 0.0f) : __fdiv_rn(amax, 127.0f);
+  if (__builtin_expect(!(amax < __int_as_float(0x7f800000)), 0)) {
+    mark_row(o, row, nvec);
+    return;
+  }
+  const bool zero_row = amax < 0x1p-120f;
+  const float inv = zero_row ? 0.0f : __fdiv_rn(127.0f, amax);
+  if (lt == 0) o.a_scale[row] = zero_row ? 0.0f : __fdiv_rn(amax, 127.0f);
   // t + 1.5 * 2^23 is t rounded to an integer, in the low bits
   constexpr float kMagic = 12582912.0f;
 #pragma unroll
@@ -243,16 +263,6 @@ __device__ __forceinline__ void store_codes(const RowCodes& o, int64_t row, int 
       for (int e = 0; e < 4; ++e) b[e] = __byte_perm(__float_as_uint(t[e].x), __float_as_uint(t[e].y), 0x0040u);
       reinterpret_cast<uint2*>(static_cast<int8_t*>(o.q) + row * o.ldq)[j] =
           make_uint2(__byte_perm(b[0], b[1], 0x5410u), __byte_perm(b[2], b[3], 0x5410u));
-    }
-  }
-  if (!finite) {   // 0 * NaN is no code: the thread's own once more
-#pragma unroll 1
-    for (int j = lt; j < nvec; j += team) {
-      if (o.form == PRISM_FORM_F16) {
-        reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.q) + row * o.ldq)[j] = make_uint4(0u, 0u, 0u, 0u);
-      } else {
-        reinterpret_cast<uint2*>(static_cast<int8_t*>(o.q) + row * o.ldq)[j] = make_uint2(0u, 0u);
-      }
     }
   }
 }
