@@ -190,25 +190,29 @@ __device__ __forceinline__ float max3(float a, float b, float c) {   // NaN wher
   return v;
 }
 
-// A row that is not finite: codes 0, and a scale of NaN, which the next linear passes on.
-// Out of the kernels' way (in line, heads without a gate took 35.6 us instead of 34.6, the
-// norm of 8192 rows of 256 6.3 instead of 6.0).
-__device__ __noinline__ void mark_row(const RowCodes& o, int64_t row, int nvec) {
-  const int team = blockDim.x, lt = threadIdx.x;
-  if (lt == 0) o.a_scale[row] = __int_as_float(0x7fffffff);
-#pragma unroll 1   // few registers, which the caller has to give
-  for (int j = lt; j < nvec; j += team) {
-    if (o.form == PRISM_FORM_F16) {
-      reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.q) + row * o.ldq)[j] = make_uint4(0u, 0u, 0u, 0u);
-    } else {
-      reinterpret_cast<uint2*>(static_cast<int8_t*>(o.q) + row * o.ldq)[j] = make_uint2(0u, 0u);
+// The codes of the CTA's rows whose scale is NaN are 0 (0 * NaN is no code): after the last
+// row, since in the rows' way this takes the kernels registers (8192 rows of 40 heads 35.6
+// us without a gate instead of 34.6; as a call, 300 rows of 96 gated heads 7.8 instead of 7.4).
+__device__ __forceinline__ void clear_marked(const RowCodes& o, int64_t M, int nvec) {
+  __syncthreads();   // the scales were written
+  for (int64_t row = blockIdx.x; row < M; row += gridDim.x) {
+    if (!isnan(*static_cast<volatile float*>(o.a_scale + row))) continue;
+#pragma unroll 1
+    for (int j = threadIdx.x; j < nvec; j += blockDim.x) {   // what the thread itself has written
+      if (o.form == PRISM_FORM_F16) {
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.q) + row * o.ldq)[j] = make_uint4(0u, 0u, 0u, 0u);
+      } else {
+        reinterpret_cast<uint2*>(static_cast<int8_t*>(o.q) + row * o.ldq)[j] = make_uint2(0u, 0u);
+      }
     }
   }
 }
 
-// The row's values y, 8 C a thread (0 past the row's end), as codes.
+// The row's values y, 8 C a thread (0 past the row's end), as codes.  Where they are not
+// all finite the scale is NaN, which the next linear passes on, the codes are those of
+// clear_marked, and the answer, one for the CTA, is true.
 template <int C>
-__device__ __forceinline__ void store_codes(const RowCodes& o, int64_t row, int nvec, const float2 (&y)[C][4], uint32_t* red) {
+__device__ __forceinline__ bool store_codes(const RowCodes& o, int64_t row, int nvec, const float2 (&y)[C][4], uint32_t* red) {
   const int team = blockDim.x, lt = threadIdx.x, lane = lt & 31;
   if (o.form == PRISM_FORM_BF16) {
 #pragma unroll
@@ -218,7 +222,7 @@ __device__ __forceinline__ void store_codes(const RowCodes& o, int64_t row, int 
         reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.q) + row * o.ldq)[j] =
             make_uint4(bf16x2(y[i][0]), bf16x2(y[i][1]), bf16x2(y[i][2]), bf16x2(y[i][3]));
     }
-    return;
+    return false;
   }
   float top = 0.0f;
 #pragma unroll
@@ -230,13 +234,9 @@ __device__ __forceinline__ void store_codes(const RowCodes& o, int64_t row, int 
   if (lane == 0) red[lt >> 5] = wm;
   __syncthreads();
   const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < (team >> 5) ? red[lane] : 0u));
-  if (__builtin_expect(!(amax < __int_as_float(0x7f800000)), 0)) {
-    mark_row(o, row, nvec);
-    return;
-  }
-  const bool zero_row = amax < 0x1p-120f;
-  const float inv = zero_row ? 0.0f : __fdiv_rn(127.0f, amax);
-  if (lt == 0) o.a_scale[row] = zero_row ? 0.0f : __fdiv_rn(amax, 127.0f);
+  const bool marked = !(amax < __int_as_float(0x7f800000)), dead = marked || amax < 0x1p-120f;
+  const float inv = dead ? 0.0f : __fdiv_rn(127.0f, amax);
+  if (lt == 0) o.a_scale[row] = dead ? __fmul_rn(amax, 0.0f) : __fdiv_rn(amax, 127.0f);
   // t + 1.5 * 2^23 is t rounded to an integer, in the low bits
   constexpr float kMagic = 12582912.0f;
 #pragma unroll
@@ -265,6 +265,7 @@ __device__ __forceinline__ void store_codes(const RowCodes& o, int64_t row, int 
           make_uint2(__byte_perm(b[0], b[1], 0x5410u), __byte_perm(b[2], b[3], 0x5410u));
     }
   }
+  return marked;
 }
 
 // A thread's vectors of one operand's next row, on their way through shared
@@ -302,6 +303,7 @@ __global__ void __maxnreg__(C <= 4 ? 56 : C <= 6 ? 80 : 128) norm_kernel(const _
   pdl_wait();
   const int team = blockDim.x, lt = threadIdx.x, nvec = static_cast<int>(a.K >> 3);
   const Ahead ax(smem, 0, C, nvec), ad(smem, 1, C, nvec);
+  bool marked = false;
   int64_t row = blockIdx.x;
   auto fill = [&](int64_t r) {
     if (r < a.M) {
@@ -379,9 +381,10 @@ __global__ void __maxnreg__(C <= 4 ? 56 : C <= 6 ? 80 : 128) norm_kernel(const _
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[i][e] = mul2(y[i][e], w[e]);
     }
-    store_codes<C>(a.o, row, nvec, y, s_top[par]);
+    marked |= store_codes<C>(a.o, row, nvec, y, s_top[par]);
   }
   cp_async_wait<0>();
+  if (marked) clear_marked(a.o, a.M, nvec);
 }
 
 // A head's channels lie in D / 8 = `lanes` neighbouring lanes, and the sums of a
@@ -433,6 +436,7 @@ __global__ void __maxnreg__(C <= 2 ? 64 : C == 4 ? 80 : 128) head_norm_kernel(co
   constexpr int kRows = kTable ? SigmoidTable::kBytes : 0;
   const int nvec = static_cast<int>(a.K >> 3), lanes = a.D >> 3;
   const Ahead ax(smem + kRows, 0, C, nvec), az(smem + kRows, 1, C, nvec);
+  bool marked = false;
   int64_t row = blockIdx.x;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
@@ -482,9 +486,10 @@ __global__ void __maxnreg__(C <= 2 ? 64 : C == 4 ? 80 : 128) head_norm_kernel(co
         }
       }
     }
-    store_codes<C>(a.o, row, nvec, y, s_top[par]);
+    marked |= store_codes<C>(a.o, row, nvec, y, s_top[par]);
   }
   cp_async_wait<0>();
+  if (marked) clear_marked(a.o, a.M, nvec);
 }
 
 template <int C, bool kTable>
@@ -498,6 +503,7 @@ __global__ void __launch_bounds__(kMaxTeam, ctas_of(C)) glu_kernel(const __grid_
   constexpr int kRows = kTable ? SigmoidTable::kBytes : 0;
   const int nvec = static_cast<int>(a.F >> 3);
   const Ahead ag(smem + kRows, 0, C, nvec), au(smem + kRows, 1, C, nvec);
+  bool marked = false;
   int64_t row = blockIdx.x;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
@@ -527,9 +533,10 @@ __global__ void __launch_bounds__(kMaxTeam, ctas_of(C)) glu_kernel(const __grid_
         for (int e = 0; e < 4; ++e) y[i][e] = mul2(y[i][e], p[e]);
       }
     }
-    store_codes<C>(a.o, row, nvec, y, s_top[par]);
+    marked |= store_codes<C>(a.o, row, nvec, y, s_top[par]);
   }
   cp_async_wait<0>();
+  if (marked) clear_marked(a.o, a.M, nvec);
 }
 
 // Vectors of 8 values a thread.  Sums cost a thread some 100 instructions, which many
