@@ -5,8 +5,8 @@
 // Up to kFewTokens tokens of a sequence (decode steps, drafted tokens): the
 // recurrence as it stands.  The state is read once into registers, every token
 // updates it and reads it out, and it is written once: bytes, 8 Dk Dv a head,
-// bound it (64 sequences of a token, 40 heads of 128 by 128: 54.5 us, 6.2 TB/s of
-// states; one sequence 3.3 us, a launch and a state's way to the SM and back).
+// bound it (64 sequences of a token, 40 heads of 128 by 128: 54.8 us, 6.2 TB/s of
+// states; one sequence 3.5 us, a launch and a state's way to the SM and back).
 //
 // More tokens go by in chunks of 64 (linear_attention_tc.cu).
 #include "linear_plan.cuh"

@@ -50,11 +50,12 @@
 //   scores (2)     the weighted scores
 //
 // A chunk takes an SM some 4000 cycles, 3100 of them in its 44 instructions (70 to 85
-// each, whatever their columns), the rest between the kinds of warps; the segments'
+// each, whatever their columns: near the pipe's rate for the 12 with 128, under half of it
+// for the 32 with 64), the rest between the kinds of warps; the segments'
 // kernel 2200, 12 instructions and the splitting of V.  64 sequences of 24
-// to 41 tokens, 40 heads: 84 us (bytes at 6784 GB/s: 57); 8191 tokens of 40 heads
-// 143 us (50): 42 segments, 9 scan, 92 outputs; 3 sequences of 48 tokens at most 9.6 us.
-// 8191 tokens of 40 heads of 64 by 64 129 us, 64 by 128 134, 128 by 64 139.
+// to 41 tokens, 40 heads: 87 us (bytes at 6784 GB/s: 57); 8191 tokens of 40 heads
+// 143 us (50): 42 segments, 9 scan, 92 outputs; 3 sequences of 48 tokens at most 10 us.
+// 8191 tokens of 40 heads of 64 by 64 126 us, 64 by 128 135, 128 by 64 136.
 //
 // Every wait on an mbarrier is bounded: after 2 s (prism_debug_wait_expiry
 // shortens that for tests) the kernel sets the device status bit; every warp leaves

@@ -16,7 +16,7 @@ namespace lin {
 
 // Tokens that take the recurrence.  40 heads of 128 by 128, 2, 4, 8 and 16 tokens by the
 // recurrence: one sequence 3.8, 4.5, 6.3 and 9.7 us, 64 of them 60, 70, 92 and 136;
-// in chunks 9.3 and 83 whatever the number (heads of 64 by 64: 8.5 and 60).
+// in chunks 9.6 and 81 whatever the number (heads of 64 by 64: 8.8 and 60).
 constexpr int kFewTokens = 8;
 constexpr int kChunk = 64;
 constexpr float kMinDecay = -16384.0f;   // e^x = 0 from far above it; sums of 64 stay finite

@@ -23,13 +23,13 @@
 // other CTAs of the SM work.
 //
 // A call's bytes (each operand once) are its floor; rows of 5120 and 17408, at 6784 GB/s:
-//   norm   8192 rows with a delta 48.2 us (90 % of that rate), 2048 rows with a delta's
-//          norm 19.1 us (65 %: a fill and seven CTAs' rows an SM, two sums in a row's way)
-//   heads  8192 rows of 40 heads of 128 with gates 55.9 us (55 %: 73 instructions for two
+//   norm   8192 rows with a delta 48.8 us (89 % of that rate), 2048 rows with a delta's
+//          norm 19.6 us (63 %: a fill and seven CTAs' rows an SM, two sums in a row's way)
+//   heads  8192 rows of 40 heads of 128 with gates 57.2 us (54 %: 73 instructions for two
 //          values, 70 % of the issue slots, the ALU and FMA pipes 49 and 43 %)
-//   glu    2048 rows 43.2 us (73 %: issue slots 58 %, weights from L2, sigmoids from
+//   glu    2048 rows 43.6 us (72 %: issue slots 58 %, weights from L2, sigmoids from
 //          shared memory)
-// One row takes 3 us, 64 rows of 17408 4.5: a launch, a row's loads and two exchanges.
+// One row takes 3.2 us, 64 rows of 17408 4.9: a launch, a row's loads and two exchanges.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -10,7 +10,8 @@ Entry points (same names as the C ABI):
 
 ``form`` says what ``q`` is: "int8" (codes for prism_w8a8_linear and the other
 int8 linears), "f16" (the same codes as float16, for prism_w8a8_linear_f16) or
-"bf16" (the values themselves; ``a_scale`` is None).  Each takes ``stream``
+"bf16" (the values themselves; ``a_scale`` is None).  A row that is not finite has
+codes 0 and a NaN for its scale, which the next linear passes on.  Each takes ``stream``
 (default: torch's current one); the outputs and the workspace that a call
 allocates belong to that stream.
 """
@@ -63,6 +64,8 @@ def prism_linear_attention(q, k, v, log_decay, state=None, state_in=None, state_
     sequence's tokens, None for one each; ``max_len``: the most tokens of one
     sequence (default: T, or 1 without cu); ``scale``: default D_k ** -0.5;
     ``workspace``: a uint8 tensor of prism_linear_attention_workspace_bytes bytes
-    (allocated when None); ``err``: optional int32 [1] device error word."""
+    (allocated when None); ``err``: optional int32 [1] device error word.  Single
+    tokens beside long sequences are faster in a call of their own, which gives the
+    same bits."""
     return _decode.linear_attention(q, k, v, log_decay, state, state_in, state_out, cu, max_len, scale, out, workspace, err,
                                     stream)

@@ -734,8 +734,9 @@ int prism_glu_quant(const void *gate_up_bf16, int64_t ldx,
  *   state_out     [S] int32: the slot that its last state goes to (its own again,
  *                 or another), -1 or NULL: none.  A slot that one sequence
  *                 writes is undefined afterwards where another of the same call
- *                 writes it too, and so are the outputs of another that starts
- *                 from it.  A sequence without tokens passes its state on.
+ *                 writes it too, and so are the outputs and the last state of
+ *                 another that starts from it.  A sequence without tokens passes
+ *                 its state on.
  *   cu            [S + 1] int32: sequence s has rows cu[s] .. cu[s + 1] - 1; NULL:
  *                 row s (T == S).  Rows of no sequence are not written; where
  *                 sequences overlap, theirs are undefined.
